@@ -31,6 +31,8 @@
  *    There is no silent fallback to another device or to the CPU.
  *    pc_last_error_message() gives a one-line reason for the last failing
  *    call on the calling host thread.
+ *  - The operators over point tokens (layer norm, rotary, attention) state
+ *    their element types and layouts themselves.
  *  - Inputs must be finite.  Ball Query never accepts a NaN distance; FPS and
  *    kNN results for non-finite coordinates are unspecified.
  *  - Sizes: B, N, Q >= 0 with N < 2^31 and every output size < 2^62 elements.
@@ -473,6 +475,121 @@ int pc_three_interpolate_backward(const float *grad_out, int64_t B, int64_t C,
 int pc_gather_points(const float *xyz, int64_t B, int64_t N,
                      const int64_t *idx, int64_t Q, int64_t K, float *out,
                      void *stream);
+
+/* ------------------------------------------------------------------------
+ * Operators over point tokens: layer norm, rotary positions with several
+ * axes, attention with a bias by distance.  A sampled or grouped cloud gives
+ * one token per center (FPS, kNN); these are what a transformer over those
+ * tokens runs, forward and backward.
+ *
+ * Elements are float32 or bfloat16 (pc_dtype); every sum, statistic and
+ * softmax is float32, and a result is rounded to its type once.  Strides are
+ * in elements, given as {batch, token, head} of a [B, L, heads, D] array
+ * whose last axis is contiguous (a slice of a fused projection, say), or
+ * NULL for a packed array.  Outputs and gradients are packed.  Results do
+ * not change from run to run (no atomic adds).
+ * ---------------------------------------------------------------------- */
+typedef enum pc_dtype { PC_F32 = 0, PC_BF16 = 1 } pc_dtype;
+
+/*
+ * Layer norm over the last axis:
+ *   out = (x - mean) * rstd * weight + bias,  rstd = 1 / sqrt(var + eps),
+ * var the mean of (x - mean)^2.
+ *
+ *   x, out     [rows, C] of dtype, device, packed.  C <= 8192
+ *              (PC_ERR_UNSUPPORTED above).
+ *   weight, bias  [C] of param_dtype (PC_F32, or the same as dtype), or NULL
+ *              (1, 0).
+ *   out_mean, out_rstd  [rows] float32, or both NULL.
+ *
+ * pc_layer_norm_backward, from the mean and rstd of the forward call:
+ *   xhat = (x - mean) rstd,  g = grad_out * weight,
+ *   grad_x = rstd (g - mean(g) - xhat mean(g xhat)),
+ *   grad_weight = sum over rows of grad_out * xhat,  grad_bias = of grad_out.
+ * grad_weight and grad_bias ([C] of param_dtype) may be NULL.  They are
+ * summed in a fixed order: scratch of at most 4 blocks per SM times 2 C
+ * float32 from the library's stream-ordered pool.
+ */
+int pc_layer_norm(const void *x, int dtype, int64_t rows, int64_t C, const void *weight,
+                  const void *bias, int param_dtype, double eps, void *out,
+                  float *out_mean, float *out_rstd, void *stream);
+
+int pc_layer_norm_backward(const void *grad_out, const void *x, int dtype, int64_t rows,
+                           int64_t C, const float *mean, const float *rstd,
+                           const void *weight, int param_dtype, void *grad_x,
+                           void *grad_weight, void *grad_bias, void *stream);
+
+/*
+ * Rotary positions with A axes (x, y, z of a point; time, height, width of a
+ * patch), for queries q [B, L, H, D] and keys k [B, L, Hkv, D] in one call
+ * (H = 0 or Hkv = 0: that side is absent and its pointers may be NULL):
+ *   pair p = a F + f (a < A, f < F) of every head of token (b, l) turns by
+ *   t = positions[b, l, a] * freqs[a, f]:
+ *     (u, v) -> (u cos t - v sin t, v cos t + u sin t).
+ * A pair is channels (2p, 2p + 1), or with PC_ROTARY_HALF_SPLIT (p, A F + p);
+ * channels from 2 A F on are copied.  PC_ROTARY_INVERSE turns by -t, which
+ * is also the gradient: the gradients of q and k are the inverse turn of
+ * those of out_q and out_k.
+ *
+ *   positions  [B, L, A] float32, 1 <= A <= 4.  freqs [A, F] float32,
+ *              2 A F <= D, A F <= 4096.
+ *   out_q, out_k  packed; they must not overlap the inputs.
+ */
+#define PC_ROTARY_HALF_SPLIT 1
+#define PC_ROTARY_INVERSE 2
+int pc_rotary(const void *q, const void *k, int dtype, int64_t B, int64_t L, int64_t H,
+              int64_t Hkv, int64_t D, const int64_t *q_strides, const int64_t *k_strides,
+              const float *positions, const float *freqs, int64_t A, int64_t F, int flags,
+              void *out_q, void *out_k, void *stream);
+
+/*
+ * Attention over point tokens with a bias by squared distance:
+ *   z_ij = scale * q_i . k_j - slopes[h] * |query_xyz_i - ref_xyz_j|^2,
+ *   out_i = sum_j softmax_j(z_ij) v_j  over j < ref_lengths[b].
+ *
+ *   q [B, Lq, H, D]; k, v [B, Lk, Hkv, D]; D <= 128 (PC_ERR_UNSUPPORTED
+ *              above).  Hkv divides H: query head h reads key head
+ *              h / (H / Hkv).
+ *   scale      finite and > 0.
+ *   query_xyz [B, Lq, 3], ref_xyz [B, Lk, 3], slopes [H] float32, packed:
+ *              all three, or all NULL (no bias); those of an empty side may
+ *              be NULL.
+ *   query_lengths, ref_lengths  [B] int64, device, or NULL (= Lq, = Lk);
+ *              clamped to [0, Lq] and [0, Lk].  What lies past a length is
+ *              not read into any result, whatever its values.
+ *   out        [B, Lq, H, D].  Rows past query_lengths, and rows of a cloud
+ *              without valid keys, are 0.
+ *   out_lse    [B, H, Lq] float32 or NULL: log sum_j exp(z_ij), -inf for the
+ *              rows that are 0 by the rule above.
+ *
+ * pc_attention_backward takes the same arguments with out and lse of the
+ * forward call and grad_out [B, Lq, H, D] (packed), and writes grad_q,
+ * grad_k, grad_v (packed, of dtype; 0 past the lengths) and, if not NULL,
+ * grad_slopes [H] float32.  The positions get no gradient.
+ *
+ * Scratch (the library's stream-ordered pool): the parts of a pass whose
+ * streamed side is split among more blocks, at most 1 GiB; in the backward
+ * pass 8 bytes, with grad_slopes 12 more per part, per query row and head.
+ *
+ * Return PC_OK, PC_ERR_INVALID_ARGUMENT, PC_ERR_UNSUPPORTED, PC_ERR_CUDA or
+ * PC_ERR_NO_DEVICE.
+ */
+int pc_attention(const void *q, const void *k, const void *v, int dtype, int64_t B,
+                 int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int64_t D,
+                 const int64_t *q_strides, const int64_t *k_strides,
+                 const int64_t *v_strides, double scale, const float *query_xyz,
+                 const float *ref_xyz, const float *slopes, const int64_t *query_lengths,
+                 const int64_t *ref_lengths, void *out, float *out_lse, void *stream);
+
+int pc_attention_backward(const void *grad_out, const void *q, const void *k, const void *v,
+                          const void *out, const float *lse, int dtype, int64_t B,
+                          int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int64_t D,
+                          const int64_t *q_strides, const int64_t *k_strides,
+                          const int64_t *v_strides, double scale, const float *query_xyz,
+                          const float *ref_xyz, const float *slopes,
+                          const int64_t *query_lengths, const int64_t *ref_lengths,
+                          void *grad_q, void *grad_k, void *grad_v, float *grad_slopes,
+                          void *stream);
 
 /*
  * Device status word.  Kernels that wait on other thread blocks bound every

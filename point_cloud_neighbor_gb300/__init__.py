@@ -1,6 +1,7 @@
 """GB300-native dense point-cloud neighbor search (FPS, kNN, Ball Query) and
 the operators built on it (exact grid search, Chamfer distance, PointNet++
-feature propagation, neighbor gather).
+feature propagation, neighbor gather), and the operators a transformer over
+point tokens runs (layer norm, rotary positions, attention; ``.tokens``).
 
 The compute lives in libpointcloud.so (CUDA kernels for sm_103a behind the C
 ABI of include/pointcloud.h); this package holds its ctypes binding, the
@@ -22,6 +23,8 @@ from .binding import (PC_FPS_AUTO, PC_FPS_BLOCK, PC_FPS_CLUSTER, PC_FPS_GRID,
                       pc_fps_sm_count, pc_fps_plan, pc_three_interpolate,
                       pc_three_interpolate_backward, three_interpolate,
                       three_nn)
+from .tokens import (attention, layer_norm, pc_attention, pc_attention_backward,
+                     pc_layer_norm, pc_layer_norm_backward, pc_rotary, rotary)
 
 __all__ = [
     "PC_FPS_AUTO", "PC_FPS_BLOCK", "PC_FPS_CLUSTER", "PC_FPS_GRID",
@@ -34,4 +37,6 @@ __all__ = [
     "pc_set_sm_reserve", "pc_fps_sm_count", "pc_fps_plan", "pc_debug_set_stall",
     "PC_STALL_FPS_GRID", "PC_STALL_FPS_CLUSTER", "PC_STALL_TILE_STREAM",
     "pc_knn_ball_query", "pc_knn_ball_query_plan", "pc_fps_set_batched",
+    "pc_layer_norm", "pc_layer_norm_backward", "layer_norm", "pc_rotary", "rotary",
+    "pc_attention", "pc_attention_backward", "attention",
 ]

@@ -73,6 +73,19 @@ _SIGNATURES = {
     "pc_gather_points": (ctypes.c_int, [_P, _I, _I, _P, _I, _I, _P, _P]),
     "pc_knn_d": (ctypes.c_int, [_P, _I, _I, _P, _I, _I, _I, ctypes.c_int, _P, _P,
                                 _P]),
+    "pc_layer_norm": (ctypes.c_int, [_P, ctypes.c_int, _I, _I, _P, _P, ctypes.c_int,
+                                     ctypes.c_double, _P, _P, _P, _P]),
+    "pc_layer_norm_backward": (ctypes.c_int, [_P, _P, ctypes.c_int, _I, _I, _P, _P, _P,
+                                              ctypes.c_int, _P, _P, _P, _P]),
+    "pc_rotary": (ctypes.c_int, [_P, _P, ctypes.c_int, _I, _I, _I, _I, _I, _P, _P, _P,
+                                 _P, _I, _I, ctypes.c_int, _P, _P, _P]),
+    "pc_attention": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, _I, _I, _I, _I, _I, _I,
+                                    _P, _P, _P, ctypes.c_double, _P, _P, _P, _P, _P,
+                                    _P, _P, _P]),
+    "pc_attention_backward": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, ctypes.c_int, _I,
+                                             _I, _I, _I, _I, _I, _P, _P, _P,
+                                             ctypes.c_double, _P, _P, _P, _P, _P, _P,
+                                             _P, _P, _P, _P]),
     "pc_device_status": (ctypes.c_int, [_P, ctypes.c_int,
                                         ctypes.POINTER(ctypes.c_int32)]),
     "pc_set_wait_timeout_ns": (None, [ctypes.c_uint64]),

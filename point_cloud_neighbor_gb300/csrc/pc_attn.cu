@@ -1,0 +1,686 @@
+// pc_attn.cu -- attention over point tokens with a bias by squared distance
+// and lengths masks: the C ABI, the float32 kernels and the joins of split
+// passes.  Formulas and the three passes are in pc_attn.cuh.
+#include "pc_attn.cuh"
+#include "pointcloud.h"
+
+#include <cmath>
+#include <cstdio>
+
+namespace pcn {
+namespace {
+
+// ---------------------------------------------------------------------------
+// float32 arithmetic on tiles of 64 rows by 64 streamed rows, 256 threads as
+// 16 x 16: a thread forms 4 x 4 scores (rows ty + 16 i, columns tx + 16 j)
+// and 4 rows by DP / 16 channels of the accumulators.
+// ---------------------------------------------------------------------------
+constexpr int SB = 64;           // rows of a tile, both sides
+constexpr int ST = 256;          // threads
+constexpr int SP = SB + 4;       // row pitch of a score tile
+
+constexpr size_t simt_smem(int mode, int DP) {
+    const size_t tile = size_t(SB) * (DP + 4), sc = size_t(SB) * SP;
+    return 4 * ((mode == ATTN_FWD ? 3 : 4) * tile + (mode == ATTN_DKV ? 2 : 1) * sc + 6 * SB);
+}
+
+// 64 rows of D channels into smem as float32, zeros past row `n` and past D.
+template <class T, int DP>
+__device__ __forceinline__ void load_rows(float *dst, const T *src, int64_t stride, int r0,
+                                          int n, int D, bool vec) {
+    constexpr int LD = DP + 4;
+    if (vec) {
+        for (int i = threadIdx.x; i < SB * DP / 4; i += ST) {
+            const int r = i / (DP / 4), c = (i % (DP / 4)) * 4;
+            float v[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+            if (r0 + r < n && c < D) Vec<T, 4>::load(src + int64_t(r0 + r) * stride + c, v);
+            Vec<float, 4>::store(dst + r * LD + c, v);
+        }
+    } else {
+        for (int i = threadIdx.x; i < SB * DP; i += ST) {
+            const int r = i / DP, c = i % DP;
+            float v = 0.0f;
+            if (r0 + r < n && c < D) Vec<T, 1>::load(src + int64_t(r0 + r) * stride + c, &v);
+            dst[r * LD + c] = v;
+        }
+    }
+}
+
+// s[i][j] = X[ty + 16 i] . Y[tx + 16 j]
+template <int DP>
+__device__ __forceinline__ void tile_scores(const float *X, const float *Y, int ty, int tx,
+                                            float (&s)[4][4]) {
+    constexpr int LD = DP + 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s[i][j] = 0.0f;
+#pragma unroll 4
+    for (int d = 0; d < DP; d += 4) {
+        float x[4][4], y[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Vec<float, 4>::load(X + (ty + 16 * i) * LD + d, x[i]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) Vec<float, 4>::load(Y + (tx + 16 * j) * LD + d, y[j]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[i][j] = fmaf(x[i][e], y[j][e], s[i][j]);
+    }
+}
+
+// acc[i][64 g + ...] += sum_c P[ty + 16 i][c] Y[c][4 tx + 64 g ...]
+template <int DP>
+__device__ __forceinline__ void tile_accumulate(const float *P, const float *Y, int ty, int tx,
+                                                float (&acc)[4][DP / 16]) {
+    constexpr int LD = DP + 4;
+#pragma unroll 2
+    for (int c = 0; c < SB; c += 4) {
+        float p[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) Vec<float, 4>::load(P + (ty + 16 * i) * SP + c, p[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+            for (int g = 0; g < DP / 64; ++g) {
+                float y[4];
+                Vec<float, 4>::load(Y + (c + e) * LD + 64 * g + 4 * tx, y);
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int f = 0; f < 4; ++f)
+                        acc[i][4 * g + f] = fmaf(p[i][e], y[f], acc[i][4 * g + f]);
+            }
+    }
+}
+
+template <class T, int MODE, int DP>
+__global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const bool vec) {
+    extern __shared__ float sm[];
+    constexpr int TILE = SB * (DP + 4);
+    constexpr bool BWD = MODE != ATTN_FWD;
+    float *X1 = sm, *X2 = X1 + (BWD ? TILE : 0);
+    float *Y1 = X2 + TILE, *Y2 = Y1 + TILE;
+    float *P = Y2 + TILE, *S = P + (MODE == ATTN_DKV ? SB * SP : 0);
+    float *yp = S + SB * SP;       // x, y, z of the streamed rows, [3][64]
+    float *ylse = yp + 3 * SB, *ydel = ylse + SB;
+
+    const int LX = MODE == ATTN_DKV ? a.Lk : a.Lq;
+    const int NH = MODE == ATTN_DKV ? a.Hkv : a.H;
+    const int G = a.H / a.Hkv;
+    const int ntile = (LX + SB - 1) / SB;
+    int64_t idx = blockIdx.x;
+    const int split = int(idx % a.nsplit);
+    idx /= a.nsplit;
+    const int tile = int(idx % ntile);
+    idx /= ntile;
+    const int head = int(idx % NH), b = int(idx / NH);
+    const int nq = attn_len(a.qlen, b, a.Lq), nk = attn_len(a.rlen, b, a.Lk);
+    const int nx = MODE == ATTN_DKV ? nk : nq, ny = MODE == ATTN_DKV ? nq : nk;
+    const int r0 = tile * SB;
+    const int ty = threadIdx.x / 16, tx = threadIdx.x % 16;
+    const bool bias = a.slopes != nullptr;
+    const float c2 = a.scale * ATTN_LOG2E;
+
+    auto qrow = [&](int h) { return static_cast<const T *>(a.q) + b * a.qs[0] + h * a.qs[2]; };
+    auto krow = [&](int h) { return static_cast<const T *>(a.k) + b * a.ks[0] + h * a.ks[2]; };
+    auto vrow = [&](int h) { return static_cast<const T *>(a.v) + b * a.vs[0] + h * a.vs[2]; };
+    auto grow = [&](int h) {
+        return static_cast<const T *>(a.go) + (int64_t(b) * a.Lq * a.H + h) * a.D;
+    };
+    const int64_t gs = int64_t(a.H) * a.D;
+
+    const int hk = MODE == ATTN_DKV ? head : head / G;
+    if (MODE == ATTN_DKV) {
+        load_rows<T, DP>(X1, krow(hk), a.ks[1], r0, nx, a.D, vec);
+        load_rows<T, DP>(X2, vrow(hk), a.vs[1], r0, nx, a.D, vec);
+    } else {
+        load_rows<T, DP>(X1, qrow(head), a.qs[1], r0, nx, a.D, vec);
+        if (BWD) load_rows<T, DP>(X2, grow(head), gs, r0, nx, a.D, vec);
+    }
+    float px[4][3];  // positions of the thread's rows
+    float lse2[4], del[4];
+    const float *xpos = MODE == ATTN_DKV ? a.rxyz : a.qxyz;
+    const float *ypos = MODE == ATTN_DKV ? a.qxyz : a.rxyz;
+    const int LY = MODE == ATTN_DKV ? a.Lq : a.Lk;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + ty + 16 * i;
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+            px[i][e] = bias && r < nx ? xpos[(int64_t(b) * LX + r) * 3 + e] : 0.0f;
+        if (MODE == ATTN_DQ) {
+            const int64_t at = (int64_t(b) * a.H + head) * a.Lq + r;
+            lse2[i] = r < nx ? a.lse2[at] : INFINITY;  // P = 0
+            del[i] = r < nx ? a.delta[at] : 0.0f;
+        }
+    }
+    float acc[4][DP / 16], acc2[4][DP / 16];
+    float mx[4], sum[4], wa[4], we[4], wd[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+#pragma unroll
+        for (int e = 0; e < DP / 16; ++e) acc[i][e] = acc2[i][e] = 0.0f;
+        mx[i] = -INFINITY;
+        sum[i] = wa[i] = we[i] = wd[i] = 0.0f;
+    }
+
+    const int nyt = (ny + SB - 1) / SB;
+    const int64_t items = nx > r0 ? int64_t(nyt) * (MODE == ATTN_DKV ? G : 1) : 0;
+    const int64_t it0 = items * split / a.nsplit, it1 = items * (split + 1) / a.nsplit;
+    for (int64_t it = it0; it < it1; ++it) {
+        const int h = MODE == ATTN_DKV ? hk * G + int(it / nyt) : head;
+        const int y0 = int(MODE == ATTN_DKV ? it % nyt : it) * SB;
+        __syncthreads();
+        if (MODE == ATTN_DKV) {
+            load_rows<T, DP>(Y1, qrow(h), a.qs[1], y0, ny, a.D, vec);
+            load_rows<T, DP>(Y2, grow(h), gs, y0, ny, a.D, vec);
+            if (threadIdx.x < SB) {
+                const int r = y0 + threadIdx.x;
+                const int64_t at = (int64_t(b) * a.H + h) * a.Lq + r;
+                ylse[threadIdx.x] = r < ny ? a.lse2[at] : INFINITY;
+                ydel[threadIdx.x] = r < ny ? a.delta[at] : 0.0f;
+            }
+        } else {
+            load_rows<T, DP>(Y1, krow(hk), a.ks[1], y0, ny, a.D, vec);
+            load_rows<T, DP>(Y2, vrow(hk), a.vs[1], y0, ny, a.D, vec);
+        }
+        if (bias)
+            for (int i = threadIdx.x; i < 3 * SB; i += ST) {
+                const int r = i / 3, e = i % 3;
+                yp[e * SB + r] = y0 + r < ny ? ypos[(int64_t(b) * LY + y0 + r) * 3 + e] : 0.0f;
+            }
+        __syncthreads();
+        const float ws = bias ? a.slopes[h] * ATTN_LOG2E : 0.0f;
+        float s[4][4], dp[4][4], d2[4][4];
+        tile_scores<DP>(X1, Y1, ty, tx, s);
+        if (BWD) tile_scores<DP>(X2, Y2, ty, tx, dp);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const int c = tx + 16 * j;
+            const float yx = yp[c], yy = yp[SB + c], yz = yp[2 * SB + c];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float z = s[i][j] * c2;
+                if (bias) {
+                    const float dx = px[i][0] - yx, dy = px[i][1] - yy, dz = px[i][2] - yz;
+                    d2[i][j] = fmaf(dz, dz, fmaf(dy, dy, dx * dx));
+                    z = fmaf(d2[i][j], -ws, z);
+                }
+                if (MODE != ATTN_DKV && y0 + c >= ny) z = -INFINITY;
+                s[i][j] = z;
+            }
+        }
+        if (MODE == ATTN_FWD) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float m = fmaxf(fmaxf(s[i][0], s[i][1]), fmaxf(s[i][2], s[i][3]));
+#pragma unroll
+                for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                m = fmaxf(m, mx[i]);
+                const float base = m == -INFINITY ? 0.0f : m;
+                const float keep = exp2f(mx[i] - base);
+                mx[i] = m;
+                float t = 0.0f;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    s[i][j] = exp2f(s[i][j] - base);
+                    t += s[i][j];
+                    P[(ty + 16 * i) * SP + tx + 16 * j] = s[i][j];
+                }
+                sum[i] = fmaf(sum[i], keep, t);
+#pragma unroll
+                for (int e = 0; e < DP / 16; ++e) acc[i][e] *= keep;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int c = tx + 16 * j;
+                    const float p = exp2f(s[i][j] - (MODE == ATTN_DKV ? ylse[c] : lse2[i]));
+                    const float ds = p * (dp[i][j] - (MODE == ATTN_DKV ? ydel[c] : del[i]));
+                    if (MODE == ATTN_DQ && bias) {
+                        wa[i] = fmaf(ds, d2[i][j], wa[i]);
+                        we[i] = fmaf(p, d2[i][j], we[i]);
+                        wd[i] += ds;
+                    }
+                    if (MODE == ATTN_DKV) P[(ty + 16 * i) * SP + c] = p;
+                    S[(ty + 16 * i) * SP + c] = ds;
+                }
+        }
+        __syncthreads();
+        if (MODE == ATTN_FWD) {
+            tile_accumulate<DP>(P, Y2, ty, tx, acc);
+        } else {
+            tile_accumulate<DP>(S, Y1, ty, tx, acc);
+            if (MODE == ATTN_DKV) tile_accumulate<DP>(P, Y2, ty, tx, acc2);
+        }
+    }
+
+    const int64_t rows = int64_t(a.B) * LX * NH;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + ty + 16 * i;
+        const int64_t hrow = (int64_t(b) * a.H + head) * a.Lq + r;  // FWD, DQ
+        if (MODE == ATTN_FWD) {
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
+        }
+        if (MODE == ATTN_DQ && bias) {
+#pragma unroll
+            for (int o = 8; o > 0; o >>= 1) {
+                wa[i] += __shfl_xor_sync(0xffffffffu, wa[i], o);
+                we[i] += __shfl_xor_sync(0xffffffffu, we[i], o);
+                wd[i] += __shfl_xor_sync(0xffffffffu, wd[i], o);
+            }
+            if (tx == 0 && r < LX && a.rowsum != nullptr) {
+                const int64_t n = int64_t(a.B) * a.H * a.Lq;
+                float *w = a.rowsum + split * 3 * n + hrow;
+                w[0] = wa[i], w[n] = we[i], w[2 * n] = wd[i];
+            }
+        }
+        if (r >= LX) continue;
+        const int64_t orow = (int64_t(b) * LX + r) * NH + head;
+        if (a.nsplit > 1) {
+            float *p1 = a.part + (int64_t(split) * rows + orow) * a.D;
+            float *p2 = p1 + int64_t(a.nsplit) * rows * a.D;
+#pragma unroll
+            for (int e = 0; e < DP / 16; ++e) {
+                const int c = 64 * (e / 4) + 4 * tx + e % 4;
+                if (c < a.D) {
+                    p1[c] = r < nx ? acc[i][e] : 0.0f;
+                    if (MODE == ATTN_DKV) p2[c] = r < nx ? acc2[i][e] : 0.0f;
+                }
+            }
+            if (MODE == ATTN_FWD && tx == 0) {
+                const int64_t n = int64_t(a.B) * a.H * a.Lq;
+                a.part_ml[int64_t(split) * 2 * n + hrow] = mx[i];
+                a.part_ml[(int64_t(split) * 2 + 1) * n + hrow] = sum[i];
+            }
+            continue;
+        }
+        const float f = MODE == ATTN_FWD ? (r < nx && sum[i] > 0.0f ? 1.0f / sum[i] : 0.0f)
+                                         : (r < nx ? a.scale : 0.0f);
+        T *o1 = static_cast<T *>(MODE == ATTN_FWD  ? a.out
+                                 : MODE == ATTN_DQ ? a.dq
+                                                   : a.dk) + orow * a.D;
+        T *o2 = static_cast<T *>(a.dv) + orow * a.D;
+#pragma unroll
+        for (int e = 0; e < DP / 16; ++e) {
+            const int c = 64 * (e / 4) + 4 * tx + e % 4;
+            if (c < a.D) {
+                const float w = r < nx ? acc[i][e] * f : 0.0f;
+                Vec<T, 1>::store(o1 + c, &w);
+                if (MODE == ATTN_DKV) {
+                    const float u = r < nx ? acc2[i][e] : 0.0f;
+                    Vec<T, 1>::store(o2 + c, &u);
+                }
+            }
+        }
+        if (MODE == ATTN_FWD && tx == 0 && a.lse != nullptr)
+            a.lse[hrow] = r < nx && sum[i] > 0.0f
+                              ? (mx[i] + log2f(sum[i])) * ATTN_LN2 : -INFINITY;
+    }
+}
+
+// delta_i = out_i . dout_i, and lse in base-2 units with +inf for rows without
+// keys (their weights 2^(z - lse2) are then 0): a warp per (token, head).
+template <class T>
+__global__ void __launch_bounds__(256)
+attn_delta_kernel(const T *out, const T *go, const float *lse, int64_t rows, int Lq, int H,
+                  int D, float *delta, float *lse2) {
+    const int64_t row = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;  // (b Lq + i) H + h
+    if (row >= rows) return;
+    const int lane = threadIdx.x % 32;
+    float s = 0.0f;
+    for (int c = lane; c < D; c += 32) {
+        float o, g;
+        Vec<T, 1>::load(out + row * D + c, &o);
+        Vec<T, 1>::load(go + row * D + c, &g);
+        s = fmaf(o, g, s);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const int64_t tok = row / H, b = tok / Lq;
+    if (lane == 0) {
+        const int64_t at = (b * H + row % H) * Lq + (tok - b * Lq);
+        delta[at] = s;
+        lse2[at] = lse[at] == -INFINITY ? INFINITY : lse[at] * ATTN_LOG2E;
+    }
+}
+
+// Joins the parts of a split forward pass: a warp per (token, head).
+template <class T>
+__global__ void __launch_bounds__(256) attn_join_forward_kernel(const AttnArgs a) {
+    const int64_t rows = int64_t(a.B) * a.Lq * a.H;
+    const int64_t row = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;
+    if (row >= rows) return;
+    const int lane = threadIdx.x % 32;
+    const int64_t tok = row / a.H, b = tok / a.Lq;
+    const int i = int(tok - b * a.Lq);
+    const int64_t hrow = (b * a.H + row % a.H) * a.Lq + i;
+    float m = -INFINITY, l = 0.0f;
+    for (int s = 0; s < a.nsplit; ++s) {
+        const float ms = a.part_ml[int64_t(s) * 2 * rows + hrow];
+        const float mn = fmaxf(m, ms), base = mn == -INFINITY ? 0.0f : mn;
+        l = fmaf(l, exp2f(m - base),
+                 a.part_ml[(int64_t(s) * 2 + 1) * rows + hrow] * exp2f(ms - base));
+        m = mn;
+    }
+    const bool any = i < attn_len(a.qlen, int(b), a.Lq) && l > 0.0f;
+    const float f = any ? 1.0f / l : 0.0f, base = m == -INFINITY ? 0.0f : m;
+    for (int c = lane; c < a.D; c += 32) {
+        float v = 0.0f;
+        if (any)
+            for (int s = 0; s < a.nsplit; ++s)
+                v = fmaf(a.part[(int64_t(s) * rows + row) * a.D + c],
+                         exp2f(a.part_ml[int64_t(s) * 2 * rows + hrow] - base), v);
+        v *= f;
+        Vec<T, 1>::store(static_cast<T *>(a.out) + row * a.D + c, &v);
+    }
+    if (lane == 0 && a.lse != nullptr)
+        a.lse[hrow] = any ? (m + log2f(l)) * ATTN_LN2 : -INFINITY;
+}
+
+// out = factor * sum of the parts.
+template <class T>
+__global__ void __launch_bounds__(256)
+attn_join_sum_kernel(const float *part, int nsplit, int64_t n, float factor, T *out) {
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    if (i >= n) return;
+    float v = 0.0f;
+    for (int s = 0; s < nsplit; ++s) v += part[int64_t(s) * n + i];
+    v *= factor;
+    Vec<T, 1>::store(out + i, &v);
+}
+
+// dslope_h = -sum over rows of (dS d2 - (dS) (P d2)), each row's sums joined
+// over the parts first: a block per head, float64, a fixed order.  A row's
+// exact dS sum to 0; what they sum to here is the error of delta (from an
+// output rounded to its type), and the second term takes its effect out.
+__global__ void __launch_bounds__(1024)
+attn_slope_kernel(const AttnArgs a, float *dslopes) {
+    __shared__ double red[32];
+    const int h = blockIdx.x;
+    const int64_t n = int64_t(a.B) * a.H * a.Lq;
+    double t = 0.0;
+    for (int64_t r = threadIdx.x; r < int64_t(a.B) * a.Lq; r += 1024) {
+        const int64_t b = r / a.Lq, at = (b * a.H + h) * a.Lq + (r - b * a.Lq);
+        float wa = 0.0f, we = 0.0f, wd = 0.0f;
+        for (int s = 0; s < a.nsplit; ++s) {
+            const float *w = a.rowsum + int64_t(s) * 3 * n + at;
+            wa += w[0], we += w[n], wd += w[2 * n];
+        }
+        t += double(fmaf(-wd, we, wa));
+    }
+    for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
+    if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = t;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        t = 0.0;
+        for (int i = 0; i < 32; ++i) t += red[i];
+        dslopes[h] = float(-t);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Host side.
+// ---------------------------------------------------------------------------
+template <class T, int MODE, int DP>
+cudaError_t simt_launch(const AttnArgs &a, bool vec, int64_t blocks, cudaStream_t st) {
+    constexpr size_t smem = simt_smem(MODE, DP);
+    const cudaError_t e = cudaFuncSetAttribute(
+        attn_simt_kernel<T, MODE, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    if (e != cudaSuccess) return e;
+    attn_simt_kernel<T, MODE, DP><<<unsigned(blocks), ST, smem, st>>>(a, vec);
+    return cudaGetLastError();
+}
+
+template <class T, int MODE>
+cudaError_t simt_pick(const AttnArgs &a, bool vec, int64_t blocks, cudaStream_t st) {
+    return a.D <= 64 ? simt_launch<T, MODE, 64>(a, vec, blocks, st)
+                     : simt_launch<T, MODE, 128>(a, vec, blocks, st);
+}
+
+bool strides_fit(const AttnArgs &a, int v, size_t bytes) {
+    auto ok = [&](const void *p, const int64_t *s) {
+        return reinterpret_cast<uintptr_t>(p) % bytes == 0 && s[0] % v == 0 && s[1] % v == 0 &&
+               s[2] % v == 0;
+    };
+    return a.D % v == 0 && ok(a.q, a.qs) && ok(a.k, a.ks) && ok(a.v, a.vs) &&
+           reinterpret_cast<uintptr_t>(a.go) % bytes == 0;
+}
+
+struct Scratch {
+    const DeviceInfo *dev;
+    cudaStream_t st;
+    void *p = nullptr;
+    ~Scratch() {
+        if (p != nullptr) scratch_free(p, st);
+    }
+    cudaError_t take(size_t bytes) { return scratch_alloc(*dev, &p, bytes, st); }
+};
+
+// Parts of the streamed side: enough blocks for `want`, at least one tile of
+// the streamed side each, at most 1 GiB of partial accumulators.
+int pick_split(int64_t want, int64_t base, int64_t items, int64_t row_floats) {
+    int64_t n = (want + base - 1) / base;
+    if (n > items) n = items;
+    if (n > 256) n = 256;
+    while (n > 1 && n * row_floats > (int64_t(1) << 28)) --n;
+    return n < 1 ? 1 : int(n);
+}
+
+template <class T>
+cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes,
+                     cudaStream_t st) {
+    const bool dkv = mode == ATTN_DKV;
+    const int64_t LX = dkv ? a.Lk : a.Lq, LY = dkv ? a.Lq : a.Lk, NH = dkv ? a.Hkv : a.H;
+    const int64_t xr = SB, yr = SB;
+    const int64_t ntile = (LX + xr - 1) / xr, nyt = (LY + yr - 1) / yr;
+    const int64_t base = ntile * NH * a.B;
+    const int64_t rows = int64_t(a.B) * LX * NH, hrows = int64_t(a.B) * a.H * a.Lq;
+    const int64_t want = int64_t(dev.sm_count) * 2;
+    a.nsplit = pick_split(want, base, dkv ? nyt * (a.H / a.Hkv) : nyt,
+                          rows * a.D * (dkv ? 2 : 1));
+    const bool slopes = mode == ATTN_DQ && a.slopes != nullptr && dslopes != nullptr;
+    const size_t part = a.nsplit > 1 ? size_t(a.nsplit) * rows * a.D * (dkv ? 2 : 1) : 0;
+    const size_t ml = a.nsplit > 1 && mode == ATTN_FWD ? size_t(a.nsplit) * 2 * hrows : 0;
+    const size_t rs = slopes ? size_t(a.nsplit) * 3 * hrows : 0;
+    Scratch ws{&dev, st};
+    cudaError_t e = cudaSuccess;
+    if (part + ml + rs > 0) {
+        if ((e = ws.take((part + ml + rs) * sizeof(float))) != cudaSuccess) return e;
+        a.part = static_cast<float *>(ws.p);
+        a.part_ml = a.part + part;
+        a.rowsum = rs ? a.part_ml + ml : nullptr;
+    }
+    const bool vec = strides_fit(a, 4, 4 * sizeof(T));
+    const int64_t blocks = base * a.nsplit;
+    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    e = mode == ATTN_FWD  ? simt_pick<T, ATTN_FWD>(a, vec, blocks, st)
+        : mode == ATTN_DQ ? simt_pick<T, ATTN_DQ>(a, vec, blocks, st)
+                          : simt_pick<T, ATTN_DKV>(a, vec, blocks, st);
+    if (e != cudaSuccess) return e;
+    if (a.nsplit > 1) {
+        const int64_t n = rows * a.D;
+        const unsigned g = unsigned((n + 255) / 256);
+        if (mode == ATTN_FWD)
+            attn_join_forward_kernel<T><<<unsigned((rows + 7) / 8), 256, 0, st>>>(a);
+        else
+            attn_join_sum_kernel<T><<<g, 256, 0, st>>>(
+                a.part, a.nsplit, n, a.scale, static_cast<T *>(dkv ? a.dk : a.dq));
+        if (dkv)
+            attn_join_sum_kernel<T><<<g, 256, 0, st>>>(a.part + int64_t(a.nsplit) * n, a.nsplit,
+                                                       n, 1.0f, static_cast<T *>(a.dv));
+    }
+    if (slopes) attn_slope_kernel<<<a.H, 1024, 0, st>>>(a, dslopes);
+    return cudaGetLastError();
+}
+
+template <class T>
+cudaError_t run_backward(const DeviceInfo &dev, AttnArgs a, const void *out, float *dslopes,
+                         cudaStream_t st) {
+    const int64_t rows = int64_t(a.B) * a.Lq * a.H;
+    Scratch ws{&dev, st};
+    cudaError_t e = ws.take(size_t(rows > 0 ? rows : 1) * 2 * sizeof(float));
+    if (e != cudaSuccess) return e;
+    float *delta = static_cast<float *>(ws.p), *lse2 = delta + rows;
+    a.delta = delta, a.lse2 = lse2;
+    if (rows > 0) {
+        attn_delta_kernel<T><<<unsigned((rows + 7) / 8), 256, 0, st>>>(
+            static_cast<const T *>(out), static_cast<const T *>(a.go), a.lse, rows, a.Lq, a.H,
+            a.D, delta, lse2);
+        if ((e = run_pass<T>(dev, a, ATTN_DQ, dslopes, st)) != cudaSuccess) return e;
+    } else if (dslopes != nullptr && a.slopes != nullptr) {
+        if ((e = cudaMemsetAsync(dslopes, 0, size_t(a.H) * 4, st)) != cudaSuccess) return e;
+    }
+    if (int64_t(a.B) * a.Lk * a.Hkv > 0) e = run_pass<T>(dev, a, ATTN_DKV, nullptr, st);
+    return e;
+}
+
+// The checks both directions share; fills `a`.  *done: nothing to run.
+int attn_check(const char *what, AttnArgs &a, const DeviceInfo **dev, const void *q,
+               const void *k, const void *v, int dtype, int64_t B, int64_t Lq, int64_t Lk,
+               int64_t H, int64_t Hkv, int64_t D, const int64_t *qs, const int64_t *ks,
+               const int64_t *vs, double scale, const float *qxyz, const float *rxyz,
+               const float *slopes, const int64_t *qlen, const int64_t *rlen) {
+    char m[220];
+    auto bad = [&](int code, const char *why) {
+        std::snprintf(m, sizeof(m), "%s: %s", what, why);
+        return api_fail(code, m);
+    };
+    if (B < 0 || Lq < 0 || Lk < 0 || H < 0 || Hkv < 0)
+        return bad(PC_ERR_INVALID_ARGUMENT, "negative size");
+    if (D < 1) return bad(PC_ERR_INVALID_ARGUMENT, "D must be at least 1");
+    if (dtype != PC_F32 && dtype != PC_BF16)
+        return bad(PC_ERR_INVALID_ARGUMENT, "dtype must be PC_F32 or PC_BF16");
+    if (H > 0 && (Hkv < 1 || H % Hkv != 0))
+        return bad(PC_ERR_INVALID_ARGUMENT, "Hkv must divide H");
+    if (!(scale > 0.0 && scale < 1e30))
+        return bad(PC_ERR_INVALID_ARGUMENT, "scale must be finite and > 0");
+    // (an empty side has no positions to point at)
+    if (slopes != nullptr ? (qxyz == nullptr && B > 0 && Lq > 0) || (rxyz == nullptr && B > 0 && Lk > 0)
+                          : qxyz != nullptr || rxyz != nullptr)
+        return bad(PC_ERR_INVALID_ARGUMENT, "slopes, query_xyz and ref_xyz go together");
+    if (D > 128) return bad(PC_ERR_UNSUPPORTED, "D above 128");
+    const int64_t lim = int64_t(1) << 30;
+    if (Lq > lim || Lk > lim || B > lim || H > 65536 ||
+        (B > 0 && H > 0 && (Lq > Lk ? Lq : Lk) > (int64_t(1) << 36) / (B * H)))
+        return bad(PC_ERR_UNSUPPORTED, "sizes beyond what the kernels index");
+    a.B = int(B), a.Lq = int(Lq), a.Lk = int(Lk), a.H = int(H), a.Hkv = int(Hkv);
+    a.D = int(D), a.scale = float(scale), a.nsplit = 1;
+    auto strides = [&](int64_t *to, const int64_t *s, int64_t L, int64_t heads) {
+        to[0] = s ? s[0] : L * heads * D;
+        to[1] = s ? s[1] : heads * D;
+        to[2] = s ? s[2] : D;
+    };
+    strides(a.qs, qs, Lq, H);
+    strides(a.ks, ks, Lk, Hkv);
+    strides(a.vs, vs, Lk, Hkv);
+    a.q = q, a.k = k, a.v = v, a.slopes = slopes, a.qxyz = qxyz, a.rxyz = rxyz;
+    a.qlen = qlen, a.rlen = rlen;
+    if (B == 0 || H == 0 || (Lq == 0 && Lk == 0)) return PC_OK;
+    int rc = api_current_device(dev);
+    if (rc != PC_OK) return rc;
+    const int d = (*dev)->device;
+    const size_t es = dtype == PC_F32 ? 4 : 2;
+    a.status = (*dev)->status_word;
+    a.timeout_ns = wait_timeout_ns();
+    if (Lq > 0 && (rc = api_check_ptr(q, d, es, "q")) != PC_OK) return rc;
+    if (Lk > 0) {
+        if ((rc = api_check_ptr(k, d, es, "k")) != PC_OK) return rc;
+        if ((rc = api_check_ptr(v, d, es, "v")) != PC_OK) return rc;
+    }
+    if (slopes) {
+        if ((rc = api_check_ptr(slopes, d, 4, "slopes")) != PC_OK) return rc;
+        if (Lq > 0 && (rc = api_check_ptr(qxyz, d, 4, "query_xyz")) != PC_OK) return rc;
+        if (Lk > 0 && (rc = api_check_ptr(rxyz, d, 4, "ref_xyz")) != PC_OK) return rc;
+    }
+    if (qlen && (rc = api_check_ptr(qlen, d, 8, "query_lengths")) != PC_OK) return rc;
+    if (rlen && (rc = api_check_ptr(rlen, d, 8, "ref_lengths")) != PC_OK) return rc;
+    return PC_OK;
+}
+
+int attn_cuda(const char *what, cudaError_t e) {
+    if (e == cudaSuccess) return PC_OK;
+    char m[200];
+    std::snprintf(m, sizeof(m), "%s: %s", what, cudaGetErrorString(e));
+    return api_fail(PC_ERR_CUDA, m);
+}
+
+}  // namespace
+}  // namespace pcn
+
+extern "C" int pc_attention(const void *q, const void *k, const void *v, int dtype, int64_t B,
+                            int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int64_t D,
+                            const int64_t *q_strides, const int64_t *k_strides,
+                            const int64_t *v_strides, double scale, const float *query_xyz,
+                            const float *ref_xyz, const float *slopes,
+                            const int64_t *query_lengths, const int64_t *ref_lengths,
+                            void *out, float *out_lse, void *stream) {
+    using namespace pcn;
+    AttnArgs a{};
+    const DeviceInfo *dev = nullptr;
+    int rc = attn_check("attention", a, &dev, q, k, v, dtype, B, Lq, Lk, H, Hkv, D, q_strides,
+                        k_strides, v_strides, scale, query_xyz, ref_xyz, slopes, query_lengths,
+                        ref_lengths);
+    if (rc != PC_OK || dev == nullptr || Lq == 0) return rc;
+    const int d = dev->device;
+    if ((rc = api_check_ptr(out, d, dtype == PC_F32 ? 4 : 2, "out")) != PC_OK) return rc;
+    if (out_lse && (rc = api_check_ptr(out_lse, d, 4, "out_lse")) != PC_OK) return rc;
+    a.out = out, a.lse = out_lse;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == PC_F32 ? run_pass<float>(*dev, a, ATTN_FWD, nullptr, st)
+                                          : run_pass<bf16>(*dev, a, ATTN_FWD, nullptr, st);
+    return attn_cuda("attention", e);
+}
+
+extern "C" int pc_attention_backward(
+    const void *grad_out, const void *q, const void *k, const void *v, const void *out,
+    const float *lse, int dtype, int64_t B, int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv,
+    int64_t D, const int64_t *q_strides, const int64_t *k_strides, const int64_t *v_strides,
+    double scale, const float *query_xyz, const float *ref_xyz, const float *slopes,
+    const int64_t *query_lengths, const int64_t *ref_lengths, void *grad_q, void *grad_k,
+    void *grad_v, float *grad_slopes, void *stream) {
+    using namespace pcn;
+    AttnArgs a{};
+    const DeviceInfo *dev = nullptr;
+    int rc = attn_check("attention_backward", a, &dev, q, k, v, dtype, B, Lq, Lk, H, Hkv, D,
+                        q_strides, k_strides, v_strides, scale, query_xyz, ref_xyz, slopes,
+                        query_lengths, ref_lengths);
+    if (rc != PC_OK) return rc;
+    if (grad_slopes != nullptr && slopes == nullptr)
+        return api_fail(PC_ERR_INVALID_ARGUMENT, "attention_backward: grad_slopes without slopes");
+    if (dev == nullptr) {  // an empty problem: only the slopes' gradient can have elements
+        if (grad_slopes == nullptr || H == 0) return PC_OK;
+        if ((rc = api_current_device(&dev)) != PC_OK) return rc;
+        if ((rc = api_check_ptr(grad_slopes, dev->device, 4, "grad_slopes")) != PC_OK) return rc;
+        return attn_cuda("attention_backward",
+                         cudaMemsetAsync(grad_slopes, 0, size_t(H) * 4,
+                                         static_cast<cudaStream_t>(stream)));
+    }
+    const int d = dev->device;
+    const size_t es = dtype == PC_F32 ? 4 : 2;
+    if (Lq > 0) {
+        if ((rc = api_check_ptr(grad_out, d, es, "grad_out")) != PC_OK) return rc;
+        if ((rc = api_check_ptr(out, d, es, "out")) != PC_OK) return rc;
+        if ((rc = api_check_ptr(lse, d, 4, "lse")) != PC_OK) return rc;
+        if ((rc = api_check_ptr(grad_q, d, es, "grad_q")) != PC_OK) return rc;
+    }
+    if (Lk > 0) {
+        if ((rc = api_check_ptr(grad_k, d, es, "grad_k")) != PC_OK) return rc;
+        if ((rc = api_check_ptr(grad_v, d, es, "grad_v")) != PC_OK) return rc;
+    }
+    if (grad_slopes && (rc = api_check_ptr(grad_slopes, d, 4, "grad_slopes")) != PC_OK)
+        return rc;
+    a.go = grad_out, a.lse = const_cast<float *>(lse);
+    a.dq = grad_q, a.dk = grad_k, a.dv = grad_v;
+    cudaStream_t st = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = dtype == PC_F32 ? run_backward<float>(*dev, a, out, grad_slopes, st)
+                                          : run_backward<bf16>(*dev, a, out, grad_slopes, st);
+    return attn_cuda("attention_backward", e);
+}

@@ -1,0 +1,59 @@
+// pc_attn.cuh -- what the attention kernels share: their arguments, the
+// three passes and the launchers.
+//
+//   z_ij = scale q_i.k_j - slope_h |x_i - y_j|^2,  j < ref_length,
+//   P = softmax_j(z), out = P v, lse_i = log sum_j exp(z_ij);
+//   delta_i = out_i . dout_i, dP = dout v^T, dS = P (dP - delta),
+//   dq = scale dS k, dk = scale dS^T q, dv = P^T dout,
+//   dslope_h = -sum_ij dS_ij |x_i - y_j|^2.
+//
+// Every pass keeps a tile of rows (its `stationary` side) and walks over the
+// other side in tiles (`streamed`):
+//   FWD  rows q        streams k, v      acc = P v
+//   DQ   rows q, dout  streams k, v      acc = dS k
+//   DKV  rows k, v     streams q, dout   acc = P^T dout and dS^T q, over all
+//                                        query heads that share the key head.
+// The backward pass forms the scores twice instead of adding into dq with
+// atomics, so the order of every sum is fixed.
+#pragma once
+
+#include "pc_internal.h"
+#include "pc_vec.cuh"
+
+#include <stdint.h>
+
+namespace pcn {
+
+enum AttnMode { ATTN_FWD = 0, ATTN_DQ = 1, ATTN_DKV = 2 };
+
+constexpr float ATTN_LOG2E = 1.4426950408889634f;
+constexpr float ATTN_LN2 = 0.6931471805599453f;
+
+struct AttnArgs {
+    const void *q, *k, *v, *go;             // go: dout, packed [B, Lq, H, D]
+    int64_t qs[3], ks[3], vs[3];            // strides (batch, length, head), elements
+    const float *qxyz, *rxyz, *slopes;      // all three or none
+    const int64_t *qlen, *rlen;             // or NULL
+    int B, Lq, Lk, H, Hkv, D;
+    float scale;
+    void *out;                              // FWD
+    float *lse;                             // FWD: written if not NULL
+    const float *delta, *lse2;              // backward: [B, H, Lq], see attn_delta_kernel
+    void *dq, *dk, *dv;
+    // the streamed side in nsplit parts: their accumulators, joined afterwards
+    int nsplit;
+    float *part;     // [nsplit][rows of the output][D] (DKV: dk, then dv)
+    float *part_ml;  // FWD: [nsplit][2][B H Lq] (maximum in base-2 units, sum)
+    // DQ with slopes: per row sums of dS d2, P d2 and dS, [nsplit][3][B H Lq]
+    float *rowsum;
+    int *status;
+    uint64_t timeout_ns;
+};
+
+__device__ __forceinline__ int attn_len(const int64_t *len, int b, int L) {
+    if (len == nullptr) return L;
+    const int64_t n = len[b];
+    return n < 0 ? 0 : n > L ? L : int(n);
+}
+
+}  // namespace pcn

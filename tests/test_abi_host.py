@@ -218,3 +218,65 @@ def test_pytorch3d_adapter_rejects_cpu_tensors(L):
     x = torch.zeros(1, 8, 3)
     with pytest.raises(ValueError, match="CUDA tensor"):
         ball_query(x, x, K=4, radius=0.5)
+
+
+def test_token_operator_validation(L):
+    # layer norm
+    assert L.pc_layer_norm(FAKE, 2, 4, 8, None, None, 0, 1e-5, FAKE, None, None, None) == 1
+    assert L.pc_layer_norm(FAKE, 0, -1, 8, None, None, 0, 1e-5, FAKE, None, None, None) == 1
+    assert L.pc_layer_norm(FAKE, 0, 4, 8, None, None, 1, 1e-5, FAKE, None, None, None) == 1
+    assert L.pc_layer_norm(FAKE, 0, 4, 8, None, None, 0, float("nan"), FAKE, None, None,
+                           None) == 1
+    assert L.pc_layer_norm(FAKE, 0, 4, 8, None, None, 0, 1e-5, FAKE, FAKE, None, None) == 1
+    assert L.pc_layer_norm(FAKE, 0, 4, 8193, None, None, 0, 1e-5, FAKE, None, None, None) == 2
+    assert L.pc_layer_norm(None, 0, 0, 8, None, None, 0, 1e-5, None, None, None, None) == 0
+    assert L.pc_layer_norm_backward(None, None, 1, 0, 8, None, None, None, 0, None, None,
+                                    None, None) == 0
+    # rotary
+    def rot(dtype=0, A=3, F=10, D=64, flags=0, B=1):
+        return L.pc_rotary(FAKE, FAKE, dtype, B, 4, 2, 1, D, None, None, FAKE, FAKE, A, F,
+                           flags, FAKE, FAKE, None)
+    assert rot(dtype=5) == 1
+    assert rot(A=0) == 1
+    assert rot(A=5, F=1) == 1
+    assert rot(F=11) == 1
+    assert "turned channels" in _msg(L)
+    assert rot(F=-1) == 1
+    assert rot(flags=4) == 1
+    assert rot(B=0) == 0
+    # attention
+    def attn(dtype=0, B=1, Lq=4, Lk=4, H=2, Hkv=1, D=64, scale=0.125, x=None, w=None):
+        return L.pc_attention(FAKE, FAKE, FAKE, dtype, B, Lq, Lk, H, Hkv, D, None, None, None,
+                              scale, x, x, w, None, None, FAKE, None, None)
+    assert attn(dtype=3) == 1
+    assert attn(Lq=-1) == 1
+    assert attn(H=3, Hkv=2) == 1
+    assert attn(Hkv=0) == 1
+    assert attn(D=0) == 1
+    assert attn(D=129) == 2
+    assert attn(scale=-1.0) == 1
+    assert attn(scale=float("inf")) == 1
+    assert attn(x=FAKE) == 1
+    assert "go together" in _msg(L)
+    assert attn(B=0) == 0
+    assert attn(B=2 ** 29, Lq=2 ** 20) == 2
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU path")
+def test_token_operators_report_no_device(L):
+    assert L.pc_layer_norm(FAKE, 0, 4, 8, None, None, 0, 1e-5, FAKE, None, None,
+                           None) == binding.PC_ERR_NO_DEVICE
+    assert L.pc_rotary(FAKE, None, 1, 1, 4, 2, 0, 64, None, None, FAKE, FAKE, 3, 10, 0, FAKE,
+                       None, None) == binding.PC_ERR_NO_DEVICE
+    assert L.pc_attention(FAKE, FAKE, FAKE, 1, 1, 4, 4, 2, 1, 64, None, None, None, 0.125,
+                          None, None, None, None, None, FAKE, None,
+                          None) == binding.PC_ERR_NO_DEVICE
+
+
+def test_token_operators_reject_cpu_tensors():
+    import point_cloud_neighbor_gb300 as pc
+    x = torch.zeros(1, 4, 2, 64)
+    for call in (lambda: pc.pc_layer_norm(x), lambda: pc.pc_rotary(x, None, x, x),
+                 lambda: pc.pc_attention(x, x, x)):
+        with pytest.raises(ValueError, match="no CPU path"):
+            call()
