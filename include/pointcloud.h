@@ -619,6 +619,10 @@ int pc_device_status(void *stream, int reset, int32_t *out_status);
  *                         its first tile's copy (nothing is left in flight):
  *                         the producer and that block's consumers run out
  *                         their waits.
+ *   PC_STALL_ATTENTION    the first thread block of a bfloat16 attention
+ *                         launch (forward or backward) never issues the
+ *                         copies of its streamed side.  That block's outputs
+ *                         are unspecified.
  * Each ends as a real timeout does: PC_ERR_DEVICE_TIMEOUT in the status
  * word, -1 in the outputs the stopped blocks did not finish.
  * pc_debug_set_fps_grid_stall(e) sets or clears PC_STALL_FPS_GRID alone.
@@ -626,6 +630,7 @@ int pc_device_status(void *stream, int reset, int32_t *out_status);
 #define PC_STALL_FPS_GRID 1
 #define PC_STALL_FPS_CLUSTER 2
 #define PC_STALL_TILE_STREAM 4
+#define PC_STALL_ATTENTION 8
 void pc_set_wait_timeout_ns(uint64_t ns);
 void pc_debug_set_stall(int mask);
 void pc_debug_set_fps_grid_stall(int enable);

@@ -14,7 +14,7 @@ from .binding import (PC_FPS_AUTO, PC_FPS_BLOCK, PC_FPS_CLUSTER, PC_FPS_GRID,
                       pc_ball_query_grid, pc_chamfer,
                       pc_debug_set_fps_grid_stall, pc_debug_set_stall,
                       PC_STALL_FPS_GRID, PC_STALL_FPS_CLUSTER, PC_STALL_TILE_STREAM,
-                      pc_device_status, pc_fps,
+                      PC_STALL_ATTENTION, pc_device_status, pc_fps,
                       pc_gather_points, pc_grid_build, pc_knn, pc_knn_d,
                       pc_knn_ball_query, pc_knn_ball_query_plan,
                       pc_fps_set_batched,
@@ -36,6 +36,7 @@ __all__ = [
     "three_interpolate", "three_nn", "pc_gather_points", "pc_knn_d",
     "pc_set_sm_reserve", "pc_fps_sm_count", "pc_fps_plan", "pc_debug_set_stall",
     "PC_STALL_FPS_GRID", "PC_STALL_FPS_CLUSTER", "PC_STALL_TILE_STREAM",
+    "PC_STALL_ATTENTION",
     "pc_knn_ball_query", "pc_knn_ball_query_plan", "pc_fps_set_batched",
     "pc_layer_norm", "pc_layer_norm_backward", "layer_norm", "pc_rotary", "rotary",
     "pc_attention", "pc_attention_backward", "attention",

@@ -633,6 +633,7 @@ def pc_debug_set_fps_grid_stall(enable: bool):
 
 
 PC_STALL_FPS_GRID, PC_STALL_FPS_CLUSTER, PC_STALL_TILE_STREAM = 1, 2, 4
+PC_STALL_ATTENTION = 8
 
 
 def pc_debug_set_stall(mask: int):

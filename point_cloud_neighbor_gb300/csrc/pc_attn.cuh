@@ -56,4 +56,12 @@ __device__ __forceinline__ int attn_len(const int64_t *len, int b, int L) {
     return n < 0 ? 0 : n > L ? L : int(n);
 }
 
+// Rows a block keeps in the tensor-core kernels, and rows of a streamed tile.
+constexpr int ATTN_TC_ROWS = 128, ATTN_TC_TILE = 64;
+
+// Whether the tensor-core kernels (pc_attn_tc.cu; bfloat16) take these sizes,
+// strides and alignments: channels a multiple of 8 and 16-byte aligned rows.
+bool attn_tc_fits(const AttnArgs &a, int mode);
+cudaError_t launch_attn_tc(const AttnArgs &a, int mode, int64_t blocks, cudaStream_t st);
+
 }  // namespace pcn

@@ -589,3 +589,24 @@ def test_refusals():
         pc.pc_attention(torch.zeros(1, 4, 1, 129, device=DEV), *[torch.zeros(1, 4, 1, 129, device=DEV)] * 2)
     with pytest.raises(ValueError, match="lse"):
         pc.pc_attention_backward(q, q, k, k, q, torch.zeros(1, 2, 5, device=DEV))
+
+
+def test_a_withheld_copy_ends_with_a_status():
+    # the first block's copies never come: its waits run out, the context stays usable
+    q, k, v, do, kw = attn_inputs(2, 200, 200, 2, 2, 64, torch.bfloat16, True, None, None)
+    want = pc.pc_attention(q, k, v, return_lse=True, **kw)
+    grads = pc.pc_attention_backward(do, q, k, v, *want, **kw)
+    torch.cuda.synchronize()
+    try:
+        pc.pc_set_wait_timeout_ns(50_000_000)
+        pc.pc_debug_set_stall(pc.PC_STALL_ATTENTION)
+        pc.pc_attention(q, k, v, **kw)
+        assert pc.pc_device_status(reset=True) == 4
+        pc.pc_attention_backward(do, q, k, v, *want, **kw)
+        assert pc.pc_device_status(reset=True) == 4
+    finally:
+        pc.pc_debug_set_stall(0)
+        pc.pc_set_wait_timeout_ns(2_000_000_000)
+    assert torch.equal(pc.pc_attention(q, k, v, **kw), want[0])
+    assert all(torch.equal(a, b) for a, b in
+               zip(pc.pc_attention_backward(do, q, k, v, *want, **kw), grads))
