@@ -480,12 +480,12 @@ cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes
     const bool dkv = mode == ATTN_DKV;
     const int64_t LX = dkv ? a.Lk : a.Lq, LY = dkv ? a.Lq : a.Lk, NH = dkv ? a.Hkv : a.H;
     const bool tc = sizeof(T) == 2 && attn_tc_fits(a, mode);
-    const int64_t xr = tc ? ATTN_TC_ROWS : SB, yr = tc ? ATTN_TC_TILE : SB;
+    const int64_t xr = tc ? attn_tc_rows(mode) : SB, yr = tc ? ATTN_TC_TILE : SB;
     const int64_t ntile = (LX + xr - 1) / xr, nyt = (LY + yr - 1) / yr;
     const int64_t base = ntile * NH * a.B;
     const int64_t rows = int64_t(a.B) * LX * NH, hrows = int64_t(a.B) * a.H * a.Lq;
-    // two blocks fit a SM, one of the tensor-core backward kernels
-    const int64_t want = int64_t(dev.sm_count) * (tc && mode != ATTN_FWD ? 1 : 2);
+    // two blocks fit a SM, one of the tensor-core kernels
+    const int64_t want = int64_t(dev.sm_count) * (tc ? 1 : 2);
     a.nsplit = pick_split(want, base, dkv ? nyt * (a.H / a.Hkv) : nyt,
                           rows * a.D * (dkv ? 2 : 1));
     const bool slopes = mode == ATTN_DQ && a.slopes != nullptr && dslopes != nullptr;

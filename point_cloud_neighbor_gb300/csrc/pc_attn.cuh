@@ -57,7 +57,8 @@ __device__ __forceinline__ int attn_len(const int64_t *len, int b, int L) {
 }
 
 // Rows a block keeps in the tensor-core kernels, and rows of a streamed tile.
-constexpr int ATTN_TC_ROWS = 128, ATTN_TC_TILE = 64;
+constexpr int attn_tc_rows(int mode) { return mode == ATTN_FWD ? 256 : 128; }
+constexpr int ATTN_TC_TILE = 64;
 
 // Whether the tensor-core kernels (pc_attn_tc.cu; bfloat16) take these sizes,
 // strides and alignments: channels a multiple of 8 and 16-byte aligned rows.

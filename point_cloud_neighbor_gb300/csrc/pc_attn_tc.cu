@@ -1,17 +1,31 @@
 // pc_attn_tc.cu -- the attention passes of pc_attn.cuh on the tensor cores,
 // for bfloat16.
 //
-// A block keeps 128 rows and walks over the other side in tiles of 64:
+// A block keeps rows (FWD 2 x 128, DQ and DKV 128) and walks over the other
+// side in tiles of 64:
 //   scores   S = X1 Y1^T (and dP = X2 Y2^T), both operands in shared memory,
 //            the result in tensor memory, one lane per row;
-//   weights  a thread owns a row: it reads its scores, adds the bias, and
-//            writes P (and dS) back as bfloat16 over the scores;
+//   weights  a thread owns half a row: it reads its scores and writes P (and
+//            dS) back as bfloat16 over them;
 //   sums     acc += P Y2 (and dS Y1), the weights read from tensor memory,
 //            the same shared-memory tile now contracted along its rows.
 // One warp copies tiles (tensor maps, 128-byte swizzle; zeros past the
-// arrays' ends) and the columns' positions, one warp issues the products,
-// the others compute weights.  The score buffers alternate, so the products
-// of one tile run under the weights of another.
+// arrays' ends), one prepares the positions, one issues the products, 16
+// compute weights in two units of 8: FWD one unit per 128 rows, DQ and DKV
+// units that take tiles in turn.  Each unit has score buffers of its own, so
+// products run under weights.
+//
+// The bias -b |x - y|^2 (b = slope / scale, in units of the raw scores) is
+// 2 b x.y - b |y|^2 - b |x|^2: a product over 27 more channels, in which every
+// number is a sum of three bfloat16 (all pairs of parts above 2^-24), added by
+// two more steps of the same products.  The coordinates are taken relative to
+// the block's first row; the parts are exact to float32, but the three terms
+// cancel where x is near y, which costs up to 2^-20 b R^2.  So a tile takes
+// this way only where slope R^2 <= 256 (R: the farthest of the block's rows
+// and the tile's from the center); elsewhere, and where the slopes' gradient
+// needs the distances themselves, the threads form the distance from the
+// coordinates' differences.  Per score the threads' work falls from about 10
+// instructions to 5.
 //
 // Both operands of a product have one type, and bfloat16 alone would cost P
 // and dS 2^-9 on average: each is written as the sum of two bfloat16 (2^-17)
@@ -30,10 +44,14 @@
 #include "pc_tiles.cuh"
 #include "pointcloud.h"
 
+#include <type_traits>
+
 namespace pcn {
 namespace {
 
-constexpr int XR = ATTN_TC_ROWS, YR = ATTN_TC_TILE;
+constexpr int XR = 128;  // rows of a product
+constexpr int YR = ATTN_TC_TILE;
+constexpr float AUG_MOST = 256.0f;  // of slope R^2: see above
 
 struct AttnMaps {
     CUtensorMap q, k, v, go;
@@ -42,28 +60,29 @@ struct AttnMaps {
 template <int MODE, int DP>
 struct Cfg {
     static constexpr bool BWD = MODE != ATTN_FWD;
-    // Warps of the weights: W sets that take tiles in turn, CH groups of four
-    // in a set that share a tile's columns.  NB score buffers.
-    static constexpr int W = BWD ? 2 : 1, CH = 2;
-    static constexpr int NB = 2;
-    // The weights as a sum of two bfloat16 (see the top of the file).
+    static constexpr int T = BWD ? 1 : 2;       // row tiles of the block
+    static constexpr int CWARPS = 16;           // two units of two halves of four warps
+    static constexpr int THREADS = 32 * (CWARPS + 4);
+    static constexpr int STAGES = DP == 64 ? 6 : 3;
+    // The weights as a sum of two bfloat16.
     static constexpr bool TWO_P = MODE != ATTN_DQ, TWO_S = BWD;
-    static constexpr int STAGES = BWD ? (DP == 64 ? 6 : 3) : (DP == 64 ? 4 : 2);
-    static constexpr int BLOCKS = BWD ? 1 : 2;  // per SM
-    static constexpr int CWARPS = 4 * W * CH;
-    static constexpr int THREADS = 32 * (CWARPS + 2);
-    // tensor memory columns: score buffers first, then the accumulators
-    static constexpr int BUF = BWD ? 2 * YR : YR;
-    static constexpr int ACC = NB * BUF;
-    static constexpr int NACC = MODE == ATTN_DKV ? 2 : 1;
-    static constexpr int COLS = ACC + NACC * DP <= 256 ? 256 : 512;
+    // tensor memory columns: score buffers (FWD two a unit, else one of S and
+    // dP), then the accumulators
+    static constexpr int NBUF = BWD ? 2 : 4, BUF = BWD ? 2 * YR : YR;
+    static constexpr int ACC = NBUF * BUF;
+    static constexpr int NACC = MODE == ATTN_DQ ? 1 : 2;  // FWD: one a unit
+    static constexpr int COLS = 512;
+    static_assert(ACC + NACC * DP <= COLS, "tensor memory");
     static constexpr int XBYTES = XR * DP * 2, YBYTES = YR * DP * 2;
-    static constexpr int XS = BWD ? 2 : 1;
-    static constexpr int COLDATA = 5 * YR * 4;  // x, y, z, lse, delta of the streamed rows
-    static constexpr size_t TILES = size_t(XS) * XBYTES + size_t(STAGES) * 2 * YBYTES;
-    // per row and group: the slope's sums (DQ), or two maxima and a sum (FWD)
-    static constexpr int ROWDATA = W * CH * 3 * XR * 4;
-    static constexpr size_t SMEM = 1024 + TILES + size_t(STAGES) * COLDATA + ROWDATA + 256;
+    static constexpr int XT = BWD ? 2 : T;      // tiles kept
+    static constexpr int XAUG = XR * 64, YAUG = YR * 64;  // 32 channels
+    static constexpr int STAGE = 2 * YBYTES + YAUG;
+    // per stage: x, y, z, -lse, -delta of the streamed rows; flag, bias factor
+    static constexpr int COLF = 5 * YR + 4;
+    static constexpr int ROWF = 2 * 6 * XR;     // per unit: exchanged row values
+    static constexpr size_t SMEM = 1024 + size_t(XT) * XBYTES + size_t(T) * XAUG +
+                                   size_t(STAGES) * (STAGE + COLF * 4) + ROWF * 4 + 512;
+    static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -101,6 +120,46 @@ __device__ __forceinline__ void dist4(const float *cd, int c, float2 nx, float2 
     d0 = __ffma2_rn(a, a, d0), d1 = __ffma2_rn(b, b, d1);
 }
 
+// A number as three bfloat16, the low one of what the others leave.
+struct Parts {
+    float h, m, l;
+    __device__ __forceinline__ explicit Parts(float v) {
+        h = __bfloat162float(__float2bfloat16_rn(v));
+        m = __bfloat162float(__float2bfloat16_rn(v - h));
+        l = (v - h) - m;  // rounded when packed
+    }
+};
+
+// The 27 channels of a row, in 64-byte rows with the 64-byte swizzle:
+// d = position - center; `query`: the side that carries b, else the keys'.
+__device__ __forceinline__ void write_aug(unsigned char *tile, int row, bool query, float dx,
+                                          float dy, float dz, float b) {
+    const float n = fmaf(dz, dz, fmaf(dy, dy, dx * dx));
+    const float f = query ? 2.0f * b : 1.0f;
+    const Parts p[4] = {Parts(f * dx), Parts(f * dy), Parts(f * dz), Parts(query ? b : -n)};
+    float v[32];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        // pairs of parts: hh, hm, mh, hl, lh, mm
+        v[6 * e] = p[e].h;
+        v[6 * e + 1] = query ? p[e].h : p[e].m;
+        v[6 * e + 2] = query ? p[e].m : p[e].h;
+        v[6 * e + 3] = query ? p[e].h : p[e].l;
+        v[6 * e + 4] = query ? p[e].l : p[e].h;
+        v[6 * e + 5] = p[e].m;
+    }
+    const Parts t(-b * n);
+    v[24] = query ? t.h : 1.0f;
+    v[25] = query ? t.m : 1.0f;
+    v[26] = query ? t.l : 1.0f;
+#pragma unroll
+    for (int e = 27; e < 32; ++e) v[e] = 0.0f;
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        Vec<bf16, 8>::store(reinterpret_cast<bf16 *>(tile + row * 64 + ((c ^ ((row >> 1) & 3)) * 16)),
+                            v + 8 * c);
+}
+
 // 32 consecutive channels of a row: bfloat16, or float32 for a part.
 __device__ __forceinline__ void store_row32(bf16 *p, const float (&v)[32], int c0, int D) {
 #pragma unroll
@@ -114,31 +173,34 @@ __device__ __forceinline__ void store_row32(float *p, const float (&v)[32], int 
 }
 
 template <int MODE, int DP, bool BIAS>
-__global__ void __launch_bounds__(Cfg<MODE, DP>::THREADS, Cfg<MODE, DP>::BLOCKS)
+__global__ void __launch_bounds__(Cfg<MODE, DP>::THREADS, 1)
 attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnMaps maps,
                const bool withhold) {
     using C = Cfg<MODE, DP>;
-    constexpr bool BWD = C::BWD;
-    constexpr int STAGES = C::STAGES, NB = C::NB, W = C::W, CH = C::CH;
+    constexpr bool BWD = C::BWD, FWD = !BWD, DKV = MODE == ATTN_DKV;
+    constexpr bool COLS = BIAS || DKV;  // the weights read data of the streamed rows
+    constexpr int STAGES = C::STAGES, T = C::T;
     extern __shared__ unsigned char smem_raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char *X1 = base, *X2 = X1 + (BWD ? C::XBYTES : 0);
-    unsigned char *Y = X1 + C::XS * C::XBYTES;  // stage s: Y1, Y2
-    float *coldata = reinterpret_cast<float *>(Y + size_t(STAGES) * 2 * C::YBYTES);
-    float *rsum = coldata + STAGES * (C::COLDATA / 4);  // [W CH][3][XR]
-    uint64_t *full = reinterpret_cast<uint64_t *>(rsum + C::ROWDATA / 4);
-    uint64_t *empty = full + STAGES, *sfull = empty + STAGES, *pfull = sfull + NB;
-    uint64_t *xfull = pfull + NB, *accfull = xfull + 1, *pvdone = accfull + 1;
-    uint64_t *mxbar = pvdone + 1;  // [4]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mxbar + 4);
-    volatile int *stop = reinterpret_cast<volatile int *>(tmem_slot + 1);
+    unsigned char *X = base;                       // FWD: q of both tiles; else X1, X2
+    unsigned char *Y = X + C::XT * C::XBYTES;      // stage s: Y1, Y2, channels of the bias
+    unsigned char *xaug = Y + size_t(STAGES) * C::STAGE;
+    float *coldata = reinterpret_cast<float *>(xaug + T * C::XAUG);
+    float *rowdata = coldata + STAGES * C::COLF;   // [unit][6][XR]
+    uint64_t *full = reinterpret_cast<uint64_t *>(rowdata + C::ROWF);
+    uint64_t *empty = full + STAGES, *sfull = empty + STAGES, *pfull = sfull + C::NBUF;
+    uint64_t *xfull = pfull + C::NBUF, *accfull = xfull + 1;
+    uint64_t *mxbar = accfull + 1;                 // [unit][quad]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mxbar + 8);
+    int *xr2 = reinterpret_cast<int *>(tmem_slot + 1);  // R^2 of the block's rows, as bits
+    volatile int *stop = reinterpret_cast<volatile int *>(xr2 + 1);
 
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int LX = MODE == ATTN_DKV ? a.Lk : a.Lq, LY = MODE == ATTN_DKV ? a.Lq : a.Lk;
-    const int NH = MODE == ATTN_DKV ? a.Hkv : a.H;
+    const int LX = DKV ? a.Lk : a.Lq, LY = DKV ? a.Lq : a.Lk;
+    const int NH = DKV ? a.Hkv : a.H;
     const int G = a.H / a.Hkv;
-    const int ntile = (LX + XR - 1) / XR;
+    const int ntile = (LX + T * XR - 1) / (T * XR);
     int64_t idx = blockIdx.x;
     const int split = int(idx % a.nsplit);
     idx /= a.nsplit;
@@ -146,33 +208,63 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
     idx /= ntile;
     const int head = int(idx % NH), b = int(idx / NH);
     const int nq = attn_len(a.qlen, b, a.Lq), nk = attn_len(a.rlen, b, a.Lk);
-    const int nx = MODE == ATTN_DKV ? nk : nq, ny = MODE == ATTN_DKV ? nq : nk;
-    const int r0 = tile * XR;
-    const int hk = MODE == ATTN_DKV ? head : head / G;
+    const int nx = DKV ? nk : nq, ny = DKV ? nq : nk;
+    const int r0 = tile * T * XR;
+    const int hk = DKV ? head : head / G;
     const int nyt = (ny + YR - 1) / YR;
-    const int64_t items = nx > r0 ? int64_t(nyt) * (MODE == ATTN_DKV ? G : 1) : 0;
+    const int64_t items = nx > r0 ? int64_t(nyt) * (DKV ? G : 1) : 0;
     const int64_t it0 = items * split / a.nsplit;
     const int n = int(items * (split + 1) / a.nsplit - it0);  // tiles of this block
+    const float *xpos = DKV ? a.rxyz : a.qxyz, *ypos = DKV ? a.qxyz : a.rxyz;
+    // the slopes' gradient needs the distances themselves
+    const bool sums = MODE == ATTN_DQ && BIAS && a.rowsum != nullptr;
 
+    // the row of a thread that computes weights
+    const int quad = warp % 4, half = (warp / 4) % 2, unit = (warp / 8) % 2;
+    const int xt = FWD ? unit : 0;
+    const int row = r0 + xt * XR + quad * 32 + lane;
+    float px = 0.0f, py = 0.0f, pz = 0.0f, cx = 0.0f, cy = 0.0f, cz = 0.0f;
+    if (BIAS && n > 0) {
+        const float *c = xpos + (int64_t(b) * LX + r0) * 3;
+        cx = c[0], cy = c[1], cz = c[2];
+        if (warp < C::CWARPS && row < nx) {
+            const float *p = xpos + (int64_t(b) * LX + row) * 3;
+            px = p[0], py = p[1], pz = p[2];
+        }
+    }
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
-            mbar_init(&full[s], 1);
-            mbar_init(&empty[s], 1 + 4 * CH);
+            mbar_init(&full[s], COLS ? 2 : 1);
+            mbar_init(&empty[s], 1 + (COLS ? (FWD ? 16 : 8) : 0));
         }
-        for (int s = 0; s < NB; ++s) {
+        for (int s = 0; s < C::NBUF; ++s) {
             mbar_init(&sfull[s], 1);
-            mbar_init(&pfull[s], 4 * CH);
+            mbar_init(&pfull[s], 8);
         }
         mbar_init(xfull, 1);
         mbar_init(accfull, 1);
-        mbar_init(pvdone, 1);
-        for (int s = 0; s < 4; ++s) mbar_init(&mxbar[s], CH);
+        for (int s = 0; s < 8; ++s) mbar_init(&mxbar[s], 2);
+        *xr2 = 0;
         *stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == C::CWARPS + 1) tmem_alloc(tmem_slot, C::COLS);
     tc_fence_before();
     __syncthreads();
+    if (BIAS && n > 0) {
+        if (warp < C::CWARPS && half == 0 && (FWD || unit == 0)) {
+            const bool in = row < nx;
+            const float dx = in ? px - cx : 0.0f, dy = in ? py - cy : 0.0f,
+                        dz = in ? pz - cz : 0.0f;
+            write_aug(xaug + xt * C::XAUG, quad * 32 + lane, !DKV, dx, dy, dz,
+                      DKV ? 0.0f : a.slopes[head] / a.scale);
+            // (a NaN or an infinity counts as the largest: no tile takes the products)
+            const float r2 = fmaf(dz, dz, fmaf(dy, dy, dx * dx));
+            atomicMax(xr2, __float_as_int(r2 <= 1e30f ? r2 : 1e30f));
+            fence_proxy_async_smem();
+        }
+        __syncthreads();
+    }
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
 
@@ -185,24 +277,23 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         }
         return __all_sync(0xffffffffu, w == WAIT_OK) != 0;
     };
-    auto item_head = [&](int k) {
-        return MODE == ATTN_DKV ? hk * G + int((it0 + k) / nyt) : head;
-    };
-    auto item_row = [&](int k) {
-        return int(MODE == ATTN_DKV ? (it0 + k) % nyt : it0 + k) * YR;
-    };
+    auto item_head = [&](int k) { return DKV ? hk * G + int((it0 + k) / nyt) : head; };
+    auto item_row = [&](int k) { return int(DKV ? (it0 + k) % nyt : it0 + k) * YR; };
 
     if (warp == C::CWARPS) {
         // ---- copies ---------------------------------------------------------------
-        if (n > 0 && lane == 0) {
-            mbar_arrive_expect_tx(xfull, C::XS * C::XBYTES);
-            const CUtensorMap *m1 = MODE == ATTN_DKV ? &maps.k : &maps.q;
-            const CUtensorMap *m2 = MODE == ATTN_DKV ? &maps.v : &maps.go;
+        if (n > 0 && elect_one()) {
+            mbar_arrive_expect_tx(xfull, C::XT * C::XBYTES);
             for (int p = 0; p < DP / 64; ++p)
                 for (int h = 0; h < 2; ++h) {
-                    const int at = p * XR * 128 + h * YR * 128;
-                    tma_load_4d(X1 + at, m1, 64 * p, r0 + YR * h, head, b, xfull);
-                    if (BWD) tma_load_4d(X2 + at, m2, 64 * p, r0 + YR * h, head, b, xfull);
+                    unsigned char *at = X + p * XR * 128 + h * YR * 128;
+                    const int r = r0 + YR * h;
+                    tma_load_4d(at, DKV ? &maps.k : &maps.q, 64 * p, r, head, b, xfull);
+                    if (FWD)
+                        tma_load_4d(at + C::XBYTES, &maps.q, 64 * p, r + XR, head, b, xfull);
+                    else
+                        tma_load_4d(at + C::XBYTES, DKV ? &maps.v : &maps.go, 64 * p, r, head, b,
+                                    xfull);
                 }
         }
         int issued = 0;
@@ -210,37 +301,15 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
             const int s = k % STAGES;
             if (k >= STAGES && !wait(&empty[s], unsigned((k / STAGES - 1) & 1))) break;
             if (withhold && blockIdx.x == 0) break;
-            const int h = item_head(k), y0 = item_row(k);
-            if (BIAS || MODE == ATTN_DKV) {
-                float *cd = coldata + s * (C::COLDATA / 4);
-                for (int c = lane; c < YR; c += 32) {
-                    // past the array's end: any row, its weight is masked
-                    const int64_t r = min(y0 + c, LY - 1);
-                    if (BIAS) {
-                        const float *p =
-                            (MODE == ATTN_DKV ? a.qxyz : a.rxyz) + (int64_t(b) * LY + r) * 3;
-                        cp_async_4(cd + c, p);
-                        cp_async_4(cd + YR + c, p + 1);
-                        cp_async_4(cd + 2 * YR + c, p + 2);
-                    }
-                    if (MODE == ATTN_DKV) {
-                        const int64_t at = (int64_t(b) * a.H + h) * a.Lq + r;
-                        cp_async_4(cd + 3 * YR + c, a.lse2 + at);
-                        cp_async_4(cd + 4 * YR + c, a.delta + at);
-                    }
-                }
-                cp_async_mbar_arrive(&full[s]);
-                __syncwarp();
-            }
-            if (lane == 0) {
+            if (elect_one()) {
+                const int y0 = item_row(k), hy = DKV ? item_head(k) : hk;
                 mbar_arrive_expect_tx(&full[s], 2 * C::YBYTES);
-                const CUtensorMap *m1 = MODE == ATTN_DKV ? &maps.q : &maps.k;
-                const CUtensorMap *m2 = MODE == ATTN_DKV ? &maps.go : &maps.v;
-                const int hy = MODE == ATTN_DKV ? h : hk;
-                unsigned char *y1 = Y + size_t(s) * 2 * C::YBYTES, *y2 = y1 + C::YBYTES;
+                unsigned char *y1 = Y + size_t(s) * C::STAGE, *y2 = y1 + C::YBYTES;
                 for (int p = 0; p < DP / 64; ++p) {
-                    tma_load_4d(y1 + p * YR * 128, m1, 64 * p, y0, hy, b, &full[s]);
-                    tma_load_4d(y2 + p * YR * 128, m2, 64 * p, y0, hy, b, &full[s]);
+                    tma_load_4d(y1 + p * YR * 128, DKV ? &maps.q : &maps.k, 64 * p, y0, hy, b,
+                                &full[s]);
+                    tma_load_4d(y2 + p * YR * 128, DKV ? &maps.go : &maps.v, 64 * p, y0, hy, b,
+                                &full[s]);
                 }
             }
             issued = k + 1;
@@ -249,108 +318,234 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         if (n > 0) mbar_wait_bounded(xfull, 0, a.timeout_ns);
         for (int k = max(0, issued - STAGES); k < issued; ++k)
             mbar_wait_bounded(&full[k % STAGES], unsigned((k / STAGES) & 1), a.timeout_ns);
-    } else if (warp == C::CWARPS + 1) {
-        // ---- products ---------------------------------------------------------------
-        bool ok = n > 0 && wait(xfull, 0);
-        const uint64_t x1 = smem_desc(smem_u32(X1), 16), x2 = smem_desc(smem_u32(X2), 16);
-        auto scores = [&](int k) {
-            const int s = k % STAGES, buf = k % NB;
-            if (!wait(&full[s], unsigned((k / STAGES) & 1))) return false;
-            unsigned char *y1 = Y + size_t(s) * 2 * C::YBYTES, *y2 = y1 + C::YBYTES;
-            const int valid = ny - item_row(k);
-            if (valid < YR && ny < LY) {
-                const uint4 zero = make_uint4(0, 0, 0, 0);
-                for (int p = 0; p < DP / 64; ++p)
-                    for (int i = valid * 8 + lane; i < YR * 8; i += 32) {
-                        if (BWD) reinterpret_cast<uint4 *>(y1 + p * YR * 128)[i] = zero;
-                        if (MODE != ATTN_DQ) reinterpret_cast<uint4 *>(y2 + p * YR * 128)[i] = zero;
-                    }
-                fence_proxy_async_smem();
-                __syncwarp();
+    } else if (COLS && warp == C::CWARPS + 2) {
+        // ---- positions --------------------------------------------------------------
+        float nxt[2][5];  // of the next tile: loaded a tile ahead
+        auto fetch = [&](int k) {
+            const int h = item_head(k), y0 = item_row(k);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int64_t r = y0 + lane + 32 * i;
+                const bool in = r < ny;
+#pragma unroll
+                for (int e = 0; e < 3; ++e)
+                    nxt[i][e] = BIAS && in ? ypos[(int64_t(b) * LY + r) * 3 + e] : 0.0f;
+                if (DKV) {
+                    const int64_t at = (int64_t(b) * a.H + h) * a.Lq + r;
+                    nxt[i][3] = in ? -a.lse2[at] : -INFINITY;
+                    nxt[i][4] = in ? -a.delta[at] : 0.0f;
+                }
+            }
+        };
+        if (n > 0) fetch(0);
+        for (int k = 0; k < n; ++k) {
+            const int s = k % STAGES;
+            float cur[2][5];
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int e = 0; e < 5; ++e) cur[i][e] = nxt[i][e];
+            const float slope = BIAS ? a.slopes[item_head(k)] : 0.0f;
+            if (k + 1 < n) fetch(k + 1);
+            if (k >= STAGES && !wait(&empty[s], unsigned((k / STAGES - 1) & 1))) break;
+            float *cd = coldata + s * C::COLF;
+            bool direct = true;
+            if (BIAS) {
+                float r2 = __int_as_float(*xr2);
+                float d[2][3];
+                const int valid = ny - item_row(k);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const bool in = lane + 32 * i < valid;
+                    d[i][0] = in ? cur[i][0] - cx : 0.0f;
+                    d[i][1] = in ? cur[i][1] - cy : 0.0f;
+                    d[i][2] = in ? cur[i][2] - cz : 0.0f;
+                    const float t = fmaf(d[i][2], d[i][2], fmaf(d[i][1], d[i][1], d[i][0] * d[i][0]));
+                    r2 = fmaxf(r2, t <= 1e30f ? t : 1e30f);
+                }
+                direct = __any_sync(0xffffffffu, !(fabsf(slope) * r2 <= AUG_MOST)) || sums;
+                if (!direct) {
+                    unsigned char *ya = Y + size_t(s) * C::STAGE + 2 * C::YBYTES;
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        write_aug(ya, lane + 32 * i, DKV, d[i][0], d[i][1], d[i][2],
+                                  DKV ? slope / a.scale : 0.0f);
+                    fence_proxy_async_smem();
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (BIAS && direct)
+#pragma unroll
+                    for (int e = 0; e < 3; ++e) cd[e * YR + lane + 32 * i] = cur[i][e];
+                if (DKV) {
+                    cd[3 * YR + lane + 32 * i] = cur[i][3];
+                    cd[4 * YR + lane + 32 * i] = cur[i][4];
+                }
             }
             if (lane == 0) {
+                cd[5 * YR] = direct ? 1.0f : 0.0f;
+                cd[5 * YR + 1] = -slope / a.scale;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&full[s]);
+        }
+    } else if (warp == C::CWARPS + 1) {
+        // ---- products ---------------------------------------------------------------
+        // The other warps of this one's scheduler are busy: the loop is kept to
+        // few instructions (running stage numbers, descriptors by addition).
+        bool ok = n > 0 && wait(xfull, 0);
+        const uint32_t x1 = smem_operand(smem_u32(X)), x2 = x1 + C::XBYTES / 16;
+        const uint32_t xa = smem_operand(smem_u32(xaug));
+        const uint32_t yk = smem_operand(smem_u32(Y)), yr = smem_operand(smem_u32(Y), YR * 128);
+        const float *flag = coldata + 5 * YR;
+        struct Stage {
+            int s = 0;
+            unsigned phase = 0;
+            __device__ __forceinline__ void next() {
+                if (++s == STAGES) s = 0, phase ^= 1;
+            }
+        } in, out;  // tiles whose scores, whose sums are issued
+        auto tile_ready = [&](int k) {
+            if (!wait(&full[in.s], in.phase)) return false;
+            if (ny < LY) {
+                const int valid = ny - item_row(k);
+                if (valid < YR) {
+                    unsigned char *y1 = Y + size_t(in.s) * C::STAGE, *y2 = y1 + C::YBYTES;
+                    const uint4 zero = make_uint4(0, 0, 0, 0);
+                    for (int p = 0; p < DP / 64; ++p)
+                        for (int i = valid * 8 + lane; i < YR * 8; i += 32) {
+                            if (BWD) reinterpret_cast<uint4 *>(y1 + p * YR * 128)[i] = zero;
+                            if (MODE != ATTN_DQ)
+                                reinterpret_cast<uint4 *>(y2 + p * YR * 128)[i] = zero;
+                        }
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                }
+            }
+            return true;
+        };
+        // the scores of the tile `in` for a unit, into its buffer
+        auto scores = [&](int u, int buf) {
+            const bool bias = BIAS && flag[in.s * C::COLF] == 0.0f;
+            if (elect_one()) {
                 constexpr uint32_t id = mma_idesc(YR, false);
                 const uint32_t d = tmem + buf * C::BUF;
-                const uint64_t d1 = smem_desc(smem_u32(y1), 16), d2 = smem_desc(smem_u32(y2), 16);
+                const uint32_t x = FWD ? x1 + u * (C::XBYTES / 16) : x1;
+                const uint32_t y = yk + in.s * (C::STAGE / 16);
 #pragma unroll
-                for (int i = 0; i < DP / 16; ++i) {
-                    const uint64_t xo = (i / 4) * (XR * 128 / 16) + (i % 4) * 2;
-                    const uint64_t yo = (i / 4) * (YR * 128 / 16) + (i % 4) * 2;
-                    mma_ss(d, x1 + xo, d1 + yo, id, i > 0);
+                for (int i = 0; i < DP / 16; ++i)
+                    mma_ss<SMEM_128B>(d, x + (i / 4) * (XR * 128 / 16) + (i % 4) * 2,
+                                      y + (i / 4) * (YR * 128 / 16) + (i % 4) * 2, id, i > 0);
+                if (bias) {
+                    const uint32_t xb = FWD ? xa + u * (C::XAUG / 16) : xa;
+                    const uint32_t yb = y + 2 * C::YBYTES / 16;
+                    mma_ss<SMEM_64B>(d, xb, yb, id, true);
+                    mma_ss<SMEM_64B>(d, xb + 2, yb + 2, id, true);
                 }
                 if (BWD)
 #pragma unroll
-                    for (int i = 0; i < DP / 16; ++i) {
-                        const uint64_t xo = (i / 4) * (XR * 128 / 16) + (i % 4) * 2;
-                        const uint64_t yo = (i / 4) * (YR * 128 / 16) + (i % 4) * 2;
-                        mma_ss(d + YR, x2 + xo, d2 + yo, id, i > 0);
-                    }
+                    for (int i = 0; i < DP / 16; ++i)
+                        mma_ss<SMEM_128B>(d + YR, x2 + (i / 4) * (XR * 128 / 16) + (i % 4) * 2,
+                                          y + C::YBYTES / 16 + (i / 4) * (YR * 128 / 16) +
+                                              (i % 4) * 2,
+                                          id, i > 0);
                 mma_commit(&sfull[buf]);
             }
-            __syncwarp();
-            return true;
         };
-        for (int k = 0; ok && k < NB - 1 && k < n; ++k) ok = scores(k);
-        for (int k = 0; ok && k < n; ++k) {
-            // the buffer of tile k - 1: its sums were issued before, and
-            // products run in the order of their issue
-            if (k + NB - 1 < n && !(ok = scores(k + NB - 1))) break;
-            const int s = k % STAGES, buf = k % NB;
-            if (!(ok = wait(&pfull[buf], unsigned((k / NB) & 1)))) break;
-            tc_fence_after();
-            if (lane == 0) {
+        // the sums of the tile `out` from a unit's weights
+        auto accumulate = [&](int u, int buf, bool first) {
+            if (elect_one()) {
                 constexpr uint32_t id = mma_idesc(DP, true);
-                unsigned char *y1 = Y + size_t(s) * 2 * C::YBYTES, *y2 = y1 + C::YBYTES;
-                const uint64_t d1 = smem_desc(smem_u32(y1), YR * 128),
-                               d2 = smem_desc(smem_u32(y2), YR * 128);
-                const uint32_t p = tmem + buf * C::BUF, acc = tmem + C::ACC;
+                const uint32_t d1 = yr + out.s * (C::STAGE / 16), d2 = d1 + C::YBYTES / 16;
+                const uint32_t p = tmem + buf * C::BUF, acc = tmem + C::ACC + (FWD ? u * DP : 0);
 #pragma unroll
                 for (int i = 0; i < YR / 16; ++i) {
                     // step i: 16 weights in 8 columns, their low parts in the next 8
                     const uint32_t at = p + 16 * i, as = at + YR;
-                    const uint64_t yo = i * (16 * 128 / 16);
-                    const bool more = k > 0 || i > 0;
-                    if (MODE == ATTN_FWD) {
-                        mma_ts(acc, at, d2 + yo, id, more);
-                        if (C::TWO_P) mma_ts(acc, at + 8, d2 + yo, id, true);
+                    constexpr uint32_t step = 16 * 128 / 16;
+                    const bool more = !first || i > 0;
+                    if (FWD) {
+                        mma_ts<SMEM_128B>(acc, at, d2 + i * step, id, more);
+                        if (C::TWO_P) mma_ts<SMEM_128B>(acc, at + 8, d2 + i * step, id, true);
                     } else {
-                        mma_ts(acc, as, d1 + yo, id, more);
-                        if (C::TWO_S) mma_ts(acc, as + 8, d1 + yo, id, true);
+                        mma_ts<SMEM_128B>(acc, as, d1 + i * step, id, more);
+                        if (C::TWO_S) mma_ts<SMEM_128B>(acc, as + 8, d1 + i * step, id, true);
                     }
-                    if (MODE == ATTN_DKV) {
-                        mma_ts(acc + DP, at, d2 + yo, id, more);
-                        if (C::TWO_P) mma_ts(acc + DP, at + 8, d2 + yo, id, true);
+                    if (DKV) {
+                        mma_ts<SMEM_128B>(acc + DP, at, d2 + i * step, id, more);
+                        if (C::TWO_P) mma_ts<SMEM_128B>(acc + DP, at + 8, d2 + i * step, id, true);
                     }
                 }
-                mma_commit(&empty[s]);
-                if (MODE == ATTN_FWD) mma_commit(pvdone);
             }
-            __syncwarp();
+        };
+        // Products run in the order of their issue, so a score buffer may be
+        // filled again as soon as the sums that read it were issued.
+        if (FWD) {
+            const bool two = r0 + XR < nx;
+            if (ok && (ok = tile_ready(0))) {
+                scores(0, 0);
+                if (two) scores(1, 2);
+                in.next();
+            }
+            for (int k = 0; ok && k < n; ++k) {
+                const int cur = k & 1, nxt = cur ^ 1;
+                const unsigned parity = unsigned(k >> 1) & 1;
+                const bool more = k + 1 < n;
+                if (more && !(ok = tile_ready(k + 1))) break;
+                // (past the last tile the commit alone tells that the sums
+                // before it are complete: a unit may wait for that to rescale)
+                if (more)
+                    scores(0, nxt);
+                else if (elect_one())
+                    mma_commit(&sfull[nxt]);
+                if (!(ok = wait(&pfull[cur], parity))) break;
+                tc_fence_after();
+                accumulate(0, cur, k == 0);
+                if (two) {
+                    if (more)
+                        scores(1, 2 + nxt);
+                    else if (elect_one())
+                        mma_commit(&sfull[2 + nxt]);
+                    if (!(ok = wait(&pfull[2 + cur], parity))) break;
+                    tc_fence_after();
+                    accumulate(1, 2 + cur, k == 0);
+                }
+                if (elect_one()) mma_commit(&empty[out.s]);
+                out.next();
+                in.next();
+            }
+        } else {
+            for (int k = 0; ok && k < 2 && k < n; ++k)
+                if ((ok = tile_ready(k))) {
+                    scores(0, k & 1);
+                    in.next();
+                }
+            for (int k = 0; ok && k < n; ++k) {
+                if (!(ok = wait(&pfull[k & 1], unsigned(k >> 1) & 1))) break;
+                tc_fence_after();
+                accumulate(0, k & 1, k == 0);
+                if (elect_one()) mma_commit(&empty[out.s]);
+                out.next();
+                if (k + 2 < n && (ok = tile_ready(k + 2))) {
+                    scores(0, k & 1);
+                    in.next();
+                }
+            }
         }
-        if (lane == 0) mma_commit(accfull);
+        __syncwarp();
+        if (elect_one()) mma_commit(accfull);
         __syncwarp();
         mbar_wait_bounded(accfull, 0, a.timeout_ns);  // before the tensor memory is freed
-    } else {
+    } else if (warp < C::CWARPS) {
         // ---- weights ------------------------------------------------------------------
-        const int quad = warp % 4, grp = warp / 4, half = grp % CH, wg = grp / CH;
-        const int row = r0 + quad * 32 + lane;
-        const bool live = r0 + quad * 32 < nx;  // of the warp: else nothing is read of its rows
+        const bool live = r0 + xt * XR + quad * 32 < nx;  // else nothing is read of its rows
+        const bool unit_live = r0 + xt * XR < nx;         // else it has no products
         const uint32_t lanes = uint32_t(quad * 32) << 16;
         const float c2 = a.scale * ATTN_LOG2E;
         const float2 c22 = make_float2(c2, c2);
-        float2 nx2 = make_float2(0.0f, 0.0f), ny2 = nx2, nz2 = nx2, nb2 = nx2;
-        if (BIAS) {
-            if (row < nx) {
-                const float *p =
-                    (MODE == ATTN_DKV ? a.rxyz : a.qxyz) + (int64_t(b) * LX + row) * 3;
-                nx2 = make_float2(-p[0], -p[0]);
-                ny2 = make_float2(-p[1], -p[1]);
-                nz2 = make_float2(-p[2], -p[2]);
-            }
-            // the bias in units of the raw scores
-            const float w = -a.slopes[head] / a.scale;
-            if (MODE != ATTN_DKV) nb2 = make_float2(w, w);
-        }
+        const float2 nx2 = make_float2(-px, -px), ny2 = make_float2(-py, -py),
+                     nz2 = make_float2(-pz, -pz);
         float nlse = -INFINITY, ndel = 0.0f;  // DQ: -lse in base 2, -delta
         if (MODE == ATTN_DQ && row < nx) {
             const int64_t at = (int64_t(b) * a.H + head) * a.Lq + row;
@@ -360,27 +555,27 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         float mc = -INFINITY;                        // FWD: the row's maximum, base 2
         float2 l2 = make_float2(0.0f, 0.0f);         // FWD: the row's sum
         float2 wa = l2, we = l2, wd = l2;            // DQ: the slope's sums
-        const bool sums = MODE == ATTN_DQ && BIAS && a.rowsum != nullptr;
-        int hcur = -1;
+        float *rd = rowdata + unit * 6 * XR + quad * 32 + lane;
         bool ok = true;
-        for (int k = wg; k < n; k += W) {
-            const int s = k % STAGES, buf = k % NB;
-            if (!(ok = wait(&sfull[buf], unsigned((k / NB) & 1)))) break;
-            if (!(ok = wait(&full[s], unsigned((k / STAGES) & 1)))) break;
+        int s = FWD ? 0 : unit;
+        unsigned phase = 0;
+        for (int k = FWD ? 0 : unit; k < n; k += FWD ? 1 : 2, s += FWD ? 1 : 2) {
+            if (s >= STAGES) s -= STAGES, phase ^= 1;
+            const int buf = FWD ? 2 * unit + (k & 1) : unit;
+            if (unit_live && !(ok = wait(&sfull[buf], unsigned((k >> 1) & 1)))) break;
+            if (COLS && !(ok = wait(&full[s], phase))) break;
             tc_fence_after();
-            const float *cd = coldata + s * (C::COLDATA / 4) + 32 * half;
+            const float *cd = coldata + s * C::COLF + 32 * half;
             const uint32_t sb = tmem + lanes + buf * C::BUF + 32 * half;
             const int valid = ny - item_row(k) - 32 * half;  // columns of this half, if < 32
-            if (MODE == ATTN_DKV && BIAS && item_head(k) != hcur) {
-                hcur = item_head(k);
-                const float w = -a.slopes[hcur] / a.scale;
-                nb2 = make_float2(w, w);
-            }
-            if (MODE == ATTN_FWD && live) {
+            const bool direct = BIAS && coldata[s * C::COLF + 5 * YR] != 0.0f;
+            const float nb = BIAS ? coldata[s * C::COLF + 5 * YR + 1] : 0.0f;
+            const float2 nb2 = make_float2(nb, nb);
+            if (FWD && live) {
                 uint32_t r[32];
                 tmem_ld32(sb, r);
                 tmem_wait_ld();
-                if (BIAS)
+                if (direct)
 #pragma unroll
                     for (int c = 0; c < 32; c += 4) {
                         float2 d0, d1;
@@ -400,11 +595,11 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
                     m = fmax3(m, __uint_as_float(r[c]), __uint_as_float(r[c + 1]));
                 // the row's maximum over both halves; the slots alternate, so
                 // one exchange a tile is enough
-                float *mx = rsum + (k & 1) * CH * XR + quad * 32 + lane;
+                float *mx = rd + (k & 1) * 2 * XR;
                 mx[half * XR] = m;
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&mxbar[quad]);
-                if (!(ok = wait(&mxbar[quad], unsigned(k & 1)))) break;
+                if (lane == 0) mbar_arrive(&mxbar[unit * 4 + quad]);
+                if (!(ok = wait(&mxbar[unit * 4 + quad], unsigned(k & 1)))) break;
                 m = fmaxf(m, mx[(half ^ 1) * XR]) * c2;
                 // The base of the exponents follows the maximum only when it
                 // grew by more than 2^8 (the weights stay below 256, far from
@@ -418,11 +613,14 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
                     l2.x *= f;
                     l2.y *= f;
                     if (k > 0) {
-                        if (!(ok = wait(pvdone, unsigned((k - 1) & 1)))) break;
+                        // the sums of the tile before come ahead of the next
+                        // tile's scores
+                        if (!(ok = wait(&sfull[buf ^ 1], unsigned(((k + 1) >> 1) & 1)))) break;
                         tc_fence_after();
 #pragma unroll 1
-                        for (int c = 0; c < DP / CH; c += 8) {
-                            const uint32_t at = tmem + lanes + C::ACC + half * (DP / CH) + c;
+                        for (int c = 0; c < DP / 2; c += 8) {
+                            const uint32_t at =
+                                tmem + lanes + C::ACC + unit * DP + half * (DP / 2) + c;
                             uint32_t o[8];
                             tmem_ld8(at, o);
                             tmem_wait_ld();
@@ -449,101 +647,110 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
                     tmem_st8(sb + 16 * h, p);
                     if (C::TWO_P) tmem_st8(sb + 16 * h + 8, lo);
                 }
-            } else if (live) {
+            } else if (BWD && live) {
+                auto weights = [&](auto tail_, auto direct_) {
+                    constexpr bool TAIL = decltype(tail_)::value, DIRECT = decltype(direct_)::value;
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t r[16], g[16], p[8], plo[8], q[8], qlo[8];
-                    tmem_ld16(sb + 16 * h, r);
-                    tmem_ld16(sb + YR + 16 * h, g);
-                    tmem_wait_ld();
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t r[16], g[16], p[8], plo[8], q[8], qlo[8];
+                        tmem_ld16(sb + 16 * h, r);
+                        tmem_ld16(sb + YR + 16 * h, g);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int c = 0; c < 16; c += 4) {
-                        float2 d[2];
-                        if (BIAS) dist4(cd, 16 * h + c, nx2, ny2, nz2, d[0], d[1]);
-                        float4 cl, cdl;
-                        if (MODE == ATTN_DKV) {
-                            cl = *reinterpret_cast<const float4 *>(cd + 3 * YR + 16 * h + c);
-                            cdl = *reinterpret_cast<const float4 *>(cd + 4 * YR + 16 * h + c);
-                        }
-#pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int i = c + 2 * e, col = 16 * h + i;
-                            float2 u = pair(r, i);
-                            if (BIAS) u = __ffma2_rn(d[e], nb2, u);
-                            float2 nl = make_float2(nlse, nlse), nd = make_float2(ndel, ndel);
-                            if (MODE == ATTN_DKV) {
-                                nl = e == 0 ? make_float2(-cl.x, -cl.y) : make_float2(-cl.z, -cl.w);
-                                nd = e == 0 ? make_float2(-cdl.x, -cdl.y)
-                                            : make_float2(-cdl.z, -cdl.w);
+                        for (int c = 0; c < 16; c += 4) {
+                            float2 d[2];
+                            if (DIRECT) dist4(cd, 16 * h + c, nx2, ny2, nz2, d[0], d[1]);
+                            float4 cl, cdl;
+                            if (DKV) {
+                                cl = *reinterpret_cast<const float4 *>(cd + 3 * YR + 16 * h + c);
+                                cdl = *reinterpret_cast<const float4 *>(cd + 4 * YR + 16 * h + c);
                             }
-                            u = __ffma2_rn(u, c22, nl);
-                            u.x = ex2(u.x);
-                            u.y = ex2(u.y);
-                            float2 ds = __fmul2_rn(u, __fadd2_rn(pair(g, i), nd));
-                            if (valid < 32) {
-                                if (col >= valid) u.x = ds.x = 0.0f;
-                                if (col + 1 >= valid) u.y = ds.y = 0.0f;
-                            }
-                            if (sums) {
-                                if (valid < 32) {  // 0 times a masked NaN
-                                    if (col >= valid) d[e].x = 0.0f;
-                                    if (col + 1 >= valid) d[e].y = 0.0f;
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int i = c + 2 * e, col = 16 * h + i;
+                                float2 u = pair(r, i);
+                                if (DIRECT) u = __ffma2_rn(d[e], nb2, u);
+                                float2 nl = make_float2(nlse, nlse), nd = make_float2(ndel, ndel);
+                                if (DKV) {
+                                    nl = e == 0 ? make_float2(cl.x, cl.y) : make_float2(cl.z, cl.w);
+                                    nd = e == 0 ? make_float2(cdl.x, cdl.y)
+                                                : make_float2(cdl.z, cdl.w);
                                 }
-                                wd = __fadd2_rn(wd, ds);
-                                wa = __ffma2_rn(ds, d[e], wa);
-                                we = __ffma2_rn(u, d[e], we);
+                                u = __ffma2_rn(u, c22, nl);
+                                u.x = ex2(u.x);
+                                u.y = ex2(u.y);
+                                float2 ds = __fmul2_rn(u, __fadd2_rn(pair(g, i), nd));
+                                if (TAIL) {
+                                    if (col >= valid) u.x = ds.x = 0.0f;
+                                    if (col + 1 >= valid) u.y = ds.y = 0.0f;
+                                }
+                                if (MODE == ATTN_DQ && DIRECT && sums) {
+                                    wd = __fadd2_rn(wd, ds);
+                                    wa = __ffma2_rn(ds, d[e], wa);
+                                    we = __ffma2_rn(u, d[e], we);
+                                }
+                                if (DKV) split_bf16(u, p[i / 2], plo[i / 2]);
+                                split_bf16(ds, q[i / 2], qlo[i / 2]);
                             }
-                            if (MODE == ATTN_DKV) split_bf16(u, p[i / 2], plo[i / 2]);
-                            split_bf16(ds, q[i / 2], qlo[i / 2]);
                         }
+                        if (DKV) {
+                            tmem_st8(sb + 16 * h, p);
+                            if (C::TWO_P) tmem_st8(sb + 16 * h + 8, plo);
+                        }
+                        tmem_st8(sb + YR + 16 * h, q);
+                        if (C::TWO_S) tmem_st8(sb + YR + 16 * h + 8, qlo);
                     }
-                    if (MODE == ATTN_DKV) {
-                        tmem_st8(sb + 16 * h, p);
-                        if (C::TWO_P) tmem_st8(sb + 16 * h + 8, plo);
-                    }
-                    tmem_st8(sb + YR + 16 * h, q);
-                    if (C::TWO_S) tmem_st8(sb + YR + 16 * h + 8, qlo);
+                };
+                constexpr std::true_type yes{};
+                constexpr std::false_type no{};
+                if (valid < 32) {
+                    if (BIAS && direct)
+                        weights(yes, std::integral_constant<bool, BIAS>{});
+                    else
+                        weights(yes, no);
+                } else {
+                    if (BIAS && direct)
+                        weights(no, std::integral_constant<bool, BIAS>{});
+                    else
+                        weights(no, no);
                 }
             }
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&pfull[buf]);
-                mbar_arrive(&empty[s]);
+                if (unit_live) mbar_arrive(&pfull[buf]);
+                if (COLS) mbar_arrive(&empty[s]);
             }
         }
         const int64_t hrow = (int64_t(b) * a.H + head) * a.Lq + row;  // FWD, DQ
         const int64_t hrows = int64_t(a.B) * a.H * a.Lq;
         if (MODE == ATTN_DQ && BIAS) {
+            // the sums of a row's four groups, in the exchange buffer as [unit][half][3]
             if (sums) {
-                float *t = rsum + grp * 3 * XR + quad * 32 + lane;
-                t[0] = wa.x + wa.y;
-                t[XR] = we.x + we.y;
-                t[2 * XR] = wd.x + wd.y;
+                rd[(half * 3) * XR] = wa.x + wa.y;
+                rd[(half * 3 + 1) * XR] = we.x + we.y;
+                rd[(half * 3 + 2) * XR] = wd.x + wd.y;
             }
             named_barrier_sync(1, C::CWARPS * 32);
-            if (sums && grp == 0 && row < LX) {
+            if (sums && unit == 0 && half == 0 && row < LX) {
                 float *o = a.rowsum + split * 3 * hrows + hrow;
 #pragma unroll
                 for (int e = 0; e < 3; ++e) {
-                    float t = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < W * CH; ++i)
-                        t += rsum[(i * 3 + e) * XR + quad * 32 + lane];
+                    const float t = (rd[e * XR] + rd[(3 + e) * XR]) +
+                                    (rd[(6 + e) * XR] + rd[(9 + e) * XR]);
                     o[e * hrows] = row < nx ? t : 0.0f;
                 }
             }
         }
         float l = l2.x + l2.y;
-        if (MODE == ATTN_FWD) {  // the row's sum over both halves
-            float *t = rsum + 2 * CH * XR + quad * 32 + lane;
-            t[half * XR] = l;
+        if (FWD) {  // the row's sum over both halves
+            rd[(4 + half) * XR] = l;
             named_barrier_sync(1, C::CWARPS * 32);
-            l = t[0] + t[XR];
+            l = rd[4 * XR] + rd[5 * XR];
         }
-        const bool any = MODE == ATTN_FWD ? row < nx && l > 0.0f : row < nx;
-        if (MODE == ATTN_FWD && row < LX && half == 0) {
+        const bool any = FWD ? row < nx && l > 0.0f : row < nx;
+        if (FWD && row < LX && half == 0) {
             if (a.nsplit > 1) {
                 a.part_ml[int64_t(split) * 2 * hrows + hrow] = mc;
                 a.part_ml[(int64_t(split) * 2 + 1) * hrows + hrow] = l;
@@ -555,30 +762,29 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         tc_fence_after();
         const int64_t orow = (int64_t(b) * LX + row) * NH + head;
         const int64_t rows = int64_t(a.B) * LX * NH;
-        // the groups share the accumulators' columns
-        for (int ch = grp; ch < C::NACC * DP / 32; ch += W * CH) {
+        // the groups of a row share its accumulators' columns
+        const bool have = n > 0 && ok && unit_live;
+        constexpr int CHUNKS = (FWD ? 1 : C::NACC) * DP / 32;
+        for (int ch = FWD ? half : 2 * unit + half; ch < CHUNKS; ch += FWD ? 2 : 4) {
             const int acc = ch / (DP / 32), c0 = (ch % (DP / 32)) * 32;
             uint32_t r[32];
             float v[32];
             __syncwarp();
-            if (n > 0 && ok) {
-                tmem_ld32(tmem + lanes + C::ACC + ch * 32, r);
+            if (have) {
+                tmem_ld32(tmem + lanes + C::ACC + (FWD ? unit * DP : 0) + ch * 32, r);
                 tmem_wait_ld();
             }
-            const float f = a.nsplit > 1 ? 1.0f
-                            : MODE == ATTN_FWD ? 1.0f / l
-                            : acc == 0         ? a.scale
-                                               : 1.0f;
+            const float f = a.nsplit > 1 ? 1.0f : FWD ? 1.0f / l : acc == 0 ? a.scale : 1.0f;
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-                v[e] = n > 0 && ok && any ? __uint_as_float(r[e]) * f : 0.0f;
+                v[e] = have && any ? __uint_as_float(r[e]) * f : 0.0f;
             if (row >= LX) {
                 // past the array's end: nothing to store
             } else if (a.nsplit > 1) {
                 store_row32(a.part + ((int64_t(acc) * a.nsplit + split) * rows + orow) * a.D + c0,
                             v, c0, a.D);
             } else {
-                void *o = MODE == ATTN_FWD ? a.out : MODE == ATTN_DQ ? a.dq : acc ? a.dv : a.dk;
+                void *o = FWD ? a.out : MODE == ATTN_DQ ? a.dq : acc ? a.dv : a.dk;
                 store_row32(static_cast<bf16 *>(o) + orow * a.D + c0, v, c0, a.D);
             }
         }

@@ -76,15 +76,32 @@ __device__ __forceinline__ void tc_fence_after() {
     asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
 }
 
+// True in one lane of a converged warp.  The products' operands live in
+// uniform registers: under a branch on a plain lane index the compiler has to
+// loop over the lanes for every instruction (80 to 150 cycles each, measured).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.b32 %0, 1, 0, p;\n\t}"
+        : "=r"(r));
+    return r != 0;
+}
+
 // --- products -------------------------------------------------------------------
 
-// Shared-memory operand of bfloat16 in 128-byte rows, 128-byte swizzle, 8-row
-// groups of 1024 bytes.  `lead`: bytes between the 64-element panels of an
-// operand whose rows are the contraction (MN-major); unused otherwise.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
-    return uint64_t((addr >> 4) & 0x3fff) | (uint64_t((lead >> 4) & 0x3fff) << 16) |
-           (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) | (uint64_t(2) << 61);
+// Shared-memory operands of bfloat16, as the two words of their descriptor.
+// The low word holds the address / 16 and, for an operand contracted along its
+// rows (MN-major), the bytes / 16 between its 64-element panels; address
+// offsets are added to it.  The high word: rows of 128 bytes with the 128-byte
+// swizzle in 8-row groups of 1024 bytes, or rows of 64 bytes with the 64-byte
+// swizzle in groups of 512.
+__device__ __forceinline__ uint32_t smem_operand(uint32_t addr, uint32_t lead = 16) {
+    return (addr >> 4) | ((lead >> 4) << 16);
 }
+constexpr uint32_t SMEM_128B = (1024 >> 4) | (1u << 14) | (2u << 29);
+constexpr uint32_t SMEM_64B = (512 >> 4) | (1u << 14) | (4u << 29);
 
 // bfloat16 x bfloat16 -> float32, M = 128.  `b_rows`: B's contraction runs
 // over its rows (MN-major) instead of along them.
@@ -93,23 +110,29 @@ __host__ __device__ constexpr uint32_t mma_idesc(int N, bool b_rows) {
            (uint32_t(N / 8) << 17) | (uint32_t(128 / 16) << 24);
 }
 
-// One thread.  D (tensor memory) = A B + (accumulate ? D : 0), 16 deep.
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+// One thread.  D (tensor memory) = A B + (accumulate ? D : 0), 16 deep; A and B
+// in shared memory, or A in tensor memory.
+template <uint32_t HI>
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 ra, rb;\n\t"
+        "mov.b64 ra, {%1, %5};\n\t"
+        "mov.b64 rb, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], ra, rb, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(uint32_t(accumulate)), "n"(HI)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+template <uint32_t HI>
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                        bool accumulate) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 rb;\n\t"
+        "mov.b64 rb, {%2, %5};\n\t"
         "setp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(accumulate))
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], rb, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(uint32_t(accumulate)), "n"(HI)
         : "memory");
 }
 // `bar` completes (one arrival) when this thread's products so far have.
