@@ -507,7 +507,7 @@ typedef enum pc_dtype { PC_F32 = 0, PC_BF16 = 1 } pc_dtype;
  *   grad_x = rstd (g - mean(g) - xhat mean(g xhat)),
  *   grad_weight = sum over rows of grad_out * xhat,  grad_bias = of grad_out.
  * grad_weight and grad_bias ([C] of param_dtype) may be NULL.  They are
- * summed in a fixed order: scratch of at most 4 blocks per SM times 2 C
+ * summed in a fixed order: scratch of at most 8 blocks per SM times 2 C
  * float32 from the library's stream-ordered pool.
  */
 int pc_layer_norm(const void *x, int dtype, int64_t rows, int64_t C, const void *weight,
@@ -532,7 +532,7 @@ int pc_layer_norm_backward(const void *grad_out, const void *x, int dtype, int64
  * those of out_q and out_k.
  *
  *   positions  [B, L, A] float32, 1 <= A <= 4.  freqs [A, F] float32,
- *              2 A F <= D, A F <= 4096.
+ *              2 A F <= D <= 16384, A F <= 4096.
  *   out_q, out_k  packed; they must not overlap the inputs.
  */
 #define PC_ROTARY_HALF_SPLIT 1

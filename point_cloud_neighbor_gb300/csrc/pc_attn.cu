@@ -432,8 +432,9 @@ attn_slope_kernel(const AttnArgs a, float *dslopes) {
 template <class T, int MODE, int DP>
 cudaError_t simt_launch(const AttnArgs &a, bool vec, int64_t blocks, cudaStream_t st) {
     constexpr size_t smem = simt_smem(MODE, DP);
-    const cudaError_t e = cudaFuncSetAttribute(
-        attn_simt_kernel<T, MODE, DP>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e =
+        allow_smem(attn_simt_kernel<T, MODE, DP>, int(smem), a.device, done);
     if (e != cudaSuccess) return e;
     attn_simt_kernel<T, MODE, DP><<<unsigned(blocks), ST, smem, st>>>(a, vec);
     return cudaGetLastError();
@@ -591,6 +592,7 @@ int attn_check(const char *what, AttnArgs &a, const DeviceInfo **dev, const void
     if (rc != PC_OK) return rc;
     const int d = (*dev)->device;
     const size_t es = dtype == PC_F32 ? 4 : 2;
+    a.device = d;
     a.status = (*dev)->status_word;
     a.timeout_ns = wait_timeout_ns();
     if (Lq > 0 && (rc = api_check_ptr(q, d, es, "q")) != PC_OK) return rc;

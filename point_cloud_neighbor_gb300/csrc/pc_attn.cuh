@@ -46,6 +46,7 @@ struct AttnArgs {
     float *part_ml;  // FWD: [nsplit][2][B H Lq] (maximum in base-2 units, sum)
     // DQ with slopes: per row sums of dS d2, P d2 and dS, [nsplit][3][B H Lq]
     float *rowsum;
+    int device;
     int *status;
     uint64_t timeout_ns;
 };

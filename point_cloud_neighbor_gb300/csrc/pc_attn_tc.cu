@@ -835,9 +835,9 @@ bool make_map(CUtensorMap *map, const void *p, const int64_t *s, int64_t B, int6
 template <int MODE, int DP, bool BIAS>
 cudaError_t tc_launch(const AttnArgs &a, const AttnMaps &m, int64_t blocks, cudaStream_t st) {
     using C = Cfg<MODE, DP>;
+    static std::atomic<uint64_t> done{0};
     const cudaError_t e =
-        cudaFuncSetAttribute(attn_tc_kernel<MODE, DP, BIAS>,
-                             cudaFuncAttributeMaxDynamicSharedMemorySize, int(C::SMEM));
+        allow_smem(attn_tc_kernel<MODE, DP, BIAS>, int(C::SMEM), a.device, done);
     if (e != cudaSuccess) return e;
     attn_tc_kernel<MODE, DP, BIAS><<<unsigned(blocks), C::THREADS, C::SMEM, st>>>(
         a, m, (debug_stall() & PC_STALL_ATTENTION) != 0);

@@ -6,6 +6,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include <atomic>
+
 namespace pcn {
 
 // Cached properties of one device, filled once per device.
@@ -33,6 +35,19 @@ struct DeviceInfo {
 cudaError_t scratch_alloc(const DeviceInfo &dev, void **p, size_t bytes,
                           cudaStream_t stream);
 cudaError_t scratch_free(void *p, cudaStream_t stream);
+
+// Lets `kernel` take `bytes` of dynamic shared memory on device `dev`; asks the
+// runtime once per kernel and device (`done`: a bit per device, kept by the
+// caller).
+template <class K>
+cudaError_t allow_smem(K kernel, int bytes, int dev, std::atomic<uint64_t> &done) {
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+    return e;
+}
 
 // Device-side wait bound, in ns (see pc_set_wait_timeout_ns).
 uint64_t wait_timeout_ns();

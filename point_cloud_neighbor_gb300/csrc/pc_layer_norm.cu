@@ -6,13 +6,21 @@
 //   dx = rstd (g - mean(g) - xhat mean(g xhat)),
 //   dw = sum_rows dy xhat,  db = sum_rows dy.
 //
-// Bound: memory.  A row is read once into registers (by one warp, or by a
-// block of 256 threads for C > 1024) and written once; the variance is summed
-// from the centred values in registers, so no cancellation of sums of
-// squares.  All sums are float32.
+// Bound: memory.  A row is read once into the registers of TPR threads (8 for
+// C <= 128, a warp up to C of about 1000, a block of 256 beyond) and written
+// once; the variance is summed from the centred values in registers, so no
+// cancellation of sums of squares.  All sums are float32.
+//
+// Rows of an odd C start at any multiple of the element size, yet the rows
+// together are one packed array.  A thread group takes every G-th row, G a
+// multiple of the V elements of a 16-byte vector, so its rows all start at
+// the same offset within a vector: it reads the aligned vectors that cover
+// the row, the first and last of them in part.  So every C has 16-byte loads,
+// and a thread's columns are the same in all its rows: weight, bias and the
+// columns' gradient sums stay in registers.
 //
 // The weight gradients need a sum over all rows.  Each backward block walks
-// its share of the rows with the columns' sums in registers, joins its warps
+// its share of the rows with the columns' sums in registers, joins its groups
 // in a fixed order and writes one row of partial sums; a second kernel adds
 // the blocks' rows in a fixed order.  No atomics: the result does not change
 // from run to run.
@@ -42,7 +50,8 @@ struct LnArgs {
 template <int TPR>
 __device__ __forceinline__ float row_sum(float v, float *red) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o >>= 1)
+        v += __shfl_xor_sync(0xffffffffu, v, o);
     if (TPR > 32) {
         __syncthreads();  // red may still be read from the last sum
         if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
@@ -54,162 +63,224 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
     return v;
 }
 
-template <class WT, int V>
-__device__ __forceinline__ void load_param(const void *p, int at, float fill, float *v) {
-    if (p == nullptr) {
+// The V elements at p[at] as they are in memory.  Some may belong to the
+// neighbouring rows; a vector that would leave the array of `total` elements
+// is read element by element, zeros outside.
+template <class T, int V>
+struct Raw {
+    T v[V];
+    __device__ __forceinline__ void load(const T *p, int64_t at, int64_t total) {
+        if (V == 1) {
+            v[0] = p[at];
+        } else if (at + V <= total) {
+            *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(p + at);
+        } else {
 #pragma unroll
-        for (int e = 0; e < V; ++e) v[e] = fill;
-    } else {
-        Vec<WT, V>::load(static_cast<const WT *>(p) + at, v);
+            for (int e = 0; e < V; ++e) v[e] = at + e < total ? p[at + e] : T(0.0f);
+        }
+    }
+    // as float32, 0 where the column col + e is not one of the row
+    __device__ __forceinline__ void get(int col, int C, float *f) const {
+        Vec<T, V>::load(v, f);
+        zero(col, C, f);
+    }
+    static __device__ __forceinline__ void zero(int col, int C, float *f) {
+        if (V > 1 ? col < 0 || col + V > C : col >= C)
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (col + e < 0 || col + e >= C) f[e] = 0.0f;
+    }
+    static __device__ __forceinline__ void store(T *p, int64_t at, int col, int C,
+                                                 const float *f) {
+        if (V == 1 || (col >= 0 && col + V <= C)) {
+            Vec<T, V>::store(p + at, f);
+        } else {
+#pragma unroll
+            for (int e = 0; e < V; ++e)
+                if (col + e >= 0 && col + e < C) Vec<T, 1>::store(p + at + e, f + e);
+        }
+    }
+};
+
+template <class WT, int V>
+__device__ __forceinline__ void load_param(const void *p, int col, int C, float fill, float *v) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+        v[e] = fill;
+        if (p != nullptr && col + e >= 0 && col + e < C)
+            Vec<WT, 1>::load(static_cast<const WT *>(p) + col + e, v + e);
     }
 }
 
-// A thread holds the vectors t, t + TPR, ... (N of V elements) of its row.
+// A thread holds the vectors t, t + TPR, ... (N of V elements) that cover its
+// row; vector i has the columns V (t + i TPR) - shift and on.  The next row is
+// on its way while one is worked on.
 template <class T, class WT, int V, int N, int TPR>
 __global__ void __launch_bounds__(LN_THREADS) ln_forward_kernel(const LnArgs a) {
     __shared__ float red[LN_THREADS / 32];
     constexpr int RPB = LN_THREADS / TPR;
-    const int64_t row = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR;
-    if (row >= a.rows) return;  // a whole warp, or (TPR = 256) never
     const int t = threadIdx.x % TPR;
-    const T *x = static_cast<const T *>(a.x) + row * a.C;
-    float v[N][V];
-    float s = 0.0f;
+    const int64_t step = int64_t(gridDim.x) * RPB, total = a.rows * a.C;
+    int64_t row = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR;
+    const int shift = V > 1 ? int(row * a.C % V) : 0;
+    const T *x = static_cast<const T *>(a.x);
+    T *y = static_cast<T *>(a.y);
+    Raw<T, V> raw[N];
+    auto fetch = [&](int64_t r) {
+        if (r < a.rows)
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const int at = (t + i * TPR) * V;
-        if (at < a.C) {
-            Vec<T, V>::load(x + at, v[i]);
-        } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e) v[i][e] = 0.0f;
-        }
-    }
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int e = 0; e < V; ++e) s += v[i][e];
-    const float mean = row_sum<TPR>(s, red) / float(a.C);
-    float q = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; ++i)
-        if ((t + i * TPR) * V < a.C)
-#pragma unroll
-            for (int e = 0; e < V; ++e) {
-                v[i][e] -= mean;
-                q = fmaf(v[i][e], v[i][e], q);
+            for (int i = 0; i < N; ++i) {
+                const int col = (t + i * TPR) * V - shift;
+                if (col < a.C) raw[i].load(x, r * a.C + col, total);
             }
-    const float rstd = 1.0f / sqrtf(row_sum<TPR>(q, red) / float(a.C) + a.eps);
-    T *y = static_cast<T *>(a.y) + row * a.C;
+    };
+    fetch(row);
+    float w[N][V], b[N][V];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int at = (t + i * TPR) * V;
-        if (at < a.C) {
-            float w[V], b[V];
-            load_param<WT, V>(a.w, at, 1.0f, w);
-            load_param<WT, V>(a.b, at, 0.0f, b);
-#pragma unroll
-            for (int e = 0; e < V; ++e) v[i][e] = fmaf(v[i][e] * rstd, w[e], b[e]);
-            Vec<T, V>::store(y + at, v[i]);
-        }
+        const int col = (t + i * TPR) * V - shift;
+        load_param<WT, V>(a.w, col, a.C, 1.0f, w[i]);
+        load_param<WT, V>(a.b, col, a.C, 0.0f, b[i]);
     }
-    if (t == 0 && a.mean != nullptr) {
-        a.mean[row] = mean;
-        a.rstd[row] = rstd;
+    // the groups of a warp go round together: they share its shuffles
+    const int64_t rounds = (a.rows + step - 1) / step;
+    for (int64_t k = 0; k < rounds; ++k, row += step) {
+        const bool in = row < a.rows;
+        float v[N][V];
+        float s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) raw[i].get((t + i * TPR) * V - shift, a.C, v[i]);
+        fetch(row + step);
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+#pragma unroll
+            for (int e = 0; e < V; ++e) s += v[i][e];
+        const float mean = row_sum<TPR>(s, red) / float(a.C);
+        float q = 0.0f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[i][e] -= mean;
+            Raw<T, V>::zero((t + i * TPR) * V - shift, a.C, v[i]);
+#pragma unroll
+            for (int e = 0; e < V; ++e) q = fmaf(v[i][e], v[i][e], q);
+        }
+        const float rstd = 1.0f / sqrtf(row_sum<TPR>(q, red) / float(a.C) + a.eps);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int col = (t + i * TPR) * V - shift;
+#pragma unroll
+            for (int e = 0; e < V; ++e) v[i][e] = fmaf(v[i][e] * rstd, w[i][e], b[i][e]);
+            if (in && col < a.C) Raw<T, V>::store(y, row * a.C + col, col, a.C, v[i]);
+        }
+        if (in && t == 0 && a.mean != nullptr) {
+            a.mean[row] = mean;
+            a.rstd[row] = rstd;
+        }
     }
 }
 
 template <class T, class WT, int V, int N, int TPR>
 __global__ void __launch_bounds__(LN_THREADS) ln_backward_kernel(const LnArgs a) {
     __shared__ float red[LN_THREADS / 32];
-    extern __shared__ float col[];  // [2][C], TPR = 32 only
+    extern __shared__ float colsum[];  // [2][C], TPR < 256 only
     constexpr int RPB = LN_THREADS / TPR;
     const int t = threadIdx.x % TPR;
-    float dw[N][V], db[N][V];
+    const int64_t step = int64_t(gridDim.x) * RPB, total = a.rows * a.C;
+    int64_t row = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR;
+    const int shift = V > 1 ? int(row * a.C % V) : 0;
+    const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
+    T *dx = static_cast<T *>(a.y);
+    Raw<T, V> rx[N], rg[N];
+    float mean_n = 0.0f, rstd_n = 0.0f;
+    auto fetch = [&](int64_t r) {
+        if (r < a.rows) {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
+            for (int i = 0; i < N; ++i) {
+                const int col = (t + i * TPR) * V - shift;
+                if (col < a.C) {
+                    rx[i].load(x, r * a.C + col, total);
+                    rg[i].load(dy, r * a.C + col, total);
+                }
+            }
+            mean_n = a.mean[r], rstd_n = a.rstd[r];
+        }
+    };
+    fetch(row);
+    float dw[N][V], db[N][V], w[N][V];
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+        load_param<WT, V>(a.w, (t + i * TPR) * V - shift, a.C, 1.0f, w[i]);
 #pragma unroll
         for (int e = 0; e < V; ++e) dw[i][e] = db[i][e] = 0.0f;
+    }
     const float inv_c = 1.0f / float(a.C);
-    for (int64_t row = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR; row < a.rows;
-         row += int64_t(gridDim.x) * RPB) {
-        const T *x = static_cast<const T *>(a.x) + row * a.C;
-        const T *dy = static_cast<const T *>(a.dy) + row * a.C;
+    const int64_t rounds = (a.rows + step - 1) / step;
+    for (int64_t k = 0; k < rounds; ++k, row += step) {
+        const bool in = row < a.rows;
         float xv[N][V], gv[N][V];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int at = (t + i * TPR) * V;
-            if (at < a.C) {
-                Vec<T, V>::load(x + at, xv[i]);
-                Vec<T, V>::load(dy + at, gv[i]);
-            }
+            const int col = (t + i * TPR) * V - shift;
+            rx[i].get(in ? col : a.C, a.C, xv[i]);  // past the rows: nothing was read,
+            rg[i].get(in ? col : a.C, a.C, gv[i]);  // no part in the columns' sums
         }
-        const float mean = a.mean[row], rstd = a.rstd[row];
+        const float mean = mean_n, rstd = rstd_n;
+        fetch(row + step);
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = (t + i * TPR) * V;
-            if (at < a.C) {
-                float w[V];
-                load_param<WT, V>(a.w, at, 1.0f, w);
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    const float xh = (xv[i][e] - mean) * rstd;
-                    dw[i][e] = fmaf(gv[i][e], xh, dw[i][e]);
-                    db[i][e] += gv[i][e];
-                    const float g = gv[i][e] * w[e];
-                    s0 += g;
-                    s1 = fmaf(g, xh, s1);
-                    xv[i][e] = xh;
-                    gv[i][e] = g;
-                }
+            for (int e = 0; e < V; ++e) {  // (dy is 0 outside the row)
+                const float xh = (xv[i][e] - mean) * rstd;
+                dw[i][e] = fmaf(gv[i][e], xh, dw[i][e]);
+                db[i][e] += gv[i][e];
+                const float g = gv[i][e] * w[i][e];
+                s0 += g;
+                s1 = fmaf(g, xh, s1);
+                xv[i][e] = xh;
+                gv[i][e] = g;
             }
-        }
         const float c0 = row_sum<TPR>(s0, red) * inv_c;
         const float c1 = row_sum<TPR>(s1, red) * inv_c;
-        T *dx = static_cast<T *>(a.y) + row * a.C;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int at = (t + i * TPR) * V;
-            if (at < a.C) {
+            const int col = (t + i * TPR) * V - shift;
 #pragma unroll
-                for (int e = 0; e < V; ++e)
-                    xv[i][e] = rstd * (gv[i][e] - fmaf(xv[i][e], c1, c0));
-                Vec<T, V>::store(dx + at, xv[i]);
-            }
+            for (int e = 0; e < V; ++e) xv[i][e] = rstd * (gv[i][e] - fmaf(xv[i][e], c1, c0));
+            if (in && col < a.C) Raw<T, V>::store(dx, row * a.C + col, col, a.C, xv[i]);
         }
     }
     if (a.part == nullptr) return;
     float *part = a.part + size_t(blockIdx.x) * 2 * a.C;
-    if (TPR == 32) {
-        // join the block's warps, one after the other
-        for (int w = 0; w < RPB; ++w) {
-            if (int(threadIdx.x / 32) == w)
+    if (TPR < LN_THREADS) {
+        // join the block's groups, one after the other
+        for (int g = 0; g < RPB; ++g) {
+            if (int(threadIdx.x / TPR) == g)
 #pragma unroll
-                for (int i = 0; i < N; ++i) {
-                    const int at = (t + i * TPR) * V;
-                    if (at < a.C)
+                for (int i = 0; i < N; ++i)
 #pragma unroll
-                        for (int e = 0; e < V; ++e) {
-                            float *c = col + at + e;
-                            c[0] = w == 0 ? dw[i][e] : c[0] + dw[i][e];
-                            c[a.C] = w == 0 ? db[i][e] : c[a.C] + db[i][e];
+                    for (int e = 0; e < V; ++e) {
+                        const int c = (t + i * TPR) * V - shift + e;
+                        if (c >= 0 && c < a.C) {
+                            colsum[c] = g == 0 ? dw[i][e] : colsum[c] + dw[i][e];
+                            colsum[a.C + c] = g == 0 ? db[i][e] : colsum[a.C + c] + db[i][e];
                         }
-                }
+                    }
             __syncthreads();
         }
-        for (int c = threadIdx.x; c < 2 * a.C; c += LN_THREADS) part[c] = col[c];
+        for (int c = threadIdx.x; c < 2 * a.C; c += LN_THREADS) part[c] = colsum[c];
     } else {
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const int at = (t + i * TPR) * V;
-            if (at < a.C)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    part[at + e] = dw[i][e];
-                    part[a.C + at + e] = db[i][e];
+            for (int e = 0; e < V; ++e) {
+                const int c = (t + i * TPR) * V - shift + e;
+                if (c >= 0 && c < a.C) {
+                    part[c] = dw[i][e];
+                    part[a.C + c] = db[i][e];
                 }
-        }
+            }
     }
 }
 
@@ -235,65 +306,91 @@ ln_param_kernel(const float *part, int nparts, int C, WT *dw, WT *db) {
 }
 
 struct LnLaunch {
-    bool backward;
-    int blocks;
+    const DeviceInfo *dev;
     cudaStream_t stream;
+    bool backward, params;
+    // backward with params: the partial sums, one row of 2 C for each block
+    void *part;
+    int blocks;
 };
 
 template <class T, class WT, int V, int N, int TPR>
-void ln_launch(const LnArgs &a, const LnLaunch &l) {
+cudaError_t ln_launch(LnArgs a, LnLaunch &l) {
+    constexpr int RPB = LN_THREADS / TPR;
+    const int64_t want = (a.rows + RPB - 1) / RPB;
+    const size_t smem = l.backward && TPR < LN_THREADS ? size_t(a.C) * 8 : 0;
+    // As many blocks as are resident together; a multiple of 8 where a group
+    // takes several rows, so that the rows of a group are a multiple of V apart.
+    static std::atomic<int> resident[2] = {{0}, {0}};
+    int per_sm = resident[l.backward].load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        const cudaError_t e =
+            l.backward ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                             &per_sm, ln_backward_kernel<T, WT, V, N, TPR>, LN_THREADS,
+                             TPR < LN_THREADS ? 32 * TPR * 8 : 0)
+                       : cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                             &per_sm, ln_forward_kernel<T, WT, V, N, TPR>, LN_THREADS, 0);
+        if (e != cudaSuccess) return e;
+        if (per_sm < 1) per_sm = 1;
+        resident[l.backward].store(per_sm, std::memory_order_relaxed);
+    }
+    const int64_t most = (int64_t(l.dev->sm_count) * per_sm + 7) / 8 * 8;
+    const unsigned blocks = unsigned(want < most ? want : most);
+    if (l.params) {
+        const cudaError_t e =
+            scratch_alloc(*l.dev, &l.part, size_t(blocks) * 2 * a.C * sizeof(float), l.stream);
+        if (e != cudaSuccess) return e;
+        a.part = static_cast<float *>(l.part);
+        l.blocks = int(blocks);
+    }
     if (l.backward)
-        ln_backward_kernel<T, WT, V, N, TPR>
-            <<<l.blocks, LN_THREADS, TPR == 32 ? size_t(a.C) * 8 : 0, l.stream>>>(a);
+        ln_backward_kernel<T, WT, V, N, TPR><<<blocks, LN_THREADS, smem, l.stream>>>(a);
     else
-        ln_forward_kernel<T, WT, V, N, TPR><<<l.blocks, LN_THREADS, 0, l.stream>>>(a);
+        ln_forward_kernel<T, WT, V, N, TPR><<<blocks, LN_THREADS, 0, l.stream>>>(a);
+    return cudaGetLastError();
 }
 
-// Elements a thread holds: 8, 16 or 32, the smallest that covers the row.
+// Vectors a thread holds: the smallest number that covers any row's `vecs`.
 template <class T, class WT, int V, int TPR>
-void ln_pick_n(const LnArgs &a, const LnLaunch &l) {
-    if (a.C <= TPR * 8)
-        ln_launch<T, WT, V, 8 / V, TPR>(a, l);
-    else if (a.C <= TPR * 16)
-        ln_launch<T, WT, V, 16 / V, TPR>(a, l);
-    else
-        ln_launch<T, WT, V, 32 / V, TPR>(a, l);
-}
-
-template <class T, class WT, int V>
-void ln_pick_tpr(const LnArgs &a, const LnLaunch &l) {
-    if (a.C <= 1024)
-        ln_pick_n<T, WT, V, 32>(a, l);
-    else
-        ln_pick_n<T, WT, V, 256>(a, l);
+cudaError_t ln_pick_n(const LnArgs &a, LnLaunch &l, int vecs) {
+    const int n = (vecs + TPR - 1) / TPR;
+    constexpr int M = 32 / V;  // at most 32 elements a thread
+    if (n <= 1)
+        return ln_launch<T, WT, V, 1, TPR>(a, l);
+    if (n <= 2)
+        return ln_launch<T, WT, V, 2 <= M ? 2 : M, TPR>(a, l);
+    if (n <= 3)
+        return ln_launch<T, WT, V, 3 <= M ? 3 : M, TPR>(a, l);
+    if (n <= 4)
+        return ln_launch<T, WT, V, 4 <= M ? 4 : M, TPR>(a, l);
+    if (n <= 5)
+        return ln_launch<T, WT, V, 5 <= M ? 5 : M, TPR>(a, l);
+    if (n <= 6)
+        return ln_launch<T, WT, V, 6 <= M ? 6 : M, TPR>(a, l);
+    return ln_launch<T, WT, V, M, TPR>(a, l);
 }
 
 bool aligned(const void *p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
 
-// Widest vector every row, parameter and gradient is aligned to.
 template <class T, class WT>
-void ln_pick_v(const LnArgs &a, const LnLaunch &l) {
+cudaError_t ln_pick_v(const LnArgs &a, LnLaunch &l) {
     constexpr int W = 16 / sizeof(T);
-    auto fits = [&](int v) {
-        return a.C % v == 0 && aligned(a.x, v * sizeof(T)) && aligned(a.y, v * sizeof(T)) &&
-               aligned(a.dy, v * sizeof(T)) && aligned(a.w, min(v * sizeof(WT), size_t(16))) &&
-               aligned(a.b, min(v * sizeof(WT), size_t(16)));
-    };
-    if (fits(W))
-        ln_pick_tpr<T, WT, W>(a, l);
-    else if (sizeof(T) == 2 && fits(2))
-        ln_pick_tpr<T, WT, sizeof(T) == 2 ? 2 : 1>(a, l);
-    else
-        ln_pick_tpr<T, WT, 1>(a, l);
+    // a row that starts at any offset may touch one vector more
+    const int vecs = a.C % W == 0 ? a.C / W : (a.C + 2 * W - 2) / W;
+    if (aligned(a.x, 16) && aligned(a.y, 16) && aligned(a.dy, 16) && vecs <= 256 * (32 / W)) {
+        if (vecs <= 8 * (16 / W))
+            return ln_pick_n<T, WT, W, 8>(a, l, vecs);
+        if (vecs <= 32 * (32 / W)) return ln_pick_n<T, WT, W, 32>(a, l, vecs);
+        return ln_pick_n<T, WT, W, 256>(a, l, vecs);
+    }
+    return a.C <= 32 * 32 ? ln_launch<T, WT, 1, 32, 32>(a, l)
+                          : ln_launch<T, WT, 1, 32, 256>(a, l);
 }
 
-void ln_dispatch(const LnArgs &a, int dtype, int param_dtype, const LnLaunch &l) {
-    if (dtype == PC_F32)
-        ln_pick_v<float, float>(a, l);
-    else if (param_dtype == PC_F32)
-        ln_pick_v<bf16, float>(a, l);
-    else
-        ln_pick_v<bf16, bf16>(a, l);
+cudaError_t ln_dispatch(const LnArgs &a, int dtype, int param_dtype, LnLaunch &l) {
+    if (dtype == PC_F32) return ln_pick_v<float, float>(a, l);
+    if (param_dtype == PC_F32) return ln_pick_v<bf16, float>(a, l);
+    return ln_pick_v<bf16, bf16>(a, l);
 }
 
 int ln_check(const char *what, int dtype, int param_dtype, int64_t rows, int64_t C) {
@@ -355,10 +452,8 @@ extern "C" int pc_layer_norm(const void *x, int dtype, int64_t rows, int64_t C,
     LnArgs a{};
     a.x = x, a.w = weight, a.b = bias, a.y = out, a.mean = out_mean, a.rstd = out_rstd;
     a.rows = rows, a.C = int(C), a.eps = float(eps);
-    const int rpb = C <= 1024 ? LN_THREADS / 32 : 1;
-    const LnLaunch l{false, int((rows + rpb - 1) / rpb), static_cast<cudaStream_t>(stream)};
-    ln_dispatch(a, dtype, param_dtype, l);
-    return ln_cuda("layer_norm", cudaGetLastError());
+    LnLaunch l{dev, static_cast<cudaStream_t>(stream), false, false, nullptr, 0};
+    return ln_cuda("layer_norm", ln_dispatch(a, dtype, param_dtype, l));
 }
 
 extern "C" int pc_layer_norm_backward(const void *grad_out, const void *x, int dtype,
@@ -388,36 +483,27 @@ extern "C" int pc_layer_norm_backward(const void *grad_out, const void *x, int d
     if (grad_bias && (rc = api_check_ptr(grad_bias, d, ps, "grad_bias")) != PC_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const bool params = grad_weight != nullptr || grad_bias != nullptr;
-    const int rpb = C <= 1024 ? LN_THREADS / 32 : 1;
-    const int64_t want = (rows + rpb - 1) / rpb;
-    const int most = dev->sm_count * 4;
-    const int blocks = int(want < most ? want : most);
     LnArgs a{};
     a.x = x, a.dy = grad_out, a.w = weight, a.y = grad_x;
     a.mean = const_cast<float *>(mean), a.rstd = const_cast<float *>(rstd);
     a.rows = rows, a.C = int(C);
-    cudaError_t e = cudaSuccess;
-    void *part = nullptr;
-    if (params && blocks > 0) {
-        e = scratch_alloc(*dev, &part, size_t(blocks) * 2 * C * sizeof(float), st);
-        if (e != cudaSuccess) return ln_cuda("layer_norm_backward: scratch", e);
-        a.part = static_cast<float *>(part);
-    }
-    if (blocks > 0) ln_dispatch(a, dtype, param_dtype, LnLaunch{true, blocks, st});
-    if (params) {
+    LnLaunch l{dev, st, true, params && rows > 0, nullptr, 0};
+    cudaError_t e = rows > 0 ? ln_dispatch(a, dtype, param_dtype, l) : cudaSuccess;
+    if (e == cudaSuccess && params) {
         const unsigned g = unsigned((2 * C + 31) / 32);
+        const float *part = static_cast<const float *>(l.part);
         if (param_dtype == PC_F32)
             ln_param_kernel<float><<<g, dim3(32, 32), 0, st>>>(
-                a.part, blocks, int(C), static_cast<float *>(grad_weight),
+                part, l.blocks, int(C), static_cast<float *>(grad_weight),
                 static_cast<float *>(grad_bias));
         else
             ln_param_kernel<bf16><<<g, dim3(32, 32), 0, st>>>(
-                a.part, blocks, int(C), static_cast<bf16 *>(grad_weight),
+                part, l.blocks, int(C), static_cast<bf16 *>(grad_weight),
                 static_cast<bf16 *>(grad_bias));
+        e = cudaGetLastError();
     }
-    e = cudaGetLastError();
-    if (part != nullptr) {
-        const cudaError_t f = scratch_free(part, st);
+    if (l.part != nullptr) {
+        const cudaError_t f = scratch_free(l.part, st);
         if (e == cudaSuccess) e = f;
     }
     return ln_cuda("layer_norm_backward", e);

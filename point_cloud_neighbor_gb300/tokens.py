@@ -22,67 +22,68 @@ _DTYPES = {torch.float32: PC_F32, torch.bfloat16: PC_BF16}
 _Strides = ctypes.c_int64 * 3
 
 
-class _NoSwitch:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return False
+# The current device and stream by their raw getters: torch.cuda's wrappers
+# cost more than a small kernel takes.
+_current = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-_HERE = _NoSwitch()
+def _run(what: str, fn, index: int, *args):
+    """Call a library function with the current stream of device `index` as its
+    last argument; raise on a status that is not PC_OK."""
+    if _current() == index:
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
+    if st:
+        _raise_on(st, what)
 
 
-def _on(device: torch.device):
-    """The device's context, without the cost of a switch where it is current."""
-    return _HERE if device.index == torch.cuda.current_device() else torch.cuda.device(device)
-
-
-def _stream(device: torch.device) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
-
-
-def _tensor(t, name: str, dtypes=None):
+def _code(t, name: str) -> int:
+    """The dtype code of a CUDA tensor of float32 or bfloat16."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor (got {t.device}); "
                          "this library has no CPU path")
-    if t.dtype not in (_DTYPES if dtypes is None else dtypes):
-        raise ValueError(f"{name} must be float32 or bfloat16 (got {t.dtype})"
-                         if dtypes is None else f"{name} must be {dtypes[0]} (got {t.dtype})")
-    return t
+    code = _DTYPES.get(t.dtype)
+    if code is None:
+        raise ValueError(f"{name} must be float32 or bfloat16 (got {t.dtype})")
+    return code
 
 
-def _same(t, name: str, shape, dtype, device, what: str = ""):
+def _same(t, name: str, shape, dtype, index: int):
     """A packed tensor of a given shape, type and device."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != device or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+    if not t.is_cuda or t.get_device() != index or t.dtype is not dtype or t.shape != shape \
+            or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape "
-                         f"{tuple(shape)} on {device}{what}")
+                         f"{tuple(shape)} on cuda:{index}")
     return t
 
 
 # --- layer norm -------------------------------------------------------------------
 
 def _norm_args(x, weight, bias):
-    _tensor(x, "x")
+    code = _code(x, "x")
     if x.dim() < 1 or not x.is_contiguous():
         raise ValueError("x must be contiguous with at least one axis")
-    C = x.shape[-1]
-    pt = None
+    C, index, pt = x.shape[-1], x.get_device(), None
     for t, name in ((weight, "weight"), (bias, "bias")):
         if t is None:
             continue
-        if not isinstance(t, torch.Tensor) or t.device != x.device or t.shape != (C,) \
-                or not t.is_contiguous() or t.dtype not in (torch.float32, x.dtype):
+        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index \
+                or t.shape != (C,) or not t.is_contiguous() \
+                or t.dtype not in (torch.float32, x.dtype):
             raise ValueError(f"{name} must be a contiguous float32 or {x.dtype} tensor "
                              f"[{C}] on {x.device}")
-        if pt is not None and t.dtype != pt:
+        if pt is not None and t.dtype is not pt:
             raise ValueError("weight and bias must have the same dtype")
         pt = t.dtype
-    return C, (x.numel() // C if C else 0), torch.float32 if pt is None else pt
+    return (code, index, C, x.numel() // C if C else 0,
+            PC_F32 if pt is None else _DTYPES[pt])
 
 
 def pc_layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
@@ -90,22 +91,18 @@ def pc_layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
                   return_stats: bool = False, out: torch.Tensor | None = None):
     """Layer norm over the last axis: y, or with ``return_stats`` (y, mean,
     rstd), the statistics float32 of shape ``x.shape[:-1]``."""
-    C, rows, pt = _norm_args(x, weight, bias)
-    dev = x.device
-    with _on(dev):
-        if out is None:
-            out = torch.empty_like(x)
-        else:
-            _same(out, "out", x.shape, x.dtype, dev)
-        mean = rstd = None
-        if return_stats:
-            mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=dev)
-            rstd = torch.empty_like(mean)
-        st = lib().pc_layer_norm(x.data_ptr(), _DTYPES[x.dtype], rows, C,
-                                 _ptr_or_none(weight), _ptr_or_none(bias), _DTYPES[pt],
-                                 float(eps), out.data_ptr(), _ptr_or_none(mean),
-                                 _ptr_or_none(rstd), _stream(dev))
-    _raise_on(st, "pc_layer_norm")
+    code, index, C, rows, pcode = _norm_args(x, weight, bias)
+    if out is None:
+        out = torch.empty_like(x)
+    else:
+        _same(out, "out", x.shape, x.dtype, index)
+    mean = rstd = None
+    if return_stats:
+        mean = torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device)
+        rstd = torch.empty_like(mean)
+    _run("pc_layer_norm", lib().pc_layer_norm, index, x.data_ptr(), code, rows, C,
+         _ptr_or_none(weight), _ptr_or_none(bias), pcode, float(eps), out.data_ptr(),
+         _ptr_or_none(mean), _ptr_or_none(rstd))
     return (out, mean, rstd) if return_stats else out
 
 
@@ -115,40 +112,38 @@ def pc_layer_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.
     """Gradients of :func:`pc_layer_norm`: (grad_x, grad_weight, grad_bias),
     None for a parameter that is None.  ``mean`` and ``rstd`` are the forward
     call's statistics."""
-    C, rows, pt = _norm_args(x, weight, bias)
-    dev = x.device
-    _same(grad_out, "grad_out", x.shape, x.dtype, dev)
-    _same(mean, "mean", x.shape[:-1], torch.float32, dev)
-    _same(rstd, "rstd", x.shape[:-1], torch.float32, dev)
-    with _on(dev):
-        dx = torch.empty_like(x)
-        dw = None if weight is None else torch.empty_like(weight)
-        db = None if bias is None else torch.empty_like(bias)
-        st = lib().pc_layer_norm_backward(
-            grad_out.data_ptr(), x.data_ptr(), _DTYPES[x.dtype], rows, C, mean.data_ptr(),
-            rstd.data_ptr(), _ptr_or_none(weight), _DTYPES[pt], dx.data_ptr(),
-            _ptr_or_none(dw), _ptr_or_none(db), _stream(dev))
-    _raise_on(st, "pc_layer_norm_backward")
+    code, index, C, rows, pcode = _norm_args(x, weight, bias)
+    _same(grad_out, "grad_out", x.shape, x.dtype, index)
+    _same(mean, "mean", x.shape[:-1], torch.float32, index)
+    _same(rstd, "rstd", x.shape[:-1], torch.float32, index)
+    dx = torch.empty_like(x)
+    dw = None if weight is None else torch.empty_like(weight)
+    db = None if bias is None else torch.empty_like(bias)
+    _run("pc_layer_norm_backward", lib().pc_layer_norm_backward, index, grad_out.data_ptr(),
+         x.data_ptr(), code, rows, C, mean.data_ptr(), rstd.data_ptr(), _ptr_or_none(weight),
+         pcode, dx.data_ptr(), _ptr_or_none(dw), _ptr_or_none(db))
     return dx, dw, db
 
 
 # --- rotary -----------------------------------------------------------------------
 
-def _heads(t, name: str, B: int, L: int, D: int, dtype, device):
-    """A [B, L, heads, D] tensor with a contiguous last axis."""
-    _tensor(t, name)
-    if t.dim() != 4 or t.shape[0] != B or t.shape[1] != L or t.shape[3] != D:
+def _heads(t, name: str, B: int, L: int, D: int, dtype, index: int):
+    """A [B, L, heads, D] tensor with a contiguous last axis: its heads and
+    strides (None if packed)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    shape = t.shape
+    if len(shape) != 4 or shape[0] != B or shape[1] != L or shape[3] != D:
         raise ValueError(f"{name} must have shape [{B}, {L}, heads, {D}] "
-                         f"(got {tuple(t.shape)})")
-    if t.dtype != dtype or t.device != device:
-        raise ValueError(f"{name} must be {dtype} on {device} (got {t.dtype} on {t.device})")
-    if t.stride(3) != 1 and D > 1:
+                         f"(got {tuple(shape)})")
+    if t.dtype is not dtype or not t.is_cuda or t.get_device() != index:
+        raise ValueError(f"{name} must be {dtype} on cuda:{index} (got {t.dtype} on {t.device})")
+    if t.is_contiguous():
+        return shape[2], None
+    sb, sl, sh, sd = t.stride()
+    if sd != 1 and D > 1:
         raise ValueError(f"{name} must be contiguous along its last axis")
-    return t
-
-
-def _strides_of(t):
-    return None if t.is_contiguous() else _Strides(t.stride(0), t.stride(1), t.stride(2))
+    return shape[2], _Strides(sb, sl, sh)
 
 
 def pc_rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
@@ -161,63 +156,60 @@ def pc_rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
     pair is channels (2p, 2p + 1), or with ``interleaved=False`` (p, A F + p).
     Channels from 2 A F on are copied.  ``inverse`` turns back: the gradient.
     """
-    _tensor(q, "q")
+    code = _code(q, "q")
     if q.dim() != 4:
         raise ValueError(f"q must have shape [B, L, H, D] (got {tuple(q.shape)})")
     B, L, H, D = q.shape
-    dev = q.device
-    _heads(q, "q", B, L, D, q.dtype, dev)
-    if k is not None:
-        _heads(k, "k", B, L, D, q.dtype, dev)
+    index, dtype = q.get_device(), q.dtype
+    qs = _heads(q, "q", B, L, D, dtype, index)[1]
+    Hkv, ks = (0, None) if k is None else _heads(k, "k", B, L, D, dtype, index)
     if not isinstance(freqs, torch.Tensor) or freqs.dim() != 2:
         raise ValueError("freqs must be a float32 CUDA tensor [A, F]")
     A, F = freqs.shape
-    _same(freqs, "freqs", (A, F), torch.float32, dev)
-    _same(positions, "positions", (B, L, A), torch.float32, dev)
+    _same(freqs, "freqs", (A, F), torch.float32, index)
+    _same(positions, "positions", (B, L, A), torch.float32, index)
     flags = (0 if interleaved else PC_ROTARY_HALF_SPLIT) | (PC_ROTARY_INVERSE if inverse else 0)
-    with _on(dev):
-        oq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        ok = None if k is None else torch.empty(k.shape, dtype=q.dtype, device=dev)
-        st = lib().pc_rotary(q.data_ptr(), _ptr_or_none(k), _DTYPES[q.dtype], B, L, H,
-                             0 if k is None else k.shape[2], D, _strides_of(q),
-                             None if k is None else _strides_of(k), positions.data_ptr(),
-                             freqs.data_ptr(), A, F, flags, oq.data_ptr(),
-                             _ptr_or_none(ok), _stream(dev))
-    _raise_on(st, "pc_rotary")
+    oq = torch.empty((B, L, H, D), dtype=dtype, device=q.device)
+    ok = None if k is None else torch.empty((B, L, Hkv, D), dtype=dtype, device=q.device)
+    _run("pc_rotary", lib().pc_rotary, index, q.data_ptr(), _ptr_or_none(k), code, B, L, H, Hkv,
+         D, qs, ks, positions.data_ptr(), freqs.data_ptr(), A, F, flags, oq.data_ptr(),
+         _ptr_or_none(ok))
     return oq, ok
 
 
 # --- attention --------------------------------------------------------------------
 
 def _attention_args(q, k, v, scale, query_xyz, ref_xyz, slopes, query_lengths, ref_lengths):
-    _tensor(q, "q")
+    code = _code(q, "q")
     if q.dim() != 4:
         raise ValueError(f"q must have shape [B, Lq, H, D] (got {tuple(q.shape)})")
     B, Lq, H, D = q.shape
-    dev = q.device
-    _heads(q, "q", B, Lq, D, q.dtype, dev)
+    index, dtype = q.get_device(), q.dtype
+    qs = _heads(q, "q", B, Lq, D, dtype, index)[1]
     if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be a CUDA tensor [B, Lk, Hkv, D]")
-    Lk, Hkv = k.shape[1], k.shape[2]
-    _heads(k, "k", B, Lk, D, q.dtype, dev)
-    _heads(v, "v", B, Lk, D, q.dtype, dev)
-    if v.shape[2] != Hkv:
+    Lk = k.shape[1]
+    Hkv, ks = _heads(k, "k", B, Lk, D, dtype, index)
+    Hv, vs = _heads(v, "v", B, Lk, D, dtype, index)
+    if Hv != Hkv:
         raise ValueError("k and v must have the same number of heads")
     if H and (Hkv < 1 or H % Hkv):
         raise ValueError(f"the {Hkv} key heads must divide the {H} query heads")
-    if (slopes is None) != (query_xyz is None) or (slopes is None) != (ref_xyz is None):
+    px = py = ps = None
+    if slopes is not None and query_xyz is not None and ref_xyz is not None:
+        ps = _same(slopes, "slopes", (H,), torch.float32, index).data_ptr()
+        px = _same(query_xyz, "query_xyz", (B, Lq, 3), torch.float32, index).data_ptr()
+        py = _same(ref_xyz, "ref_xyz", (B, Lk, 3), torch.float32, index).data_ptr()
+    elif not (slopes is None and query_xyz is None and ref_xyz is None):
         raise ValueError("slopes, query_xyz and ref_xyz go together")
-    if slopes is not None:
-        _same(slopes, "slopes", (H,), torch.float32, dev)
-        _same(query_xyz, "query_xyz", (B, Lq, 3), torch.float32, dev)
-        _same(ref_xyz, "ref_xyz", (B, Lk, 3), torch.float32, dev)
-    ql = _check_lengths(query_lengths, B, dev, "query_lengths")
-    rl = _check_lengths(ref_lengths, B, dev, "ref_lengths")
+    ql = None if query_lengths is None else \
+        _check_lengths(query_lengths, B, q.device, "query_lengths").data_ptr()
+    rl = None if ref_lengths is None else \
+        _check_lengths(ref_lengths, B, q.device, "ref_lengths").data_ptr()
     if scale is None:
         scale = 1.0 / math.sqrt(max(D, 1))
-    return (_DTYPES[q.dtype], B, Lq, Lk, H, Hkv, D, _strides_of(q), _strides_of(k),
-            _strides_of(v), float(scale), _ptr_or_none(query_xyz), _ptr_or_none(ref_xyz),
-            _ptr_or_none(slopes), _ptr_or_none(ql), _ptr_or_none(rl))
+    return index, (q.data_ptr(), k.data_ptr(), v.data_ptr()), \
+        (code, B, Lq, Lk, H, Hkv, D, qs, ks, vs, float(scale), px, py, ps, ql, rl)
 
 
 def pc_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
@@ -234,18 +226,15 @@ def pc_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
     [B, Lk, 3] are float32, all given or none.  Rows past
     ``query_lengths[b]`` and rows without keys are 0 (lse -inf).
     """
-    args = _attention_args(q, k, v, scale, query_xyz, ref_xyz, slopes, query_lengths,
-                           ref_lengths)
-    dev = q.device
-    with _on(dev):
-        out = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        lse = None
-        if return_lse:
-            lse = torch.empty((q.shape[0], q.shape[2], q.shape[1]), dtype=torch.float32,
-                              device=dev)
-        st = lib().pc_attention(q.data_ptr(), k.data_ptr(), v.data_ptr(), *args,
-                                out.data_ptr(), _ptr_or_none(lse), _stream(dev))
-    _raise_on(st, "pc_attention")
+    index, qkv, args = _attention_args(q, k, v, scale, query_xyz, ref_xyz, slopes,
+                                       query_lengths, ref_lengths)
+    B, Lq, H, D = q.shape
+    out = torch.empty((B, Lq, H, D), dtype=q.dtype, device=q.device)
+    lse = None
+    if return_lse:
+        lse = torch.empty((B, H, Lq), dtype=torch.float32, device=q.device)
+    _run("pc_attention", lib().pc_attention, index, *qkv, *args, out.data_ptr(),
+         _ptr_or_none(lse))
     return (out, lse) if return_lse else out
 
 
@@ -261,23 +250,20 @@ def pc_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tens
     """Gradients of :func:`pc_attention` from its ``out`` and ``lse``: (grad_q,
     grad_k, grad_v, grad_slopes), the last None without slopes or with
     ``need_slopes=False``.  The positions get no gradient."""
-    args = _attention_args(q, k, v, scale, query_xyz, ref_xyz, slopes, query_lengths,
-                           ref_lengths)
-    dev = q.device
-    B, Lq, H, _ = q.shape
-    _same(grad_out, "grad_out", q.shape, q.dtype, dev)
-    _same(out, "out", q.shape, q.dtype, dev)
-    _same(lse, "lse", (B, H, Lq), torch.float32, dev)
-    with _on(dev):
-        dq = torch.empty(q.shape, dtype=q.dtype, device=dev)
-        dk = torch.empty(k.shape, dtype=q.dtype, device=dev)
-        dv = torch.empty(v.shape, dtype=q.dtype, device=dev)
-        ds = torch.empty_like(slopes) if slopes is not None and need_slopes else None
-        st = lib().pc_attention_backward(
-            grad_out.data_ptr(), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
-            lse.data_ptr(), *args, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-            _ptr_or_none(ds), _stream(dev))
-    _raise_on(st, "pc_attention_backward")
+    index, qkv, args = _attention_args(q, k, v, scale, query_xyz, ref_xyz, slopes,
+                                       query_lengths, ref_lengths)
+    B, Lq, H, D = shape = q.shape
+    dtype, dev = q.dtype, q.device
+    _same(grad_out, "grad_out", shape, dtype, index)
+    _same(out, "out", shape, dtype, index)
+    _same(lse, "lse", (B, H, Lq), torch.float32, index)
+    dq = torch.empty(shape, dtype=dtype, device=dev)
+    dk = torch.empty(k.shape, dtype=dtype, device=dev)
+    dv = torch.empty(v.shape, dtype=dtype, device=dev)
+    ds = torch.empty_like(slopes) if slopes is not None and need_slopes else None
+    _run("pc_attention_backward", lib().pc_attention_backward, index, grad_out.data_ptr(), *qkv,
+         out.data_ptr(), lse.data_ptr(), *args, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+         _ptr_or_none(ds))
     return dq, dk, dv, ds
 
 
