@@ -10,7 +10,7 @@
 //   sums     acc += P Y2 (and dS Y1), the weights read from tensor memory,
 //            the same shared-memory tile now contracted along its rows.
 // One warp copies tiles (tensor maps, 128-byte swizzle; zeros past the
-// arrays' ends), one prepares the positions, one issues the products, 16
+// arrays' ends), two prepare the positions, one issues the products, 16
 // compute weights in two units of 8: FWD one unit per 128 rows, DQ and DKV
 // units that take tiles in turn.  Each unit has score buffers of its own, so
 // products run under weights.
@@ -65,14 +65,19 @@ struct Cfg {
     static constexpr int THREADS = 32 * (CWARPS + 4);
     static constexpr int STAGES = DP == 64 ? 6 : 3;
     // The weights as a sum of two bfloat16.
-    static constexpr bool TWO_P = MODE != ATTN_DQ, TWO_S = BWD;
+    static constexpr bool TWO_P = MODE != ATTN_DQ, TWO_S = false;
     // tensor memory columns: score buffers (FWD two a unit, else one of S and
     // dP), then the accumulators
     static constexpr int NBUF = BWD ? 2 : 4, BUF = BWD ? 2 * YR : YR;
     static constexpr int ACC = NBUF * BUF;
     static constexpr int NACC = MODE == ATTN_DQ ? 1 : 2;  // FWD: one a unit
+    // The rows kept, where tensor memory has room for them: a product that reads
+    // both operands from shared memory is bound by that (48 cycles instead of 32
+    // for 128 x 64 x 16).
+    static constexpr int XCOL = ACC + NACC * DP;
+    static constexpr bool X_TMEM = XCOL + DP <= 512;
     static constexpr int COLS = 512;
-    static_assert(ACC + NACC * DP <= COLS, "tensor memory");
+    static_assert(XCOL <= COLS, "tensor memory");
     static constexpr int XBYTES = XR * DP * 2, YBYTES = YR * DP * 2;
     static constexpr int XT = BWD ? 2 : T;      // tiles kept
     static constexpr int XAUG = XR * 64, YAUG = YR * 64;  // 32 channels
@@ -80,11 +85,13 @@ struct Cfg {
     // per stage: x, y, z, -lse, -delta of the streamed rows; flag, bias factor
     static constexpr int COLF = 5 * YR + 4;
     static constexpr int ROWF = 2 * 6 * XR;     // per unit: exchanged row values
-    static constexpr size_t SMEM = 1024 + size_t(XT) * XBYTES + size_t(T) * XAUG +
+    static constexpr size_t XSMEM = X_TMEM ? 0 : size_t(XT) * XBYTES;
+    static constexpr size_t SMEM = 1024 + XSMEM + size_t(T) * XAUG +
                                    size_t(STAGES) * (STAGE + COLF * 4) + ROWF * 4 + 512;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
 
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -183,20 +190,23 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
     extern __shared__ unsigned char smem_raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    unsigned char *X = base;                       // FWD: q of both tiles; else X1, X2
-    unsigned char *Y = X + C::XT * C::XBYTES;      // stage s: Y1, Y2, channels of the bias
+    unsigned char *X = base;  // FWD: q of both tiles; else X1, X2 (if not in tensor memory)
+    unsigned char *Y = X + C::XSMEM;               // stage s: Y1, Y2, channels of the bias
     unsigned char *xaug = Y + size_t(STAGES) * C::STAGE;
     float *coldata = reinterpret_cast<float *>(xaug + T * C::XAUG);
     float *rowdata = coldata + STAGES * C::COLF;   // [unit][6][XR]
     uint64_t *full = reinterpret_cast<uint64_t *>(rowdata + C::ROWF);
     uint64_t *empty = full + STAGES, *sfull = empty + STAGES, *pfull = sfull + C::NBUF;
     uint64_t *xfull = pfull + C::NBUF, *accfull = xfull + 1;
-    uint64_t *mxbar = accfull + 1;                 // [unit][quad]
+    uint64_t *fixed = accfull + 1, *mxbar = fixed + STAGES;  // mxbar: [unit][quad]
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(mxbar + 8);
     int *xr2 = reinterpret_cast<int *>(tmem_slot + 1);  // R^2 of the block's rows, as bits
     volatile int *stop = reinterpret_cast<volatile int *>(xr2 + 1);
 
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    // (values broadcast by a shuffle are known to be the same in all lanes: the
+    // branches on them, and what the products' operands are formed from, then
+    // stay in uniform registers)
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const int LX = DKV ? a.Lk : a.Lq, LY = DKV ? a.Lq : a.Lk;
     const int NH = DKV ? a.Hkv : a.H;
     const int G = a.H / a.Hkv;
@@ -208,14 +218,15 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
     idx /= ntile;
     const int head = int(idx % NH), b = int(idx / NH);
     const int nq = attn_len(a.qlen, b, a.Lq), nk = attn_len(a.rlen, b, a.Lk);
-    const int nx = DKV ? nk : nq, ny = DKV ? nq : nk;
+    const int nx = uniform(DKV ? nk : nq), ny = uniform(DKV ? nq : nk);
     const int r0 = tile * T * XR;
     const int hk = DKV ? head : head / G;
     const int nyt = (ny + YR - 1) / YR;
     const int64_t items = nx > r0 ? int64_t(nyt) * (DKV ? G : 1) : 0;
     const int64_t it0 = items * split / a.nsplit;
-    const int n = int(items * (split + 1) / a.nsplit - it0);  // tiles of this block
+    const int n = uniform(int(items * (split + 1) / a.nsplit - it0));  // tiles of this block
     const float *xpos = DKV ? a.rxyz : a.qxyz, *ypos = DKV ? a.qxyz : a.rxyz;
+    const bool ragged = ny < LY && ny % YR != 0;  // the last tile has rows past the length
     // the slopes' gradient needs the distances themselves
     const bool sums = MODE == ATTN_DQ && BIAS && a.rowsum != nullptr;
 
@@ -235,6 +246,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
             mbar_init(&full[s], COLS ? 2 : 1);
+            mbar_init(&fixed[s], 1);
             mbar_init(&empty[s], 1 + (COLS ? (FWD ? 16 : 8) : 0));
         }
         for (int s = 0; s < C::NBUF; ++s) {
@@ -251,6 +263,41 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
     if (warp == C::CWARPS + 1) tmem_alloc(tmem_slot, C::COLS);
     tc_fence_before();
     __syncthreads();
+    if (C::X_TMEM && n > 0 && warp < C::CWARPS) {
+        // FWD: each unit its tile's q, half the channels each; else unit 0 X1 and
+        // unit 1 X2.  Two channels a column, zeros past the rows and channels.
+        tc_fence_after();
+        const bf16 *src;
+        if (FWD || (MODE == ATTN_DQ && unit == 0))
+            src = static_cast<const bf16 *>(a.q) + b * a.qs[0] + head * a.qs[2] +
+                  int64_t(row) * a.qs[1];
+        else if (MODE == ATTN_DQ)
+            src = static_cast<const bf16 *>(a.go) +
+                  ((int64_t(b) * a.Lq + row) * a.H + head) * a.D;
+        else if (unit == 0)
+            src = static_cast<const bf16 *>(a.k) + b * a.ks[0] + head * a.ks[2] +
+                  int64_t(row) * a.ks[1];
+        else
+            src = static_cast<const bf16 *>(a.v) + b * a.vs[0] + head * a.vs[2] +
+                  int64_t(row) * a.vs[1];
+        const uint32_t at = uint32_t(uniform(int(*tmem_slot))) + (uint32_t(quad * 32) << 16) +
+                            C::XCOL + unit * (DP / 2) + half * (DP / 4);
+#pragma unroll
+        for (int c = 0; c < DP / 2; c += 16) {
+            uint32_t r[8];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int ch = half * (DP / 2) + c + 8 * e;
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (row < nx && ch < a.D) v = *reinterpret_cast<const uint4 *>(src + ch);
+                r[4 * e] = v.x, r[4 * e + 1] = v.y, r[4 * e + 2] = v.z, r[4 * e + 3] = v.w;
+            }
+            tmem_st8(at + c / 2, r);
+        }
+        tmem_wait_st();
+        tc_fence_before();
+    }
+    if (C::X_TMEM && !BIAS) __syncthreads();
     if (BIAS && n > 0) {
         if (warp < C::CWARPS && half == 0 && (FWD || unit == 0)) {
             const bool in = row < nx;
@@ -266,7 +313,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         __syncthreads();
     }
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;
+    const uint32_t tmem = uniform(int(*tmem_slot));
 
     // A bounded wait of a whole warp; false: stop.
     auto wait = [&](uint64_t *bar, unsigned parity) {
@@ -277,12 +324,28 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         }
         return __all_sync(0xffffffffu, w == WAIT_OK) != 0;
     };
-    auto item_head = [&](int k) { return DKV ? hk * G + int((it0 + k) / nyt) : head; };
-    auto item_row = [&](int k) { return int(DKV ? (it0 + k) % nyt : it0 + k) * YR; };
+    // The head and first row of the block's tiles, one after the other.
+    struct Walk {
+        int h, y, end;
+        __device__ __forceinline__ void next(int tiles = 1) {
+            y += tiles * YR;
+            if (DKV)
+                while (y >= end) y -= end, ++h;
+        }
+    };
+    auto walk = [&](int skip) {
+        Walk w{DKV ? hk * G : head, 0, nyt * YR};
+        if (n > 0) {
+            if (DKV) w.h += int(it0 / nyt);
+            w.y = int(DKV ? it0 % nyt : it0) * YR;
+            w.next(skip);
+        }
+        return w;
+    };
 
     if (warp == C::CWARPS) {
         // ---- copies ---------------------------------------------------------------
-        if (n > 0 && elect_one()) {
+        if (!C::X_TMEM && n > 0 && elect_one()) {
             mbar_arrive_expect_tx(xfull, C::XT * C::XBYTES);
             for (int p = 0; p < DP / 64; ++p)
                 for (int h = 0; h < 2; ++h) {
@@ -296,13 +359,35 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
                                     xfull);
                 }
         }
+        // Rows of a tile past the length are overwritten with zeros once the tile
+        // is there: two tiles later, so that copies stay ahead.
+        Walk late = walk(0);
+        auto fix = [&](int k) {
+            const int valid = ny - late.y, s = k % STAGES;
+            late.next();
+            if (!ragged || valid >= YR) return true;
+            if (!wait(&full[s], unsigned((k / STAGES) & 1))) return false;
+            unsigned char *y1 = Y + size_t(s) * C::STAGE, *y2 = y1 + C::YBYTES;
+            const uint4 zero = make_uint4(0, 0, 0, 0);
+            for (int p = 0; p < DP / 64; ++p)
+                for (int i = valid * 8 + lane; i < YR * 8; i += 32) {
+                    if (BWD) reinterpret_cast<uint4 *>(y1 + p * YR * 128)[i] = zero;
+                    if (MODE != ATTN_DQ) reinterpret_cast<uint4 *>(y2 + p * YR * 128)[i] = zero;
+                }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&fixed[s]);
+            return true;
+        };
         int issued = 0;
-        for (int k = 0; k < n; ++k) {
+        bool ok = true;
+        Walk at = walk(0);
+        for (int k = 0; ok && k < n; ++k, at.next()) {
             const int s = k % STAGES;
             if (k >= STAGES && !wait(&empty[s], unsigned((k / STAGES - 1) & 1))) break;
             if (withhold && blockIdx.x == 0) break;
             if (elect_one()) {
-                const int y0 = item_row(k), hy = DKV ? item_head(k) : hk;
+                const int y0 = at.y, hy = DKV ? at.h : hk;
                 mbar_arrive_expect_tx(&full[s], 2 * C::YBYTES);
                 unsigned char *y1 = Y + size_t(s) * C::STAGE, *y2 = y1 + C::YBYTES;
                 for (int p = 0; p < DP / 64; ++p) {
@@ -313,47 +398,56 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
                 }
             }
             issued = k + 1;
+            if (k >= 2) ok = fix(k - 2);
         }
+        if (issued == n)
+            for (int k = max(0, n - 2); ok && k < n; ++k) ok = fix(k);
         // nothing is in flight when the block ends
-        if (n > 0) mbar_wait_bounded(xfull, 0, a.timeout_ns);
+        if (!C::X_TMEM && n > 0) mbar_wait_bounded(xfull, 0, a.timeout_ns);
         for (int k = max(0, issued - STAGES); k < issued; ++k)
             mbar_wait_bounded(&full[k % STAGES], unsigned((k / STAGES) & 1), a.timeout_ns);
-    } else if (COLS && warp == C::CWARPS + 2) {
-        // ---- positions --------------------------------------------------------------
-        float nxt[2][5];  // of the next tile: loaded a tile ahead
-        auto fetch = [&](int k) {
-            const int h = item_head(k), y0 = item_row(k);
+    } else if (COLS && warp >= C::CWARPS + 2) {
+        // ---- positions: two warps, every other tile each ------------------------------
+        const int first = warp - (C::CWARPS + 2);
+        Walk at = walk(first);
+        float nxt[2][5], slope_nxt = 0.0f;  // of the warp's next tile: loaded a tile ahead
+        auto fetch = [&]() {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int64_t r = y0 + lane + 32 * i;
+                const int64_t r = at.y + lane + 32 * i;
                 const bool in = r < ny;
 #pragma unroll
                 for (int e = 0; e < 3; ++e)
                     nxt[i][e] = BIAS && in ? ypos[(int64_t(b) * LY + r) * 3 + e] : 0.0f;
                 if (DKV) {
-                    const int64_t at = (int64_t(b) * a.H + h) * a.Lq + r;
-                    nxt[i][3] = in ? -a.lse2[at] : -INFINITY;
-                    nxt[i][4] = in ? -a.delta[at] : 0.0f;
+                    const int64_t o = (int64_t(b) * a.H + at.h) * a.Lq + r;
+                    nxt[i][3] = in ? -a.lse2[o] : -INFINITY;
+                    nxt[i][4] = in ? -a.delta[o] : 0.0f;
                 }
             }
+            if (BIAS) slope_nxt = a.slopes[at.h];
         };
-        if (n > 0) fetch(0);
-        for (int k = 0; k < n; ++k) {
-            const int s = k % STAGES;
+        const float xmost = BIAS ? __int_as_float(*xr2) : 0.0f;
+        if (first < n) fetch();
+        int s = first;
+        unsigned phase = 1;  // of the stage's last release: none in the first round
+        for (int k = first; k < n; k += 2, s += 2) {
+            if (s >= STAGES) s -= STAGES, phase ^= 1;
             float cur[2][5];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
 #pragma unroll
                 for (int e = 0; e < 5; ++e) cur[i][e] = nxt[i][e];
-            const float slope = BIAS ? a.slopes[item_head(k)] : 0.0f;
-            if (k + 1 < n) fetch(k + 1);
-            if (k >= STAGES && !wait(&empty[s], unsigned((k / STAGES - 1) & 1))) break;
+            const float slope = slope_nxt;
+            const int valid = ny - at.y;
+            at.next(2);
+            if (k + 2 < n) fetch();
+            if (k >= STAGES && !wait(&empty[s], phase)) break;
             float *cd = coldata + s * C::COLF;
             bool direct = true;
             if (BIAS) {
-                float r2 = __int_as_float(*xr2);
+                float r2 = xmost;
                 float d[2][3];
-                const int valid = ny - item_row(k);
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
                     const bool in = lane + 32 * i < valid;
@@ -392,52 +486,58 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         }
     } else if (warp == C::CWARPS + 1) {
         // ---- products ---------------------------------------------------------------
-        // The other warps of this one's scheduler are busy: the loop is kept to
-        // few instructions (running stage numbers, descriptors by addition).
-        bool ok = n > 0 && wait(xfull, 0);
-        const uint32_t x1 = smem_operand(smem_u32(X)), x2 = x1 + C::XBYTES / 16;
-        const uint32_t xa = smem_operand(smem_u32(xaug));
-        const uint32_t yk = smem_operand(smem_u32(Y)), yr = smem_operand(smem_u32(Y), YR * 128);
-        const float *flag = coldata + 5 * YR;
-        struct Stage {
-            int s = 0;
-            unsigned phase = 0;
-            __device__ __forceinline__ void next() {
-                if (++s == STAGES) s = 0, phase ^= 1;
-            }
-        } in, out;  // tiles whose scores, whose sums are issued
-        auto tile_ready = [&](int k) {
-            if (!wait(&full[in.s], in.phase)) return false;
-            if (ny < LY) {
-                const int valid = ny - item_row(k);
-                if (valid < YR) {
-                    unsigned char *y1 = Y + size_t(in.s) * C::STAGE, *y2 = y1 + C::YBYTES;
-                    const uint4 zero = make_uint4(0, 0, 0, 0);
-                    for (int p = 0; p < DP / 64; ++p)
-                        for (int i = valid * 8 + lane; i < YR * 8; i += 32) {
-                            if (BWD) reinterpret_cast<uint4 *>(y1 + p * YR * 128)[i] = zero;
-                            if (MODE != ATTN_DQ)
-                                reinterpret_cast<uint4 *>(y2 + p * YR * 128)[i] = zero;
-                        }
-                    fence_proxy_async_smem();
-                    __syncwarp();
+        // One thread runs the loop.  The other warps of its scheduler are busy, so
+        // every instruction counts: running stage numbers, operands by addition.
+        if (elect_one()) {
+            const uint32_t x1 = smem_operand(smem_u32(X)), x2 = x1 + C::XBYTES / 16;
+            const uint32_t xa = smem_operand(smem_u32(xaug));
+            const uint32_t yk = smem_operand(smem_u32(Y));
+            const uint32_t yr = smem_operand(smem_u32(Y), YR * 128);
+            const float *flag = coldata + 5 * YR;
+            struct Stage {
+                int s = 0;
+                unsigned phase = 0;
+                __device__ __forceinline__ void next() {
+                    if (++s == STAGES) s = 0, phase ^= 1;
                 }
-            }
-            return true;
-        };
-        // the scores of the tile `in` for a unit, into its buffer
-        auto scores = [&](int u, int buf) {
-            const bool bias = BIAS && flag[in.s * C::COLF] == 0.0f;
-            if (elect_one()) {
+            } in, out;  // tiles whose scores, whose sums are issued
+            Walk at = walk(0);
+            unsigned fixes = 0;  // a bit per stage: the parity of its next fix
+            auto await = [&](uint64_t *bar, unsigned parity) {
+                const WaitResult w = mbar_wait_or_stop(bar, parity, stop, a.timeout_ns);
+                if (w == WAIT_TIMEOUT) {
+                    *stop = 1;
+                    raise_status(a.status, PC_ERR_DEVICE_TIMEOUT);
+                }
+                return w == WAIT_OK;
+            };
+            auto tile_ready = [&]() {
+                if (!await(&full[in.s], in.phase)) return false;
+                const int valid = ny - at.y;
+                at.next();
+                if (ragged && valid < YR) {
+                    const unsigned parity = (fixes >> in.s) & 1;
+                    fixes ^= 1u << in.s;
+                    return await(&fixed[in.s], parity);
+                }
+                return true;
+            };
+            // the scores of the tile `in` for a unit, into its buffer
+            auto scores = [&](int u, int buf) {
                 constexpr uint32_t id = mma_idesc(YR, false);
                 const uint32_t d = tmem + buf * C::BUF;
                 const uint32_t x = FWD ? x1 + u * (C::XBYTES / 16) : x1;
                 const uint32_t y = yk + in.s * (C::STAGE / 16);
 #pragma unroll
-                for (int i = 0; i < DP / 16; ++i)
-                    mma_ss<SMEM_128B>(d, x + (i / 4) * (XR * 128 / 16) + (i % 4) * 2,
-                                      y + (i / 4) * (YR * 128 / 16) + (i % 4) * 2, id, i > 0);
-                if (bias) {
+                for (int i = 0; i < DP / 16; ++i) {
+                    const uint32_t yo = y + (i / 4) * (YR * 128 / 16) + (i % 4) * 2;
+                    if (C::X_TMEM)
+                        mma_ts<SMEM_128B>(d, tmem + C::XCOL + u * (DP / 2) + 8 * i, yo, id, i > 0);
+                    else
+                        mma_ss<SMEM_128B>(d, x + (i / 4) * (XR * 128 / 16) + (i % 4) * 2, yo, id,
+                                          i > 0);
+                }
+                if (BIAS && flag[in.s * C::COLF] == 0.0f) {
                     const uint32_t xb = FWD ? xa + u * (C::XAUG / 16) : xa;
                     const uint32_t yb = y + 2 * C::YBYTES / 16;
                     mma_ss<SMEM_64B>(d, xb, yb, id, true);
@@ -445,17 +545,20 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
                 }
                 if (BWD)
 #pragma unroll
-                    for (int i = 0; i < DP / 16; ++i)
-                        mma_ss<SMEM_128B>(d + YR, x2 + (i / 4) * (XR * 128 / 16) + (i % 4) * 2,
-                                          y + C::YBYTES / 16 + (i / 4) * (YR * 128 / 16) +
-                                              (i % 4) * 2,
-                                          id, i > 0);
+                    for (int i = 0; i < DP / 16; ++i) {
+                        const uint32_t yo = y + C::YBYTES / 16 + (i / 4) * (YR * 128 / 16) +
+                                            (i % 4) * 2;
+                        if (C::X_TMEM)
+                            mma_ts<SMEM_128B>(d + YR, tmem + C::XCOL + DP / 2 + 8 * i, yo, id,
+                                              i > 0);
+                        else
+                            mma_ss<SMEM_128B>(d + YR, x2 + (i / 4) * (XR * 128 / 16) + (i % 4) * 2,
+                                              yo, id, i > 0);
+                    }
                 mma_commit(&sfull[buf]);
-            }
-        };
-        // the sums of the tile `out` from a unit's weights
-        auto accumulate = [&](int u, int buf, bool first) {
-            if (elect_one()) {
+            };
+            // the sums of the tile `out` from a unit's weights
+            auto accumulate = [&](int u, int buf, bool first) {
                 constexpr uint32_t id = mma_idesc(DP, true);
                 const uint32_t d1 = yr + out.s * (C::STAGE / 16), d2 = d1 + C::YBYTES / 16;
                 const uint32_t p = tmem + buf * C::BUF, acc = tmem + C::ACC + (FWD ? u * DP : 0);
@@ -477,66 +580,66 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
                         if (C::TWO_P) mma_ts<SMEM_128B>(acc + DP, at + 8, d2 + i * step, id, true);
                     }
                 }
-            }
-        };
-        // Products run in the order of their issue, so a score buffer may be
-        // filled again as soon as the sums that read it were issued.
-        if (FWD) {
-            const bool two = r0 + XR < nx;
-            if (ok && (ok = tile_ready(0))) {
-                scores(0, 0);
-                if (two) scores(1, 2);
-                in.next();
-            }
-            for (int k = 0; ok && k < n; ++k) {
-                const int cur = k & 1, nxt = cur ^ 1;
-                const unsigned parity = unsigned(k >> 1) & 1;
-                const bool more = k + 1 < n;
-                if (more && !(ok = tile_ready(k + 1))) break;
-                // (past the last tile the commit alone tells that the sums
-                // before it are complete: a unit may wait for that to rescale)
-                if (more)
-                    scores(0, nxt);
-                else if (elect_one())
-                    mma_commit(&sfull[nxt]);
-                if (!(ok = wait(&pfull[cur], parity))) break;
-                tc_fence_after();
-                accumulate(0, cur, k == 0);
-                if (two) {
+            };
+            bool ok = n > 0 && (C::X_TMEM || await(xfull, 0));
+            // Products run in the order of their issue, so a score buffer may be
+            // filled again as soon as the sums that read it were issued.
+            if (FWD) {
+                const bool two = r0 + XR < nx;
+                if (ok && (ok = tile_ready())) {
+                    scores(0, 0);
+                    if (two) scores(1, 2);
+                    in.next();
+                }
+                for (int k = 0; ok && k < n; ++k) {
+                    const int cur = k & 1, nxt = cur ^ 1;
+                    const unsigned parity = unsigned(k >> 1) & 1;
+                    const bool more = k + 1 < n;
+                    if (more && !(ok = tile_ready())) break;
+                    // (past the last tile the commit alone tells that the sums
+                    // before it are complete: a unit may wait for that to rescale)
                     if (more)
-                        scores(1, 2 + nxt);
-                    else if (elect_one())
-                        mma_commit(&sfull[2 + nxt]);
-                    if (!(ok = wait(&pfull[2 + cur], parity))) break;
+                        scores(0, nxt);
+                    else
+                        mma_commit(&sfull[nxt]);
+                    if (!(ok = await(&pfull[cur], parity))) break;
                     tc_fence_after();
-                    accumulate(1, 2 + cur, k == 0);
-                }
-                if (elect_one()) mma_commit(&empty[out.s]);
-                out.next();
-                in.next();
-            }
-        } else {
-            for (int k = 0; ok && k < 2 && k < n; ++k)
-                if ((ok = tile_ready(k))) {
-                    scores(0, k & 1);
+                    accumulate(0, cur, k == 0);
+                    if (two) {
+                        if (more)
+                            scores(1, 2 + nxt);
+                        else
+                            mma_commit(&sfull[2 + nxt]);
+                        if (!(ok = await(&pfull[2 + cur], parity))) break;
+                        tc_fence_after();
+                        accumulate(1, 2 + cur, k == 0);
+                    }
+                    mma_commit(&empty[out.s]);
+                    out.next();
                     in.next();
                 }
-            for (int k = 0; ok && k < n; ++k) {
-                if (!(ok = wait(&pfull[k & 1], unsigned(k >> 1) & 1))) break;
-                tc_fence_after();
-                accumulate(0, k & 1, k == 0);
-                if (elect_one()) mma_commit(&empty[out.s]);
-                out.next();
-                if (k + 2 < n && (ok = tile_ready(k + 2))) {
-                    scores(0, k & 1);
-                    in.next();
+            } else {
+                for (int k = 0; ok && k < 2 && k < n; ++k)
+                    if ((ok = tile_ready())) {
+                        scores(0, k & 1);
+                        in.next();
+                    }
+                for (int k = 0; ok && k < n; ++k) {
+                    if (!(ok = await(&pfull[k & 1], unsigned(k >> 1) & 1))) break;
+                    tc_fence_after();
+                    accumulate(0, k & 1, k == 0);
+                    mma_commit(&empty[out.s]);
+                    out.next();
+                    if (k + 2 < n && (ok = tile_ready())) {
+                        scores(0, k & 1);
+                        in.next();
+                    }
                 }
             }
+            mma_commit(accfull);
+            mbar_wait_bounded(accfull, 0, a.timeout_ns);  // before the tensor memory is freed
         }
         __syncwarp();
-        if (elect_one()) mma_commit(accfull);
-        __syncwarp();
-        mbar_wait_bounded(accfull, 0, a.timeout_ns);  // before the tensor memory is freed
     } else if (warp < C::CWARPS) {
         // ---- weights ------------------------------------------------------------------
         const bool live = r0 + xt * XR + quad * 32 < nx;  // else nothing is read of its rows
@@ -559,6 +662,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         bool ok = true;
         int s = FWD ? 0 : unit;
         unsigned phase = 0;
+        Walk at = walk(FWD ? 0 : unit);
         for (int k = FWD ? 0 : unit; k < n; k += FWD ? 1 : 2, s += FWD ? 1 : 2) {
             if (s >= STAGES) s -= STAGES, phase ^= 1;
             const int buf = FWD ? 2 * unit + (k & 1) : unit;
@@ -567,7 +671,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
             tc_fence_after();
             const float *cd = coldata + s * C::COLF + 32 * half;
             const uint32_t sb = tmem + lanes + buf * C::BUF + 32 * half;
-            const int valid = ny - item_row(k) - 32 * half;  // columns of this half, if < 32
+            const int valid = ny - at.y - 32 * half;  // columns of this half, if < 32
+            at.next(FWD ? 1 : 2);
             const bool direct = BIAS && coldata[s * C::COLF + 5 * YR] != 0.0f;
             const float nb = BIAS ? coldata[s * C::COLF + 5 * YR + 1] : 0.0f;
             const float2 nb2 = make_float2(nb, nb);
@@ -602,10 +707,10 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
                 if (!(ok = wait(&mxbar[unit * 4 + quad], unsigned(k & 1)))) break;
                 m = fmaxf(m, mx[(half ^ 1) * XR]) * c2;
                 // The base of the exponents follows the maximum only when it
-                // grew by more than 2^8 (the weights stay below 256, far from
+                // grew by more than 2^16 (the weights stay below 65536, far from
                 // float32's and bfloat16's ends): the accumulator is seldom
                 // rescaled.
-                const bool need = m > mc + 8.0f;
+                const bool need = m > mc + 16.0f;
                 if (__any_sync(0xffffffffu, need)) {
                     const float mn = need ? m : mc;
                     const float f = mn == -INFINITY ? 1.0f : ex2(mc - mn);
