@@ -477,16 +477,17 @@ int pick_split(int64_t want, int64_t base, int64_t items, int64_t row_floats) {
 
 template <class T>
 cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes,
-                     cudaStream_t st) {
+                     const AttnSplit *parts, cudaStream_t st) {
     const bool dkv = mode == ATTN_DKV;
     const int64_t LX = dkv ? a.Lk : a.Lq, LY = dkv ? a.Lq : a.Lk, NH = dkv ? a.Hkv : a.H;
     const bool tc = sizeof(T) == 2 && attn_tc_fits(a, mode);
-    const int64_t xr = tc ? attn_tc_rows(mode) : SB, yr = tc ? ATTN_TC_TILE : SB;
+    const int64_t xr = tc ? attn_tc_rows(mode) : parts ? 128 : SB;
+    const int64_t yr = tc || parts ? ATTN_TC_TILE : SB;
     const int64_t ntile = (LX + xr - 1) / xr, nyt = (LY + yr - 1) / yr;
     const int64_t base = ntile * NH * a.B;
     const int64_t rows = int64_t(a.B) * LX * NH, hrows = int64_t(a.B) * a.H * a.Lq;
     // two blocks fit a SM, one of the tensor-core kernels
-    const int64_t want = int64_t(dev.sm_count) * (tc ? 1 : 2);
+    const int64_t want = int64_t(dev.sm_count) * (tc || parts ? 1 : 2);
     a.nsplit = pick_split(want, base, dkv ? nyt * (a.H / a.Hkv) : nyt,
                           rows * a.D * (dkv ? 2 : 1));
     const bool slopes = mode == ATTN_DQ && a.slopes != nullptr && dslopes != nullptr;
@@ -504,7 +505,8 @@ cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes
     const bool vec = strides_fit(a, 4, 4 * sizeof(T));
     const int64_t blocks = base * a.nsplit;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    e = tc                ? launch_attn_tc(a, mode, blocks, st)
+    e = tc                 ? launch_attn_tc(a, mode, blocks, st)
+        : parts            ? launch_attn_tc32(a, *parts, mode, blocks, st)
         : mode == ATTN_FWD ? simt_pick<T, ATTN_FWD>(a, vec, blocks, st)
         : mode == ATTN_DQ ? simt_pick<T, ATTN_DQ>(a, vec, blocks, st)
                           : simt_pick<T, ATTN_DKV>(a, vec, blocks, st);
@@ -525,24 +527,48 @@ cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes
     return cudaGetLastError();
 }
 
+// Whether float32 goes to the tensor cores: from AAAA scores on.
+template <class T>
+bool in_parts(const AttnArgs &a) {
+    return sizeof(T) == 4 && attn_tc32_fits(a);
+}
+
+template <class T>
+cudaError_t run_forward(const DeviceInfo &dev, const AttnArgs &a, cudaStream_t st) {
+    if (!in_parts<T>(a)) return run_pass<T>(dev, a, ATTN_FWD, nullptr, nullptr, st);
+    Scratch ws{&dev, st};
+    AttnSplit s;
+    cudaError_t e = ws.take(attn_split_bytes(a, false));
+    if (e == cudaSuccess) e = launch_attn_split(a, false, ws.p, &s, st);
+    return e == cudaSuccess ? run_pass<T>(dev, a, ATTN_FWD, nullptr, &s, st) : e;
+}
+
 template <class T>
 cudaError_t run_backward(const DeviceInfo &dev, AttnArgs a, const void *out, float *dslopes,
                          cudaStream_t st) {
     const int64_t rows = int64_t(a.B) * a.Lq * a.H;
+    const bool parts = in_parts<T>(a);
+    const size_t sides = (size_t(rows) * 2 * sizeof(float) + 255) / 256 * 256;
     Scratch ws{&dev, st};
-    cudaError_t e = ws.take(size_t(rows > 0 ? rows : 1) * 2 * sizeof(float));
+    cudaError_t e = ws.take(sides + (parts ? attn_split_bytes(a, true) : 1));
     if (e != cudaSuccess) return e;
     float *delta = static_cast<float *>(ws.p), *lse2 = delta + rows;
     a.delta = delta, a.lse2 = lse2;
+    AttnSplit sp, *s = nullptr;
+    if (parts) {
+        e = launch_attn_split(a, true, static_cast<char *>(ws.p) + sides, &sp, st);
+        if (e != cudaSuccess) return e;
+        s = &sp;
+    }
     if (rows > 0) {
         attn_delta_kernel<T><<<unsigned((rows + 7) / 8), 256, 0, st>>>(
             static_cast<const T *>(out), static_cast<const T *>(a.go), a.lse, rows, a.Lq, a.H,
             a.D, delta, lse2);
-        if ((e = run_pass<T>(dev, a, ATTN_DQ, dslopes, st)) != cudaSuccess) return e;
+        if ((e = run_pass<T>(dev, a, ATTN_DQ, dslopes, s, st)) != cudaSuccess) return e;
     } else if (dslopes != nullptr && a.slopes != nullptr) {
         if ((e = cudaMemsetAsync(dslopes, 0, size_t(a.H) * 4, st)) != cudaSuccess) return e;
     }
-    if (int64_t(a.B) * a.Lk * a.Hkv > 0) e = run_pass<T>(dev, a, ATTN_DKV, nullptr, st);
+    if (int64_t(a.B) * a.Lk * a.Hkv > 0) e = run_pass<T>(dev, a, ATTN_DKV, nullptr, s, st);
     return e;
 }
 
@@ -639,8 +665,8 @@ extern "C" int pc_attention(const void *q, const void *k, const void *v, int dty
     if (out_lse && (rc = api_check_ptr(out_lse, d, 4, "out_lse")) != PC_OK) return rc;
     a.out = out, a.lse = out_lse;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == PC_F32 ? run_pass<float>(*dev, a, ATTN_FWD, nullptr, st)
-                                          : run_pass<bf16>(*dev, a, ATTN_FWD, nullptr, st);
+    const cudaError_t e = dtype == PC_F32 ? run_forward<float>(*dev, a, st)
+                                          : run_forward<bf16>(*dev, a, st);
     return attn_cuda("attention", e);
 }
 

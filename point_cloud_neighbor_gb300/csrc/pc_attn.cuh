@@ -66,4 +66,17 @@ constexpr int ATTN_TC_TILE = 64;
 bool attn_tc_fits(const AttnArgs &a, int mode);
 cudaError_t launch_attn_tc(const AttnArgs &a, int mode, int64_t blocks, cudaStream_t st);
 
+// float32 on the tensor cores (pc_attn_tc32.cu; D <= 64): the arrays as three
+// bfloat16 parts [3][B, L, heads, Dp] each, written into `space` once a call.
+struct AttnSplit {
+    const bf16 *q, *k, *v, *go;
+    int Dp;
+};
+bool attn_tc32_fits(const AttnArgs &a);
+size_t attn_split_bytes(const AttnArgs &a, bool backward);
+cudaError_t launch_attn_split(const AttnArgs &a, bool backward, void *space, AttnSplit *s,
+                              cudaStream_t st);
+cudaError_t launch_attn_tc32(const AttnArgs &a, const AttnSplit &s, int mode, int64_t blocks,
+                             cudaStream_t st);
+
 }  // namespace pcn

@@ -39,9 +39,7 @@
 // Every wait is bounded: when one runs out the block raises the status word,
 // lets its copies and products finish, frees its tensor memory and returns;
 // its outputs are then unspecified.
-#include "pc_attn.cuh"
-#include "pc_tcgen05.cuh"
-#include "pc_tiles.cuh"
+#include "pc_attn_tc.cuh"
 #include "pointcloud.h"
 
 #include <type_traits>
@@ -49,8 +47,6 @@
 namespace pcn {
 namespace {
 
-constexpr int XR = 128;  // rows of a product
-constexpr int YR = ATTN_TC_TILE;
 constexpr float AUG_MOST = 256.0f;  // of slope R^2: see above
 
 struct AttnMaps {
@@ -90,42 +86,6 @@ struct Cfg {
                                    size_t(STAGES) * (STAGE + COLF * 4) + ROWF * 4 + 512;
     static_assert(SMEM <= 227 * 1024, "shared memory");
 };
-
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float fmax3(float a, float b, float c) {
-    float r;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
-    return r;
-}
-
-__device__ __forceinline__ float2 pair(const uint32_t *r, int i) {
-    return make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1]));
-}
-// v = hi + lo to 2^-16 of v, both bfloat16
-__device__ __forceinline__ void split_bf16(float2 v, uint32_t &hi, uint32_t &lo) {
-    hi = pack_bf16(v.x, v.y);
-    const float2 h = unpack_bf16(hi);
-    lo = pack_bf16(v.x - h.x, v.y - h.y);
-}
-
-// Squared distances of one point to four columns, in pairs.
-__device__ __forceinline__ void dist4(const float *cd, int c, float2 nx, float2 ny, float2 nz,
-                                      float2 &d0, float2 &d1) {
-    const float4 x = *reinterpret_cast<const float4 *>(cd + c);
-    const float4 y = *reinterpret_cast<const float4 *>(cd + YR + c);
-    const float4 z = *reinterpret_cast<const float4 *>(cd + 2 * YR + c);
-    float2 a = __fadd2_rn(make_float2(x.x, x.y), nx), b = __fadd2_rn(make_float2(x.z, x.w), nx);
-    d0 = __fmul2_rn(a, a), d1 = __fmul2_rn(b, b);
-    a = __fadd2_rn(make_float2(y.x, y.y), ny), b = __fadd2_rn(make_float2(y.z, y.w), ny);
-    d0 = __ffma2_rn(a, a, d0), d1 = __ffma2_rn(b, b, d1);
-    a = __fadd2_rn(make_float2(z.x, z.y), nz), b = __fadd2_rn(make_float2(z.z, z.w), nz);
-    d0 = __ffma2_rn(a, a, d0), d1 = __ffma2_rn(b, b, d1);
-}
 
 // A number as three bfloat16, the low one of what the others leave.
 struct Parts {
@@ -324,23 +284,8 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         }
         return __all_sync(0xffffffffu, w == WAIT_OK) != 0;
     };
-    // The head and first row of the block's tiles, one after the other.
-    struct Walk {
-        int h, y, end;
-        __device__ __forceinline__ void next(int tiles = 1) {
-            y += tiles * YR;
-            if (DKV)
-                while (y >= end) y -= end, ++h;
-        }
-    };
     auto walk = [&](int skip) {
-        Walk w{DKV ? hk * G : head, 0, nyt * YR};
-        if (n > 0) {
-            if (DKV) w.h += int(it0 / nyt);
-            w.y = int(DKV ? it0 % nyt : it0) * YR;
-            w.next(skip);
-        }
-        return w;
+        return TileWalk(DKV, DKV ? hk * G : head, n > 0 ? nyt : 0, it0, skip);
     };
 
     if (warp == C::CWARPS) {
@@ -361,7 +306,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         }
         // Rows of a tile past the length are overwritten with zeros once the tile
         // is there: two tiles later, so that copies stay ahead.
-        Walk late = walk(0);
+        TileWalk late = walk(0);
         auto fix = [&](int k) {
             const int valid = ny - late.y, s = k % STAGES;
             late.next();
@@ -381,7 +326,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         };
         int issued = 0;
         bool ok = true;
-        Walk at = walk(0);
+        TileWalk at = walk(0);
         for (int k = 0; ok && k < n; ++k, at.next()) {
             const int s = k % STAGES;
             if (k >= STAGES && !wait(&empty[s], unsigned((k / STAGES - 1) & 1))) break;
@@ -409,7 +354,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
     } else if (COLS && warp >= C::CWARPS + 2) {
         // ---- positions: two warps, every other tile each ------------------------------
         const int first = warp - (C::CWARPS + 2);
-        Walk at = walk(first);
+        TileWalk at = walk(first);
         float nxt[2][5], slope_nxt = 0.0f;  // of the warp's next tile: loaded a tile ahead
         auto fetch = [&]() {
 #pragma unroll
@@ -501,7 +446,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
                     if (++s == STAGES) s = 0, phase ^= 1;
                 }
             } in, out;  // tiles whose scores, whose sums are issued
-            Walk at = walk(0);
+            TileWalk at = walk(0);
             unsigned fixes = 0;  // a bit per stage: the parity of its next fix
             auto await = [&](uint64_t *bar, unsigned parity) {
                 const WaitResult w = mbar_wait_or_stop(bar, parity, stop, a.timeout_ns);
@@ -662,7 +607,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         bool ok = true;
         int s = FWD ? 0 : unit;
         unsigned phase = 0;
-        Walk at = walk(FWD ? 0 : unit);
+        TileWalk at = walk(FWD ? 0 : unit);
         for (int k = FWD ? 0 : unit; k < n; k += FWD ? 1 : 2, s += FWD ? 1 : 2) {
             if (s >= STAGES) s -= STAGES, phase ^= 1;
             const int buf = FWD ? 2 * unit + (k & 1) : unit;
@@ -898,43 +843,6 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
     __syncthreads();
     tc_fence_after();
     if (warp == C::CWARPS + 1) tmem_free(tmem, C::COLS);
-}
-
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-    static const EncodeFn fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            p = nullptr;
-        }
-        return reinterpret_cast<EncodeFn>(p);
-    }();
-    return fn;
-}
-
-// [B, L, heads, D] as boxes of 64 rows by 64 channels.
-bool make_map(CUtensorMap *map, const void *p, const int64_t *s, int64_t B, int64_t L,
-              int64_t heads, int64_t D) {
-    const EncodeFn fn = encode_fn();
-    if (fn == nullptr) return false;
-    const cuuint64_t dims[4] = {cuuint64_t(D), cuuint64_t(L), cuuint64_t(heads), cuuint64_t(B)};
-    // the stride of an axis of one element is never used: any valid one
-    const cuuint64_t strides[3] = {cuuint64_t(L > 1 ? s[1] : D) * 2,
-                                   cuuint64_t(heads > 1 ? s[2] : D) * 2,
-                                   cuuint64_t(B > 1 ? s[0] : D) * 2};
-    const cuuint32_t box[4] = {64, YR, 1, 1}, ones[4] = {1, 1, 1, 1};
-    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(p), dims, strides, box,
-              ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 template <int MODE, int DP, bool BIAS>
