@@ -481,7 +481,7 @@ cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes
     const bool dkv = mode == ATTN_DKV;
     const int64_t LX = dkv ? a.Lk : a.Lq, LY = dkv ? a.Lq : a.Lk, NH = dkv ? a.Hkv : a.H;
     const bool tc = sizeof(T) == 2 && attn_tc_fits(a, mode);
-    const int64_t xr = tc ? attn_tc_rows(mode) : parts ? 128 : SB;
+    const int64_t xr = tc ? attn_tc_rows(mode) : parts ? attn_tc32_rows(a, mode) : SB;
     const int64_t yr = tc || parts ? ATTN_TC_TILE : SB;
     const int64_t ntile = (LX + xr - 1) / xr, nyt = (LY + yr - 1) / yr;
     const int64_t base = ntile * NH * a.B;

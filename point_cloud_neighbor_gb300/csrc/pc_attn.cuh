@@ -66,13 +66,14 @@ constexpr int ATTN_TC_TILE = 64;
 bool attn_tc_fits(const AttnArgs &a, int mode);
 cudaError_t launch_attn_tc(const AttnArgs &a, int mode, int64_t blocks, cudaStream_t st);
 
-// float32 on the tensor cores (pc_attn_tc32.cu; D <= 64): the arrays as three
+// float32 on the tensor cores (pc_attn_tc32.cu): the arrays as three
 // bfloat16 parts [3][B, L, heads, Dp] each, written into `space` once a call.
 struct AttnSplit {
     const bf16 *q, *k, *v, *go;
     int Dp;
 };
 bool attn_tc32_fits(const AttnArgs &a);
+int attn_tc32_rows(const AttnArgs &a, int mode);  // rows a block keeps
 size_t attn_split_bytes(const AttnArgs &a, bool backward);
 cudaError_t launch_attn_split(const AttnArgs &a, bool backward, void *space, AttnSplit *s,
                               cudaStream_t st);

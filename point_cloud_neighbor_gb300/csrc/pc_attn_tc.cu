@@ -374,10 +374,14 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         };
         const float xmost = BIAS ? __int_as_float(*xr2) : 0.0f;
         if (first < n) fetch();
-        int s = first;
+        int s = 0;
         unsigned phase = 1;  // of the stage's last release: none in the first round
-        for (int k = first; k < n; k += 2, s += 2) {
-            if (s >= STAGES) s -= STAGES, phase ^= 1;
+        for (int k = 0; k < n; ++k, ++s) {
+            if (s == STAGES) s = 0, phase ^= 1;
+            // (no release is passed over: a parity tells only the last from the
+            // one before)
+            if (k >= STAGES && !wait(&empty[s], phase)) break;
+            if ((k & 1) != first) continue;
             float cur[2][5];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -387,7 +391,6 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
             const int valid = ny - at.y;
             at.next(2);
             if (k + 2 < n) fetch();
-            if (k >= STAGES && !wait(&empty[s], phase)) break;
             float *cd = coldata + s * C::COLF;
             bool direct = true;
             if (BIAS) {

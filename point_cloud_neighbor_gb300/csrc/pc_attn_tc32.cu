@@ -1,5 +1,5 @@
 // pc_attn_tc32.cu -- the attention passes of pc_attn.cuh on the tensor cores,
-// for float32 and up to 64 channels.
+// for float32.
 //
 // A float32 is the sum of three bfloat16 (8 bits each), and a product of two
 // such sums is six products of bfloat16 to about 2^-24: low x high, high x low,
@@ -16,8 +16,10 @@
 //
 // A block keeps 128 rows and walks over the other side in tiles of 64; eight
 // warps compute weights, a thread half a row; two score buffers, so that the
-// products of one tile run under the weights of another.  The bias is formed
-// from coordinates' differences.  Bound: the products, 6 times those of
+// products of one tile run under the weights of another.  The parts of more
+// than 64 channels leave room for less in the backward passes: 64 rows (of
+// products of 128: half the rate), one stage and one score buffer.  The bias
+// is formed from coordinates' differences.  Bound: the products, 6 times those of
 // bfloat16; the same passes in float32 instructions take 5 to 8 times longer.
 //
 // Lengths, waits and their end as in pc_attn_tc.cu.
@@ -27,25 +29,26 @@
 namespace pcn {
 namespace {
 
-constexpr int DP = 64;  // channels of a tile, zeros past D
-
 struct SplitMaps {
     CUtensorMap q, k, v, go;  // [3 B, L, heads, Dp] bfloat16
 };
 
-template <int MODE>
+template <int MODE, int DP>
 struct Cfg32 {
-    static constexpr bool BWD = MODE != ATTN_FWD;
+    static constexpr bool BWD = MODE != ATTN_FWD, WIDE = DP == 128;
     static constexpr int CWARPS = 8, THREADS = 32 * (CWARPS + 4);
-    static constexpr int STAGES = MODE == ATTN_FWD ? 4 : MODE == ATTN_DQ ? 4 : 2;
-    // Tensor memory: two score buffers (S, dP and room for the parts of P and
-    // dS), the tile's sums, and where there is room the rows kept.
+    static constexpr int ROWS = BWD && WIDE ? 64 : XR;  // rows kept
+    static constexpr int NB = BWD && WIDE ? 1 : 2;      // score buffers
+    static constexpr int STAGES = WIDE ? (BWD ? 1 : 2) : MODE == ATTN_DKV ? 2 : 4;
+    // Tensor memory: score buffers (S, dP and room for the parts of P and dS),
+    // the tile's sums, and where there is room the rows kept.
     static constexpr int BUF = MODE == ATTN_FWD ? 96 : MODE == ATTN_DQ ? 128 : 192;
     static constexpr int NACC = MODE == ATTN_DKV ? 2 : 1;
-    static constexpr int ACC = 2 * BUF, XCOL = ACC + NACC * DP;
-    static constexpr bool X_TMEM = MODE != ATTN_DKV;
-    static_assert(XCOL + (X_TMEM ? (BWD ? 2 : 1) * 96 : 0) <= 512, "tensor memory");
-    static constexpr int XP = XR * DP * 2, YP = YR * DP * 2;  // bytes of a part
+    static constexpr int ACC = NB * BUF, XCOL = ACC + NACC * DP;
+    static constexpr int XCOLS = 3 * DP / 2;            // three parts of one array
+    static constexpr bool X_TMEM = MODE == ATTN_FWD || (MODE == ATTN_DQ && !WIDE);
+    static_assert(XCOL + (X_TMEM ? (BWD ? 2 : 1) * XCOLS : 0) <= 512, "tensor memory");
+    static constexpr int XP = ROWS * DP * 2, YP = YR * DP * 2;  // bytes of a part
     static constexpr size_t XSMEM = X_TMEM ? 0 : 6 * XP;
     static constexpr int STAGE = 6 * YP;
     static constexpr int COLF = 5 * YR + 4;
@@ -82,11 +85,11 @@ __device__ __forceinline__ void store_row(float *p, const float (&v)[32], int c0
     }
 }
 
-template <int MODE, bool BIAS>
-__global__ void __launch_bounds__(Cfg32<MODE>::THREADS, 1)
+template <int MODE, int DP, bool BIAS>
+__global__ void __launch_bounds__(Cfg32<MODE, DP>::THREADS, 1)
 attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ SplitMaps maps,
                  const AttnSplit split_ptr, const bool withhold) {
-    using C = Cfg32<MODE>;
+    using C = Cfg32<MODE, DP>;
     constexpr bool BWD = C::BWD, FWD = !BWD, DKV = MODE == ATTN_DKV;
     constexpr int STAGES = C::STAGES;
     extern __shared__ unsigned char smem_raw[];
@@ -106,7 +109,7 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
     const int LX = DKV ? a.Lk : a.Lq, LY = DKV ? a.Lq : a.Lk;
     const int NH = DKV ? a.Hkv : a.H;
     const int G = a.H / a.Hkv;
-    const int ntile = (LX + XR - 1) / XR;
+    const int ntile = (LX + C::ROWS - 1) / C::ROWS;
     int64_t idx = blockIdx.x;
     const int split = int(idx % a.nsplit);
     idx /= a.nsplit;
@@ -115,7 +118,7 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
     const int head = int(idx % NH), b = int(idx / NH);
     const int nq = attn_len(a.qlen, b, a.Lq), nk = attn_len(a.rlen, b, a.Lk);
     const int nx = uniform(DKV ? nk : nq), ny = uniform(DKV ? nq : nk);
-    const int r0 = tile * XR;
+    const int r0 = tile * C::ROWS;
     const int hk = DKV ? head : head / G;
     const int nyt = (ny + YR - 1) / YR;
     const int64_t items = nx > r0 ? int64_t(nyt) * (DKV ? G : 1) : 0;
@@ -124,7 +127,8 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
     const float *xpos = DKV ? a.rxyz : a.qxyz, *ypos = DKV ? a.qxyz : a.rxyz;
     const bool ragged = ny < LY && ny % YR != 0;
     const int quad = warp % 4, half = (warp / 4) % 2;
-    const int row = r0 + quad * 32 + lane;
+    // (lanes of products past the rows kept have no row)
+    const int row = quad * 32 < C::ROWS ? r0 + quad * 32 + lane : 0x7fffffff;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) {
@@ -159,17 +163,19 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
                                   ((int64_t(p * a.B + b) * a.Lq + row) * a.H + head) *
                                       split_ptr.Dp;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
+                for (int c = 0; c < DP / 32; ++c) {
                     uint32_t r[8];
 #pragma unroll
                     for (int e = 0; e < 2; ++e) {
-                        const int ch = half * 32 + 16 * c + 8 * e;
+                        const int ch = half * (DP / 2) + 16 * c + 8 * e;
                         uint4 v = make_uint4(0, 0, 0, 0);
                         if (row < nx && ch < split_ptr.Dp)
                             v = *reinterpret_cast<const uint4 *>(src + ch);
                         r[4 * e] = v.x, r[4 * e + 1] = v.y, r[4 * e + 2] = v.z, r[4 * e + 3] = v.w;
                     }
-                    tmem_st8(tmem + lanes + C::XCOL + t * 96 + p * 32 + half * 16 + 8 * c, r);
+                    tmem_st8(tmem + lanes + C::XCOL + t * C::XCOLS + p * (DP / 2) + half * (DP / 4) +
+                                 8 * c,
+                             r);
                 }
             }
         tmem_wait_st();
@@ -193,14 +199,18 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
 
     if (warp == C::CWARPS) {
         // ---- copies ---------------------------------------------------------------
-        if (DKV && n > 0 && elect_one()) {
+        if (!C::X_TMEM && n > 0 && elect_one()) {
             mbar_arrive_expect_tx(xfull, 6 * C::XP);
             for (int p = 0; p < 3; ++p)
-                for (int h = 0; h < 2; ++h) {
-                    unsigned char *at = X + p * C::XP + h * C::YP;
-                    tma_load_4d(at, &maps.k, 0, r0 + YR * h, head, p * a.B + b, xfull);
-                    tma_load_4d(at + 3 * C::XP, &maps.v, 0, r0 + YR * h, head, p * a.B + b, xfull);
-                }
+                for (int c = 0; c < DP / 64; ++c)
+                    for (int h = 0; h < C::ROWS / YR; ++h) {
+                        unsigned char *at =
+                            X + p * C::XP + c * C::ROWS * 128 + h * YR * 128;
+                        tma_load_4d(at, DKV ? &maps.k : &maps.q, 64 * c, r0 + YR * h, head,
+                                    p * a.B + b, xfull);
+                        tma_load_4d(at + 3 * C::XP, DKV ? &maps.v : &maps.go, 64 * c, r0 + YR * h,
+                                    head, p * a.B + b, xfull);
+                    }
         }
         TileWalk late = walk(0);
         auto fix = [&](int k) {
@@ -211,8 +221,9 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
             uint4 *y = reinterpret_cast<uint4 *>(Y + size_t(s) * C::STAGE);
             for (int p = 0; p < 6; ++p)
                 if (BWD ? DKV || p < 3 : p >= 3)
-                    for (int i = valid * 8 + lane; i < YR * 8; i += 32)
-                        y[p * (C::YP / 16) + i] = make_uint4(0, 0, 0, 0);
+                    for (int c = 0; c < DP / 64; ++c)
+                        for (int i = valid * 8 + lane; i < YR * 8; i += 32)
+                            y[p * (C::YP / 16) + c * YR * 8 + i] = make_uint4(0, 0, 0, 0);
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(&fixed[s]);
@@ -221,7 +232,7 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
         int issued = 0;
         bool ok = true;
         TileWalk at = walk(0);
-        constexpr int LAG = STAGES > 2 ? 2 : 1;
+        constexpr int LAG = STAGES > 2 ? 2 : STAGES - 1;
         for (int k = 0; ok && k < n; ++k, at.next()) {
             const int s = k % STAGES;
             if (k >= STAGES && !wait(&empty[s], unsigned((k / STAGES - 1) & 1))) break;
@@ -230,12 +241,13 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
                 const int hy = DKV ? at.h : hk;
                 mbar_arrive_expect_tx(&full[s], 6 * C::YP);
                 unsigned char *y = Y + size_t(s) * C::STAGE;
-                for (int p = 0; p < 3; ++p) {
-                    tma_load_4d(y + p * C::YP, DKV ? &maps.q : &maps.k, 0, at.y, hy,
-                                p * a.B + b, &full[s]);
-                    tma_load_4d(y + (3 + p) * C::YP, DKV ? &maps.go : &maps.v, 0, at.y, hy,
-                                p * a.B + b, &full[s]);
-                }
+                for (int p = 0; p < 3; ++p)
+                    for (int c = 0; c < DP / 64; ++c) {
+                        tma_load_4d(y + p * C::YP + c * YR * 128, DKV ? &maps.q : &maps.k, 64 * c,
+                                    at.y, hy, p * a.B + b, &full[s]);
+                        tma_load_4d(y + (3 + p) * C::YP + c * YR * 128, DKV ? &maps.go : &maps.v,
+                                    64 * c, at.y, hy, p * a.B + b, &full[s]);
+                    }
             }
             issued = k + 1;
             if (k >= LAG) ok = fix(k - LAG);
@@ -243,7 +255,7 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
         if (issued == n)
             for (int k = max(0, n - LAG); ok && k < n; ++k) ok = fix(k);
         // nothing is in flight when the block ends
-        if (DKV && n > 0) mbar_wait_bounded(xfull, 0, a.timeout_ns);
+        if (!C::X_TMEM && n > 0) mbar_wait_bounded(xfull, 0, a.timeout_ns);
         for (int k = max(0, issued - STAGES); k < issued; ++k)
             mbar_wait_bounded(&full[k % STAGES], unsigned((k / STAGES) & 1), a.timeout_ns);
     } else if (warp >= C::CWARPS + 2) {
@@ -268,10 +280,14 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
             if (BIAS) slope_nxt = a.slopes[at.h];
         };
         if (first < n) fetch();
-        int s = first % STAGES;
-        unsigned phase = 1;
-        for (int k = first; k < n; k += 2, s += 2) {
-            if (s >= STAGES) s -= STAGES, phase ^= 1;
+        int s = 0;
+        unsigned phase = 1;  // of the stage's last release: none in the first round
+        for (int k = 0; k < n; ++k, ++s) {
+            if (s == STAGES) s = 0, phase ^= 1;
+            // (no release is passed over: a parity tells only the last from the
+            // one before)
+            if (k >= STAGES && !wait(&empty[s], phase)) break;
+            if ((k & 1) != first) continue;
             float cur[2][5];
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -280,7 +296,6 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
             const float slope = slope_nxt;
             at.next(2);
             if (k + 2 < n) fetch();
-            if (k >= STAGES && !wait(&empty[s], phase)) break;
             float *cd = coldata + s * C::COLF;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
@@ -295,7 +310,7 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
         // ---- products, issued by one thread -------------------------------------------
         if (elect_one()) {
             const uint32_t x0 = smem_operand(smem_u32(X)), yk = smem_operand(smem_u32(Y));
-            const uint32_t yr = smem_operand(smem_u32(Y), 16);
+            const uint32_t yr = smem_operand(smem_u32(Y), YR * 128);
             int in = 0, out = 0;  // stages of the tiles whose scores, whose sums come next
             unsigned phase = 0, fixes = 0;
             TileWalk at = walk(0);
@@ -324,15 +339,17 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
                     for (int p = 0; p < 6; ++p)
 #pragma unroll
                         for (int i = 0; i < DP / 16; ++i) {
-                            const uint32_t yo =
-                                y + (3 * t + PAIR_B[p]) * (C::YP / 16) + 2 * i;
+                            const uint32_t yo = y + (3 * t + PAIR_B[p]) * (C::YP / 16) +
+                                                (i / 4) * (YR * 128 / 16) + 2 * (i % 4);
                             if (C::X_TMEM)
                                 mma_ts<SMEM_128B>(d + t * YR,
-                                                  tmem + C::XCOL + 96 * t + 32 * PAIR_A[p] + 8 * i,
+                                                  tmem + C::XCOL + C::XCOLS * t +
+                                                      (DP / 2) * PAIR_A[p] + 8 * i,
                                                   yo, id, p > 0 || i > 0);
                             else
                                 mma_ss<SMEM_128B>(d + t * YR,
-                                                  x0 + (3 * t + PAIR_A[p]) * (C::XP / 16) + 2 * i,
+                                                  x0 + (3 * t + PAIR_A[p]) * (C::XP / 16) +
+                                                      (i / 4) * (C::ROWS * 128 / 16) + 2 * (i % 4),
                                                   yo, id, p > 0 || i > 0);
                         }
                 mma_commit(&sfull[buf]);
@@ -366,12 +383,14 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
             };
             bool ok = n > 0 && (C::X_TMEM || await(xfull, 0)) && scores(0);
             for (int k = 0; ok && k < n; ++k) {
-                // Products run in the order of their issue: the buffer of tile
-                // k - 1 is free again, its sums were issued.
-                if (k + 1 < n && !(ok = scores((k + 1) & 1))) break;
-                if (!(ok = await(&pfull[k & 1], unsigned(k >> 1) & 1))) break;
+                // Products run in the order of their issue: a buffer is free again
+                // once the sums that read it were issued.
+                const int buf = C::NB == 2 ? k & 1 : 0;
+                if (C::NB == 2 && k + 1 < n && !(ok = scores(buf ^ 1))) break;
+                if (!(ok = await(&pfull[buf], unsigned(C::NB == 2 ? k >> 1 : k) & 1))) break;
                 tc_fence_after();
-                accumulate(k & 1);
+                accumulate(buf);
+                if (C::NB == 1 && k + 1 < n) ok = scores(0);
             }
             mma_commit(accdone);
             mbar_wait_bounded(accdone, 0, a.timeout_ns);  // before the tensor memory is freed
@@ -379,7 +398,7 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
         __syncwarp();
     } else {
         // ---- weights ------------------------------------------------------------------
-        const bool live = r0 + quad * 32 < nx;
+        const bool live = quad * 32 < C::ROWS && r0 + quad * 32 < nx;
         const float c2 = a.scale * ATTN_LOG2E;
         const float2 c22 = make_float2(c2, c2);
         float px = 0.0f, py = 0.0f, pz = 0.0f;
@@ -399,24 +418,26 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
         float2 l2 = make_float2(0.0f, 0.0f), wa = l2, we = l2, wd = l2;
         const bool sums = MODE == ATTN_DQ && BIAS && a.rowsum != nullptr;
         float *rd = rowdata + quad * 32 + lane;
-        float acc[C::NACC][32];
+        float acc[C::NACC][DP / 2];
 #pragma unroll
         for (int t = 0; t < C::NACC; ++t)
 #pragma unroll
-            for (int e = 0; e < 32; ++e) acc[t][e] = 0.0f;
+            for (int e = 0; e < DP / 2; ++e) acc[t][e] = 0.0f;
         // the sums of tile k into the registers
         auto drain = [&](int k) {
             if (!wait(tfull, unsigned(k & 1))) return false;
             tc_fence_after();
             if (live)
 #pragma unroll
-                for (int t = 0; t < C::NACC; ++t) {
-                    uint32_t r[32];
-                    tmem_ld32(tmem + lanes + C::ACC + t * DP + 32 * half, r);
-                    tmem_wait_ld();
+                for (int t = 0; t < C::NACC; ++t)
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) acc[t][e] += __uint_as_float(r[e]);
-                }
+                    for (int c = 0; c < DP / 64; ++c) {
+                        uint32_t r[32];
+                        tmem_ld32(tmem + lanes + C::ACC + t * DP + half * (DP / 2) + 32 * c, r);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) acc[t][32 * c + e] += __uint_as_float(r[e]);
+                    }
             return true;
         };
         bool ok = true;
@@ -424,8 +445,8 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
         unsigned phase = 0;
         TileWalk at = walk(0);
         for (int k = 0; k < n; ++k) {
-            const int buf = k & 1;
-            if (!(ok = wait(&sfull[buf], unsigned(k >> 1) & 1))) break;
+            const int buf = C::NB == 2 ? k & 1 : 0;
+            if (!(ok = wait(&sfull[buf], unsigned(C::NB == 2 ? k >> 1 : k) & 1))) break;
             if (!(ok = wait(&full[s], phase))) break;
             tc_fence_after();
             const float *cd = coldata + s * C::COLF + 32 * half;
@@ -544,7 +565,7 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
             if (k > 0 && !(ok = drain(k - 1))) break;
             if (FWD && f != 1.0f)
 #pragma unroll
-                for (int e = 0; e < 32; ++e) acc[0][e] *= f;
+                for (int e = 0; e < DP / 2; ++e) acc[0][e] *= f;
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();
@@ -589,19 +610,23 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
         if (row < LX) {
             const int64_t orow = (int64_t(b) * LX + row) * NH + head;
             const int64_t rows = int64_t(a.B) * LX * NH;
-            const int c0 = 32 * half;
 #pragma unroll
             for (int t = 0; t < C::NACC; ++t) {
                 const float g = a.nsplit > 1 ? 1.0f : FWD ? 1.0f / l : t == 0 ? a.scale : 1.0f;
-                float v[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = any ? acc[t][e] * g : 0.0f;
-                if (a.nsplit > 1) {
-                    store_row(a.part + ((int64_t(t) * a.nsplit + split) * rows + orow) * a.D + c0,
-                              v, c0, a.D);
-                } else {
-                    void *o = FWD ? a.out : MODE == ATTN_DQ ? a.dq : t ? a.dv : a.dk;
-                    store_row(static_cast<float *>(o) + orow * a.D + c0, v, c0, a.D);
+                for (int c = 0; c < DP / 64; ++c) {
+                    const int c0 = half * (DP / 2) + 32 * c;
+                    float v[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = any ? acc[t][32 * c + e] * g : 0.0f;
+                    if (a.nsplit > 1) {
+                        store_row(
+                            a.part + ((int64_t(t) * a.nsplit + split) * rows + orow) * a.D + c0, v,
+                            c0, a.D);
+                    } else {
+                        void *o = FWD ? a.out : MODE == ATTN_DQ ? a.dq : t ? a.dv : a.dk;
+                        store_row(static_cast<float *>(o) + orow * a.D + c0, v, c0, a.D);
+                    }
                 }
             }
         }
@@ -645,28 +670,36 @@ __global__ void __launch_bounds__(256) attn_split_kernel(const SplitArgs a) {
             make_uint4(p[t][0], p[t][1], p[t][2], p[t][3]);
 }
 
-template <int MODE>
+template <int MODE, int DP, bool BIAS>
 cudaError_t tc32_launch(const AttnArgs &a, const SplitMaps &m, const AttnSplit &s, int64_t blocks,
                         cudaStream_t st) {
-    using C = Cfg32<MODE>;
-    const bool withhold = (debug_stall() & PC_STALL_ATTENTION) != 0;
-    static std::atomic<uint64_t> done[2] = {{0}, {0}};
-    cudaError_t e;
-    if (a.slopes) {
-        e = allow_smem(attn_tc32_kernel<MODE, true>, int(C::SMEM), a.device, done[1]);
-        if (e != cudaSuccess) return e;
-        attn_tc32_kernel<MODE, true><<<unsigned(blocks), C::THREADS, C::SMEM, st>>>(a, m, s, withhold);
-    } else {
-        e = allow_smem(attn_tc32_kernel<MODE, false>, int(C::SMEM), a.device, done[0]);
-        if (e != cudaSuccess) return e;
-        attn_tc32_kernel<MODE, false><<<unsigned(blocks), C::THREADS, C::SMEM, st>>>(a, m, s, withhold);
-    }
+    using C = Cfg32<MODE, DP>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e =
+        allow_smem(attn_tc32_kernel<MODE, DP, BIAS>, int(C::SMEM), a.device, done);
+    if (e != cudaSuccess) return e;
+    attn_tc32_kernel<MODE, DP, BIAS><<<unsigned(blocks), C::THREADS, C::SMEM, st>>>(
+        a, m, s, (debug_stall() & PC_STALL_ATTENTION) != 0);
     return cudaGetLastError();
+}
+
+template <int MODE>
+cudaError_t tc32_pick(const AttnArgs &a, const SplitMaps &m, const AttnSplit &s, int64_t blocks,
+                      cudaStream_t st) {
+    if (a.D <= 64)
+        return a.slopes ? tc32_launch<MODE, 64, true>(a, m, s, blocks, st)
+                        : tc32_launch<MODE, 64, false>(a, m, s, blocks, st);
+    return a.slopes ? tc32_launch<MODE, 128, true>(a, m, s, blocks, st)
+                    : tc32_launch<MODE, 128, false>(a, m, s, blocks, st);
 }
 
 }  // namespace
 
-bool attn_tc32_fits(const AttnArgs &a) { return a.D <= DP && a.Lq >= 1 && a.Lk >= 1; }
+bool attn_tc32_fits(const AttnArgs &a) { return a.Lq >= 1 && a.Lk >= 1; }
+
+int attn_tc32_rows(const AttnArgs &a, int mode) {
+    return mode != ATTN_FWD && a.D > 64 ? 64 : XR;
+}
 
 size_t attn_split_bytes(const AttnArgs &a, bool backward) {
     const size_t Dp = size_t(a.D + 7) / 8 * 8;
@@ -712,9 +745,9 @@ cudaError_t launch_attn_tc32(const AttnArgs &a, const AttnSplit &s, int mode, in
         !make_map(&m.v, s.v, ks, planes, a.Lk, a.Hkv, D) ||
         (mode != ATTN_FWD && !make_map(&m.go, s.go, qs, planes, a.Lq, a.H, D)))
         return cudaErrorInvalidValue;
-    return mode == ATTN_FWD  ? tc32_launch<ATTN_FWD>(a, m, s, blocks, st)
-           : mode == ATTN_DQ ? tc32_launch<ATTN_DQ>(a, m, s, blocks, st)
-                             : tc32_launch<ATTN_DKV>(a, m, s, blocks, st);
+    return mode == ATTN_FWD  ? tc32_pick<ATTN_FWD>(a, m, s, blocks, st)
+           : mode == ATTN_DQ ? tc32_pick<ATTN_DQ>(a, m, s, blocks, st)
+                             : tc32_pick<ATTN_DKV>(a, m, s, blocks, st);
 }
 
 }  // namespace pcn
