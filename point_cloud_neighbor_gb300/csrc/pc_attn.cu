@@ -352,49 +352,74 @@ attn_delta_kernel(const T *out, const T *go, const float *lse, int64_t rows, int
     }
 }
 
-// Joins the parts of a split forward pass: a warp per (token, head).
-template <class T>
+// Joins the parts of a split forward pass: a thread per V channels of a row.
+template <class T, int V>
 __global__ void __launch_bounds__(256) attn_join_forward_kernel(const AttnArgs a) {
     const int64_t rows = int64_t(a.B) * a.Lq * a.H;
-    const int64_t row = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;
+    const int64_t id = int64_t(blockIdx.x) * 256 + threadIdx.x;
+    const int groups = a.D / V;
+    const int64_t row = id / groups;
     if (row >= rows) return;
-    const int lane = threadIdx.x % 32;
+    const int c = int(id - row * groups) * V;
     const int64_t tok = row / a.H, b = tok / a.Lq;
     const int i = int(tok - b * a.Lq);
-    const int64_t hrow = (b * a.H + row % a.H) * a.Lq + i;
-    float m = -INFINITY, l = 0.0f;
+    const int64_t hrow = (b * a.H + (row - tok * a.H)) * a.Lq + i;
+    const float *ml = a.part_ml + hrow;
+    float m = -INFINITY;
+#pragma unroll 4
+    for (int s = 0; s < a.nsplit; ++s) m = fmaxf(m, ml[int64_t(s) * 2 * rows]);
+    const float base = m == -INFINITY ? 0.0f : m;
+    const bool valid = i < attn_len(a.qlen, int(b), a.Lq);
+    float l = 0.0f, v[V] = {};
+#pragma unroll 4
     for (int s = 0; s < a.nsplit; ++s) {
-        const float ms = a.part_ml[int64_t(s) * 2 * rows + hrow];
-        const float mn = fmaxf(m, ms), base = mn == -INFINITY ? 0.0f : mn;
-        l = fmaf(l, exp2f(m - base),
-                 a.part_ml[(int64_t(s) * 2 + 1) * rows + hrow] * exp2f(ms - base));
-        m = mn;
+        const float w = exp2f(ml[int64_t(s) * 2 * rows] - base);
+        float p[V];
+        Vec<float, V>::load(a.part + (int64_t(s) * rows + row) * a.D + c, p);
+        l = fmaf(w, ml[(int64_t(s) * 2 + 1) * rows], l);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = fmaf(w, p[e], v[e]);
     }
-    const bool any = i < attn_len(a.qlen, int(b), a.Lq) && l > 0.0f;
-    const float f = any ? 1.0f / l : 0.0f, base = m == -INFINITY ? 0.0f : m;
-    for (int c = lane; c < a.D; c += 32) {
-        float v = 0.0f;
-        if (any)
-            for (int s = 0; s < a.nsplit; ++s)
-                v = fmaf(a.part[(int64_t(s) * rows + row) * a.D + c],
-                         exp2f(a.part_ml[int64_t(s) * 2 * rows + hrow] - base), v);
-        v *= f;
-        Vec<T, 1>::store(static_cast<T *>(a.out) + row * a.D + c, &v);
-    }
-    if (lane == 0 && a.lse != nullptr)
+    const bool any = valid && l > 0.0f;
+    const float f = 1.0f / l;
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] = any ? v[e] * f : 0.0f;
+    Vec<T, V>::store(static_cast<T *>(a.out) + row * a.D + c, v);
+    if (c == 0 && a.lse != nullptr)
         a.lse[hrow] = any ? (m + log2f(l)) * ATTN_LN2 : -INFINITY;
 }
 
-// out = factor * sum of the parts.
-template <class T>
+// out = factor * sum of the parts, V elements a thread; a second array of the
+// same size follows with blockIdx.y = 1.
+template <class T, int V>
 __global__ void __launch_bounds__(256)
-attn_join_sum_kernel(const float *part, int nsplit, int64_t n, float factor, T *out) {
-    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x;
+attn_join_sum_kernel(const float *part, int nsplit, int64_t n, float factor, T *out, T *out2) {
+    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * V;
     if (i >= n) return;
-    float v = 0.0f;
-    for (int s = 0; s < nsplit; ++s) v += part[int64_t(s) * n + i];
-    v *= factor;
-    Vec<T, 1>::store(out + i, &v);
+    if (blockIdx.y == 1) part += int64_t(nsplit) * n, out = out2, factor = 1.0f;
+    float v[V] = {};
+#pragma unroll 4
+    for (int s = 0; s < nsplit; ++s) {
+        float p[V];
+        Vec<float, V>::load(part + int64_t(s) * n + i, p);
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] += p[e];
+    }
+#pragma unroll
+    for (int e = 0; e < V; ++e) v[e] *= factor;
+    Vec<T, V>::store(out + i, v);
+}
+
+template <class T, int V>
+void launch_join(const AttnArgs &a, int mode, int64_t rows, cudaStream_t st) {
+    const int64_t n = rows * a.D;
+    const unsigned g = unsigned((n / V + 255) / 256);
+    if (mode == ATTN_FWD)
+        attn_join_forward_kernel<T, V><<<g, 256, 0, st>>>(a);
+    else
+        attn_join_sum_kernel<T, V><<<dim3(g, mode == ATTN_DKV ? 2 : 1), 256, 0, st>>>(
+            a.part, a.nsplit, n, a.scale, static_cast<T *>(mode == ATTN_DKV ? a.dk : a.dq),
+            static_cast<T *>(a.dv));
 }
 
 // dslope_h = -sum over rows of (dS d2 - (dS) (P d2)), each row's sums joined
@@ -465,14 +490,26 @@ struct Scratch {
     cudaError_t take(size_t bytes) { return scratch_alloc(*dev, &p, bytes, st); }
 };
 
-// Parts of the streamed side: enough blocks for `want`, at least one tile of
-// the streamed side each, at most 1 GiB of partial accumulators.
-int pick_split(int64_t want, int64_t base, int64_t items, int64_t row_floats) {
-    int64_t n = (want + base - 1) / base;
-    if (n > items) n = items;
-    if (n > 256) n = 256;
-    while (n > 1 && n * row_floats > (int64_t(1) << 28)) --n;
-    return n < 1 ? 1 : int(n);
+// Parts of the streamed side.  A block takes about `start` us before its
+// first tile and `tile` us a tile; blocks run in waves of `slots`; parts have
+// to be joined, which takes another launch and moves every partial sum twice.
+// The number with the smallest estimate, at most 1 GiB of partial sums.
+// (Measured, one query over 100,000 keys, 8 heads of 64: 1 part 1029 us, 8
+// parts 144, 19 parts 72, 38 parts 90; 256 queries and keys, 8 clouds of 8
+// heads: 1 part 13 us, 2 parts 25.)
+int pick_split(int64_t slots, int64_t base, int64_t items, int64_t part_floats, float start,
+               float tile) {
+    int best = 1;
+    float least = INFINITY;
+    for (int64_t n = 1; n <= items && n <= 256; ++n) {
+        if (n > 1 && n * part_floats > (int64_t(1) << 28)) break;
+        const int64_t waves = (base * n + slots - 1) / slots, each = (items + n - 1) / n;
+        float t = float(waves) * (start + tile * float(each));
+        if (n > 1) t += 4.0f + float(n * part_floats) * (8.0f / 4e6f);
+        if (t < least) least = t, best = int(n);
+        if (n > 1 && base * (n - 1) > 4 * slots) break;  // more waves do not help
+    }
+    return best;
 }
 
 template <class T>
@@ -486,10 +523,15 @@ cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes
     const int64_t ntile = (LX + xr - 1) / xr, nyt = (LY + yr - 1) / yr;
     const int64_t base = ntile * NH * a.B;
     const int64_t rows = int64_t(a.B) * LX * NH, hrows = int64_t(a.B) * a.H * a.Lq;
-    // two blocks fit a SM, one of the tensor-core kernels
-    const int64_t want = int64_t(dev.sm_count) * (tc || parts ? 1 : 2);
-    a.nsplit = pick_split(want, base, dkv ? nyt * (a.H / a.Hkv) : nyt,
-                          rows * a.D * (dkv ? 2 : 1));
+    // Two blocks fit a SM, one of the tensor-core kernels.  Us a block takes to
+    // its first tile, and a tile (measured with all its rows in use).
+    const int64_t slots = int64_t(dev.sm_count) * (tc || parts ? 1 : 2);
+    const bool wide = a.D > 64, fwd = mode == ATTN_FWD;
+    const float tile = tc ? (wide ? 1.4f : 1.1f)
+                       : parts ? (fwd ? 1.7f : dkv ? 3.2f : 2.4f) * (wide ? 2.0f : 1.0f)
+                               : (wide ? 12.0f : 6.0f);
+    a.nsplit = pick_split(slots, base, dkv ? nyt * (a.H / a.Hkv) : nyt,
+                          rows * a.D * (dkv ? 2 : 1), 5.0f, tile);
     const bool slopes = mode == ATTN_DQ && a.slopes != nullptr && dslopes != nullptr;
     const size_t part = a.nsplit > 1 ? size_t(a.nsplit) * rows * a.D * (dkv ? 2 : 1) : 0;
     const size_t ml = a.nsplit > 1 && mode == ATTN_FWD ? size_t(a.nsplit) * 2 * hrows : 0;
@@ -512,16 +554,14 @@ cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes
                           : simt_pick<T, ATTN_DKV>(a, vec, blocks, st);
     if (e != cudaSuccess) return e;
     if (a.nsplit > 1) {
-        const int64_t n = rows * a.D;
-        const unsigned g = unsigned((n + 255) / 256);
-        if (mode == ATTN_FWD)
-            attn_join_forward_kernel<T><<<unsigned((rows + 7) / 8), 256, 0, st>>>(a);
+        const bool v4 = a.D % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 &&
+                        reinterpret_cast<uintptr_t>(a.dq) % 16 == 0 &&
+                        reinterpret_cast<uintptr_t>(a.dk) % 16 == 0 &&
+                        reinterpret_cast<uintptr_t>(a.dv) % 16 == 0;
+        if (v4)
+            launch_join<T, 4>(a, mode, rows, st);
         else
-            attn_join_sum_kernel<T><<<g, 256, 0, st>>>(
-                a.part, a.nsplit, n, a.scale, static_cast<T *>(dkv ? a.dk : a.dq));
-        if (dkv)
-            attn_join_sum_kernel<T><<<g, 256, 0, st>>>(a.part + int64_t(a.nsplit) * n, a.nsplit,
-                                                       n, 1.0f, static_cast<T *>(a.dv));
+            launch_join<T, 1>(a, mode, rows, st);
     }
     if (slopes) attn_slope_kernel<<<a.H, 1024, 0, st>>>(a, dslopes);
     return cudaGetLastError();

@@ -305,7 +305,11 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
                 }
         }
         // Rows of a tile past the length are overwritten with zeros once the tile
-        // is there: two tiles later, so that copies stay ahead.
+        // is there: LAG tiles later, so that copies stay ahead.  A tile's stage is
+        // free only after the next tile's scores (which wait for its zeros) were
+        // issued, so the zeros of tile k - STAGES + 1 come before the wait for the
+        // stage of tile k: LAG <= STAGES - 2.
+        constexpr int LAG = STAGES > 3 ? 2 : STAGES - 2;
         TileWalk late = walk(0);
         auto fix = [&](int k) {
             const int valid = ny - late.y, s = k % STAGES;
@@ -343,10 +347,10 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
                 }
             }
             issued = k + 1;
-            if (k >= 2) ok = fix(k - 2);
+            if (k >= LAG) ok = fix(k - LAG);
         }
         if (issued == n)
-            for (int k = max(0, n - 2); ok && k < n; ++k) ok = fix(k);
+            for (int k = max(0, n - LAG); ok && k < n; ++k) ok = fix(k);
         // nothing is in flight when the block ends
         if (!C::X_TMEM && n > 0) mbar_wait_bounded(xfull, 0, a.timeout_ns);
         for (int k = max(0, issued - STAGES); k < issued; ++k)

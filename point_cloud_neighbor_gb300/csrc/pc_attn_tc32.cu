@@ -232,7 +232,8 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
         int issued = 0;
         bool ok = true;
         TileWalk at = walk(0);
-        constexpr int LAG = STAGES > 2 ? 2 : STAGES - 1;
+        // (as in pc_attn_tc.cu; one score buffer does not look a tile ahead)
+        constexpr int LAG = C::NB == 1 ? STAGES - 1 : STAGES > 3 ? 2 : STAGES - 2;
         for (int k = 0; ok && k < n; ++k, at.next()) {
             const int s = k % STAGES;
             if (k >= STAGES && !wait(&empty[s], unsigned((k / STAGES - 1) & 1))) break;

@@ -360,6 +360,31 @@ def test_attention(B, Lq, Lk, H, Hkv, D, ql, rl, bias, dtype):
     check_attention(q, k, v, do, kw, dtype)
 
 
+# Many clouds and heads: blocks walk over several tiles and heads each, most of them
+# with a ragged end (the keys' gradient over the query heads of a group too).
+MANY = [
+    (12, 333, 333, 16, 8, [333, 300, 257, 256, 255, 193, 129, 128, 65, 64, 1, 0],
+     [333, 1, 64, 65, 128, 129, 193, 255, 256, 257, 300, 333]),
+    (16, 90, 400, 12, 6, list(range(90, 10, -5)), list(range(400, 0, -25))),
+    (40, 70, 70, 24, 4, [70 - i for i in range(40)], [31 + i for i in range(40)]),
+]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,ql,rl", MANY)
+def test_attention_many_ragged_clouds(B, Lq, Lk, H, Hkv, ql, rl, bias, D, dtype):
+    q, k, v, do, kw = attn_inputs(B, Lq, Lk, H, Hkv, D, dtype, bias, ql, rl)
+    for t in (q, do):
+        for b in range(B):
+            t[b, ql[b]:] = math.nan
+    for t in (k, v):
+        for b in range(B):
+            t[b, rl[b]:] = math.nan
+    check_attention(q, k, v, do, kw, dtype)
+
+
 @pytest.mark.parametrize("dtype", DTYPES)
 def test_attention_scale_and_large_scores(dtype):
     # scores of several hundreds: the running maximum has to carry them
