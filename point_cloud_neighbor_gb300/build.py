@@ -28,7 +28,7 @@ LIB = os.path.join(BUILD, "libpointcloud.so")
 SOURCES = ["pc_api.cu", "pc_fps.cu", "pc_knn.cu", "pc_ball_query.cu",
            "pc_fps_static.cu", "pc_grid.cu", "pc_chamfer.cu", "pc_interp.cu",
            "pc_knn_d.cu", "pc_layer_norm.cu", "pc_rotary.cu", "pc_attn.cu",
-           "pc_attn_tc.cu", "pc_attn_tc32.cu"]
+           "pc_attn_tc.cu", "pc_attn_tc32.cu", "pc_attn_few.cu"]
 HEADERS = ["pc_device.cuh", "pc_tiles.cuh", "pc_filter.cuh", "pc_stream.cuh",
            "pc_internal.h", "pc_vec.cuh", "pc_attn.cuh", "pc_tcgen05.cuh",
            "pc_attn_tc.cuh"]

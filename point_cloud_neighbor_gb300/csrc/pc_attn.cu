@@ -410,6 +410,67 @@ attn_join_sum_kernel(const float *part, int nsplit, int64_t n, float factor, T *
     Vec<T, V>::store(out + i, v);
 }
 
+// Few rows and many parts: a block per row of the output (forward, or dq), the
+// parts over its threads.  The row's sums for the slopes' gradient are joined
+// too and left as those of part 0.
+template <class T, bool FWD>
+__global__ void __launch_bounds__(256) attn_join_rows_kernel(const AttnArgs a) {
+    __shared__ float wt[256], red[32], part[256];
+    const int64_t rows = int64_t(a.B) * a.Lq * a.H, row = blockIdx.x;
+    const int64_t tok = row / a.H, b = tok / a.Lq;
+    const int i = int(tok - b * a.Lq), t = threadIdx.x;
+    const int64_t hrow = (b * a.H + (row - tok * a.H)) * a.Lq + i;
+    // the sum or the maximum over the block, in a fixed order
+    auto over = [&](float v, bool most) {
+        for (int o = 16; o > 0; o >>= 1) {
+            const float u = __shfl_xor_sync(0xffffffffu, v, o);
+            v = most ? fmaxf(v, u) : v + u;
+        }
+        __syncthreads();
+        if (t % 32 == 0) red[t / 32] = v;
+        __syncthreads();
+        v = red[0];
+        for (int k = 1; k < 8; ++k) v = most ? fmaxf(v, red[k]) : v + red[k];
+        return v;
+    };
+    const bool mine = t < a.nsplit;  // at most 256 parts
+    float f = FWD ? 0.0f : a.scale;
+    if (FWD) {
+        const float *ml = a.part_ml + int64_t(t) * 2 * rows + hrow;
+        const float mt = mine ? ml[0] : -INFINITY;
+        const float m = over(mt, true), base = m == -INFINITY ? 0.0f : m;
+        const float w = mine ? exp2f(mt - base) : 0.0f;
+        wt[t] = w;
+        const float l = over(mine ? w * ml[rows] : 0.0f, false);
+        const bool any = i < attn_len(a.qlen, int(b), a.Lq) && l > 0.0f;
+        if (any) f = 1.0f / l;
+        if (t == 0 && a.lse != nullptr)
+            a.lse[hrow] = any ? (m + log2f(l)) * ATTN_LN2 : -INFINITY;
+    } else if (a.rowsum != nullptr) {
+        for (int e = 0; e < 3; ++e) {
+            const float v = over(mine ? a.rowsum[(int64_t(t) * 3 + e) * rows + hrow] : 0.0f, false);
+            if (t == 0) a.rowsum[e * rows + hrow] = v;
+        }
+    }
+    __syncthreads();
+    // C channels at a time, 256 / C threads for each
+    const int C = a.D > 64 ? 128 : a.D > 32 ? 64 : 32, K = 256 / C, k = t / C, c = t % C;
+    float v = 0.0f;
+    if (c < a.D)
+#pragma unroll 8
+        for (int s = k; s < a.nsplit; s += K) {
+            const float p = a.part[(int64_t(s) * rows + row) * a.D + c];
+            v = FWD ? fmaf(p, wt[s], v) : v + p;
+        }
+    part[t] = v;
+    __syncthreads();
+    if (k == 0 && c < a.D) {
+        for (int u = 1; u < K; ++u) v += part[u * C + c];
+        v = f == 0.0f ? 0.0f : v * f;
+        Vec<T, 1>::store(static_cast<T *>(FWD ? a.out : a.dq) + row * a.D + c, &v);
+    }
+}
+
 template <class T, int V>
 void launch_join(const AttnArgs &a, int mode, int64_t rows, cudaStream_t st) {
     const int64_t n = rows * a.D;
@@ -516,6 +577,7 @@ template <class T>
 cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes,
                      const AttnSplit *parts, cudaStream_t st) {
     const bool dkv = mode == ATTN_DKV;
+    const bool few = !dkv && attn_few_fits(a, sizeof(T), mode == ATTN_DQ);
     const int64_t LX = dkv ? a.Lk : a.Lq, LY = dkv ? a.Lq : a.Lk, NH = dkv ? a.Hkv : a.H;
     const bool tc = sizeof(T) == 2 && attn_tc_fits(a, mode);
     const int64_t xr = tc ? attn_tc_rows(mode) : parts ? attn_tc32_rows(a, mode) : SB;
@@ -530,8 +592,9 @@ cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes
     const float tile = tc ? (wide ? 1.4f : 1.1f)
                        : parts ? (fwd ? 1.7f : dkv ? 3.2f : 2.4f) * (wide ? 2.0f : 1.0f)
                                : (wide ? 12.0f : 6.0f);
-    a.nsplit = pick_split(slots, base, dkv ? nyt * (a.H / a.Hkv) : nyt,
-                          rows * a.D * (dkv ? 2 : 1), 5.0f, tile);
+    a.nsplit = few ? attn_few_parts(dev, a, sizeof(T), mode == ATTN_DQ)
+                   : pick_split(slots, base, dkv ? nyt * (a.H / a.Hkv) : nyt,
+                                rows * a.D * (dkv ? 2 : 1), 5.0f, tile);
     const bool slopes = mode == ATTN_DQ && a.slopes != nullptr && dslopes != nullptr;
     const size_t part = a.nsplit > 1 ? size_t(a.nsplit) * rows * a.D * (dkv ? 2 : 1) : 0;
     const size_t ml = a.nsplit > 1 && mode == ATTN_FWD ? size_t(a.nsplit) * 2 * hrows : 0;
@@ -547,7 +610,8 @@ cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes
     const bool vec = strides_fit(a, 4, 4 * sizeof(T));
     const int64_t blocks = base * a.nsplit;
     if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    e = tc                 ? launch_attn_tc(a, mode, blocks, st)
+    e = few                ? launch_attn_few(a, sizeof(T), mode == ATTN_DQ, st)
+        : tc               ? launch_attn_tc(a, mode, blocks, st)
         : parts            ? launch_attn_tc32(a, *parts, mode, blocks, st)
         : mode == ATTN_FWD ? simt_pick<T, ATTN_FWD>(a, vec, blocks, st)
         : mode == ATTN_DQ ? simt_pick<T, ATTN_DQ>(a, vec, blocks, st)
@@ -558,7 +622,14 @@ cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes
                         reinterpret_cast<uintptr_t>(a.dq) % 16 == 0 &&
                         reinterpret_cast<uintptr_t>(a.dk) % 16 == 0 &&
                         reinterpret_cast<uintptr_t>(a.dv) % 16 == 0;
-        if (v4)
+        // (8 rows of 64 in 152 parts: 27 us a thread per 4 channels, 4 us a block per row)
+        if (!dkv && a.nsplit >= 8 && rows <= 4096) {
+            if (mode == ATTN_FWD)
+                attn_join_rows_kernel<T, true><<<unsigned(rows), 256, 0, st>>>(a);
+            else
+                attn_join_rows_kernel<T, false><<<unsigned(rows), 256, 0, st>>>(a);
+            a.nsplit = 1;  // for the slopes' sums
+        } else if (v4)
             launch_join<T, 4>(a, mode, rows, st);
         else
             launch_join<T, 1>(a, mode, rows, st);
@@ -575,7 +646,8 @@ bool in_parts(const AttnArgs &a) {
 
 template <class T>
 cudaError_t run_forward(const DeviceInfo &dev, const AttnArgs &a, cudaStream_t st) {
-    if (!in_parts<T>(a)) return run_pass<T>(dev, a, ATTN_FWD, nullptr, nullptr, st);
+    if (!in_parts<T>(a) || attn_few_fits(a, sizeof(T), false))
+        return run_pass<T>(dev, a, ATTN_FWD, nullptr, nullptr, st);
     Scratch ws{&dev, st};
     AttnSplit s;
     cudaError_t e = ws.take(attn_split_bytes(a, false));
@@ -587,7 +659,8 @@ template <class T>
 cudaError_t run_backward(const DeviceInfo &dev, AttnArgs a, const void *out, float *dslopes,
                          cudaStream_t st) {
     const int64_t rows = int64_t(a.B) * a.Lq * a.H;
-    const bool parts = in_parts<T>(a);
+    const bool few = attn_few_fits(a, sizeof(T), true);  // one launch for all gradients
+    const bool parts = !few && in_parts<T>(a);
     const size_t sides = (size_t(rows) * 2 * sizeof(float) + 255) / 256 * 256;
     Scratch ws{&dev, st};
     cudaError_t e = ws.take(sides + (parts ? attn_split_bytes(a, true) : 1));
@@ -608,7 +681,7 @@ cudaError_t run_backward(const DeviceInfo &dev, AttnArgs a, const void *out, flo
     } else if (dslopes != nullptr && a.slopes != nullptr) {
         if ((e = cudaMemsetAsync(dslopes, 0, size_t(a.H) * 4, st)) != cudaSuccess) return e;
     }
-    if (int64_t(a.B) * a.Lk * a.Hkv > 0) e = run_pass<T>(dev, a, ATTN_DKV, nullptr, s, st);
+    if (!few && int64_t(a.B) * a.Lk * a.Hkv > 0) e = run_pass<T>(dev, a, ATTN_DKV, nullptr, s, st);
     return e;
 }
 

@@ -66,6 +66,12 @@ constexpr int ATTN_TC_TILE = 64;
 bool attn_tc_fits(const AttnArgs &a, int mode);
 cudaError_t launch_attn_tc(const AttnArgs &a, int mode, int64_t blocks, cudaStream_t st);
 
+// Few queries per key head (pc_attn_few.cu); backward, one launch writes dk and
+// dv and the parts of dq.  nsplit comes from attn_few_parts.
+bool attn_few_fits(const AttnArgs &a, size_t elem, bool backward);
+int attn_few_parts(const DeviceInfo &dev, const AttnArgs &a, size_t elem, bool backward);
+cudaError_t launch_attn_few(const AttnArgs &a, size_t elem, bool backward, cudaStream_t st);
+
 // float32 on the tensor cores (pc_attn_tc32.cu): the arrays as three
 // bfloat16 parts [3][B, L, heads, Dp] each, written into `space` once a call.
 struct AttnSplit {
