@@ -487,13 +487,18 @@ void launch_join(const AttnArgs &a, int mode, int64_t rows, cudaStream_t st) {
 // over the parts first: a block per head, float64, a fixed order.  A row's
 // exact dS sum to 0; what they sum to here is the error of delta (from an
 // output rounded to its type), and the second term takes its effect out.
+// With `tiles` the sums are already one number for each tile of a head's rows.
 __global__ void __launch_bounds__(1024)
-attn_slope_kernel(const AttnArgs a, float *dslopes) {
+attn_slope_kernel(const AttnArgs a, int tiles, float *dslopes) {
     __shared__ double red[32];
     const int h = blockIdx.x;
     const int64_t n = int64_t(a.B) * a.H * a.Lq;
     double t = 0.0;
-    for (int64_t r = threadIdx.x; r < int64_t(a.B) * a.Lq; r += 1024) {
+    if (tiles > 0)
+        for (int64_t r = threadIdx.x; r < int64_t(a.B) * tiles; r += 1024)
+            t += double(a.rowsum[(r / tiles * a.H + h) * tiles + r % tiles]);
+    else
+      for (int64_t r = threadIdx.x; r < int64_t(a.B) * a.Lq; r += 1024) {
         const int64_t b = r / a.Lq, at = (b * a.H + h) * a.Lq + (r - b * a.Lq);
         float wa = 0.0f, we = 0.0f, wd = 0.0f;
         for (int s = 0; s < a.nsplit; ++s) {
@@ -595,10 +600,11 @@ cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes
     a.nsplit = few ? attn_few_parts(dev, a, sizeof(T), mode == ATTN_DQ)
                    : pick_split(slots, base, dkv ? nyt * (a.H / a.Hkv) : nyt,
                                 rows * a.D * (dkv ? 2 : 1), 5.0f, tile);
+    const bool one_part = a.nsplit == 1;
     const bool slopes = mode == ATTN_DQ && a.slopes != nullptr && dslopes != nullptr;
     const size_t part = a.nsplit > 1 ? size_t(a.nsplit) * rows * a.D * (dkv ? 2 : 1) : 0;
     const size_t ml = a.nsplit > 1 && mode == ATTN_FWD ? size_t(a.nsplit) * 2 * hrows : 0;
-    const size_t rs = slopes ? size_t(a.nsplit) * 3 * hrows : 0;
+    const size_t rs = slopes ? size_t(a.nsplit) * 3 * hrows + size_t(base) : 0;
     Scratch ws{&dev, st};
     cudaError_t e = cudaSuccess;
     if (part + ml + rs > 0) {
@@ -634,7 +640,9 @@ cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes
         else
             launch_join<T, 1>(a, mode, rows, st);
     }
-    if (slopes) attn_slope_kernel<<<a.H, 1024, 0, st>>>(a, dslopes);
+    if (slopes)
+        attn_slope_kernel<<<a.H, 1024, 0, st>>>(
+            a, !few && (tc || parts) && one_part ? int(ntile) : 0, dslopes);
     return cudaGetLastError();
 }
 

@@ -55,16 +55,17 @@ struct AttnMaps {
 
 template <int MODE, int DP>
 struct Cfg {
-    static constexpr bool BWD = MODE != ATTN_FWD;
+    static constexpr bool BWD = MODE != ATTN_FWD, FWD_ = !BWD;
     static constexpr int T = BWD ? 1 : 2;       // row tiles of the block
     static constexpr int CWARPS = 16;           // two units of two halves of four warps
     static constexpr int THREADS = 32 * (CWARPS + 4);
     static constexpr int STAGES = DP == 64 ? 6 : 3;
     // The weights as a sum of two bfloat16.
     static constexpr bool TWO_P = MODE != ATTN_DQ, TWO_S = false;
-    // tensor memory columns: score buffers (FWD two a unit, else one of S and
-    // dP), then the accumulators
-    static constexpr int NBUF = BWD ? 2 : 4, BUF = BWD ? 2 * YR : YR;
+    // Tensor memory columns: score buffers (FWD two a unit; else of S and dP, one
+    // a unit, and for up to 64 channels a third, so that the scores of a unit's
+    // next tile are there before its weights are used up), then the accumulators.
+    static constexpr int NBUF = FWD_ ? 4 : DP == 64 ? 3 : 2, BUF = BWD ? 2 * YR : YR;
     static constexpr int ACC = NBUF * BUF;
     static constexpr int NACC = MODE == ATTN_DQ ? 1 : 2;  // FWD: one a unit
     // The rows kept, where tensor memory has room for them: a product that reads
@@ -80,7 +81,7 @@ struct Cfg {
     static constexpr int STAGE = 2 * YBYTES + YAUG;
     // per stage: x, y, z, -lse, -delta of the streamed rows; flag, bias factor
     static constexpr int COLF = 5 * YR + 4;
-    static constexpr int ROWF = 2 * 6 * XR;     // per unit: exchanged row values
+    static constexpr int ROWF = 2 * 6 * XR + 4;  // per unit: exchanged row values
     static constexpr size_t XSMEM = X_TMEM ? 0 : size_t(XT) * XBYTES;
     static constexpr size_t SMEM = 1024 + XSMEM + size_t(T) * XAUG +
                                    size_t(STAGES) * (STAGE + COLF * 4) + ROWF * 4 + 512;
@@ -306,10 +307,13 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         }
         // Rows of a tile past the length are overwritten with zeros once the tile
         // is there: LAG tiles later, so that copies stay ahead.  A tile's stage is
-        // free only after the next tile's scores (which wait for its zeros) were
-        // issued, so the zeros of tile k - STAGES + 1 come before the wait for the
-        // stage of tile k: LAG <= STAGES - 2.
-        constexpr int LAG = STAGES > 3 ? 2 : STAGES - 2;
+        // free only after the scores of the next tiles (NBUF - 1 of them, FWD one),
+        // which wait for their zeros, were issued: those zeros come before the
+        // wait for the stage that the next copy goes to.
+        constexpr int LAG = STAGES - 1 - (FWD ? 1 : C::NBUF - 1) < 2
+                                ? STAGES - 1 - (FWD ? 1 : C::NBUF - 1)
+                                : 2;
+        static_assert(LAG >= 0, "more stages than score buffers");
         TileWalk late = walk(0);
         auto fix = [&](int k) {
             const int valid = ny - late.y, s = k % STAGES;
@@ -571,21 +575,25 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
                     in.next();
                 }
             } else {
-                for (int k = 0; ok && k < 2 && k < n; ++k)
+                constexpr int AHEAD = C::NBUF;
+                for (int k = 0; ok && k < AHEAD && k < n; ++k)
                     if ((ok = tile_ready())) {
-                        scores(0, k & 1);
+                        scores(0, k);
                         in.next();
                     }
+                int buf = 0;
+                unsigned parity = 0;
                 for (int k = 0; ok && k < n; ++k) {
-                    if (!(ok = await(&pfull[k & 1], unsigned(k >> 1) & 1))) break;
+                    if (!(ok = await(&pfull[buf], parity))) break;
                     tc_fence_after();
-                    accumulate(0, k & 1, k == 0);
+                    accumulate(0, buf, k == 0);
                     mma_commit(&empty[out.s]);
                     out.next();
-                    if (k + 2 < n && (ok = tile_ready())) {
-                        scores(0, k & 1);
+                    if (k + AHEAD < n && (ok = tile_ready())) {
+                        scores(0, buf);
                         in.next();
                     }
+                    if (++buf == AHEAD) buf = 0, parity ^= 1;
                 }
             }
             mma_commit(accfull);
@@ -612,13 +620,16 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         float2 wa = l2, we = l2, wd = l2;            // DQ: the slope's sums
         float *rd = rowdata + unit * 6 * XR + quad * 32 + lane;
         bool ok = true;
-        int s = FWD ? 0 : unit;
-        unsigned phase = 0;
+        int s = FWD ? 0 : unit, sbuf = unit;  // stage; BWD: score buffer
+        unsigned phase = 0, sphase = 0;
         TileWalk at = walk(FWD ? 0 : unit);
         for (int k = FWD ? 0 : unit; k < n; k += FWD ? 1 : 2, s += FWD ? 1 : 2) {
             if (s >= STAGES) s -= STAGES, phase ^= 1;
-            const int buf = FWD ? 2 * unit + (k & 1) : unit;
-            if (unit_live && !(ok = wait(&sfull[buf], unsigned((k >> 1) & 1)))) break;
+            if (BWD && sbuf >= C::NBUF) sbuf -= C::NBUF, sphase ^= 1;
+            const int buf = FWD ? 2 * unit + (k & 1) : sbuf;
+            if (unit_live && !(ok = wait(&sfull[buf], FWD ? unsigned((k >> 1) & 1) : sphase)))
+                break;
+            sbuf += 2;
             if (COLS && !(ok = wait(&full[s], phase))) break;
             tc_fence_after();
             const float *cd = coldata + s * C::COLF + 32 * half;
@@ -790,14 +801,14 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
                 rd[(half * 3 + 2) * XR] = wd.x + wd.y;
             }
             named_barrier_sync(1, C::CWARPS * 32);
-            if (sums && unit == 0 && half == 0 && row < LX) {
-                float *o = a.rowsum + split * 3 * hrows + hrow;
+            if (sums && unit == 0 && half == 0) {
+                float t[3];
 #pragma unroll
                 for (int e = 0; e < 3; ++e) {
-                    const float t = (rd[e * XR] + rd[(3 + e) * XR]) +
-                                    (rd[(6 + e) * XR] + rd[(9 + e) * XR]);
-                    o[e * hrows] = row < nx ? t : 0.0f;
+                    t[e] = (rd[e * XR] + rd[(3 + e) * XR]) + (rd[(6 + e) * XR] + rd[(9 + e) * XR]);
+                    if (row >= nx) t[e] = 0.0f;
                 }
+                put_slope_sums(a, t, split, hrow, row < LX, quad, lane, rowdata + 12 * XR);
             }
         }
         float l = l2.x + l2.y;

@@ -47,6 +47,28 @@ __device__ __forceinline__ void dist4(const float *cd, int c, float2 nx, float2 
     d0 = __ffma2_rn(a, a, d0), d1 = __ffma2_rn(b, b, d1);
 }
 
+// The slopes' sums of a block's 128 rows, a thread each in four warps: with one
+// part the rows' values are complete and added up here, one number a block
+// (`red`: 4 floats); else the rows' three sums go to their part.
+__device__ __forceinline__ void put_slope_sums(const AttnArgs &a, const float (&t)[3], int split,
+                                               int64_t hrow, bool in, int quad, int lane,
+                                               float *red) {
+    if (a.nsplit > 1) {
+        const int64_t n = int64_t(a.B) * a.H * a.Lq;
+        if (in) {
+            float *o = a.rowsum + split * 3 * n + hrow;
+            o[0] = t[0], o[n] = t[1], o[2 * n] = t[2];
+        }
+        return;
+    }
+    float v = fmaf(-t[2], t[1], t[0]);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    if (lane == 0) red[quad] = v;
+    named_barrier_sync(2, 128);
+    if (quad == 0 && lane == 0) a.rowsum[blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
+}
+
 // The head and first row of a block's tiles, one after the other: `heads`
 // query heads of `end` rows each (DKV), else one head.
 struct TileWalk {

@@ -52,7 +52,7 @@ struct Cfg32 {
     static constexpr size_t XSMEM = X_TMEM ? 0 : 6 * XP;
     static constexpr int STAGE = 6 * YP;
     static constexpr int COLF = 5 * YR + 4;
-    static constexpr int ROWF = 6 * XR;
+    static constexpr int ROWF = 6 * XR + 4;
     static constexpr size_t SMEM =
         1024 + XSMEM + size_t(STAGES) * (STAGE + COLF * 4) + ROWF * 4 + 512;
     static_assert(SMEM <= 227 * 1024, "shared memory");
@@ -587,11 +587,11 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
                 rd[2 * XR] = wd.x + wd.y;
             }
             named_barrier_sync(1, C::CWARPS * 32);
-            if (sums && half == 0 && row < LX) {
-                float *o = a.rowsum + split * 3 * hrows + hrow;
-                o[0] = row < nx ? (wa.x + wa.y) + rd[0] : 0.0f;
-                o[hrows] = row < nx ? (we.x + we.y) + rd[XR] : 0.0f;
-                o[2 * hrows] = row < nx ? (wd.x + wd.y) + rd[2 * XR] : 0.0f;
+            if (sums && half == 0) {
+                float t[3] = {(wa.x + wa.y) + rd[0], (we.x + we.y) + rd[XR],
+                              (wd.x + wd.y) + rd[2 * XR]};
+                if (row >= nx) t[0] = t[1] = t[2] = 0.0f;
+                put_slope_sums(a, t, split, hrow, row < LX, quad, lane, rowdata + 6 * XR);
             }
         }
         if (FWD) {  // the row's sum over both halves
