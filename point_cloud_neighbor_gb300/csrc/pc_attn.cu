@@ -327,29 +327,48 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
 }
 
 // delta_i = out_i . dout_i, and lse in base-2 units with +inf for rows without
-// keys (their weights 2^(z - lse2) are then 0): a warp per (token, head).
-template <class T>
+// keys (their weights 2^(z - lse2) are then 0): LPR lanes per (token, head), V
+// channels at a time.  (16 x 1024 tokens, 8 heads of 64 in bfloat16: a warp per
+// row and one channel a load 32 us, 8 lanes per row 5 us.)
+template <class T, int V, int LPR>
 __global__ void __launch_bounds__(256)
 attn_delta_kernel(const T *out, const T *go, const float *lse, int64_t rows, int Lq, int H,
                   int D, float *delta, float *lse2) {
-    const int64_t row = int64_t(blockIdx.x) * 8 + threadIdx.x / 32;  // (b Lq + i) H + h
-    if (row >= rows) return;
-    const int lane = threadIdx.x % 32;
+    const int64_t row = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LPR;  // (b Lq + i) H + h
+    const int lane = threadIdx.x % LPR;
     float s = 0.0f;
-    for (int c = lane; c < D; c += 32) {
-        float o, g;
-        Vec<T, 1>::load(out + row * D + c, &o);
-        Vec<T, 1>::load(go + row * D + c, &g);
-        s = fmaf(o, g, s);
-    }
+    if (row < rows)
+        for (int c = lane * V; c < D; c += LPR * V) {
+            float o[V], g[V];
+            Vec<T, V>::load(out + row * D + c, o);
+            Vec<T, V>::load(go + row * D + c, g);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const int64_t tok = row / H, b = tok / Lq;
-    if (lane == 0) {
+            for (int e = 0; e < V; ++e) s = fmaf(o[e], g[e], s);
+        }
+#pragma unroll
+    for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    if (row < rows && lane == 0) {
+        const int64_t tok = row / H, b = tok / Lq;
         const int64_t at = (b * H + row % H) * Lq + (tok - b * Lq);
         delta[at] = s;
         lse2[at] = lse[at] == -INFINITY ? INFINITY : lse[at] * ATTN_LOG2E;
     }
+}
+
+template <class T>
+void launch_delta(const AttnArgs &a, const T *out, int64_t rows, float *delta, float *lse2,
+                  cudaStream_t st) {
+    const T *go = static_cast<const T *>(a.go);
+    constexpr int W = 16 / sizeof(T);
+    const bool wide = a.D % W == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
+                      reinterpret_cast<uintptr_t>(go) % 16 == 0;
+    const unsigned g8 = unsigned((rows * 8 + 255) / 256), g32 = unsigned((rows * 32 + 255) / 256);
+    if (wide)
+        attn_delta_kernel<T, W, 8><<<g8, 256, 0, st>>>(out, go, a.lse, rows, a.Lq, a.H, a.D,
+                                                       delta, lse2);
+    else
+        attn_delta_kernel<T, 1, 32><<<g32, 256, 0, st>>>(out, go, a.lse, rows, a.Lq, a.H, a.D,
+                                                         delta, lse2);
 }
 
 // Joins the parts of a split forward pass: a thread per V channels of a row.
@@ -414,8 +433,8 @@ attn_join_sum_kernel(const float *part, int nsplit, int64_t n, float factor, T *
 // parts over its threads.  The row's sums for the slopes' gradient are joined
 // too and left as those of part 0.
 template <class T, bool FWD>
-__global__ void __launch_bounds__(256) attn_join_rows_kernel(const AttnArgs a) {
-    __shared__ float wt[256], red[32], part[256];
+__global__ void __launch_bounds__(1024) attn_join_rows_kernel(const AttnArgs a) {
+    __shared__ float wt[256], red[32], part[1024];
     const int64_t rows = int64_t(a.B) * a.Lq * a.H, row = blockIdx.x;
     const int64_t tok = row / a.H, b = tok / a.Lq;
     const int i = int(tok - b * a.Lq), t = threadIdx.x;
@@ -430,7 +449,7 @@ __global__ void __launch_bounds__(256) attn_join_rows_kernel(const AttnArgs a) {
         if (t % 32 == 0) red[t / 32] = v;
         __syncthreads();
         v = red[0];
-        for (int k = 1; k < 8; ++k) v = most ? fmaxf(v, red[k]) : v + red[k];
+        for (int k = 1; k < 32; ++k) v = most ? fmaxf(v, red[k]) : v + red[k];
         return v;
     };
     const bool mine = t < a.nsplit;  // at most 256 parts
@@ -440,7 +459,7 @@ __global__ void __launch_bounds__(256) attn_join_rows_kernel(const AttnArgs a) {
         const float mt = mine ? ml[0] : -INFINITY;
         const float m = over(mt, true), base = m == -INFINITY ? 0.0f : m;
         const float w = mine ? exp2f(mt - base) : 0.0f;
-        wt[t] = w;
+        if (t < 256) wt[t] = w;
         const float l = over(mine ? w * ml[rows] : 0.0f, false);
         const bool any = i < attn_len(a.qlen, int(b), a.Lq) && l > 0.0f;
         if (any) f = 1.0f / l;
@@ -453,8 +472,8 @@ __global__ void __launch_bounds__(256) attn_join_rows_kernel(const AttnArgs a) {
         }
     }
     __syncthreads();
-    // C channels at a time, 256 / C threads for each
-    const int C = a.D > 64 ? 128 : a.D > 32 ? 64 : 32, K = 256 / C, k = t / C, c = t % C;
+    // C channels at a time, 1024 / C threads for each
+    const int C = a.D > 64 ? 128 : a.D > 32 ? 64 : 32, K = 1024 / C, k = t / C, c = t % C;
     float v = 0.0f;
     if (c < a.D)
 #pragma unroll 8
@@ -631,9 +650,9 @@ cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes
         // (8 rows of 64 in 152 parts: 27 us a thread per 4 channels, 4 us a block per row)
         if (!dkv && a.nsplit >= 8 && rows <= 4096) {
             if (mode == ATTN_FWD)
-                attn_join_rows_kernel<T, true><<<unsigned(rows), 256, 0, st>>>(a);
+                attn_join_rows_kernel<T, true><<<unsigned(rows), 1024, 0, st>>>(a);
             else
-                attn_join_rows_kernel<T, false><<<unsigned(rows), 256, 0, st>>>(a);
+                attn_join_rows_kernel<T, false><<<unsigned(rows), 1024, 0, st>>>(a);
             a.nsplit = 1;  // for the slopes' sums
         } else if (v4)
             launch_join<T, 4>(a, mode, rows, st);
@@ -682,9 +701,7 @@ cudaError_t run_backward(const DeviceInfo &dev, AttnArgs a, const void *out, flo
         s = &sp;
     }
     if (rows > 0) {
-        attn_delta_kernel<T><<<unsigned((rows + 7) / 8), 256, 0, st>>>(
-            static_cast<const T *>(out), static_cast<const T *>(a.go), a.lse, rows, a.Lq, a.H,
-            a.D, delta, lse2);
+        launch_delta<T>(a, static_cast<const T *>(out), rows, delta, lse2, st);
         if ((e = run_pass<T>(dev, a, ATTN_DQ, dslopes, s, st)) != cudaSuccess) return e;
     } else if (dslopes != nullptr && a.slopes != nullptr) {
         if ((e = cudaMemsetAsync(dslopes, 0, size_t(a.H) * 4, st)) != cudaSuccess) return e;

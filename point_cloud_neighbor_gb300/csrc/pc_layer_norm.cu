@@ -33,7 +33,8 @@
 namespace pcn {
 namespace {
 
-constexpr int LN_THREADS = 256;
+// Threads of a block: small blocks fill the registers of a SM better.
+__host__ __device__ constexpr int ln_threads(int tpr) { return tpr > 128 ? tpr : 128; }
 constexpr int LN_MAX_C = 8192;
 
 struct LnArgs {
@@ -116,9 +117,9 @@ __device__ __forceinline__ void load_param(const void *p, int col, int C, float 
 // row; vector i has the columns V (t + i TPR) - shift and on.  The next row is
 // on its way while one is worked on.
 template <class T, class WT, int V, int N, int TPR>
-__global__ void __launch_bounds__(LN_THREADS) ln_forward_kernel(const LnArgs a) {
-    __shared__ float red[LN_THREADS / 32];
-    constexpr int RPB = LN_THREADS / TPR;
+__global__ void __launch_bounds__(ln_threads(TPR)) ln_forward_kernel(const LnArgs a) {
+    constexpr int THREADS = ln_threads(TPR), RPB = THREADS / TPR;
+    __shared__ float red[THREADS / 32];
     const int t = threadIdx.x % TPR;
     const int64_t step = int64_t(gridDim.x) * RPB, total = a.rows * a.C;
     int64_t row = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR;
@@ -181,10 +182,10 @@ __global__ void __launch_bounds__(LN_THREADS) ln_forward_kernel(const LnArgs a) 
 }
 
 template <class T, class WT, int V, int N, int TPR>
-__global__ void __launch_bounds__(LN_THREADS) ln_backward_kernel(const LnArgs a) {
-    __shared__ float red[LN_THREADS / 32];
-    extern __shared__ float colsum[];  // [2][C], TPR < 256 only
-    constexpr int RPB = LN_THREADS / TPR;
+__global__ void __launch_bounds__(ln_threads(TPR)) ln_backward_kernel(const LnArgs a) {
+    constexpr int THREADS = ln_threads(TPR), RPB = THREADS / TPR;
+    __shared__ float red[THREADS / 32];
+    extern __shared__ float colsum[];  // [2][C], several rows a block only
     const int t = threadIdx.x % TPR;
     const int64_t step = int64_t(gridDim.x) * RPB, total = a.rows * a.C;
     int64_t row = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR;
@@ -253,7 +254,7 @@ __global__ void __launch_bounds__(LN_THREADS) ln_backward_kernel(const LnArgs a)
     }
     if (a.part == nullptr) return;
     float *part = a.part + size_t(blockIdx.x) * 2 * a.C;
-    if (TPR < LN_THREADS) {
+    if (RPB > 1) {
         // join the block's groups, one after the other
         for (int g = 0; g < RPB; ++g) {
             if (int(threadIdx.x / TPR) == g)
@@ -269,7 +270,7 @@ __global__ void __launch_bounds__(LN_THREADS) ln_backward_kernel(const LnArgs a)
                     }
             __syncthreads();
         }
-        for (int c = threadIdx.x; c < 2 * a.C; c += LN_THREADS) part[c] = colsum[c];
+        for (int c = threadIdx.x; c < 2 * a.C; c += THREADS) part[c] = colsum[c];
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -316,9 +317,9 @@ struct LnLaunch {
 
 template <class T, class WT, int V, int N, int TPR>
 cudaError_t ln_launch(LnArgs a, LnLaunch &l) {
-    constexpr int RPB = LN_THREADS / TPR;
+    constexpr int THREADS = ln_threads(TPR), RPB = THREADS / TPR;
     const int64_t want = (a.rows + RPB - 1) / RPB;
-    const size_t smem = l.backward && TPR < LN_THREADS ? size_t(a.C) * 8 : 0;
+    const size_t smem = l.backward && RPB > 1 ? size_t(a.C) * 8 : 0;
     // As many blocks as are resident together; a multiple of 8 where a group
     // takes several rows, so that the rows of a group are a multiple of V apart.
     static std::atomic<int> resident[2] = {{0}, {0}};
@@ -326,10 +327,10 @@ cudaError_t ln_launch(LnArgs a, LnLaunch &l) {
     if (per_sm == 0) {
         const cudaError_t e =
             l.backward ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                             &per_sm, ln_backward_kernel<T, WT, V, N, TPR>, LN_THREADS,
-                             TPR < LN_THREADS ? 32 * TPR * 8 : 0)
+                             &per_sm, ln_backward_kernel<T, WT, V, N, TPR>, THREADS,
+                             RPB > 1 ? 32 * TPR * 8 : 0)
                        : cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                             &per_sm, ln_forward_kernel<T, WT, V, N, TPR>, LN_THREADS, 0);
+                             &per_sm, ln_forward_kernel<T, WT, V, N, TPR>, THREADS, 0);
         if (e != cudaSuccess) return e;
         if (per_sm < 1) per_sm = 1;
         resident[l.backward].store(per_sm, std::memory_order_relaxed);
@@ -344,9 +345,9 @@ cudaError_t ln_launch(LnArgs a, LnLaunch &l) {
         l.blocks = int(blocks);
     }
     if (l.backward)
-        ln_backward_kernel<T, WT, V, N, TPR><<<blocks, LN_THREADS, smem, l.stream>>>(a);
+        ln_backward_kernel<T, WT, V, N, TPR><<<blocks, THREADS, smem, l.stream>>>(a);
     else
-        ln_forward_kernel<T, WT, V, N, TPR><<<blocks, LN_THREADS, 0, l.stream>>>(a);
+        ln_forward_kernel<T, WT, V, N, TPR><<<blocks, THREADS, 0, l.stream>>>(a);
     return cudaGetLastError();
 }
 
