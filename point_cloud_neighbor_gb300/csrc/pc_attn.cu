@@ -597,117 +597,165 @@ int pick_split(int64_t slots, int64_t base, int64_t items, int64_t part_floats, 
     return best;
 }
 
+// Which kernels run a pass: few queries, tensor cores (bfloat16), tensor cores
+// in three parts (float32), or float32 instructions (what is left: bfloat16
+// rows that are not 16-byte aligned, and sides without rows).
+enum AttnPath { PATH_FEW, PATH_TC, PATH_PARTS, PATH_SIMT };
+
 template <class T>
-cudaError_t run_pass(const DeviceInfo &dev, AttnArgs a, int mode, float *dslopes,
-                     const AttnSplit *parts, cudaStream_t st) {
-    const bool dkv = mode == ATTN_DKV;
-    const bool few = !dkv && attn_few_fits(a, sizeof(T), mode == ATTN_DQ);
-    const int64_t LX = dkv ? a.Lk : a.Lq, LY = dkv ? a.Lq : a.Lk, NH = dkv ? a.Hkv : a.H;
-    const bool tc = sizeof(T) == 2 && attn_tc_fits(a, mode);
-    const int64_t xr = tc ? attn_tc_rows(mode) : parts ? attn_tc32_rows(a, mode) : SB;
-    const int64_t yr = tc || parts ? ATTN_TC_TILE : SB;
-    const int64_t ntile = (LX + xr - 1) / xr, nyt = (LY + yr - 1) / yr;
-    const int64_t base = ntile * NH * a.B;
-    const int64_t rows = int64_t(a.B) * LX * NH, hrows = int64_t(a.B) * a.H * a.Lq;
-    // Two blocks fit a SM, one of the tensor-core kernels.  Us a block takes to
-    // its first tile, and a tile (measured with all its rows in use).
-    const int64_t slots = int64_t(dev.sm_count) * (tc || parts ? 1 : 2);
-    const bool wide = a.D > 64, fwd = mode == ATTN_FWD;
-    const float tile = tc ? (wide ? 1.4f : 1.1f)
-                       : parts ? (fwd ? 1.7f : dkv ? 3.2f : 2.4f) * (wide ? 2.0f : 1.0f)
-                               : (wide ? 12.0f : 6.0f);
-    a.nsplit = few ? attn_few_parts(dev, a, sizeof(T), mode == ATTN_DQ)
-                   : pick_split(slots, base, dkv ? nyt * (a.H / a.Hkv) : nyt,
-                                rows * a.D * (dkv ? 2 : 1), 5.0f, tile);
-    const bool one_part = a.nsplit == 1;
-    const bool slopes = mode == ATTN_DQ && a.slopes != nullptr && dslopes != nullptr;
-    const size_t part = a.nsplit > 1 ? size_t(a.nsplit) * rows * a.D * (dkv ? 2 : 1) : 0;
-    const size_t ml = a.nsplit > 1 && mode == ATTN_FWD ? size_t(a.nsplit) * 2 * hrows : 0;
-    const size_t rs = slopes ? size_t(a.nsplit) * 3 * hrows + size_t(base) : 0;
-    Scratch ws{&dev, st};
-    cudaError_t e = cudaSuccess;
-    if (part + ml + rs > 0) {
-        if ((e = ws.take((part + ml + rs) * sizeof(float))) != cudaSuccess) return e;
-        a.part = static_cast<float *>(ws.p);
-        a.part_ml = a.part + part;
-        a.rowsum = rs ? a.part_ml + ml : nullptr;
-    }
-    const bool vec = strides_fit(a, 4, 4 * sizeof(T));
-    const int64_t blocks = base * a.nsplit;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    e = few                ? launch_attn_few(a, sizeof(T), mode == ATTN_DQ, st)
-        : tc               ? launch_attn_tc(a, mode, blocks, st)
-        : parts            ? launch_attn_tc32(a, *parts, mode, blocks, st)
-        : mode == ATTN_FWD ? simt_pick<T, ATTN_FWD>(a, vec, blocks, st)
-        : mode == ATTN_DQ ? simt_pick<T, ATTN_DQ>(a, vec, blocks, st)
-                          : simt_pick<T, ATTN_DKV>(a, vec, blocks, st);
-    if (e != cudaSuccess) return e;
-    if (a.nsplit > 1) {
-        const bool v4 = a.D % 4 == 0 && reinterpret_cast<uintptr_t>(a.out) % 16 == 0 &&
-                        reinterpret_cast<uintptr_t>(a.dq) % 16 == 0 &&
-                        reinterpret_cast<uintptr_t>(a.dk) % 16 == 0 &&
-                        reinterpret_cast<uintptr_t>(a.dv) % 16 == 0;
-        // (8 rows of 64 in 152 parts: 27 us a thread per 4 channels, 4 us a block per row)
-        if (!dkv && a.nsplit >= 8 && rows <= 4096) {
-            if (mode == ATTN_FWD)
-                attn_join_rows_kernel<T, true><<<unsigned(rows), 1024, 0, st>>>(a);
-            else
-                attn_join_rows_kernel<T, false><<<unsigned(rows), 1024, 0, st>>>(a);
-            a.nsplit = 1;  // for the slopes' sums
-        } else if (v4)
-            launch_join<T, 4>(a, mode, rows, st);
-        else
-            launch_join<T, 1>(a, mode, rows, st);
-    }
-    if (slopes)
-        attn_slope_kernel<<<a.H, 1024, 0, st>>>(
-            a, !few && (tc || parts) && one_part ? int(ntile) : 0, dslopes);
-    return cudaGetLastError();
+AttnPath pick_path(const AttnArgs &a, bool backward) {
+    if (attn_few_fits(a, sizeof(T), backward)) return PATH_FEW;
+    if (sizeof(T) == 4) return attn_tc32_fits(a) ? PATH_PARTS : PATH_SIMT;
+    return attn_tc_fits(a, backward ? ATTN_DQ : ATTN_FWD) ? PATH_TC : PATH_SIMT;
 }
 
-// Whether float32 goes to the tensor cores: from AAAA scores on.
+// A pass: its number of parts, blocks and scratch.
+struct Pass {
+    AttnArgs a;
+    int mode;
+    bool slopes;             // DQ: row sums for the slopes' gradient
+    int64_t rows, ntile, base, blocks;
+    size_t part, ml, floats;  // scratch: partial sums, forward statistics, all
+};
+
 template <class T>
-bool in_parts(const AttnArgs &a) {
-    return sizeof(T) == 4 && attn_tc32_fits(a);
+Pass plan_pass(const DeviceInfo &dev, const AttnArgs &a, int mode, AttnPath path, bool slopes) {
+    Pass p{a, mode, slopes};
+    const bool dkv = mode == ATTN_DKV, wide = a.D > 64;
+    const int64_t LX = dkv ? a.Lk : a.Lq, LY = dkv ? a.Lq : a.Lk, NH = dkv ? a.Hkv : a.H;
+    const int64_t xr = path == PATH_TC      ? attn_tc_rows(mode)
+                       : path == PATH_PARTS ? attn_tc32_rows(a, mode)
+                                            : SB;
+    const int64_t nyt = (LY + ATTN_TC_TILE - 1) / ATTN_TC_TILE;
+    static_assert(SB == ATTN_TC_TILE, "all kernels stream tiles of 64 rows");
+    p.ntile = (LX + xr - 1) / xr;
+    p.base = p.ntile * NH * a.B;
+    p.rows = int64_t(a.B) * LX * NH;
+    // Two blocks fit a SM, one of the tensor-core kernels.  Us a tile takes
+    // (measured with all its rows in use).
+    const int64_t slots = int64_t(dev.sm_count) * (path == PATH_SIMT ? 2 : 1);
+    const float tile = path == PATH_TC      ? (wide ? 1.4f : 1.1f)
+                       : path == PATH_PARTS ? (mode == ATTN_FWD ? 1.7f : dkv ? 3.2f : 2.4f) *
+                                                  (wide ? 2.0f : 1.0f)
+                                            : (wide ? 12.0f : 6.0f);
+    p.a.nsplit = path == PATH_FEW
+                     ? attn_few_parts(dev, a, sizeof(T), mode == ATTN_DQ)
+                     : pick_split(slots, p.base, dkv ? nyt * (a.H / a.Hkv) : nyt,
+                                  p.rows * a.D * (dkv ? 2 : 1), 5.0f, tile);
+    p.blocks = p.base * p.a.nsplit;
+    const size_t n = size_t(p.a.nsplit), hrows = size_t(a.B) * a.H * a.Lq;
+    p.part = n > 1 ? n * size_t(p.rows) * a.D * (dkv ? 2 : 1) : 0;
+    p.ml = n > 1 && mode == ATTN_FWD ? n * 2 * hrows : 0;
+    p.floats = (p.part + p.ml + (slopes ? n * 3 * hrows + size_t(p.base) : 0) + 3) / 4 * 4;
+    return p;
+}
+
+void place_pass(Pass &p, float *space) {
+    p.a.part = space;
+    p.a.part_ml = space + p.part;
+    p.a.rowsum = p.slopes ? p.a.part_ml + p.ml : nullptr;
+}
+
+// What follows the kernel of a pass: its parts joined, the slopes' gradient.
+template <class T>
+void finish_pass(Pass &p, AttnPath path, float *dslopes, cudaStream_t st) {
+    AttnArgs &a = p.a;
+    const bool one_part = a.nsplit == 1;
+    auto aligned = [](const void *q) { return reinterpret_cast<uintptr_t>(q) % 16 == 0; };
+    if (!one_part) {
+        // (8 rows of 64 in 152 parts: 27 us a thread per 4 channels, 8 us a block per row)
+        if (p.mode != ATTN_DKV && a.nsplit >= 8 && p.rows <= 4096) {
+            if (p.mode == ATTN_FWD)
+                attn_join_rows_kernel<T, true><<<unsigned(p.rows), 1024, 0, st>>>(a);
+            else
+                attn_join_rows_kernel<T, false><<<unsigned(p.rows), 1024, 0, st>>>(a);
+            a.nsplit = 1;  // for the slopes' sums
+        } else if (a.D % 4 == 0 && aligned(a.out) && aligned(a.dq) && aligned(a.dk) &&
+                   aligned(a.dv)) {
+            launch_join<T, 4>(a, p.mode, p.rows, st);
+        } else {
+            launch_join<T, 1>(a, p.mode, p.rows, st);
+        }
+    }
+    if (p.slopes)
+        attn_slope_kernel<<<a.H, 1024, 0, st>>>(
+            a, (path == PATH_TC || path == PATH_PARTS) && one_part ? int(p.ntile) : 0, dslopes);
 }
 
 template <class T>
 cudaError_t run_forward(const DeviceInfo &dev, const AttnArgs &a, cudaStream_t st) {
-    if (!in_parts<T>(a) || attn_few_fits(a, sizeof(T), false))
-        return run_pass<T>(dev, a, ATTN_FWD, nullptr, nullptr, st);
+    const AttnPath path = pick_path<T>(a, false);
+    Pass p = plan_pass<T>(dev, a, ATTN_FWD, path, false);
+    if (p.blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     Scratch ws{&dev, st};
-    AttnSplit s;
-    cudaError_t e = ws.take(attn_split_bytes(a, false));
-    if (e == cudaSuccess) e = launch_attn_split(a, false, ws.p, &s, st);
-    return e == cudaSuccess ? run_pass<T>(dev, a, ATTN_FWD, nullptr, &s, st) : e;
+    const size_t bytes =
+        p.floats * sizeof(float) + (path == PATH_PARTS ? attn_split_bytes(a, false) : 0);
+    cudaError_t e = bytes > 0 ? ws.take(bytes) : cudaSuccess;
+    if (e != cudaSuccess) return e;
+    float *space = static_cast<float *>(ws.p);
+    place_pass(p, space);
+    if (path == PATH_FEW) {
+        e = launch_attn_few(p.a, sizeof(T), false, st);
+    } else if (path == PATH_TC) {
+        e = launch_attn_tc_forward(p.a, unsigned(p.blocks), st);
+    } else if (path == PATH_PARTS) {
+        AttnSplit s;
+        e = launch_attn_split(a, false, space + p.floats, &s, st);
+        if (e == cudaSuccess) e = launch_attn_tc32_forward(p.a, s, unsigned(p.blocks), st);
+    } else {
+        e = simt_pick<T, ATTN_FWD>(p.a, strides_fit(a, 4, 4 * sizeof(T)), p.blocks, st);
+    }
+    if (e != cudaSuccess) return e;
+    finish_pass<T>(p, path, nullptr, st);
+    return cudaGetLastError();
 }
 
 template <class T>
 cudaError_t run_backward(const DeviceInfo &dev, AttnArgs a, const void *out, float *dslopes,
                          cudaStream_t st) {
-    const int64_t rows = int64_t(a.B) * a.Lq * a.H;
-    const bool few = attn_few_fits(a, sizeof(T), true);  // one launch for all gradients
-    const bool parts = !few && in_parts<T>(a);
-    const size_t sides = (size_t(rows) * 2 * sizeof(float) + 255) / 256 * 256;
+    const int64_t rows = int64_t(a.B) * a.Lq * a.H, keys = int64_t(a.B) * a.Lk * a.Hkv;
+    const bool slopes = dslopes != nullptr && a.slopes != nullptr;
+    if (rows == 0) {  // no queries: the keys' gradients are 0
+        const size_t n = size_t(keys) * a.D * sizeof(T);
+        cudaError_t e = slopes ? cudaMemsetAsync(dslopes, 0, size_t(a.H) * 4, st) : cudaSuccess;
+        if (e == cudaSuccess && n > 0) e = cudaMemsetAsync(a.dk, 0, n, st);
+        if (e == cudaSuccess && n > 0) e = cudaMemsetAsync(a.dv, 0, n, st);
+        return e;
+    }
+    const AttnPath path = pick_path<T>(a, true);
+    Pass dq = plan_pass<T>(dev, a, ATTN_DQ, path, slopes);
+    Pass dkv = plan_pass<T>(dev, a, ATTN_DKV, path == PATH_FEW ? PATH_SIMT : path, false);
+    if (path == PATH_FEW || keys == 0) dkv.blocks = 0, dkv.part = dkv.floats = 0;  // no such pass
+    if (dq.blocks + dkv.blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
+    const size_t sides = (size_t(rows) * 2 + 3) / 4 * 4;  // delta, lse2
     Scratch ws{&dev, st};
-    cudaError_t e = ws.take(sides + (parts ? attn_split_bytes(a, true) : 1));
+    cudaError_t e = ws.take((sides + dq.floats + dkv.floats) * sizeof(float) +
+                            (path == PATH_PARTS ? attn_split_bytes(a, true) : 0));
     if (e != cudaSuccess) return e;
-    float *delta = static_cast<float *>(ws.p), *lse2 = delta + rows;
-    a.delta = delta, a.lse2 = lse2;
-    AttnSplit sp, *s = nullptr;
-    if (parts) {
-        e = launch_attn_split(a, true, static_cast<char *>(ws.p) + sides, &sp, st);
-        if (e != cudaSuccess) return e;
-        s = &sp;
+    float *delta = static_cast<float *>(ws.p), *space = delta + sides;
+    dq.a.delta = dkv.a.delta = delta;
+    dq.a.lse2 = dkv.a.lse2 = delta + rows;
+    place_pass(dq, space);
+    place_pass(dkv, space + dq.floats);
+    launch_delta<T>(a, static_cast<const T *>(out), rows, delta, delta + rows, st);
+    const unsigned nq = unsigned(dq.blocks), nk = unsigned(dkv.blocks);
+    if (path == PATH_FEW) {
+        e = launch_attn_few(dq.a, sizeof(T), true, st);
+    } else if (path == PATH_TC) {
+        e = launch_attn_tc_backward(dkv.a, nk, dq.a, nq, st);
+    } else if (path == PATH_PARTS) {
+        AttnSplit s;
+        e = launch_attn_split(a, true, space + dq.floats + dkv.floats, &s, st);
+        if (e == cudaSuccess) e = launch_attn_tc32_backward(dkv.a, nk, dq.a, nq, s, st);
+    } else {
+        const bool vec = strides_fit(a, 4, 4 * sizeof(T));
+        e = simt_pick<T, ATTN_DQ>(dq.a, vec, nq, st);
+        if (e == cudaSuccess && nk > 0) e = simt_pick<T, ATTN_DKV>(dkv.a, vec, nk, st);
     }
-    if (rows > 0) {
-        launch_delta<T>(a, static_cast<const T *>(out), rows, delta, lse2, st);
-        if ((e = run_pass<T>(dev, a, ATTN_DQ, dslopes, s, st)) != cudaSuccess) return e;
-    } else if (dslopes != nullptr && a.slopes != nullptr) {
-        if ((e = cudaMemsetAsync(dslopes, 0, size_t(a.H) * 4, st)) != cudaSuccess) return e;
-    }
-    if (!few && int64_t(a.B) * a.Lk * a.Hkv > 0) e = run_pass<T>(dev, a, ATTN_DKV, nullptr, s, st);
-    return e;
+    if (e != cudaSuccess) return e;
+    if (nk > 0) finish_pass<T>(dkv, path, nullptr, st);
+    finish_pass<T>(dq, path, dslopes, st);
+    return cudaGetLastError();
 }
 
 // The checks both directions share; fills `a`.  *done: nothing to run.

@@ -65,7 +65,10 @@ constexpr int ATTN_TC_TILE = 64;
 // Whether the tensor-core kernels (pc_attn_tc.cu; bfloat16) take these sizes,
 // strides and alignments: channels a multiple of 8 and 16-byte aligned rows.
 bool attn_tc_fits(const AttnArgs &a, int mode);
-cudaError_t launch_attn_tc(const AttnArgs &a, int mode, int64_t blocks, cudaStream_t st);
+cudaError_t launch_attn_tc_forward(const AttnArgs &a, unsigned blocks, cudaStream_t st);
+// Both backward passes: `first` blocks of DKV and `second` of DQ in one launch.
+cudaError_t launch_attn_tc_backward(const AttnArgs &dkv, unsigned first, const AttnArgs &dq,
+                                    unsigned second, cudaStream_t st);
 
 // Few queries per key head (pc_attn_few.cu); backward, one launch writes dk and
 // dv and the parts of dq.  nsplit comes from attn_few_parts.
@@ -84,7 +87,9 @@ int attn_tc32_rows(const AttnArgs &a, int mode);  // rows a block keeps
 size_t attn_split_bytes(const AttnArgs &a, bool backward);
 cudaError_t launch_attn_split(const AttnArgs &a, bool backward, void *space, AttnSplit *s,
                               cudaStream_t st);
-cudaError_t launch_attn_tc32(const AttnArgs &a, const AttnSplit &s, int mode, int64_t blocks,
-                             cudaStream_t st);
+cudaError_t launch_attn_tc32_forward(const AttnArgs &a, const AttnSplit &s, unsigned blocks,
+                                     cudaStream_t st);
+cudaError_t launch_attn_tc32_backward(const AttnArgs &dkv, unsigned first, const AttnArgs &dq,
+                                      unsigned second, const AttnSplit &s, cudaStream_t st);
 
 }  // namespace pcn

@@ -140,10 +140,10 @@ __device__ __forceinline__ void store_row32(float *p, const float (&v)[32], int 
         if (c0 + 4 * i < D) Vec<float, 4>::store(p + 4 * i, v + 4 * i);
 }
 
+// One pass of block `bid`.
 template <int MODE, int DP, bool BIAS>
-__global__ void __launch_bounds__(Cfg<MODE, DP>::THREADS, 1)
-attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnMaps maps,
-               const bool withhold) {
+__device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &maps,
+                                             const bool withhold, const unsigned bid) {
     using C = Cfg<MODE, DP>;
     constexpr bool BWD = C::BWD, FWD = !BWD, DKV = MODE == ATTN_DKV;
     constexpr bool COLS = BIAS || DKV;  // the weights read data of the streamed rows
@@ -172,7 +172,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
     const int NH = DKV ? a.Hkv : a.H;
     const int G = a.H / a.Hkv;
     const int ntile = (LX + T * XR - 1) / (T * XR);
-    int64_t idx = blockIdx.x;
+    int64_t idx = bid;
     const int split = int(idx % a.nsplit);
     idx /= a.nsplit;
     const int tile = int(idx % ntile);
@@ -338,7 +338,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
         for (int k = 0; ok && k < n; ++k, at.next()) {
             const int s = k % STAGES;
             if (k >= STAGES && !wait(&empty[s], unsigned((k / STAGES - 1) & 1))) break;
-            if (withhold && blockIdx.x == 0) break;
+            if (withhold && bid == 0) break;
             if (elect_one()) {
                 const int y0 = at.y, hy = DKV ? at.h : hk;
                 mbar_arrive_expect_tx(&full[s], 2 * C::YBYTES);
@@ -808,7 +808,7 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
                     t[e] = (rd[e * XR] + rd[(3 + e) * XR]) + (rd[(6 + e) * XR] + rd[(9 + e) * XR]);
                     if (row >= nx) t[e] = 0.0f;
                 }
-                put_slope_sums(a, t, split, hrow, row < LX, quad, lane, rowdata + 12 * XR);
+                put_slope_sums(a, t, split, hrow, row < LX, quad, lane, rowdata + 12 * XR, bid);
             }
         }
         float l = l2.x + l2.y;
@@ -863,25 +863,64 @@ attn_tc_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnM
     if (warp == C::CWARPS + 1) tmem_free(tmem, C::COLS);
 }
 
-template <int MODE, int DP, bool BIAS>
-cudaError_t tc_launch(const AttnArgs &a, const AttnMaps &m, int64_t blocks, cudaStream_t st) {
-    using C = Cfg<MODE, DP>;
+template <int DP, bool BIAS>
+__global__ void __launch_bounds__(Cfg<ATTN_FWD, DP>::THREADS, 1)
+attn_tc_forward_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnMaps maps,
+                       const bool withhold) {
+    attn_tc_pass<ATTN_FWD, DP, BIAS>(a, maps, withhold, blockIdx.x);
+}
+
+// Both backward passes in one launch, the keys' first: their blocks are fewer
+// and longer, and the queries' fill what they leave of the GPU.
+template <int DP, bool BIAS>
+__global__ void __launch_bounds__(Cfg<ATTN_DQ, DP>::THREADS, 1)
+attn_tc_backward_kernel(const __grid_constant__ AttnArgs dkv, const __grid_constant__ AttnArgs dq,
+                        const __grid_constant__ AttnMaps maps, const unsigned first,
+                        const bool withhold) {
+    if (blockIdx.x < first)
+        attn_tc_pass<ATTN_DKV, DP, BIAS>(dkv, maps, withhold, blockIdx.x);
+    else
+        attn_tc_pass<ATTN_DQ, DP, BIAS>(dq, maps, withhold, blockIdx.x - first);
+}
+
+bool tc_maps(const AttnArgs &a, bool backward, AttnMaps &m) {
+    const int64_t gs[3] = {int64_t(a.Lq) * a.H * a.D, int64_t(a.H) * a.D, a.D};
+    return make_map(&m.q, a.q, a.qs, a.B, a.Lq, a.H, a.D) &&
+           make_map(&m.k, a.k, a.ks, a.B, a.Lk, a.Hkv, a.D) &&
+           make_map(&m.v, a.v, a.vs, a.B, a.Lk, a.Hkv, a.D) &&
+           (!backward || make_map(&m.go, a.go, gs, a.B, a.Lq, a.H, a.D));
+}
+
+bool withheld() { return (debug_stall() & PC_STALL_ATTENTION) != 0; }
+
+template <int DP, bool BIAS>
+cudaError_t tc_forward(const AttnArgs &a, unsigned blocks, cudaStream_t st) {
+    using C = Cfg<ATTN_FWD, DP>;
+    AttnMaps m{};
+    if (!tc_maps(a, false, m)) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e =
-        allow_smem(attn_tc_kernel<MODE, DP, BIAS>, int(C::SMEM), a.device, done);
+        allow_smem(attn_tc_forward_kernel<DP, BIAS>, int(C::SMEM), a.device, done);
     if (e != cudaSuccess) return e;
-    attn_tc_kernel<MODE, DP, BIAS><<<unsigned(blocks), C::THREADS, C::SMEM, st>>>(
-        a, m, (debug_stall() & PC_STALL_ATTENTION) != 0);
+    attn_tc_forward_kernel<DP, BIAS><<<blocks, C::THREADS, C::SMEM, st>>>(a, m, withheld());
     return cudaGetLastError();
 }
 
-template <int MODE>
-cudaError_t tc_pick(const AttnArgs &a, const AttnMaps &m, int64_t blocks, cudaStream_t st) {
-    if (a.D <= 64)
-        return a.slopes ? tc_launch<MODE, 64, true>(a, m, blocks, st)
-                        : tc_launch<MODE, 64, false>(a, m, blocks, st);
-    return a.slopes ? tc_launch<MODE, 128, true>(a, m, blocks, st)
-                    : tc_launch<MODE, 128, false>(a, m, blocks, st);
+template <int DP, bool BIAS>
+cudaError_t tc_backward(const AttnArgs &dkv, unsigned first, const AttnArgs &dq, unsigned second,
+                        cudaStream_t st) {
+    using C = Cfg<ATTN_DQ, DP>;
+    constexpr size_t other = Cfg<ATTN_DKV, DP>::SMEM;
+    constexpr int smem = int(C::SMEM > other ? C::SMEM : other);
+    static_assert(C::THREADS == Cfg<ATTN_DKV, DP>::THREADS, "one launch");
+    AttnMaps m{};
+    if (!tc_maps(dq, true, m)) return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(attn_tc_backward_kernel<DP, BIAS>, smem, dq.device, done);
+    if (e != cudaSuccess) return e;
+    attn_tc_backward_kernel<DP, BIAS>
+        <<<first + second, C::THREADS, smem, st>>>(dkv, dq, m, first, withheld());
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -902,17 +941,19 @@ bool attn_tc_fits(const AttnArgs &a, int mode) {
     return aligned(a.go) && aligned(a.dq) && aligned(a.dk) && aligned(a.dv);
 }
 
-cudaError_t launch_attn_tc(const AttnArgs &a, int mode, int64_t blocks, cudaStream_t st) {
-    AttnMaps m{};
-    const int64_t gs[3] = {int64_t(a.Lq) * a.H * a.D, int64_t(a.H) * a.D, a.D};
-    if (!make_map(&m.q, a.q, a.qs, a.B, a.Lq, a.H, a.D) ||
-        !make_map(&m.k, a.k, a.ks, a.B, a.Lk, a.Hkv, a.D) ||
-        !make_map(&m.v, a.v, a.vs, a.B, a.Lk, a.Hkv, a.D) ||
-        (mode != ATTN_FWD && !make_map(&m.go, a.go, gs, a.B, a.Lq, a.H, a.D)))
-        return cudaErrorInvalidValue;
-    return mode == ATTN_FWD  ? tc_pick<ATTN_FWD>(a, m, blocks, st)
-           : mode == ATTN_DQ ? tc_pick<ATTN_DQ>(a, m, blocks, st)
-                             : tc_pick<ATTN_DKV>(a, m, blocks, st);
+cudaError_t launch_attn_tc_forward(const AttnArgs &a, unsigned blocks, cudaStream_t st) {
+    if (a.D <= 64)
+        return a.slopes ? tc_forward<64, true>(a, blocks, st) : tc_forward<64, false>(a, blocks, st);
+    return a.slopes ? tc_forward<128, true>(a, blocks, st) : tc_forward<128, false>(a, blocks, st);
+}
+
+cudaError_t launch_attn_tc_backward(const AttnArgs &dkv, unsigned first, const AttnArgs &dq,
+                                    unsigned second, cudaStream_t st) {
+    if (dq.D <= 64)
+        return dq.slopes ? tc_backward<64, true>(dkv, first, dq, second, st)
+                         : tc_backward<64, false>(dkv, first, dq, second, st);
+    return dq.slopes ? tc_backward<128, true>(dkv, first, dq, second, st)
+                     : tc_backward<128, false>(dkv, first, dq, second, st);
 }
 
 }  // namespace pcn

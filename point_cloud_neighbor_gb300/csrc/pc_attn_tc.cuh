@@ -52,7 +52,7 @@ __device__ __forceinline__ void dist4(const float *cd, int c, float2 nx, float2 
 // (`red`: 4 floats); else the rows' three sums go to their part.
 __device__ __forceinline__ void put_slope_sums(const AttnArgs &a, const float (&t)[3], int split,
                                                int64_t hrow, bool in, int quad, int lane,
-                                               float *red) {
+                                               float *red, unsigned bid) {
     if (a.nsplit > 1) {
         const int64_t n = int64_t(a.B) * a.H * a.Lq;
         if (in) {
@@ -66,7 +66,7 @@ __device__ __forceinline__ void put_slope_sums(const AttnArgs &a, const float (&
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (lane == 0) red[quad] = v;
     named_barrier_sync(2, 128);
-    if (quad == 0 && lane == 0) a.rowsum[blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
+    if (quad == 0 && lane == 0) a.rowsum[bid] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
 // The head and first row of a block's tiles, one after the other: `heads`

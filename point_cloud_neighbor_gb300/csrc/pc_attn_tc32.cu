@@ -85,10 +85,11 @@ __device__ __forceinline__ void store_row(float *p, const float (&v)[32], int c0
     }
 }
 
+// One pass of block `bid`.
 template <int MODE, int DP, bool BIAS>
-__global__ void __launch_bounds__(Cfg32<MODE, DP>::THREADS, 1)
-attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ SplitMaps maps,
-                 const AttnSplit split_ptr, const bool withhold) {
+__device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMaps &maps,
+                                               const AttnSplit &split_ptr, const bool withhold,
+                                               const unsigned bid) {
     using C = Cfg32<MODE, DP>;
     constexpr bool BWD = C::BWD, FWD = !BWD, DKV = MODE == ATTN_DKV;
     constexpr int STAGES = C::STAGES;
@@ -110,7 +111,7 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
     const int NH = DKV ? a.Hkv : a.H;
     const int G = a.H / a.Hkv;
     const int ntile = (LX + C::ROWS - 1) / C::ROWS;
-    int64_t idx = blockIdx.x;
+    int64_t idx = bid;
     const int split = int(idx % a.nsplit);
     idx /= a.nsplit;
     const int tile = int(idx % ntile);
@@ -237,7 +238,7 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
         for (int k = 0; ok && k < n; ++k, at.next()) {
             const int s = k % STAGES;
             if (k >= STAGES && !wait(&empty[s], unsigned((k / STAGES - 1) & 1))) break;
-            if (withhold && blockIdx.x == 0) break;
+            if (withhold && bid == 0) break;
             if (elect_one()) {
                 const int hy = DKV ? at.h : hk;
                 mbar_arrive_expect_tx(&full[s], 6 * C::YP);
@@ -591,7 +592,7 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
                 float t[3] = {(wa.x + wa.y) + rd[0], (we.x + we.y) + rd[XR],
                               (wd.x + wd.y) + rd[2 * XR]};
                 if (row >= nx) t[0] = t[1] = t[2] = 0.0f;
-                put_slope_sums(a, t, split, hrow, row < LX, quad, lane, rowdata + 6 * XR);
+                put_slope_sums(a, t, split, hrow, row < LX, quad, lane, rowdata + 6 * XR, bid);
             }
         }
         if (FWD) {  // the row's sum over both halves
@@ -638,6 +639,27 @@ attn_tc32_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ Spl
     if (warp == C::CWARPS + 1) tmem_free(tmem, 512);
 }
 
+template <int DP, bool BIAS>
+__global__ void __launch_bounds__(Cfg32<ATTN_FWD, DP>::THREADS, 1)
+attn_tc32_forward_kernel(const __grid_constant__ AttnArgs a,
+                         const __grid_constant__ SplitMaps maps, const AttnSplit s,
+                         const bool withhold) {
+    attn_tc32_pass<ATTN_FWD, DP, BIAS>(a, maps, s, withhold, blockIdx.x);
+}
+
+// Both backward passes in one launch, the keys' (the longer blocks) first.
+template <int DP, bool BIAS>
+__global__ void __launch_bounds__(Cfg32<ATTN_DQ, DP>::THREADS, 1)
+attn_tc32_backward_kernel(const __grid_constant__ AttnArgs dkv,
+                          const __grid_constant__ AttnArgs dq,
+                          const __grid_constant__ SplitMaps maps, const AttnSplit s,
+                          const unsigned first, const bool withhold) {
+    if (blockIdx.x < first)
+        attn_tc32_pass<ATTN_DKV, DP, BIAS>(dkv, maps, s, withhold, blockIdx.x);
+    else
+        attn_tc32_pass<ATTN_DQ, DP, BIAS>(dq, maps, s, withhold, blockIdx.x - first);
+}
+
 // The three parts of an array [B, L, heads, D] of any strides, rows padded
 // with zeros to Dp channels: out[3][B, L, heads, Dp].
 struct SplitArgs {
@@ -671,27 +693,47 @@ __global__ void __launch_bounds__(256) attn_split_kernel(const SplitArgs a) {
             make_uint4(p[t][0], p[t][1], p[t][2], p[t][3]);
 }
 
-template <int MODE, int DP, bool BIAS>
-cudaError_t tc32_launch(const AttnArgs &a, const SplitMaps &m, const AttnSplit &s, int64_t blocks,
-                        cudaStream_t st) {
-    using C = Cfg32<MODE, DP>;
+bool tc32_maps(const AttnArgs &a, const AttnSplit &s, bool backward, SplitMaps &m) {
+    const int64_t D = s.Dp, planes = 3 * int64_t(a.B);
+    const int64_t qs[3] = {int64_t(a.Lq) * a.H * D, int64_t(a.H) * D, D};
+    const int64_t ks[3] = {int64_t(a.Lk) * a.Hkv * D, int64_t(a.Hkv) * D, D};
+    return make_map(&m.q, s.q, qs, planes, a.Lq, a.H, D) &&
+           make_map(&m.k, s.k, ks, planes, a.Lk, a.Hkv, D) &&
+           make_map(&m.v, s.v, ks, planes, a.Lk, a.Hkv, D) &&
+           (!backward || make_map(&m.go, s.go, qs, planes, a.Lq, a.H, D));
+}
+
+bool withheld() { return (debug_stall() & PC_STALL_ATTENTION) != 0; }
+
+template <int DP, bool BIAS>
+cudaError_t tc32_forward(const AttnArgs &a, const AttnSplit &s, unsigned blocks,
+                         cudaStream_t st) {
+    using C = Cfg32<ATTN_FWD, DP>;
+    SplitMaps m{};
+    if (!tc32_maps(a, s, false, m)) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
     const cudaError_t e =
-        allow_smem(attn_tc32_kernel<MODE, DP, BIAS>, int(C::SMEM), a.device, done);
+        allow_smem(attn_tc32_forward_kernel<DP, BIAS>, int(C::SMEM), a.device, done);
     if (e != cudaSuccess) return e;
-    attn_tc32_kernel<MODE, DP, BIAS><<<unsigned(blocks), C::THREADS, C::SMEM, st>>>(
-        a, m, s, (debug_stall() & PC_STALL_ATTENTION) != 0);
+    attn_tc32_forward_kernel<DP, BIAS><<<blocks, C::THREADS, C::SMEM, st>>>(a, m, s, withheld());
     return cudaGetLastError();
 }
 
-template <int MODE>
-cudaError_t tc32_pick(const AttnArgs &a, const SplitMaps &m, const AttnSplit &s, int64_t blocks,
-                      cudaStream_t st) {
-    if (a.D <= 64)
-        return a.slopes ? tc32_launch<MODE, 64, true>(a, m, s, blocks, st)
-                        : tc32_launch<MODE, 64, false>(a, m, s, blocks, st);
-    return a.slopes ? tc32_launch<MODE, 128, true>(a, m, s, blocks, st)
-                    : tc32_launch<MODE, 128, false>(a, m, s, blocks, st);
+template <int DP, bool BIAS>
+cudaError_t tc32_backward(const AttnArgs &dkv, unsigned first, const AttnArgs &dq,
+                          unsigned second, const AttnSplit &s, cudaStream_t st) {
+    using C = Cfg32<ATTN_DQ, DP>;
+    constexpr size_t other = Cfg32<ATTN_DKV, DP>::SMEM;
+    constexpr int smem = int(C::SMEM > other ? C::SMEM : other);
+    static_assert(C::THREADS == Cfg32<ATTN_DKV, DP>::THREADS, "one launch");
+    SplitMaps m{};
+    if (!tc32_maps(dq, s, true, m)) return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e = allow_smem(attn_tc32_backward_kernel<DP, BIAS>, smem, dq.device, done);
+    if (e != cudaSuccess) return e;
+    attn_tc32_backward_kernel<DP, BIAS>
+        <<<first + second, C::THREADS, smem, st>>>(dkv, dq, m, s, first, withheld());
+    return cudaGetLastError();
 }
 
 }  // namespace
@@ -734,21 +776,22 @@ cudaError_t launch_attn_split(const AttnArgs &a, bool backward, void *space, Att
     return cudaGetLastError();
 }
 
-cudaError_t launch_attn_tc32(const AttnArgs &a, const AttnSplit &s, int mode, int64_t blocks,
-                             cudaStream_t st) {
-    SplitMaps m{};
-    const int64_t D = s.Dp;
-    const int64_t qs[3] = {int64_t(a.Lq) * a.H * D, int64_t(a.H) * D, D};
-    const int64_t ks[3] = {int64_t(a.Lk) * a.Hkv * D, int64_t(a.Hkv) * D, D};
-    const int64_t planes = 3 * int64_t(a.B);
-    if (!make_map(&m.q, s.q, qs, planes, a.Lq, a.H, D) ||
-        !make_map(&m.k, s.k, ks, planes, a.Lk, a.Hkv, D) ||
-        !make_map(&m.v, s.v, ks, planes, a.Lk, a.Hkv, D) ||
-        (mode != ATTN_FWD && !make_map(&m.go, s.go, qs, planes, a.Lq, a.H, D)))
-        return cudaErrorInvalidValue;
-    return mode == ATTN_FWD  ? tc32_pick<ATTN_FWD>(a, m, s, blocks, st)
-           : mode == ATTN_DQ ? tc32_pick<ATTN_DQ>(a, m, s, blocks, st)
-                             : tc32_pick<ATTN_DKV>(a, m, s, blocks, st);
+cudaError_t launch_attn_tc32_forward(const AttnArgs &a, const AttnSplit &s, unsigned blocks,
+                                     cudaStream_t st) {
+    if (a.D <= 64)
+        return a.slopes ? tc32_forward<64, true>(a, s, blocks, st)
+                        : tc32_forward<64, false>(a, s, blocks, st);
+    return a.slopes ? tc32_forward<128, true>(a, s, blocks, st)
+                    : tc32_forward<128, false>(a, s, blocks, st);
+}
+
+cudaError_t launch_attn_tc32_backward(const AttnArgs &dkv, unsigned first, const AttnArgs &dq,
+                                      unsigned second, const AttnSplit &s, cudaStream_t st) {
+    if (dq.D <= 64)
+        return dq.slopes ? tc32_backward<64, true>(dkv, first, dq, second, s, st)
+                         : tc32_backward<64, false>(dkv, first, dq, second, s, st);
+    return dq.slopes ? tc32_backward<128, true>(dkv, first, dq, second, s, st)
+                     : tc32_backward<128, false>(dkv, first, dq, second, s, st);
 }
 
 }  // namespace pcn
