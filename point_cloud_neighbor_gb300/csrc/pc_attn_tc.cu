@@ -27,14 +27,27 @@
 // coordinates' differences.  Per score the threads' work falls from about 10
 // instructions to 5.
 //
-// Both operands of a product have one type, and bfloat16 alone would cost P
-// and dS 2^-9 on average: each is written as the sum of two bfloat16 (2^-17)
-// and multiplied twice.  The sums of P, the statistics and all accumulators
-// are float32, and the slopes' gradient uses the unrounded weights.
+// Both operands of a product have one type, and P in bfloat16 alone would cost
+// up to 2^-8 of a term (the output's and dv's error against float64 0.0024
+// instead of 0.0017, which is the rounding of the result): P is written as the
+// sum of two bfloat16 (2^-17) and multiplied twice.  So is dS where one side has
+// at most 512 rows, whose few terms do not average out; beyond, one
+// bfloat16 gives dq and dk 0.0024 and saves 11 to 15% of the backward pass.  The sums
+// of P, the statistics and all accumulators are float32, and the slopes'
+// gradient uses the unrounded weights.
 //
 // What lies past a cloud's length is masked in the weights; rows of a
 // streamed tile past the length (they would meet weights that are 0, and 0
 // times NaN is NaN) are overwritten with zeros in shared memory.
+//
+// Measured, 4864 queries and keys, 16 heads: 64 channels, forward 137 us (706
+// TFLOP/s of 4 D a score; with the bias 196 us), both backward passes 316 us
+// (765 TFLOP/s of 10 D; 391 us); 128 channels 169 us (1146; 227 us) and 583 us
+// (831; 625 us).  The weights' threads issue on 60% of the cycles, the tensor
+// cores' math is active 40 to 50%.  The products are small (128 x 64 x 16), so
+// what issues them matters: from a branch on a lane index each took 80 to 150
+// cycles, from an elected lane 30 to 70, from one thread that runs the whole
+// loop they are limited by the tensor cores' queue.
 //
 // Every wait is bounded: when one runs out the block raises the status word,
 // lets its copies and products finish, frees its tensor memory and returns;
@@ -48,6 +61,7 @@ namespace pcn {
 namespace {
 
 constexpr float AUG_MOST = 256.0f;  // of slope R^2: see above
+constexpr int ATTN_TWO_S = 512;     // rows of a side up to which dS has two parts
 
 struct AttnMaps {
     CUtensorMap q, k, v, go;
@@ -60,8 +74,6 @@ struct Cfg {
     static constexpr int CWARPS = 16;           // two units of two halves of four warps
     static constexpr int THREADS = 32 * (CWARPS + 4);
     static constexpr int STAGES = DP == 64 ? 6 : 3;
-    // The weights as a sum of two bfloat16.
-    static constexpr bool TWO_P = MODE != ATTN_DQ, TWO_S = false;
     // Tensor memory columns: score buffers (FWD two a unit; else of S and dP, one
     // a unit, and for up to 64 channels a third, so that the scores of a unit's
     // next tile are there before its weights are used up), then the accumulators.
@@ -141,7 +153,7 @@ __device__ __forceinline__ void store_row32(float *p, const float (&v)[32], int 
 }
 
 // One pass of block `bid`.
-template <int MODE, int DP, bool BIAS>
+template <int MODE, int DP, bool BIAS, bool TWO>
 __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &maps,
                                              const bool withhold, const unsigned bid) {
     using C = Cfg<MODE, DP>;
@@ -526,14 +538,14 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
                     const bool more = !first || i > 0;
                     if (FWD) {
                         mma_ts<SMEM_128B>(acc, at, d2 + i * step, id, more);
-                        if (C::TWO_P) mma_ts<SMEM_128B>(acc, at + 8, d2 + i * step, id, true);
+                        mma_ts<SMEM_128B>(acc, at + 8, d2 + i * step, id, true);
                     } else {
                         mma_ts<SMEM_128B>(acc, as, d1 + i * step, id, more);
-                        if (C::TWO_S) mma_ts<SMEM_128B>(acc, as + 8, d1 + i * step, id, true);
+                        if (TWO) mma_ts<SMEM_128B>(acc, as + 8, d1 + i * step, id, true);
                     }
                     if (DKV) {
                         mma_ts<SMEM_128B>(acc + DP, at, d2 + i * step, id, more);
-                        if (C::TWO_P) mma_ts<SMEM_128B>(acc + DP, at + 8, d2 + i * step, id, true);
+                        mma_ts<SMEM_128B>(acc + DP, at + 8, d2 + i * step, id, true);
                     }
                 }
             };
@@ -713,7 +725,7 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
                         split_bf16(t, p[c / 2], lo[c / 2]);
                     }
                     tmem_st8(sb + 16 * h, p);
-                    if (C::TWO_P) tmem_st8(sb + 16 * h + 8, lo);
+                    tmem_st8(sb + 16 * h + 8, lo);
                 }
             } else if (BWD && live) {
                 auto weights = [&](auto tail_, auto direct_) {
@@ -758,27 +770,31 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
                                     we = __ffma2_rn(u, d[e], we);
                                 }
                                 if (DKV) split_bf16(u, p[i / 2], plo[i / 2]);
-                                split_bf16(ds, q[i / 2], qlo[i / 2]);
+                                if (TWO)
+                                    split_bf16(ds, q[i / 2], qlo[i / 2]);
+                                else
+                                    q[i / 2] = pack_bf16(ds.x, ds.y);
                             }
                         }
                         if (DKV) {
                             tmem_st8(sb + 16 * h, p);
-                            if (C::TWO_P) tmem_st8(sb + 16 * h + 8, plo);
+                            tmem_st8(sb + 16 * h + 8, plo);
                         }
                         tmem_st8(sb + YR + 16 * h, q);
-                        if (C::TWO_S) tmem_st8(sb + YR + 16 * h + 8, qlo);
+                        if (TWO) tmem_st8(sb + YR + 16 * h + 8, qlo);
                     }
                 };
                 constexpr std::true_type yes{};
                 constexpr std::false_type no{};
+                constexpr std::integral_constant<bool, BIAS> differences{};
                 if (valid < 32) {
                     if (BIAS && direct)
-                        weights(yes, std::integral_constant<bool, BIAS>{});
+                        weights(yes, differences);
                     else
                         weights(yes, no);
                 } else {
                     if (BIAS && direct)
-                        weights(no, std::integral_constant<bool, BIAS>{});
+                        weights(no, differences);
                     else
                         weights(no, no);
                 }
@@ -867,20 +883,20 @@ template <int DP, bool BIAS>
 __global__ void __launch_bounds__(Cfg<ATTN_FWD, DP>::THREADS, 1)
 attn_tc_forward_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnMaps maps,
                        const bool withhold) {
-    attn_tc_pass<ATTN_FWD, DP, BIAS>(a, maps, withhold, blockIdx.x);
+    attn_tc_pass<ATTN_FWD, DP, BIAS, false>(a, maps, withhold, blockIdx.x);
 }
 
 // Both backward passes in one launch, the keys' first: their blocks are fewer
 // and longer, and the queries' fill what they leave of the GPU.
-template <int DP, bool BIAS>
+template <int DP, bool BIAS, bool TWO>
 __global__ void __launch_bounds__(Cfg<ATTN_DQ, DP>::THREADS, 1)
 attn_tc_backward_kernel(const __grid_constant__ AttnArgs dkv, const __grid_constant__ AttnArgs dq,
                         const __grid_constant__ AttnMaps maps, const unsigned first,
                         const bool withhold) {
     if (blockIdx.x < first)
-        attn_tc_pass<ATTN_DKV, DP, BIAS>(dkv, maps, withhold, blockIdx.x);
+        attn_tc_pass<ATTN_DKV, DP, BIAS, TWO>(dkv, maps, withhold, blockIdx.x);
     else
-        attn_tc_pass<ATTN_DQ, DP, BIAS>(dq, maps, withhold, blockIdx.x - first);
+        attn_tc_pass<ATTN_DQ, DP, BIAS, TWO>(dq, maps, withhold, blockIdx.x - first);
 }
 
 bool tc_maps(const AttnArgs &a, bool backward, AttnMaps &m) {
@@ -906,7 +922,7 @@ cudaError_t tc_forward(const AttnArgs &a, unsigned blocks, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <int DP, bool BIAS>
+template <int DP, bool BIAS, bool TWO>
 cudaError_t tc_backward(const AttnArgs &dkv, unsigned first, const AttnArgs &dq, unsigned second,
                         cudaStream_t st) {
     using C = Cfg<ATTN_DQ, DP>;
@@ -916,9 +932,9 @@ cudaError_t tc_backward(const AttnArgs &dkv, unsigned first, const AttnArgs &dq,
     AttnMaps m{};
     if (!tc_maps(dq, true, m)) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(attn_tc_backward_kernel<DP, BIAS>, smem, dq.device, done);
+    const cudaError_t e = allow_smem(attn_tc_backward_kernel<DP, BIAS, TWO>, smem, dq.device, done);
     if (e != cudaSuccess) return e;
-    attn_tc_backward_kernel<DP, BIAS>
+    attn_tc_backward_kernel<DP, BIAS, TWO>
         <<<first + second, C::THREADS, smem, st>>>(dkv, dq, m, first, withheld());
     return cudaGetLastError();
 }
@@ -947,13 +963,21 @@ cudaError_t launch_attn_tc_forward(const AttnArgs &a, unsigned blocks, cudaStrea
     return a.slopes ? tc_forward<128, true>(a, blocks, st) : tc_forward<128, false>(a, blocks, st);
 }
 
+template <int DP, bool BIAS>
+static cudaError_t pick_two(const AttnArgs &dkv, unsigned first, const AttnArgs &dq,
+                            unsigned second, cudaStream_t st) {
+    return dq.Lq <= ATTN_TWO_S || dq.Lk <= ATTN_TWO_S
+               ? tc_backward<DP, BIAS, true>(dkv, first, dq, second, st)
+               : tc_backward<DP, BIAS, false>(dkv, first, dq, second, st);
+}
+
 cudaError_t launch_attn_tc_backward(const AttnArgs &dkv, unsigned first, const AttnArgs &dq,
                                     unsigned second, cudaStream_t st) {
     if (dq.D <= 64)
-        return dq.slopes ? tc_backward<64, true>(dkv, first, dq, second, st)
-                         : tc_backward<64, false>(dkv, first, dq, second, st);
-    return dq.slopes ? tc_backward<128, true>(dkv, first, dq, second, st)
-                     : tc_backward<128, false>(dkv, first, dq, second, st);
+        return dq.slopes ? pick_two<64, true>(dkv, first, dq, second, st)
+                         : pick_two<64, false>(dkv, first, dq, second, st);
+    return dq.slopes ? pick_two<128, true>(dkv, first, dq, second, st)
+                     : pick_two<128, false>(dkv, first, dq, second, st);
 }
 
 }  // namespace pcn
