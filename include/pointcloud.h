@@ -569,7 +569,15 @@ int pc_rotary(const void *q, const void *k, int dtype, int64_t B, int64_t L, int
  *
  * Scratch (the library's stream-ordered pool): the parts of a pass whose
  * streamed side is split among more blocks, at most 1 GiB; in the backward
- * pass 8 bytes, with grad_slopes 12 more per part, per query row and head.
+ * pass 8 bytes, with grad_slopes 12 more per part, per query row and head;
+ * for float32 three bfloat16 parts of q, k, v and grad_out (6 bytes an
+ * element, channels rounded up to 8).
+ *
+ * bfloat16 with D a multiple of 8 and 16-byte aligned rows and strides, and
+ * float32, run on the tensor cores; other bfloat16 layouts run in float32
+ * instructions.  The tensor-core kernels bound their device-side waits: if
+ * one runs out the block's outputs are unspecified and the device status
+ * word holds PC_ERR_DEVICE_TIMEOUT.
  *
  * Return PC_OK, PC_ERR_INVALID_ARGUMENT, PC_ERR_UNSUPPORTED, PC_ERR_CUDA or
  * PC_ERR_NO_DEVICE.
@@ -619,10 +627,10 @@ int pc_device_status(void *stream, int reset, int32_t *out_status);
  *                         its first tile's copy (nothing is left in flight):
  *                         the producer and that block's consumers run out
  *                         their waits.
- *   PC_STALL_ATTENTION    the first thread block of a bfloat16 attention
- *                         launch (forward or backward) never issues the
- *                         copies of its streamed side.  That block's outputs
- *                         are unspecified.
+ *   PC_STALL_ATTENTION    the first thread block of each pass of a
+ *                         tensor-core attention launch (forward, backward)
+ *                         never issues the copies of its streamed side.
+ *                         That block's outputs are unspecified.
  * Each ends as a real timeout does: PC_ERR_DEVICE_TIMEOUT in the status
  * word, -1 in the outputs the stopped blocks did not finish.
  * pc_debug_set_fps_grid_stall(e) sets or clears PC_STALL_FPS_GRID alone.

@@ -1,6 +1,7 @@
 // pc_attn.cu -- attention over point tokens with a bias by squared distance
-// and lengths masks: the C ABI, the float32 kernels and the joins of split
-// passes.  Formulas and the three passes are in pc_attn.cuh.
+// and lengths masks: the C ABI, the choice of kernels, the joins of split
+// passes, and kernels in float32 instructions for what the others do not take.
+// Formulas and the three passes are in pc_attn.cuh.
 #include "pc_attn.cuh"
 #include "pointcloud.h"
 
@@ -13,7 +14,10 @@ namespace {
 // ---------------------------------------------------------------------------
 // float32 arithmetic on tiles of 64 rows by 64 streamed rows, 256 threads as
 // 16 x 16: a thread forms 4 x 4 scores (rows ty + 16 i, columns tx + 16 j)
-// and 4 rows by DP / 16 channels of the accumulators.
+// and 4 rows by DP / 16 channels of the accumulators.  Any channels, strides
+// and alignment.  Bound by shared-memory reads (8 of 16 bytes for 64
+// multiply-adds); 1024 queries and keys, 8 heads of 64: forward 83 us,
+// backward 324 us, against 19 and 39 us on the tensor cores.
 // ---------------------------------------------------------------------------
 constexpr int SB = 64;           // rows of a tile, both sides
 constexpr int ST = 256;          // threads

