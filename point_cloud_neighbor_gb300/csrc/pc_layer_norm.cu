@@ -6,7 +6,7 @@
 //   dx = rstd (g - mean(g) - xhat mean(g xhat)),
 //   dw = sum_rows dy xhat,  db = sum_rows dy.
 //
-// Bound: memory.  A row is read once into the registers of TPR threads (8 for
+// Bound: memory.  A row is read once by TPR threads (8 for
 // C <= 128, a warp up to C of about 1000, a block of 256 beyond) and written
 // once; the variance is summed from the centred values in registers, so no
 // cancellation of sums of squares.  All sums are float32.
@@ -25,11 +25,15 @@
 // the blocks' rows in a fixed order.  No atomics: the result does not change
 // from run to run.
 //
-// The next row is on its way while one is worked on, and blocks are small (128
-// threads): what counts is the bytes in flight.  Measured, 100,000 x 512
-// float32: forward 72 us (5.7 TB/s), backward 114 us (5.4 TB/s); C = 515: 83
-// and 145 us; 65,536 x 1024 bfloat16: 60 us (4.5 TB/s) and 102 us (3.9 TB/s).
-// With one element a load C = 515 took 158 and 368 us.
+// What counts is the bytes in flight.  A thread's rows come through a ring of
+// slots in shared memory, up to 4 rows deep, by asynchronous copies; a slot is
+// written and read by one thread alone, so there is nothing to wait for but the
+// thread's own copies.  Blocks are small (128 threads) and fill the registers.
+// Measured, 100,000 x 512 float32: forward 74 us (5.5 TB/s), backward 111 us
+// (5.5 TB/s); C = 515: 75 and 125 us (with the next row in registers 85 and
+// 147 us, with one element a load 158 and 368 us); 65,536 x 1024 bfloat16: 52
+// us (5.2 TB/s) and 100 us (4.0 TB/s; registers 60 and 102 us); 100,000 x 515
+// bfloat16: 76 and 149 us (registers 78 and 136 us), bound by instructions.
 #include "pc_internal.h"
 #include "pc_vec.cuh"
 #include "pointcloud.h"
@@ -70,42 +74,94 @@ __device__ __forceinline__ float row_sum(float v, float *red) {
     return v;
 }
 
-// The V elements at p[at] as they are in memory.  Some may belong to the
-// neighbouring rows; a vector that would leave the array of `total` elements
-// is read element by element, zeros outside.
+// 1 / sqrt(v) from the hardware's approximation and a step of Newton's method;
+// infinity for 0 (a constant row with eps 0) as it is.
+__device__ __forceinline__ float inv_sqrt(float v) {
+    const float r = rsqrtf(v), d = fmaf(-v * r, r, 1.0f);
+    return v > 0.0f && v < INFINITY ? fmaf(0.5f * r, d, r) : r;
+}
+
+// V elements on their way through a slot of shared memory that one thread
+// alone writes and reads.  At the ends of a row a vector has elements of the
+// neighbouring rows too (`edge`); one that would leave the array, of which
+// `left` elements remain, is read in part, zeros beyond.
 template <class T, int V>
-struct Raw {
-    T v[V];
-    __device__ __forceinline__ void load(const T *p, int64_t at, int64_t total) {
+struct Slot {
+    static constexpr int BYTES = V * int(sizeof(T));
+    static __device__ __forceinline__ void copy(unsigned char *slot, const T *p, bool edge,
+                                                int64_t left) {
         if (V == 1) {
-            v[0] = p[at];
-        } else if (at + V <= total) {
-            *reinterpret_cast<uint4 *>(v) = *reinterpret_cast<const uint4 *>(p + at);
+            *reinterpret_cast<T *>(slot) = *p;
         } else {
-#pragma unroll
-            for (int e = 0; e < V; ++e) v[e] = at + e < total ? p[at + e] : T(0.0f);
+            const int n = edge && left < V ? int(left) * int(sizeof(T)) : 16;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             uint32_t(__cvta_generic_to_shared(slot))),
+                         "l"(p), "r"(n)
+                         : "memory");
         }
     }
-    // as float32, 0 where the column col + e is not one of the row
-    __device__ __forceinline__ void get(int col, int C, float *f) const {
-        Vec<T, V>::load(v, f);
-        zero(col, C, f);
+    // as float32
+    static __device__ __forceinline__ void get(const unsigned char *slot, float *f) {
+        Vec<T, V>::load(reinterpret_cast<const T *>(slot), f);
     }
+    // 0 where the column col + e is not one of the row
     static __device__ __forceinline__ void zero(int col, int C, float *f) {
-        if (V > 1 ? col < 0 || col + V > C : col >= C)
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                if (col + e < 0 || col + e >= C) f[e] = 0.0f;
+        for (int e = 0; e < V; ++e)
+            if (col + e < 0 || col + e >= C) f[e] = 0.0f;
     }
-    static __device__ __forceinline__ void store(T *p, int64_t at, int col, int C,
+    static __device__ __forceinline__ void store(T *p, bool edge, int col, int C,
                                                  const float *f) {
-        if (V == 1 || (col >= 0 && col + V <= C)) {
-            Vec<T, V>::store(p + at, f);
+        if (!edge) {
+            Vec<T, V>::store(p, f);
         } else {
 #pragma unroll
             for (int e = 0; e < V; ++e)
-                if (col + e >= 0 && col + e < C) Vec<T, 1>::store(p + at + e, f + e);
+                if (col + e >= 0 && col + e < C) Vec<T, 1>::store(p + e, f + e);
         }
+    }
+};
+
+// A thread's vectors, the same in all its rows: vector i has the columns
+// first + i TPR V and on; bit i of `live`: some are the row's, of `edge`: not all.
+template <int V, int N, int TPR>
+struct Columns {
+    int first, C;
+    unsigned live = 0, edge = 0;
+    __device__ __forceinline__ Columns(int t, int shift, int C_) : first(t * V - shift), C(C_) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            if (col(i) < C) live |= 1u << i;
+            if (col(i) < 0 || col(i) + V > C) edge |= 1u << i;
+        }
+    }
+    __device__ __forceinline__ int col(int i) const { return first + i * TPR * V; }
+    __device__ __forceinline__ bool is_live(int i) const { return live >> i & 1; }
+    __device__ __forceinline__ bool is_edge(int i) const { return edge >> i & 1; }
+};
+
+// Rows a thread has on their way, and its ring of slots for ARRAYS inputs:
+// slot (stage, array, i) of a thread is BYTES from its neighbours', so a warp's
+// accesses are contiguous.
+template <class T, int V, int N, int TPR, int ARRAYS>
+struct Ring {
+    static constexpr int THREADS = ln_threads(TPR);
+    static constexpr int ROW = ARRAYS * N * THREADS * Slot<T, V>::BYTES;
+    static constexpr int DEEP = 65536 / ROW;
+    static constexpr int STAGES = DEEP > 4 ? 4 : DEEP < 2 ? 2 : DEEP;
+    static constexpr int BYTES = STAGES * ROW;
+    static __device__ __forceinline__ unsigned char *slot(unsigned char *ring, int stage,
+                                                          int array, int i) {
+        return ring +
+               (size_t((stage * ARRAYS + array) * N + i) * THREADS + threadIdx.x) *
+                   Slot<T, V>::BYTES;
+    }
+    static __device__ __forceinline__ void close() {
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    // the oldest of STAGES rows is there
+    static __device__ __forceinline__ void wait() {
+        asm volatile("cp.async.wait_group %0;" ::"n"(STAGES - 1) : "memory");
     }
 };
 
@@ -119,9 +175,9 @@ __device__ __forceinline__ void load_param(const void *p, int col, int C, float 
     }
 }
 
-// A thread holds the vectors t, t + TPR, ... (N of V elements) that cover its
-// row; vector i has the columns V (t + i TPR) - shift and on.  The next row is
-// on its way while one is worked on.
+// A thread takes the vectors t, t + TPR, ... (N of V elements) that cover its
+// row; vector i has the columns V (t + i TPR) - shift and on.  A slot is filled
+// again once the row's first sum has used what was in it.
 template <class T, class WT, int V, int N, int TPR>
 __global__ void __launch_bounds__(ln_threads(TPR)) ln_forward_kernel(const LnArgs a) {
     constexpr int THREADS = ln_threads(TPR), RPB = THREADS / TPR;
@@ -129,56 +185,69 @@ __global__ void __launch_bounds__(ln_threads(TPR)) ln_forward_kernel(const LnArg
     const int t = threadIdx.x % TPR;
     const int64_t step = int64_t(gridDim.x) * RPB, total = a.rows * a.C;
     int64_t row = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR;
-    const int shift = V > 1 ? int(row * a.C % V) : 0;
+    const Columns<V, N, TPR> c(t, V > 1 ? int(row * a.C % V) : 0, a.C);
+    int64_t at = row * a.C + c.first;  // the thread's first vector
+    const int64_t stride = step * a.C;
     const T *x = static_cast<const T *>(a.x);
     T *y = static_cast<T *>(a.y);
-    Raw<T, V> raw[N];
-    auto fetch = [&](int64_t r) {
-        if (r < a.rows)
+    using R = Ring<T, V, N, TPR, 1>;
+    extern __shared__ __align__(16) unsigned char ring[];
+    auto fetch = [&](int ahead, int stage) {
+        if (row + ahead * step < a.rows) {
+            const int64_t f = at + ahead * stride;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int col = (t + i * TPR) * V - shift;
-                if (col < a.C) raw[i].load(x, r * a.C + col, total);
-            }
+            for (int i = 0; i < N; ++i)
+                if (c.is_live(i))
+                    Slot<T, V>::copy(R::slot(ring, stage, 0, i), x + f + i * TPR * V,
+                                     c.is_edge(i), total - (f + i * TPR * V));
+        }
+        R::close();
     };
-    fetch(row);
+#pragma unroll
+    for (int i = 0; i < R::STAGES; ++i) fetch(i, i);
     float w[N][V], b[N][V];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const int col = (t + i * TPR) * V - shift;
-        load_param<WT, V>(a.w, col, a.C, 1.0f, w[i]);
-        load_param<WT, V>(a.b, col, a.C, 0.0f, b[i]);
+        load_param<WT, V>(a.w, c.col(i), a.C, 1.0f, w[i]);
+        load_param<WT, V>(a.b, c.col(i), a.C, 0.0f, b[i]);
     }
     // the groups of a warp go round together: they share its shuffles
     const int64_t rounds = (a.rows + step - 1) / step;
-    for (int64_t k = 0; k < rounds; ++k, row += step) {
+    const float inv_c = 1.0f / float(a.C);
+    int stage = 0;
+    for (int64_t k = 0; k < rounds; ++k, row += step, at += stride) {
         const bool in = row < a.rows;
         float v[N][V];
         float s = 0.0f;
+        R::wait();
 #pragma unroll
-        for (int i = 0; i < N; ++i) raw[i].get((t + i * TPR) * V - shift, a.C, v[i]);
-        fetch(row + step);
+        for (int i = 0; i < N; ++i) {
+            Slot<T, V>::get(R::slot(ring, stage, 0, i), v[i]);
+            if (c.is_edge(i)) Slot<T, V>::zero(c.col(i), a.C, v[i]);
+        }
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int e = 0; e < V; ++e) s += v[i][e];
-        const float mean = row_sum<TPR>(s, red) / float(a.C);
+        const float mean = row_sum<TPR>(s, red) * inv_c;
+        fetch(R::STAGES, stage);
+        stage = stage + 1 == R::STAGES ? 0 : stage + 1;
         float q = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
 #pragma unroll
             for (int e = 0; e < V; ++e) v[i][e] -= mean;
-            Raw<T, V>::zero((t + i * TPR) * V - shift, a.C, v[i]);
+            if (c.is_edge(i)) Slot<T, V>::zero(c.col(i), a.C, v[i]);
 #pragma unroll
             for (int e = 0; e < V; ++e) q = fmaf(v[i][e], v[i][e], q);
         }
-        const float rstd = 1.0f / sqrtf(row_sum<TPR>(q, red) / float(a.C) + a.eps);
+        const float rstd = inv_sqrt(fmaf(row_sum<TPR>(q, red), inv_c, a.eps));
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int col = (t + i * TPR) * V - shift;
 #pragma unroll
             for (int e = 0; e < V; ++e) v[i][e] = fmaf(v[i][e] * rstd, w[i][e], b[i][e]);
-            if (in && col < a.C) Raw<T, V>::store(y, row * a.C + col, col, a.C, v[i]);
+            if (in && c.is_live(i))
+                Slot<T, V>::store(y + at + i * TPR * V, c.is_edge(i), c.col(i), a.C, v[i]);
         }
         if (in && t == 0 && a.mean != nullptr) {
             a.mean[row] = mean;
@@ -191,49 +260,68 @@ template <class T, class WT, int V, int N, int TPR>
 __global__ void __launch_bounds__(ln_threads(TPR)) ln_backward_kernel(const LnArgs a) {
     constexpr int THREADS = ln_threads(TPR), RPB = THREADS / TPR;
     __shared__ float red[THREADS / 32];
-    extern __shared__ float colsum[];  // [2][C], several rows a block only
+    using R = Ring<T, V, N, TPR, 2>;
+    extern __shared__ __align__(16) unsigned char ring[];
+    float *colsum = reinterpret_cast<float *>(ring);  // [2][C] after the last row
     const int t = threadIdx.x % TPR;
     const int64_t step = int64_t(gridDim.x) * RPB, total = a.rows * a.C;
     int64_t row = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR;
-    const int shift = V > 1 ? int(row * a.C % V) : 0;
+    const Columns<V, N, TPR> c(t, V > 1 ? int(row * a.C % V) : 0, a.C);
+    int64_t at = row * a.C + c.first;  // the thread's first vector
+    const int64_t stride = step * a.C;
     const T *x = static_cast<const T *>(a.x), *dy = static_cast<const T *>(a.dy);
     T *dx = static_cast<T *>(a.y);
-    Raw<T, V> rx[N], rg[N];
     float mean_n = 0.0f, rstd_n = 0.0f;
-    auto fetch = [&](int64_t r) {
-        if (r < a.rows) {
+    auto fetch = [&](int ahead, int stage) {
+        if (row + ahead * step < a.rows) {
+            const int64_t f = at + ahead * stride;
 #pragma unroll
-            for (int i = 0; i < N; ++i) {
-                const int col = (t + i * TPR) * V - shift;
-                if (col < a.C) {
-                    rx[i].load(x, r * a.C + col, total);
-                    rg[i].load(dy, r * a.C + col, total);
+            for (int i = 0; i < N; ++i)
+                if (c.is_live(i)) {
+                    const int64_t g = f + i * TPR * V;
+                    Slot<T, V>::copy(R::slot(ring, stage, 0, i), x + g, c.is_edge(i), total - g);
+                    Slot<T, V>::copy(R::slot(ring, stage, 1, i), dy + g, c.is_edge(i), total - g);
                 }
-            }
-            mean_n = a.mean[r], rstd_n = a.rstd[r];
         }
+        R::close();
     };
-    fetch(row);
+    auto stats = [&](int64_t r) {
+        if (r < a.rows) mean_n = a.mean[r], rstd_n = a.rstd[r];
+    };
+#pragma unroll
+    for (int i = 0; i < R::STAGES; ++i) fetch(i, i);
+    stats(row);
     float dw[N][V], db[N][V], w[N][V];
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        load_param<WT, V>(a.w, (t + i * TPR) * V - shift, a.C, 1.0f, w[i]);
+        load_param<WT, V>(a.w, c.col(i), a.C, 1.0f, w[i]);
 #pragma unroll
         for (int e = 0; e < V; ++e) dw[i][e] = db[i][e] = 0.0f;
     }
     const float inv_c = 1.0f / float(a.C);
     const int64_t rounds = (a.rows + step - 1) / step;
-    for (int64_t k = 0; k < rounds; ++k, row += step) {
+    int stage = 0;
+    for (int64_t k = 0; k < rounds; ++k, row += step, at += stride) {
         const bool in = row < a.rows;
+        R::wait();
         float xv[N][V], gv[N][V];
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int col = (t + i * TPR) * V - shift;
-            rx[i].get(in ? col : a.C, a.C, xv[i]);  // past the rows: nothing was read,
-            rg[i].get(in ? col : a.C, a.C, gv[i]);  // no part in the columns' sums
+            Slot<T, V>::get(R::slot(ring, stage, 0, i), xv[i]);
+            Slot<T, V>::get(R::slot(ring, stage, 1, i), gv[i]);
+            if (c.is_edge(i)) {
+                Slot<T, V>::zero(c.col(i), a.C, xv[i]);
+                Slot<T, V>::zero(c.col(i), a.C, gv[i]);
+            }
+        }
+        if (!in) {  // past the rows: nothing was read, no part in the columns' sums
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+#pragma unroll
+                for (int e = 0; e < V; ++e) xv[i][e] = gv[i][e] = 0.0f;
         }
         const float mean = mean_n, rstd = rstd_n;
-        fetch(row + step);
+        stats(row + step);
         float s0 = 0.0f, s1 = 0.0f;
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -249,18 +337,21 @@ __global__ void __launch_bounds__(ln_threads(TPR)) ln_backward_kernel(const LnAr
                 gv[i][e] = g;
             }
         const float c0 = row_sum<TPR>(s0, red) * inv_c;
+        fetch(R::STAGES, stage);
+        stage = stage + 1 == R::STAGES ? 0 : stage + 1;
         const float c1 = row_sum<TPR>(s1, red) * inv_c;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int col = (t + i * TPR) * V - shift;
 #pragma unroll
             for (int e = 0; e < V; ++e) xv[i][e] = rstd * (gv[i][e] - fmaf(xv[i][e], c1, c0));
-            if (in && col < a.C) Raw<T, V>::store(dx, row * a.C + col, col, a.C, xv[i]);
+            if (in && c.is_live(i))
+                Slot<T, V>::store(dx + at + i * TPR * V, c.is_edge(i), c.col(i), a.C, xv[i]);
         }
     }
     if (a.part == nullptr) return;
     float *part = a.part + size_t(blockIdx.x) * 2 * a.C;
     if (RPB > 1) {
+        __syncthreads();  // (the ring's last groups of copies are empty)
         // join the block's groups, one after the other
         for (int g = 0; g < RPB; ++g) {
             if (int(threadIdx.x / TPR) == g)
@@ -268,24 +359,24 @@ __global__ void __launch_bounds__(ln_threads(TPR)) ln_backward_kernel(const LnAr
                 for (int i = 0; i < N; ++i)
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        const int c = (t + i * TPR) * V - shift + e;
-                        if (c >= 0 && c < a.C) {
-                            colsum[c] = g == 0 ? dw[i][e] : colsum[c] + dw[i][e];
-                            colsum[a.C + c] = g == 0 ? db[i][e] : colsum[a.C + c] + db[i][e];
+                        const int n = c.col(i) + e;
+                        if (n >= 0 && n < a.C) {
+                            colsum[n] = g == 0 ? dw[i][e] : colsum[n] + dw[i][e];
+                            colsum[a.C + n] = g == 0 ? db[i][e] : colsum[a.C + n] + db[i][e];
                         }
                     }
             __syncthreads();
         }
-        for (int c = threadIdx.x; c < 2 * a.C; c += THREADS) part[c] = colsum[c];
+        for (int n = threadIdx.x; n < 2 * a.C; n += THREADS) part[n] = colsum[n];
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                const int c = (t + i * TPR) * V - shift + e;
-                if (c >= 0 && c < a.C) {
-                    part[c] = dw[i][e];
-                    part[a.C + c] = db[i][e];
+                const int n = c.col(i) + e;
+                if (n >= 0 && n < a.C) {
+                    part[n] = dw[i][e];
+                    part[a.C + n] = db[i][e];
                 }
             }
     }
@@ -325,18 +416,25 @@ template <class T, class WT, int V, int N, int TPR>
 cudaError_t ln_launch(LnArgs a, LnLaunch &l) {
     constexpr int THREADS = ln_threads(TPR), RPB = THREADS / TPR;
     const int64_t want = (a.rows + RPB - 1) / RPB;
-    const size_t smem = l.backward && RPB > 1 ? size_t(a.C) * 8 : 0;
+    constexpr int FORWARD = Ring<T, V, N, TPR, 1>::BYTES;
+    constexpr int SUMS = RPB > 1 ? 2 * 4 * V * N * TPR : 0;  // [2][C], C at most V N TPR
+    constexpr int RING2 = Ring<T, V, N, TPR, 2>::BYTES, BACKWARD = RING2 > SUMS ? RING2 : SUMS;
     // As many blocks as are resident together; a multiple of 8 where a group
     // takes several rows, so that the rows of a group are a multiple of V apart.
+    static std::atomic<uint64_t> allowed[2] = {{0}, {0}};
+    cudaError_t e =
+        l.backward ? allow_smem(ln_backward_kernel<T, WT, V, N, TPR>, BACKWARD, l.dev->device,
+                                allowed[1])
+                   : allow_smem(ln_forward_kernel<T, WT, V, N, TPR>, FORWARD, l.dev->device,
+                                allowed[0]);
+    if (e != cudaSuccess) return e;
     static std::atomic<int> resident[2] = {{0}, {0}};
     int per_sm = resident[l.backward].load(std::memory_order_relaxed);
     if (per_sm == 0) {
-        const cudaError_t e =
-            l.backward ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                             &per_sm, ln_backward_kernel<T, WT, V, N, TPR>, THREADS,
-                             RPB > 1 ? 32 * TPR * 8 : 0)
+        e = l.backward ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                             &per_sm, ln_backward_kernel<T, WT, V, N, TPR>, THREADS, BACKWARD)
                        : cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                             &per_sm, ln_forward_kernel<T, WT, V, N, TPR>, THREADS, 0);
+                             &per_sm, ln_forward_kernel<T, WT, V, N, TPR>, THREADS, FORWARD);
         if (e != cudaSuccess) return e;
         if (per_sm < 1) per_sm = 1;
         resident[l.backward].store(per_sm, std::memory_order_relaxed);
@@ -344,16 +442,15 @@ cudaError_t ln_launch(LnArgs a, LnLaunch &l) {
     const int64_t most = (int64_t(l.dev->sm_count) * per_sm + 7) / 8 * 8;
     const unsigned blocks = unsigned(want < most ? want : most);
     if (l.params) {
-        const cudaError_t e =
-            scratch_alloc(*l.dev, &l.part, size_t(blocks) * 2 * a.C * sizeof(float), l.stream);
+        e = scratch_alloc(*l.dev, &l.part, size_t(blocks) * 2 * a.C * sizeof(float), l.stream);
         if (e != cudaSuccess) return e;
         a.part = static_cast<float *>(l.part);
         l.blocks = int(blocks);
     }
     if (l.backward)
-        ln_backward_kernel<T, WT, V, N, TPR><<<blocks, THREADS, smem, l.stream>>>(a);
+        ln_backward_kernel<T, WT, V, N, TPR><<<blocks, THREADS, BACKWARD, l.stream>>>(a);
     else
-        ln_forward_kernel<T, WT, V, N, TPR><<<blocks, THREADS, 0, l.stream>>>(a);
+        ln_forward_kernel<T, WT, V, N, TPR><<<blocks, THREADS, FORWARD, l.stream>>>(a);
     return cudaGetLastError();
 }
 
