@@ -41,9 +41,9 @@
 // times NaN is NaN) are overwritten with zeros in shared memory.
 //
 // Measured, 4864 queries and keys, 16 heads: 64 channels, forward 137 us (706
-// TFLOP/s of 4 D a score; with the bias 196 us), both backward passes 316 us
-// (765 TFLOP/s of 10 D; 391 us); 128 channels 169 us (1146; 227 us) and 583 us
-// (831; 625 us).  The weights' threads issue on 60% of the cycles, the tensor
+// TFLOP/s of 4 D a score; with the bias 195 us), both backward passes 316 us
+// (766 TFLOP/s of 10 D; 395 us); 128 channels 169 us (1149; 223 us) and 564 us
+// (859; 626 us).  The weights' threads issue on 60% of the cycles, the tensor
 // cores' math is active 40 to 50%.  The products are small (128 x 64 x 16), so
 // what issues them matters: from a branch on a lane index each took 80 to 150
 // cycles, from an elected lane 30 to 70, from one thread that runs the whole
@@ -736,6 +736,9 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
                         tmem_ld16(sb + 16 * h, r);
                         tmem_ld16(sb + YR + 16 * h, g);
                         tmem_wait_ld();
+                        // sums of 16 columns first: chains as long as a row would
+                        // round away as much as the plain form's error again
+                        float2 ta = make_float2(0.0f, 0.0f), te = ta, td = ta;
 #pragma unroll
                         for (int c = 0; c < 16; c += 4) {
                             float2 d[2];
@@ -765,9 +768,9 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
                                     if (col + 1 >= valid) u.y = ds.y = 0.0f;
                                 }
                                 if (MODE == ATTN_DQ && DIRECT && sums) {
-                                    wd = __fadd2_rn(wd, ds);
-                                    wa = __ffma2_rn(ds, d[e], wa);
-                                    we = __ffma2_rn(u, d[e], we);
+                                    td = __fadd2_rn(td, ds);
+                                    ta = __ffma2_rn(ds, d[e], ta);
+                                    te = __ffma2_rn(u, d[e], te);
                                 }
                                 if (DKV) split_bf16(u, p[i / 2], plo[i / 2]);
                                 if (TWO)
@@ -775,6 +778,11 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
                                 else
                                     q[i / 2] = pack_bf16(ds.x, ds.y);
                             }
+                        }
+                        if (MODE == ATTN_DQ && DIRECT && sums) {
+                            wd = __fadd2_rn(wd, td);
+                            wa = __fadd2_rn(wa, ta);
+                            we = __fadd2_rn(we, te);
                         }
                         if (DKV) {
                             tmem_st8(sb + 16 * h, p);

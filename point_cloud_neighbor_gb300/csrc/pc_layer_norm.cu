@@ -6,10 +6,10 @@
 //   dx = rstd (g - mean(g) - xhat mean(g xhat)),
 //   dw = sum_rows dy xhat,  db = sum_rows dy.
 //
-// Bound: memory.  A row is read once by TPR threads (8 for
-// C <= 128, a warp up to C of about 1000, a block of 256 beyond) and written
-// once; the variance is summed from the centred values in registers, so no
-// cancellation of sums of squares.  All sums are float32.
+// Bound: memory.  A row is read once by TPR threads (8 for C <= 128, a warp up
+// to C of about 1000, a block of 256 beyond) and written once; the variance is
+// summed from the centred values in registers, so no cancellation of sums of
+// squares.  All sums are float32.
 //
 // Rows of an odd C start at any multiple of the element size, yet the rows
 // together are one packed array.  A thread group takes every G-th row, G a
