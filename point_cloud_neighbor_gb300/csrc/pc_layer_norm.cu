@@ -20,7 +20,7 @@
 // columns' gradient sums stay in registers.
 //
 // The weight gradients need a sum over all rows.  Each backward block walks
-// its share of the rows with the columns' sums in registers, joins its groups
+// its share of the rows with the columns' sums in registers, adds its groups'
 // in a fixed order and writes one row of partial sums; a second kernel adds
 // the blocks' rows in a fixed order.  No atomics: the result does not change
 // from run to run.
@@ -29,11 +29,11 @@
 // slots in shared memory, up to 4 rows deep, by asynchronous copies; a slot is
 // written and read by one thread alone, so there is nothing to wait for but the
 // thread's own copies.  Blocks are small (128 threads) and fill the registers.
-// Measured, 100,000 x 512 float32: forward 74 us (5.5 TB/s), backward 111 us
-// (5.5 TB/s); C = 515: 75 and 125 us (with the next row in registers 85 and
-// 147 us, with one element a load 158 and 368 us); 65,536 x 1024 bfloat16: 52
-// us (5.2 TB/s) and 100 us (4.0 TB/s; registers 60 and 102 us); 100,000 x 515
-// bfloat16: 76 and 149 us (registers 78 and 136 us), bound by instructions.
+// Measured, 100,000 x 512 float32: forward 73 us (5.6 TB/s), backward 108 us
+// (5.7 TB/s); C = 515: 76 and 121 us (with the next row in registers 85 and
+// 147 us, with one element a load 158 and 368 us); 65,536 x 1024 bfloat16: 50
+// us (5.4 TB/s) and 84 us (4.8 TB/s; registers 60 and 102 us); 100,000 x 515
+// bfloat16: 76 and 96 us (registers 78 and 136 us), bound by instructions.
 #include "pc_internal.h"
 #include "pc_vec.cuh"
 #include "pointcloud.h"
@@ -262,7 +262,6 @@ __global__ void __launch_bounds__(ln_threads(TPR)) ln_backward_kernel(const LnAr
     __shared__ float red[THREADS / 32];
     using R = Ring<T, V, N, TPR, 2>;
     extern __shared__ __align__(16) unsigned char ring[];
-    float *colsum = reinterpret_cast<float *>(ring);  // [2][C] after the last row
     const int t = threadIdx.x % TPR;
     const int64_t step = int64_t(gridDim.x) * RPB, total = a.rows * a.C;
     int64_t row = int64_t(blockIdx.x) * RPB + threadIdx.x / TPR;
@@ -351,23 +350,28 @@ __global__ void __launch_bounds__(ln_threads(TPR)) ln_backward_kernel(const LnAr
     if (a.part == nullptr) return;
     float *part = a.part + size_t(blockIdx.x) * 2 * a.C;
     if (RPB > 1) {
+        // the groups' sums side by side in the ring, then a thread a column
         __syncthreads();  // (the ring's last groups of copies are empty)
-        // join the block's groups, one after the other
-        for (int g = 0; g < RPB; ++g) {
-            if (int(threadIdx.x / TPR) == g)
+        constexpr int ROW = V * N * TPR, S = V == 1 ? 1 : 4;
+        float *sums = reinterpret_cast<float *>(ring);  // [RPB][2][ROW]
+        float *mine = sums + (threadIdx.x / TPR) * 2 * ROW + t * V;
 #pragma unroll
-                for (int i = 0; i < N; ++i)
+        for (int i = 0; i < N; ++i)
 #pragma unroll
-                    for (int e = 0; e < V; ++e) {
-                        const int n = c.col(i) + e;
-                        if (n >= 0 && n < a.C) {
-                            colsum[n] = g == 0 ? dw[i][e] : colsum[n] + dw[i][e];
-                            colsum[a.C + n] = g == 0 ? db[i][e] : colsum[a.C + n] + db[i][e];
-                        }
-                    }
-            __syncthreads();
+            for (int e = 0; e < V; e += S) {
+                Vec<float, S>::store(mine + i * TPR * V + e, dw[i] + e);
+                Vec<float, S>::store(mine + ROW + i * TPR * V + e, db[i] + e);
+            }
+        __syncthreads();
+        for (int n = threadIdx.x; n < 2 * a.C; n += THREADS) {
+            const float *p = sums + (n < a.C ? n : ROW + n - a.C);
+            const int64_t first = int64_t(blockIdx.x) * RPB;
+            float s = 0.0f;
+#pragma unroll
+            for (int g = 0; g < RPB; ++g)
+                s += p[g * 2 * ROW + (V > 1 ? int((first + g) * a.C % V) : 0)];
+            part[n] = s;
         }
-        for (int n = threadIdx.x; n < 2 * a.C; n += THREADS) part[n] = colsum[n];
     } else {
 #pragma unroll
         for (int i = 0; i < N; ++i)
@@ -417,7 +421,7 @@ cudaError_t ln_launch(LnArgs a, LnLaunch &l) {
     constexpr int THREADS = ln_threads(TPR), RPB = THREADS / TPR;
     const int64_t want = (a.rows + RPB - 1) / RPB;
     constexpr int FORWARD = Ring<T, V, N, TPR, 1>::BYTES;
-    constexpr int SUMS = RPB > 1 ? 2 * 4 * V * N * TPR : 0;  // [2][C], C at most V N TPR
+    constexpr int SUMS = RPB > 1 ? RPB * 2 * 4 * V * N * TPR : 0;  // of the block's groups
     constexpr int RING2 = Ring<T, V, N, TPR, 2>::BYTES, BACKWARD = RING2 > SUMS ? RING2 : SUMS;
     // As many blocks as are resident together; a multiple of 8 where a group
     // takes several rows, so that the rows of a group are a multiple of V apart.
