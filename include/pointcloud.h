@@ -562,6 +562,9 @@ int pc_rotary(const void *q, const void *k, int dtype, int64_t B, int64_t L, int
  *   out_lse    [B, H, Lq] float32 or NULL: log sum_j exp(z_ij), -inf for the
  *              rows that are 0 by the rule above.
  *
+ * Values that are not finite are not hidden: a NaN in a valid row or key, and a
+ * row whose scores overflow, give NaN in the outputs and gradients they enter.
+ *
  * pc_attention_backward takes the same arguments with out and lse of the
  * forward call and grad_out [B, Lq, H, D] (packed), and writes grad_q,
  * grad_k, grad_v (packed, of dtype; 0 past the lengths) and, if not NULL,

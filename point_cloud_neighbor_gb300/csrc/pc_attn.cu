@@ -306,8 +306,8 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
             }
             continue;
         }
-        const float f = MODE == ATTN_FWD ? (r < nx && sum[i] > 0.0f ? 1.0f / sum[i] : 0.0f)
-                                         : (r < nx ? a.scale : 0.0f);
+        const bool any = r < nx && (MODE != ATTN_FWD || ny > 0);
+        const float f = MODE == ATTN_FWD ? 1.0f / sum[i] : a.scale;
         T *o1 = static_cast<T *>(MODE == ATTN_FWD  ? a.out
                                  : MODE == ATTN_DQ ? a.dq
                                                    : a.dk) + orow * a.D;
@@ -316,7 +316,7 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
         for (int e = 0; e < DP / 16; ++e) {
             const int c = 64 * (e / 4) + 4 * tx + e % 4;
             if (c < a.D) {
-                const float w = r < nx ? acc[i][e] * f : 0.0f;
+                const float w = any ? acc[i][e] * f : 0.0f;
                 Vec<T, 1>::store(o1 + c, &w);
                 if (MODE == ATTN_DKV) {
                     const float u = r < nx ? acc2[i][e] : 0.0f;
@@ -325,8 +325,7 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
             }
         }
         if (MODE == ATTN_FWD && tx == 0 && a.lse != nullptr)
-            a.lse[hrow] = r < nx && sum[i] > 0.0f
-                              ? (mx[i] + log2f(sum[i])) * ATTN_LN2 : -INFINITY;
+            a.lse[hrow] = any ? (mx[i] + log2f(sum[i])) * ATTN_LN2 : -INFINITY;
     }
 }
 
@@ -392,7 +391,6 @@ __global__ void __launch_bounds__(256) attn_join_forward_kernel(const AttnArgs a
 #pragma unroll 4
     for (int s = 0; s < a.nsplit; ++s) m = fmaxf(m, ml[int64_t(s) * 2 * rows]);
     const float base = m == -INFINITY ? 0.0f : m;
-    const bool valid = i < attn_len(a.qlen, int(b), a.Lq);
     float l = 0.0f, v[V] = {};
 #pragma unroll 4
     for (int s = 0; s < a.nsplit; ++s) {
@@ -403,7 +401,7 @@ __global__ void __launch_bounds__(256) attn_join_forward_kernel(const AttnArgs a
 #pragma unroll
         for (int e = 0; e < V; ++e) v[e] = fmaf(w, p[e], v[e]);
     }
-    const bool any = valid && l > 0.0f;
+    const bool any = attn_row_has_keys(a, int(b), i);
     const float f = 1.0f / l;
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] = any ? v[e] * f : 0.0f;
@@ -465,7 +463,7 @@ __global__ void __launch_bounds__(1024) attn_join_rows_kernel(const AttnArgs a) 
         const float w = mine ? exp2f(mt - base) : 0.0f;
         if (t < 256) wt[t] = w;
         const float l = over(mine ? w * ml[rows] : 0.0f, false);
-        const bool any = i < attn_len(a.qlen, int(b), a.Lq) && l > 0.0f;
+        const bool any = attn_row_has_keys(a, int(b), i);
         if (any) f = 1.0f / l;
         if (t == 0 && a.lse != nullptr)
             a.lse[hrow] = any ? (m + log2f(l)) * ATTN_LN2 : -INFINITY;

@@ -58,6 +58,13 @@ __device__ __forceinline__ int attn_len(const int64_t *len, int b, int L) {
     return n < 0 ? 0 : n > L ? L : int(n);
 }
 
+// Whether a query row has anything to attend to, which the lengths alone decide:
+// its sum of weights may be NaN (a NaN in a valid row or key, a score that
+// overflowed), and that is what the row then shows.
+__device__ __forceinline__ bool attn_row_has_keys(const AttnArgs &a, int b, int i) {
+    return i < attn_len(a.qlen, b, a.Lq) && attn_len(a.rlen, b, a.Lk) > 0;
+}
+
 // Rows a block keeps in the tensor-core kernels, and rows of a streamed tile.
 constexpr int attn_tc_rows(int mode) { return mode == ATTN_FWD ? 256 : 128; }
 constexpr int ATTN_TC_TILE = 64;

@@ -208,7 +208,7 @@ few_forward_kernel(const AttnArgs a) {
         }
         const int64_t orow = (int64_t(w.b) * a.Lq + i) * a.H + h;
         const int64_t hrow = (int64_t(w.b) * a.H + h) * a.Lq + i;
-        const bool any = i < w.nq && s > 0.0f;
+        const bool any = i < w.nq && w.nk > 0;
         if (a.nsplit > 1) {
             a.part[(int64_t(w.split) * hrows + orow) * a.D + c] = v;
             if (c == 0) {
@@ -238,6 +238,7 @@ few_backward_kernel(const AttnArgs a) {
     const float c2 = a.scale * ATTN_LOG2E;
     // q times scale: the scores need it, and so do the keys' gradients
     float q[R][V], go[R][V], px[R][3], ws[R], lse2[R], del[R], dq[R][V], wa[R], we[R], wd[R];
+    unsigned live = 0;  // a bit a row: the others take no part, whatever the keys hold
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         const int g = r / a.Lq, i = r - g * a.Lq, h = w.hk * G + g;
@@ -256,6 +257,7 @@ few_backward_kernel(const AttnArgs a) {
         }
         if (in) {
             const int64_t at = (int64_t(w.b) * a.H + h) * a.Lq + i;
+            live |= 1u << r;
             lse2[r] = a.lse2[at], del[r] = a.delta[at];
             if (bias) {
                 const float *p = a.qxyz + (int64_t(w.b) * a.Lq + i) * 3;
@@ -310,8 +312,9 @@ few_backward_kernel(const AttnArgs a) {
                     d2 = fmaf(dz, dz, fmaf(dy, dy, dx * dx));
                     z = fmaf(d2, -ws[r], z);
                 }
-                const float p = in ? ex2(z - lse2[r]) : 0.0f;
-                const float ds = p * (dp - del[r]);
+                const bool on = in && (live >> r & 1);
+                const float p = on ? ex2(z - lse2[r]) : 0.0f;
+                const float ds = on ? p * (dp - del[r]) : 0.0f;
                 wa[r] = fmaf(ds, d2, wa[r]);
                 we[r] = fmaf(p, d2, we[r]);
                 wd[r] += ds;
@@ -325,7 +328,10 @@ few_backward_kernel(const AttnArgs a) {
             if (at[u] < w.j1 && chan) {
                 const int64_t o = ((int64_t(w.b) * a.Lk + at[u]) * a.Hkv + w.hk) * a.D + c0;
 #pragma unroll
-                for (int e = 0; e < V; ++e) dk[e] *= a.scale;
+                for (int e = 0; e < V; ++e) {
+                    dk[e] = in ? dk[e] * a.scale : 0.0f;
+                    dv[e] = in ? dv[e] : 0.0f;
+                }
                 Vec<T, V>::store(static_cast<T *>(a.dk) + o, dk);
                 Vec<T, V>::store(static_cast<T *>(a.dv) + o, dv);
             }
@@ -359,6 +365,7 @@ few_backward_kernel(const AttnArgs a) {
         float v = 0.0f;
 #pragma unroll
         for (int k = 0; k < FEW_WARPS; ++k) v += sm[k][r][c < a.D ? c : LPK * V + c - a.D];
+        if (i >= w.nq) v = 0.0f;  // (weights of 0, but keys that may be NaN)
         const int64_t orow = (int64_t(w.b) * a.Lq + i) * a.H + h;
         const int64_t hrow = (int64_t(w.b) * a.H + h) * a.Lq + i;
         if (c >= a.D) {

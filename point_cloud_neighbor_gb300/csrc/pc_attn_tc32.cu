@@ -603,7 +603,7 @@ __device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMap
             named_barrier_sync(1, C::CWARPS * 32);
             l = rd[4 * XR] + rd[5 * XR];
         }
-        const bool any = FWD ? row < nx && l > 0.0f : row < nx;
+        const bool any = row < nx && (!FWD || ny > 0);
         if (FWD && row < LX && half == 0) {
             if (a.nsplit > 1) {
                 a.part_ml[int64_t(split) * 2 * hrows + hrow] = mc;

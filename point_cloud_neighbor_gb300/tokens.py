@@ -224,7 +224,8 @@ def pc_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
     [B, Lq, H, D], k and v [B, Lk, Hkv, D] (last axis contiguous, others of
     any stride), Hkv divides H.  slopes [H], query_xyz [B, Lq, 3] and ref_xyz
     [B, Lk, 3] are float32, all given or none.  Rows past
-    ``query_lengths[b]`` and rows without keys are 0 (lse -inf).
+    ``query_lengths[b]`` and rows without keys are 0 (lse -inf); a NaN in a
+    valid row or key gives NaN in the rows it enters.
     """
     index, qkv, args = _attention_args(q, k, v, scale, query_xyz, ref_xyz, slopes,
                                        query_lengths, ref_lengths)
