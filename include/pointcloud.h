@@ -577,8 +577,8 @@ int pc_rotary(const void *q, const void *k, int dtype, int64_t B, int64_t L, int
  * element, channels rounded up to 8).
  *
  * bfloat16 with D a multiple of 8 and 16-byte aligned rows and strides, and
- * float32, run on the tensor cores; other bfloat16 layouts run in float32
- * instructions.  The tensor-core kernels bound their device-side waits: if
+ * float32 with B below 2^31 / 3, run on the tensor cores; other layouts run in
+ * float32 instructions.  The tensor-core kernels bound their device-side waits: if
  * one runs out the block's outputs are unspecified and the device status
  * word holds PC_ERR_DEVICE_TIMEOUT.
  *

@@ -601,7 +601,8 @@ int pick_split(int64_t slots, int64_t base, int64_t items, int64_t part_floats, 
 
 // Which kernels run a pass: few queries, tensor cores (bfloat16), tensor cores
 // in three parts (float32), or float32 instructions (what is left: bfloat16
-// rows that are not 16-byte aligned, and sides without rows).
+// rows that are not 16-byte aligned, sides without rows, and float32 with more
+// clouds than three planes each are numbered in 32 bits).
 enum AttnPath { PATH_FEW, PATH_TC, PATH_PARTS, PATH_SIMT };
 
 template <class T>

@@ -741,7 +741,10 @@ cudaError_t tc32_backward(const AttnArgs &dkv, unsigned first, const AttnArgs &d
 
 }  // namespace
 
-bool attn_tc32_fits(const AttnArgs &a) { return a.Lq >= 1 && a.Lk >= 1; }
+// (the planes of the parts, 3 B of them, are numbered in 32 bits)
+bool attn_tc32_fits(const AttnArgs &a) {
+    return a.Lq >= 1 && a.Lk >= 1 && a.B <= 0x7fffffff / 3;
+}
 
 int attn_tc32_rows(const AttnArgs &a, int mode) {
     return mode != ATTN_FWD && a.D > 64 ? 64 : XR;

@@ -99,3 +99,16 @@ def test_attention_rows_without_keys_are_zeros_among_rows_that_are_nan(B, Lq, Lk
     assert not any(t[:2].any() for t in grads[:3])
     assert not grads[0][2, Lq - 1:].any()
     assert not grads[1][2, 1:].any() and not grads[2][2, 1:].any()
+
+
+# --- more clouds than an index of three parts holds -----------------------------------
+
+def test_attention_more_clouds_than_a_third_of_2_31():
+    # float32 on the tensor cores numbers 3 B planes in 32 bits; past that the other kernels run
+    B = 2 ** 31 // 3 + 2
+    q = torch.zeros(B, 1, 1, 1, device=DEV)
+    v = torch.zeros(B, 1, 1, 1, device=DEV)
+    v[-3:, 0, 0, 0] = torch.tensor([1.5, -2.0, 7.0], device=DEV)
+    v[:3, 0, 0, 0] = torch.tensor([3.0, 0.25, -1.0], device=DEV)
+    out = pc.pc_attention(q, q, v)   # one key: its value
+    assert torch.equal(out, v)
