@@ -30,10 +30,9 @@
 // Both operands of a product have one type, and P in bfloat16 alone would cost
 // up to 2^-8 of a term (the output's and dv's error against float64 0.0024
 // instead of 0.0017, which is the rounding of the result): P is written as the
-// sum of two bfloat16 (2^-17) and multiplied twice.  So is dS where one side has
-// at most 512 rows, whose few terms do not average out; beyond, one
-// bfloat16 gives dq and dk 0.0024 and saves 11 to 15% of the backward pass.  The sums
-// of P, the statistics and all accumulators are float32, and the slopes'
+// sum of two bfloat16 (2^-17) and multiplied twice.  So is dS: in one bfloat16,
+// at any number of rows, dq and dk would be off by 0.0024 too (it would save 11 to
+// 15% of the backward pass).  The sums of P, the statistics and all accumulators are float32, and the slopes'
 // gradient uses the unrounded weights.
 //
 // What lies past a cloud's length is masked in the weights; rows of a
@@ -61,7 +60,6 @@ namespace pcn {
 namespace {
 
 constexpr float AUG_MOST = 256.0f;  // of slope R^2: see above
-constexpr int ATTN_TWO_S = 512;     // rows of a side up to which dS has two parts
 
 struct AttnMaps {
     CUtensorMap q, k, v, go;
@@ -153,7 +151,7 @@ __device__ __forceinline__ void store_row32(float *p, const float (&v)[32], int 
 }
 
 // One pass of block `bid`.
-template <int MODE, int DP, bool BIAS, bool TWO>
+template <int MODE, int DP, bool BIAS>
 __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &maps,
                                              const bool withhold, const unsigned bid) {
     using C = Cfg<MODE, DP>;
@@ -541,7 +539,7 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
                         mma_ts<SMEM_128B>(acc, at + 8, d2 + i * step, id, true);
                     } else {
                         mma_ts<SMEM_128B>(acc, as, d1 + i * step, id, more);
-                        if (TWO) mma_ts<SMEM_128B>(acc, as + 8, d1 + i * step, id, true);
+                        mma_ts<SMEM_128B>(acc, as + 8, d1 + i * step, id, true);
                     }
                     if (DKV) {
                         mma_ts<SMEM_128B>(acc + DP, at, d2 + i * step, id, more);
@@ -773,10 +771,7 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
                                     te = __ffma2_rn(u, d[e], te);
                                 }
                                 if (DKV) split_bf16(u, p[i / 2], plo[i / 2]);
-                                if (TWO)
-                                    split_bf16(ds, q[i / 2], qlo[i / 2]);
-                                else
-                                    q[i / 2] = pack_bf16(ds.x, ds.y);
+                                split_bf16(ds, q[i / 2], qlo[i / 2]);
                             }
                         }
                         if (MODE == ATTN_DQ && DIRECT && sums) {
@@ -789,7 +784,7 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
                             tmem_st8(sb + 16 * h + 8, plo);
                         }
                         tmem_st8(sb + YR + 16 * h, q);
-                        if (TWO) tmem_st8(sb + YR + 16 * h + 8, qlo);
+                        tmem_st8(sb + YR + 16 * h + 8, qlo);
                     }
                 };
                 constexpr std::true_type yes{};
@@ -891,20 +886,20 @@ template <int DP, bool BIAS>
 __global__ void __launch_bounds__(Cfg<ATTN_FWD, DP>::THREADS, 1)
 attn_tc_forward_kernel(const __grid_constant__ AttnArgs a, const __grid_constant__ AttnMaps maps,
                        const bool withhold) {
-    attn_tc_pass<ATTN_FWD, DP, BIAS, false>(a, maps, withhold, blockIdx.x);
+    attn_tc_pass<ATTN_FWD, DP, BIAS>(a, maps, withhold, blockIdx.x);
 }
 
 // Both backward passes in one launch, the keys' first: their blocks are fewer
 // and longer, and the queries' fill what they leave of the GPU.
-template <int DP, bool BIAS, bool TWO>
+template <int DP, bool BIAS>
 __global__ void __launch_bounds__(Cfg<ATTN_DQ, DP>::THREADS, 1)
 attn_tc_backward_kernel(const __grid_constant__ AttnArgs dkv, const __grid_constant__ AttnArgs dq,
                         const __grid_constant__ AttnMaps maps, const unsigned first,
                         const bool withhold) {
     if (blockIdx.x < first)
-        attn_tc_pass<ATTN_DKV, DP, BIAS, TWO>(dkv, maps, withhold, blockIdx.x);
+        attn_tc_pass<ATTN_DKV, DP, BIAS>(dkv, maps, withhold, blockIdx.x);
     else
-        attn_tc_pass<ATTN_DQ, DP, BIAS, TWO>(dq, maps, withhold, blockIdx.x - first);
+        attn_tc_pass<ATTN_DQ, DP, BIAS>(dq, maps, withhold, blockIdx.x - first);
 }
 
 bool tc_maps(const AttnArgs &a, bool backward, AttnMaps &m) {
@@ -930,7 +925,7 @@ cudaError_t tc_forward(const AttnArgs &a, unsigned blocks, cudaStream_t st) {
     return cudaGetLastError();
 }
 
-template <int DP, bool BIAS, bool TWO>
+template <int DP, bool BIAS>
 cudaError_t tc_backward(const AttnArgs &dkv, unsigned first, const AttnArgs &dq, unsigned second,
                         cudaStream_t st) {
     using C = Cfg<ATTN_DQ, DP>;
@@ -940,9 +935,9 @@ cudaError_t tc_backward(const AttnArgs &dkv, unsigned first, const AttnArgs &dq,
     AttnMaps m{};
     if (!tc_maps(dq, true, m)) return cudaErrorInvalidValue;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e = allow_smem(attn_tc_backward_kernel<DP, BIAS, TWO>, smem, dq.device, done);
+    const cudaError_t e = allow_smem(attn_tc_backward_kernel<DP, BIAS>, smem, dq.device, done);
     if (e != cudaSuccess) return e;
-    attn_tc_backward_kernel<DP, BIAS, TWO>
+    attn_tc_backward_kernel<DP, BIAS>
         <<<first + second, C::THREADS, smem, st>>>(dkv, dq, m, first, withheld());
     return cudaGetLastError();
 }
@@ -971,21 +966,13 @@ cudaError_t launch_attn_tc_forward(const AttnArgs &a, unsigned blocks, cudaStrea
     return a.slopes ? tc_forward<128, true>(a, blocks, st) : tc_forward<128, false>(a, blocks, st);
 }
 
-template <int DP, bool BIAS>
-static cudaError_t pick_two(const AttnArgs &dkv, unsigned first, const AttnArgs &dq,
-                            unsigned second, cudaStream_t st) {
-    return dq.Lq <= ATTN_TWO_S || dq.Lk <= ATTN_TWO_S
-               ? tc_backward<DP, BIAS, true>(dkv, first, dq, second, st)
-               : tc_backward<DP, BIAS, false>(dkv, first, dq, second, st);
-}
-
 cudaError_t launch_attn_tc_backward(const AttnArgs &dkv, unsigned first, const AttnArgs &dq,
                                     unsigned second, cudaStream_t st) {
     if (dq.D <= 64)
-        return dq.slopes ? pick_two<64, true>(dkv, first, dq, second, st)
-                         : pick_two<64, false>(dkv, first, dq, second, st);
-    return dq.slopes ? pick_two<128, true>(dkv, first, dq, second, st)
-                     : pick_two<128, false>(dkv, first, dq, second, st);
+        return dq.slopes ? tc_backward<64, true>(dkv, first, dq, second, st)
+                         : tc_backward<64, false>(dkv, first, dq, second, st);
+    return dq.slopes ? tc_backward<128, true>(dkv, first, dq, second, st)
+                     : tc_backward<128, false>(dkv, first, dq, second, st);
 }
 
 }  // namespace pcn

@@ -112,3 +112,56 @@ def test_attention_more_clouds_than_a_third_of_2_31():
     v[:3, 0, 0, 0] = torch.tensor([3.0, 0.25, -1.0], device=DEV)
     out = pc.pc_attention(q, q, v)   # one key: its value
     assert torch.equal(out, v)
+
+
+# --- bits of the weights' gradients ---------------------------------------------------
+
+def gradients64(q, k, v, do, kw):
+    """dq, dk, dv, dslopes in float64, no lengths."""
+    B, Lq, H, D = q.shape
+    Hkv = k.shape[2]
+    G = H // Hkv
+    s = 1 / math.sqrt(D)
+    dq, dk, dv = (torch.zeros(t.shape, dtype=torch.float64, device=DEV) for t in (q, k, v))
+    ds = torch.zeros(H, dtype=torch.float64, device=DEV)
+    for b in range(B):
+        d2 = 0.0
+        if "slopes" in kw:
+            x, y = kw["query_xyz"][b].double(), kw["ref_xyz"][b].double()
+            d2 = ((x[:, None] - y[None]) ** 2).sum(-1)
+        for h in range(H):
+            Q, K, V, g = q[b, :, h].double(), k[b, :, h // G].double(), v[b, :, h // G].double(), \
+                do[b, :, h].double()
+            z = s * Q @ K.T
+            if "slopes" in kw:
+                z = z - kw["slopes"][h].double() * d2
+            P = torch.softmax(z, 1)
+            dP = g @ V.T
+            dS = P * (dP - (P * dP).sum(1, keepdim=True))
+            dq[b, :, h] = s * dS @ K
+            dk[b, :, h // G] += s * dS.T @ Q
+            dv[b, :, h // G] += P.T @ g
+            ds[h] = ds[h] - (dS * d2).sum()
+    return dq, dk, dv, ds
+
+
+def norm_error(got, want):
+    return float((got.double() - want).norm() / want.norm())
+
+
+@pytest.mark.parametrize("bias", [True, False])
+@pytest.mark.parametrize("Lq,Lk,H,Hkv,D", [(1024, 1024, 4, 2, 64), (600, 700, 2, 1, 40),
+                                           (520, 2000, 2, 2, 128), (1500, 513, 2, 1, 96),
+                                           (2048, 2048, 2, 2, 64)])
+def test_attention_gradients_are_as_exact_as_their_type(Lq, Lk, H, Hkv, D, bias):
+    # A result rounded once to bfloat16 is off by 2^-8 / sqrt(3) of its binade, which for
+    # normally distributed values is 0.0017 of the norm.  Weights of 8 bits in the sums would add
+    # 0.0017 again (0.0024 together); with 16 bits and a flat softmax (delta's error averages
+    # out, as the outputs are small) at most a tenth is added.
+    q, k, v, do, kw = attn_inputs(1, Lq, Lk, H, Hkv, D, torch.bfloat16, bias, None, None)
+    if bias:
+        kw["slopes"] = 0.05 * kw["slopes"]
+    out, lse = pc.pc_attention(q, k, v, return_lse=True, **kw)
+    got = pc.pc_attention_backward(do, q, k, v, out, lse, **kw)
+    for t, w in zip(got[:3], gradients64(q, k, v, do, kw)):
+        assert norm_error(t, w) <= 0.0019
