@@ -570,6 +570,16 @@ int pc_rotary(const void *q, const void *k, int dtype, int64_t B, int64_t L, int
  * grad_k, grad_v (packed, of dtype; 0 past the lengths) and, if not NULL,
  * grad_slopes [H] float32.  The positions get no gradient.
  *
+ * The _ex calls take out_low too ([B, Lq, H, D] bfloat16, or NULL; bfloat16
+ * calls only): the forward call writes there what rounding out to bfloat16 left,
+ * the backward call reads it.  The backward pass needs
+ * delta_i = out_i . grad_out_i, and subtracts it from numbers of its own size:
+ * with out_low it is that of the output before its rounding, and the gradients
+ * are rounded once.  Without, it is off by up to 2^-8 |out_i| |grad_out_i|, which
+ * P_ij times reaches dS_ij: little where many keys share a row (the gradients' norm
+ * is off by 0.0017 as a result rounded once at 1024 keys), much where few do
+ * (0.0034 at 16 keys and slopes of 8, 0.6 at 2).
+ *
  * Scratch (the library's stream-ordered pool): the parts of a pass whose
  * streamed side is split among more blocks, at most 1 GiB; in the backward
  * pass 8 bytes, with grad_slopes 12 more per part, per query row and head;
@@ -601,6 +611,24 @@ int pc_attention_backward(const void *grad_out, const void *q, const void *k, co
                           const int64_t *query_lengths, const int64_t *ref_lengths,
                           void *grad_q, void *grad_k, void *grad_v, float *grad_slopes,
                           void *stream);
+
+int pc_attention_ex(const void *q, const void *k, const void *v, int dtype, int64_t B,
+                    int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int64_t D,
+                    const int64_t *q_strides, const int64_t *k_strides,
+                    const int64_t *v_strides, double scale, const float *query_xyz,
+                    const float *ref_xyz, const float *slopes, const int64_t *query_lengths,
+                    const int64_t *ref_lengths, void *out, void *out_low, float *out_lse,
+                    void *stream);
+
+int pc_attention_backward_ex(const void *grad_out, const void *q, const void *k,
+                             const void *v, const void *out, const void *out_low,
+                             const float *lse, int dtype, int64_t B, int64_t Lq, int64_t Lk,
+                             int64_t H, int64_t Hkv, int64_t D, const int64_t *q_strides,
+                             const int64_t *k_strides, const int64_t *v_strides, double scale,
+                             const float *query_xyz, const float *ref_xyz, const float *slopes,
+                             const int64_t *query_lengths, const int64_t *ref_lengths,
+                             void *grad_q, void *grad_k, void *grad_v, float *grad_slopes,
+                             void *stream);
 
 /*
  * Device status word.  Kernels that wait on other thread blocks bound every

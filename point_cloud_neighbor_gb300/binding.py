@@ -86,6 +86,13 @@ _SIGNATURES = {
                                              _I, _I, _I, _I, _I, _P, _P, _P,
                                              ctypes.c_double, _P, _P, _P, _P, _P, _P,
                                              _P, _P, _P, _P]),
+    "pc_attention_ex": (ctypes.c_int, [_P, _P, _P, ctypes.c_int, _I, _I, _I, _I, _I, _I,
+                                       _P, _P, _P, ctypes.c_double, _P, _P, _P, _P, _P,
+                                       _P, _P, _P, _P]),
+    "pc_attention_backward_ex": (ctypes.c_int, [_P, _P, _P, _P, _P, _P, _P, ctypes.c_int,
+                                                _I, _I, _I, _I, _I, _I, _P, _P, _P,
+                                                ctypes.c_double, _P, _P, _P, _P, _P, _P,
+                                                _P, _P, _P, _P]),
     "pc_device_status": (ctypes.c_int, [_P, ctypes.c_int,
                                         ctypes.POINTER(ctypes.c_int32)]),
     "pc_set_wait_timeout_ns": (None, [ctypes.c_uint64]),

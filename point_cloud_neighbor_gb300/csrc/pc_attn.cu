@@ -318,6 +318,10 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
             if (c < a.D) {
                 const float w = any ? acc[i][e] * f : 0.0f;
                 Vec<T, 1>::store(o1 + c, &w);
+                if (MODE == ATTN_FWD && a.low != nullptr) {
+                    const float l = rest<T>(w);
+                    Vec<T, 1>::store(static_cast<T *>(a.low) + orow * a.D + c, &l);
+                }
                 if (MODE == ATTN_DKV) {
                     const float u = r < nx ? acc2[i][e] : 0.0f;
                     Vec<T, 1>::store(o2 + c, &u);
@@ -329,13 +333,13 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
     }
 }
 
-// delta_i = out_i . dout_i, and lse in base-2 units with +inf for rows without
+// delta_i = (out_i + low_i) . dout_i, and lse in base-2 units with +inf for rows without
 // keys (their weights 2^(z - lse2) are then 0): LPR lanes per (token, head), V
 // channels at a time.  (16 x 1024 tokens, 8 heads of 64 in bfloat16: a warp per
 // row and one channel a load 32 us, 8 lanes per row 5 us.)
 template <class T, int V, int LPR>
 __global__ void __launch_bounds__(256)
-attn_delta_kernel(const T *out, const T *go, const float *lse, int64_t rows, int Lq, int H,
+attn_delta_kernel(const T *out, const T *low, const T *go, const float *lse, int64_t rows, int Lq, int H,
                   int D, float *delta, float *lse2) {
     const int64_t row = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LPR;  // (b Lq + i) H + h
     const int lane = threadIdx.x % LPR;
@@ -345,6 +349,12 @@ attn_delta_kernel(const T *out, const T *go, const float *lse, int64_t rows, int
             float o[V], g[V];
             Vec<T, V>::load(out + row * D + c, o);
             Vec<T, V>::load(go + row * D + c, g);
+            if (low != nullptr) {
+                float l[V];
+                Vec<T, V>::load(low + row * D + c, l);
+#pragma unroll
+                for (int e = 0; e < V; ++e) o[e] += l[e];  // (16 bits: exact)
+            }
 #pragma unroll
             for (int e = 0; e < V; ++e) s = fmaf(o[e], g[e], s);
         }
@@ -359,19 +369,19 @@ attn_delta_kernel(const T *out, const T *go, const float *lse, int64_t rows, int
 }
 
 template <class T>
-void launch_delta(const AttnArgs &a, const T *out, int64_t rows, float *delta, float *lse2,
-                  cudaStream_t st) {
+void launch_delta(const AttnArgs &a, const T *out, const T *low, int64_t rows, float *delta,
+                  float *lse2, cudaStream_t st) {
     const T *go = static_cast<const T *>(a.go);
     constexpr int W = 16 / sizeof(T);
-    const bool wide = a.D % W == 0 && reinterpret_cast<uintptr_t>(out) % 16 == 0 &&
-                      reinterpret_cast<uintptr_t>(go) % 16 == 0;
+    auto aligned = [](const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+    const bool wide = a.D % W == 0 && aligned(out) && aligned(low) && aligned(go);
     const unsigned g8 = unsigned((rows * 8 + 255) / 256), g32 = unsigned((rows * 32 + 255) / 256);
     if (wide)
-        attn_delta_kernel<T, W, 8><<<g8, 256, 0, st>>>(out, go, a.lse, rows, a.Lq, a.H, a.D,
-                                                       delta, lse2);
+        attn_delta_kernel<T, W, 8><<<g8, 256, 0, st>>>(out, low, go, a.lse, rows, a.Lq, a.H,
+                                                       a.D, delta, lse2);
     else
-        attn_delta_kernel<T, 1, 32><<<g32, 256, 0, st>>>(out, go, a.lse, rows, a.Lq, a.H, a.D,
-                                                         delta, lse2);
+        attn_delta_kernel<T, 1, 32><<<g32, 256, 0, st>>>(out, low, go, a.lse, rows, a.Lq, a.H,
+                                                         a.D, delta, lse2);
 }
 
 // Joins the parts of a split forward pass: a thread per V channels of a row.
@@ -406,6 +416,11 @@ __global__ void __launch_bounds__(256) attn_join_forward_kernel(const AttnArgs a
 #pragma unroll
     for (int e = 0; e < V; ++e) v[e] = any ? v[e] * f : 0.0f;
     Vec<T, V>::store(static_cast<T *>(a.out) + row * a.D + c, v);
+    if (a.low != nullptr) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[e] = rest<T>(v[e]);
+        Vec<T, V>::store(static_cast<T *>(a.low) + row * a.D + c, v);
+    }
     if (c == 0 && a.lse != nullptr)
         a.lse[hrow] = any ? (m + log2f(l)) * ATTN_LN2 : -INFINITY;
 }
@@ -489,6 +504,10 @@ __global__ void __launch_bounds__(1024) attn_join_rows_kernel(const AttnArgs a) 
         for (int u = 1; u < K; ++u) v += part[u * C + c];
         v = f == 0.0f ? 0.0f : v * f;
         Vec<T, 1>::store(static_cast<T *>(FWD ? a.out : a.dq) + row * a.D + c, &v);
+        if (FWD && a.low != nullptr) {
+            v = rest<T>(v);
+            Vec<T, 1>::store(static_cast<T *>(a.low) + row * a.D + c, &v);
+        }
     }
 }
 
@@ -673,8 +692,8 @@ void finish_pass(Pass &p, AttnPath path, float *dslopes, cudaStream_t st) {
             else
                 attn_join_rows_kernel<T, false><<<unsigned(p.rows), 1024, 0, st>>>(a);
             a.nsplit = 1;  // for the slopes' sums
-        } else if (a.D % 4 == 0 && aligned(a.out) && aligned(a.dq) && aligned(a.dk) &&
-                   aligned(a.dv)) {
+        } else if (a.D % 4 == 0 && aligned(a.out) && aligned(a.low) && aligned(a.dq) &&
+                   aligned(a.dk) && aligned(a.dv)) {
             launch_join<T, 4>(a, p.mode, p.rows, st);
         } else {
             launch_join<T, 1>(a, p.mode, p.rows, st);
@@ -714,8 +733,8 @@ cudaError_t run_forward(const DeviceInfo &dev, const AttnArgs &a, cudaStream_t s
 }
 
 template <class T>
-cudaError_t run_backward(const DeviceInfo &dev, AttnArgs a, const void *out, float *dslopes,
-                         cudaStream_t st) {
+cudaError_t run_backward(const DeviceInfo &dev, AttnArgs a, const void *out, const void *low,
+                         float *dslopes, cudaStream_t st) {
     const int64_t rows = int64_t(a.B) * a.Lq * a.H, keys = int64_t(a.B) * a.Lk * a.Hkv;
     const bool slopes = dslopes != nullptr && a.slopes != nullptr;
     if (rows == 0) {  // no queries: the keys' gradients are 0
@@ -740,7 +759,8 @@ cudaError_t run_backward(const DeviceInfo &dev, AttnArgs a, const void *out, flo
     dq.a.lse2 = dkv.a.lse2 = delta + rows;
     place_pass(dq, space);
     place_pass(dkv, space + dq.floats);
-    launch_delta<T>(a, static_cast<const T *>(out), rows, delta, delta + rows, st);
+    launch_delta<T>(a, static_cast<const T *>(out), static_cast<const T *>(low), rows, delta,
+                    delta + rows, st);
     const unsigned nq = unsigned(dq.blocks), nk = unsigned(dkv.blocks);
     if (path == PATH_FEW) {
         e = launch_attn_few(dq.a, sizeof(T), true, st);
@@ -842,17 +862,33 @@ extern "C" int pc_attention(const void *q, const void *k, const void *v, int dty
                             const float *ref_xyz, const float *slopes,
                             const int64_t *query_lengths, const int64_t *ref_lengths,
                             void *out, float *out_lse, void *stream) {
+    return pc_attention_ex(q, k, v, dtype, B, Lq, Lk, H, Hkv, D, q_strides, k_strides, v_strides,
+                           scale, query_xyz, ref_xyz, slopes, query_lengths, ref_lengths, out,
+                           nullptr, out_lse, stream);
+}
+
+extern "C" int pc_attention_ex(const void *q, const void *k, const void *v, int dtype, int64_t B,
+                               int64_t Lq, int64_t Lk, int64_t H, int64_t Hkv, int64_t D,
+                               const int64_t *q_strides, const int64_t *k_strides,
+                               const int64_t *v_strides, double scale, const float *query_xyz,
+                               const float *ref_xyz, const float *slopes,
+                               const int64_t *query_lengths, const int64_t *ref_lengths,
+                               void *out, void *out_low, float *out_lse, void *stream) {
     using namespace pcn;
     AttnArgs a{};
     const DeviceInfo *dev = nullptr;
     int rc = attn_check("attention", a, &dev, q, k, v, dtype, B, Lq, Lk, H, Hkv, D, q_strides,
                         k_strides, v_strides, scale, query_xyz, ref_xyz, slopes, query_lengths,
                         ref_lengths);
-    if (rc != PC_OK || dev == nullptr || Lq == 0) return rc;
+    if (rc != PC_OK) return rc;
+    if (out_low != nullptr && dtype != PC_BF16)
+        return api_fail(PC_ERR_INVALID_ARGUMENT, "attention: out_low is of a bfloat16 output");
+    if (dev == nullptr || Lq == 0) return PC_OK;
     const int d = dev->device;
     if ((rc = api_check_ptr(out, d, dtype == PC_F32 ? 4 : 2, "out")) != PC_OK) return rc;
+    if (out_low && (rc = api_check_ptr(out_low, d, 2, "out_low")) != PC_OK) return rc;
     if (out_lse && (rc = api_check_ptr(out_lse, d, 4, "out_lse")) != PC_OK) return rc;
-    a.out = out, a.lse = out_lse;
+    a.out = out, a.low = out_low, a.lse = out_lse;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     const cudaError_t e = dtype == PC_F32 ? run_forward<float>(*dev, a, st)
                                           : run_forward<bf16>(*dev, a, st);
@@ -866,6 +902,19 @@ extern "C" int pc_attention_backward(
     double scale, const float *query_xyz, const float *ref_xyz, const float *slopes,
     const int64_t *query_lengths, const int64_t *ref_lengths, void *grad_q, void *grad_k,
     void *grad_v, float *grad_slopes, void *stream) {
+    return pc_attention_backward_ex(grad_out, q, k, v, out, nullptr, lse, dtype, B, Lq, Lk, H,
+                                    Hkv, D, q_strides, k_strides, v_strides, scale, query_xyz,
+                                    ref_xyz, slopes, query_lengths, ref_lengths, grad_q, grad_k,
+                                    grad_v, grad_slopes, stream);
+}
+
+extern "C" int pc_attention_backward_ex(
+    const void *grad_out, const void *q, const void *k, const void *v, const void *out,
+    const void *out_low, const float *lse, int dtype, int64_t B, int64_t Lq, int64_t Lk,
+    int64_t H, int64_t Hkv, int64_t D, const int64_t *q_strides, const int64_t *k_strides,
+    const int64_t *v_strides, double scale, const float *query_xyz, const float *ref_xyz,
+    const float *slopes, const int64_t *query_lengths, const int64_t *ref_lengths, void *grad_q,
+    void *grad_k, void *grad_v, float *grad_slopes, void *stream) {
     using namespace pcn;
     AttnArgs a{};
     const DeviceInfo *dev = nullptr;
@@ -875,6 +924,9 @@ extern "C" int pc_attention_backward(
     if (rc != PC_OK) return rc;
     if (grad_slopes != nullptr && slopes == nullptr)
         return api_fail(PC_ERR_INVALID_ARGUMENT, "attention_backward: grad_slopes without slopes");
+    if (out_low != nullptr && dtype != PC_BF16)
+        return api_fail(PC_ERR_INVALID_ARGUMENT,
+                        "attention_backward: out_low is of a bfloat16 output");
     if (dev == nullptr) {  // an empty problem: only the slopes' gradient can have elements
         if (grad_slopes == nullptr || H == 0) return PC_OK;
         if ((rc = api_current_device(&dev)) != PC_OK) return rc;
@@ -888,6 +940,7 @@ extern "C" int pc_attention_backward(
     if (Lq > 0) {
         if ((rc = api_check_ptr(grad_out, d, es, "grad_out")) != PC_OK) return rc;
         if ((rc = api_check_ptr(out, d, es, "out")) != PC_OK) return rc;
+        if (out_low && (rc = api_check_ptr(out_low, d, 2, "out_low")) != PC_OK) return rc;
         if ((rc = api_check_ptr(lse, d, 4, "lse")) != PC_OK) return rc;
         if ((rc = api_check_ptr(grad_q, d, es, "grad_q")) != PC_OK) return rc;
     }
@@ -900,7 +953,8 @@ extern "C" int pc_attention_backward(
     a.go = grad_out, a.lse = const_cast<float *>(lse);
     a.dq = grad_q, a.dk = grad_k, a.dv = grad_v;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
-    const cudaError_t e = dtype == PC_F32 ? run_backward<float>(*dev, a, out, grad_slopes, st)
-                                          : run_backward<bf16>(*dev, a, out, grad_slopes, st);
+    const cudaError_t e = dtype == PC_F32
+                              ? run_backward<float>(*dev, a, out, nullptr, grad_slopes, st)
+                              : run_backward<bf16>(*dev, a, out, out_low, grad_slopes, st);
     return attn_cuda("attention_backward", e);
 }

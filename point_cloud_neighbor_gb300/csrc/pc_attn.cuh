@@ -3,7 +3,7 @@
 //
 //   z_ij = scale q_i.k_j - slope_h |x_i - y_j|^2,  j < ref_length,
 //   P = softmax_j(z), out = P v, lse_i = log sum_j exp(z_ij);
-//   delta_i = out_i . dout_i, dP = dout v^T, dS = P (dP - delta),
+//   delta_i = out_i . dout_i = sum_j P_ij dP_ij, dP = dout v^T, dS = P (dP - delta),
 //   dq = scale dS k, dk = scale dS^T q, dv = P^T dout,
 //   dslope_h = -sum_ij dS_ij |x_i - y_j|^2.
 //
@@ -15,6 +15,13 @@
 //                                        query heads that share the key head.
 // The backward pass forms the scores twice instead of adding into dq with
 // atomics, so the order of every sum is fixed.
+//
+// delta takes the output before its rounding.  Where P has few large weights
+// dP is near delta and dS = P (dP - delta) small: half a unit of a bfloat16 output
+// is then as large as dS itself (dq off by 0.0034 of its norm at 16 keys with slopes
+// of 8, by 0.6 at 2, where a result rounded once has 0.0017).  So a forward pass
+// can write what the rounding left as a second bfloat16 array, `low`, for 2 bytes
+// an element, and delta adds it.
 #pragma once
 
 #include "pc_internal.h"
@@ -37,6 +44,7 @@ struct AttnArgs {
     int B, Lq, Lk, H, Hkv, D;
     float scale;
     void *out;                              // FWD
+    void *low;                              // FWD: what rounding out to bfloat16 left, or NULL
     float *lse;                             // FWD: written if not NULL
     const float *delta, *lse2;              // backward: [B, H, Lq], see attn_delta_kernel
     void *dq, *dk, *dv;

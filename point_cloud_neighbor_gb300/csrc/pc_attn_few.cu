@@ -218,6 +218,10 @@ few_forward_kernel(const AttnArgs a) {
         } else {
             v = any ? v / s : 0.0f;
             Vec<T, 1>::store(static_cast<T *>(a.out) + orow * a.D + c, &v);
+            if (a.low != nullptr) {
+                v = rest<T>(v);
+                Vec<T, 1>::store(static_cast<T *>(a.low) + orow * a.D + c, &v);
+            }
             if (c == 0 && a.lse != nullptr)
                 a.lse[hrow] = any ? (mn + log2f(s)) * ATTN_LN2 : -INFINITY;
         }

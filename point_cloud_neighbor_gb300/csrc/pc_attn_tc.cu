@@ -873,6 +873,11 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
             } else {
                 void *o = FWD ? a.out : MODE == ATTN_DQ ? a.dq : acc ? a.dv : a.dk;
                 store_row32(static_cast<bf16 *>(o) + orow * a.D + c0, v, c0, a.D);
+                if (FWD && a.low != nullptr) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = rest<bf16>(v[e]);
+                    store_row32(static_cast<bf16 *>(a.low) + orow * a.D + c0, v, c0, a.D);
+                }
             }
         }
         tc_fence_before();
@@ -956,7 +961,7 @@ bool attn_tc_fits(const AttnArgs &a, int mode) {
     if (!fits(a.q, a.qs, a.Lq, a.H) || !fits(a.k, a.ks, a.Lk, a.Hkv) ||
         !fits(a.v, a.vs, a.Lk, a.Hkv))
         return false;
-    if (mode == ATTN_FWD) return aligned(a.out);
+    if (mode == ATTN_FWD) return aligned(a.out) && aligned(a.low);
     return aligned(a.go) && aligned(a.dq) && aligned(a.dk) && aligned(a.dv);
 }
 

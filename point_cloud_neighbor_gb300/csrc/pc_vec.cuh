@@ -111,6 +111,18 @@ struct Vec<bf16, 8> {
     }
 };
 
+// What rounding v to T leaves: v is T(v) + rest<T>(v).
+template <class T>
+__device__ __forceinline__ float rest(float v);
+template <>
+__device__ __forceinline__ float rest<float>(float) {
+    return 0.0f;
+}
+template <>
+__device__ __forceinline__ float rest<bf16>(float v) {
+    return v - __bfloat162float(__float2bfloat16_rn(v));
+}
+
 // Unsigned division by a divisor fixed per launch: n / d for n < 2^31 as one
 // high product and a shift.  m = floor(2^32 (2^s - d) / d) + 1 with
 // 2^(s-1) < d <= 2^s (the round-up method of Granlund and Montgomery).

@@ -216,8 +216,10 @@ def pc_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
                  scale: float | None = None, query_xyz: torch.Tensor | None = None,
                  ref_xyz: torch.Tensor | None = None, slopes: torch.Tensor | None = None,
                  query_lengths: torch.Tensor | None = None,
-                 ref_lengths: torch.Tensor | None = None, return_lse: bool = False):
-    """Attention over point tokens: out [B, Lq, H, D], or (out, lse [B, H, Lq]).
+                 ref_lengths: torch.Tensor | None = None, return_lse: bool = False,
+                 return_low: bool = False):
+    """Attention over point tokens: out [B, Lq, H, D], or (out, lse [B, H, Lq]),
+    or (out, lse, low).
 
     z_ij = scale q_i.k_j - slopes[h] |query_xyz_i - ref_xyz_j|^2 over the
     first ``ref_lengths[b]`` keys; ``scale`` is 1 / sqrt(D) by default.  q
@@ -226,16 +228,25 @@ def pc_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
     [B, Lk, 3] are float32, all given or none.  Rows past
     ``query_lengths[b]`` and rows without keys are 0 (lse -inf); a NaN in a
     valid row or key gives NaN in the rows it enters.
+
+    ``return_low`` (with ``return_lse``): what rounding the output to bfloat16
+    left, [B, Lq, H, D] bfloat16, for the backward call; None in float32.
     """
     index, qkv, args = _attention_args(q, k, v, scale, query_xyz, ref_xyz, slopes,
                                        query_lengths, ref_lengths)
     B, Lq, H, D = q.shape
+    if return_low and not return_lse:
+        raise ValueError("return_low goes with return_lse")
     out = torch.empty((B, Lq, H, D), dtype=q.dtype, device=q.device)
-    lse = None
+    lse = low = None
     if return_lse:
         lse = torch.empty((B, H, Lq), dtype=torch.float32, device=q.device)
-    _run("pc_attention", lib().pc_attention, index, *qkv, *args, out.data_ptr(),
-         _ptr_or_none(lse))
+    if return_low and q.dtype is torch.bfloat16:
+        low = torch.empty((B, Lq, H, D), dtype=q.dtype, device=q.device)
+    _run("pc_attention", lib().pc_attention_ex, index, *qkv, *args, out.data_ptr(),
+         _ptr_or_none(low), _ptr_or_none(lse))
+    if return_low:
+        return out, lse, low
     return (out, lse) if return_lse else out
 
 
@@ -247,10 +258,17 @@ def pc_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tens
                           slopes: torch.Tensor | None = None,
                           query_lengths: torch.Tensor | None = None,
                           ref_lengths: torch.Tensor | None = None,
-                          need_slopes: bool = True):
+                          need_slopes: bool = True,
+                          out_low: torch.Tensor | None = None):
     """Gradients of :func:`pc_attention` from its ``out`` and ``lse``: (grad_q,
     grad_k, grad_v, grad_slopes), the last None without slopes or with
-    ``need_slopes=False``.  The positions get no gradient."""
+    ``need_slopes=False``.  The positions get no gradient.
+
+    In bfloat16 ``out_low``, the forward call's ``low``, keeps the gradients as
+    exact as their type.  Without it they are formed from the rounded output,
+    whose error (2^-8 of |out| |grad_out|) stays in them: little where a row
+    has many keys of weight, much where it has few.
+    """
     index, qkv, args = _attention_args(q, k, v, scale, query_xyz, ref_xyz, slopes,
                                        query_lengths, ref_lengths)
     B, Lq, H, D = shape = q.shape
@@ -258,12 +276,16 @@ def pc_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tens
     _same(grad_out, "grad_out", shape, dtype, index)
     _same(out, "out", shape, dtype, index)
     _same(lse, "lse", (B, H, Lq), torch.float32, index)
+    if out_low is not None:
+        if dtype is not torch.bfloat16:
+            raise ValueError("out_low belongs to bfloat16 outputs")
+        _same(out_low, "out_low", shape, dtype, index)
     dq = torch.empty(shape, dtype=dtype, device=dev)
     dk = torch.empty(k.shape, dtype=dtype, device=dev)
     dv = torch.empty(v.shape, dtype=dtype, device=dev)
     ds = torch.empty_like(slopes) if slopes is not None and need_slopes else None
-    _run("pc_attention_backward", lib().pc_attention_backward, index, grad_out.data_ptr(), *qkv,
-         out.data_ptr(), lse.data_ptr(), *args, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+    _run("pc_attention_backward", lib().pc_attention_backward_ex, index, grad_out.data_ptr(),
+         *qkv, out.data_ptr(), _ptr_or_none(out_low), lse.data_ptr(), *args, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
          _ptr_or_none(ds))
     return dq, dk, dv, ds
 
@@ -314,21 +336,22 @@ def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
 class _Attention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, slopes, scale, query_xyz, ref_xyz, query_lengths, ref_lengths):
-        out, lse = pc_attention(q, k, v, scale=scale, query_xyz=query_xyz, ref_xyz=ref_xyz,
-                                slopes=slopes, query_lengths=query_lengths,
-                                ref_lengths=ref_lengths, return_lse=True)
-        ctx.save_for_backward(q, k, v, out, lse, slopes, query_xyz, ref_xyz, query_lengths,
+        out, lse, low = pc_attention(q, k, v, scale=scale, query_xyz=query_xyz,
+                                     ref_xyz=ref_xyz, slopes=slopes,
+                                     query_lengths=query_lengths, ref_lengths=ref_lengths,
+                                     return_lse=True, return_low=True)
+        ctx.save_for_backward(q, k, v, out, lse, low, slopes, query_xyz, ref_xyz, query_lengths,
                               ref_lengths)
         ctx.scale = scale
         return out
 
     @staticmethod
     def backward(ctx, g):
-        q, k, v, out, lse, slopes, qx, rx, ql, rl = ctx.saved_tensors
+        q, k, v, out, lse, low, slopes, qx, rx, ql, rl = ctx.saved_tensors
         dq, dk, dv, ds = pc_attention_backward(
             g.contiguous(), q, k, v, out, lse, scale=ctx.scale, query_xyz=qx, ref_xyz=rx,
             slopes=slopes, query_lengths=ql, ref_lengths=rl,
-            need_slopes=ctx.needs_input_grad[3])
+            need_slopes=ctx.needs_input_grad[3], out_low=low)
         return dq, dk, dv, ds, None, None, None, None, None
 
 

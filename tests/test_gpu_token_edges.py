@@ -165,3 +165,64 @@ def test_attention_gradients_are_as_exact_as_their_type(Lq, Lk, H, Hkv, D, bias)
     got = pc.pc_attention_backward(do, q, k, v, out, lse, **kw)
     for t, w in zip(got[:3], gradients64(q, k, v, do, kw)):
         assert norm_error(t, w) <= 0.0019
+
+
+# Few keys, or a steep bias: a row's delta is near its largest dP, and what the rounding of the
+# output does to it stays in dS whole.
+PEAKED = [(8, 2, 2, 4, 2, 64), (4, 16, 16, 4, 4, 64), (2, 64, 64, 4, 2, 64), (2, 65, 33, 2, 1, 36),
+          (1, 300, 300, 2, 2, 128), (2, 1, 40, 4, 2, 64), (1, 3, 5000, 2, 2, 128),
+          (1, 600, 2000, 1, 1, 64), (1, 40, 2000, 1, 1, 36)]
+
+
+@pytest.mark.parametrize("steep", [0.0, 4.0, 60.0])
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D", PEAKED)
+def test_attention_delta_keeps_the_output_s_low_part(B, Lq, Lk, H, Hkv, D, steep):
+    q, k, v, do, kw = attn_inputs(B, Lq, Lk, H, Hkv, D, torch.bfloat16, True, None, None)
+    kw["slopes"] = torch.full((H,), steep, device=DEV)
+    out, lse, low = pc.pc_attention(q, k, v, return_lse=True, return_low=True, **kw)
+    got = pc.pc_attention_backward(do, q, k, v, out, lse, out_low=low, **kw)
+    ts = [t.clone().requires_grad_() for t in (q, k, v, kw["slopes"])]
+    pos = {n: t for n, t in kw.items() if n != "slopes"}
+    pc.attention(*ts[:3], slopes=ts[3], **pos).backward(do)
+    assert all(torch.equal(t.grad, g) for t, g in zip(ts, got))
+    # float32's bounds, and: the weights' two parts (2^-16 twice), the bias through the products
+    # (2^-20 slope R^2 of a score, at most 2^-20 * 256), what out + low leaves of the output
+    ref = Ref(q, k, v, do, 1 / math.sqrt(D), kw, torch.float32)
+    s, P = 1 / math.sqrt(D), 2.0 ** -16
+    for b in range(B):
+        R2 = float(torch.cat([kw["query_xyz"][b], kw["ref_xyz"][b]]).double().norm(dim=1).max()) ** 2 * 4
+        ez = 2 * min(steep * R2, 256.0) * 2.0 ** -20
+        for h in range(H):
+            kh = h // (H // Hkv)
+            Q, K, V, g = (t.double() for t in (q[b, :, h], k[b, :, kh], v[b, :, kh], do[b, :, h]))
+            d2 = ((kw["query_xyz"][b].double()[:, None] - kw["ref_xyz"][b].double()[None]) ** 2).sum(-1)
+            W = torch.softmax(s * Q @ K.T - steep * d2, 1)
+            eO = (ez + 2 * P) * (W @ V.abs())
+            dS = W * (g @ V.T - (W * (g @ V.T)).sum(1, keepdim=True))
+            edl = ((eO + 2 * P * ref.out[b, :, h].abs()) * g.abs()).sum(1, keepdim=True)
+            eS = W * edl + (ez + P) * dS.abs()
+            ref.eout[b, :, h] += eO
+            ref.edq[b, :, h] += s * eS @ K.abs()
+            ref.edk[b, :, kh] += s * eS.T @ Q.abs()
+            ref.edv[b, :, kh] += (ez + P) * W.T @ g.abs()
+    close(out.double() + low.double(), ref.out, 4 * ref.eout + P * ref.out.abs() + 1e-30, "out + low")
+    assert (low.abs().double() <= HALF[torch.bfloat16] * out.abs().double() + 1e-30).all()
+    half = HALF[torch.bfloat16]
+    # (the tensor cores' sums round with up to 4 units a step where float32's bounds have 1)
+    for t, w, err, name in ((got[0], ref.dq, ref.edq, "dq"), (got[1], ref.dk, ref.edk, "dk"),
+                            (got[2], ref.dv, ref.edv, "dv")):
+        close(t, w, 4 * err + half * w.abs() + 1e-30, name)
+
+
+def test_attention_low_part_refusals():
+    q = torch.zeros(1, 4, 2, 64, device=DEV)
+    with pytest.raises(ValueError, match="return_lse"):
+        pc.pc_attention(q, q, q, return_low=True)
+    out, lse, low = pc.pc_attention(q, q, q, return_lse=True, return_low=True)
+    assert low is None      # a float32 output has none
+    with pytest.raises(ValueError, match="out_low"):
+        pc.pc_attention_backward(q, q, q, q, out, lse, out_low=q)
+    b = q.bfloat16()
+    out, lse, low = pc.pc_attention(b, b, b, return_lse=True, return_low=True)
+    with pytest.raises(ValueError, match="out_low"):
+        pc.pc_attention_backward(b, b, b, b, out, lse, out_low=low[:, :2])
