@@ -226,3 +226,28 @@ def test_attention_low_part_refusals():
     out, lse, low = pc.pc_attention(b, b, b, return_lse=True, return_low=True)
     with pytest.raises(ValueError, match="out_low"):
         pc.pc_attention_backward(b, b, b, b, out, lse, out_low=low[:, :2])
+
+
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D", PEAKED[1:])
+def test_attention_delta_in_norm(B, Lq, Lk, H, Hkv, D):
+    # A result rounded once is off by at most 2^-8 / sqrt(3) of its binade in the mean square (and
+    # that at its binade's lower end).  What 16 bits of the weights and of the output leave in dS is
+    # 2^-16 of P (|out| |dout| + |dP|), at most; the rounded output would leave 2^-9 of it.
+    q, k, v, do, kw = attn_inputs(B, Lq, Lk, H, Hkv, D, torch.bfloat16, True, None, None)
+    kw["slopes"] = torch.full((H,), 3.0, device=DEV)
+    out, lse, low = pc.pc_attention(q, k, v, return_lse=True, return_low=True, **kw)
+    got = pc.pc_attention_backward(do, q, k, v, out, lse, out_low=low, **kw)
+    want = gradients64(q, k, v, do, kw)
+    s, P = 1 / math.sqrt(D), 2.0 ** -16
+    edq, edk = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    for b in range(B):
+        d2 = torch.cdist(kw["query_xyz"][b].double(), kw["ref_xyz"][b].double()) ** 2
+        for h in range(H):
+            kh = h // (H // Hkv)
+            Q, K, V, g = (t.double() for t in (q[b, :, h], k[b, :, kh], v[b, :, kh], do[b, :, h]))
+            W = torch.softmax(s * Q @ K.T - 3.0 * d2, 1)
+            eS = P * W * ((W @ V * g).abs().sum(1, keepdim=True) + (g @ V.T).abs())
+            edq[b, :, h] = s * eS @ K.abs()
+            edk[b, :, kh] += s * eS.T @ Q.abs()
+    for t, w, e in zip(got, want, (edq, edk)):
+        assert float((t.double() - w).norm()) <= 2.0 ** -8 / math.sqrt(3) * float(w.norm()) + float(e.norm())
