@@ -162,13 +162,14 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
         }
     }
     float acc[4][DP / 16], acc2[4][DP / 16];
-    float mx[4], sum[4], wa[4], we[4], wd[4];
+    float mx[4], sum[4];
+    LongSum wa[4], we[4], wd[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
         for (int e = 0; e < DP / 16; ++e) acc[i][e] = acc2[i][e] = 0.0f;
         mx[i] = -INFINITY;
-        sum[i] = wa[i] = we[i] = wd[i] = 0.0f;
+        sum[i] = 0.0f;
     }
 
     const int nyt = (ny + SB - 1) / SB;
@@ -240,20 +241,23 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int i = 0; i < 4; ++i) {
+                float ta = 0.0f, te = 0.0f, td = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int c = tx + 16 * j;
                     const float p = exp2f(s[i][j] - (MODE == ATTN_DKV ? ylse[c] : lse2[i]));
                     const float ds = p * (dp[i][j] - (MODE == ATTN_DKV ? ydel[c] : del[i]));
                     if (MODE == ATTN_DQ && bias) {
-                        wa[i] = fmaf(ds, d2[i][j], wa[i]);
-                        we[i] = fmaf(p, d2[i][j], we[i]);
-                        wd[i] += ds;
+                        ta = fmaf(ds, d2[i][j], ta);
+                        te = fmaf(p, d2[i][j], te);
+                        td += ds;
                     }
                     if (MODE == ATTN_DKV) P[(ty + 16 * i) * SP + c] = p;
                     S[(ty + 16 * i) * SP + c] = ds;
                 }
+                if (MODE == ATTN_DQ && bias) wa[i].add(ta), we[i].add(te), wd[i].add(td);
+            }
         }
         __syncthreads();
         if (MODE == ATTN_FWD) {
@@ -274,16 +278,17 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
             for (int o = 8; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
         }
         if (MODE == ATTN_DQ && bias) {
+            float ta = wa[i].value(), te = we[i].value(), td = wd[i].value();
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) {
-                wa[i] += __shfl_xor_sync(0xffffffffu, wa[i], o);
-                we[i] += __shfl_xor_sync(0xffffffffu, we[i], o);
-                wd[i] += __shfl_xor_sync(0xffffffffu, wd[i], o);
+                ta += __shfl_xor_sync(0xffffffffu, ta, o);
+                te += __shfl_xor_sync(0xffffffffu, te, o);
+                td += __shfl_xor_sync(0xffffffffu, td, o);
             }
             if (tx == 0 && r < LX && a.rowsum != nullptr) {
                 const int64_t n = int64_t(a.B) * a.H * a.Lq;
                 float *w = a.rowsum + split * 3 * n + hrow;
-                w[0] = wa[i], w[n] = we[i], w[2 * n] = wd[i];
+                w[0] = ta, w[n] = te, w[2 * n] = td;
             }
         }
         if (r >= LX) continue;
@@ -534,18 +539,20 @@ attn_slope_kernel(const AttnArgs a, int tiles, float *dslopes) {
     const int h = blockIdx.x;
     const int64_t n = int64_t(a.B) * a.H * a.Lq;
     double t = 0.0;
-    if (tiles > 0)
+    if (tiles > 0) {
         for (int64_t r = threadIdx.x; r < int64_t(a.B) * tiles; r += 1024)
             t += double(a.rowsum[(r / tiles * a.H + h) * tiles + r % tiles]);
-    else
-      for (int64_t r = threadIdx.x; r < int64_t(a.B) * a.Lq; r += 1024) {
-        const int64_t b = r / a.Lq, at = (b * a.H + h) * a.Lq + (r - b * a.Lq);
-        float wa = 0.0f, we = 0.0f, wd = 0.0f;
-        for (int s = 0; s < a.nsplit; ++s) {
-            const float *w = a.rowsum + int64_t(s) * 3 * n + at;
-            wa += w[0], we += w[n], wd += w[2 * n];
+    } else {
+        for (int64_t r = threadIdx.x; r < int64_t(a.B) * a.Lq; r += 1024) {
+            const int64_t b = r / a.Lq, at = (b * a.H + h) * a.Lq + (r - b * a.Lq);
+            double wa = 0.0, we = 0.0, wd = 0.0;
+#pragma unroll 2  // (further, and the loads' registers spill)
+            for (int s = 0; s < a.nsplit; ++s) {
+                const float *w = a.rowsum + int64_t(s) * 3 * n + at;
+                wa += w[0], we += w[n], wd += w[2 * n];
+            }
+            t += wa - wd * we;
         }
-        t += double(fmaf(-wd, we, wa));
     }
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
     if (threadIdx.x % 32 == 0) red[threadIdx.x / 32] = t;

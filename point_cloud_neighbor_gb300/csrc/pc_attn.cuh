@@ -52,7 +52,8 @@ struct AttnArgs {
     int nsplit;
     float *part;     // [nsplit][rows of the output][D] (DKV: dk, then dv)
     float *part_ml;  // FWD: [nsplit][2][B H Lq] (maximum in base-2 units, sum)
-    // DQ with slopes: per row sums of dS d2, P d2 and dS, [nsplit][3][B H Lq]; or
+    // DQ with slopes: per row sums of dS d2, P d2 and dS, [nsplit][3][B H Lq], each
+    // a LongSum of a few columns' sums; or
     // (tensor cores, one part) one number a block, [B H][tiles]
     float *rowsum;
     int device;
@@ -65,6 +66,20 @@ __device__ __forceinline__ int attn_len(const int64_t *len, int b, int L) {
     const int64_t n = len[b];
     return n < 0 ? 0 : n > L ? L : int(n);
 }
+
+// A float32 sum of any length: what an addition rounds away is taken from the next
+// number (Kahan's sum: off by 2 units of the sum of magnitudes, whatever the
+// length).  For the slopes' gradient, whose terms are as many as pairs: a plain chain
+// over 131,072 keys was off by 2^-13 of it.
+struct LongSum {
+    float s = 0.0f, over = 0.0f;
+    __device__ __forceinline__ void add(float v) {
+        const float y = v - over, t = s + y;
+        over = (t - s) - y;
+        s = t;
+    }
+    __device__ __forceinline__ float value() const { return s; }
+};
 
 // Whether a query row has anything to attend to, which the lengths alone decide:
 // its sum of weights may be NaN (a NaN in a valid row or key, a score that

@@ -241,7 +241,8 @@ few_backward_kernel(const AttnArgs a) {
     const int G = a.H / a.Hkv, rows = G * a.Lq;
     const float c2 = a.scale * ATTN_LOG2E;
     // q times scale: the scores need it, and so do the keys' gradients
-    float q[R][V], go[R][V], px[R][3], ws[R], lse2[R], del[R], dq[R][V], wa[R], we[R], wd[R];
+    float q[R][V], go[R][V], px[R][3], ws[R], lse2[R], del[R], dq[R][V];
+    LongSum wa[R], we[R], wd[R];
     unsigned live = 0;  // a bit a row: the others take no part, whatever the keys hold
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -249,7 +250,7 @@ few_backward_kernel(const AttnArgs a) {
         const bool in = r < rows && i < w.nq;
 #pragma unroll
         for (int e = 0; e < V; ++e) q[r][e] = go[r][e] = dq[r][e] = 0.0f;
-        ws[r] = px[r][0] = px[r][1] = px[r][2] = del[r] = wa[r] = we[r] = wd[r] = 0.0f;
+        ws[r] = px[r][0] = px[r][1] = px[r][2] = del[r] = 0.0f;
         lse2[r] = INFINITY;
         if (in && chan) {
             Vec<T, V>::load(static_cast<const T *>(a.q) + w.b * a.qs[0] + i * a.qs[1] +
@@ -319,9 +320,9 @@ few_backward_kernel(const AttnArgs a) {
                 const bool on = in && (live >> r & 1);
                 const float p = on ? ex2(z - lse2[r]) : 0.0f;
                 const float ds = on ? p * (dp - del[r]) : 0.0f;
-                wa[r] = fmaf(ds, d2, wa[r]);
-                we[r] = fmaf(p, d2, we[r]);
-                wd[r] += ds;
+                wa[r].add(ds * d2);
+                we[r].add(p * d2);
+                wd[r].add(ds);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     dq[r][e] = fmaf(ds, kx[e], dq[r][e]);
@@ -343,11 +344,12 @@ few_backward_kernel(const AttnArgs a) {
     }
 #pragma unroll
     for (int r = 0; r < R; ++r) {
+        float ta = wa[r].value(), te = we[r].value(), td = wd[r].value();
 #pragma unroll
         for (int o = LPK; o < 32; o <<= 1) {
-            wa[r] += __shfl_xor_sync(0xffffffffu, wa[r], o);
-            we[r] += __shfl_xor_sync(0xffffffffu, we[r], o);
-            wd[r] += __shfl_xor_sync(0xffffffffu, wd[r], o);
+            ta += __shfl_xor_sync(0xffffffffu, ta, o);
+            te += __shfl_xor_sync(0xffffffffu, te, o);
+            td += __shfl_xor_sync(0xffffffffu, td, o);
 #pragma unroll
             for (int e = 0; e < V; ++e) dq[r][e] += __shfl_xor_sync(0xffffffffu, dq[r][e], o);
         }
@@ -355,9 +357,9 @@ few_backward_kernel(const AttnArgs a) {
 #pragma unroll
             for (int e = 0; e < V; ++e) sm[warp][r][c0 + e] = dq[r][e];
         if (lane == 0) {
-            sm[warp][r][LPK * V] = wa[r];
-            sm[warp][r][LPK * V + 1] = we[r];
-            sm[warp][r][LPK * V + 2] = wd[r];
+            sm[warp][r][LPK * V] = ta;
+            sm[warp][r][LPK * V + 1] = te;
+            sm[warp][r][LPK * V + 2] = td;
         }
     }
     __syncthreads();

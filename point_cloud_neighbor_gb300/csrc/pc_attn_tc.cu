@@ -627,7 +627,7 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
         }
         float mc = -INFINITY;                        // FWD: the row's maximum, base 2
         float2 l2 = make_float2(0.0f, 0.0f);         // FWD: the row's sum
-        float2 wa = l2, we = l2, wd = l2;            // DQ: the slope's sums
+        LongSum wa, we, wd;                          // DQ: the slope's sums
         float *rd = rowdata + unit * 6 * XR + quad * 32 + lane;
         bool ok = true;
         int s = FWD ? 0 : unit, sbuf = unit;  // stage; BWD: score buffer
@@ -728,15 +728,13 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
             } else if (BWD && live) {
                 auto weights = [&](auto tail_, auto direct_) {
                     constexpr bool TAIL = decltype(tail_)::value, DIRECT = decltype(direct_)::value;
+                    float2 ta = make_float2(0.0f, 0.0f), te = ta, td = ta;  // of the tile
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t r[16], g[16], p[8], plo[8], q[8], qlo[8];
                         tmem_ld16(sb + 16 * h, r);
                         tmem_ld16(sb + YR + 16 * h, g);
                         tmem_wait_ld();
-                        // sums of 16 columns first: chains as long as a row would
-                        // round away as much as the plain form's error again
-                        float2 ta = make_float2(0.0f, 0.0f), te = ta, td = ta;
 #pragma unroll
                         for (int c = 0; c < 16; c += 4) {
                             float2 d[2];
@@ -774,17 +772,17 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
                                 split_bf16(ds, q[i / 2], qlo[i / 2]);
                             }
                         }
-                        if (MODE == ATTN_DQ && DIRECT && sums) {
-                            wd = __fadd2_rn(wd, td);
-                            wa = __fadd2_rn(wa, ta);
-                            we = __fadd2_rn(we, te);
-                        }
                         if (DKV) {
                             tmem_st8(sb + 16 * h, p);
                             tmem_st8(sb + 16 * h + 8, plo);
                         }
                         tmem_st8(sb + YR + 16 * h, q);
                         tmem_st8(sb + YR + 16 * h + 8, qlo);
+                    }
+                    if (MODE == ATTN_DQ && DIRECT && sums) {
+                        wd.add(td.x + td.y);
+                        wa.add(ta.x + ta.y);
+                        we.add(te.x + te.y);
                     }
                 };
                 constexpr std::true_type yes{};
@@ -815,9 +813,9 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
         if (MODE == ATTN_DQ && BIAS) {
             // the sums of a row's four groups, in the exchange buffer as [unit][half][3]
             if (sums) {
-                rd[(half * 3) * XR] = wa.x + wa.y;
-                rd[(half * 3 + 1) * XR] = we.x + we.y;
-                rd[(half * 3 + 2) * XR] = wd.x + wd.y;
+                rd[(half * 3) * XR] = wa.value();
+                rd[(half * 3 + 1) * XR] = we.value();
+                rd[(half * 3 + 2) * XR] = wd.value();
             }
             named_barrier_sync(1, C::CWARPS * 32);
             if (sums && unit == 0 && half == 0) {

@@ -420,7 +420,8 @@ __device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMap
             ndel = -a.delta[at];
         }
         float mc = -INFINITY;
-        float2 l2 = make_float2(0.0f, 0.0f), wa = l2, we = l2, wd = l2;
+        float2 l2 = make_float2(0.0f, 0.0f);
+        LongSum wa, we, wd;  // DQ: the slope's sums
         const bool sums = MODE == ATTN_DQ && BIAS && a.rowsum != nullptr;
         float *rd = rowdata + quad * 32 + lane;
         float acc[C::NACC][DP / 2];
@@ -514,6 +515,7 @@ __device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMap
                     tmem_st8(sb + 64 + 8 * i, p[2]);
                 }
             } else if (BWD && live) {
+                float2 ta = make_float2(0.0f, 0.0f), te = ta, td = ta;  // of the tile
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int i = 2 * half + h;
@@ -547,9 +549,9 @@ __device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMap
                             if (col >= valid) u.x = ds.x = 0.0f;
                             if (col + 1 >= valid) u.y = ds.y = 0.0f;
                             if (sums) {
-                                wd = __fadd2_rn(wd, ds);
-                                wa = __ffma2_rn(ds, d[e], wa);
-                                we = __ffma2_rn(u, d[e], we);
+                                td = __fadd2_rn(td, ds);
+                                ta = __ffma2_rn(ds, d[e], ta);
+                                te = __ffma2_rn(u, d[e], te);
                             }
                             if (DKV) split3(u, p[0][j / 2], p[1][j / 2], p[2][j / 2]);
                             split3(ds, q[0][j / 2], q[1][j / 2], q[2][j / 2]);
@@ -563,6 +565,11 @@ __device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMap
                     tmem_st8(sb + 64 + 16 * i, q[0]);
                     tmem_st8(sb + 64 + 16 * i + 8, q[1]);
                     tmem_st8(sb + (DKV ? 160 + 8 * i : 16 * i), q[2]);
+                }
+                if (sums) {
+                    wd.add(td.x + td.y);
+                    wa.add(ta.x + ta.y);
+                    we.add(te.x + te.y);
                 }
             }
             // the sums of the tile before leave tensor memory before this
@@ -586,14 +593,13 @@ __device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMap
         float l = l2.x + l2.y;
         if (MODE == ATTN_DQ) {
             if (half == 1) {
-                rd[0] = wa.x + wa.y;
-                rd[XR] = we.x + we.y;
-                rd[2 * XR] = wd.x + wd.y;
+                rd[0] = wa.value();
+                rd[XR] = we.value();
+                rd[2 * XR] = wd.value();
             }
             named_barrier_sync(1, C::CWARPS * 32);
             if (sums && half == 0) {
-                float t[3] = {(wa.x + wa.y) + rd[0], (we.x + we.y) + rd[XR],
-                              (wd.x + wd.y) + rd[2 * XR]};
+                float t[3] = {wa.value() + rd[0], we.value() + rd[XR], wd.value() + rd[2 * XR]};
                 if (row >= nx) t[0] = t[1] = t[2] = 0.0f;
                 put_slope_sums(a, t, split, hrow, row < LX, quad, lane, rowdata + 6 * XR, bid);
             }

@@ -251,3 +251,36 @@ def test_attention_delta_in_norm(B, Lq, Lk, H, Hkv, D):
             edk[b, :, kh] += s * eS.T @ Q.abs()
     for t, w, e in zip(got, want, (edq, edk)):
         assert float((t.double() - w).norm()) <= 2.0 ** -8 / math.sqrt(3) * float(w.norm()) + float(e.norm())
+
+
+# --- long sums -------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype,B,Lq,n,H,Hkv,D", [
+    (torch.float32, 1, 2432, 2 ** 17, 8, 8, 64),     # tensor cores, one part a row
+    (torch.float32, 1, 1216, 2 ** 16, 8, 8, 128),    # 64 rows a block
+    (torch.bfloat16, 1, 2432, 2 ** 17, 8, 8, 64),
+    (torch.bfloat16, 40, 20, 2 ** 15, 8, 1, 36),     # float32 instructions
+    (torch.float32, 152, 1, 2 ** 15, 8, 8, 4),       # few queries
+    (torch.bfloat16, 152, 1, 2 ** 15, 8, 8, 8),
+    (torch.float32, 1, 1, 2 ** 17, 1, 1, 64)])       # many parts
+def test_attention_slopes_gradient_does_not_lose_with_length(dtype, B, Lq, n, H, Hkv, D):
+    # Equal weights 1 / n, one half of the keys at distance^2 c1 with dP = 1, the other at c2 with
+    # dP = -1: a row's sum is (c1 - c2) / 2, of n terms of equal size.  One float32 chain of n / 4 of
+    # them is off by n / 16 units or so, always to the same side.
+    q = torch.zeros(B, Lq, H, D, dtype=dtype, device=DEV)
+    k = torch.zeros(B, n, Hkv, D, dtype=dtype, device=DEV)
+    v, do = torch.zeros_like(k), torch.zeros_like(q)
+    v[:, :n // 2, :, 0], v[:, n // 2:, :, 0], do[..., 0] = 1, -1, 1
+    x, y = torch.zeros(B, Lq, 3, device=DEV), torch.zeros(B, n, 3, device=DEV)
+    y[:, :n // 2, 0], y[:, n // 2:, 1] = 1.1, 0.7
+    kw = dict(slopes=torch.zeros(H, device=DEV), query_xyz=x, ref_xyz=y)
+    out, lse = pc.pc_attention(q, k, v, return_lse=True, **kw)
+    assert not out.any()
+    ds = pc.pc_attention_backward(do, q, k, v, out, lse, **kw)[3]
+    c1, c2 = float(y[0, 0, 0].double() ** 2), float(y[0, -1, 1].double() ** 2)
+    # the weight's exponent log2 n through log, times ln 2 and back, and exp2: the same for all;
+    # a distance 2 roundings, a product 1; chains of 16 or of a tile's 4, joins of 2^8
+    lg = math.log2(n)
+    rel = 4 * U * lg * math.log(2) + 2.0 ** -22 + (2 + 1 + 16 + 8) * U
+    close(ds, torch.full((H,), -B * Lq * (c1 - c2) / 2, dtype=torch.float64, device=DEV),
+          rel * B * Lq * (c1 + c2) / 2, "dslopes")
