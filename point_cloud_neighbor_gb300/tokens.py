@@ -12,6 +12,7 @@ import ctypes
 import math
 
 import torch
+from torch.autograd.function import once_differentiable
 
 from .binding import _check_lengths, _ptr_or_none, _raise_on, lib
 
@@ -292,6 +293,18 @@ def pc_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tens
 
 # --- differentiable forms -----------------------------------------------------------
 
+def _no_gradient(**tensors):
+    """Raise for a tensor that asks for a gradient these operators do not form."""
+    if torch.is_grad_enabled():
+        for name, t in tensors.items():
+            if isinstance(t, torch.Tensor) and t.requires_grad:
+                raise ValueError(f"{name} gets no gradient from this operator: pass "
+                                 f"{name}.detach()")
+
+
+# Layer norm and attention are differentiable once: their gradients come from
+# library calls that autograd does not see, so a second derivative has to raise.
+
 class _LayerNorm(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, eps):
@@ -300,6 +313,7 @@ class _LayerNorm(torch.autograd.Function):
         return y
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         x, weight, bias, mean, rstd = ctx.saved_tensors
         dx, dw, db = pc_layer_norm_backward(g.contiguous(), x, mean, rstd, weight, bias)
@@ -308,29 +322,32 @@ class _LayerNorm(torch.autograd.Function):
 
 def layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
                bias: torch.Tensor | None = None, eps: float = 1e-5) -> torch.Tensor:
-    """Differentiable :func:`pc_layer_norm` (x, weight and bias)."""
+    """Differentiable :func:`pc_layer_norm` (x, weight and bias; once)."""
     return _LayerNorm.apply(x.contiguous(), weight, bias, eps)
 
 
 class _Rotary(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, positions, freqs, interleaved):
+    def forward(ctx, q, k, positions, freqs, interleaved, inverse):
         ctx.save_for_backward(positions, freqs)
-        ctx.interleaved = interleaved
-        return pc_rotary(q, k, positions, freqs, interleaved=interleaved)
+        ctx.interleaved, ctx.inverse = interleaved, inverse
+        return pc_rotary(q, k, positions, freqs, interleaved=interleaved, inverse=inverse)
 
     @staticmethod
     def backward(ctx, gq, gk):
+        # the turn back, itself differentiable
         positions, freqs = ctx.saved_tensors
-        dq, dk = pc_rotary(gq.contiguous(), None if gk is None else gk.contiguous(),
-                           positions, freqs, interleaved=ctx.interleaved, inverse=True)
-        return dq, dk, None, None, None
+        dq, dk = _Rotary.apply(gq.contiguous(), None if gk is None else gk.contiguous(),
+                               positions, freqs, ctx.interleaved, not ctx.inverse)
+        return dq, dk, None, None, None, None
 
 
 def rotary(q: torch.Tensor, k: torch.Tensor | None, positions: torch.Tensor,
            freqs: torch.Tensor, interleaved: bool = True):
-    """Differentiable :func:`pc_rotary` (q and k; not positions, not freqs)."""
-    return _Rotary.apply(q, k, positions, freqs, interleaved)
+    """Differentiable :func:`pc_rotary` (q and k, any number of times; positions
+    and freqs get no gradient and must not ask for one)."""
+    _no_gradient(positions=positions, freqs=freqs)
+    return _Rotary.apply(q, k, positions, freqs, interleaved, False)
 
 
 class _Attention(torch.autograd.Function):
@@ -346,6 +363,7 @@ class _Attention(torch.autograd.Function):
         return out
 
     @staticmethod
+    @once_differentiable
     def backward(ctx, g):
         q, k, v, out, lse, low, slopes, qx, rx, ql, rl = ctx.saved_tensors
         dq, dk, dv, ds = pc_attention_backward(
@@ -360,7 +378,8 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
               ref_xyz: torch.Tensor | None = None, slopes: torch.Tensor | None = None,
               query_lengths: torch.Tensor | None = None,
               ref_lengths: torch.Tensor | None = None) -> torch.Tensor:
-    """Differentiable :func:`pc_attention` (q, k, v and slopes; not the
-    positions)."""
+    """Differentiable :func:`pc_attention` (q, k, v and slopes, once; the
+    positions get no gradient and must not ask for one)."""
+    _no_gradient(query_xyz=query_xyz, ref_xyz=ref_xyz)
     return _Attention.apply(q, k, v, slopes, scale, query_xyz, ref_xyz, query_lengths,
                             ref_lengths)

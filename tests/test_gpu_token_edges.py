@@ -284,3 +284,23 @@ def test_attention_slopes_gradient_does_not_lose_with_length(dtype, B, Lq, n, H,
     rel = 4 * U * lg * math.log(2) + 2.0 ** -22 + (2 + 1 + 16 + 8) * U
     close(ds, torch.full((H,), -B * Lq * (c1 - c2) / 2, dtype=torch.float64, device=DEV),
           rel * B * Lq * (c1 + c2) / 2, "dslopes")
+
+
+# --- second derivatives -------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_second_derivatives_raise_or_are_right(dtype):
+    g = gen(110)
+    x, q = randn(g, 4, 16, dtype=dtype).requires_grad_(), randn(g, 1, 9, 2, 16, dtype=dtype).requires_grad_()
+    for y, at in ((pc.layer_norm(x), x), (pc.attention(q, q, q), q)):
+        d, = torch.autograd.grad(y.square().sum(), at, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            (d.float().square().sum() + at.float().square().sum()).backward()
+    pos, f = randn(g, 1, 9, 3), torch.rand(3, 2, generator=g, device=DEV)
+    d, = torch.autograd.grad(pc.rotary(q, None, pos, f)[0].square().sum(), q, create_graph=True)
+    # |R q|^2 = |q|^2: the gradient is 2 q, its square's 8 q
+    dd, = torch.autograd.grad(d.square().sum(), q)
+    want = 8 * q.detach().double()
+    # four turns, each rounded to the type and 6 units of both channels of a pair
+    size = want.abs() + want.unflatten(-1, (-1, 2)).flip(-1).flatten(-2).abs()
+    close(dd, want, 5 * (HALF[dtype] + 6 * U) * size, "second derivative")

@@ -3,8 +3,9 @@ validation of the C ABI, and the autograd rules over stand-ins of the calls."""
 import ctypes
 
 import pytest
+import torch
 
-from point_cloud_neighbor_gb300 import build
+from point_cloud_neighbor_gb300 import build, tokens
 from point_cloud_neighbor_gb300.binding import lib
 
 FAKE = ctypes.c_void_p(0x1000)   # never read: the checks come first
@@ -29,3 +30,103 @@ def test_the_output_s_low_part_is_bfloat16_s(L):
         assert call(1, FAKE) == 0 and call(0, None) == 0
         assert call(0, FAKE) == 1
         assert "out_low" in L.pc_last_error_message().decode()
+
+
+# --- autograd over stand-ins: as the library's calls, they are hidden from autograd -------
+
+def _turned(x, pos, freqs, inverse):
+    a = (pos[..., None] * freqs).flatten(-2)[:, :, None]
+    R = a.shape[-1]
+    c, s = a.cos(), -a.sin() if inverse else a.sin()
+    u, v = x[..., 0:2 * R:2], x[..., 1:2 * R:2]
+    return torch.cat([torch.stack([u * c - v * s, v * c + u * s], -1).flatten(-2), x[..., 2 * R:]], -1)
+
+
+@pytest.fixture
+def stand_ins(monkeypatch):
+    """float64 restatements of the plain calls on CPU tensors; what was asked of each."""
+    asked = []
+
+    @torch.no_grad()
+    def layer_norm(x, w=None, b=None, eps=1e-5, *, return_stats=False):
+        mean, var = x.mean(-1), x.var(-1, unbiased=False)
+        rstd = (var + eps).rsqrt()
+        y = (x - mean[..., None]) * rstd[..., None]
+        y = y * (1 if w is None else w) + (0 if b is None else b)
+        return (y, mean, rstd) if return_stats else y
+
+    def layer_norm_backward(g, x, mean, rstd, w=None, b=None, **need):
+        asked.append(need)
+        with torch.enable_grad():
+            ts = [t.detach().requires_grad_() for t in (x, w, b) if t is not None]
+            y = torch.nn.functional.layer_norm(ts[0], ts[0].shape[-1:], *ts[1:])
+            grads = list(torch.autograd.grad(y, ts, g.detach()))
+        return tuple(grads + [None] * (3 - len(grads)))
+
+    @torch.no_grad()
+    def rotary(q, k, pos, freqs, *, interleaved=True, inverse=False):
+        asked.append((q is not None, k is not None))
+        return tuple(None if t is None else _turned(t, pos, freqs, inverse) for t in (q, k))
+
+    def scores(q, k, v):
+        p = torch.softmax(torch.einsum("bihd,bjhd->bhij", q, k) / q.shape[-1] ** 0.5, -1)
+        return torch.einsum("bhij,bjhd->bihd", p, v)
+
+    @torch.no_grad()
+    def attention(q, k, v, **kw):
+        return scores(q, k, v), None, None
+
+    def attention_backward(g, q, k, v, out, lse, **kw):
+        asked.append({n: x for n, x in kw.items() if n.startswith("need")})
+        with torch.enable_grad():
+            ts = [t.detach().requires_grad_() for t in (q, k, v)]
+            return (*torch.autograd.grad(scores(*ts), ts, g.detach()), None)
+
+    for name, f in (("pc_layer_norm", layer_norm), ("pc_layer_norm_backward", layer_norm_backward),
+                    ("pc_rotary", rotary), ("pc_attention", attention),
+                    ("pc_attention_backward", attention_backward)):
+        monkeypatch.setattr(tokens, name, f)
+    return asked
+
+
+def _leaf(*shape, seed):
+    g = torch.Generator().manual_seed(seed)
+    return torch.randn(*shape, generator=g, dtype=torch.float64).requires_grad_()
+
+
+def test_second_derivatives_raise(stand_ins):
+    x, w, b = _leaf(3, 8, seed=1), _leaf(8, seed=2), _leaf(8, seed=3)
+    q, k, v = (_leaf(1, 4, 2, 8, seed=i) for i in (4, 5, 6))
+    for y, at in ((tokens.layer_norm(x, w, b), x), (tokens.attention(q, k, v), q)):
+        g, = torch.autograd.grad(y.square().sum(), at, create_graph=True)
+        with pytest.raises(RuntimeError, match="once_differentiable"):
+            (g.square().sum() + at.square().sum()).backward()
+
+
+def test_second_derivatives_of_rotary(stand_ins):
+    q, k = _leaf(1, 5, 2, 8, seed=7), _leaf(1, 5, 1, 8, seed=8)
+    pos, freqs = _leaf(1, 5, 3, seed=9).detach(), _leaf(3, 1, seed=10).detach()
+    results = []
+    for turn in (tokens.rotary, lambda q, k, p, f: (_turned(q, p, f, False), _turned(k, p, f, False))):
+        a, b = turn(q, k, pos, freqs)
+        loss = (a ** 3).sum() + (b ** 2).sum()
+        gq, gk = torch.autograd.grad(loss, (q, k), create_graph=True)
+        results.append(torch.autograd.grad(gq.pow(2).sum() + gk.pow(3).sum(), (q, k)))
+    for got, want in zip(*results):
+        assert torch.allclose(got, want, rtol=1e-12, atol=1e-12)
+    alone, none = tokens.rotary(q, None, pos, freqs)
+    g, = torch.autograd.grad((alone ** 3).sum(), q, create_graph=True)
+    assert none is None and g.requires_grad
+
+
+def test_positions_that_ask_for_a_gradient_are_refused(stand_ins):
+    q, pos, freqs = _leaf(1, 5, 2, 8, seed=7), _leaf(1, 5, 3, seed=9), _leaf(3, 1, seed=10)
+    for args, name in (((pos, freqs.detach()), "positions"), ((pos.detach(), freqs), "freqs")):
+        with pytest.raises(ValueError, match=name):
+            tokens.rotary(q, None, *args)
+    for name in ("query_xyz", "ref_xyz"):
+        kw = dict(query_xyz=pos.detach(), ref_xyz=pos.detach(), slopes=torch.ones(2))
+        with pytest.raises(ValueError, match=name):
+            tokens.attention(q, q, q, **{**kw, name: pos})
+    with torch.no_grad():
+        tokens.rotary(q, None, pos, freqs)
