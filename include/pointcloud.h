@@ -568,7 +568,9 @@ int pc_rotary(const void *q, const void *k, int dtype, int64_t B, int64_t L, int
  * pc_attention_backward takes the same arguments with out and lse of the
  * forward call and grad_out [B, Lq, H, D] (packed), and writes grad_q,
  * grad_k, grad_v (packed, of dtype; 0 past the lengths) and, if not NULL,
- * grad_slopes [H] float32.  The positions get no gradient.
+ * grad_slopes [H] float32.  The positions get no gradient.  grad_q may be NULL
+ * where grad_slopes is, grad_k and grad_v may be NULL together: their pass is left
+ * out.
  *
  * The _ex calls take out_low too ([B, Lq, H, D] bfloat16, or NULL; bfloat16
  * calls only): the forward call writes there what rounding out to bfloat16 left,

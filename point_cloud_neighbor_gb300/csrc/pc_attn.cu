@@ -742,7 +742,8 @@ cudaError_t run_forward(const DeviceInfo &dev, const AttnArgs &a, cudaStream_t s
 template <class T>
 cudaError_t run_backward(const DeviceInfo &dev, AttnArgs a, const void *out, const void *low,
                          float *dslopes, cudaStream_t st) {
-    const int64_t rows = int64_t(a.B) * a.Lq * a.H, keys = int64_t(a.B) * a.Lk * a.Hkv;
+    const int64_t rows = int64_t(a.B) * a.Lq * a.H;
+    const int64_t keys = a.dk == nullptr ? 0 : int64_t(a.B) * a.Lk * a.Hkv;
     const bool slopes = dslopes != nullptr && a.slopes != nullptr;
     if (rows == 0) {  // no queries: the keys' gradients are 0
         const size_t n = size_t(keys) * a.D * sizeof(T);
@@ -751,10 +752,16 @@ cudaError_t run_backward(const DeviceInfo &dev, AttnArgs a, const void *out, con
         if (e == cudaSuccess && n > 0) e = cudaMemsetAsync(a.dv, 0, n, st);
         return e;
     }
+    if (a.dq == nullptr && keys == 0) return cudaSuccess;
     const AttnPath path = pick_path<T>(a, true);
     Pass dq = plan_pass<T>(dev, a, ATTN_DQ, path, slopes);
     Pass dkv = plan_pass<T>(dev, a, ATTN_DKV, path == PATH_FEW ? PATH_SIMT : path, false);
-    if (path == PATH_FEW || keys == 0) dkv.blocks = 0, dkv.part = dkv.floats = 0;  // no such pass
+    // no such pass (few queries: one kernel forms all)
+    if (path == PATH_FEW || keys == 0) dkv.blocks = 0, dkv.part = dkv.floats = 0;
+    if (a.dq == nullptr) {
+        if (path != PATH_FEW) dq.blocks = 0;
+        dq.part = dq.floats = 0;
+    }
     if (dq.blocks + dkv.blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const size_t sides = (size_t(rows) * 2 + 3) / 4 * 4;  // delta, lse2
     Scratch ws{&dev, st};
@@ -779,12 +786,12 @@ cudaError_t run_backward(const DeviceInfo &dev, AttnArgs a, const void *out, con
         if (e == cudaSuccess) e = launch_attn_tc32_backward(dkv.a, nk, dq.a, nq, s, st);
     } else {
         const bool vec = strides_fit(a, 4, 4 * sizeof(T));
-        e = simt_pick<T, ATTN_DQ>(dq.a, vec, nq, st);
+        e = nq > 0 ? simt_pick<T, ATTN_DQ>(dq.a, vec, nq, st) : cudaSuccess;
         if (e == cudaSuccess && nk > 0) e = simt_pick<T, ATTN_DKV>(dkv.a, vec, nk, st);
     }
     if (e != cudaSuccess) return e;
     if (nk > 0) finish_pass<T>(dkv, path, nullptr, st);
-    finish_pass<T>(dq, path, dslopes, st);
+    if (a.dq != nullptr) finish_pass<T>(dq, path, dslopes, st);
     return cudaGetLastError();
 }
 
@@ -923,6 +930,12 @@ extern "C" int pc_attention_backward_ex(
     const float *slopes, const int64_t *query_lengths, const int64_t *ref_lengths, void *grad_q,
     void *grad_k, void *grad_v, float *grad_slopes, void *stream) {
     using namespace pcn;
+    const bool empty_q = B == 0 || Lq == 0 || H == 0, empty_k = B == 0 || Lk == 0 || H == 0;
+    if ((!empty_k && (grad_k == nullptr) != (grad_v == nullptr)) ||
+        (!empty_q && grad_q == nullptr && grad_slopes != nullptr))
+        return api_fail(PC_ERR_INVALID_ARGUMENT,
+                        "attention_backward: grad_k and grad_v go together, grad_slopes needs "
+                        "grad_q");
     AttnArgs a{};
     const DeviceInfo *dev = nullptr;
     int rc = attn_check("attention_backward", a, &dev, q, k, v, dtype, B, Lq, Lk, H, Hkv, D,
@@ -949,9 +962,9 @@ extern "C" int pc_attention_backward_ex(
         if ((rc = api_check_ptr(out, d, es, "out")) != PC_OK) return rc;
         if (out_low && (rc = api_check_ptr(out_low, d, 2, "out_low")) != PC_OK) return rc;
         if ((rc = api_check_ptr(lse, d, 4, "lse")) != PC_OK) return rc;
-        if ((rc = api_check_ptr(grad_q, d, es, "grad_q")) != PC_OK) return rc;
+        if (grad_q && (rc = api_check_ptr(grad_q, d, es, "grad_q")) != PC_OK) return rc;
     }
-    if (Lk > 0) {
+    if (Lk > 0 && grad_k) {
         if ((rc = api_check_ptr(grad_k, d, es, "grad_k")) != PC_OK) return rc;
         if ((rc = api_check_ptr(grad_v, d, es, "grad_v")) != PC_OK) return rc;
     }

@@ -47,7 +47,7 @@ struct AttnArgs {
     void *low;                              // FWD: what rounding out to bfloat16 left, or NULL
     float *lse;                             // FWD: written if not NULL
     const float *delta, *lse2;              // backward: [B, H, Lq], see attn_delta_kernel
-    void *dq, *dk, *dv;
+    void *dq, *dk, *dv;  // dq, or dk and dv, may be NULL: not asked for
     // the streamed side in nsplit parts: their accumulators, joined afterwards
     int nsplit;
     float *part;     // [nsplit][rows of the output][D] (DKV: dk, then dv)

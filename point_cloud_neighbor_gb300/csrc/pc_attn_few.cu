@@ -330,7 +330,7 @@ few_backward_kernel(const AttnArgs a) {
                     dv[e] = fmaf(p, go[r][e], dv[e]);
                 }
             }
-            if (at[u] < w.j1 && chan) {
+            if (a.dk != nullptr && at[u] < w.j1 && chan) {
                 const int64_t o = ((int64_t(w.b) * a.Lk + at[u]) * a.Hkv + w.hk) * a.D + c0;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
@@ -342,6 +342,7 @@ few_backward_kernel(const AttnArgs a) {
             }
         }
     }
+    if (a.dq == nullptr) return;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
         float ta = wa[r].value(), te = we[r].value(), td = wd[r].value();

@@ -109,17 +109,18 @@ def pc_layer_norm(x: torch.Tensor, weight: torch.Tensor | None = None,
 
 def pc_layer_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
                            rstd: torch.Tensor, weight: torch.Tensor | None = None,
-                           bias: torch.Tensor | None = None):
+                           bias: torch.Tensor | None = None, *, need_weight: bool = True,
+                           need_bias: bool = True):
     """Gradients of :func:`pc_layer_norm`: (grad_x, grad_weight, grad_bias),
-    None for a parameter that is None.  ``mean`` and ``rstd`` are the forward
-    call's statistics."""
+    None for a parameter that is None or not needed.  ``mean`` and ``rstd``
+    are the forward call's statistics."""
     code, index, C, rows, pcode = _norm_args(x, weight, bias)
     _same(grad_out, "grad_out", x.shape, x.dtype, index)
     _same(mean, "mean", x.shape[:-1], torch.float32, index)
     _same(rstd, "rstd", x.shape[:-1], torch.float32, index)
     dx = torch.empty_like(x)
-    dw = None if weight is None else torch.empty_like(weight)
-    db = None if bias is None else torch.empty_like(bias)
+    dw = torch.empty_like(weight) if weight is not None and need_weight else None
+    db = torch.empty_like(bias) if bias is not None and need_bias else None
     _run("pc_layer_norm_backward", lib().pc_layer_norm_backward, index, grad_out.data_ptr(),
          x.data_ptr(), code, rows, C, mean.data_ptr(), rstd.data_ptr(), _ptr_or_none(weight),
          pcode, dx.data_ptr(), _ptr_or_none(dw), _ptr_or_none(db))
@@ -259,11 +260,14 @@ def pc_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tens
                           slopes: torch.Tensor | None = None,
                           query_lengths: torch.Tensor | None = None,
                           ref_lengths: torch.Tensor | None = None,
-                          need_slopes: bool = True,
+                          need_slopes: bool = True, need_q: bool = True, need_kv: bool = True,
                           out_low: torch.Tensor | None = None):
     """Gradients of :func:`pc_attention` from its ``out`` and ``lse``: (grad_q,
     grad_k, grad_v, grad_slopes), the last None without slopes or with
-    ``need_slopes=False``.  The positions get no gradient.
+    ``need_slopes=False``.  The positions get no gradient.  With
+    ``need_q=False`` or ``need_kv=False`` the pass that forms grad_q (and the
+    slopes' gradient, for which it runs all the same), or grad_k and grad_v, is
+    left out and they are None.
 
     In bfloat16 ``out_low``, the forward call's ``low``, keeps the gradients as
     exact as their type.  Without it they are formed from the rounded output,
@@ -281,14 +285,17 @@ def pc_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tens
         if dtype is not torch.bfloat16:
             raise ValueError("out_low belongs to bfloat16 outputs")
         _same(out_low, "out_low", shape, dtype, index)
-    dq = torch.empty(shape, dtype=dtype, device=dev)
-    dk = torch.empty(k.shape, dtype=dtype, device=dev)
-    dv = torch.empty(v.shape, dtype=dtype, device=dev)
     ds = torch.empty_like(slopes) if slopes is not None and need_slopes else None
+    dq = dk = dv = None
+    if need_q or ds is not None:
+        dq = torch.empty(shape, dtype=dtype, device=dev)
+    if need_kv:
+        dk = torch.empty(k.shape, dtype=dtype, device=dev)
+        dv = torch.empty(v.shape, dtype=dtype, device=dev)
     _run("pc_attention_backward", lib().pc_attention_backward_ex, index, grad_out.data_ptr(),
-         *qkv, out.data_ptr(), _ptr_or_none(out_low), lse.data_ptr(), *args, dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-         _ptr_or_none(ds))
-    return dq, dk, dv, ds
+         *qkv, out.data_ptr(), _ptr_or_none(out_low), lse.data_ptr(), *args, _ptr_or_none(dq),
+         _ptr_or_none(dk), _ptr_or_none(dv), _ptr_or_none(ds))
+    return dq if need_q else None, dk, dv, ds
 
 
 # --- differentiable forms -----------------------------------------------------------
@@ -316,7 +323,9 @@ class _LayerNorm(torch.autograd.Function):
     @once_differentiable
     def backward(ctx, g):
         x, weight, bias, mean, rstd = ctx.saved_tensors
-        dx, dw, db = pc_layer_norm_backward(g.contiguous(), x, mean, rstd, weight, bias)
+        _, need_weight, need_bias, _ = ctx.needs_input_grad
+        dx, dw, db = pc_layer_norm_backward(g.contiguous(), x, mean, rstd, weight, bias,
+                                            need_weight=need_weight, need_bias=need_bias)
         return dx, dw, db, None
 
 
@@ -335,10 +344,11 @@ class _Rotary(torch.autograd.Function):
 
     @staticmethod
     def backward(ctx, gq, gk):
-        # the turn back, itself differentiable
-        positions, freqs = ctx.saved_tensors
-        dq, dk = _Rotary.apply(gq.contiguous(), None if gk is None else gk.contiguous(),
-                               positions, freqs, ctx.interleaved, not ctx.inverse)
+        # the turn back, itself differentiable, of what is asked for
+        gs = [g.contiguous() for g, need in zip((gq, gk), ctx.needs_input_grad) if need]
+        turned = _Rotary.apply(gs[0], gs[1] if len(gs) > 1 else None, *ctx.saved_tensors,
+                               ctx.interleaved, not ctx.inverse)
+        dq, dk = turned if ctx.needs_input_grad[0] else (None, turned[0])
         return dq, dk, None, None, None, None
 
 
@@ -369,7 +379,8 @@ class _Attention(torch.autograd.Function):
         dq, dk, dv, ds = pc_attention_backward(
             g.contiguous(), q, k, v, out, lse, scale=ctx.scale, query_xyz=qx, ref_xyz=rx,
             slopes=slopes, query_lengths=ql, ref_lengths=rl,
-            need_slopes=ctx.needs_input_grad[3], out_low=low)
+            need_slopes=ctx.needs_input_grad[3], need_q=ctx.needs_input_grad[0],
+            need_kv=ctx.needs_input_grad[1] or ctx.needs_input_grad[2], out_low=low)
         return dq, dk, dv, ds, None, None, None, None, None
 
 

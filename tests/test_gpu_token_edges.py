@@ -304,3 +304,57 @@ def test_second_derivatives_raise_or_are_right(dtype):
     # four turns, each rounded to the type and 6 units of both channels of a pair
     size = want.abs() + want.unflatten(-1, (-1, 2)).flip(-1).flatten(-2).abs()
     close(dd, want, 5 * (HALF[dtype] + 6 * U) * size, "second derivative")
+
+
+# --- gradients that are not asked for -----------------------------------------------------
+
+GRAD_SHAPES = [(2, 70, 90, 4, 2, 64), (1, 1, 300, 2, 2, 64), (1, 30, 40, 2, 1, 36),
+               (1, 1, 9000, 2, 2, 64), (1, 40, 3000, 1, 1, 128), (2, 0, 5, 2, 1, 64),
+               (2, 5, 0, 2, 1, 64)]
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D", GRAD_SHAPES)
+def test_attention_backward_of_some_inputs(B, Lq, Lk, H, Hkv, D, dtype):
+    q, k, v, do, kw = attn_inputs(B, Lq, Lk, H, Hkv, D, dtype, True, None, None)
+    out, lse = pc.pc_attention(q, k, v, return_lse=True, **kw)
+    # (whether the slopes' gradient is asked for chooses how dq's pass forms the bias)
+    for slopes in (True, False):
+        full = pc.pc_attention_backward(do, q, k, v, out, lse, need_slopes=slopes, **kw)
+        for nq in (True, False):
+            for nkv in (True, False):
+                got = pc.pc_attention_backward(do, q, k, v, out, lse, need_q=nq, need_kv=nkv,
+                                               need_slopes=slopes, **kw)
+                for t, w, need in zip(got, full, (nq, nkv, nkv, slopes)):
+                    assert t is None if not need else torch.equal(t, w)
+
+
+def test_layer_norm_backward_of_some_parameters():
+    g = gen(80)
+    x, dy, w, b = randn(g, 300, 96), randn(g, 300, 96), randn(g, 96), randn(g, 96)
+    y, mean, rstd = pc.pc_layer_norm(x, w, b, return_stats=True)
+    full = pc.pc_layer_norm_backward(dy, x, mean, rstd, w, b)
+    for nw in (True, False):
+        for nb in (True, False):
+            got = pc.pc_layer_norm_backward(dy, x, mean, rstd, w, b, need_weight=nw, need_bias=nb)
+            for t, f, need in zip(got, full, (True, nw, nb)):
+                assert t is None if not need else torch.equal(t, f)
+
+
+def test_autograd_of_frozen_inputs():
+    g = gen(81)
+    q, k, v = (randn(g, 1, 40, 2, 64) for _ in range(3))
+    full = [t.clone().requires_grad_() for t in (q, k, v)]
+    pc.attention(*full).square().sum().backward()
+    for only in range(3):
+        ts = [t.clone().requires_grad_(i == only) for i, t in enumerate((q, k, v))]
+        pc.attention(*ts).square().sum().backward()
+        for i in range(3):
+            assert ts[i].grad is None if i != only else torch.equal(ts[i].grad, full[i].grad)
+    pos, f = randn(g, 1, 40, 3), torch.rand(3, 10, generator=g, device=DEV)
+    a, b = q.clone().requires_grad_(), k.clone().requires_grad_()
+    (sum(t.square().sum() for t in pc.rotary(a, b, pos, f))).backward()
+    for only in range(2):
+        ts = [t.clone().requires_grad_(i == only) for i, t in enumerate((q, k))]
+        (sum(t.square().sum() for t in pc.rotary(*ts, pos, f))).backward()
+        assert ts[1 - only].grad is None and torch.equal(ts[only].grad, (a, b)[only].grad)

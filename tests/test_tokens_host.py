@@ -130,3 +130,34 @@ def test_positions_that_ask_for_a_gradient_are_refused(stand_ins):
             tokens.attention(q, q, q, **{**kw, name: pos})
     with torch.no_grad():
         tokens.rotary(q, None, pos, freqs)
+
+
+def test_only_what_is_asked_for_is_formed(stand_ins):
+    x, w, b = _leaf(3, 8, seed=1), _leaf(8, seed=2), _leaf(8, seed=3)
+    tokens.layer_norm(x, w.detach(), b).sum().backward()
+    assert stand_ins.pop() == {"need_weight": False, "need_bias": True}
+    tokens.layer_norm(x, w, b.detach()).sum().backward()
+    assert stand_ins.pop() == {"need_weight": True, "need_bias": False}
+    q, k, v = (_leaf(1, 4, 2, 8, seed=i) for i in (4, 5, 6))
+    tokens.attention(q, k.detach(), v.detach()).sum().backward()
+    assert stand_ins.pop() == {"need_slopes": False, "need_q": True, "need_kv": False}
+    tokens.attention(q.detach(), k.detach(), v).sum().backward()
+    assert stand_ins.pop() == {"need_slopes": False, "need_q": False, "need_kv": True}
+    pos, freqs = _leaf(1, 4, 3, seed=9).detach(), _leaf(3, 1, seed=10).detach()
+    for i, ts in enumerate(((q.detach(), k), (q, k.detach()))):
+        stand_ins.clear()
+        ts[1 - i].grad = None
+        a, b = tokens.rotary(*ts, pos, freqs)
+        ((a ** 2).sum() + (b ** 2).sum()).backward()
+        assert stand_ins == [(True, True), (True, False)]   # one turn back, of one tensor
+        assert torch.allclose(ts[1 - i].grad, 2 * ts[1 - i].detach())
+
+
+def test_the_pass_of_a_null_gradient(L):
+    def backward(dq, dk, dv, slopes=None, ds=None, Lq=4, Lk=4):
+        return L.pc_attention_backward(FAKE, FAKE, FAKE, FAKE, FAKE, FAKE, 0, 1, Lq, Lk, 2, 1, 64,
+                                       None, None, None, 0.125, slopes, slopes, slopes, None, None,
+                                       dq, dk, dv, ds, None)
+    assert backward(FAKE, FAKE, None) == 1 and backward(FAKE, None, FAKE) == 1
+    assert "go together" in L.pc_last_error_message().decode()
+    assert backward(None, FAKE, FAKE, FAKE, FAKE) == 1
