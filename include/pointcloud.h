@@ -583,7 +583,9 @@ int pc_rotary(const void *q, const void *k, int dtype, int64_t B, int64_t L, int
  * (0.0034 at 16 keys and slopes of 8, 0.6 at 2).
  *
  * Scratch (the library's stream-ordered pool): the parts of a pass whose
- * streamed side is split among more blocks, at most 1 GiB; in the backward
+ * streamed side is split among more blocks, at most 1 GiB, or where a bfloat16
+ * pass streams more than 16,384 rows, a part for each 16,384 of them, at most 8
+ * GiB (4 bytes an output element a part, 8 for grad_k and grad_v); in the backward
  * pass 8 bytes, with grad_slopes 12 more per part, per query row and head;
  * for float32 three bfloat16 parts of q, k, v and grad_out (6 bytes an
  * element, channels rounded up to 8).

@@ -5,6 +5,7 @@
 #include "pc_attn.cuh"
 #include "pointcloud.h"
 
+#include <algorithm>
 #include <cmath>
 #include <cstdio>
 
@@ -606,21 +607,26 @@ struct Scratch {
 // Parts of the streamed side.  A block takes about `start` us before its
 // first tile and `tile` us a tile; blocks run in waves of `slots`; parts have
 // to be joined, which takes another launch and moves every partial sum twice.
-// The number with the smallest estimate, at most 1 GiB of partial sums.
+// The number with the smallest estimate, at most 1 GiB of partial sums beyond
+// what the longest part asks for.
 // (Measured, one query over 100,000 keys, 8 heads of 64: 1 part 1029 us, 8
 // parts 144, 19 parts 72, 38 parts 90; 256 queries and keys, 8 clouds of 8
 // heads: 1 part 13 us, 2 parts 25.)
 int pick_split(int64_t slots, int64_t base, int64_t items, int64_t part_floats, float start,
-               float tile) {
-    int best = 1;
+               float tile, int64_t most_items) {
+    // no more than `most_items` a part, as far as 8 GiB and 256 parts allow
+    int64_t first = (items + most_items - 1) / most_items;
+    first = std::min(first, (int64_t(1) << 31) / std::max(part_floats, int64_t(1)));
+    first = std::max(std::min(first, int64_t(256)), int64_t(1));
+    int best = int(first);
     float least = INFINITY;
-    for (int64_t n = 1; n <= items && n <= 256; ++n) {
-        if (n > 1 && n * part_floats > (int64_t(1) << 28)) break;
+    for (int64_t n = first; n <= items && n <= 256; ++n) {
+        if (n > first && n * part_floats > (int64_t(1) << 28)) break;
         const int64_t waves = (base * n + slots - 1) / slots, each = (items + n - 1) / n;
         float t = float(waves) * (start + tile * float(each));
         if (n > 1) t += 4.0f + float(n * part_floats) * (8.0f / 4e6f);
         if (t < least) least = t, best = int(n);
-        if (n > 1 && base * (n - 1) > 4 * slots) break;  // more waves do not help
+        if (n > first && base * (n - 1) > 4 * slots) break;  // more waves do not help
     }
     return best;
 }
@@ -670,7 +676,8 @@ Pass plan_pass(const DeviceInfo &dev, const AttnArgs &a, int mode, AttnPath path
     p.a.nsplit = path == PATH_FEW
                      ? attn_few_parts(dev, a, sizeof(T), mode == ATTN_DQ)
                      : pick_split(slots, p.base, dkv ? nyt * (a.H / a.Hkv) : nyt,
-                                  p.rows * a.D * (dkv ? 2 : 1), 5.0f, tile);
+                                  p.rows * a.D * (dkv ? 2 : 1), 5.0f, tile,
+                                  path == PATH_TC ? ATTN_TC_CHAIN : INT64_MAX / 2);
     p.blocks = p.base * p.a.nsplit;
     const size_t n = size_t(p.a.nsplit), hrows = size_t(a.B) * a.H * a.Lq;
     p.part = n > 1 ? n * size_t(p.rows) * a.D * (dkv ? 2 : 1) : 0;

@@ -91,6 +91,12 @@ __device__ __forceinline__ bool attn_row_has_keys(const AttnArgs &a, int b, int 
 // Rows a block keeps in the tensor-core kernels, and rows of a streamed tile.
 constexpr int attn_tc_rows(int mode) { return mode == ATTN_FWD ? 256 : 128; }
 constexpr int ATTN_TC_TILE = 64;
+// Tiles whose sums run in one chain of the bfloat16 kernels' accumulators.  The tensor
+// cores cut off what an addition leaves below the accumulator's last place: sums of
+// one sign lose 4.4e-7 of themselves a tile (measured: 1.8e-3 over 4096 tiles, as
+// much as a bfloat16's rounding, and always towards 0).  Parts of 256 tiles (16,384
+// rows), joined in float32, keep that below 1.2e-4.
+constexpr int ATTN_TC_CHAIN = 256;
 
 // Whether the tensor-core kernels (pc_attn_tc.cu; bfloat16) take these sizes,
 // strides and alignments: channels a multiple of 8 and 16-byte aligned rows.

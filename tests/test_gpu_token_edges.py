@@ -286,6 +286,37 @@ def test_attention_slopes_gradient_does_not_lose_with_length(dtype, B, Lq, n, H,
           rel * B * Lq * (c1 + c2) / 2, "dslopes")
 
 
+@pytest.mark.parametrize("side", ["out", "dv"])
+def test_attention_long_sums_on_the_tensor_cores_have_no_bias(side):
+    # The tensor cores cut off what an addition leaves below their accumulator's last place: about
+    # 4.4e-7 of a sum of numbers of one sign a tile of 64 rows.  Parts of at most 16,384 streamed
+    # rows bound that by 1.2e-4; one chain over 2^18 rows would be off by 1.8e-3.  The mean of the
+    # relative errors of many outputs, each rounded to bfloat16 (0.0017 at most, either way), is
+    # within 1e-4 of the bias.
+    n, rows, H, D = 2 ** 18, 4864 if side == "out" else 2432, 8, 64   # (a block a SM, one part)
+    g = gen(70)
+    bf = torch.bfloat16
+    near_one = lambda *s: (1 + 0.25 * torch.randn(*s, generator=g, device=DEV)).to(bf)  # noqa: E731
+    few, many = randn(g, 1, rows, H, D, dtype=bf), randn(g, 1, n, H, D, dtype=bf)
+    if side == "out":
+        v = near_one(1, n, H, D) * (0.75 + 0.5 * torch.rand(H, D, generator=g, device=DEV)).to(bf)
+        got = pc.pc_attention(few, many, v)[0]
+        want = torch.stack([torch.softmax(few[0, :, h].double() @ many[0, :, h].double().T / 8, 1)
+                            @ v[0, :, h].double() for h in range(2)], 1)
+    else:
+        do, v = near_one(1, n, H, D), randn(g, 1, rows, H, D, dtype=bf)
+        out, lse = pc.pc_attention(many, few, v, return_lse=True)
+        got = pc.pc_attention_backward(do, many, few, v, out, lse)[2][0]
+        want = torch.zeros(rows, 2, D, dtype=torch.float64, device=DEV)
+        for h in range(2):
+            K = few[0, :, h].double()
+            for i in range(0, n, 32768):
+                P = torch.softmax(many[0, i:i + 32768, h].double() @ K.T / 8, 1)
+                want[:, h] += P.T @ do[0, i:i + 32768, h].double()
+    err = (got[:, :2].double() - want) / want
+    assert abs(float(err.mean())) <= 1.2e-4 + 1e-4
+
+
 # --- second derivatives -------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype", DTYPES)
