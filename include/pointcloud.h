@@ -550,7 +550,7 @@ int pc_rotary(const void *q, const void *k, int dtype, int64_t B, int64_t L, int
  *   q [B, Lq, H, D]; k, v [B, Lk, Hkv, D]; D <= 128 (PC_ERR_UNSUPPORTED
  *              above).  Hkv divides H: query head h reads key head
  *              h / (H / Hkv).
- *   scale      finite and > 0.
+ *   scale      1e-30 to 1e30.
  *   query_xyz [B, Lq, 3], ref_xyz [B, Lk, 3], slopes [H] float32, packed:
  *              all three, or all NULL (no bias); those of an empty side may
  *              be NULL.

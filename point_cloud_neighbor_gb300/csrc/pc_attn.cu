@@ -820,8 +820,9 @@ int attn_check(const char *what, AttnArgs &a, const DeviceInfo **dev, const void
         return bad(PC_ERR_INVALID_ARGUMENT, "dtype must be PC_F32 or PC_BF16");
     if (H > 0 && (Hkv < 1 || H % Hkv != 0))
         return bad(PC_ERR_INVALID_ARGUMENT, "Hkv must divide H");
-    if (!(scale > 0.0 && scale < 1e30))
-        return bad(PC_ERR_INVALID_ARGUMENT, "scale must be finite and > 0");
+    // (the kernels divide the slopes by it in float32)
+    if (!(scale >= 1e-30 && scale <= 1e30))
+        return bad(PC_ERR_INVALID_ARGUMENT, "scale must be between 1e-30 and 1e30");
     // (an empty side has no positions to point at)
     if (slopes != nullptr ? (qxyz == nullptr && B > 0 && Lq > 0) || (rxyz == nullptr && B > 0 && Lk > 0)
                           : qxyz != nullptr || rxyz != nullptr)

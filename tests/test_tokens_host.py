@@ -161,3 +161,13 @@ def test_the_pass_of_a_null_gradient(L):
     assert backward(FAKE, FAKE, None) == 1 and backward(FAKE, None, FAKE) == 1
     assert "go together" in L.pc_last_error_message().decode()
     assert backward(None, FAKE, FAKE, FAKE, FAKE) == 1
+
+
+def test_a_scale_that_float32_does_not_hold_is_refused(L):
+    def forward(scale):
+        return L.pc_attention(FAKE, FAKE, FAKE, 0, 0, 4, 4, 2, 1, 64, None, None, None, scale, FAKE,
+                              FAKE, FAKE, None, None, FAKE, None, None)
+    assert forward(1e-30) == 0 and forward(1.0) == 0 and forward(1e30) == 0
+    for scale in (1e-50, 1e-39, 2e30, 0.0, float("nan")):
+        assert forward(scale) == 1
+        assert "scale" in L.pc_last_error_message().decode()
