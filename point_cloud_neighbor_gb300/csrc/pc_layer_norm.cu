@@ -423,8 +423,9 @@ cudaError_t ln_launch(LnArgs a, LnLaunch &l) {
     constexpr int FORWARD = Ring<T, V, N, TPR, 1>::BYTES;
     constexpr int SUMS = RPB > 1 ? RPB * 2 * 4 * V * N * TPR : 0;  // of the block's groups
     constexpr int RING2 = Ring<T, V, N, TPR, 2>::BYTES, BACKWARD = RING2 > SUMS ? RING2 : SUMS;
-    // As many blocks as are resident together; a multiple of 8 where a group
-    // takes several rows, so that the rows of a group are a multiple of V apart.
+    // As many blocks as are resident together, at most 8 a SM (which bounds the
+    // partial sums); a multiple of 8 where a group takes several rows, so that the
+    // rows of a group are a multiple of V apart.
     static std::atomic<uint64_t> allowed[2] = {{0}, {0}};
     cudaError_t e =
         l.backward ? allow_smem(ln_backward_kernel<T, WT, V, N, TPR>, BACKWARD, l.dev->device,
@@ -432,16 +433,17 @@ cudaError_t ln_launch(LnArgs a, LnLaunch &l) {
                    : allow_smem(ln_forward_kernel<T, WT, V, N, TPR>, FORWARD, l.dev->device,
                                 allowed[0]);
     if (e != cudaSuccess) return e;
-    static std::atomic<int> resident[2] = {{0}, {0}};
-    int per_sm = resident[l.backward].load(std::memory_order_relaxed);
+    static std::atomic<int> resident[2][64] = {};  // of each device
+    std::atomic<int> &kept = resident[l.backward][l.dev->device & 63];
+    int per_sm = kept.load(std::memory_order_relaxed);
     if (per_sm == 0) {
         e = l.backward ? cudaOccupancyMaxActiveBlocksPerMultiprocessor(
                              &per_sm, ln_backward_kernel<T, WT, V, N, TPR>, THREADS, BACKWARD)
                        : cudaOccupancyMaxActiveBlocksPerMultiprocessor(
                              &per_sm, ln_forward_kernel<T, WT, V, N, TPR>, THREADS, FORWARD);
         if (e != cudaSuccess) return e;
-        if (per_sm < 1) per_sm = 1;
-        resident[l.backward].store(per_sm, std::memory_order_relaxed);
+        per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
+        kept.store(per_sm, std::memory_order_relaxed);
     }
     const int64_t most = (int64_t(l.dev->sm_count) * per_sm + 7) / 8 * 8;
     const unsigned blocks = unsigned(want < most ? want : most);

@@ -4,6 +4,7 @@ sums, and the steady state of the kernels' loops.
 
 Tolerances are derived from the arithmetic as in test_gpu_tokens.py.
 """
+import ctypes
 import math
 
 import pytest
@@ -11,6 +12,7 @@ import torch
 
 import point_cloud_neighbor_gb300 as pc
 import test_gpu_tokens as base
+from point_cloud_neighbor_gb300.binding import lib
 from test_gpu_tokens import (DEV, DTYPES, HALF, U, Ref, attn_inputs,  # noqa: F401
                              clean_status, close, gen, lens, randn)
 
@@ -389,3 +391,56 @@ def test_autograd_of_frozen_inputs():
         ts = [t.clone().requires_grad_(i == only) for i, t in enumerate((q, k))]
         (sum(t.square().sum() for t in pc.rotary(*ts, pos, f))).backward()
         assert ts[1 - only].grad is None and torch.equal(ts[only].grad, (a, b)[only].grad)
+
+
+# --- scratch --------------------------------------------------------------------------------
+
+class _Props(ctypes.Structure):          # CUDA_MEM_ALLOC_NODE_PARAMS of the driver
+    _fields_ = [("pool", ctypes.c_byte * 88), ("access", ctypes.c_void_p),
+                ("accesses", ctypes.c_size_t), ("bytes", ctypes.c_size_t), ("ptr", ctypes.c_uint64)]
+
+
+def allocations(call, stream):
+    """The sizes of the stream-ordered allocations a call makes, from a capture of it."""
+    cu = ctypes.CDLL("libcuda.so.1")
+
+    def ok(status):
+        assert status == 0, f"driver status {status}"
+
+    s, graph, count, kind = ctypes.c_void_p(stream), ctypes.c_void_p(), ctypes.c_size_t(), ctypes.c_int()
+    ok(cu.cuStreamBeginCapture_v2(s, ctypes.c_int(2)))
+    try:
+        call()
+    finally:
+        ok(cu.cuStreamEndCapture(s, ctypes.byref(graph)))
+    sizes = []
+    ok(cu.cuGraphGetNodes(graph, None, ctypes.byref(count)))
+    nodes = (ctypes.c_void_p * count.value)()
+    ok(cu.cuGraphGetNodes(graph, nodes, ctypes.byref(count)))
+    for n in nodes:
+        ok(cu.cuGraphNodeGetType(ctypes.c_void_p(n), ctypes.byref(kind)))
+        if kind.value == 10:             # CU_GRAPH_NODE_TYPE_MEM_ALLOC
+            p = _Props()
+            ok(cu.cuGraphMemAllocNodeGetParams(ctypes.c_void_p(n), ctypes.byref(p)))
+            sizes.append(p.bytes)
+    ok(cu.cuGraphDestroy(graph))
+    return sizes
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("C", [7, 32, 96, 515, 2050, 8192])
+def test_layer_norm_backward_scratch_is_bounded(C, dtype):
+    # 8 blocks a SM with a row of 2 C float32 each, as the header says
+    rows = max(4, 40_000_000 // C // 16)
+    x, dy = torch.zeros(rows, C, dtype=dtype, device=DEV), torch.zeros(rows, C, dtype=dtype, device=DEV)
+    w, b = torch.ones(C, device=DEV), torch.zeros(C, device=DEV)
+    y, mean, rstd = pc.pc_layer_norm(x, w, b, return_stats=True)
+    dx, dw, db = pc.pc_layer_norm_backward(dy, x, mean, rstd, w, b)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    sizes = allocations(lambda: lib().pc_layer_norm_backward(
+        dy.data_ptr(), x.data_ptr(), 0 if dtype is torch.float32 else 1, rows, C, mean.data_ptr(),
+        rstd.data_ptr(), w.data_ptr(), 0, dx.data_ptr(), dw.data_ptr(), db.data_ptr(),
+        s.cuda_stream), s.cuda_stream)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    assert len(sizes) == 1 and 0 < sizes[0] <= 8 * sms * 2 * C * 4
