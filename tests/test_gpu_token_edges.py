@@ -444,3 +444,125 @@ def test_layer_norm_backward_scratch_is_bounded(C, dtype):
         s.cuda_stream), s.cuda_stream)
     sms = torch.cuda.get_device_properties(0).multi_processor_count
     assert len(sizes) == 1 and 0 < sizes[0] <= 8 * sms * 2 * C * 4
+
+
+# --- the loops' steady state -----------------------------------------------------------
+
+# More rows than the blocks that are resident together take in a round (at most 8 blocks of 4 to 16
+# rows a SM, one of 8 for rows of a block), several rounds and a part of one.
+@pytest.mark.parametrize("dtype,pdtype", [(torch.float32, torch.float32),
+                                          (torch.bfloat16, torch.float32),
+                                          (torch.bfloat16, torch.bfloat16)])
+@pytest.mark.parametrize("shape", [(100_003, 33), (60_001, 96), (20_003, 515), (9_001, 1025),
+                                   (9_001, 1024), (5_003, 2051), (4_001, 8192)])
+def test_layer_norm_of_many_rounds(shape, dtype, pdtype):
+    base.test_layer_norm(shape, dtype, pdtype)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(7, 33), (20_003, 515), (5_003, 2051)])
+def test_layer_norm_of_unaligned_rows(shape, dtype):
+    # one element off a vector: an element a load; the same values within the bounds of both
+    g = gen(90)
+    rows, C = shape
+    x, dy = (randn(g, rows * C + 1, dtype=dtype)[1:].view(rows, C) for _ in range(2))
+    w, b = randn(g, C) + 1, randn(g, C)
+    y, mean, rstd = pc.pc_layer_norm(x, w, b, return_stats=True)
+    dx, dw, db = pc.pc_layer_norm_backward(dy, x, mean, rstd, w, b)
+    r = base.ln_reference(x, w, b, 1e-5, dy)
+    # (rows of mean about 0 and deviation 1: the bounds of the aligned test with |x| rstd <= 8)
+    K, half = 64 * U, HALF[dtype]
+    exh = (2 * K + 8 * U * 8) * (r["xh"].abs() + 1)
+    close(y, r["y"], r["w"].abs() * exh + 4 * U * (r["y"].abs() + r["b"].abs()) + half * r["y"].abs(), "y")
+    ga, xa, rs = r["g"].abs(), r["xh"].abs(), r["rstd"].unsqueeze(-1)
+    mg, mgx = ga.mean(-1, keepdim=True), (ga * xa).mean(-1, keepdim=True)
+    edx = rs * (K * (ga + mg + xa * mgx) + exh * mgx + xa * (ga * exh).mean(-1, keepdim=True))
+    close(dx, r["dx"], 2 * edx + half * r["dx"].abs() + 1e-30, "dx")
+    da, n = dy.double().abs(), (rows + 64) * U
+    close(dw, r["dw"], (da * (exh + n * xa)).sum(0) + U * r["dw"].abs(), "dw")
+    close(db, r["db"], n * da.sum(0) + U * r["db"].abs(), "db")
+
+
+# Enough tokens that a thread goes over five heads and more, several of them in flight; every
+# remainder of the pairs by the elements of a vector.
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("interleaved", [True, False])
+@pytest.mark.parametrize("B,L,H,Hkv,D,A,F", [
+    (2, 4099, 9, 4, 64, 1, 8), (1, 8201, 9, 4, 64, 1, 9), (3, 6007, 11, 2, 64, 2, 5),
+    (1, 20011, 7, 2, 64, 1, 11), (2, 4099, 9, 4, 128, 3, 20), (1, 20011, 5, 0, 64, 1, 13),
+    (2, 9001, 13, 0, 64, 2, 15), (1, 20011, 3, 4, 64, 3, 5), (2, 8191, 9, 4, 64, 3, 10)])
+def test_rotary_of_many_heads_a_thread(B, L, H, Hkv, D, A, F, interleaved, dtype):
+    if Hkv:
+        base.test_rotary(B, L, H, Hkv, D, A, F, interleaved, dtype)
+        return
+    g = gen(B + L)
+    q, pos = randn(g, B, L, H, D, dtype=dtype), randn(g, B, L, A)
+    freqs = 30 * torch.rand(A, F, generator=g, device=DEV)
+    got, none = pc.pc_rotary(q, None, pos, freqs, interleaved=interleaved)
+    want, e = base.rotary_reference(q, pos, freqs, interleaved, False)
+    assert none is None
+    close(got, want, 6 * U * e + HALF[dtype] * want.abs() + 1e-30, "rotary")
+
+
+# --- attention: both ways to form the bias, both sides long ------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D,ql,rl", [
+    (1, 600, 700, 2, 1, 64, None, None), (1, 600, 700, 2, 1, 40, [600], [650]),
+    (3, 1024, 1024, 8, 2, 64, [1024, 700, 31], [1024, 700, 31]),
+    (2, 1024, 1024, 4, 1, 40, [1024, 513], [1024, 513])])
+@pytest.mark.parametrize("bias", [True, False])
+def test_attention_both_sides_long(B, Lq, Lk, H, Hkv, D, ql, rl, bias, dtype):
+    q, k, v, do, kw = attn_inputs(B, Lq, Lk, H, Hkv, D, dtype, bias, ql, rl)
+    base.check_attention(q, k, v, do, kw, dtype)
+
+
+def spread(B, L, g, most):
+    """Points whose distance from the origin grows from 0 to `most` along the cloud."""
+    p = randn(g, B, L, 3)
+    r = torch.linspace(0, most, L, device=DEV).view(1, L, 1)
+    return p / p.norm(dim=-1, keepdim=True) * r
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("D", [64, 128, 40])
+@pytest.mark.parametrize("most,slope", [(8.0, 10.0), (60.0, 0.3), (3.0, 100.0), (3.0, -5.0)])
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv", [(1, 500, 700, 2, 1), (2, 130, 330, 4, 4)])
+def test_attention_tiles_near_and_far(B, Lq, Lk, H, Hkv, D, most, slope, dtype):
+    # slope R^2 passes 256 within the cloud: some tiles of a block take the bias through the
+    # products, the others from the coordinates' differences (a scene in metres, a steep bias)
+    g = gen(100)
+    q, k, v, do, kw = attn_inputs(B, Lq, Lk, H, Hkv, D, dtype, True, None, None)
+    kw["query_xyz"], kw["ref_xyz"] = spread(B, Lq, g, most), spread(B, Lk, g, most)
+    kw["slopes"] = slope * (0.5 + torch.rand(H, generator=g, device=DEV))
+    base.check_attention(q, k, v, do, kw, dtype)
+    # without the slopes' gradient the pass of dq takes the bias as the others do
+    ref = Ref(q, k, v, do, 1 / math.sqrt(D), kw, dtype)
+    out, lse = pc.pc_attention(q, k, v, return_lse=True, **kw)
+    dq, dk, dv, ds = pc.pc_attention_backward(do, q, k, v, out, lse, need_slopes=False, **kw)
+    assert ds is None
+    for t, w, e, name in ((dq, ref.dq, ref.edq, "dq"), (dk, ref.dk, ref.edk, "dk"),
+                          (dv, ref.dv, ref.edv, "dv")):
+        close(t, w, e + 1e-30, name)
+
+
+@pytest.mark.parametrize("dtype,D", [(torch.float32, 64), (torch.float32, 128), (torch.bfloat16, 128)])
+def test_a_withheld_copy_ends_with_a_status_in_every_kernel(dtype, D):
+    # the first block's copies never come: its waits run out, the context stays usable
+    q, k, v, do, kw = attn_inputs(2, 200, 200, 2, 2, D, dtype, True, None, None)
+    want = pc.pc_attention(q, k, v, return_lse=True, **kw)
+    grads = pc.pc_attention_backward(do, q, k, v, *want, **kw)
+    torch.cuda.synchronize()
+    try:
+        pc.pc_set_wait_timeout_ns(50_000_000)
+        pc.pc_debug_set_stall(pc.PC_STALL_ATTENTION)
+        pc.pc_attention(q, k, v, **kw)
+        assert pc.pc_device_status(reset=True) == 4
+        pc.pc_attention_backward(do, q, k, v, *want, **kw)
+        assert pc.pc_device_status(reset=True) == 4
+    finally:
+        pc.pc_debug_set_stall(0)
+        pc.pc_set_wait_timeout_ns(2_000_000_000)
+    assert torch.equal(pc.pc_attention(q, k, v, **kw), want[0])
+    assert all(torch.equal(a, b) for a, b in
+               zip(pc.pc_attention_backward(do, q, k, v, *want, **kw), grads))
