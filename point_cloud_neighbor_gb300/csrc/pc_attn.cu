@@ -270,6 +270,7 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
     }
 
     const int64_t rows = int64_t(a.B) * LX * NH;
+    const float one = MODE == ATTN_FWD ? 1.0f : attn_ds_factor(nk);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = r0 + ty + 16 * i;
@@ -279,7 +280,7 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
             for (int o = 8; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
         }
         if (MODE == ATTN_DQ && bias) {
-            float ta = wa[i].value(), te = we[i].value(), td = wd[i].value();
+            float ta = one * wa[i].value(), te = we[i].value(), td = one * wd[i].value();
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) {
                 ta += __shfl_xor_sync(0xffffffffu, ta, o);
@@ -301,7 +302,7 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
             for (int e = 0; e < DP / 16; ++e) {
                 const int c = 64 * (e / 4) + 4 * tx + e % 4;
                 if (c < a.D) {
-                    p1[c] = r < nx ? acc[i][e] : 0.0f;
+                    p1[c] = r < nx ? one * acc[i][e] : 0.0f;
                     if (MODE == ATTN_DKV) p2[c] = r < nx ? acc2[i][e] : 0.0f;
                 }
             }
@@ -313,7 +314,7 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
             continue;
         }
         const bool any = r < nx && (MODE != ATTN_FWD || ny > 0);
-        const float f = MODE == ATTN_FWD ? 1.0f / sum[i] : a.scale;
+        const float f = MODE == ATTN_FWD ? 1.0f / sum[i] : one * a.scale;
         T *o1 = static_cast<T *>(MODE == ATTN_FWD  ? a.out
                                  : MODE == ATTN_DQ ? a.dq
                                                    : a.dk) + orow * a.D;

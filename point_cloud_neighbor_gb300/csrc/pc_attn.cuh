@@ -6,6 +6,8 @@
 //   delta_i = out_i . dout_i = sum_j P_ij dP_ij, dP = dout v^T, dS = P (dP - delta),
 //   dq = scale dS k, dk = scale dS^T q, dv = P^T dout,
 //   dslope_h = -sum_ij dS_ij |x_i - y_j|^2.
+// A cloud with one key has P = 1 and dS = 0 exactly: delta and dP, which are summed
+// in different orders, would leave their rounding.  Sums of its dS are taken as 0.
 //
 // Every pass keeps a tile of rows (its `stationary` side) and walks over the
 // other side in tiles (`streamed`):
@@ -87,6 +89,9 @@ struct LongSum {
 __device__ __forceinline__ bool attn_row_has_keys(const AttnArgs &a, int b, int i) {
     return i < attn_len(a.qlen, b, a.Lq) && attn_len(a.rlen, b, a.Lk) > 0;
 }
+
+// The factor of sums of dS: see above.
+__device__ __forceinline__ float attn_ds_factor(int nk) { return nk > 1 ? 1.0f : 0.0f; }
 
 // Rows a block keeps in the tensor-core kernels, and rows of a streamed tile.
 constexpr int attn_tc_rows(int mode) { return mode == ATTN_FWD ? 256 : 128; }

@@ -274,6 +274,7 @@ few_backward_kernel(const AttnArgs a) {
     const T *kb = static_cast<const T *>(a.k) + w.b * a.ks[0] + w.hk * a.ks[2] + c0;
     const T *vb = static_cast<const T *>(a.v) + w.b * a.vs[0] + w.hk * a.vs[2] + c0;
     const float *yb = a.rxyz + int64_t(w.b) * a.Lk * 3;
+    const float one = attn_ds_factor(w.nk);
     for (int j = w.j0; j < w.j1; j += U * STEP) {
         FewChunk<T> kc[U], vc[U];
         float y[U][3];
@@ -334,7 +335,7 @@ few_backward_kernel(const AttnArgs a) {
                 const int64_t o = ((int64_t(w.b) * a.Lk + at[u]) * a.Hkv + w.hk) * a.D + c0;
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
-                    dk[e] = in ? dk[e] * a.scale : 0.0f;
+                    dk[e] = in ? dk[e] * (one * a.scale) : 0.0f;
                     dv[e] = in ? dv[e] : 0.0f;
                 }
                 Vec<T, V>::store(static_cast<T *>(a.dk) + o, dk);
@@ -372,7 +373,7 @@ few_backward_kernel(const AttnArgs a) {
         float v = 0.0f;
 #pragma unroll
         for (int k = 0; k < FEW_WARPS; ++k) v += sm[k][r][c < a.D ? c : LPK * V + c - a.D];
-        if (i >= w.nq) v = 0.0f;  // (weights of 0, but keys that may be NaN)
+        v = i < w.nq ? one * v : 0.0f;  // (past the length weights of 0, but keys that may be NaN)
         const int64_t orow = (int64_t(w.b) * a.Lq + i) * a.H + h;
         const int64_t hrow = (int64_t(w.b) * a.H + h) * a.Lq + i;
         if (c >= a.D) {

@@ -810,6 +810,7 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
         }
         const int64_t hrow = (int64_t(b) * a.H + head) * a.Lq + row;  // FWD, DQ
         const int64_t hrows = int64_t(a.B) * a.H * a.Lq;
+        const float one = FWD ? 1.0f : attn_ds_factor(nk);
         if (MODE == ATTN_DQ && BIAS) {
             // the sums of a row's four groups, in the exchange buffer as [unit][half][3]
             if (sums) {
@@ -823,7 +824,7 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
 #pragma unroll
                 for (int e = 0; e < 3; ++e) {
                     t[e] = (rd[e * XR] + rd[(3 + e) * XR]) + (rd[(6 + e) * XR] + rd[(9 + e) * XR]);
-                    if (row >= nx) t[e] = 0.0f;
+                    t[e] = row < nx ? one * t[e] : 0.0f;
                 }
                 put_slope_sums(a, t, split, hrow, row < LX, quad, lane, rowdata + 12 * XR, bid);
             }
@@ -859,7 +860,8 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
                 tmem_ld32(tmem + lanes + C::ACC + (FWD ? unit * DP : 0) + ch * 32, r);
                 tmem_wait_ld();
             }
-            const float f = a.nsplit > 1 ? 1.0f : FWD ? 1.0f / l : acc == 0 ? a.scale : 1.0f;
+            const float f = FWD ? (a.nsplit > 1 ? 1.0f : 1.0f / l)
+                            : acc != 0 ? 1.0f : a.nsplit > 1 ? one : one * a.scale;
 #pragma unroll
             for (int e = 0; e < 32; ++e)
                 v[e] = have && any ? __uint_as_float(r[e]) * f : 0.0f;

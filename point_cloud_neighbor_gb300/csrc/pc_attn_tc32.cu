@@ -590,6 +590,7 @@ __device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMap
         if (ok && n > 0) ok = drain(n - 1);
         const int64_t hrow = (int64_t(b) * a.H + head) * a.Lq + row;  // FWD, DQ
         const int64_t hrows = int64_t(a.B) * a.H * a.Lq;
+        const float one = FWD ? 1.0f : attn_ds_factor(nk);
         float l = l2.x + l2.y;
         if (MODE == ATTN_DQ) {
             if (half == 1) {
@@ -600,7 +601,8 @@ __device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMap
             named_barrier_sync(1, C::CWARPS * 32);
             if (sums && half == 0) {
                 float t[3] = {wa.value() + rd[0], we.value() + rd[XR], wd.value() + rd[2 * XR]};
-                if (row >= nx) t[0] = t[1] = t[2] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 3; ++e) t[e] = row < nx ? one * t[e] : 0.0f;
                 put_slope_sums(a, t, split, hrow, row < LX, quad, lane, rowdata + 6 * XR, bid);
             }
         }
@@ -623,7 +625,8 @@ __device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMap
             const int64_t rows = int64_t(a.B) * LX * NH;
 #pragma unroll
             for (int t = 0; t < C::NACC; ++t) {
-                const float g = a.nsplit > 1 ? 1.0f : FWD ? 1.0f / l : t == 0 ? a.scale : 1.0f;
+                const float g = FWD ? (a.nsplit > 1 ? 1.0f : 1.0f / l)
+                                : t != 0 ? 1.0f : a.nsplit > 1 ? one : one * a.scale;
 #pragma unroll
                 for (int c = 0; c < DP / 64; ++c) {
                     const int c0 = half * (DP / 2) + 32 * c;

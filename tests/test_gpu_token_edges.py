@@ -103,6 +103,33 @@ def test_attention_rows_without_keys_are_zeros_among_rows_that_are_nan(B, Lq, Lk
     assert not grads[1][2, 1:].any() and not grads[2][2, 1:].any()
 
 
+# --- one key ---------------------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D,rl", [
+    (3, 1, 1, 4, 4, 64, None), (2, 1, 300, 2, 2, 64, [1, 0]), (2, 2, 9000, 2, 2, 128, [1, 1]),
+    (4, 30, 1, 4, 2, 64, None), (1, 3000, 1, 8, 1, 128, None), (2, 100, 200, 2, 2, 40, [1, 1]),
+    (3, 20, 1, 2, 1, 36, None), (1, 3000, 70, 2, 1, 36, [1]), (1, 40, 2000, 1, 1, 128, [1])])
+def test_attention_of_one_key_has_no_gradient_through_its_scores(B, Lq, Lk, H, Hkv, D, rl, dtype):
+    # the weight is 1 whatever the score
+    q, k, v, do, kw = attn_inputs(B, Lq, Lk, H, Hkv, D, dtype, True, None, rl)
+    out, lse = pc.pc_attention(q, k, v, return_lse=True, **kw)
+    dq, dk, dv, ds = pc.pc_attention_backward(do, q, k, v, out, lse, **kw)
+    assert not dq.any() and not dk.any() and not ds.any()
+    n = torch.tensor([1] * B if rl is None else rl, device=DEV).view(B, 1, 1, 1)
+    G = H // Hkv
+    # a bfloat16 value as it is; of a float32's three parts up to 4 units a sum are cut off
+    one = (n * v[:, :1].repeat_interleave(G, 2)).expand(B, Lq, H, D).double()
+    close(out, one, (0.0 if dtype is torch.bfloat16 else 8 * U) * one.abs() + 1e-30, "out")
+    g = do.double().view(B, Lq, Hkv, G, D)
+    # (G Lq terms, up to 4 units a step on the tensor cores, and weights within 2^-16 of 1)
+    size = g.abs().sum((1, 3)).unsqueeze(1) * n
+    want = g.sum((1, 3)).unsqueeze(1) * n
+    tol = (4 * U * (G * Lq + 4) + 2.0 ** -16) * size + HALF[dtype] * want.abs() + 1e-30
+    close(dv[:, :1], want, tol, "dv")
+    assert not dv[:, 1:].any()
+
+
 # --- more clouds than an index of three parts holds -----------------------------------
 
 def test_attention_more_clouds_than_a_third_of_2_31():
