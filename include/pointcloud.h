@@ -576,17 +576,17 @@ int pc_rotary(const void *q, const void *k, int dtype, int64_t B, int64_t L, int
  * calls only): the forward call writes there what rounding out to bfloat16 left,
  * the backward call reads it.  The backward pass needs
  * delta_i = out_i . grad_out_i, and subtracts it from numbers of its own size:
- * with out_low it is that of the output before its rounding, and the gradients
- * are rounded once.  Without, it is off by up to 2^-8 |out_i| |grad_out_i|, which
- * P_ij times reaches dS_ij: little where many keys share a row (the gradients' norm
- * is off by 0.0017 as a result rounded once at 1024 keys), much where few do
- * (0.0034 at 16 keys and slopes of 8, 0.6 at 2).
+ * it has to be that of the output before its rounding (that of the rounded output
+ * leaves an error as large as the gradients where few keys share a row).  Without
+ * out_low a bfloat16 backward call runs the forward pass again for it; out is then
+ * not read.  Both give the same bits.
  *
  * Scratch (the library's stream-ordered pool): the parts of a pass whose
  * streamed side is split among more blocks, at most 1 GiB, or where a bfloat16
  * pass streams more than 16,384 rows, a part for each 16,384 of them, at most 8
  * GiB (4 bytes an output element a part, 8 for grad_k and grad_v); in the backward
- * pass 8 bytes, with grad_slopes 12 more per part, per query row and head;
+ * pass 8 bytes, with grad_slopes 12 more per part, per query row and head, in
+ * bfloat16 without out_low 4 D more and what the forward pass takes;
  * for float32 three bfloat16 parts of q, k, v and grad_out (6 bytes an
  * element, channels rounded up to 8).
  *

@@ -772,10 +772,23 @@ cudaError_t run_backward(const DeviceInfo &dev, AttnArgs a, const void *out, con
     }
     if (dq.blocks + dkv.blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
     const size_t sides = (size_t(rows) * 2 + 3) / 4 * 4;  // delta, lse2
+    // a bfloat16 output without its low part: both again (a multiple of 16 bytes each)
+    const bool again = sizeof(T) == 2 && low == nullptr;
+    const size_t outs = again ? (size_t(rows) * a.D + 7) / 8 * 8 : 0;
+    const size_t tail = 2 * outs * sizeof(T);
     Scratch ws{&dev, st};
-    cudaError_t e = ws.take((sides + dq.floats + dkv.floats) * sizeof(float) +
+    cudaError_t e = ws.take((sides + dq.floats + dkv.floats) * sizeof(float) + tail +
                             (path == PATH_PARTS ? attn_split_bytes(a, true) : 0));
     if (e != cudaSuccess) return e;
+    if (again) {
+        AttnArgs f = a;
+        f.out = static_cast<char *>(ws.p) + (sides + dq.floats + dkv.floats) * sizeof(float);
+        f.low = static_cast<T *>(f.out) + outs;
+        f.lse = nullptr;
+        f.dq = f.dk = f.dv = nullptr;
+        if ((e = run_forward<T>(dev, f, st)) != cudaSuccess) return e;
+        out = f.out, low = f.low;
+    }
     float *delta = static_cast<float *>(ws.p), *space = delta + sides;
     dq.a.delta = dkv.a.delta = delta;
     dq.a.lse2 = dkv.a.lse2 = delta + rows;

@@ -23,7 +23,8 @@
 // is then as large as dS itself (dq off by 0.0034 of its norm at 16 keys with slopes
 // of 8, by 0.6 at 2, where a result rounded once has 0.0017).  So a forward pass
 // can write what the rounding left as a second bfloat16 array, `low`, for 2 bytes
-// an element, and delta adds it.
+// an element, and delta adds it.  A backward call without it runs the forward pass
+// again for both arrays (4096 tokens, 16 + 4 heads of 128: 164 us on 572).
 #pragma once
 
 #include "pc_internal.h"

@@ -269,10 +269,9 @@ def pc_attention_backward(grad_out: torch.Tensor, q: torch.Tensor, k: torch.Tens
     slopes' gradient, for which it runs all the same), or grad_k and grad_v, is
     left out and they are None.
 
-    In bfloat16 ``out_low``, the forward call's ``low``, keeps the gradients as
-    exact as their type.  Without it they are formed from the rounded output,
-    whose error (2^-8 of |out| |grad_out|) stays in them: little where a row
-    has many keys of weight, much where it has few.
+    A bfloat16 call needs the output before its rounding: from ``out_low``, the
+    forward call's ``low``, or it runs the forward pass again.  The results are
+    the same.
     """
     index, qkv, args = _attention_args(q, k, v, scale, query_xyz, ref_xyz, slopes,
                                        query_lengths, ref_lengths)

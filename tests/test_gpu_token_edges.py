@@ -282,6 +282,24 @@ def test_attention_delta_in_norm(B, Lq, Lk, H, Hkv, D):
         assert float((t.double() - w).norm()) <= 2.0 ** -8 / math.sqrt(3) * float(w.norm()) + float(e.norm())
 
 
+@pytest.mark.parametrize("ragged", [True, False])
+@pytest.mark.parametrize("B,Lq,Lk,H,Hkv,D", PEAKED)
+def test_attention_backward_without_the_low_part_forms_it(B, Lq, Lk, H, Hkv, D, ragged):
+    # the plain calls are as exact as those that keep the low part: the same bits
+    ql, rl = ([max(Lq - b, 0) for b in range(B)], [max(Lk - 2 * b, 0) for b in range(B)]) \
+        if ragged else (None, None)
+    q, k, v, do, kw = attn_inputs(B, Lq, Lk, H, Hkv, D, torch.bfloat16, True, ql, rl)
+    out, lse, low = pc.pc_attention(q, k, v, return_lse=True, return_low=True, **kw)
+    want = pc.pc_attention_backward(do, q, k, v, out, lse, out_low=low, **kw)
+    got = pc.pc_attention_backward(do, q, k, v, out, lse, **kw)
+    assert all(torch.equal(t, w) for t, w in zip(got, want))
+    # and through strided views
+    base = torch.cat([t.flatten(2) for t in (k, v)], -1)
+    k2, v2 = (t.unflatten(-1, (Hkv, D)) for t in base.split(Hkv * D, -1))
+    got = pc.pc_attention_backward(do, q, k2, v2, out, lse, **kw)
+    assert all(torch.equal(t, w) for t, w in zip(got, want))
+
+
 # --- long sums -------------------------------------------------------------------------
 
 @pytest.mark.parametrize("dtype,B,Lq,n,H,Hkv,D", [
