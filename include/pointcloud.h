@@ -585,7 +585,7 @@ int pc_rotary(const void *q, const void *k, int dtype, int64_t B, int64_t L, int
  * streamed side is split among more blocks, at most 1 GiB, or where a bfloat16
  * pass streams more than 16,384 rows, a part for each 16,384 of them, at most 8
  * GiB (4 bytes an output element a part, 8 for grad_k and grad_v); in the backward
- * pass 8 bytes, with grad_slopes 12 more per part, per query row and head, in
+ * pass 8 bytes, with grad_slopes 16 more per part, per query row and head, in
  * bfloat16 without out_low 4 D more and what the forward pass takes;
  * for float32 three bfloat16 parts of q, k, v and grad_out (6 bytes an
  * element, channels rounded up to 8).

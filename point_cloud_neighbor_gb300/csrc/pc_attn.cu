@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
             }
             if (tx == 0 && r < LX && a.rowsum != nullptr) {
                 const int64_t n = int64_t(a.B) * a.H * a.Lq;
-                float *w = a.rowsum + split * 3 * n + hrow;
+                float *w = a.rowsum + int64_t(split) * 3 * n + hrow;
                 w[0] = ta, w[n] = te, w[2 * n] = td;
             }
         }
@@ -490,8 +490,9 @@ __global__ void __launch_bounds__(1024) attn_join_rows_kernel(const AttnArgs a) 
         if (t == 0 && a.lse != nullptr)
             a.lse[hrow] = any ? (m + log2f(l)) * ATTN_LN2 : -INFINITY;
     } else if (a.rowsum != nullptr) {
-        for (int e = 0; e < 3; ++e) {
-            const float v = over(mine ? a.rowsum[(int64_t(t) * 3 + e) * rows + hrow] : 0.0f, false);
+        for (int e = 0; e < a.nsums; ++e) {
+            const float *w = a.rowsum + (int64_t(t) * a.nsums + e) * rows + hrow;
+            const float v = over(mine ? *w : 0.0f, false);
             if (t == 0) a.rowsum[e * rows + hrow] = v;
         }
     }
@@ -533,7 +534,10 @@ void launch_join(const AttnArgs &a, int mode, int64_t rows, cudaStream_t st) {
 // dslope_h = -sum over rows of (dS d2 - (dS) (P d2)), each row's sums joined
 // over the parts first: a block per head, float64, a fixed order.  A row's
 // exact dS sum to 0; what they sum to here is the error of delta (from an
-// output rounded to its type), and the second term takes its effect out.
+// output rounded to its type), and the second term takes its effect out.  Where the
+// sum of P is there (bfloat16 on the tensor cores) the row's P are divided by it: the
+// forward pass may have formed the bias through the products and this one from
+// differences, and the row's lse is then off by up to 2^-20 slope R^2.
 // With `tiles` the sums are already one number for each tile of a head's rows.
 __global__ void __launch_bounds__(1024)
 attn_slope_kernel(const AttnArgs a, int tiles, float *dslopes) {
@@ -547,13 +551,14 @@ attn_slope_kernel(const AttnArgs a, int tiles, float *dslopes) {
     } else {
         for (int64_t r = threadIdx.x; r < int64_t(a.B) * a.Lq; r += 1024) {
             const int64_t b = r / a.Lq, at = (b * a.H + h) * a.Lq + (r - b * a.Lq);
-            double wa = 0.0, we = 0.0, wd = 0.0;
+            double wa = 0.0, we = 0.0, wd = 0.0, wp = a.nsums == 4 ? 0.0 : 1.0;
 #pragma unroll 2  // (further, and the loads' registers spill)
             for (int s = 0; s < a.nsplit; ++s) {
-                const float *w = a.rowsum + int64_t(s) * 3 * n + at;
+                const float *w = a.rowsum + int64_t(s) * a.nsums * n + at;
                 wa += w[0], we += w[n], wd += w[2 * n];
+                if (a.nsums == 4) wp += w[3 * n];
             }
-            t += wa - wd * we;
+            if (wp != 0.0) t += (wa - wd * we / wp) / wp;
         }
     }
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
@@ -683,7 +688,8 @@ Pass plan_pass(const DeviceInfo &dev, const AttnArgs &a, int mode, AttnPath path
     const size_t n = size_t(p.a.nsplit), hrows = size_t(a.B) * a.H * a.Lq;
     p.part = n > 1 ? n * size_t(p.rows) * a.D * (dkv ? 2 : 1) : 0;
     p.ml = n > 1 && mode == ATTN_FWD ? n * 2 * hrows : 0;
-    p.floats = (p.part + p.ml + (slopes ? n * 3 * hrows + size_t(p.base) : 0) + 3) / 4 * 4;
+    p.a.nsums = path == PATH_TC ? 4 : 3;
+    p.floats = (p.part + p.ml + (slopes ? n * p.a.nsums * hrows + size_t(p.base) : 0) + 3) / 4 * 4;
     return p;
 }
 

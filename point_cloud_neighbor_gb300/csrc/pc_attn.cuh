@@ -55,10 +55,11 @@ struct AttnArgs {
     int nsplit;
     float *part;     // [nsplit][rows of the output][D] (DKV: dk, then dv)
     float *part_ml;  // FWD: [nsplit][2][B H Lq] (maximum in base-2 units, sum)
-    // DQ with slopes: per row sums of dS d2, P d2 and dS, [nsplit][3][B H Lq], each
-    // a LongSum of a few columns' sums; or
+    // DQ with slopes: per row sums of dS d2, P d2 and dS (and, nsums = 4, of P),
+    // [nsplit][nsums][B H Lq], each a LongSum of a few columns' sums; or
     // (tensor cores, one part) one number a block, [B H][tiles]
     float *rowsum;
+    int nsums;
     int device;
     int *status;
     uint64_t timeout_ns;

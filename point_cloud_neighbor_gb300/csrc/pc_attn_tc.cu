@@ -91,7 +91,7 @@ struct Cfg {
     static constexpr int STAGE = 2 * YBYTES + YAUG;
     // per stage: x, y, z, -lse, -delta of the streamed rows; flag, bias factor
     static constexpr int COLF = 5 * YR + 4;
-    static constexpr int ROWF = 2 * 6 * XR + 4;  // per unit: exchanged row values
+    static constexpr int ROWF = 2 * 8 * XR + 4;  // per unit: exchanged row values
     static constexpr size_t XSMEM = X_TMEM ? 0 : size_t(XT) * XBYTES;
     static constexpr size_t SMEM = 1024 + XSMEM + size_t(T) * XAUG +
                                    size_t(STAGES) * (STAGE + COLF * 4) + ROWF * 4 + 512;
@@ -165,7 +165,7 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
     unsigned char *Y = X + C::XSMEM;               // stage s: Y1, Y2, channels of the bias
     unsigned char *xaug = Y + size_t(STAGES) * C::STAGE;
     float *coldata = reinterpret_cast<float *>(xaug + T * C::XAUG);
-    float *rowdata = coldata + STAGES * C::COLF;   // [unit][6][XR]
+    float *rowdata = coldata + STAGES * C::COLF;   // [unit][8][XR]
     uint64_t *full = reinterpret_cast<uint64_t *>(rowdata + C::ROWF);
     uint64_t *empty = full + STAGES, *sfull = empty + STAGES, *pfull = sfull + C::NBUF;
     uint64_t *xfull = pfull + C::NBUF, *accfull = xfull + 1;
@@ -627,8 +627,8 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
         }
         float mc = -INFINITY;                        // FWD: the row's maximum, base 2
         float2 l2 = make_float2(0.0f, 0.0f);         // FWD: the row's sum
-        LongSum wa, we, wd;                          // DQ: the slope's sums
-        float *rd = rowdata + unit * 6 * XR + quad * 32 + lane;
+        LongSum wa, we, wd, wp;                      // DQ: the slope's sums
+        float *rd = rowdata + unit * 8 * XR + quad * 32 + lane;
         bool ok = true;
         int s = FWD ? 0 : unit, sbuf = unit;  // stage; BWD: score buffer
         unsigned phase = 0, sphase = 0;
@@ -728,7 +728,7 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
             } else if (BWD && live) {
                 auto weights = [&](auto tail_, auto direct_) {
                     constexpr bool TAIL = decltype(tail_)::value, DIRECT = decltype(direct_)::value;
-                    float2 ta = make_float2(0.0f, 0.0f), te = ta, td = ta;  // of the tile
+                    float2 ta = make_float2(0.0f, 0.0f), te = ta, td = ta, tp = ta;  // of the tile
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t r[16], g[16], p[8], plo[8], q[8], qlo[8];
@@ -765,6 +765,7 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
                                 }
                                 if (MODE == ATTN_DQ && DIRECT && sums) {
                                     td = __fadd2_rn(td, ds);
+                                    tp = __fadd2_rn(tp, u);
                                     ta = __ffma2_rn(ds, d[e], ta);
                                     te = __ffma2_rn(u, d[e], te);
                                 }
@@ -783,6 +784,7 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
                         wd.add(td.x + td.y);
                         wa.add(ta.x + ta.y);
                         we.add(te.x + te.y);
+                        wp.add(tp.x + tp.y);
                     }
                 };
                 constexpr std::true_type yes{};
@@ -812,21 +814,22 @@ __device__ __forceinline__ void attn_tc_pass(const AttnArgs &a, const AttnMaps &
         const int64_t hrows = int64_t(a.B) * a.H * a.Lq;
         const float one = FWD ? 1.0f : attn_ds_factor(nk);
         if (MODE == ATTN_DQ && BIAS) {
-            // the sums of a row's four groups, in the exchange buffer as [unit][half][3]
+            // the sums of a row's four groups, in the exchange buffer as [unit][half][4]
             if (sums) {
-                rd[(half * 3) * XR] = wa.value();
-                rd[(half * 3 + 1) * XR] = we.value();
-                rd[(half * 3 + 2) * XR] = wd.value();
+                rd[(half * 4) * XR] = wa.value();
+                rd[(half * 4 + 1) * XR] = we.value();
+                rd[(half * 4 + 2) * XR] = wd.value();
+                rd[(half * 4 + 3) * XR] = wp.value();
             }
             named_barrier_sync(1, C::CWARPS * 32);
             if (sums && unit == 0 && half == 0) {
-                float t[3];
+                float t[4];
 #pragma unroll
-                for (int e = 0; e < 3; ++e) {
-                    t[e] = (rd[e * XR] + rd[(3 + e) * XR]) + (rd[(6 + e) * XR] + rd[(9 + e) * XR]);
+                for (int e = 0; e < 4; ++e) {
+                    t[e] = (rd[e * XR] + rd[(4 + e) * XR]) + (rd[(8 + e) * XR] + rd[(12 + e) * XR]);
                     t[e] = row < nx ? one * t[e] : 0.0f;
                 }
-                put_slope_sums(a, t, split, hrow, row < LX, quad, lane, rowdata + 12 * XR, bid);
+                put_slope_sums(a, t, split, hrow, row < LX, quad, lane, rowdata + 16 * XR, bid);
             }
         }
         float l = l2.x + l2.y;

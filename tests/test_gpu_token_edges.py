@@ -333,6 +333,36 @@ def test_attention_slopes_gradient_does_not_lose_with_length(dtype, B, Lq, n, H,
           rel * B * Lq * (c1 + c2) / 2, "dslopes")
 
 
+@pytest.mark.parametrize("steepest", [8.0, 60.0])
+@pytest.mark.parametrize("Lq,Lk,H,Hkv,D", [(286, 286, 1, 1, 80), (300, 500, 8, 4, 64),
+                                           (1500, 1500, 4, 4, 64), (128, 4000, 4, 2, 128),
+                                           (1, 3000, 8, 8, 64), (50, 70, 4, 2, 36)])
+def test_attention_slopes_gradient_of_bfloat16_inputs_is_float32(Lq, Lk, H, Hkv, D,
+                                                                     steepest):
+    # It is float32 though the inputs are not: no further from the definition than one and a half
+    # times the elementary form in float32 is, or 1e-6 of it.  (The forward pass forms the bias
+    # through the products here, slope R^2 < 256, and its lse is off by 2^-20 slope R^2.)
+    q, k, v, do, kw = attn_inputs(1, Lq, Lk, H, Hkv, D, torch.bfloat16, True, None, None)
+    for n in ("query_xyz", "ref_xyz"):
+        kw[n] = kw[n] / kw[n].norm(dim=-1, keepdim=True)
+    if Lq == Lk:
+        kw["query_xyz"] = kw["ref_xyz"]
+    kw["slopes"] = steepest * 2.0 ** (-8.0 * torch.arange(H, device=DEV) / H)
+    out, lse = pc.pc_attention(q, k, v, return_lse=True, **kw)
+    got = pc.pc_attention_backward(do, q, k, v, out, lse, **kw)[3]
+    want = gradients64(q, k, v, do, kw)[3]
+    d2 = ((kw["query_xyz"][0][:, None] - kw["ref_xyz"][0][None]) ** 2).sum(-1)
+    plain = []
+    for h in range(H):
+        Q, K, V, g = (t.float() for t in (q[0, :, h], k[0, :, h * Hkv // H], v[0, :, h * Hkv // H],
+                                          do[0, :, h]))
+        P = torch.softmax((Q @ K.T) / math.sqrt(D) - kw["slopes"][h] * d2, 1)
+        dP = g @ V.T
+        plain.append(-(P * (dP - (P * dP).sum(1, keepdim=True)) * d2).sum())
+    error = norm_error(torch.stack(plain), want)
+    assert norm_error(got, want) <= max(1.5 * error, 1e-6)
+
+
 @pytest.mark.parametrize("side", ["out", "dv"])
 def test_attention_long_sums_on_the_tensor_cores_have_no_bias(side):
     # The tensor cores cut off what an addition leaves below their accumulator's last place: about
