@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
     }
     float acc[4][DP / 16], acc2[4][DP / 16];
     float mx[4], sum[4];
-    LongSum wa[4], we[4], wd[4];
+    LongSum wa[4], we[4], wd[4], wp[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
 #pragma unroll
@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
         } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                float ta = 0.0f, te = 0.0f, td = 0.0f;
+                float ta = 0.0f, te = 0.0f, td = 0.0f, tp = 0.0f;
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
                     const int c = tx + 16 * j;
@@ -253,11 +253,13 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
                         ta = fmaf(ds, d2[i][j], ta);
                         te = fmaf(p, d2[i][j], te);
                         td += ds;
+                        tp += p;
                     }
                     if (MODE == ATTN_DKV) P[(ty + 16 * i) * SP + c] = p;
                     S[(ty + 16 * i) * SP + c] = ds;
                 }
-                if (MODE == ATTN_DQ && bias) wa[i].add(ta), we[i].add(te), wd[i].add(td);
+                if (MODE == ATTN_DQ && bias)
+                    wa[i].add(ta), we[i].add(te), wd[i].add(td), wp[i].add(tp);
             }
         }
         __syncthreads();
@@ -280,17 +282,19 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
             for (int o = 8; o > 0; o >>= 1) sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], o);
         }
         if (MODE == ATTN_DQ && bias) {
-            float ta = one * wa[i].value(), te = we[i].value(), td = one * wd[i].value();
+            float ta = one * wa[i].value(), te = we[i].value(), td = one * wd[i].value(),
+                  tp = wp[i].value();
 #pragma unroll
             for (int o = 8; o > 0; o >>= 1) {
                 ta += __shfl_xor_sync(0xffffffffu, ta, o);
                 te += __shfl_xor_sync(0xffffffffu, te, o);
                 td += __shfl_xor_sync(0xffffffffu, td, o);
+                tp += __shfl_xor_sync(0xffffffffu, tp, o);
             }
             if (tx == 0 && r < LX && a.rowsum != nullptr) {
                 const int64_t n = int64_t(a.B) * a.H * a.Lq;
-                float *w = a.rowsum + int64_t(split) * 3 * n + hrow;
-                w[0] = ta, w[n] = te, w[2 * n] = td;
+                float *w = a.rowsum + int64_t(split) * 4 * n + hrow;
+                w[0] = ta, w[n] = te, w[2 * n] = td, w[3 * n] = tp;
             }
         }
         if (r >= LX) continue;
@@ -490,8 +494,8 @@ __global__ void __launch_bounds__(1024) attn_join_rows_kernel(const AttnArgs a) 
         if (t == 0 && a.lse != nullptr)
             a.lse[hrow] = any ? (m + log2f(l)) * ATTN_LN2 : -INFINITY;
     } else if (a.rowsum != nullptr) {
-        for (int e = 0; e < a.nsums; ++e) {
-            const float *w = a.rowsum + (int64_t(t) * a.nsums + e) * rows + hrow;
+        for (int e = 0; e < 4; ++e) {
+            const float *w = a.rowsum + (int64_t(t) * 4 + e) * rows + hrow;
             const float v = over(mine ? *w : 0.0f, false);
             if (t == 0) a.rowsum[e * rows + hrow] = v;
         }
@@ -532,12 +536,13 @@ void launch_join(const AttnArgs &a, int mode, int64_t rows, cudaStream_t st) {
 }
 
 // dslope_h = -sum over rows of (dS d2 - (dS) (P d2)), each row's sums joined
-// over the parts first: a block per head, float64, a fixed order.  A row's
-// exact dS sum to 0; what they sum to here is the error of delta (from an
-// output rounded to its type), and the second term takes its effect out.  Where the
-// sum of P is there (bfloat16 on the tensor cores) the row's P are divided by it: the
-// forward pass may have formed the bias through the products and this one from
-// differences, and the row's lse is then off by up to 2^-20 slope R^2.
+// over the parts first: a block per head, float64 over the rows (the GPU has few
+// such units: 4 x 1021 rows of 6 heads take 13 us, with float64 in a row too 59), a
+// fixed order.  A row's exact dS sum to 0; what they sum to here is the error of
+// delta, and the second term takes its effect out.  The row's P are divided by what
+// they sum to: lse, from which they come, is rounded to float32 (3e-7 of a weight at
+// lse = 8), and where the forward pass formed the bias through the products and this
+// one from differences it is off by up to 2^-20 slope R^2.
 // With `tiles` the sums are already one number for each tile of a head's rows.
 __global__ void __launch_bounds__(1024)
 attn_slope_kernel(const AttnArgs a, int tiles, float *dslopes) {
@@ -551,14 +556,12 @@ attn_slope_kernel(const AttnArgs a, int tiles, float *dslopes) {
     } else {
         for (int64_t r = threadIdx.x; r < int64_t(a.B) * a.Lq; r += 1024) {
             const int64_t b = r / a.Lq, at = (b * a.H + h) * a.Lq + (r - b * a.Lq);
-            double wa = 0.0, we = 0.0, wd = 0.0, wp = a.nsums == 4 ? 0.0 : 1.0;
+            LongSum w[4];
 #pragma unroll 2  // (further, and the loads' registers spill)
-            for (int s = 0; s < a.nsplit; ++s) {
-                const float *w = a.rowsum + int64_t(s) * a.nsums * n + at;
-                wa += w[0], we += w[n], wd += w[2 * n];
-                if (a.nsums == 4) wp += w[3 * n];
-            }
-            if (wp != 0.0) t += (wa - wd * we / wp) / wp;
+            for (int s = 0; s < a.nsplit; ++s)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) w[e].add(a.rowsum[(int64_t(s) * 4 + e) * n + at]);
+            t += double(attn_slope_row(w[0].value(), w[1].value(), w[2].value(), w[3].value()));
         }
     }
     for (int o = 16; o > 0; o >>= 1) t += __shfl_xor_sync(0xffffffffu, t, o);
@@ -688,8 +691,7 @@ Pass plan_pass(const DeviceInfo &dev, const AttnArgs &a, int mode, AttnPath path
     const size_t n = size_t(p.a.nsplit), hrows = size_t(a.B) * a.H * a.Lq;
     p.part = n > 1 ? n * size_t(p.rows) * a.D * (dkv ? 2 : 1) : 0;
     p.ml = n > 1 && mode == ATTN_FWD ? n * 2 * hrows : 0;
-    p.a.nsums = path == PATH_TC ? 4 : 3;
-    p.floats = (p.part + p.ml + (slopes ? n * p.a.nsums * hrows + size_t(p.base) : 0) + 3) / 4 * 4;
+    p.floats = (p.part + p.ml + (slopes ? n * 4 * hrows + size_t(p.base) : 0) + 3) / 4 * 4;
     return p;
 }
 

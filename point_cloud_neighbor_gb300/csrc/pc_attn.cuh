@@ -55,11 +55,10 @@ struct AttnArgs {
     int nsplit;
     float *part;     // [nsplit][rows of the output][D] (DKV: dk, then dv)
     float *part_ml;  // FWD: [nsplit][2][B H Lq] (maximum in base-2 units, sum)
-    // DQ with slopes: per row sums of dS d2, P d2 and dS (and, nsums = 4, of P),
-    // [nsplit][nsums][B H Lq], each a LongSum of a few columns' sums; or
+    // DQ with slopes: per row sums of dS d2, P d2, dS and P, [nsplit][4][B H Lq], each
+    // a LongSum of a few columns' sums; or
     // (tensor cores, one part) one number a block, [B H][tiles]
     float *rowsum;
-    int nsums;
     int device;
     int *status;
     uint64_t timeout_ns;
@@ -84,6 +83,12 @@ struct LongSum {
     }
     __device__ __forceinline__ float value() const { return s; }
 };
+
+// What a row adds to -dslope: its sums of dS d2, P d2, dS and P, the P made to add up
+// to 1.
+__device__ __forceinline__ float attn_slope_row(float a, float e, float d, float p) {
+    return p == 0.0f ? 0.0f : fmaf(-d, e / p, a) / p;
+}
 
 // Whether a query row has anything to attend to, which the lengths alone decide:
 // its sum of weights may be NaN (a NaN in a valid row or key, a score that

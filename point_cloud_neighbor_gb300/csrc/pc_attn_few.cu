@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(FEW_THREADS, R == 1 ? 3 : R == 2 ? 2 : 1)
 few_backward_kernel(const AttnArgs a) {
     constexpr int V = 16 / sizeof(T), KPW = 32 / LPK, STEP = FEW_WARPS * KPW;
     constexpr int U = 2;
-    __shared__ float sm[FEW_WARPS][R][LPK * V + 3];
+    __shared__ float sm[FEW_WARPS][R][LPK * V + 4];
     const FewBlock w = few_block(a, STEP);
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     const int gl = lane % LPK, c0 = gl * V;
@@ -242,7 +242,7 @@ few_backward_kernel(const AttnArgs a) {
     const float c2 = a.scale * ATTN_LOG2E;
     // q times scale: the scores need it, and so do the keys' gradients
     float q[R][V], go[R][V], px[R][3], ws[R], lse2[R], del[R], dq[R][V];
-    LongSum wa[R], we[R], wd[R];
+    LongSum wa[R], we[R], wd[R], wp[R];
     unsigned live = 0;  // a bit a row: the others take no part, whatever the keys hold
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -324,6 +324,7 @@ few_backward_kernel(const AttnArgs a) {
                 wa[r].add(ds * d2);
                 we[r].add(p * d2);
                 wd[r].add(ds);
+                wp[r].add(p);
 #pragma unroll
                 for (int e = 0; e < V; ++e) {
                     dq[r][e] = fmaf(ds, kx[e], dq[r][e]);
@@ -346,12 +347,13 @@ few_backward_kernel(const AttnArgs a) {
     if (a.dq == nullptr) return;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-        float ta = wa[r].value(), te = we[r].value(), td = wd[r].value();
+        float ta = wa[r].value(), te = we[r].value(), td = wd[r].value(), tp = wp[r].value();
 #pragma unroll
         for (int o = LPK; o < 32; o <<= 1) {
             ta += __shfl_xor_sync(0xffffffffu, ta, o);
             te += __shfl_xor_sync(0xffffffffu, te, o);
             td += __shfl_xor_sync(0xffffffffu, td, o);
+            tp += __shfl_xor_sync(0xffffffffu, tp, o);
 #pragma unroll
             for (int e = 0; e < V; ++e) dq[r][e] += __shfl_xor_sync(0xffffffffu, dq[r][e], o);
         }
@@ -362,11 +364,12 @@ few_backward_kernel(const AttnArgs a) {
             sm[warp][r][LPK * V] = ta;
             sm[warp][r][LPK * V + 1] = te;
             sm[warp][r][LPK * V + 2] = td;
+            sm[warp][r][LPK * V + 3] = tp;
         }
     }
     __syncthreads();
     const int64_t hrows = int64_t(a.B) * a.H * a.Lq;
-    const int per = a.D + (a.rowsum != nullptr ? 3 : 0);
+    const int per = a.D + (a.rowsum != nullptr ? 4 : 0);
     for (int t = threadIdx.x; t < rows * per; t += FEW_THREADS) {
         const int r = t / per, c = t - r * per;
         const int g = r / a.Lq, i = r - g * a.Lq, h = w.hk * G + g;
@@ -377,7 +380,7 @@ few_backward_kernel(const AttnArgs a) {
         const int64_t orow = (int64_t(w.b) * a.Lq + i) * a.H + h;
         const int64_t hrow = (int64_t(w.b) * a.H + h) * a.Lq + i;
         if (c >= a.D) {
-            a.rowsum[(int64_t(w.split) * 3 + c - a.D) * hrows + hrow] = v;
+            a.rowsum[(int64_t(w.split) * 4 + c - a.D) * hrows + hrow] = v;
         } else if (a.nsplit > 1) {
             a.part[(int64_t(w.split) * hrows + orow) * a.D + c] = v;
         } else {

@@ -50,24 +50,19 @@ __device__ __forceinline__ void dist4(const float *cd, int c, float2 nx, float2 
 // The slopes' sums of a block's 128 rows, a thread each in four warps: with one
 // part the rows' values are complete and added up here, one number a block
 // (`red`: 4 floats); else the rows' sums go to their part.
-template <int N>
-__device__ __forceinline__ void put_slope_sums(const AttnArgs &a, const float (&t)[N], int split,
+__device__ __forceinline__ void put_slope_sums(const AttnArgs &a, const float (&t)[4], int split,
                                                int64_t hrow, bool in, int quad, int lane,
                                                float *red, unsigned bid) {
     if (a.nsplit > 1) {
         const int64_t n = int64_t(a.B) * a.H * a.Lq;
         if (in) {
-            float *o = a.rowsum + int64_t(split) * N * n + hrow;
+            float *o = a.rowsum + int64_t(split) * 4 * n + hrow;
 #pragma unroll
-            for (int e = 0; e < N; ++e) o[e * n] = t[e];
+            for (int e = 0; e < 4; ++e) o[e * n] = t[e];
         }
         return;
     }
-    float v;
-    if (N == 4)
-        v = t[N - 1] == 0.0f ? 0.0f : fmaf(-t[2], t[1] / t[N - 1], t[0]) / t[N - 1];
-    else
-        v = fmaf(-t[2], t[1], t[0]);
+    float v = attn_slope_row(t[0], t[1], t[2], t[3]);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
     if (lane == 0) red[quad] = v;

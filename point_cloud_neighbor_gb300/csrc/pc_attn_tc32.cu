@@ -421,7 +421,7 @@ __device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMap
         }
         float mc = -INFINITY;
         float2 l2 = make_float2(0.0f, 0.0f);
-        LongSum wa, we, wd;  // DQ: the slope's sums
+        LongSum wa, we, wd, wp;  // DQ: the slope's sums
         const bool sums = MODE == ATTN_DQ && BIAS && a.rowsum != nullptr;
         float *rd = rowdata + quad * 32 + lane;
         float acc[C::NACC][DP / 2];
@@ -515,7 +515,7 @@ __device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMap
                     tmem_st8(sb + 64 + 8 * i, p[2]);
                 }
             } else if (BWD && live) {
-                float2 ta = make_float2(0.0f, 0.0f), te = ta, td = ta;  // of the tile
+                float2 ta = make_float2(0.0f, 0.0f), te = ta, td = ta, tp = ta;  // of the tile
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     const int i = 2 * half + h;
@@ -550,6 +550,7 @@ __device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMap
                             if (col + 1 >= valid) u.y = ds.y = 0.0f;
                             if (sums) {
                                 td = __fadd2_rn(td, ds);
+                                tp = __fadd2_rn(tp, u);
                                 ta = __ffma2_rn(ds, d[e], ta);
                                 te = __ffma2_rn(u, d[e], te);
                             }
@@ -570,6 +571,7 @@ __device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMap
                     wd.add(td.x + td.y);
                     wa.add(ta.x + ta.y);
                     we.add(te.x + te.y);
+                    wp.add(tp.x + tp.y);
                 }
             }
             // the sums of the tile before leave tensor memory before this
@@ -597,12 +599,14 @@ __device__ __forceinline__ void attn_tc32_pass(const AttnArgs &a, const SplitMap
                 rd[0] = wa.value();
                 rd[XR] = we.value();
                 rd[2 * XR] = wd.value();
+                rd[3 * XR] = wp.value();
             }
             named_barrier_sync(1, C::CWARPS * 32);
             if (sums && half == 0) {
-                float t[3] = {wa.value() + rd[0], we.value() + rd[XR], wd.value() + rd[2 * XR]};
+                float t[4] = {wa.value() + rd[0], we.value() + rd[XR], wd.value() + rd[2 * XR],
+                              wp.value() + rd[3 * XR]};
 #pragma unroll
-                for (int e = 0; e < 3; ++e) t[e] = row < nx ? one * t[e] : 0.0f;
+                for (int e = 0; e < 4; ++e) t[e] = row < nx ? one * t[e] : 0.0f;
                 put_slope_sums(a, t, split, hrow, row < LX, quad, lane, rowdata + 6 * XR, bid);
             }
         }

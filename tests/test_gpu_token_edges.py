@@ -363,6 +363,33 @@ def test_attention_slopes_gradient_of_bfloat16_inputs_is_float32(Lq, Lk, H, Hkv,
     assert norm_error(got, want) <= max(1.5 * error, 1e-6)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("B,Lq,Lk,H,D,Hkv", [(8, 900, 900, 1, 100, 1), (6, 1100, 1100, 1, 64, 1),
+                                             (24, 1, 900, 2, 64, 2), (8, 40, 600, 1, 128, 1),
+                                             (1, 128, 4000, 4, 128, 2)])
+def test_attention_slopes_gradient_over_clouds_that_cancel(B, Lq, Lk, H, D, Hkv, dtype):
+    # The rows' parts have either sign, so what an lse rounded to float32 does to a row's weights (3e-7
+    # of them at lse = 8) is not small against their sum.  As above: one and a half times the
+    # elementary form's error, or 1e-6.
+    q, k, v, do, kw = attn_inputs(B, Lq, Lk, H, Hkv, D, dtype, True, None, None)
+    for n in ("query_xyz", "ref_xyz"):
+        kw[n] = kw[n] / kw[n].norm(dim=-1, keepdim=True)
+    kw["slopes"] = 8.0 * 2.0 ** (-8.0 * torch.arange(H, device=DEV) / H)
+    out, lse = pc.pc_attention(q, k, v, return_lse=True, **kw)
+    got = pc.pc_attention_backward(do, q, k, v, out, lse, **kw)[3]
+    want = gradients64(q, k, v, do, kw)[3]
+    d2 = ((kw["query_xyz"][:, :, None] - kw["ref_xyz"][:, None]) ** 2).sum(-1)
+    plain = []
+    for h in range(H):
+        Q, K, V, g = (t.float() for t in (q[:, :, h], k[:, :, h * Hkv // H], v[:, :, h * Hkv // H],
+                                          do[:, :, h]))
+        P = torch.softmax((Q @ K.transpose(1, 2)) / math.sqrt(D) - kw["slopes"][h] * d2, 2)
+        dP = g @ V.transpose(1, 2)
+        plain.append(-(P * (dP - (P * dP).sum(2, keepdim=True)) * d2).sum())
+    error = norm_error(torch.stack(plain), want)
+    assert norm_error(got, want) <= max(1.5 * error, 1e-6)
+
+
 @pytest.mark.parametrize("side", ["out", "dv"])
 def test_attention_long_sums_on_the_tensor_cores_have_no_bias(side):
     # The tensor cores cut off what an addition leaves below their accumulator's last place: about
