@@ -24,7 +24,7 @@
 // of 8, by 0.6 at 2, where a result rounded once has 0.0017).  So a forward pass
 // can write what the rounding left as a second bfloat16 array, `low`, for 2 bytes
 // an element, and delta adds it.  A backward call without it runs the forward pass
-// again for both arrays (4096 tokens, 16 + 4 heads of 128: 164 us on 572).
+// again for both arrays (4096 tokens, 16 + 4 heads of 128: 752 us instead of 585).
 #pragma once
 
 #include "pc_internal.h"
@@ -72,8 +72,8 @@ __device__ __forceinline__ int attn_len(const int64_t *len, int b, int L) {
 
 // A float32 sum of any length: what an addition rounds away is taken from the next
 // number (Kahan's sum: off by 2 units of the sum of magnitudes, whatever the
-// length).  For the slopes' gradient, whose terms are as many as pairs: a plain chain
-// over 131,072 keys was off by 2^-13 of it.
+// length).  For the slopes' gradient, whose terms are as many as pairs: plain chains
+// over 65,536 equal terms were off by 1.6e-4 of their sum.
 struct LongSum {
     float s = 0.0f, over = 0.0f;
     __device__ __forceinline__ void add(float v) {

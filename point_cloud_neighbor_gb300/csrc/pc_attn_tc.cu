@@ -39,18 +39,21 @@
 // streamed tile past the length (they would meet weights that are 0, and 0
 // times NaN is NaN) are overwritten with zeros in shared memory.
 //
-// Measured, 4864 queries and keys, 16 heads: 64 channels, forward 137 us (706
-// TFLOP/s of 4 D a score; with the bias 195 us), both backward passes 316 us
-// (766 TFLOP/s of 10 D; 395 us); 128 channels 169 us (1149; 223 us) and 564 us
-// (859; 626 us).  The weights' threads issue on 60% of the cycles, the tensor
-// cores' math is active 40 to 50%.  The products are small (128 x 64 x 16), so
+// Measured, 4864 queries and keys, 16 heads: 64 channels, forward 137 us (707
+// TFLOP/s of 4 D a score; with the bias 165 us), both backward passes with delta 370
+// us (655 TFLOP/s of 10 D; 441 us, with the slopes' gradient 571 us); 128 channels 169
+// us (1147; 207 us) and 640 us (757; 719 and 822 us).  The weights' threads issue on
+// 60% of the cycles, the tensor cores' math is active 40 to 50%.  The products are small (128 x 64 x 16), so
 // what issues them matters: from a branch on a lane index each took 80 to 150
 // cycles, from an elected lane 30 to 70, from one thread that runs the whole
 // loop they are limited by the tensor cores' queue.
 //
-// Every wait is bounded: when one runs out the block raises the status word,
-// lets its copies and products finish, frees its tensor memory and returns;
-// its outputs are then unspecified.
+// Every wait on a barrier is bounded: when one runs out the block raises the status
+// word, lets its copies and products finish, frees its tensor memory and returns;
+// its outputs are then unspecified.  The allocation of tensor memory has no bound
+// of its own: it waits while another block on the SM holds some.  No two blocks of
+// these kernels fit one SM, so that can only be another library's kernel, and for
+// as long as that runs.
 #include "pc_attn_tc.cuh"
 #include "pointcloud.h"
 
@@ -96,6 +99,7 @@ struct Cfg {
     static constexpr size_t SMEM = 1024 + XSMEM + size_t(T) * XAUG +
                                    size_t(STAGES) * (STAGE + COLF * 4) + ROWF * 4 + 512;
     static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(SMEM > 114 * 1024, "one block a SM: none waits for tensor memory");
 };
 
 // A number as three bfloat16, the low one of what the others leave.

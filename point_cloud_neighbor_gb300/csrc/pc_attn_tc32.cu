@@ -22,10 +22,13 @@
 // is formed from coordinates' differences.
 //
 // Bound: the products, six times those of bfloat16.  Measured, 4 x 1021 tokens,
-// 6 heads of 48 padded to 64: forward 60 us, both backward passes 172 us (258
-// and 930 us in float32 instructions); 2 x 2048, 8 heads of 96: 223 us forward.
+// 6 heads of 48 padded to 64: forward 60 us, both backward passes 162 us (258
+// and 930 us in float32 instructions); 2 x 2048, 8 heads of 96: 227 us forward.
+// Short clouds are the other way round: 32 x 64 tokens, 8 heads of 64, forward 21 us
+// and 15 in float32 instructions; 4 x 128 of 64 15 and 13, of 128 22 and 17.
 //
-// Lengths, waits and their end as in pc_attn_tc.cu.
+// Lengths, waits and their end, and the allocation of tensor memory, as in
+// pc_attn_tc.cu.
 #include "pc_attn_tc.cuh"
 #include "pointcloud.h"
 
@@ -59,6 +62,7 @@ struct Cfg32 {
     static constexpr size_t SMEM =
         1024 + XSMEM + size_t(STAGES) * (STAGE + COLF * 4) + ROWF * 4 + 512;
     static_assert(SMEM <= 227 * 1024, "shared memory");
+    static_assert(SMEM > 114 * 1024, "one block a SM: none waits for tensor memory");
 };
 
 // The six products, the smallest first: part of the one, part of the other.
