@@ -483,7 +483,8 @@ int pc_gather_points(const float *xyz, int64_t B, int64_t N,
  * tokens runs, forward and backward.
  *
  * Elements are float32 or bfloat16 (pc_dtype); every sum, statistic and
- * softmax is float32, and a result is rounded to its type once.  Strides are
+ * softmax is float32, and a result is rounded to its type once (the products of
+ * bfloat16 attention take the weights in two parts, to 2^-17).  Strides are
  * in elements, given as {batch, token, head} of a [B, L, heads, D] array
  * whose last axis is contiguous (a slice of a fused projection, say), or
  * NULL for a packed array.  Outputs and gradients are packed.  Results do

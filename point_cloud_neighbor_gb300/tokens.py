@@ -391,5 +391,10 @@ def attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, *,
     """Differentiable :func:`pc_attention` (q, k, v and slopes, once; the
     positions get no gradient and must not ask for one)."""
     _no_gradient(query_xyz=query_xyz, ref_xyz=ref_xyz)
+    if not torch.is_grad_enabled() or not any(
+            isinstance(t, torch.Tensor) and t.requires_grad for t in (q, k, v, slopes)):
+        # nothing to keep for a backward pass
+        return pc_attention(q, k, v, scale=scale, query_xyz=query_xyz, ref_xyz=ref_xyz,
+                            slopes=slopes, query_lengths=query_lengths, ref_lengths=ref_lengths)
     return _Attention.apply(q, k, v, slopes, scale, query_xyz, ref_xyz, query_lengths,
                             ref_lengths)

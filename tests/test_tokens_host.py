@@ -171,3 +171,21 @@ def test_a_scale_that_float32_does_not_hold_is_refused(L):
     for scale in (1e-50, 1e-39, 2e30, 0.0, float("nan")):
         assert forward(scale) == 1
         assert "scale" in L.pc_last_error_message().decode()
+
+
+def test_attention_keeps_nothing_where_no_gradient_is_asked(stand_ins, monkeypatch):
+    asked, plain = [], tokens.pc_attention
+
+    def attention(q, k, v, **kw):
+        asked.append((kw.pop("return_lse", False), kw.pop("return_low", False)))
+        out = plain(q, k, v, **kw)
+        return out if asked[-1][0] else out[0]
+
+    monkeypatch.setattr(tokens, "pc_attention", attention)
+    q, k, v = (_leaf(1, 4, 2, 8, seed=i) for i in (4, 5, 6))
+    want = tokens.attention(q, k, v)
+    with torch.no_grad():
+        a = tokens.attention(q, k, v)
+    b = tokens.attention(*(t.detach() for t in (q, k, v)))
+    assert asked == [(True, True), (False, False), (False, False)]
+    assert want.requires_grad and torch.equal(a, want) and torch.equal(b, want)
