@@ -344,14 +344,14 @@ __global__ void __launch_bounds__(ST) attn_simt_kernel(const AttnArgs a, const b
     }
 }
 
-// delta_i = (out_i + low_i) . dout_i, and lse in base-2 units with +inf for rows without
-// keys (their weights 2^(z - lse2) are then 0): LPR lanes per (token, head), V
-// channels at a time.  (16 x 1024 tokens, 8 heads of 64 in bfloat16: a warp per
+// delta_i = (out_i + low_i) . dout_i, and lse in base-2 units with +inf for rows
+// without keys (their weights 2^(z - lse2) are then 0): LPR lanes per (token, head),
+// V channels at a time.  (16 x 1024 tokens, 8 heads of 64 in bfloat16: a warp per
 // row and one channel a load 32 us, 8 lanes per row 5 us.)
 template <class T, int V, int LPR>
 __global__ void __launch_bounds__(256)
-attn_delta_kernel(const T *out, const T *low, const T *go, const float *lse, int64_t rows, int Lq, int H,
-                  int D, float *delta, float *lse2) {
+attn_delta_kernel(const T *out, const T *low, const T *go, const float *lse, int64_t rows,
+                  int Lq, int H, int D, float *delta, float *lse2) {
     const int64_t row = (int64_t(blockIdx.x) * 256 + threadIdx.x) / LPR;  // (b Lq + i) H + h
     const int lane = threadIdx.x % LPR;
     float s = 0.0f;
