@@ -31,9 +31,9 @@
 // up to 2^-8 of a term (the output's and dv's error against float64 0.0024
 // instead of 0.0017, which is the rounding of the result): P is written as the
 // sum of two bfloat16 (2^-17) and multiplied twice.  So is dS: in one bfloat16,
-// at any number of rows, dq and dk would be off by 0.0024 too (it would save 11 to
-// 15% of the backward pass).  The sums of P, the statistics and all accumulators are float32, and the slopes'
-// gradient uses the unrounded weights.
+// at any number of rows, dq and dk would be off by 0.0024 too (it would save 9 to
+// 15% of the backward pass).  The sums of P, the statistics and all accumulators
+// are float32, and the slopes' gradient uses the unrounded weights.
 //
 // What lies past a cloud's length is masked in the weights; rows of a
 // streamed tile past the length (they would meet weights that are 0, and 0
@@ -43,10 +43,10 @@
 // TFLOP/s of 4 D a score; with the bias 165 us), both backward passes with delta 370
 // us (655 TFLOP/s of 10 D; 441 us, with the slopes' gradient 571 us); 128 channels 169
 // us (1147; 207 us) and 640 us (757; 719 and 822 us).  The weights' threads issue on
-// 60% of the cycles, the tensor cores' math is active 40 to 50%.  The products are small (128 x 64 x 16), so
-// what issues them matters: from a branch on a lane index each took 80 to 150
-// cycles, from an elected lane 30 to 70, from one thread that runs the whole
-// loop they are limited by the tensor cores' queue.
+// 60% of the cycles, the tensor cores' math is active on about 40%.  The products
+// are small (128 x 64 x 16), so what issues them matters: from a branch on a lane
+// index each took 80 to 150 cycles, from an elected lane 30 to 70, from one thread
+// that runs the whole loop they are limited by the tensor cores' queue.
 //
 // Every wait on a barrier is bounded: when one runs out the block raises the status
 // word, lets its copies and products finish, frees its tensor memory and returns;
