@@ -285,7 +285,7 @@ def _own_embedding(st):
     import point_cloud_neighbor_gb300 as pc
     out = {"y": pc.pc_embedding(st["table"], st["ids"], st["scale"])}
     if st["case"]["train"]:
-        out["dtable"] = pc.pc_embedding_backward(st["dy"], st["ids"], st["case"]["V"],
+        out["dtable"] = pc.pc_embedding_backward(st["dy"], st["ids"], st["table"].shape,
                                                  st["scale"])
     return out
 
