@@ -635,6 +635,115 @@ int pc_attention_backward_ex(const void *grad_out, const void *q, const void *k,
                              void *grad_q, void *grad_k, void *grad_v, float *grad_slopes,
                              void *stream);
 
+/* ------------------------------------------------------------------------
+ * Operators over the features of points: what a network over point tokens
+ * runs around attention.  Elements, sums, rounding, pointers and streams as
+ * for the token operators above; arrays are packed; results do not change
+ * from run to run.
+ * ---------------------------------------------------------------------- */
+
+/* silu(z) = z / (1 + exp(-z)), gelu(z) = z Phi(z) with the normal
+ * distribution's Phi, relu(z) = max(z, 0) (derivative 0 at 0), sigmoid(z) =
+ * 1 / (1 + exp(-z)).  A NaN stays a NaN. */
+typedef enum pc_activation {
+    PC_ACT_NONE = 0,
+    PC_ACT_SILU = 1,
+    PC_ACT_GELU = 2,
+    PC_ACT_RELU = 3,
+    PC_ACT_SIGMOID = 4
+} pc_activation;
+
+/*
+ * Group norm of channels-last features, over each cloud's valid points, with
+ * an activation:
+ *   group g of cloud b: the values x[b, i, c], i < lengths[b], of the
+ *   C / groups consecutive channels c of the group; mean and var of these,
+ *   rstd = 1 / sqrt(var + eps);
+ *   out = act(z),  z = (x - mean) * rstd * weight[c] + bias[c].
+ *
+ *   x, out     [B, L, C] of dtype; groups divides C.  C <= 16384
+ *              (PC_ERR_UNSUPPORTED above).
+ *   weight, bias  [C] of param_dtype (PC_F32, or the same as dtype), or NULL
+ *              (1, 0).
+ *   lengths    [B] int64, device, or NULL (= L); clamped to [0, L].  What
+ *              lies past a length is not read into any result, whatever its
+ *              values; out is 0 there.
+ *   out_mean, out_rstd  [B, groups] float32, or both NULL; 0 for a cloud
+ *              without valid points.
+ *
+ * pc_group_norm_backward, from the mean and rstd of the forward call:
+ *   d = grad_out * act'(z),  xhat = (x - mean) rstd,  g = d * weight,
+ *   grad_x = rstd (g - mean(g) - xhat mean(g xhat)), means over the group,
+ *   grad_weight = sum over clouds and valid points of d xhat, grad_bias of d.
+ * grad_x is 0 past the lengths.  grad_x, grad_weight and grad_bias ([C] of
+ * param_dtype) may be NULL.
+ *
+ * Scratch (the library's stream-ordered pool): at most 16 C float32 for each SM
+ * (8 blocks, two sums a channel), 4 float32 for each group and cloud, and 2 B C
+ * float32 in the backward call.
+ */
+int pc_group_norm(const void *x, int dtype, int64_t B, int64_t L, int64_t C, int64_t groups,
+                  const void *weight, const void *bias, int param_dtype, double eps,
+                  int activation, const int64_t *lengths, void *out, float *out_mean,
+                  float *out_rstd, void *stream);
+
+int pc_group_norm_backward(const void *grad_out, const void *x, int dtype, int64_t B,
+                           int64_t L, int64_t C, int64_t groups, const float *mean,
+                           const float *rstd, const void *weight, const void *bias,
+                           int param_dtype, int activation, const int64_t *lengths,
+                           void *grad_x, void *grad_weight, void *grad_bias, void *stream);
+
+/*
+ * Lookup of feature rows, scaled:
+ *   out[b, t, :] = scale * table[b, idx[b, t], :], or zeros for idx = -1 (a
+ *   neighbour that kNN or Ball Query did not find).
+ * One table for all indices is B = 1.
+ *
+ *   table      [B, V, C] of dtype; idx [B, T] int64; out [B, T, C].
+ *   Other out-of-range indices give zeros and set PC_ERR_INVALID_ARGUMENT in
+ *   the device status word.  scale is finite.
+ *
+ * pc_embedding_backward writes grad_table [B, V, C] in full:
+ *   grad_table[b, v, :] = scale * sum of grad_out[b, t, :] over idx[b, t] = v.
+ * The tokens are sorted by their row and added in float32, those of a row in
+ * the order of t (runs of 64 at a time where a row has more).
+ *
+ * B V and B T are below 2^31 - 2^20 in the backward call (PC_ERR_UNSUPPORTED
+ * above); scratch there: 24 bytes a token, and 4 C bytes for every 64 tokens.
+ */
+int pc_embedding(const void *table, int dtype, int64_t B, int64_t V, int64_t C,
+                 const int64_t *idx, int64_t T, double scale, void *out, void *stream);
+
+int pc_embedding_backward(const void *grad_out, int dtype, int64_t B, int64_t V, int64_t C,
+                          const int64_t *idx, int64_t T, double scale, void *grad_table,
+                          void *stream);
+
+/*
+ * Gated projection, the first half of a gated feed-forward block:
+ *   a = x w_gate^T + b_gate,  u = x w_up^T + b_up,  out = act(a) * u.
+ *
+ *   x          [rows, C]; w_gate, w_up [F, C] (the layout of a linear layer);
+ *              b_gate, b_up [F], both or neither (NULL); out [rows, F]; all of
+ *              dtype.
+ *
+ * pc_gated_linear_backward takes the same arguments and grad_out [rows, F]:
+ *   da = grad_out * u * act'(a),  du = grad_out * act(a),
+ *   grad_x = da w_gate + du w_up,  grad_w_gate = da^T x,  grad_w_up = du^T x,
+ *   grad_b_gate, grad_b_up = sums of da and du over the rows.
+ * It forms a and u again, so that nothing but the arguments is kept between
+ * the calls.  Outputs may be NULL: grad_x; grad_w_gate and grad_w_up together;
+ * grad_b_gate and grad_b_up together.
+ */
+int pc_gated_linear(const void *x, int dtype, int64_t rows, int64_t C, int64_t F,
+                    const void *w_gate, const void *w_up, const void *b_gate,
+                    const void *b_up, int activation, void *out, void *stream);
+
+int pc_gated_linear_backward(const void *grad_out, const void *x, int dtype, int64_t rows,
+                             int64_t C, int64_t F, const void *w_gate, const void *w_up,
+                             const void *b_gate, const void *b_up, int activation,
+                             void *grad_x, void *grad_w_gate, void *grad_w_up,
+                             void *grad_b_gate, void *grad_b_up, void *stream);
+
 /*
  * Device status word.  Kernels that wait on other thread blocks bound every
  * wait; when a wait runs out they record PC_ERR_DEVICE_TIMEOUT here (the

@@ -1,7 +1,9 @@
 """GB300-native dense point-cloud neighbor search (FPS, kNN, Ball Query) and
 the operators built on it (exact grid search, Chamfer distance, PointNet++
-feature propagation, neighbor gather), and the operators a transformer over
-point tokens runs (layer norm, rotary positions, attention; ``.tokens``).
+feature propagation, neighbor gather), the operators a transformer over point
+tokens runs (layer norm, rotary positions, attention; ``.tokens``), and those
+over the points' features around it (group norm, gated projection, lookup of
+rows; ``.features``).
 
 The compute lives in libpointcloud.so (CUDA kernels for sm_103a behind the C
 ABI of include/pointcloud.h); this package holds its ctypes binding, the
@@ -23,6 +25,9 @@ from .binding import (PC_FPS_AUTO, PC_FPS_BLOCK, PC_FPS_CLUSTER, PC_FPS_GRID,
                       pc_fps_sm_count, pc_fps_plan, pc_three_interpolate,
                       pc_three_interpolate_backward, three_interpolate,
                       three_nn)
+from .features import (embedding, gated_linear, group_norm, pc_embedding,
+                       pc_embedding_backward, pc_gated_linear, pc_gated_linear_backward,
+                       pc_group_norm, pc_group_norm_backward)
 from .tokens import (attention, layer_norm, pc_attention, pc_attention_backward,
                      pc_layer_norm, pc_layer_norm_backward, pc_rotary, rotary)
 
@@ -40,4 +45,7 @@ __all__ = [
     "pc_knn_ball_query", "pc_knn_ball_query_plan", "pc_fps_set_batched",
     "pc_layer_norm", "pc_layer_norm_backward", "layer_norm", "pc_rotary", "rotary",
     "pc_attention", "pc_attention_backward", "attention",
+    "pc_group_norm", "pc_group_norm_backward", "group_norm", "pc_gated_linear",
+    "pc_gated_linear_backward", "gated_linear", "pc_embedding", "pc_embedding_backward",
+    "embedding",
 ]
