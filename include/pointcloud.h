@@ -724,7 +724,8 @@ int pc_embedding_backward(const void *grad_out, int dtype, int64_t B, int64_t V,
  *
  *   x          [rows, C]; w_gate, w_up [F, C] (the layout of a linear layer);
  *              b_gate, b_up [F], both or neither (NULL); out [rows, F]; all of
- *              dtype.
+ *              dtype.  rows <= 2^30, C <= 16384, F <= 65536 (PC_ERR_UNSUPPORTED
+ *              above).
  *
  * pc_gated_linear_backward takes the same arguments and grad_out [rows, F]:
  *   da = grad_out * u * act'(a),  du = grad_out * act(a),
@@ -776,6 +777,8 @@ int pc_device_status(void *stream, int reset, int32_t *out_status);
  *                         tensor-core attention launch (forward, backward)
  *                         never issues the copies of its streamed side.
  *                         That block's outputs are unspecified.
+ *   PC_STALL_GATED        the same for the launches of a gated projection: the
+ *                         first thread block never issues a copy.
  * Each ends as a real timeout does: PC_ERR_DEVICE_TIMEOUT in the status
  * word, -1 in the outputs the stopped blocks did not finish.
  * pc_debug_set_fps_grid_stall(e) sets or clears PC_STALL_FPS_GRID alone.
@@ -784,6 +787,7 @@ int pc_device_status(void *stream, int reset, int32_t *out_status);
 #define PC_STALL_FPS_CLUSTER 2
 #define PC_STALL_TILE_STREAM 4
 #define PC_STALL_ATTENTION 8
+#define PC_STALL_GATED 16
 void pc_set_wait_timeout_ns(uint64_t ns);
 void pc_debug_set_stall(int mask);
 void pc_debug_set_fps_grid_stall(int enable);

@@ -11,7 +11,6 @@ namespace {
 constexpr int XR = 128;  // rows of a product
 constexpr int YR = ATTN_TC_TILE;
 
-__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
 __device__ __forceinline__ float ex2(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
@@ -89,26 +88,6 @@ struct TileWalk {
             while (y >= end) y -= end, ++h;
     }
 };
-
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
-                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
-                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
-                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn encode_fn() {
-    static const EncodeFn fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult r;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
-                                             cudaEnableDefault, &r) != cudaSuccess ||
-            r != cudaDriverEntryPointSuccess) {
-            cudaGetLastError();
-            p = nullptr;
-        }
-        return reinterpret_cast<EncodeFn>(p);
-    }();
-    return fn;
-}
 
 // [B, L, heads, D] as boxes of 64 rows by 64 channels.
 bool make_map(CUtensorMap *map, const void *p, const int64_t *s, int64_t B, int64_t L,

@@ -1,0 +1,815 @@
+// pc_gated_tc.cu -- the gated projection on the tensor cores.
+//
+//   FWD   a = x Wg^T, u = x Wu^T, y = act(a) u
+//   GRAD  a and u again, da = dy u act'(a), du = dy act(a)
+//   DX    dx = da Wg + du Wu
+//   DW    dWg = da^T x, dWu = du^T x
+//
+// All four are one kernel: a persistent block walks over output tiles of 128
+// rows by BN columns (FWD, GRAD: BN / 2 hidden units, whose rows of Wg and Wu
+// lie side by side in the B tile, so that a thread finds a and u of the same
+// unit in its own row of the accumulator).  One warp copies operand tiles, 64 deep,
+// by tensor maps into a ring of stages; one thread issues the products; eight
+// warps take the accumulators, of which there are two, so that the products of
+// one tile run under the other's arithmetic and stores.  What is contracted
+// along its rows (DX: the weights; DW: both sides) is read as it lies, by
+// MN-major operands.  Zeros past the arrays' ends make every size fit.
+//
+// float32 runs as three bfloat16 parts of each operand and six products,
+// low x high, high x low, middle x middle, middle x high, high x middle, high x
+// high (to 2^-24).  The tensor cores cut their sums off instead of rounding
+// them, so a chain is one stage long, the small products first, and the stages
+// are added up in registers.  A bfloat16 chain over the rows is at most 16,384
+// long, joined in float32.
+//
+// da and du are operands of two products each and have to be bfloat16: one
+// rounding, which leaves dx and dW off by 1.42 times what rounding the results
+// does (a second part would double the work of both).  In float32 they are three parts.
+//
+// The biases' gradients are summed from the unrounded da and du: 32 rows by
+// shuffles in GRAD, the parts in a kernel of their own.
+//
+// DX and DW split their contraction among blocks where there are few tiles; the
+// parts are added in a fixed order by a kernel of its own.
+//
+// Waits are bounded and end as in pc_attn_tc.cu; the blocks take more than half a
+// SM's shared memory, so none waits for another's tensor memory.
+#include "pc_act.cuh"
+#include "pc_gated.cuh"
+#include "pc_tcgen05.cuh"
+#include "pc_tiles.cuh"
+#include "pointcloud.h"
+
+#include <type_traits>
+
+namespace pcn {
+namespace {
+
+enum { G_FWD = 0, G_GRAD = 1, G_DX = 2, G_DW = 3 };
+constexpr int BM = 128, BK = 64, CHAIN = 16384;
+constexpr int PANEL = 64 * 128;  // bytes of a 64 x 64 panel of an MN-major operand
+
+struct GemmMaps {
+    CUtensorMap a0, a1, b0, b1;
+};
+
+struct GemmArgs {
+    int64_t M;           // rows of the output
+    int N;               // its columns
+    int kb0, kb;         // stages of the first part of the contraction (DX: da), of all
+    int mt, nt, nsplit;  // tiles; parts of the contraction
+    void *out, *out2;    // y; dx; dWg and dWu
+    float *part;         // [nsplit][rows of all outputs][N] where nsplit > 1
+    const void *bg, *bu, *dy;
+    bf16 *d;             // [da, du][parts][M][ld]
+    float *bpart;        // GRAD: [4 mt][da, du][N], sums over 32 rows, or NULL
+    int ld, act;
+    bool vec, dvec;      // rows of the output, of dy, in 16-byte vectors
+    bool withhold;
+    uint64_t timeout_ns;
+    int *status;
+};
+
+template <int MODE, int P, int BN>
+struct GCfg {
+    static constexpr bool PAIR = MODE == G_FWD || MODE == G_GRAD;
+    static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;  // of a part
+    static constexpr int STAGE = P * (A_BYTES + B_BYTES);
+    static constexpr int FIT = (224 * 1024 - 1024) / STAGE, STAGES = FIT > 8 ? 8 : FIT;
+    static_assert(STAGES >= 2, "shared memory");
+    static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + 512;
+    static_assert(SMEM > 114 * 1024 && SMEM <= 227 * 1024, "one block a SM");
+    static constexpr int EWARPS = 8, THREADS = 32 * (4 + EWARPS);
+    static constexpr int COLS = 2 * BN;                  // tensor memory
+    static constexpr int NL = BN / 2;                    // columns of a thread
+    static constexpr int CH = PAIR ? (BN / 4 < 32 ? BN / 4 : 32) : 32;
+    // column of the thread's chunk j of CH; PAIR: first the gate's, then the up's
+    static __host__ __device__ constexpr int column(int half, int j) {
+        constexpr int n = PAIR ? NL / 2 / CH : NL / CH;
+        return PAIR ? (j < n ? half * (BN / 4) + j * CH : BN / 2 + half * (BN / 4) + (j - n) * CH)
+                    : half * NL + j * CH;
+    }
+};
+
+// The six products of three parts, the smallest first.
+__device__ constexpr int PART_A[6] = {2, 0, 1, 1, 0, 0};
+__device__ constexpr int PART_B[6] = {0, 2, 1, 0, 1, 0};
+
+template <int CH>
+__device__ __forceinline__ void tmem_load(uint32_t addr, float (&v)[CH]) {
+    uint32_t r[CH];
+    if constexpr (CH == 32)
+        tmem_ld32(addr, r);
+    else
+        tmem_ld16(addr, r);
+    tmem_wait_ld();
+#pragma unroll
+    for (int i = 0; i < CH; ++i) v[i] = __uint_as_float(r[i]);
+}
+
+// `left` columns of a row.
+template <class T, int CH>
+__device__ __forceinline__ void put(T *p, const float (&v)[CH], int left, bool vec) {
+    constexpr int V = 16 / sizeof(T);
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < CH / V; ++i)
+            if (V * i < left) Vec<T, V>::store(p + V * i, v + V * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            if (i < left) Vec<T, 1>::store(p + i, v + i);
+    }
+}
+template <class T, int CH>
+__device__ __forceinline__ void take(const T *p, float (&v)[CH], int left, bool vec) {
+    constexpr int V = 16 / sizeof(T);
+#pragma unroll
+    for (int i = 0; i < CH; ++i) v[i] = 0.0f;
+    if (vec) {
+#pragma unroll
+        for (int i = 0; i < CH / V; ++i)
+            if (V * i < left) Vec<T, V>::load(p + V * i, v + V * i);
+    } else {
+#pragma unroll
+        for (int i = 0; i < CH; ++i)
+            if (i < left) Vec<T, 1>::load(p + i, v + i);
+    }
+}
+
+// P parts of eight numbers, `plane` elements apart.
+template <int P>
+__device__ __forceinline__ void put_parts(bf16 *p, int64_t plane, const float *v) {
+    float t[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) t[i] = v[i];
+#pragma unroll
+    for (int k = 0; k < P; ++k) {
+        uint32_t w[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            w[i] = pack_bf16(t[2 * i], t[2 * i + 1]);
+            const float2 f = unpack_bf16(w[i]);
+            t[2 * i] -= f.x, t[2 * i + 1] -= f.y;
+        }
+        *reinterpret_cast<uint4 *>(p + k * plane) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// The sums of CH columns over the warp's rows: that of column c in the lanes with
+// lane % CH = c.  Halves of the columns change places at every step.
+template <int CH>
+__device__ __forceinline__ float column_sums(const float (&x)[CH], int lane) {
+    float v[CH];
+#pragma unroll
+    for (int i = 0; i < CH; ++i) {
+        v[i] = x[i];
+        if (CH < 32) v[i] += __shfl_xor_sync(0xffffffffu, v[i], 16);
+    }
+#pragma unroll
+    for (int o = CH / 2; o > 0; o >>= 1)
+#pragma unroll
+        for (int i = 0; i < o; ++i) {
+            const bool high = lane & o;
+            const float keep = high ? v[i + o] : v[i], give = high ? v[i] : v[i + o];
+            v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+    return v[0];
+}
+
+template <int MODE, int P, int BN>
+__global__ void __launch_bounds__(GCfg<MODE, P, BN>::THREADS, 1)
+gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
+    using C = GCfg<MODE, P, BN>;
+    using T = std::conditional_t<P == 1, bf16, float>;
+    constexpr int STAGES = C::STAGES, CH = C::CH;
+    extern __shared__ unsigned char smem_raw[];
+    unsigned char *base = reinterpret_cast<unsigned char *>(
+        (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *full = reinterpret_cast<uint64_t *>(base + size_t(STAGES) * C::STAGE);
+    uint64_t *empty = full + STAGES, *accfull = empty + STAGES, *accempty = accfull + 2;
+    uint64_t *done = accempty + 2;
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+    volatile int *stop = reinterpret_cast<volatile int *>(tmem_slot + 1);
+
+    const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
+    const int tiles = a.mt * a.nt;
+    const int64_t items = int64_t(tiles) * a.nsplit;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
+        for (int s = 0; s < 2; ++s) mbar_init(&accfull[s], 1), mbar_init(&accempty[s], C::EWARPS);
+        mbar_init(done, 1);
+        *stop = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 2) tmem_alloc(tmem_slot, C::COLS);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = uniform(int(*tmem_slot));
+
+    // A bounded wait; false: stop.
+    auto await = [&](uint64_t *bar, unsigned parity) {
+        const WaitResult w = mbar_wait_or_stop(bar, parity, stop, a.timeout_ns);
+        if (w == WAIT_TIMEOUT) {
+            *stop = 1;
+            raise_status(a.status, PC_ERR_DEVICE_TIMEOUT);
+        }
+        return w == WAIT_OK;
+    };
+    // an item: a tile and a part of its contraction
+    struct Item {
+        int m, n, k0, k1, split;
+        __device__ __forceinline__ Item(const GemmArgs &a, int64_t i, int tiles) {
+            split = int(i / tiles);
+            const int t = int(i - int64_t(split) * tiles);
+            m = t / a.nt, n = t - m * a.nt;
+            k0 = int(int64_t(a.kb) * split / a.nsplit);
+            k1 = int(int64_t(a.kb) * (split + 1) / a.nsplit);
+        }
+    };
+
+    if (warp == 0) {
+        // ---- copies ---------------------------------------------------------------
+        if (elect_one()) {
+            int s = 0;
+            unsigned phase = 1;  // (of the ring's first round: passes at once)
+            int64_t issued = 0;
+            bool ok = !(a.withhold && blockIdx.x == 0);
+            for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+                const Item it(a, i, tiles);
+                const int dw_mt = a.mt / 2;  // DW: tiles of dWg, then of dWu
+                for (int k = it.k0; k < it.k1; ++k) {
+                    if (!(ok = await(&empty[s], phase))) break;
+                    unsigned char *A = base + size_t(s) * C::STAGE, *B = A + P * C::A_BYTES;
+                    uint64_t *bar = &full[s];
+                    mbar_arrive_expect_tx(bar, C::STAGE);
+#pragma unroll
+                    for (int p = 0; p < P; ++p) {
+                        unsigned char *Ap = A + p * C::A_BYTES, *Bp = B + p * C::B_BYTES;
+                        if (C::PAIR) {
+                            tma_load_3d(Ap, &maps.a0, k * BK, it.m * BM, p, bar);
+                            tma_load_3d(Bp, &maps.b0, k * BK, it.n * (BN / 2), p, bar);
+                            tma_load_3d(Bp + C::B_BYTES / 2, &maps.b1, k * BK, it.n * (BN / 2), p,
+                                        bar);
+                        } else if (MODE == G_DX) {
+                            const bool up = k >= a.kb0;
+                            const int f = (up ? k - a.kb0 : k) * BK;
+                            tma_load_3d(Ap, up ? &maps.a1 : &maps.a0, f, it.m * BM, p, bar);
+#pragma unroll
+                            for (int j = 0; j < BN / 64; ++j)
+                                tma_load_3d(Bp + j * PANEL, up ? &maps.b1 : &maps.b0,
+                                            it.n * BN + 64 * j, f, p, bar);
+                        } else {
+                            const bool up = it.m >= dw_mt;
+                            const int f = (up ? it.m - dw_mt : it.m) * BM;
+#pragma unroll
+                            for (int j = 0; j < BM / 64; ++j)
+                                tma_load_3d(Ap + j * PANEL, up ? &maps.a1 : &maps.a0, f + 64 * j,
+                                            k * BK, p, bar);
+#pragma unroll
+                            for (int j = 0; j < BN / 64; ++j)
+                                tma_load_3d(Bp + j * PANEL, &maps.b0, it.n * BN + 64 * j, k * BK, p,
+                                            bar);
+                        }
+                    }
+                    ++issued;
+                    if (++s == STAGES) s = 0, phase ^= 1;
+                }
+            }
+            // nothing is in flight when the block ends
+            for (int64_t k = issued > STAGES ? issued - STAGES : 0; k < issued; ++k)
+                mbar_wait_bounded(&full[k % STAGES], unsigned((k / STAGES) & 1), a.timeout_ns);
+        }
+    } else if (warp == 1) {
+        // ---- products ---------------------------------------------------------------
+        if (elect_one()) {
+            constexpr bool AR = MODE == G_DW, BR = !C::PAIR;  // contracted along their rows
+            constexpr uint32_t id = mma_idesc(BN, BR, AR);
+            constexpr uint32_t da = AR ? 16 * 128 / 16 : 2, db = BR ? 16 * 128 / 16 : 2;
+            const uint32_t a0 = smem_operand(smem_u32(base), AR ? PANEL : 16);
+            const uint32_t b0 =
+                smem_operand(smem_u32(base) + P * C::A_BYTES, BR ? PANEL : 16);
+            int s = 0, buf = 0;
+            unsigned phase = 0, aphase = 1;
+            bool ok = true;
+            for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+                const Item it(a, i, tiles);
+                for (int k = it.k0; k < it.k1; ++k) {
+                    if ((P > 1 || k == it.k0) && !(ok = await(&accempty[buf], aphase))) break;
+                    if (!(ok = await(&full[s], phase))) break;
+                    tc_fence_after();
+                    const uint32_t d = tmem + buf * BN;
+                    const uint32_t as = a0 + s * (C::STAGE / 16), bs = b0 + s * (C::STAGE / 16);
+                    if (P == 1) {
+#pragma unroll
+                        for (int j = 0; j < BK / 16; ++j)
+                            mma_ss<SMEM_128B>(d, as + j * da, bs + j * db, id, k > it.k0 || j > 0);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 6; ++q)
+#pragma unroll
+                            for (int j = 0; j < BK / 16; ++j)
+                                mma_ss<SMEM_128B>(d, as + PART_A[q] * (C::A_BYTES / 16) + j * da,
+                                                  bs + PART_B[q] * (C::B_BYTES / 16) + j * db, id,
+                                                  q > 0 || j > 0);
+                    }
+                    mma_commit(&empty[s]);
+                    if (P > 1 || k + 1 == it.k1) {
+                        mma_commit(&accfull[buf]);
+                        buf ^= 1;
+                        if (buf == 0) aphase ^= 1;
+                    }
+                    if (++s == STAGES) s = 0, phase ^= 1;
+                }
+            }
+            mma_commit(done);
+            mbar_wait_bounded(done, 0, a.timeout_ns);
+        }
+    } else if (warp >= 4) {
+        // ---- accumulators -------------------------------------------------------------
+        const int quad = warp % 4, half = (warp - 4) / 4;
+        const uint32_t lanes = uint32_t(quad * 32) << 16;
+        int buf = 0;
+        unsigned phase = 0;
+        bool ok = true;
+        auto wait = [&]() { return __all_sync(0xffffffffu, await(&accfull[buf], phase)) != 0; };
+        auto release = [&]() {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&accempty[buf]);
+            buf ^= 1;
+            if (buf == 0) phase ^= 1;
+        };
+        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+            const Item it(a, i, tiles);
+            float sum[P == 1 ? 1 : C::NL];
+            if (P > 1) {
+#pragma unroll
+                for (int c = 0; c < (P == 1 ? 1 : C::NL); ++c) sum[c] = 0.0f;
+                for (int k = it.k0; k < it.k1; ++k) {
+                    if (!(ok = wait())) break;
+                    tc_fence_after();
+#pragma unroll
+                    for (int j = 0; j < C::NL / CH; ++j) {
+                        float v[CH];
+                        tmem_load<CH>(tmem + lanes + buf * BN + C::column(half, j), v);
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) sum[(P == 1 ? 0 : j * CH + c)] += v[c];
+                    }
+                    release();
+                }
+                if (!ok) break;
+            }
+            // chunk j of the thread's columns
+            auto get = [&](int j, float (&v)[CH]) {
+                if (P == 1) {
+                    tmem_load<CH>(tmem + lanes + buf * BN + C::column(half, j), v);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < CH; ++c) v[c] = sum[P == 1 ? 0 : j * CH + c];
+                }
+            };
+            if constexpr (C::PAIR) {
+                constexpr int n = C::NL / 2 / CH;
+                const int64_t row = int64_t(it.m) * BM + quad * 32 + lane;
+                const bool in = row < a.M;
+#pragma unroll
+                for (int j = 0; j < n; ++j) {
+                    const int c0 = it.n * (BN / 2) + C::column(half, j);
+                    const int left = in ? a.N - c0 : 0;
+                    float dy[MODE == G_GRAD ? CH : 1];
+                    if constexpr (MODE == G_GRAD)
+                        take<T, CH>(static_cast<const T *>(a.dy) + row * a.N + c0, dy, left, a.dvec);
+                    if (P == 1 && j == 0) {
+                        if (!(ok = wait())) break;
+                        tc_fence_after();
+                    }
+                    float g[CH], u[CH];
+                    get(j, g);
+                    get(n + j, u);
+                    if (P == 1 && j == n - 1) release();
+                    if (a.bg != nullptr) {
+                        float bg = 0.0f, bu = 0.0f;  // of column c0 + lane
+                        if (lane < CH && c0 + lane < a.N) {
+                            Vec<T, 1>::load(static_cast<const T *>(a.bg) + c0 + lane, &bg);
+                            Vec<T, 1>::load(static_cast<const T *>(a.bu) + c0 + lane, &bu);
+                        }
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            g[c] += __shfl_sync(0xffffffffu, bg, c);
+                            u[c] += __shfl_sync(0xffffffffu, bu, c);
+                        }
+                    }
+                    if constexpr (MODE == G_FWD) {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) g[c] = act_value<P == 1>(a.act, g[c]) * u[c];
+                        put<T, CH>(static_cast<T *>(a.out) + row * a.N + c0, g, left, a.vec);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) {
+                            float slope;
+                            const float f = act_both<P == 1>(a.act, g[c], slope);
+                            g[c] = dy[c] * u[c] * slope;
+                            u[c] = dy[c] * f;
+                        }
+                        if (a.bpart != nullptr) {  // (before they are rounded)
+                            const float sg = column_sums<CH>(g, lane);
+                            const float su = column_sums<CH>(u, lane);
+                            float *o = a.bpart + (int64_t(it.m) * 4 + quad) * 2 * a.N + c0 + lane;
+                            if (lane < CH && c0 + lane < a.N) o[0] = sg, o[a.N] = su;
+                        }
+                        const int64_t plane = a.M * a.ld;
+                        bf16 *at = a.d + row * a.ld + c0;
+#pragma unroll
+                        for (int c = 0; c < CH; c += 8)
+                            if (c < left) {  // (the rows' padding takes zeros)
+                                put_parts<P>(at + c, plane, g + c);
+                                put_parts<P>(at + P * plane + c, plane, u + c);
+                            }
+                    }
+                }
+                if (!ok) break;
+            } else {
+                constexpr int n = C::NL / CH;
+                const int dw_mt = a.mt / 2;
+                const bool up = MODE == G_DW && it.m >= dw_mt;
+                const int64_t row =
+                    int64_t(up ? it.m - dw_mt : it.m) * BM + quad * 32 + lane;
+                if (P == 1) {
+                    if (!(ok = wait())) break;
+                    tc_fence_after();
+                }
+#pragma unroll
+                for (int j = 0; j < n; ++j) {
+                    float v[CH];
+                    get(j, v);
+                    if (P == 1 && j == n - 1) release();
+                    const int c0 = it.n * BN + C::column(half, j);
+                    const int left = row < a.M ? a.N - c0 : 0;
+                    if (a.nsplit > 1) {
+                        const int64_t all = MODE == G_DW ? 2 * a.M : a.M;
+                        put<float, CH>(a.part + (it.split * all + (up ? a.M : 0) + row) * a.N + c0,
+                                       v, left, a.N % 4 == 0);
+                    } else {
+                        put<T, CH>(static_cast<T *>(up ? a.out2 : a.out) + row * a.N + c0, v, left,
+                                   a.vec);
+                    }
+                }
+            }
+        }
+    }
+    __syncwarp();
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_free(tmem, C::COLS);
+    }
+}
+
+// --- operands that the tensor maps cannot read as they are -------------------------
+
+struct PackJob {
+    const void *src;
+    bf16 *dst;       // [P][rows][ld]
+    int64_t rows;
+    int C, ld, blocks;
+    bool vec;
+};
+struct PackJobs {
+    PackJob job[3];
+};
+constexpr int PACK_ROWS = 16;
+
+// Rows of T as P bfloat16 parts, padded to eight columns.
+template <class T, int P>
+__global__ void __launch_bounds__(256) gated_pack_kernel(PackJobs jobs) {
+    int b = blockIdx.x, k = 0;
+    while (k < 2 && b >= jobs.job[k].blocks) b -= jobs.job[k++].blocks;
+    const PackJob &j = jobs.job[k];
+    const int64_t r0 = int64_t(b) * PACK_ROWS;
+    const int rows = int(min(int64_t(PACK_ROWS), j.rows - r0));
+    const int groups = j.ld / 8;
+    for (int i = threadIdx.x; i < rows * groups; i += 256) {
+        const int64_t r = r0 + i / groups;
+        const int c = i % groups * 8;
+        float v[8];
+        take<T, 8>(static_cast<const T *>(j.src) + r * j.C + c, v, j.C - c, j.vec);
+        put_parts<P>(j.dst + r * j.ld + c, j.rows * j.ld, v);
+    }
+}
+
+// --- sums of parts -------------------------------------------------------------------
+
+// out[i] = sum over the parts, in their order: the first `half` numbers to out,
+// the others to out2.
+template <class T, int V>
+__global__ void __launch_bounds__(256)
+gated_join_kernel(const float *part, int nparts, int64_t n, int64_t half, T *out, T *out2) {
+    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * V;
+    if (i >= n) return;
+    float s[V];
+    Vec<float, V>::load(part + i, s);
+#pragma unroll 4
+    for (int p = 1; p < nparts; ++p) {
+        float v[V];
+        Vec<float, V>::load(part + p * n + i, v);
+#pragma unroll
+        for (int e = 0; e < V; ++e) s[e] += v[e];
+    }
+    Vec<T, V>::store(i < half ? out + i : out2 + (i - half), s);
+}
+
+// The biases' gradients: 32 columns a block, 32 warps every 32nd part, in a fixed order.
+template <class T>
+__global__ void __launch_bounds__(1024)
+gated_bias_kernel(const float *part, int nparts, int F, T *dbg, T *dbu) {
+    __shared__ float acc[32][33];
+    const int c = blockIdx.x * 32 + threadIdx.x;
+    float s = 0.0f;
+    if (c < 2 * F)
+#pragma unroll 4
+        for (int p = threadIdx.y; p < nparts; p += 32) s += part[int64_t(p) * 2 * F + c];
+    acc[threadIdx.y][threadIdx.x] = s;
+    __syncthreads();
+    if (threadIdx.y == 0 && c < 2 * F) {
+        s = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) s += acc[i][threadIdx.x];
+        Vec<T, 1>::store(c < F ? dbg + c : dbu + (c - F), &s);
+    }
+}
+
+// --- host ------------------------------------------------------------------------------
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+int pad8(int64_t n) { return int((n + 7) / 8 * 8); }
+bool aligned16(const void *p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// Rows of bfloat16, P parts, that a tensor map can read.
+struct Operand {
+    const bf16 *p = nullptr;
+    int64_t rows = 0;
+    int cols = 0, ld = 0, parts = 1;
+};
+
+// Boxes of 64 columns by `box` rows of one part.
+bool make_map3(CUtensorMap *map, const Operand &o, int box) {
+    const EncodeFn fn = encode_fn();
+    if (fn == nullptr) return false;
+    const cuuint64_t dims[3] = {cuuint64_t(o.cols), cuuint64_t(o.rows), cuuint64_t(o.parts)};
+    const cuuint64_t strides[2] = {cuuint64_t(o.ld) * 2, cuuint64_t(o.rows) * o.ld * 2};
+    const cuuint32_t b[3] = {64, cuuint32_t(box), 1}, ones[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16 *>(o.p), dims, strides, b,
+              ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Scratch handed out in pieces: sizes first, then addresses.
+struct Scratch {
+    size_t bytes = 0;
+    char *base = nullptr;
+    size_t take(size_t n) {
+        const size_t at = bytes;
+        bytes += (n + 1023) / 1024 * 1024;
+        return at;
+    }
+};
+
+// The columns of a tile and the parts of the contraction: the smallest estimate
+// in SM cycles.  A stage of a tile costs its products (limited by the reads of shared
+// memory: 128 bytes a cycle) or a wave's epilogue, whichever is longer; parts cost
+// their writes and reads and a launch.
+struct GemmPlan {
+    int BN = 0, nsplit = 1;
+};
+GemmPlan plan_gemm(int sms, bool pair, int P, int64_t M, int64_t N, int64_t mtiles, int64_t kb,
+                   bool may_split) {
+    GemmPlan best;
+    double least = 1e300;
+    for (int BN = P == 1 ? 256 : 128; BN >= 64; BN /= 2) {
+        const int64_t tiles = mtiles * ceil_div(N, pair ? BN / 2 : BN);
+        const double stage = (P == 1 ? 1 : 6) * 4.0 *
+                             (BN / 2 > (BM + BN) / 4 ? BN / 2 : (BM + BN) / 4);
+        const double epilogue = pair ? 14.0 * BN : 6.0 * BN;
+        const int64_t first = may_split && P == 1 ? ceil_div(kb * BK, CHAIN) : 1;
+        const int64_t most = may_split ? (kb < 64 ? kb : 64) : 1;
+        for (int64_t ns = first; ns <= (most > first ? most : first); ++ns) {
+            const double k = double(ceil_div(kb, ns));
+            const double item = k * stage > epilogue ? k * stage : epilogue;
+            double cost = double(ceil_div(tiles * ns, sms)) * item + epilogue + 1500;
+            if (ns > 1) cost += 6000 + 8.0 * double(ns) * double(M) * double(N) / 3000;
+            if (cost < least) least = cost, best.BN = BN, best.nsplit = int(ns);
+        }
+    }
+    return best;
+}
+
+template <int MODE, int P, int BN>
+cudaError_t run_gemm(const DeviceInfo &dev, const GemmMaps &maps, const GemmArgs &g,
+                     cudaStream_t st) {
+    using C = GCfg<MODE, P, BN>;
+    static std::atomic<uint64_t> done{0};
+    const cudaError_t e =
+        allow_smem(gated_gemm_kernel<MODE, P, BN>, int(C::SMEM), dev.device, done);
+    if (e != cudaSuccess) return e;
+    const int64_t items = int64_t(g.mt) * g.nt * g.nsplit;
+    const unsigned blocks = unsigned(items < dev.sm_count ? items : dev.sm_count);
+    gated_gemm_kernel<MODE, P, BN><<<blocks, C::THREADS, C::SMEM, st>>>(maps, g);
+    return cudaGetLastError();
+}
+template <int MODE, int P>
+cudaError_t run_gemm(const DeviceInfo &dev, const GemmMaps &maps, const GemmArgs &g, int BN,
+                     cudaStream_t st) {
+    if constexpr (P == 1)
+        if (BN == 256) return run_gemm<MODE, P, 256>(dev, maps, g, st);
+    return BN == 128 ? run_gemm<MODE, P, 128>(dev, maps, g, st)
+                     : run_gemm<MODE, P, 64>(dev, maps, g, st);
+}
+
+template <class T>
+cudaError_t join(const float *part, int nparts, int64_t n, int64_t half, void *out, void *out2,
+                 cudaStream_t st) {
+    T *o = static_cast<T *>(out), *o2 = static_cast<T *>(out2);
+    if (n % 4 == 0 && half % 4 == 0 && aligned16(out) && (out2 == nullptr || aligned16(out2)))
+        gated_join_kernel<T, 4><<<unsigned(ceil_div(n, 1024)), 256, 0, st>>>(part, nparts, n, half,
+                                                                            o, o2);
+    else
+        gated_join_kernel<T, 1><<<unsigned(ceil_div(n, 256)), 256, 0, st>>>(part, nparts, n, half,
+                                                                           o, o2);
+    return cudaGetLastError();
+}
+
+// x and the weights as operands, split or copied where they have to be.
+struct Inputs {
+    Operand x, wg, wu;
+    size_t at[3];
+    bool packed[3];
+};
+template <class T, int P>
+void plan_inputs(const GatedArgs &a, Inputs &in, Scratch &s) {
+    Operand *o[3] = {&in.x, &in.wg, &in.wu};
+    const void *src[3] = {a.x, a.wg, a.wu};
+    for (int i = 0; i < 3; ++i) {
+        o[i]->rows = i ? a.F : a.rows, o[i]->cols = a.C, o[i]->parts = P;
+        in.packed[i] = P > 1 || a.C % 8 || !aligned16(src[i]);
+        o[i]->ld = in.packed[i] ? pad8(a.C) : a.C;
+        if (in.packed[i])
+            in.at[i] = s.take(size_t(P) * o[i]->rows * o[i]->ld * sizeof(bf16));
+        else
+            o[i]->p = static_cast<const bf16 *>(src[i]);
+    }
+}
+template <class T, int P>
+cudaError_t pack_inputs(const GatedArgs &a, Inputs &in, const Scratch &s, cudaStream_t st) {
+    Operand *o[3] = {&in.x, &in.wg, &in.wu};
+    const void *src[3] = {a.x, a.wg, a.wu};
+    PackJobs jobs{};
+    int n = 0;
+    int64_t blocks = 0;
+    for (int i = 0; i < 3; ++i) {
+        if (!in.packed[i]) continue;
+        bf16 *dst = reinterpret_cast<bf16 *>(s.base + in.at[i]);
+        o[i]->p = dst;
+        PackJob &j = jobs.job[n++];
+        j.src = src[i], j.dst = dst, j.rows = o[i]->rows, j.C = a.C, j.ld = o[i]->ld;
+        j.blocks = int(ceil_div(j.rows, PACK_ROWS));
+        j.vec = a.C % (16 / sizeof(T)) == 0 && aligned16(src[i]);
+        blocks += j.blocks;
+    }
+    if (n == 0) return cudaSuccess;
+    gated_pack_kernel<T, P><<<unsigned(blocks), 256, 0, st>>>(jobs);
+    return cudaGetLastError();
+}
+
+GemmArgs gemm_args(const DeviceInfo &dev, const GatedArgs &a) {
+    GemmArgs g{};
+    g.bg = a.bg, g.bu = a.bu, g.dy = a.dy, g.act = a.act;
+    g.timeout_ns = wait_timeout_ns(), g.status = dev.status_word;
+    g.withhold = (debug_stall() & PC_STALL_GATED) != 0;
+    g.nsplit = 1;
+    return g;
+}
+
+template <class T, int P>
+cudaError_t forward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st) {
+    Scratch s;
+    Inputs in;
+    plan_inputs<T, P>(a, in, s);
+    cudaError_t e = cudaSuccess;
+    if (s.bytes && (e = scratch_alloc(dev, reinterpret_cast<void **>(&s.base), s.bytes, st)) !=
+                       cudaSuccess)
+        return e;
+    e = pack_inputs<T, P>(a, in, s, st);
+    if (e == cudaSuccess) {
+        GemmArgs g = gemm_args(dev, a);
+        g.M = a.rows, g.N = a.F, g.kb = int(ceil_div(a.C, BK)), g.kb0 = g.kb;
+        g.mt = int(ceil_div(a.rows, BM));
+        const GemmPlan p = plan_gemm(dev.sm_count, true, P, g.M, g.N, g.mt, g.kb, false);
+        g.nt = int(ceil_div(a.F, p.BN / 2));
+        g.out = a.y, g.vec = a.F % (16 / sizeof(T)) == 0 && aligned16(a.y);
+        GemmMaps m{};
+        const bool ok = make_map3(&m.a0, in.x, BM) && make_map3(&m.b0, in.wg, p.BN / 2) &&
+                        make_map3(&m.b1, in.wu, p.BN / 2);
+        e = ok ? run_gemm<G_FWD, P>(dev, m, g, p.BN, st) : cudaErrorInvalidValue;
+    }
+    if (s.base) {
+        const cudaError_t f = scratch_free(s.base, st);
+        if (e == cudaSuccess) e = f;
+    }
+    return e;
+}
+
+template <class T, int P>
+cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st) {
+    Scratch s;
+    Inputs in;
+    plan_inputs<T, P>(a, in, s);
+    const int ld = pad8(a.F);
+    const size_t d_at = s.take(size_t(2) * P * a.rows * ld * sizeof(bf16));
+    const int mt = int(ceil_div(a.rows, BM)), ft = int(ceil_div(a.F, BM));
+    const int kf = int(ceil_div(a.F, BK)), kr = int(ceil_div(a.rows, BK));
+    GemmPlan px, pw;
+    size_t part_x = 0, part_w = 0, part_b = 0;
+    if (a.dx) {
+        px = plan_gemm(dev.sm_count, false, P, a.rows, a.C, mt, 2 * kf, true);
+        if (px.nsplit > 1) part_x = s.take(size_t(px.nsplit) * a.rows * a.C * sizeof(float));
+    }
+    if (a.dwg) {
+        pw = plan_gemm(dev.sm_count, false, P, 2 * a.F, a.C, 2 * ft, kr, true);
+        if (pw.nsplit > 1) part_w = s.take(size_t(pw.nsplit) * 2 * a.F * a.C * sizeof(float));
+    }
+    if (a.dbg) part_b = s.take(size_t(mt) * 4 * 2 * a.F * sizeof(float));
+    cudaError_t e = scratch_alloc(dev, reinterpret_cast<void **>(&s.base), s.bytes, st);
+    if (e != cudaSuccess) return e;
+    e = pack_inputs<T, P>(a, in, s, st);
+    Operand d[2];
+    for (int i = 0; i < 2; ++i) {
+        d[i].p = reinterpret_cast<const bf16 *>(s.base + d_at) + int64_t(i) * P * a.rows * ld;
+        d[i].rows = a.rows, d[i].cols = a.F, d[i].ld = ld, d[i].parts = P;
+    }
+    auto partials = [&](size_t at) { return reinterpret_cast<float *>(s.base + at); };
+    if (e == cudaSuccess) {
+        GemmArgs g = gemm_args(dev, a);
+        g.M = a.rows, g.N = a.F, g.kb = int(ceil_div(a.C, BK)), g.kb0 = g.kb, g.mt = mt;
+        const GemmPlan p = plan_gemm(dev.sm_count, true, P, g.M, g.N, g.mt, g.kb, false);
+        g.nt = int(ceil_div(a.F, p.BN / 2));
+        g.d = const_cast<bf16 *>(d[0].p), g.ld = ld;
+        g.dvec = a.F % (16 / sizeof(T)) == 0 && aligned16(a.dy);
+        if (a.dbg) g.bpart = partials(part_b);
+        GemmMaps m{};
+        const bool ok = make_map3(&m.a0, in.x, BM) && make_map3(&m.b0, in.wg, p.BN / 2) &&
+                        make_map3(&m.b1, in.wu, p.BN / 2);
+        e = ok ? run_gemm<G_GRAD, P>(dev, m, g, p.BN, st) : cudaErrorInvalidValue;
+    }
+    if (e == cudaSuccess && a.dx) {
+        GemmArgs g = gemm_args(dev, a);
+        g.M = a.rows, g.N = a.C, g.kb0 = kf, g.kb = 2 * kf, g.mt = mt;
+        g.nt = int(ceil_div(a.C, px.BN)), g.nsplit = px.nsplit;
+        g.out = a.dx, g.vec = a.C % (16 / sizeof(T)) == 0 && aligned16(a.dx);
+        g.part = partials(part_x);
+        GemmMaps m{};
+        const bool ok = make_map3(&m.a0, d[0], BM) && make_map3(&m.a1, d[1], BM) &&
+                        make_map3(&m.b0, in.wg, 64) && make_map3(&m.b1, in.wu, 64);
+        e = ok ? run_gemm<G_DX, P>(dev, m, g, px.BN, st) : cudaErrorInvalidValue;
+        if (e == cudaSuccess && g.nsplit > 1)
+            e = join<T>(g.part, g.nsplit, a.rows * a.C, a.rows * a.C, a.dx, nullptr, st);
+    }
+    if (e == cudaSuccess && a.dwg) {
+        GemmArgs g = gemm_args(dev, a);
+        g.M = a.F, g.N = a.C, g.kb = kr, g.kb0 = kr, g.mt = 2 * ft;
+        g.nt = int(ceil_div(a.C, pw.BN)), g.nsplit = pw.nsplit;
+        g.out = a.dwg, g.out2 = a.dwu;
+        g.vec = a.C % (16 / sizeof(T)) == 0 && aligned16(a.dwg) && aligned16(a.dwu);
+        g.part = partials(part_w);
+        GemmMaps m{};
+        const bool ok = make_map3(&m.a0, d[0], 64) && make_map3(&m.a1, d[1], 64) &&
+                        make_map3(&m.b0, in.x, 64);
+        e = ok ? run_gemm<G_DW, P>(dev, m, g, pw.BN, st) : cudaErrorInvalidValue;
+        const int64_t n = int64_t(a.F) * a.C;
+        if (e == cudaSuccess && g.nsplit > 1)
+            e = join<T>(g.part, g.nsplit, 2 * n, n, a.dwg, a.dwu, st);
+    }
+    if (e == cudaSuccess && a.dbg) {
+        gated_bias_kernel<T><<<unsigned(ceil_div(2 * a.F, 32)), dim3(32, 32), 0, st>>>(
+            partials(part_b), 4 * mt, a.F, static_cast<T *>(a.dbg), static_cast<T *>(a.dbu));
+        e = cudaGetLastError();
+    }
+    const cudaError_t f = scratch_free(s.base, st);
+    return e == cudaSuccess ? f : e;
+}
+
+}  // namespace
+
+cudaError_t gated_tc_forward(const DeviceInfo &dev, const GatedArgs &a, int dtype,
+                             cudaStream_t st) {
+    return dtype == PC_F32 ? forward<float, 3>(dev, a, st) : forward<bf16, 1>(dev, a, st);
+}
+cudaError_t gated_tc_backward(const DeviceInfo &dev, const GatedArgs &a, int dtype,
+                              cudaStream_t st) {
+    return dtype == PC_F32 ? backward<float, 3>(dev, a, st) : backward<bf16, 1>(dev, a, st);
+}
+
+}  // namespace pcn

@@ -1,5 +1,6 @@
 // pc_tcgen05.cuh -- the fifth-generation tensor cores and tensor-map copies:
-// thin wrappers of the PTX instructions the attention kernels use.
+// thin wrappers of the PTX instructions the attention and gated-projection
+// kernels use.
 #pragma once
 
 #include "pc_device.cuh"
@@ -89,6 +90,10 @@ __device__ __forceinline__ bool elect_one() {
     return r != 0;
 }
 
+// The value of lane 0, known to be the same in all lanes: branches on it, and what
+// the products' operands are formed from, stay in uniform registers.
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(0xffffffffu, v, 0); }
+
 // --- products -------------------------------------------------------------------
 
 // Shared-memory operands of bfloat16, as the two words of their descriptor.
@@ -104,10 +109,10 @@ constexpr uint32_t SMEM_128B = (1024 >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t SMEM_64B = (512 >> 4) | (1u << 14) | (4u << 29);
 
 // bfloat16 x bfloat16 -> float32, M = 128.  `b_rows`: B's contraction runs
-// over its rows (MN-major) instead of along them.
-__host__ __device__ constexpr uint32_t mma_idesc(int N, bool b_rows) {
-    return (1u << 4) | (1u << 7) | (1u << 10) | (b_rows ? 1u << 16 : 0u) |
-           (uint32_t(N / 8) << 17) | (uint32_t(128 / 16) << 24);
+// over its rows (MN-major) instead of along them; `a_rows`: A's.
+__host__ __device__ constexpr uint32_t mma_idesc(int N, bool b_rows, bool a_rows = false) {
+    return (1u << 4) | (1u << 7) | (1u << 10) | (a_rows ? 1u << 15 : 0u) |
+           (b_rows ? 1u << 16 : 0u) | (uint32_t(N / 8) << 17) | (uint32_t(128 / 16) << 24);
 }
 
 // One thread.  D (tensor memory) = A B + (accumulate ? D : 0), 16 deep; A and B
@@ -152,6 +157,36 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const CUtensorMap *map, i
         "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
         "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
         : "memory");
+}
+
+__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1,
+                                            int c2, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cta.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+        : "memory");
+}
+
+// The driver's function that makes a tensor map.
+using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *,
+                              const cuuint64_t *, const cuuint64_t *, const cuuint32_t *,
+                              const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                              CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+inline EncodeFn encode_fn() {
+    static const EncodeFn fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000,
+                                             cudaEnableDefault, &r) != cudaSuccess ||
+            r != cudaDriverEntryPointSuccess) {
+            cudaGetLastError();
+            p = nullptr;
+        }
+        return reinterpret_cast<EncodeFn>(p);
+    }();
+    return fn;
 }
 
 }  // namespace pcn

@@ -55,7 +55,7 @@ def test_gated_linear_validation(L):
     assert call(rows=-1) == 1 and call(F=-1) == 1 and call(C=0) == 1
     assert call(bg=FAKE) == 1 and "go together" in _msg(L)
     assert call(act=6) == 1
-    assert call(C=65537) == 2 and call(F=65537) == 2 and call(rows=2 ** 31) == 2
+    assert call(C=16385) == 2 and call(F=65537) == 2 and call(rows=2 ** 30 + 1) == 2
     assert call(rows=0) == 0 and call(F=0) == 0
 
     def back(dwg=FAKE, dwu=FAKE, dbg=None, dbu=None, dx=FAKE, dtype=0):

@@ -689,6 +689,26 @@ def test_results_do_not_change_from_run_to_run():
                 assert torch.equal(first[k], again[k]), k
 
 
+def test_a_withheld_copy_ends_with_the_status_word():
+    for dtype in DTYPES:
+        ins = gated_inputs(gen(6), 700, 256, 320, dtype)
+        want = gated_all(*ins, "silu")
+        x, wg, wu, bg, bu, dy = ins
+        torch.cuda.synchronize()
+        try:
+            pc.pc_set_wait_timeout_ns(50_000_000)
+            pc.pc_debug_set_stall(pc.PC_STALL_GATED)
+            pc.pc_gated_linear(x, wg, wu, bg, bu)
+            assert pc.pc_device_status(reset=True) == 4
+            pc.pc_gated_linear_backward(dy, x, wg, wu, bg, bu)
+            assert pc.pc_device_status(reset=True) == 4
+        finally:
+            pc.pc_debug_set_stall(0)
+            pc.pc_set_wait_timeout_ns(2_000_000_000)
+        again = gated_all(*ins, "silu")
+        assert all(torch.equal(want[k], again[k]) for k in want)
+
+
 def test_refusals():
     g = gen(0)
     x, w = randn(g, 4, 16), randn(g, 8, 16)
