@@ -6,6 +6,8 @@
 
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 namespace pcn {
 
 // s(z) = 1 / (1 + exp(-z)).  FAST, for results that are rounded to bfloat16:
@@ -25,43 +27,55 @@ __device__ __forceinline__ float normal_cdf(float z) {
     return 0.5f * erfcf(-R * z);
 }
 
-// act(z)
-template <bool FAST>
-__device__ __forceinline__ float act_value(int act, float z) {
-    switch (act) {
-        case PC_ACT_SILU: return z * logistic<FAST>(z);
-        case PC_ACT_GELU: return z * normal_cdf<FAST>(z);
-        case PC_ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;  // (a NaN stays)
-        case PC_ACT_SIGMOID: return logistic<FAST>(z);
-        default: return z;
-    }
+// act(z).  The activation is a template parameter: a switch for every value keeps
+// the values of a thread from being computed side by side (a tile's epilogue took
+// ten times as long).
+template <int ACT, bool FAST>
+__device__ __forceinline__ float act_value(float z) {
+    if (ACT == PC_ACT_SILU) return z * logistic<FAST>(z);
+    if (ACT == PC_ACT_GELU) return z * normal_cdf<FAST>(z);
+    if (ACT == PC_ACT_RELU) return z > 0.0f || z != z ? z : 0.0f;  // (a NaN stays)
+    if (ACT == PC_ACT_SIGMOID) return logistic<FAST>(z);
+    return z;
 }
 
 // act(z) and act'(z)
-template <bool FAST>
-__device__ __forceinline__ float act_both(int act, float z, float &slope) {
+template <int ACT, bool FAST>
+__device__ __forceinline__ float act_both(float z, float &slope) {
+    if (ACT == PC_ACT_SILU) {
+        const float s = logistic<FAST>(z);
+        slope = s * fmaf(z, 1.0f - s, 1.0f);
+        return z * s;
+    }
+    if (ACT == PC_ACT_GELU) {
+        constexpr float N = 0.39894228040143268f;  // 1 / sqrt(2 pi)
+        const float c = normal_cdf<FAST>(z);
+        const float e = FAST ? __expf(-0.5f * z * z) : expf(-0.5f * z * z);
+        slope = fmaf(z * N, e, c);
+        return z * c;
+    }
+    if (ACT == PC_ACT_RELU) {
+        slope = z > 0.0f ? 1.0f : z != z ? z : 0.0f;
+        return z > 0.0f || z != z ? z : 0.0f;
+    }
+    if (ACT == PC_ACT_SIGMOID) {
+        const float s = logistic<FAST>(z);
+        slope = s * (1.0f - s);
+        return s;
+    }
+    slope = 1.0f;
+    return z;
+}
+
+// f(activation as a compile-time constant)
+template <class F>
+__device__ __forceinline__ void act_switch(int act, F f) {
     switch (act) {
-        case PC_ACT_SILU: {
-            const float s = logistic<FAST>(z);
-            slope = s * fmaf(z, 1.0f - s, 1.0f);
-            return z * s;
-        }
-        case PC_ACT_GELU: {
-            constexpr float N = 0.39894228040143268f;  // 1 / sqrt(2 pi)
-            const float c = normal_cdf<FAST>(z);
-            const float e = FAST ? __expf(-0.5f * z * z) : expf(-0.5f * z * z);
-            slope = fmaf(z * N, e, c);
-            return z * c;
-        }
-        case PC_ACT_RELU:
-            slope = z > 0.0f ? 1.0f : z != z ? z : 0.0f;
-            return z > 0.0f || z != z ? z : 0.0f;
-        case PC_ACT_SIGMOID: {
-            const float s = logistic<FAST>(z);
-            slope = s * (1.0f - s);
-            return s;
-        }
-        default: slope = 1.0f; return z;
+        case PC_ACT_SILU: f(std::integral_constant<int, PC_ACT_SILU>{}); break;
+        case PC_ACT_GELU: f(std::integral_constant<int, PC_ACT_GELU>{}); break;
+        case PC_ACT_RELU: f(std::integral_constant<int, PC_ACT_RELU>{}); break;
+        case PC_ACT_SIGMOID: f(std::integral_constant<int, PC_ACT_SIGMOID>{}); break;
+        default: f(std::integral_constant<int, PC_ACT_NONE>{}); break;
     }
 }
 

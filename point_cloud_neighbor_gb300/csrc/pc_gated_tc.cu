@@ -402,17 +402,22 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                         }
                     }
                     if constexpr (MODE == G_FWD) {
+                        act_switch(a.act, [&](auto act) {
 #pragma unroll
-                        for (int c = 0; c < CH; ++c) g[c] = act_value<P == 1>(a.act, g[c]) * u[c];
+                            for (int c = 0; c < CH; ++c)
+                                g[c] = act_value<act.value, P == 1>(g[c]) * u[c];
+                        });
                         put<T, CH>(static_cast<T *>(a.out) + row * a.N + c0, g, left, a.vec);
                     } else {
+                        act_switch(a.act, [&](auto act) {
 #pragma unroll
-                        for (int c = 0; c < CH; ++c) {
-                            float slope;
-                            const float f = act_both<P == 1>(a.act, g[c], slope);
-                            g[c] = dy[c] * u[c] * slope;
-                            u[c] = dy[c] * f;
-                        }
+                            for (int c = 0; c < CH; ++c) {
+                                float slope;
+                                const float f = act_both<act.value, P == 1>(g[c], slope);
+                                g[c] = dy[c] * u[c] * slope;
+                                u[c] = dy[c] * f;
+                            }
+                        });
                         if (a.bpart != nullptr) {  // (before they are rounded)
                             const float sg = column_sums<CH>(g, lane);
                             const float su = column_sums<CH>(u, lane);

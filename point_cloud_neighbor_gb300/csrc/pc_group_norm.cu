@@ -261,17 +261,21 @@ __global__ void __launch_bounds__(GN_THREADS) gn_apply_kernel(GnArgs a, int nblk
         for (int u = 0; u < U; ++u)
             if (r + int64_t(u) * p.R < r1 && r + int64_t(u) * p.R < len)
                 Vec<T, V>::load(x + (r + int64_t(u) * p.R) * a.C, v[u]);
+        act_switch(a.act, [&](auto act) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < V; ++e)
+                    v[u][e] = act_value<act.value, sizeof(T) == 2>(
+                        fmaf(v[u][e] - mean[e], f[e], o[e]));
+        });
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t i = r + int64_t(u) * p.R;
-            if (i >= r1) break;
-            float t[V];
+            if (i >= len)
 #pragma unroll
-            for (int e = 0; e < V; ++e)
-                t[e] = i < len ? act_value<sizeof(T) == 2>(
-                                     a.act, fmaf(v[u][e] - mean[e], f[e], o[e]))
-                               : 0.0f;
-            Vec<T, V>::store(y + i * a.C, t);
+                for (int e = 0; e < V; ++e) v[u][e] = 0.0f;
+            if (i < r1) Vec<T, V>::store(y + i * a.C, v[u]);
         }
     }
 }
@@ -289,12 +293,20 @@ struct GnChannels {
             b[e] = gn_param<T>(a.b, a.wf32, c + e, 0.0f);
         }
     }
-    // d and xhat of a value
-    __device__ __forceinline__ float d(int act, int e, float x, float dy, float &xhat) const {
-        xhat = (x - mean[e]) * rstd[e];
-        float slope;
-        act_both<sizeof(T) == 2>(act, fmaf(xhat, w[e], b[e]), slope);
-        return dy * slope;
+    // x and dy of U vectors become xhat and d
+    template <int U>
+    __device__ __forceinline__ void form(int act, float (&x)[U][V], float (&dy)[U][V]) const {
+        act_switch(act, [&](auto a) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < V; ++e) {
+                    float slope;
+                    x[u][e] = (x[u][e] - mean[e]) * rstd[e];
+                    act_both<a.value, sizeof(T) == 2>(fmaf(x[u][e], w[e], b[e]), slope);
+                    dy[u][e] *= slope;
+                }
+        });
     }
 };
 
@@ -321,15 +333,14 @@ __global__ void __launch_bounds__(GN_THREADS) gn_sums_kernel(GnArgs a) {
                     Vec<T, V>::load(x + (r + int64_t(u) * p.R) * a.C, v[u]);
                     Vec<T, V>::load(dy + (r + int64_t(u) * p.R) * a.C, g[u]);
                 }
+            ch.form(a.act, v, g);
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (r + int64_t(u) * p.R < r1)
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        float xhat;
-                        const float d = ch.d(a.act, e, v[u][e], g[u][e], xhat);
-                        t1[e] += d;
-                        t2[e] = fmaf(d, xhat, t2[e]);
+                        t1[e] += g[u][e];
+                        t2[e] = fmaf(g[u][e], v[u][e], t2[e]);
                     }
         }
     }
@@ -452,18 +463,17 @@ __global__ void __launch_bounds__(GN_THREADS) gn_dx_kernel(GnArgs a, int nblk, i
                 Vec<T, V>::load(dy + i * a.C, g[u]);
             }
         }
+        ch.form(a.act, v, g);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t i = r + int64_t(u) * p.R;
-            if (i >= r1) break;
             float t[V];
 #pragma unroll
-            for (int e = 0; e < V; ++e) {
-                float xhat;
-                const float d = ch.d(a.act, e, v[u][e], g[u][e], xhat);
-                t[e] = i < len ? ch.rstd[e] * (fmaf(d, ch.w[e], -h1[e]) - xhat * h2[e]) : 0.0f;
-            }
-            Vec<T, V>::store(dx + i * a.C, t);
+            for (int e = 0; e < V; ++e)
+                t[e] = i < len ? ch.rstd[e] *
+                                     (fmaf(g[u][e], ch.w[e], -h1[e]) - v[u][e] * h2[e])
+                               : 0.0f;
+            if (i < r1) Vec<T, V>::store(dx + i * a.C, t);
         }
     }
 }
