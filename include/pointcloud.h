@@ -678,9 +678,13 @@ typedef enum pc_activation {
  * grad_x is 0 past the lengths.  grad_x, grad_weight and grad_bias ([C] of
  * param_dtype) may be NULL.
  *
- * Scratch (the library's stream-ordered pool): at most 16 C float32 for each SM
- * (8 blocks, two sums a channel), 4 float32 for each group and cloud, and 2 B C
- * float32 in the backward call.
+ * Clouds that fit the shared memory of a thread block cluster (up to 16 blocks)
+ * are read once, in one launch, where that is the shorter way; its waits are bounded
+ * as those of the attention kernels.
+ *
+ * Scratch (the library's stream-ordered pool): forward 2 float32 for each group and
+ * block and each group and cloud, backward 2 C float32 for each block and cloud; the
+ * blocks are at most 8 a SM, or one a cloud (16 in a cluster) where that is more.
  */
 int pc_group_norm(const void *x, int dtype, int64_t B, int64_t L, int64_t C, int64_t groups,
                   const void *weight, const void *bias, int param_dtype, double eps,
@@ -778,7 +782,9 @@ int pc_device_status(void *stream, int reset, int32_t *out_status);
  *                         never issues the copies of its streamed side.
  *                         That block's outputs are unspecified.
  *   PC_STALL_GATED        the same for the launches of a gated projection: the
- *                         first thread block never issues a copy.
+ *                         first thread block never issues a copy;
+ *   PC_STALL_GROUP_NORM   the same for group norm of clouds that fit a thread
+ *                         block cluster.
  * Each ends as a real timeout does: PC_ERR_DEVICE_TIMEOUT in the status
  * word, -1 in the outputs the stopped blocks did not finish.
  * pc_debug_set_fps_grid_stall(e) sets or clears PC_STALL_FPS_GRID alone.
@@ -788,6 +794,7 @@ int pc_device_status(void *stream, int reset, int32_t *out_status);
 #define PC_STALL_TILE_STREAM 4
 #define PC_STALL_ATTENTION 8
 #define PC_STALL_GATED 16
+#define PC_STALL_GROUP_NORM 32
 void pc_set_wait_timeout_ns(uint64_t ns);
 void pc_debug_set_stall(int mask);
 void pc_debug_set_fps_grid_stall(int enable);

@@ -10,21 +10,46 @@
 
 namespace pcn {
 
-// s(z) = 1 / (1 + exp(-z)).  FAST, for results that are rounded to bfloat16:
-// the approximate exponential and quotient, off by up to 2^-21 (|z| + 2) relative.
+__device__ __forceinline__ float approx_rcp(float x) {
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float approx_ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float LOG2_E = 1.4426950408889634f;
+
+// s(z) = 1 / (1 + exp(-z)); the reciprocal of a number from 1 on, off by 2^-23.
+// FAST, for results that are rounded to bfloat16: exp as a power of 2 whose exponent is
+// rounded once: off by up to 2^-21 (|z| + 2) relative.
 template <bool FAST>
 __device__ __forceinline__ float logistic(float z) {
-    if (FAST) return __fdividef(1.0f, 1.0f + __expf(-z));
-    return 1.0f / (1.0f + expf(-z));
+    return approx_rcp(1.0f + (FAST ? approx_ex2(-LOG2_E * z) : expf(-z)));
 }
 
-// The normal distribution's cumulative function.  Not FAST: by erfc, so that
-// the far negative side keeps its relative accuracy; FAST off by 2^-24 absolute.
+// The normal distribution's cumulative function and e = exp(-z^2 / 2).  Not FAST: by
+// erfc, so that the far negative side keeps its relative accuracy.  FAST: formula
+// 7.1.26 of Abramowitz and Stegun's Handbook of Mathematical Functions,
+//   erfc(x) = (a1 t + ... + a5 t^5) exp(-x^2),  t = 1 / (1 + 0.3275911 x),
+// off by 1.5e-7 absolute (here half of that), at x = |z| / sqrt(2); it takes half the
+// instructions of erff and shares the exponential with the derivative.
 template <bool FAST>
-__device__ __forceinline__ float normal_cdf(float z) {
-    constexpr float R = 0.70710678118654752f;
-    if (FAST) return fmaf(0.5f, erff(R * z), 0.5f);
-    return 0.5f * erfcf(-R * z);
+__device__ __forceinline__ float normal_cdf(float z, float &e) {
+    if (!FAST) {
+        e = expf(-0.5f * z * z);
+        return 0.5f * erfcf(-0.70710678118654752f * z);
+    }
+    const float t = approx_rcp(fmaf(fabsf(z), 0.3275911f * 0.70710678f, 1.0f));
+    e = approx_ex2(-0.5f * LOG2_E * z * z);
+    float p = fmaf(0.5f * 1.061405429f, t, 0.5f * -1.453152027f);
+    p = fmaf(p, t, 0.5f * 1.421413741f);
+    p = fmaf(p, t, 0.5f * -0.284496736f);
+    p = fmaf(p, t, 0.5f * 0.254829592f);
+    const float q = p * t * e;
+    return z < 0.0f ? q : 1.0f - q;
 }
 
 // act(z).  The activation is a template parameter: a switch for every value keeps
@@ -33,7 +58,10 @@ __device__ __forceinline__ float normal_cdf(float z) {
 template <int ACT, bool FAST>
 __device__ __forceinline__ float act_value(float z) {
     if (ACT == PC_ACT_SILU) return z * logistic<FAST>(z);
-    if (ACT == PC_ACT_GELU) return z * normal_cdf<FAST>(z);
+    if (ACT == PC_ACT_GELU) {
+        float e;
+        return z * normal_cdf<FAST>(z, e);
+    }
     if (ACT == PC_ACT_RELU) return z > 0.0f || z != z ? z : 0.0f;  // (a NaN stays)
     if (ACT == PC_ACT_SIGMOID) return logistic<FAST>(z);
     return z;
@@ -49,8 +77,8 @@ __device__ __forceinline__ float act_both(float z, float &slope) {
     }
     if (ACT == PC_ACT_GELU) {
         constexpr float N = 0.39894228040143268f;  // 1 / sqrt(2 pi)
-        const float c = normal_cdf<FAST>(z);
-        const float e = FAST ? __expf(-0.5f * z * z) : expf(-0.5f * z * z);
+        float e;
+        const float c = normal_cdf<FAST>(z, e);
         slope = fmaf(z * N, e, c);
         return z * c;
     }

@@ -194,7 +194,7 @@ void pc_debug_set_fps_grid_stall(int enable) {
 
 void pc_debug_set_stall(int mask) {
     g_stall.store(mask & (PC_STALL_FPS_GRID | PC_STALL_FPS_CLUSTER | PC_STALL_TILE_STREAM |
-                          PC_STALL_ATTENTION | PC_STALL_GATED));
+                          PC_STALL_ATTENTION | PC_STALL_GATED | PC_STALL_GROUP_NORM));
 }
 
 void pc_set_sm_reserve(int sms) { g_sm_reserve.store(sms < 0 ? 0 : sms); }

@@ -24,70 +24,26 @@
 // No atomics; every join has a fixed order.
 //
 // Bound: memory.
-#include "pc_act.cuh"
-#include "pc_internal.h"
-#include "pc_vec.cuh"
+#include "pc_group_norm.cuh"
 #include "pointcloud.h"
 
+#include <atomic>
 #include <cstdio>
 
 namespace pcn {
 namespace {
 
-constexpr int GN_THREADS = 256;
-constexpr int GN_MAX_C = 16384;
-
-struct GnArgs {
-    const void *x, *dy, *w, *b;
-    void *y;                 // forward: y; backward: dx
-    const int64_t *lengths;
-    float *mean, *rstd;      // [B, G]
-    float2 *gpart;           // forward: [B][nblk][G, or chunks] mean and sum of squares
-    float *cpart;            // backward: [B][nblk][2][C]
-    float *chan;             // backward: [B][2][C]
-    void *dw, *db;
-    int64_t B, L;
-    int C, G, cg;            // channels, groups, channels of a group
-    int width, nchunk;       // channels of a chunk (a block's), chunks
-    int per;                 // chunks of a group wider than a block, else 0
-    int nblk;                // blocks that share a cloud's rows
-    float eps;
-    int act;
-    bool wf32;               // weight and bias are float32
-};
-
-__device__ __forceinline__ int64_t gn_len(const GnArgs &a, int64_t b) {
-    if (a.lengths == nullptr) return a.L;
-    const int64_t n = a.lengths[b];
-    return n < 0 ? 0 : n > a.L ? a.L : n;
-}
-
-// rows of a block of `nblk` that share `n`: [n blk / nblk, n (blk + 1) / nblk)
-__device__ __forceinline__ int64_t gn_row(int64_t n, int blk, int nblk) {
-    return n * blk / nblk;
-}
-
-template <class T>
-__device__ __forceinline__ float gn_param(const void *p, bool f32, int c, float none) {
-    if (p == nullptr) return none;
-    if (f32) return static_cast<const float *>(p)[c];
-    float v;
-    Vec<T, 1>::load(static_cast<const T *>(p) + c, &v);
-    return v;
-}
-
-// A count, a mean and a sum of squares around it.
-struct Moments {
-    float n = 0.0f, m = 0.0f, s = 0.0f;
-    __device__ __forceinline__ void join(float nb, float mb, float sb) {
-        const float t = n + nb;
-        if (nb == 0.0f) return;
-        const float f = nb / t, d = mb - m;
-        s = s + fmaf(d * d, n * f, sb);
-        m = fmaf(d, f, m);
-        n = t;
+// V elements written past the caches' other contents.
+template <class T, int V>
+__device__ __forceinline__ void stream(T *p, const float *v) {
+    if constexpr (V * sizeof(T) == 16) {
+        float4 t;
+        Vec<T, V>::store(reinterpret_cast<T *>(&t), v);
+        __stcs(reinterpret_cast<float4 *>(p), t);
+    } else {
+        Vec<T, V>::store(p, v);
     }
-};
+}
 
 // The place of a block: its cloud, chunk of channels, share of the rows; and
 // a thread's vector of channels and first row.
@@ -97,10 +53,10 @@ struct GnPlace {
     int blk, chunk, c0, width, tpr, R, c, r;
     bool on;
     __device__ __forceinline__ GnPlace(const GnArgs &a, int nblk) {
-        int64_t i = blockIdx.x;
-        blk = int(i % nblk), i /= nblk;
-        chunk = int(i % a.nchunk);
-        b = i / a.nchunk;
+        unsigned i = blockIdx.x;
+        blk = int(i % unsigned(nblk)), i /= unsigned(nblk);
+        chunk = int(i % unsigned(a.nchunk));
+        b = i / unsigned(a.nchunk);
         if (a.per == 0) {
             c0 = chunk * a.width;
             width = min(a.width, a.C - c0);
@@ -124,7 +80,8 @@ __global__ void __launch_bounds__(GN_THREADS) gn_stats_kernel(GnArgs a) {
     __shared__ float sm[GN_THREADS * V], ss[GN_THREADS * V], sn[GN_THREADS];
     const GnPlace<V> p(a, a.nblk);
     const int64_t len = gn_len(a, p.b);
-    const int64_t r0 = gn_row(len, p.blk, a.nblk), r1 = gn_row(len, p.blk + 1, a.nblk);
+    const GnSplit split(len, a.nblk);
+    const int64_t r0 = split.row(p.blk), r1 = split.row(p.blk + 1);
     const T *x = static_cast<const T *>(a.x) + p.b * a.L * a.C + p.c;
     float n = 0.0f, m[V], s[V];
 #pragma unroll
@@ -210,13 +167,13 @@ __global__ void __launch_bounds__(128) gn_join_kernel(GnArgs a) {
     const int64_t bg = blockIdx.x, b = bg / a.G;
     const int g = int(bg % a.G), per = a.per ? a.per : 1, all = a.G * per;
     const int64_t len = gn_len(a, b);
+    const GnSplit split(len, a.nblk);
     Moments t;
     for (int i = threadIdx.x; i < a.nblk * per; i += 128) {
         const int blk = i / per, k = i % per;
         const float2 v = a.gpart[(b * a.nblk + blk) * all + g * per + k];
         const int each = a.per ? min(a.width, a.cg - k * a.width) : a.cg;
-        t.join(float(gn_row(len, blk + 1, a.nblk) - gn_row(len, blk, a.nblk)) * float(each), v.x,
-               v.y);
+        t.join(float(split.rows(blk)) * float(each), v.x, v.y);
     }
     __shared__ float red[3][4];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -243,19 +200,25 @@ __global__ void __launch_bounds__(GN_THREADS) gn_apply_kernel(GnArgs a, int nblk
     const GnPlace<V> p(a, nblk);
     if (!p.on) return;
     const int64_t len = gn_len(a, p.b);
-    const int64_t r0 = gn_row(a.L, p.blk, nblk), r1 = gn_row(a.L, p.blk + 1, nblk);
+    const GnSplit split(a.L, nblk);
+    const int64_t r0 = split.row(p.blk), r1 = split.row(p.blk + 1);
     const int64_t at = p.b * a.L * a.C + p.c;
     const T *x = static_cast<const T *>(a.x) + at;
     T *y = static_cast<T *>(a.y) + at;
     float mean[V], f[V], o[V];
+    int group[V];
+    gn_groups(p.c, a.cg, group);
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        const int64_t g = p.b * a.G + (p.c + e) / a.cg;
+        const int64_t g = p.b * a.G + group[e];
         mean[e] = a.mean[g];
         f[e] = a.rstd[g] * gn_param<T>(a.w, a.wf32, p.c + e, 1.0f);
         o[e] = gn_param<T>(a.b, a.wf32, p.c + e, 0.0f);
     }
-    for (int64_t r = r0 + p.r; r < r1; r += int64_t(U) * p.R) {
+    // from the end, where the second level cache still has what the first pass read
+    const int64_t step = int64_t(U) * p.R, first = r0 + p.r;
+    for (int64_t r = first < r1 ? first + (r1 - 1 - first) / step * step : -1; r >= first;
+         r -= step) {
         float v[U][V];
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -275,40 +238,10 @@ __global__ void __launch_bounds__(GN_THREADS) gn_apply_kernel(GnArgs a, int nblk
             if (i >= len)
 #pragma unroll
                 for (int e = 0; e < V; ++e) v[u][e] = 0.0f;
-            if (i < r1) Vec<T, V>::store(y + i * a.C, v[u]);
+            if (i < r1) stream<T, V>(y + i * a.C, v[u]);
         }
     }
 }
-
-// The values of a thread's channels in the backward passes.
-template <class T, int V>
-struct GnChannels {
-    float mean[V], rstd[V], w[V], b[V];
-    __device__ __forceinline__ GnChannels(const GnArgs &a, int64_t cloud, int c) {
-#pragma unroll
-        for (int e = 0; e < V; ++e) {
-            const int64_t g = cloud * a.G + (c + e) / a.cg;
-            mean[e] = a.mean[g], rstd[e] = a.rstd[g];
-            w[e] = gn_param<T>(a.w, a.wf32, c + e, 1.0f);
-            b[e] = gn_param<T>(a.b, a.wf32, c + e, 0.0f);
-        }
-    }
-    // x and dy of U vectors become xhat and d
-    template <int U>
-    __device__ __forceinline__ void form(int act, float (&x)[U][V], float (&dy)[U][V]) const {
-        act_switch(act, [&](auto a) {
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < V; ++e) {
-                    float slope;
-                    x[u][e] = (x[u][e] - mean[e]) * rstd[e];
-                    act_both<a.value, sizeof(T) == 2>(fmaf(x[u][e], w[e], b[e]), slope);
-                    dy[u][e] *= slope;
-                }
-        });
-    }
-};
 
 // Backward 1: the channels' sums of d and d xhat over a block's rows.
 template <class T, int V>
@@ -317,7 +250,8 @@ __global__ void __launch_bounds__(GN_THREADS) gn_sums_kernel(GnArgs a) {
     __shared__ float s1[GN_THREADS * V], s2[GN_THREADS * V];
     const GnPlace<V> p(a, a.nblk);
     const int64_t len = gn_len(a, p.b);
-    const int64_t r0 = gn_row(len, p.blk, a.nblk), r1 = gn_row(len, p.blk + 1, a.nblk);
+    const GnSplit split(len, a.nblk);
+    const int64_t r0 = split.row(p.blk), r1 = split.row(p.blk + 1);
     const int64_t at = p.b * a.L * a.C + p.c;
     const T *x = static_cast<const T *>(a.x) + at, *dy = static_cast<const T *>(a.dy) + at;
     float t1[V], t2[V];
@@ -442,7 +376,8 @@ __global__ void __launch_bounds__(GN_THREADS) gn_dx_kernel(GnArgs a, int nblk, i
     }
     __syncthreads();
     if (!p.on) return;
-    const int64_t r0 = gn_row(a.L, p.blk, nblk), r1 = gn_row(a.L, p.blk + 1, nblk);
+    const GnSplit split(a.L, nblk);
+    const int64_t r0 = split.row(p.blk), r1 = split.row(p.blk + 1);
     const int64_t at = p.b * a.L * a.C + p.c;
     const T *x = static_cast<const T *>(a.x) + at, *dy = static_cast<const T *>(a.dy) + at;
     T *dx = static_cast<T *>(a.y) + at;
@@ -450,10 +385,12 @@ __global__ void __launch_bounds__(GN_THREADS) gn_dx_kernel(GnArgs a, int nblk, i
     float h1[V], h2[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-        h1[e] = m1[(p.c + e) / a.cg - g0];
-        h2[e] = m2[(p.c + e) / a.cg - g0];
+        h1[e] = m1[ch.group[e] - g0];
+        h2[e] = m2[ch.group[e] - g0];
     }
-    for (int64_t r = r0 + p.r; r < r1; r += int64_t(U) * p.R) {
+    const int64_t step = int64_t(U) * p.R, first = r0 + p.r;
+    for (int64_t r = first < r1 ? first + (r1 - 1 - first) / step * step : -1; r >= first;
+         r -= step) {
         float v[U][V], g[U][V];
 #pragma unroll
         for (int u = 0; u < U; ++u) {
@@ -473,7 +410,7 @@ __global__ void __launch_bounds__(GN_THREADS) gn_dx_kernel(GnArgs a, int nblk, i
                 t[e] = i < len ? ch.rstd[e] *
                                      (fmaf(g[u][e], ch.w[e], -h1[e]) - v[u][e] * h2[e])
                                : 0.0f;
-            if (i < r1) Vec<T, V>::store(dx + i * a.C, t);
+            if (i < r1) stream<T, V>(dx + i * a.C, t);
         }
     }
 }
@@ -502,25 +439,51 @@ struct GnPlan {
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Blocks that share a cloud's rows: as many as are resident together, so that each has
+// a long share, and none without a batch of rows.
+template <class K>
+cudaError_t gn_blocks(K kernel, std::atomic<int> (&resident)[64], const DeviceInfo &dev,
+                      int64_t sets, int64_t L, int batch, int *out) {
+    std::atomic<int> &kept = resident[dev.device & 63];
+    int per_sm = kept.load(std::memory_order_relaxed);
+    if (per_sm == 0) {
+        const cudaError_t e =
+            cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, GN_THREADS, 0);
+        if (e != cudaSuccess) return e;
+        per_sm = per_sm < 1 ? 1 : per_sm > 8 ? 8 : per_sm;
+        kept.store(per_sm, std::memory_order_relaxed);
+    }
+    int64_t n = int64_t(dev.sm_count) * per_sm / sets;
+    const int64_t want = ceil_div(L, batch);
+    if (n > want) n = want;
+    *out = int(n < 1 ? 1 : n);
+    return cudaSuccess;
+}
+
 template <class T, int V>
 cudaError_t gn_run(GnArgs a, const GnPlan &p) {
     const int R = GN_THREADS / (a.width / V);
-    const int64_t sets = a.B * a.nchunk, most = int64_t(p.dev->sm_count) * 8;
-    const int u1 = p.backward ? (V >= 4 ? 2 : 4) : (V >= 4 ? 4 : 8);
-    int64_t nblk = ceil_div(most, sets);
-    const int64_t want = ceil_div(a.L, int64_t(R) * u1);
-    if (nblk > want) nblk = want;
-    if (nblk < 1) nblk = 1;
-    a.nblk = int(nblk);
-    if (sets * nblk > 2147483647 || a.B * a.G > 2147483647 ||
-        a.B * ((2 * int64_t(a.C) + 31) / 32) > 2147483647)
-        return cudaErrorInvalidConfiguration;
-    cudaStream_t st = p.stream;
-    const unsigned grid = unsigned(sets * nblk);
-    void *scratch = nullptr;
+    const int64_t sets = a.B * a.nchunk;
+    const int batch = R * (p.backward ? (V >= 4 ? 2 : 4) : (V >= 4 ? 4 : 8));
+    static std::atomic<int> resident[4][64] = {};
+    int second = 1;  // blocks a cloud of the second pass
     cudaError_t e;
     if (!p.backward) {
-        const size_t parts = size_t(a.B) * nblk * (a.per ? a.nchunk : a.G) * sizeof(float2);
+        e = gn_blocks(gn_stats_kernel<T, V>, resident[0], *p.dev, sets, a.L, batch, &a.nblk);
+        if (e == cudaSuccess)
+            e = gn_blocks(gn_apply_kernel<T, V>, resident[1], *p.dev, sets, a.L, batch, &second);
+    } else {
+        e = gn_blocks(gn_sums_kernel<T, V>, resident[2], *p.dev, sets, a.L, batch, &a.nblk);
+        if (e == cudaSuccess)
+            e = gn_blocks(gn_dx_kernel<T, V>, resident[3], *p.dev, sets, a.L, batch, &second);
+    }
+    if (e != cudaSuccess) return e;
+    // (B C is at most 2^30, so no grid is beyond 31 bits)
+    cudaStream_t st = p.stream;
+    const unsigned grid = unsigned(sets * a.nblk), grid2 = unsigned(sets * second);
+    void *scratch = nullptr;
+    if (!p.backward) {
+        const size_t parts = size_t(a.B) * a.nblk * (a.per ? a.nchunk : a.G) * sizeof(float2);
         const size_t stats = a.mean == nullptr ? size_t(a.B) * a.G * sizeof(float) : 0;
         if ((e = scratch_alloc(*p.dev, &scratch, parts + 2 * stats, st)) != cudaSuccess) return e;
         a.gpart = static_cast<float2 *>(scratch);
@@ -530,9 +493,9 @@ cudaError_t gn_run(GnArgs a, const GnPlan &p) {
         }
         gn_stats_kernel<T, V><<<grid, GN_THREADS, 0, st>>>(a);
         gn_join_kernel<<<unsigned(a.B * a.G), 128, 0, st>>>(a);
-        gn_apply_kernel<T, V><<<grid, GN_THREADS, 0, st>>>(a, a.nblk);
+        gn_apply_kernel<T, V><<<grid2, GN_THREADS, 0, st>>>(a, second);
     } else {
-        const size_t parts = size_t(a.B) * nblk * 2 * a.C * sizeof(float);
+        const size_t parts = size_t(a.B) * a.nblk * 2 * a.C * sizeof(float);
         const size_t chan = size_t(a.B) * 2 * a.C * sizeof(float);
         if ((e = scratch_alloc(*p.dev, &scratch, parts + chan, st)) != cudaSuccess) return e;
         a.cpart = static_cast<float *>(scratch);
@@ -540,9 +503,9 @@ cudaError_t gn_run(GnArgs a, const GnPlan &p) {
         gn_sums_kernel<T, V><<<grid, GN_THREADS, 0, st>>>(a);
         gn_channel_kernel<<<unsigned(a.B * ((2 * a.C + 31) / 32)), dim3(32, 32), 0, st>>>(a);
         const int nparam = a.dw || a.db ? int(ceil_div(2 * a.C, GN_THREADS)) : 0;
-        const unsigned dxgrid = a.y ? grid : 0;
+        const unsigned dxgrid = a.y ? grid2 : 0;
         if (dxgrid + nparam > 0)
-            gn_dx_kernel<T, V><<<dxgrid + nparam, GN_THREADS, 0, st>>>(a, a.nblk, nparam);
+            gn_dx_kernel<T, V><<<dxgrid + nparam, GN_THREADS, 0, st>>>(a, second, nparam);
     }
     e = cudaGetLastError();
     const cudaError_t f = scratch_free(scratch, st);
@@ -553,8 +516,12 @@ template <class T>
 cudaError_t gn_dispatch(GnArgs a, const GnPlan &p) {
     uintptr_t bits = reinterpret_cast<uintptr_t>(a.x) | reinterpret_cast<uintptr_t>(a.y) |
                      reinterpret_cast<uintptr_t>(a.dy);
+    const int dtype = sizeof(T) == 2 ? PC_BF16 : PC_F32;
     for (int V = 16 / int(sizeof(T)); V >= 1; V /= 2) {
-        if (bits % (V * sizeof(T))) continue;
+        if (bits % (V * sizeof(T)) || a.C % V) continue;
+        const GnCluster cl = gn_cluster_plan(*p.dev, a, dtype, V, p.backward);
+        if (cl.blocks > 0)
+            return gn_cluster_run(*p.dev, a, dtype, V, p.backward, cl, p.stream);
         a.width = gn_width(a.C, a.cg, V, &a.per);
         if (a.width == 0) continue;
         a.nchunk = a.per ? a.G * a.per : (a.C + a.width - 1) / a.width;

@@ -313,7 +313,8 @@ GN_SHAPES = [(1, 1, 2, 1), (1, 1, 64, 2), (2, 3, 6, 3), (1, 64, 384, 32), (3, 17
              (5, 100, 48, 4), (2, 333, 195, 13), (2, 50, 515, 5), (1, 1000, 2048, 1),
              (2, 40, 2048, 32), (1, 30, 4104, 3), (1, 9, 16384, 1), (1, 20, 2310, 2),
              (2, 11, 1021, 1), (40, 7, 32, 8), (1, 5000, 64, 8), (1, 20000, 24, 2),
-             (300, 2, 16, 4), (7, 257, 12, 4), (16, 1024, 128, 32)]
+             (300, 2, 16, 4), (7, 257, 12, 4), (16, 1024, 128, 32), (1, 60000, 40, 4),
+             (2, 30011, 35, 7), (3, 4093, 195, 13), (1, 2048, 384, 32), (2, 9000, 64, 1)]
 
 
 @pytest.mark.parametrize("dtype,pdtype", [(torch.float32, torch.float32),
@@ -707,6 +708,25 @@ def test_a_withheld_copy_ends_with_the_status_word():
             pc.pc_set_wait_timeout_ns(2_000_000_000)
         again = gated_all(*ins, "silu")
         assert all(torch.equal(want[k], again[k]) for k in want)
+
+
+def test_a_withheld_copy_of_group_norm_ends_with_the_status_word():
+    g = gen(6)
+    x, dy, w = randn(g, 3, 2000, 64), randn(g, 3, 2000, 64), randn(g, 64)
+    want = gn_all(x, 4, w, w, "silu", None, dy)
+    torch.cuda.synchronize()
+    try:
+        pc.pc_set_wait_timeout_ns(50_000_000)
+        pc.pc_debug_set_stall(pc.PC_STALL_GROUP_NORM)
+        pc.pc_group_norm(x, 4, w, w)
+        assert pc.pc_device_status(reset=True) == 4
+        pc.pc_group_norm_backward(dy, x, want["mean"], want["rstd"], 4, w, w)
+        assert pc.pc_device_status(reset=True) == 4
+    finally:
+        pc.pc_debug_set_stall(0)
+        pc.pc_set_wait_timeout_ns(2_000_000_000)
+    again = gn_all(x, 4, w, w, "silu", None, dy)
+    assert all(torch.equal(want[k], again[k]) for k in want)
 
 
 def test_refusals():
