@@ -738,16 +738,39 @@ int pc_embedding_backward(const void *grad_out, int dtype, int64_t B, int64_t V,
  * It forms a and u again, so that nothing but the arguments is kept between
  * the calls.  Outputs may be NULL: grad_x; grad_w_gate and grad_w_up together;
  * grad_b_gate and grad_b_up together.
+ *
+ * Scratch: workspace (device, 256-byte aligned, not shared with calls that may run at
+ * the same time) where it is not NULL and has at least
+ * pc_gated_linear_workspace_bytes(dtype, rows, C, F, gradients) bytes, else the
+ * library's stream-ordered pool (which returns what is beyond 256 MiB at every
+ * synchronization, so that large calls spend long on mapping it again).  gradients: 0
+ * for the forward call, or which gradients are asked for.  bfloat16 forward calls with C
+ * a multiple of 8 and 16-byte aligned arrays need none; backward calls keep da and du (4
+ * bytes a hidden unit and row, float32 12), float32 calls three bfloat16 parts of x and
+ * the weights; parts of split sums come to it.
+ *
+ * Runs on the tensor cores, which add in float32 and cut off what a chain of at most
+ * 16,384 products leaves; da and du are rounded to bfloat16 in bfloat16 calls.  float32
+ * takes three bfloat16 parts of each operand (products to 2^-24, sums rounded to nearest
+ * every 64).  Device-side waits are bounded as those of the attention kernels.
  */
+#define PC_GATED_GRAD_X 1
+#define PC_GATED_GRAD_WEIGHT 2
+#define PC_GATED_GRAD_BIAS 4
+size_t pc_gated_linear_workspace_bytes(int dtype, int64_t rows, int64_t C, int64_t F,
+                                       int gradients);
+
 int pc_gated_linear(const void *x, int dtype, int64_t rows, int64_t C, int64_t F,
                     const void *w_gate, const void *w_up, const void *b_gate,
-                    const void *b_up, int activation, void *out, void *stream);
+                    const void *b_up, int activation, void *out, void *workspace,
+                    size_t workspace_bytes, void *stream);
 
 int pc_gated_linear_backward(const void *grad_out, const void *x, int dtype, int64_t rows,
                              int64_t C, int64_t F, const void *w_gate, const void *w_up,
                              const void *b_gate, const void *b_up, int activation,
                              void *grad_x, void *grad_w_gate, void *grad_w_up,
-                             void *grad_b_gate, void *grad_b_up, void *stream);
+                             void *grad_b_gate, void *grad_b_up, void *workspace,
+                             size_t workspace_bytes, void *stream);
 
 /*
  * Device status word.  Kernels that wait on other thread blocks bound every

@@ -103,9 +103,12 @@ _SIGNATURES = {
     "pc_embedding_backward": (ctypes.c_int, [_P, ctypes.c_int, _I, _I, _I, _P, _I,
                                              ctypes.c_double, _P, _P]),
     "pc_gated_linear": (ctypes.c_int, [_P, ctypes.c_int, _I, _I, _I, _P, _P, _P, _P,
-                                       ctypes.c_int, _P, _P]),
+                                       ctypes.c_int, _P, _P, ctypes.c_size_t, _P]),
     "pc_gated_linear_backward": (ctypes.c_int, [_P, _P, ctypes.c_int, _I, _I, _I, _P, _P, _P,
-                                                _P, ctypes.c_int, _P, _P, _P, _P, _P, _P]),
+                                                _P, ctypes.c_int, _P, _P, _P, _P, _P, _P,
+                                                ctypes.c_size_t, _P]),
+    "pc_gated_linear_workspace_bytes": (ctypes.c_size_t, [ctypes.c_int, _I, _I, _I,
+                                                          ctypes.c_int]),
     "pc_device_status": (ctypes.c_int, [_P, ctypes.c_int,
                                         ctypes.POINTER(ctypes.c_int32)]),
     "pc_set_wait_timeout_ns": (None, [ctypes.c_uint64]),

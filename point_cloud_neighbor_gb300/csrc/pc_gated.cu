@@ -43,7 +43,8 @@ int gated_cuda(const char *what, cudaError_t e) {
 
 extern "C" int pc_gated_linear(const void *x, int dtype, int64_t rows, int64_t C, int64_t F,
                                const void *w_gate, const void *w_up, const void *b_gate,
-                               const void *b_up, int activation, void *out, void *stream) {
+                               const void *b_up, int activation, void *out, void *workspace,
+                               size_t workspace_bytes, void *stream) {
     using namespace pcn;
     int rc = gated_check("gated_linear", dtype, rows, C, F, b_gate, b_up, activation);
     if (rc != PC_OK) return rc;
@@ -61,6 +62,8 @@ extern "C" int pc_gated_linear(const void *x, int dtype, int64_t rows, int64_t C
     GatedArgs a{};
     a.x = x, a.wg = w_gate, a.wu = w_up, a.bg = b_gate, a.bu = b_up, a.y = out;
     a.rows = rows, a.C = int(C), a.F = int(F), a.act = activation;
+    a.workspace = workspace, a.workspace_bytes = workspace_bytes;
+    if (workspace && (rc = api_check_ptr(workspace, d, 256, "workspace")) != PC_OK) return rc;
     cudaStream_t st = static_cast<cudaStream_t>(stream);
     return gated_cuda("gated_linear", gated_tc_forward(*dev, a, dtype, st));
 }
@@ -70,7 +73,7 @@ extern "C" int pc_gated_linear_backward(const void *grad_out, const void *x, int
                                         const void *w_up, const void *b_gate, const void *b_up,
                                         int activation, void *grad_x, void *grad_w_gate,
                                         void *grad_w_up, void *grad_b_gate, void *grad_b_up,
-                                        void *stream) {
+                                        void *workspace, size_t workspace_bytes, void *stream) {
     using namespace pcn;
     const char *what = "gated_linear_backward";
     int rc = gated_check(what, dtype, rows, C, F, b_gate, b_up, activation);
@@ -113,5 +116,24 @@ extern "C" int pc_gated_linear_backward(const void *grad_out, const void *x, int
     a.x = x, a.wg = w_gate, a.wu = w_up, a.bg = b_gate, a.bu = b_up, a.dy = grad_out;
     a.dx = outs[0], a.dwg = outs[1], a.dwu = outs[2], a.dbg = outs[3], a.dbu = outs[4];
     a.rows = rows, a.C = int(C), a.F = int(F), a.act = activation;
+    a.workspace = workspace, a.workspace_bytes = workspace_bytes;
+    if (workspace && (rc = api_check_ptr(workspace, d, 256, "workspace")) != PC_OK) return rc;
     return gated_cuda(what, gated_tc_backward(*dev, a, dtype, st));
+}
+
+extern "C" size_t pc_gated_linear_workspace_bytes(int dtype, int64_t rows, int64_t C, int64_t F,
+                                                  int gradients) {
+    using namespace pcn;
+    const DeviceInfo *dev = nullptr;
+    if (gated_check("gated_linear_workspace_bytes", dtype, rows, C, F, nullptr, nullptr,
+                    PC_ACT_NONE) != PC_OK ||
+        rows == 0 || F == 0 || api_current_device(&dev) != PC_OK)
+        return 0;
+    GatedArgs a{};
+    a.rows = rows, a.C = int(C), a.F = int(F);
+    void *some = &a;  // (only which gradients there are counts)
+    if (gradients & PC_GATED_GRAD_X) a.dx = some;
+    if (gradients & PC_GATED_GRAD_WEIGHT) a.dwg = a.dwu = some;
+    if (gradients & PC_GATED_GRAD_BIAS) a.dbg = a.dbu = some;
+    return gated_tc_scratch(*dev, a, dtype, gradients != 0);
 }

@@ -11,9 +11,12 @@ struct GatedArgs {
     void *y, *dx, *dwg, *dwu, *dbg, *dbu;
     int64_t rows;
     int C, F, act;
+    void *workspace;
+    size_t workspace_bytes;
 };
 
-// On the tensor cores (pc_gated_tc.cu), any sizes and alignment.
+// On the tensor cores (pc_gated_tc.cu), any sizes and alignment; the scratch these take.
+size_t gated_tc_scratch(const DeviceInfo &dev, const GatedArgs &a, int dtype, bool backward);
 cudaError_t gated_tc_forward(const DeviceInfo &dev, const GatedArgs &a, int dtype,
                              cudaStream_t st);
 cudaError_t gated_tc_backward(const DeviceInfo &dev, const GatedArgs &a, int dtype,

@@ -51,6 +51,7 @@ constexpr int PANEL = 64 * 128;  // bytes of a 64 x 64 panel of an MN-major oper
 
 struct GemmMaps {
     CUtensorMap a0, a1, b0, b1;
+    CUtensorMap dy, o0, o1;  // boxes of 32 x 32: GRAD dy, da, du; FWD y in o0
 };
 
 struct GemmArgs {
@@ -73,13 +74,19 @@ struct GemmArgs {
 template <int MODE, int P, int BN>
 struct GCfg {
     static constexpr bool PAIR = MODE == G_FWD || MODE == G_GRAD;
-    static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;  // of a part
-    static constexpr int STAGE = P * (A_BYTES + B_BYTES);
-    static constexpr int FIT = (224 * 1024 - 1024) / STAGE, STAGES = FIT > 8 ? 8 : FIT;
-    static_assert(STAGES >= 2, "shared memory");
-    static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + 512;
-    static_assert(SMEM > 114 * 1024 && SMEM <= 227 * 1024, "one block a SM");
+    static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+    static constexpr int STAGE = A_BYTES + B_BYTES;  // of one part of both operands
     static constexpr int EWARPS = 8, THREADS = 32 * (4 + EWARPS);
+    // PAIR with chunks of 32 columns: a warp's 32 x 32 tiles of the arrays that are as
+    // large as the result, on their way from or to global memory.  bfloat16: as tensor
+    // maps have them, or with rows of 34; float32: column c of row r at c ^ r.
+    static constexpr bool STAGED = PAIR && BN >= 128;
+    static constexpr int ROOM = !STAGED ? 0 : P > 1 ? 4096 : MODE == G_FWD ? 2560 : 8192;
+    static constexpr int FIT = (227 * 1024 - 1024 - 512 - EWARPS * ROOM) / STAGE,
+                         STAGES = FIT > 8 ? 8 : FIT;
+    static_assert(STAGES >= 2 * P, "shared memory");
+    static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + EWARPS * ROOM + 512;
+    static_assert(SMEM > 114 * 1024 && SMEM <= 227 * 1024, "one block a SM");
     static constexpr int COLS = 2 * BN;                  // tensor memory
     static constexpr int NL = BN / 2;                    // columns of a thread
     static constexpr int CH = PAIR ? (BN / 4 < 32 ? BN / 4 : 32) : 32;
@@ -137,6 +144,21 @@ __device__ __forceinline__ void take(const T *p, float (&v)[CH], int left, bool 
     }
 }
 
+// A lane's row of 32 bfloat16 of a tile as a tensor map with the 64-byte swizzle has it.
+__device__ __forceinline__ unsigned char *row_part(unsigned char *tile, int lane, int c) {
+    return tile + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16);
+}
+__device__ __forceinline__ void put_row(unsigned char *tile, int lane, const float *v) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        Vec<bf16, 8>::store(reinterpret_cast<bf16 *>(row_part(tile, lane, c)), v + 8 * c);
+}
+__device__ __forceinline__ void get_row(unsigned char *tile, int lane, float *v) {
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        Vec<bf16, 8>::load(reinterpret_cast<const bf16 *>(row_part(tile, lane, c)), v + 8 * c);
+}
+
 // P parts of eight numbers, `plane` elements apart.
 template <int P>
 __device__ __forceinline__ void put_parts(bf16 *p, int64_t plane, const float *v) {
@@ -186,10 +208,11 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
     extern __shared__ unsigned char smem_raw[];
     unsigned char *base = reinterpret_cast<unsigned char *>(
         (reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
-    uint64_t *full = reinterpret_cast<uint64_t *>(base + size_t(STAGES) * C::STAGE);
+    unsigned char *rooms = base + size_t(STAGES) * C::STAGE;
+    uint64_t *full = reinterpret_cast<uint64_t *>(rooms + C::EWARPS * C::ROOM);
     uint64_t *empty = full + STAGES, *accfull = empty + STAGES, *accempty = accfull + 2;
-    uint64_t *done = accempty + 2;
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(done + 1);
+    uint64_t *done = accempty + 2, *dybar = done + 1;  // dybar: [warp][chunk]
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dybar + 2 * C::EWARPS);
     volatile int *stop = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
@@ -199,6 +222,7 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
         for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
         for (int s = 0; s < 2; ++s) mbar_init(&accfull[s], 1), mbar_init(&accempty[s], C::EWARPS);
         mbar_init(done, 1);
+        for (int s = 0; s < 2 * C::EWARPS; ++s) mbar_init(&dybar[s], 1);
         *stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -239,43 +263,41 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
             for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
                 const Item it(a, i, tiles);
                 const int dw_mt = a.mt / 2;  // DW: tiles of dWg, then of dWu
-                for (int k = it.k0; k < it.k1; ++k) {
-                    if (!(ok = await(&empty[s], phase))) break;
-                    unsigned char *A = base + size_t(s) * C::STAGE, *B = A + P * C::A_BYTES;
-                    uint64_t *bar = &full[s];
-                    mbar_arrive_expect_tx(bar, C::STAGE);
+                for (int k = it.k0; ok && k < it.k1; ++k)
 #pragma unroll
-                    for (int p = 0; p < P; ++p) {
-                        unsigned char *Ap = A + p * C::A_BYTES, *Bp = B + p * C::B_BYTES;
+                    for (int p = P - 1; p >= 0; --p) {
+                        if (!(ok = await(&empty[s], phase))) break;
+                        unsigned char *A = base + size_t(s) * C::STAGE, *B = A + C::A_BYTES;
+                        uint64_t *bar = &full[s];
+                        mbar_arrive_expect_tx(bar, C::STAGE);
                         if (C::PAIR) {
-                            tma_load_3d(Ap, &maps.a0, k * BK, it.m * BM, p, bar);
-                            tma_load_3d(Bp, &maps.b0, k * BK, it.n * (BN / 2), p, bar);
-                            tma_load_3d(Bp + C::B_BYTES / 2, &maps.b1, k * BK, it.n * (BN / 2), p,
+                            tma_load_3d(A, &maps.a0, k * BK, it.m * BM, p, bar);
+                            tma_load_3d(B, &maps.b0, k * BK, it.n * (BN / 2), p, bar);
+                            tma_load_3d(B + C::B_BYTES / 2, &maps.b1, k * BK, it.n * (BN / 2), p,
                                         bar);
                         } else if (MODE == G_DX) {
                             const bool up = k >= a.kb0;
                             const int f = (up ? k - a.kb0 : k) * BK;
-                            tma_load_3d(Ap, up ? &maps.a1 : &maps.a0, f, it.m * BM, p, bar);
+                            tma_load_3d(A, up ? &maps.a1 : &maps.a0, f, it.m * BM, p, bar);
 #pragma unroll
                             for (int j = 0; j < BN / 64; ++j)
-                                tma_load_3d(Bp + j * PANEL, up ? &maps.b1 : &maps.b0,
+                                tma_load_3d(B + j * PANEL, up ? &maps.b1 : &maps.b0,
                                             it.n * BN + 64 * j, f, p, bar);
                         } else {
                             const bool up = it.m >= dw_mt;
                             const int f = (up ? it.m - dw_mt : it.m) * BM;
 #pragma unroll
                             for (int j = 0; j < BM / 64; ++j)
-                                tma_load_3d(Ap + j * PANEL, up ? &maps.a1 : &maps.a0, f + 64 * j,
+                                tma_load_3d(A + j * PANEL, up ? &maps.a1 : &maps.a0, f + 64 * j,
                                             k * BK, p, bar);
 #pragma unroll
                             for (int j = 0; j < BN / 64; ++j)
-                                tma_load_3d(Bp + j * PANEL, &maps.b0, it.n * BN + 64 * j, k * BK, p,
+                                tma_load_3d(B + j * PANEL, &maps.b0, it.n * BN + 64 * j, k * BK, p,
                                             bar);
                         }
+                        ++issued;
+                        if (++s == STAGES) s = 0, phase ^= 1;
                     }
-                    ++issued;
-                    if (++s == STAGES) s = 0, phase ^= 1;
-                }
             }
             // nothing is in flight when the block ends
             for (int64_t k = issued > STAGES ? issued - STAGES : 0; k < issued; ++k)
@@ -288,39 +310,45 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
             constexpr uint32_t id = mma_idesc(BN, BR, AR);
             constexpr uint32_t da = AR ? 16 * 128 / 16 : 2, db = BR ? 16 * 128 / 16 : 2;
             const uint32_t a0 = smem_operand(smem_u32(base), AR ? PANEL : 16);
-            const uint32_t b0 =
-                smem_operand(smem_u32(base) + P * C::A_BYTES, BR ? PANEL : 16);
+            const uint32_t b0 = smem_operand(smem_u32(base) + C::A_BYTES, BR ? PANEL : 16);
             int s = 0, buf = 0;
             unsigned phase = 0, aphase = 1;
             bool ok = true;
             for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
                 const Item it(a, i, tiles);
                 for (int k = it.k0; k < it.k1; ++k) {
-                    if ((P > 1 || k == it.k0) && !(ok = await(&accempty[buf], aphase))) break;
-                    if (!(ok = await(&full[s], phase))) break;
+                    // (float32: an accumulator for every 64 of the depth)
+                    const bool first = P > 1 || k == it.k0;
+                    if (first && !(ok = await(&accempty[buf], aphase))) break;
+                    int at[P];  // the stages of the parts, which come in falling order
+#pragma unroll
+                    for (int p = P - 1; p >= 0; --p) {
+                        ok = ok && await(&full[s], phase);
+                        at[p] = s;
+                        if (++s == STAGES) s = 0, phase ^= 1;
+                    }
+                    if (!ok) break;
                     tc_fence_after();
                     const uint32_t d = tmem + buf * BN;
-                    const uint32_t as = a0 + s * (C::STAGE / 16), bs = b0 + s * (C::STAGE / 16);
-                    if (P == 1) {
+                    // a stage is free after the last product that takes its part
+#pragma unroll
+                    for (int q = 0; q < (P == 1 ? 1 : 6); ++q) {
+                        const int pa = P == 1 ? 0 : PART_A[q], pb = P == 1 ? 0 : PART_B[q];
+                        const uint32_t as = a0 + at[pa] * (C::STAGE / 16),
+                                       bs = b0 + at[pb] * (C::STAGE / 16);
 #pragma unroll
                         for (int j = 0; j < BK / 16; ++j)
-                            mma_ss<SMEM_128B>(d, as + j * da, bs + j * db, id, k > it.k0 || j > 0);
-                    } else {
-#pragma unroll
-                        for (int q = 0; q < 6; ++q)
-#pragma unroll
-                            for (int j = 0; j < BK / 16; ++j)
-                                mma_ss<SMEM_128B>(d, as + PART_A[q] * (C::A_BYTES / 16) + j * da,
-                                                  bs + PART_B[q] * (C::B_BYTES / 16) + j * db, id,
-                                                  q > 0 || j > 0);
+                            mma_ss<SMEM_128B>(d, as + j * da, bs + j * db, id,
+                                              !first || q > 0 || j > 0);
+                        if (P == 1 || q == 5) mma_commit(&empty[at[0]]);
+                        if (P > 1 && q == 4) mma_commit(&empty[at[P > 1 ? 1 : 0]]);
+                        if (P > 1 && q == 1) mma_commit(&empty[at[P > 1 ? 2 : 0]]);
                     }
-                    mma_commit(&empty[s]);
                     if (P > 1 || k + 1 == it.k1) {
                         mma_commit(&accfull[buf]);
                         buf ^= 1;
                         if (buf == 0) aphase ^= 1;
                     }
-                    if (++s == STAGES) s = 0, phase ^= 1;
                 }
             }
             mma_commit(done);
@@ -341,10 +369,65 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
             buf ^= 1;
             if (buf == 0) phase ^= 1;
         };
+        // the warp's room, and what goes through it
+        unsigned char *room = rooms + (warp - 4) * C::ROOM;
+        unsigned char *dyroom = room + (P == 1 && MODE == G_GRAD ? 4096 : 0);
+        const bool leader = elect_one();
+        unsigned dyphase = 0;
+        int64_t dyissued[2] = {-1, -1};  // the last item whose chunk is under way or there
+        // a column of a row of unaligned arrays
+        auto place = [](int r, int c) { return P > 1 ? r * 32 + (c ^ r) : r * 34 + c; };
+        constexpr int W = P > 1 ? 1 : 2;
+        auto dy_ahead = [&](int64_t i, int j) {
+            if (i >= items) return;
+            const Item it(a, i, tiles);
+            uint64_t *bar = &dybar[2 * (warp - 4) + j];
+            mbar_arrive_expect_tx(bar, 2048);
+            tma_load_3d(dyroom + j * 2048, &maps.dy, it.n * (BN / 2) + C::column(half, j),
+                        it.m * BM + quad * 32, 0, bar);
+            dyissued[j] = i;
+        };
+        auto rows_in = [&](T *to, const T *from, int64_t r0, int c0) {
+            T v[32];  // (all loads before the first store)
+            from += r0 * a.N + c0 + lane;
+            const int rows = c0 + lane < a.N ? int(min(a.M - r0, int64_t(32))) : 0;
+#pragma unroll
+            for (int r = 0; r < 32; ++r, from += a.N) v[r] = r < rows ? *from : T(0.0f);
+#pragma unroll
+            for (int r = 0; r < 32; ++r) to[place(r, lane)] = v[r];
+        };
+        auto rows_out = [&](T *to, const T *from, int64_t r0, int c0) {
+            T v[32];
+#pragma unroll
+            for (int r = 0; r < 32; ++r) v[r] = from[place(r, lane)];
+            to += r0 * a.N + c0 + lane;
+            const int rows = c0 + lane < a.N ? int(min(a.M - r0, int64_t(32))) : 0;
+#pragma unroll
+            for (int r = 0; r < 32; ++r, to += a.N)
+                if (r < rows) *to = v[r];
+        };
+        auto own_row = [&](const T *p, float *v) {
+#pragma unroll
+            for (int c = 0; c < 32; c += W) Vec<T, W>::load(p + place(lane, c), v + c);
+        };
+        auto set_row = [&](T *p, const float *v) {
+#pragma unroll
+            for (int c = 0; c < 32; c += W) Vec<T, W>::store(p + place(lane, c), v + c);
+        };
+        constexpr bool AHEAD = MODE == G_GRAD && C::STAGED && P == 1;
+        if (AHEAD && a.dvec && leader)
+            for (int j = 0; j < C::NL / 2 / CH; ++j) dy_ahead(blockIdx.x, j);
         for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
             const Item it(a, i, tiles);
             float sum[P == 1 ? 1 : C::NL];
             if (P > 1) {
+                if (MODE == G_GRAD && C::STAGED) {  // (under the products)
+                    if (leader) bulk_wait_read_all();
+                    __syncwarp();
+                    rows_in(reinterpret_cast<T *>(dyroom), static_cast<const T *>(a.dy),
+                            int64_t(it.m) * BM + quad * 32,
+                            it.n * (BN / 2) + C::column(half, 0));
+                }
 #pragma unroll
                 for (int c = 0; c < (P == 1 ? 1 : C::NL); ++c) sum[c] = 0.0f;
                 for (int k = it.k0; k < it.k1; ++k) {
@@ -372,15 +455,32 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
             };
             if constexpr (C::PAIR) {
                 constexpr int n = C::NL / 2 / CH;
-                const int64_t row = int64_t(it.m) * BM + quad * 32 + lane;
-                const bool in = row < a.M;
+                static_assert(P == 1 || n == 1, "one chunk of dy");
+                const int64_t row0 = int64_t(it.m) * BM + quad * 32, row = row0 + lane;
 #pragma unroll
                 for (int j = 0; j < n; ++j) {
                     const int c0 = it.n * (BN / 2) + C::column(half, j);
-                    const int left = in ? a.N - c0 : 0;
+                    const int left = row < a.M ? a.N - c0 : 0;
+                    const bool live = row0 < a.M && c0 < a.N;  // the warp has something to write
                     float dy[MODE == G_GRAD ? CH : 1];
-                    if constexpr (MODE == G_GRAD)
-                        take<T, CH>(static_cast<const T *>(a.dy) + row * a.N + c0, dy, left, a.dvec);
+                    if constexpr (MODE == G_GRAD) {
+                        const T *src = static_cast<const T *>(a.dy);
+                        if (!C::STAGED) {
+                            take<T, CH>(src + row * a.N + c0, dy, left, a.dvec);
+                        } else if (P == 1 && a.dvec) {
+                            if (!(ok = __all_sync(0xffffffffu,
+                                                  await(&dybar[2 * (warp - 4) + j], dyphase))))
+                                break;
+                            get_row(dyroom + j * 2048, lane, dy);
+                            __syncwarp();
+                            if (leader) dy_ahead(i + gridDim.x, j);
+                        } else {
+                            if (P == 1) rows_in(reinterpret_cast<T *>(dyroom), src, row0, c0);
+                            __syncwarp();
+                            own_row(reinterpret_cast<const T *>(dyroom), dy);
+                            __syncwarp();
+                        }
+                    }
                     if (P == 1 && j == 0) {
                         if (!(ok = wait())) break;
                         tc_fence_after();
@@ -407,7 +507,25 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                             for (int c = 0; c < CH; ++c)
                                 g[c] = act_value<act.value, P == 1>(g[c]) * u[c];
                         });
-                        put<T, CH>(static_cast<T *>(a.out) + row * a.N + c0, g, left, a.vec);
+                        T *out = static_cast<T *>(a.out);
+                        if (!C::STAGED) {
+                            put<T, CH>(out + row * a.N + c0, g, left, a.vec);
+                        } else if (P == 1 && a.vec) {
+                            if (leader) bulk_wait_read_all();  // the room is free
+                            __syncwarp();
+                            put_row(room, lane, g);
+                            fence_proxy_async_smem();
+                            __syncwarp();
+                            if (leader && live) {
+                                tma_store_3d(&maps.o0, room, c0, int(row0), 0);
+                                bulk_commit();
+                            }
+                        } else {
+                            set_row(reinterpret_cast<T *>(room), g);
+                            __syncwarp();
+                            rows_out(out, reinterpret_cast<const T *>(room), row0, c0);
+                            __syncwarp();
+                        }
                     } else {
                         act_switch(a.act, [&](auto act) {
 #pragma unroll
@@ -424,17 +542,39 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                             float *o = a.bpart + (int64_t(it.m) * 4 + quad) * 2 * a.N + c0 + lane;
                             if (lane < CH && c0 + lane < a.N) o[0] = sg, o[a.N] = su;
                         }
-                        const int64_t plane = a.M * a.ld;
-                        bf16 *at = a.d + row * a.ld + c0;
+                        if constexpr (C::STAGED) {
 #pragma unroll
-                        for (int c = 0; c < CH; c += 8)
-                            if (c < left) {  // (the rows' padding takes zeros)
-                                put_parts<P>(at + c, plane, g + c);
-                                put_parts<P>(at + P * plane + c, plane, u + c);
+                            for (int part = 0; part < P; ++part) {
+                                if (leader) bulk_wait_read_all();
+                                __syncwarp();
+                                put_row(room, lane, g);
+                                put_row(room + 2048, lane, u);
+                                fence_proxy_async_smem();
+                                __syncwarp();
+                                if (leader && live) {
+                                    tma_store_3d(&maps.o0, room, c0, int(row0), part);
+                                    tma_store_3d(&maps.o1, room + 2048, c0, int(row0), part);
+                                    bulk_commit();
+                                }
+                                if (part + 1 < P)
+#pragma unroll
+                                    for (int c = 0; c < CH; ++c)
+                                        g[c] = rest<bf16>(g[c]), u[c] = rest<bf16>(u[c]);
                             }
+                        } else {
+                            const int64_t plane = a.M * a.ld;
+                            bf16 *at = a.d + row * a.ld + c0;
+#pragma unroll
+                            for (int c = 0; c < CH; c += 8)
+                                if (c < left) {  // (the rows' padding takes zeros)
+                                    put_parts<P>(at + c, plane, g + c);
+                                    put_parts<P>(at + P * plane + c, plane, u + c);
+                                }
+                        }
                     }
                 }
                 if (!ok) break;
+                dyphase ^= 1;
             } else {
                 constexpr int n = C::NL / CH;
                 const int dw_mt = a.mt / 2;
@@ -463,6 +603,14 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                 }
             }
         }
+        // nothing is in flight when the block ends
+        if (leader) bulk_wait_read_all();
+        if (AHEAD && !ok && leader)
+            for (int j = 0; j < 2; ++j)
+                if (dyissued[j] >= 0)
+                    mbar_wait_bounded(&dybar[2 * (warp - 4) + j],
+                                      unsigned((dyissued[j] - blockIdx.x) / gridDim.x) & 1,
+                                      a.timeout_ns);
     }
     __syncwarp();
     tc_fence_before();
@@ -559,17 +707,24 @@ struct Operand {
     int cols = 0, ld = 0, parts = 1;
 };
 
-// Boxes of 64 columns by `box` rows of one part.
-bool make_map3(CUtensorMap *map, const Operand &o, int box) {
+// Boxes of `columns` (64, or 32) columns by `box` rows of one part.
+bool make_map3(CUtensorMap *map, const Operand &o, int box, int columns = 64) {
     const EncodeFn fn = encode_fn();
     if (fn == nullptr) return false;
     const cuuint64_t dims[3] = {cuuint64_t(o.cols), cuuint64_t(o.rows), cuuint64_t(o.parts)};
     const cuuint64_t strides[2] = {cuuint64_t(o.ld) * 2, cuuint64_t(o.rows) * o.ld * 2};
-    const cuuint32_t b[3] = {64, cuuint32_t(box), 1}, ones[3] = {1, 1, 1};
+    const cuuint32_t b[3] = {cuuint32_t(columns), cuuint32_t(box), 1}, ones[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16 *>(o.p), dims, strides, b,
-              ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+              ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              columns == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// The same of a result or its gradient in bfloat16, 32 x 32.
+bool make_tile_map(CUtensorMap *map, const void *p, int64_t rows, int cols, int ld) {
+    Operand o;
+    o.p = static_cast<const bf16 *>(p), o.rows = rows, o.cols = cols, o.ld = ld;
+    return make_map3(map, o, 32, 32);
 }
 
 // Scratch handed out in pieces: sizes first, then addresses.
@@ -583,24 +738,29 @@ struct Scratch {
     }
 };
 
-// The columns of a tile and the parts of the contraction: the smallest estimate
-// in SM cycles.  A stage of a tile costs its products (limited by the reads of shared
-// memory: 128 bytes a cycle) or a wave's epilogue, whichever is longer; parts cost
-// their writes and reads and a launch.
+// The columns of a tile and the parts of the contraction: the smallest estimate in SM
+// cycles.  Measured per 64 of the depth: 708 cycles with 256 columns, 385 with 128, 277
+// with 64 (32,768 x 8192 x 1024, all SMs; the products alone would be 512, 256 and 192:
+// operand reads and the copies share the memory's 128 bytes a cycle), float32 six times
+// 430 with 128; a tile's epilogue, under the next tile's products, 1500 + 14 a column
+// forward, 600 + 30 for the gradients, 500 + 8 for plain results.  Parts cost their
+// writes and reads and a launch.
 struct GemmPlan {
     int BN = 0, nsplit = 1;
 };
-GemmPlan plan_gemm(int sms, bool pair, int P, int64_t M, int64_t N, int64_t mtiles, int64_t kb,
-                   bool may_split) {
+GemmPlan plan_gemm(int sms, int mode, int P, int64_t M, int64_t N, int64_t mtiles, int64_t kb) {
     GemmPlan best;
     double least = 1e300;
+    const bool pair = mode == G_FWD || mode == G_GRAD;
     for (int BN = P == 1 ? 256 : 128; BN >= 64; BN /= 2) {
         const int64_t tiles = mtiles * ceil_div(N, pair ? BN / 2 : BN);
-        const double stage = (P == 1 ? 1 : 6) * 4.0 *
-                             (BN / 2 > (BM + BN) / 4 ? BN / 2 : (BM + BN) / 4);
-        const double epilogue = pair ? 14.0 * BN : 6.0 * BN;
-        const int64_t first = may_split && P == 1 ? ceil_div(kb * BK, CHAIN) : 1;
-        const int64_t most = may_split ? (kb < 64 ? kb : 64) : 1;
+        const double stage = (P == 1 ? 1.0 : 6.7) * (BN == 256 ? 708 : BN == 128 ? 385 : 277);
+        const double epilogue = mode == G_FWD    ? 1500 + 14.0 * BN
+                                : mode == G_GRAD ? 600 + 30.0 * BN
+                                                 : 500 + 8.0 * BN;
+        // (a part has a row of a chain's length at most in bfloat16)
+        const int64_t first = !pair && P == 1 ? ceil_div(kb * BK, CHAIN) : 1;
+        const int64_t most = pair ? 1 : kb < 64 ? kb : 64;
         for (int64_t ns = first; ns <= (most > first ? most : first); ++ns) {
             const double k = double(ceil_div(kb, ns));
             const double item = k * stage > epilogue ? k * stage : epilogue;
@@ -698,75 +858,114 @@ GemmArgs gemm_args(const DeviceInfo &dev, const GatedArgs &a) {
     return g;
 }
 
+// What a backward call keeps in scratch.
+struct BackwardPlan {
+    Scratch s;
+    Inputs in;
+    int ld = 0, mt = 0, ft = 0, kf = 0, kr = 0;
+    GemmPlan px, pw;
+    size_t d_at = 0, part_x = 0, part_w = 0, part_b = 0;
+};
+template <class T, int P>
+BackwardPlan plan_backward(const DeviceInfo &dev, const GatedArgs &a) {
+    BackwardPlan b;
+    plan_inputs<T, P>(a, b.in, b.s);
+    b.ld = pad8(a.F);
+    b.d_at = b.s.take(size_t(2) * P * a.rows * b.ld * sizeof(bf16));
+    b.mt = int(ceil_div(a.rows, BM)), b.ft = int(ceil_div(a.F, BM));
+    b.kf = int(ceil_div(a.F, BK)), b.kr = int(ceil_div(a.rows, BK));
+    if (a.dx) {
+        b.px = plan_gemm(dev.sm_count, G_DX, P, a.rows, a.C, b.mt, 2 * b.kf);
+        if (b.px.nsplit > 1)
+            b.part_x = b.s.take(size_t(b.px.nsplit) * a.rows * a.C * sizeof(float));
+    }
+    if (a.dwg) {
+        b.pw = plan_gemm(dev.sm_count, G_DW, P, 2 * a.F, a.C, 2 * b.ft, b.kr);
+        if (b.pw.nsplit > 1)
+            b.part_w = b.s.take(size_t(b.pw.nsplit) * 2 * a.F * a.C * sizeof(float));
+    }
+    if (a.dbg) b.part_b = b.s.take(size_t(b.mt) * 4 * 2 * a.F * sizeof(float));
+    return b;
+}
+
+// The caller's workspace where it is large enough, else the library's pool.
+struct Memory {
+    cudaStream_t st;
+    void *own = nullptr;
+    cudaError_t take(const DeviceInfo &dev, Scratch &s, const GatedArgs &a) {
+        if (s.bytes == 0) return cudaSuccess;
+        if (a.workspace != nullptr && a.workspace_bytes >= s.bytes) {
+            s.base = static_cast<char *>(a.workspace);
+            return cudaSuccess;
+        }
+        const cudaError_t e = scratch_alloc(dev, &own, s.bytes, st);
+        s.base = static_cast<char *>(own);
+        return e;
+    }
+    cudaError_t give(cudaError_t e) {
+        if (own == nullptr) return e;
+        const cudaError_t f = scratch_free(own, st);
+        return e == cudaSuccess ? f : e;
+    }
+};
+
 template <class T, int P>
 cudaError_t forward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st) {
     Scratch s;
     Inputs in;
     plan_inputs<T, P>(a, in, s);
-    cudaError_t e = cudaSuccess;
-    if (s.bytes && (e = scratch_alloc(dev, reinterpret_cast<void **>(&s.base), s.bytes, st)) !=
-                       cudaSuccess)
-        return e;
+    Memory memory{st};
+    cudaError_t e = memory.take(dev, s, a);
+    if (e != cudaSuccess) return e;
     e = pack_inputs<T, P>(a, in, s, st);
     if (e == cudaSuccess) {
         GemmArgs g = gemm_args(dev, a);
         g.M = a.rows, g.N = a.F, g.kb = int(ceil_div(a.C, BK)), g.kb0 = g.kb;
         g.mt = int(ceil_div(a.rows, BM));
-        const GemmPlan p = plan_gemm(dev.sm_count, true, P, g.M, g.N, g.mt, g.kb, false);
+        const GemmPlan p = plan_gemm(dev.sm_count, G_FWD, P, g.M, g.N, g.mt, g.kb);
         g.nt = int(ceil_div(a.F, p.BN / 2));
         g.out = a.y, g.vec = a.F % (16 / sizeof(T)) == 0 && aligned16(a.y);
         GemmMaps m{};
         const bool ok = make_map3(&m.a0, in.x, BM) && make_map3(&m.b0, in.wg, p.BN / 2) &&
-                        make_map3(&m.b1, in.wu, p.BN / 2);
+                        make_map3(&m.b1, in.wu, p.BN / 2) &&
+                        (P > 1 || !g.vec || make_tile_map(&m.o0, a.y, a.rows, a.F, a.F));
         e = ok ? run_gemm<G_FWD, P>(dev, m, g, p.BN, st) : cudaErrorInvalidValue;
     }
-    if (s.base) {
-        const cudaError_t f = scratch_free(s.base, st);
-        if (e == cudaSuccess) e = f;
-    }
-    return e;
+    return memory.give(e);
 }
 
 template <class T, int P>
 cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st) {
-    Scratch s;
-    Inputs in;
-    plan_inputs<T, P>(a, in, s);
-    const int ld = pad8(a.F);
-    const size_t d_at = s.take(size_t(2) * P * a.rows * ld * sizeof(bf16));
-    const int mt = int(ceil_div(a.rows, BM)), ft = int(ceil_div(a.F, BM));
-    const int kf = int(ceil_div(a.F, BK)), kr = int(ceil_div(a.rows, BK));
-    GemmPlan px, pw;
-    size_t part_x = 0, part_w = 0, part_b = 0;
-    if (a.dx) {
-        px = plan_gemm(dev.sm_count, false, P, a.rows, a.C, mt, 2 * kf, true);
-        if (px.nsplit > 1) part_x = s.take(size_t(px.nsplit) * a.rows * a.C * sizeof(float));
-    }
-    if (a.dwg) {
-        pw = plan_gemm(dev.sm_count, false, P, 2 * a.F, a.C, 2 * ft, kr, true);
-        if (pw.nsplit > 1) part_w = s.take(size_t(pw.nsplit) * 2 * a.F * a.C * sizeof(float));
-    }
-    if (a.dbg) part_b = s.take(size_t(mt) * 4 * 2 * a.F * sizeof(float));
-    cudaError_t e = scratch_alloc(dev, reinterpret_cast<void **>(&s.base), s.bytes, st);
+    BackwardPlan b = plan_backward<T, P>(dev, a);
+    Scratch &s = b.s;
+    Inputs &in = b.in;
+    const int ld = b.ld, mt = b.mt, ft = b.ft, kf = b.kf, kr = b.kr;
+    const GemmPlan px = b.px, pw = b.pw;
+    const size_t part_x = b.part_x, part_w = b.part_w, part_b = b.part_b;
+    Memory memory{st};
+    cudaError_t e = memory.take(dev, s, a);
     if (e != cudaSuccess) return e;
     e = pack_inputs<T, P>(a, in, s, st);
     Operand d[2];
     for (int i = 0; i < 2; ++i) {
-        d[i].p = reinterpret_cast<const bf16 *>(s.base + d_at) + int64_t(i) * P * a.rows * ld;
+        d[i].p = reinterpret_cast<const bf16 *>(s.base + b.d_at) + int64_t(i) * P * a.rows * ld;
         d[i].rows = a.rows, d[i].cols = a.F, d[i].ld = ld, d[i].parts = P;
     }
     auto partials = [&](size_t at) { return reinterpret_cast<float *>(s.base + at); };
     if (e == cudaSuccess) {
         GemmArgs g = gemm_args(dev, a);
         g.M = a.rows, g.N = a.F, g.kb = int(ceil_div(a.C, BK)), g.kb0 = g.kb, g.mt = mt;
-        const GemmPlan p = plan_gemm(dev.sm_count, true, P, g.M, g.N, g.mt, g.kb, false);
+        const GemmPlan p = plan_gemm(dev.sm_count, G_GRAD, P, g.M, g.N, g.mt, g.kb);
         g.nt = int(ceil_div(a.F, p.BN / 2));
         g.d = const_cast<bf16 *>(d[0].p), g.ld = ld;
         g.dvec = a.F % (16 / sizeof(T)) == 0 && aligned16(a.dy);
         if (a.dbg) g.bpart = partials(part_b);
         GemmMaps m{};
-        const bool ok = make_map3(&m.a0, in.x, BM) && make_map3(&m.b0, in.wg, p.BN / 2) &&
-                        make_map3(&m.b1, in.wu, p.BN / 2);
+        const bool ok = make_map3(&m.a0, in.x, BM) &&
+                        make_map3(&m.b0, in.wg, p.BN / 2) &&
+                        make_map3(&m.b1, in.wu, p.BN / 2) &&
+                        make_map3(&m.o0, d[0], 32, 32) && make_map3(&m.o1, d[1], 32, 32) &&
+                        (P > 1 || !g.dvec || make_tile_map(&m.dy, a.dy, a.rows, a.F, a.F));
         e = ok ? run_gemm<G_GRAD, P>(dev, m, g, p.BN, st) : cudaErrorInvalidValue;
     }
     if (e == cudaSuccess && a.dx) {
@@ -776,7 +975,8 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
         g.out = a.dx, g.vec = a.C % (16 / sizeof(T)) == 0 && aligned16(a.dx);
         g.part = partials(part_x);
         GemmMaps m{};
-        const bool ok = make_map3(&m.a0, d[0], BM) && make_map3(&m.a1, d[1], BM) &&
+        const bool ok = make_map3(&m.a0, d[0], BM) &&
+                        make_map3(&m.a1, d[1], BM) &&
                         make_map3(&m.b0, in.wg, 64) && make_map3(&m.b1, in.wu, 64);
         e = ok ? run_gemm<G_DX, P>(dev, m, g, px.BN, st) : cudaErrorInvalidValue;
         if (e == cudaSuccess && g.nsplit > 1)
@@ -802,12 +1002,23 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
             partials(part_b), 4 * mt, a.F, static_cast<T *>(a.dbg), static_cast<T *>(a.dbu));
         e = cudaGetLastError();
     }
-    const cudaError_t f = scratch_free(s.base, st);
-    return e == cudaSuccess ? f : e;
+    return memory.give(e);
 }
 
 }  // namespace
 
+size_t gated_tc_scratch(const DeviceInfo &dev, const GatedArgs &a, int dtype, bool backward) {
+    if (backward)
+        return (dtype == PC_F32 ? plan_backward<float, 3>(dev, a) : plan_backward<bf16, 1>(dev, a))
+            .s.bytes;
+    Scratch s;
+    Inputs in;
+    if (dtype == PC_F32)
+        plan_inputs<float, 3>(a, in, s);
+    else
+        plan_inputs<bf16, 1>(a, in, s);
+    return s.bytes;
+}
 cudaError_t gated_tc_forward(const DeviceInfo &dev, const GatedArgs &a, int dtype,
                              cudaStream_t st) {
     return dtype == PC_F32 ? forward<float, 3>(dev, a, st) : forward<bf16, 1>(dev, a, st);

@@ -134,6 +134,19 @@ def _gated_args(x, w_gate, w_up, b_gate, b_up, activation):
                    _ptr_or_none(b_gate), _ptr_or_none(b_up), _activation(activation)), F
 
 
+PC_GATED_GRAD_X, PC_GATED_GRAD_WEIGHT, PC_GATED_GRAD_BIAS = 1, 2, 4
+
+
+def _workspace(x, rows: int, C: int, F: int, gradients: int, index: int):
+    """Scratch of a large call from torch's allocator, which keeps it (the library's
+    pool does for smaller ones)."""
+    if rows * (C + 2 * F) < 1 << 24:
+        return None, 0
+    with torch.cuda.device(index):
+        n = lib().pc_gated_linear_workspace_bytes(_DTYPES[x.dtype], rows, C, F, gradients)
+    return (torch.empty(n, dtype=torch.uint8, device=x.device), n) if n else (None, 0)
+
+
 def pc_gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
                     b_gate: torch.Tensor | None = None, b_up: torch.Tensor | None = None, *,
                     activation: str | None = "silu",
@@ -148,7 +161,9 @@ def pc_gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
         out = torch.empty(shape, dtype=x.dtype, device=x.device)
     else:
         _same(out, "out", shape, x.dtype, index)
-    _run("pc_gated_linear", lib().pc_gated_linear, index, *args, out.data_ptr())
+    work, n = _workspace(x, *args[2:5], 0, index)
+    _run("pc_gated_linear", lib().pc_gated_linear, index, *args, out.data_ptr(),
+         _ptr_or_none(work), n)
     return out
 
 
@@ -168,9 +183,12 @@ def pc_gated_linear_backward(grad_out: torch.Tensor, x: torch.Tensor, w_gate: to
         dwg, dwu = torch.empty_like(w_gate), torch.empty_like(w_up)
     if need_bias and b_gate is not None:
         dbg, dbu = torch.empty_like(b_gate), torch.empty_like(b_up)
+    which = (PC_GATED_GRAD_X if need_x else 0) | (PC_GATED_GRAD_WEIGHT if need_weight else 0) \
+        | (PC_GATED_GRAD_BIAS if dbg is not None else 0)
+    work, n = _workspace(x, *args[2:5], which, index) if which else (None, 0)
     _run("pc_gated_linear_backward", lib().pc_gated_linear_backward, index,
          grad_out.data_ptr(), *args, _ptr_or_none(dx), _ptr_or_none(dwg), _ptr_or_none(dwu),
-         _ptr_or_none(dbg), _ptr_or_none(dbu))
+         _ptr_or_none(dbg), _ptr_or_none(dbu), _ptr_or_none(work), n)
     return dx, dwg, dwu, dbg, dbu
 
 

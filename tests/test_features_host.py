@@ -50,7 +50,8 @@ def test_group_norm_validation(L):
 
 def test_gated_linear_validation(L):
     def call(dtype=0, rows=4, C=8, F=8, bg=None, bu=None, act=1):
-        return L.pc_gated_linear(FAKE, dtype, rows, C, F, FAKE, FAKE, bg, bu, act, FAKE, None)
+        return L.pc_gated_linear(FAKE, dtype, rows, C, F, FAKE, FAKE, bg, bu, act, FAKE, None, 0,
+                                 None)
     assert call(dtype=3) == 1
     assert call(rows=-1) == 1 and call(F=-1) == 1 and call(C=0) == 1
     assert call(bg=FAKE) == 1 and "go together" in _msg(L)
@@ -60,7 +61,7 @@ def test_gated_linear_validation(L):
 
     def back(dwg=FAKE, dwu=FAKE, dbg=None, dbu=None, dx=FAKE, dtype=0):
         return L.pc_gated_linear_backward(FAKE, FAKE, dtype, 4, 8, 8, FAKE, FAKE, None, None, 1,
-                                          dx, dwg, dwu, dbg, dbu, None)
+                                          dx, dwg, dwu, dbg, dbu, None, 0, None)
     assert back(dwu=None) == 1 and back(dbg=FAKE) == 1 and back(dtype=-1) == 1
     assert back(dwg=None, dwu=None, dx=None) == 0
 
@@ -84,8 +85,9 @@ def test_embedding_validation(L):
 @pytest.mark.skipif(torch.cuda.is_available(), reason="checks the no-GPU path")
 def test_feature_operators_report_no_device(L):
     assert gn(L) == binding.PC_ERR_NO_DEVICE
-    assert L.pc_gated_linear(FAKE, 0, 4, 8, 8, FAKE, FAKE, None, None, 1, FAKE,
+    assert L.pc_gated_linear(FAKE, 0, 4, 8, 8, FAKE, FAKE, None, None, 1, FAKE, None, 0,
                              None) == binding.PC_ERR_NO_DEVICE
+    assert L.pc_gated_linear_workspace_bytes(0, 4, 8, 8, 7) == 0
     assert L.pc_embedding(FAKE, 0, 1, 5, 8, FAKE, 3, 1.0, FAKE, None) == binding.PC_ERR_NO_DEVICE
     assert L.pc_embedding_backward(FAKE, 0, 1, 5, 8, FAKE, 3, 1.0, FAKE,
                                    None) == binding.PC_ERR_NO_DEVICE

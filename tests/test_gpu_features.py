@@ -219,6 +219,38 @@ def test_gated_linear_gradients_of_some(dtype):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+def test_gated_linear_in_a_caller_s_workspace(dtype):
+    """The C ABI with and without a workspace, and the sizes it asks for."""
+    from point_cloud_neighbor_gb300.binding import lib
+    L = lib()
+    for shape in ((300, 128, 200), (70, 33, 41)):
+        ins = x, wg, wu, bg, bu, dy = gated_inputs(gen(8), *shape, dtype)
+        want = gated_all(*ins, "silu")
+        code = 0 if dtype is torch.float32 else 1
+        outs = {k: torch.full_like(v, math.nan) for k, v in want.items()}
+        n = L.pc_gated_linear_workspace_bytes(code, *shape, 7)
+        assert n > 4 * shape[0] * shape[2]
+        work = torch.empty(n + 256, dtype=torch.uint8, device=DEV)
+        work[n:] = 77
+        s = torch.cuda.current_stream().cuda_stream
+        args = [x.data_ptr(), code, *shape, wg.data_ptr(), wu.data_ptr(), bg.data_ptr(),
+                bu.data_ptr(), 1]
+        m = L.pc_gated_linear_workspace_bytes(code, *shape, 0)
+        assert (m == 0) == (dtype is torch.bfloat16 and shape[1] % 8 == 0)
+        assert L.pc_gated_linear(*args, outs["y"].data_ptr(), work.data_ptr() if m else None, m,
+                                 s) == 0
+        grads = [outs[k].data_ptr() for k in ("dx", "dwg", "dwu", "dbg", "dbu")]
+        for bytes_ in (n, n - 1, 0):   # too small: the library's own
+            assert L.pc_gated_linear_backward(dy.data_ptr(), *args, *grads, work.data_ptr(),
+                                              bytes_, s) == 0
+            for k in want:
+                assert torch.equal(outs[k], want[k]), k
+                if k != "y":
+                    outs[k].fill_(math.nan)
+        assert (work[n:] == 77).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_gated_linear_empty(dtype):
     g = gen(1)
     x, wg, wu, bg, bu, dy = gated_inputs(g, 0, 24, 40, dtype)
