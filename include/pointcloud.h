@@ -710,10 +710,11 @@ int pc_group_norm_backward(const void *grad_out, const void *x, int dtype, int64
  * pc_embedding_backward writes grad_table [B, V, C] in full:
  *   grad_table[b, v, :] = scale * sum of grad_out[b, t, :] over idx[b, t] = v.
  * The tokens are sorted by their row and added in float32, those of a row in
- * the order of t (runs of 64 at a time where a row has more).
+ * the order of t, in runs that end at every 64th (in smaller calls 32nd or 16th) of the
+ * sorted tokens, and these in their order.
  *
  * B V and B T are below 2^31 - 2^20 in the backward call (PC_ERR_UNSUPPORTED
- * above); scratch there: 24 bytes a token, and 4 C bytes for every 64 tokens.
+ * above); scratch there: 18 bytes a token, and 8 C bytes for every run.
  */
 int pc_embedding(const void *table, int dtype, int64_t B, int64_t V, int64_t C,
                  const int64_t *idx, int64_t T, double scale, void *out, void *stream);

@@ -4,18 +4,18 @@
 //   out[b, t, :] = scale table[b, idx[b, t], :]
 //   grad_table[b, v, :] = scale sum of grad_out[b, t, :] over idx[b, t] = v
 //
-// Forward: a thread a vector of up to 16 bytes, four in flight.  Bound: memory,
-// the writes of the output.
+// Forward: a group of threads a token, three tokens in flight.  Bound: memory, the writes
+// of the output.
 //
 // Backward: the tokens are sorted by their row with a stable radix sort of 32-bit
-// keys (b V + idx; absent tokens last): per digit of at most 8 bits the blocks'
+// keys (b V + idx; absent tokens last): per digit of at most 9 bits the blocks'
 // histograms, their sums over the blocks before, and a scatter in which a warp
-// ranks 32 keys at a time by the lanes that hold the same digit.  Then every
-// row of the table finds its run of tokens by bisection and adds it up, in the
-// order of the tokens, and is written once, zeros among them.  Runs of more
-// than 64 tokens are added in chunks of 64 consecutive sorted tokens, and these in
-// chunks of 64 again, by kernels of their own before, so that one frequent row
-// is not one thread group's work.  Everything in float32 and in a fixed order.
+// ranks 32 keys at a time by the lanes that hold the same digit.  Then groups
+// of threads walk over chunks of 64 sorted tokens (fewer in small calls), write the rows
+// that begin and end there, and leave the sums of rows that reach over a chunk's border,
+// which are joined afterwards: a row's chunks in their order, of a row of more than 32
+// chunks in 32s summed by a kernel of their own.  So a frequent row is many groups' work.
+// Everything in float32 and in a fixed order.
 // Bound: memory, the gradient's rows read once in the order of the table's.
 #include "pc_device.cuh"
 #include "pc_internal.h"
@@ -28,83 +28,126 @@ namespace pcn {
 namespace {
 
 constexpr int EMB_THREADS = 256;
-constexpr int RUN = 64;  // tokens of a chunk, chunks of a second chunk
+constexpr int RUN2 = 32;  // chunks of a second sum
+
+// V elements as they are in memory.
+template <int BYTES>
+struct Raw;
+template <>
+struct Raw<16> {
+    using type = uint4;
+};
+template <>
+struct Raw<8> {
+    using type = uint2;
+};
+template <>
+struct Raw<4> {
+    using type = uint32_t;
+};
+template <>
+struct Raw<2> {
+    using type = uint16_t;
+};
+template <class T, int V>
+using RawV = typename Raw<V * int(sizeof(T))>::type;
+
+template <class T, int V>
+__device__ __forceinline__ void widen(const RawV<T, V> &r, float *v) {
+    Vec<T, V>::load(reinterpret_cast<const T *>(&r), v);
+}
 
 // --- forward ------------------------------------------------------------------
 
+// G threads a token, U tokens a thread at a time.
+constexpr int FORWARD_TOKENS = 3;
 template <class T, int V>
 __global__ void __launch_bounds__(EMB_THREADS)
-emb_forward_kernel(const T *__restrict__ table, int64_t rows, int C, const int64_t *__restrict__ idx,
-                   int64_t T_, int64_t tokens, float scale, T *__restrict__ out, int *status) {
-    constexpr int U = 4;
-    const int nv = C / V;
-    const int64_t total = tokens * nv, step = int64_t(gridDim.x) * EMB_THREADS;
-    for (int64_t i0 = int64_t(blockIdx.x) * EMB_THREADS + threadIdx.x; i0 < total;
-         i0 += U * step) {
-        float v[U][V];
+emb_forward_kernel(const T *__restrict__ table, int64_t rows, int C,
+                   const int64_t *__restrict__ idx, int64_t per_cloud, int64_t tokens, float scale,
+                   T *__restrict__ out, int G, int *status) {
+    constexpr int U = FORWARD_TOKENS;
+    using R = RawV<T, V>;
+    const int per = EMB_THREADS / G, g = threadIdx.x / G, l = threadIdx.x - g * G;
+    const int64_t t0 = int64_t(blockIdx.x) * (per * U) + g;
+    if (g >= per) return;
+    const T *from[U];  // nullptr: no row
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int64_t t = t0 + u * per;
+        from[u] = nullptr;
+        if (t >= tokens) continue;
+        const int64_t r = idx[t];
+        int64_t cloud = 0;
+        if (per_cloud < tokens)
+            cloud = tokens <= 0xffffffffll ? uint32_t(t) / uint32_t(per_cloud) : t / per_cloud;
+        if (r >= 0 && r < rows)
+            from[u] = table + (cloud * rows + r) * C;
+        else if (r != -1)
+            raise_status(status, PC_ERR_INVALID_ARGUMENT);
+    }
+    for (int c = l * V; c < C; c += G * V) {
+        R raw[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            raw[u] = from[u] ? *reinterpret_cast<const R *>(from[u] + c) : R{};
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const int64_t i = i0 + u * step;
+            const int64_t t = t0 + u * per;
+            if (t >= tokens) break;
+            float v[V];
+            widen<T, V>(raw[u], v);
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[u][e] = 0.0f;
-            if (i < total) {
-                const int64_t t = i / nv;
-                const int c = int(i - t * nv) * V;
-                const int64_t r = idx[t];
-                if (r >= 0 && r < rows)
-                    Vec<T, V>::load(table + (t / T_ * rows + r) * C + c, v[u]);
-                else if (r != -1)
-                    raise_status(status, PC_ERR_INVALID_ARGUMENT);
-            }
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int64_t i = i0 + u * step;
-            if (i < total) {
-#pragma unroll
-                for (int e = 0; e < V; ++e) v[u][e] *= scale;
-                Vec<T, V>::store(out + i * V, v[u]);
-            }
+            for (int e = 0; e < V; ++e) v[e] = from[u] ? v[e] * scale : 0.0f;
+            // (written past the caches: they keep the table)
+            R w;
+            Vec<T, V>::store(reinterpret_cast<T *>(&w), v);
+            __stcs(reinterpret_cast<R *>(out + t * C + c), w);
         }
     }
 }
 
 // --- the sort -------------------------------------------------------------------
 
-constexpr int ITEMS = 8, TILE = EMB_THREADS * ITEMS;
+constexpr int ITEMS = 4, TILE = EMB_THREADS * ITEMS;
+constexpr int DIGITS = 512;  // of a pass, at most
 
 struct SortArgs {
     const int64_t *idx;            // first pass: keys are formed from these
-    const uint32_t *keys, *vals;   // later passes
-    uint32_t *out_keys, *out_vals;
+    const uint2 *in;               // later passes: key, token
+    uint2 *out;
     uint32_t *count;               // [digits][blocks], then the sums over the blocks before
     uint32_t *total;               // [digits]
-    int64_t rows, per_cloud;       // V, T
+    int64_t rows;                  // V
+    uint32_t per_cloud;            // T
     uint32_t n, absent;            // tokens; the key of those without a row
     int blocks, shift, bits;
     int *status;
 };
 
 __device__ __forceinline__ uint32_t sort_key(const SortArgs &a, uint32_t i, bool report) {
-    if (a.idx == nullptr) return a.keys[i];
     const int64_t r = a.idx[i];
-    if (r >= 0 && r < a.rows) return uint32_t(i / a.per_cloud * a.rows + r);
+    if (r >= 0 && r < a.rows) return i / a.per_cloud * uint32_t(a.rows) + uint32_t(r);
     if (report && r != -1) raise_status(a.status, PC_ERR_INVALID_ARGUMENT);
     return a.absent;
 }
 
 __global__ void __launch_bounds__(EMB_THREADS) sort_count_kernel(SortArgs a) {
-    __shared__ uint32_t hist[256];
-    hist[threadIdx.x] = 0;
+    __shared__ uint32_t hist[DIGITS];
+    hist[threadIdx.x] = hist[threadIdx.x + EMB_THREADS] = 0;
     __syncthreads();
     const uint32_t mask = (1u << a.bits) - 1, i0 = blockIdx.x * uint32_t(TILE) + threadIdx.x;
 #pragma unroll
     for (int u = 0; u < ITEMS; ++u) {
         const uint32_t i = i0 + u * EMB_THREADS;
-        if (i < a.n) atomicAdd(&hist[(sort_key(a, i, true) >> a.shift) & mask], 1u);
+        if (i < a.n) {
+            const uint32_t key = a.idx ? sort_key(a, i, true) : a.in[i].x;
+            atomicAdd(&hist[(key >> a.shift) & mask], 1u);
+        }
     }
     __syncthreads();
-    if (threadIdx.x <= mask) a.count[size_t(threadIdx.x) * a.blocks + blockIdx.x] = hist[threadIdx.x];
+    for (uint32_t d = threadIdx.x; d <= mask; d += EMB_THREADS)
+        a.count[size_t(d) * a.blocks + blockIdx.x] = hist[d];
 }
 
 // A warp a digit: the sums over the blocks before, in place, and the total.
@@ -128,105 +171,168 @@ __global__ void __launch_bounds__(EMB_THREADS) sort_scan_kernel(SortArgs a) {
 
 __global__ void __launch_bounds__(EMB_THREADS) sort_scatter_kernel(SortArgs a) {
     constexpr int WARPS = EMB_THREADS / 32;
-    __shared__ uint32_t hist[WARPS][256], base[256], sums[WARPS];
+    __shared__ uint32_t hist[WARPS][DIGITS], sums[WARPS];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, t = threadIdx.x;
     const uint32_t mask = (1u << a.bits) - 1;
+    // the warp's 32 ITEMS consecutive tokens
+    uint2 it[ITEMS];
+    uint32_t rank[ITEMS];
+    const uint32_t i0 = blockIdx.x * uint32_t(TILE) + warp * (32 * ITEMS) + lane;
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) hist[w][t] = 0;
-    // where the digits start
-    const uint32_t tot = t <= mask ? a.total[t] : 0;
-    uint32_t s = tot;
+    for (int u = 0; u < ITEMS; ++u) {
+        const uint32_t i = i0 + 32 * u;
+        it[u] = make_uint2(0, i);
+        if (i < a.n) {
+            if (a.idx)
+                it[u].x = sort_key(a, i, false);
+            else
+                it[u] = a.in[i];
+        }
+    }
+    for (int d = lane; d < DIGITS; d += 32) hist[warp][d] = 0;
+    // where the digits 2 t and 2 t + 1 start
+    uint32_t tot[2], before[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        const uint32_t d = 2 * t + k;
+        tot[k] = d <= mask ? a.total[d] : 0;
+        before[k] = d <= mask ? a.count[size_t(d) * a.blocks + blockIdx.x] : 0;
+    }
+    uint32_t s = tot[0] + tot[1];
 #pragma unroll
     for (int o = 1; o < 32; o *= 2) {
         const uint32_t v = __shfl_up_sync(~0u, s, o);
         if (lane >= o) s += v;
     }
     if (lane == 31) sums[warp] = s;
-    __syncthreads();
-    for (int w = 0; w < warp; ++w) s += sums[w];
-    base[t] = s - tot + (t <= mask ? a.count[size_t(t) * a.blocks + blockIdx.x] : 0);
-    // ranks within the warp's 32 ITEMS consecutive tokens
-    uint32_t key[ITEMS], val[ITEMS], rank[ITEMS];
-    const uint32_t i0 = blockIdx.x * uint32_t(TILE) + warp * (32 * ITEMS) + lane;
-#pragma unroll
-    for (int u = 0; u < ITEMS; ++u) {
-        const uint32_t i = i0 + 32 * u;
-        key[u] = val[u] = 0;
-        if (i < a.n) {
-            key[u] = sort_key(a, i, false);
-            val[u] = a.idx ? i : a.vals[i];
-        }
-    }
+    __syncwarp();
+    // ranks among the warp's tokens
 #pragma unroll
     for (int u = 0; u < ITEMS; ++u) {
         // (tokens past the end rank among themselves)
         const bool in = i0 + 32 * u < a.n;
-        const uint32_t d = (key[u] >> a.shift) & mask;
+        const uint32_t d = (it[u].x >> a.shift) & mask;
         const uint32_t peers = __match_any_sync(~0u, in ? d : 0xffffffffu);
-        const uint32_t before = in ? hist[warp][d] : 0;
-        rank[u] = before + __popc(peers & lanemask_lt());
+        const uint32_t had = in ? hist[warp][d] : 0;
+        rank[u] = had + __popc(peers & lanemask_lt());
         __syncwarp();
-        if (in && lane == __ffs(peers) - 1) hist[warp][d] = before + __popc(peers);
+        if (in && lane == __ffs(peers) - 1) hist[warp][d] = had + __popc(peers);
         __syncwarp();
     }
     __syncthreads();
-    uint32_t run = base[t];
+    for (int w = 0; w < warp; ++w) s += sums[w];
+    s -= tot[0] + tot[1];
 #pragma unroll
-    for (int w = 0; w < WARPS; ++w) {
-        const uint32_t v = hist[w][t];
-        hist[w][t] = run;
-        run += v;
+    for (int k = 0; k < 2; ++k) {
+        uint32_t run = s + before[k];
+        s += tot[k];
+#pragma unroll
+        for (int w = 0; w < WARPS; ++w) {
+            const uint32_t v = hist[w][2 * t + k];
+            hist[w][2 * t + k] = run;
+            run += v;
+        }
     }
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < ITEMS; ++u)
-        if (i0 + 32 * u < a.n) {
-            const uint32_t at = hist[warp][(key[u] >> a.shift) & mask] + rank[u];
-            a.out_keys[at] = key[u];
-            a.out_vals[at] = val[u];
-        }
+        if (i0 + 32 * u < a.n)
+            a.out[hist[warp][(it[u].x >> a.shift) & mask] + rank[u]] = it[u];
 }
 
 // --- the rows' sums ---------------------------------------------------------------
 
 struct SumArgs {
     const void *dy;
-    const uint32_t *keys, *vals;
-    float *part1, *part2;  // sums of chunks of RUN tokens, of RUN such chunks
+    const uint2 *sorted;  // row, token
+    float *head, *tail;   // [chunks][C]: see emb_chunk_kernel
+    float *part2;         // sums of RUN2 heads whose chunks are one row's
     void *dtable;
-    uint32_t n;
-    int64_t rows;          // of all tables
-    int C;
+    uint32_t n, rows;     // tokens, rows of all tables
+    int C, run;           // tokens of a chunk
     float scale;
 };
 
-// sum += rows [i0, i1) of sorted tokens
 template <class T, int V>
-__device__ __forceinline__ void add_tokens(const SumArgs &a, uint32_t i0, uint32_t i1, int c,
-                                           float (&sum)[V]) {
-    constexpr int U = 4;
-    const T *dy = static_cast<const T *>(a.dy) + c;
-    uint32_t i = i0;
-    for (; i + U <= i1; i += U) {
-        float v[U][V];
+__device__ __forceinline__ void put_row(const SumArgs &a, uint32_t row, int c, float (&sum)[V]) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) Vec<T, V>::load(dy + size_t(a.vals[i + u]) * a.C, v[u]);
+    for (int e = 0; e < V; ++e) sum[e] *= a.scale;
+    Vec<T, V>::store(static_cast<T *>(a.dtable) + size_t(row) * a.C + c, sum);
+}
+
+// A chunk of `run` sorted tokens, by G threads: a row whose tokens all lie in the chunk
+// is written; of one that goes on from the chunk before, the sum goes to the chunk's head,
+// of one that goes on in the next alone, to its tail.
+template <class T, int V>
+__global__ void __launch_bounds__(EMB_THREADS) emb_chunk_kernel(SumArgs a, int G) {
+    constexpr int U = 8;
+    using R = RawV<T, V>;
+    const int per = EMB_THREADS / G, g = threadIdx.x / G, l = threadIdx.x - g * G;
+    const uint32_t k = blockIdx.x * per + g;
+    if (g >= per || uint64_t(k) * a.run >= a.n) return;
+    const uint32_t i0 = k * a.run, i1 = min(a.n, i0 + a.run);
+    const uint32_t first = a.sorted[i0].x, none = 0xffffffffu;
+    if (first >= a.rows) return;
+    const bool from = i0 > 0 && a.sorted[i0 - 1].x == first;
+    const uint32_t after = i1 < a.n ? a.sorted[i1].x : none;
+    for (int c = l * V; c < a.C; c += G * V) {
+        const T *dy = static_cast<const T *>(a.dy) + c;
+        float sum[V];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int e = 0; e < V; ++e) sum[e] = 0.0f;
+        uint32_t cur = first;
+        bool open = from;
+        // the row `cur` ends, or the chunk does
+        auto close = [&]() {
+            if (open)
+                Vec<float, V>::store(a.head + size_t(k) * a.C + c, sum);
+            else
+                put_row<T, V>(a, cur, c, sum);
+            open = false;
 #pragma unroll
-            for (int e = 0; e < V; ++e) sum[e] += v[u][e];
-    }
-    for (; i < i1; ++i) {
-        float v[V];
-        Vec<T, V>::load(dy + size_t(a.vals[i]) * a.C, v);
+            for (int e = 0; e < V; ++e) sum[e] = 0.0f;
+        };
+        uint2 next[U];  // a batch ahead
 #pragma unroll
-        for (int e = 0; e < V; ++e) sum[e] += v[e];
+        for (int u = 0; u < U; ++u) next[u] = i0 + u < i1 ? a.sorted[i0 + u] : make_uint2(none, 0);
+        for (uint32_t i = i0; i < i1; i += U) {
+            uint2 it[U];
+            R raw[U];
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                it[u] = next[u];
+                if (it[u].x < a.rows)
+                    raw[u] = __ldcs(reinterpret_cast<const R *>(dy + size_t(it[u].y) * a.C));
+            }
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                next[u] = i + U + u < i1 ? a.sorted[i + U + u] : make_uint2(none, 0);
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                if (it[u].x == none) continue;  // past the chunk's end
+                if (it[u].x != cur && cur < a.rows) close();
+                cur = it[u].x;
+                if (cur < a.rows) {
+                    float v[V];
+                    widen<T, V>(raw[u], v);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) sum[e] += v[e];
+                }
+            }
+        }
+        if (cur < a.rows) {
+            if (!open && after == cur)
+                Vec<float, V>::store(a.tail + size_t(k) * a.C + c, sum);
+            else
+                close();
+        }
     }
 }
+
 template <int V>
 __device__ __forceinline__ void add_parts(const float *part, uint32_t i0, uint32_t i1, int c, int C,
                                           float (&sum)[V]) {
-#pragma unroll 4
+#pragma unroll 8
     for (uint32_t i = i0; i < i1; ++i) {
         float v[V];
         Vec<float, V>::load(part + size_t(i) * C + c, v);
@@ -235,104 +341,93 @@ __device__ __forceinline__ void add_parts(const float *part, uint32_t i0, uint32
     }
 }
 
-// Chunks of one row alone: of tokens (LEVEL 1), of chunks (LEVEL 2).  A thread
-// a vector of a chunk.
-template <class T, int V, int LEVEL>
-__global__ void __launch_bounds__(EMB_THREADS) emb_chunk_kernel(SumArgs a) {
-    const int nv = a.C / V;
-    const int64_t i = int64_t(blockIdx.x) * EMB_THREADS + threadIdx.x;
-    const uint32_t span = LEVEL == 1 ? RUN : RUN * RUN;
-    const int64_t k = i / nv;
-    const int c = int(i - k * nv) * V;
-    if ((k + 1) * span > a.n) return;
-    const uint32_t i0 = uint32_t(k) * span, first = a.keys[i0];
-    if (first >= a.rows || a.keys[i0 + span - 1] != first) return;
-    float sum[V];
-#pragma unroll
-    for (int e = 0; e < V; ++e) sum[e] = 0.0f;
-    if (LEVEL == 1)
-        add_tokens<T, V>(a, i0, i0 + RUN, c, sum);
-    else
-        add_parts<V>(a.part1, uint32_t(k) * RUN, uint32_t(k + 1) * RUN, c, a.C, sum);
-    Vec<float, V>::store((LEVEL == 1 ? a.part1 : a.part2) + size_t(k) * a.C + c, sum);
-}
-
-// the first sorted token whose row is not below `row`
-__device__ __forceinline__ uint32_t lower_bound(const uint32_t *keys, uint32_t n, uint32_t row) {
-    uint32_t lo = 0, hi = n;
-    while (lo < hi) {
-        const uint32_t mid = lo + (hi - lo) / 2;
-        if (keys[mid] < row)
-            lo = mid + 1;
-        else
-            hi = mid;
-    }
-    return lo;
-}
-
-// G threads a row of the table.
-template <class T, int V>
-__global__ void __launch_bounds__(EMB_THREADS) emb_rows_kernel(SumArgs a, int G) {
-    const int per = EMB_THREADS / G, g = threadIdx.x / G, l = threadIdx.x % G;
-    __shared__ uint32_t bounds[EMB_THREADS + 1];
-    const int64_t r0 = int64_t(blockIdx.x) * per;
-    for (int i = threadIdx.x; i <= per; i += EMB_THREADS)
-        bounds[i] = lower_bound(a.keys, a.n, uint32_t(min(r0 + int64_t(i), a.rows)));
-    __syncthreads();
-    const int64_t row = r0 + g;
-    if (g >= per || row >= a.rows) return;
-    const uint32_t s = bounds[g], e = bounds[g + 1];
+// RUN2 chunks that one row fills and came into.
+template <int V>
+__global__ void __launch_bounds__(EMB_THREADS) emb_second_kernel(SumArgs a, int G) {
+    const int per = EMB_THREADS / G, g = threadIdx.x / G, l = threadIdx.x - g * G;
+    const uint32_t j = blockIdx.x * per + g, span = uint32_t(a.run) * RUN2;
+    if (g >= per || (uint64_t(j) + 1) * span > a.n) return;
+    const uint32_t row = a.sorted[j * span].x;
+    if (row >= a.rows || a.sorted[j * span + span - 1].x != row) return;
+    if (j == 0 || a.sorted[j * span - 1].x != row) return;
     for (int c = l * V; c < a.C; c += G * V) {
         float sum[V];
 #pragma unroll
-        for (int k = 0; k < V; ++k) sum[k] = 0.0f;
-        // whole chunks of the row: [c0, c1), and of those whole second chunks [d0, d1)
-        const uint32_t c0 = (s + RUN - 1) / RUN, c1 = e / RUN;
-        if (c0 >= c1) {
-            add_tokens<T, V>(a, s, e, c, sum);
+        for (int e = 0; e < V; ++e) sum[e] = 0.0f;
+        add_parts<V>(a.head, j * RUN2, (j + 1) * RUN2, c, a.C, sum);
+        Vec<float, V>::store(a.part2 + size_t(j) * a.C + c, sum);
+    }
+}
+
+// The rows that go on beyond the chunk k that they begin in: its tail and the heads of the
+// chunks after it.
+template <class T, int V>
+__global__ void __launch_bounds__(EMB_THREADS) emb_join_kernel(SumArgs a, int G) {
+    const int per = EMB_THREADS / G, g = threadIdx.x / G, l = threadIdx.x - g * G;
+    const uint32_t k = blockIdx.x * per + g;
+    if (g >= per || (uint64_t(k) + 1) * a.run >= a.n) return;
+    const uint32_t i0 = k * a.run, i1 = i0 + a.run, row = a.sorted[i1].x;
+    if (row >= a.rows || a.sorted[i1 - 1].x != row) return;
+    if (k > 0 && a.sorted[i0].x == row && a.sorted[i0 - 1].x == row) return;  // began before
+    // the last chunk that starts with the row
+    uint32_t lo = k + 1, hi = (a.n - 1) / a.run;
+    if (lo < hi && a.sorted[(lo + 1) * a.run].x != row) hi = lo;
+    while (lo < hi) {
+        const uint32_t mid = lo + (hi - lo + 1) / 2;
+        if (a.sorted[mid * a.run].x == row)
+            lo = mid;
+        else
+            hi = mid - 1;
+    }
+    // heads [k + 1, lo]; second sums [j0, j1) of those that the row fills, all but the last
+    const uint32_t h0 = k + 1, h1 = lo + 1, j0 = (h0 + RUN2 - 1) / RUN2, j1 = lo / RUN2;
+    for (int c = l * V; c < a.C; c += G * V) {
+        float sum[V];
+        Vec<float, V>::load(a.tail + size_t(k) * a.C + c, sum);
+        if (j0 < j1) {
+            add_parts<V>(a.head, h0, j0 * RUN2, c, a.C, sum);
+            add_parts<V>(a.part2, j0, j1, c, a.C, sum);
+            add_parts<V>(a.head, j1 * RUN2, h1, c, a.C, sum);
         } else {
-            const uint32_t d0 = (c0 + RUN - 1) / RUN, d1 = c1 / RUN;
-            add_tokens<T, V>(a, s, c0 * RUN, c, sum);
-            if (d0 >= d1) {
-                add_parts<V>(a.part1, c0, c1, c, a.C, sum);
-            } else {
-                add_parts<V>(a.part1, c0, d0 * RUN, c, a.C, sum);
-                add_parts<V>(a.part2, d0, d1, c, a.C, sum);
-                add_parts<V>(a.part1, d1 * RUN, c1, c, a.C, sum);
-            }
-            add_tokens<T, V>(a, c1 * RUN, e, c, sum);
+            add_parts<V>(a.head, h0, h1, c, a.C, sum);
         }
-#pragma unroll
-        for (int k = 0; k < V; ++k) sum[k] *= a.scale;
-        Vec<T, V>::store(static_cast<T *>(a.dtable) + row * a.C + c, sum);
+        put_row<T, V>(a, row, c, sum);
     }
 }
 
 // --- launches ---------------------------------------------------------------------
 
+// Threads of a row of `nv` vectors: a warp takes rows of more in several goes.
+int emb_group(int nv) { return nv < 32 ? nv : nv <= 64 ? (nv + 1) / 2 : 32; }
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
 template <class T, int V>
 cudaError_t emb_forward(const DeviceInfo &dev, const void *table, int64_t V_, int C,
                         const int64_t *idx, int64_t T_, int64_t tokens, float scale, void *out,
                         cudaStream_t st) {
-    const int64_t want = (tokens * (C / V) + 4 * EMB_THREADS - 1) / (4 * EMB_THREADS);
-    const int64_t most = int64_t(dev.sm_count) * 8 * 16;
-    emb_forward_kernel<T, V><<<unsigned(want < most ? want : most), EMB_THREADS, 0, st>>>(
-        static_cast<const T *>(table), V_, C, idx, T_, tokens, scale, static_cast<T *>(out),
+    const int G = emb_group(C / V), per = EMB_THREADS / G;
+    const int64_t blocks = ceil_div(tokens, per * FORWARD_TOKENS);
+    if (blocks > 2147483647) return cudaErrorInvalidConfiguration;
+    emb_forward_kernel<T, V><<<unsigned(blocks), EMB_THREADS, 0, st>>>(
+        static_cast<const T *>(table), V_, C, idx, T_, tokens, scale, static_cast<T *>(out), G,
         dev.status_word);
     return cudaGetLastError();
 }
 
 template <class T, int V>
 cudaError_t emb_sums(const SumArgs &a, cudaStream_t st) {
-    const int nv = a.C / V;
-    auto blocks = [&](int64_t chunks) {
-        return unsigned((chunks * nv + EMB_THREADS - 1) / EMB_THREADS);
-    };
-    if (a.n >= RUN) emb_chunk_kernel<T, V, 1><<<blocks(a.n / RUN), EMB_THREADS, 0, st>>>(a);
-    if (a.n >= RUN * RUN)
-        emb_chunk_kernel<T, V, 2><<<blocks(a.n / (RUN * RUN)), EMB_THREADS, 0, st>>>(a);
-    const int G = nv < EMB_THREADS ? nv : EMB_THREADS, per = EMB_THREADS / G;
-    emb_rows_kernel<T, V><<<unsigned((a.rows + per - 1) / per), EMB_THREADS, 0, st>>>(a, G);
+    const int G = emb_group(a.C / V), per = EMB_THREADS / G;
+    auto blocks = [&](int64_t n) { return unsigned(ceil_div(n, per)); };
+    const int64_t chunks = ceil_div(a.n, a.run);
+    emb_chunk_kernel<T, V><<<blocks(chunks), EMB_THREADS, 0, st>>>(a, G);
+    if (chunks > 1) {
+        const int nv = a.C / V, G2 = nv < EMB_THREADS ? nv : EMB_THREADS, per2 = EMB_THREADS / G2;
+        if (chunks > RUN2)
+            emb_second_kernel<V>
+                <<<unsigned(ceil_div(chunks / RUN2, per2)), EMB_THREADS, 0, st>>>(a, G2);
+        emb_join_kernel<T, V>
+            <<<unsigned(ceil_div(chunks - 1, per2)), EMB_THREADS, 0, st>>>(a, G2);
+    }
     return cudaGetLastError();
 }
 
@@ -372,40 +467,49 @@ cudaError_t emb_sums_any(const SumArgs &a, cudaStream_t st) {
 cudaError_t emb_backward(const DeviceInfo &dev, const void *dy, int dtype, int64_t B, int64_t V,
                          int C, const int64_t *idx, int64_t T, float scale, void *dtable,
                          cudaStream_t st) {
+    // rows without tokens are 0 (the others are written again)
+    const size_t es = dtype == PC_F32 ? 4 : 2;
+    cudaError_t e = cudaMemsetAsync(dtable, 0, size_t(B) * V * C * es, st);
+    if (e != cudaSuccess || B * T == 0) return e;
     SumArgs a{};
-    a.dy = dy, a.dtable = dtable, a.n = uint32_t(B * T), a.rows = B * V, a.C = C, a.scale = scale;
+    a.dy = dy, a.dtable = dtable, a.n = uint32_t(B * T), a.rows = uint32_t(B * V), a.C = C;
+    a.scale = scale;
+    // 64 tokens a chunk, or 32 or 16 where that leaves the SMs short of warps
+    const int64_t warps = ceil_div(int64_t(C) * es, 512) * a.n;
+    a.run = warps / 64 >= int64_t(dev.sm_count) * 32 ? 64
+            : warps / 32 >= int64_t(dev.sm_count) * 32 ? 32
+                                                       : 16;
     // keys 0 .. rows, the last for absent tokens
     int bits = 0;
-    while ((int64_t(1) << bits) <= a.rows) ++bits;
-    const int passes = (bits + 7) / 8, each = (bits + passes - 1) / passes;
+    while ((int64_t(1) << bits) <= int64_t(a.rows)) ++bits;
+    const int passes = (bits + 8) / 9, each = (bits + passes - 1) / passes;
     const int blocks = int((int64_t(a.n) + TILE - 1) / TILE);
     auto round = [](size_t v) { return (v + 255) / 256 * 256; };
-    const size_t list = round(size_t(a.n) * 4), count = round((size_t(blocks) + 1) * 256 * 4);
-    const size_t part1 = round(size_t(a.n / RUN) * C * 4);
-    const size_t part2 = round(size_t(a.n / (RUN * RUN)) * C * 4);
+    const size_t list = round(size_t(a.n) * sizeof(uint2));
+    const size_t count = round((size_t(blocks) + 1) * (size_t(1) << each) * 4);
+    const size_t chunks = size_t(ceil_div(a.n, a.run)), part = round(chunks * C * 4);
     char *mem = nullptr;
-    cudaError_t e = scratch_alloc(dev, reinterpret_cast<void **>(&mem),
-                                  4 * list + count + part1 + part2, st);
+    e = scratch_alloc(dev, reinterpret_cast<void **>(&mem),
+                      2 * list + count + 2 * part + round(chunks / RUN2 * C * 4), st);
     if (e != cudaSuccess) return e;
-    uint32_t *lists[2][2];  // [which][keys, tokens]
-    for (int i = 0; i < 4; ++i) lists[i / 2][i % 2] = reinterpret_cast<uint32_t *>(mem + i * list);
+    uint2 *lists[2] = {reinterpret_cast<uint2 *>(mem), reinterpret_cast<uint2 *>(mem + list)};
     SortArgs s{};
-    s.idx = idx, s.rows = V, s.per_cloud = T, s.n = a.n, s.absent = uint32_t(a.rows);
-    s.count = reinterpret_cast<uint32_t *>(mem + 4 * list);
-    s.total = s.count + size_t(256) * blocks;
+    s.idx = idx, s.rows = V, s.per_cloud = uint32_t(T), s.n = a.n, s.absent = a.rows;
+    s.count = reinterpret_cast<uint32_t *>(mem + 2 * list);
+    s.total = s.count + (size_t(blocks) << each);
     s.blocks = blocks, s.bits = each, s.status = dev.status_word;
-    if (a.n > 0)
-        for (int p = 0; p < passes; ++p) {
-            s.shift = p * each;
-            s.out_keys = lists[p % 2][0], s.out_vals = lists[p % 2][1];
-            sort_count_kernel<<<blocks, EMB_THREADS, 0, st>>>(s);
-            sort_scan_kernel<<<((1 << each) + 7) / 8, EMB_THREADS, 0, st>>>(s);
-            sort_scatter_kernel<<<blocks, EMB_THREADS, 0, st>>>(s);
-            s.idx = nullptr, s.keys = s.out_keys, s.vals = s.out_vals;
-        }
-    a.keys = lists[(passes + 1) % 2][0], a.vals = lists[(passes + 1) % 2][1];
-    a.part1 = reinterpret_cast<float *>(mem + 4 * list + count);
-    a.part2 = reinterpret_cast<float *>(mem + 4 * list + count + part1);
+    for (int p = 0; p < passes; ++p) {
+        s.shift = p * each;
+        s.out = lists[p % 2];
+        sort_count_kernel<<<blocks, EMB_THREADS, 0, st>>>(s);
+        sort_scan_kernel<<<((1 << each) + 7) / 8, EMB_THREADS, 0, st>>>(s);
+        sort_scatter_kernel<<<blocks, EMB_THREADS, 0, st>>>(s);
+        s.idx = nullptr, s.in = s.out;
+    }
+    a.sorted = s.out;
+    a.head = reinterpret_cast<float *>(mem + 2 * list + count);
+    a.tail = a.head + part / sizeof(float);
+    a.part2 = a.tail + part / sizeof(float);
     e = cudaGetLastError();
     if (e == cudaSuccess)
         e = dtype == PC_F32 ? emb_sums_any<float>(a, st) : emb_sums_any<bf16>(a, st);

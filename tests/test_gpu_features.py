@@ -499,21 +499,34 @@ def test_embedding(shape, tokens, dtype):
     dy = randn(g, *tokens, C, dtype=dtype)
     d = pc.pc_embedding_backward(dy, idx, shape, scale)
     s, m = emb_reference(dy, idx, shape, scale)
-    # a run of 64 tokens, chunks of 64, chunks of these, the two ends: each at most 64 + 5 long
+    # a run of at most 64 tokens, up to 64 runs, sums of 64 runs, the ends: each at most 64 + 5
     close(d, s, (5 * 70 * U) * m + HALF[dtype] * s.abs() + 1e-30, "grad_table")
     assert torch.equal(d, pc.pc_embedding_backward(dy, idx, shape, scale))
 
 
 def test_embedding_adds_in_the_order_of_the_tokens():
-    """Rows of up to 64 tokens: the float32 sum, one token after the other."""
+    """The float32 sums of a row's tokens one after the other, in runs that end at every 16th
+    of the sorted tokens (a small call), and the runs one after the other."""
     g = gen(12)
     idx = torch.randint(0, 300, (5000,), generator=g, device=DEV)
     dy = randn(g, 5000, 6)
     d = pc.pc_embedding_backward(dy, idx, (300, 6))
+    order = torch.sort(idx, stable=True)[1].cpu()
+    rows, dy = idx.cpu(), dy.cpu()
+    runs = {}
+    for at, i in enumerate(order.tolist()):
+        runs.setdefault(int(rows[i]), {}).setdefault(at // 16, []).append(dy[i])
     want = torch.zeros(300, 6)
-    for i, v in zip(idx.tolist(), dy.cpu()):
-        want[i] += v
-    assert int(torch.bincount(idx).max()) <= 64
+    for row, parts in runs.items():
+        sums = []
+        for part in parts.values():
+            s = torch.zeros(6)
+            for v in part:
+                s = s + v
+            sums.append(s)
+        want[row] = sums[0]
+        for s in sums[1:]:
+            want[row] += s
     assert torch.equal(d.cpu(), want)
 
 
@@ -550,7 +563,7 @@ def test_embedding_long_sum_of_one_row():
     dy = 1.0 + 0.25 * torch.rand(T, 4, generator=gen(5), device=DEV)
     d = pc.pc_embedding_backward(dy, torch.zeros(T, dtype=torch.int64, device=DEV), (3, 4))
     s, m = emb_reference(dy, torch.zeros(T, dtype=torch.int64, device=DEV), (3, 4), 1.0)
-    close(d, s, (5 * 70 + 150) * U * m + 1e-30, "grad_table")   # 146 chunks of chunks
+    close(d, s, (5 * 70 + 600) * U * m + 1e-30, "grad_table")   # 586 sums of 64 runs of 16
     assert not d[1:].any()
 
 
