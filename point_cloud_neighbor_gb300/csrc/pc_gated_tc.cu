@@ -40,6 +40,7 @@
 #include "pc_tiles.cuh"
 #include "pointcloud.h"
 
+#include <cstdlib>
 #include <type_traits>
 
 namespace pcn {
@@ -71,31 +72,29 @@ struct GemmArgs {
     int *status;
 };
 
-template <int MODE, int P, int BN>
+template <int MODE, int P, int BN, int CG>
 struct GCfg {
     static constexpr bool PAIR = MODE == G_FWD || MODE == G_GRAD;
-    static constexpr int A_BYTES = BM * 128, B_BYTES = BN * 128;
+    static constexpr int A_BYTES = BM * 128, B_BYTES = BN / CG * 128;
+    static constexpr int M = BM * CG;  // rows of a tile
     static constexpr int STAGE = A_BYTES + B_BYTES;  // of one part of both operands
-    static constexpr int EWARPS = 8, THREADS = 32 * (4 + EWARPS);
-    // PAIR with chunks of 32 columns: a warp's 32 x 32 tiles of the arrays that are as
-    // large as the result, on their way from or to global memory.  bfloat16: as tensor
-    // maps have them, or with rows of 34; float32: column c of row r at c ^ r.
-    static constexpr bool STAGED = PAIR && BN >= 128;
-    static constexpr int ROOM = !STAGED ? 0 : P > 1 ? 4096 : MODE == G_FWD ? 2560 : 8192;
+    // Warps that take the accumulators: four for the 128 rows, times parts of the columns.
+    // 16 where a tile's arithmetic outlasts its products otherwise.
+    static constexpr int EWARPS = PAIR && BN == 256 ? 16 : 8, THREADS = 32 * (4 + EWARPS);
+    static constexpr int COLS = 2 * BN;               // tensor memory
+    static constexpr int NL = BN / (EWARPS / 4);      // columns of a thread
+    static constexpr int CH = PAIR ? NL / 2 : 32;     // PAIR: hidden units, else of a chunk
+    static_assert(!PAIR || CH == 32 || CH == 16, "chunks");
+    // PAIR with 32 units a warp: its 32 x 32 tiles of the arrays that are as large as the
+    // result, on their way from or to global memory, 2 KB each in bfloat16: dy, da and
+    // du; y.  As tensor maps have them, or (float32, unaligned rows) as place() does.
+    static constexpr bool STAGED = PAIR && CH == 32;
+    static constexpr int ROOM = !STAGED ? 0 : P > 1 ? 4096 : MODE == G_FWD ? 2048 : 6144;
     static constexpr int FIT = (227 * 1024 - 1024 - 512 - EWARPS * ROOM) / STAGE,
                          STAGES = FIT > 8 ? 8 : FIT;
     static_assert(STAGES >= 2 * P, "shared memory");
     static constexpr size_t SMEM = 1024 + size_t(STAGES) * STAGE + EWARPS * ROOM + 512;
     static_assert(SMEM > 114 * 1024 && SMEM <= 227 * 1024, "one block a SM");
-    static constexpr int COLS = 2 * BN;                  // tensor memory
-    static constexpr int NL = BN / 2;                    // columns of a thread
-    static constexpr int CH = PAIR ? (BN / 4 < 32 ? BN / 4 : 32) : 32;
-    // column of the thread's chunk j of CH; PAIR: first the gate's, then the up's
-    static __host__ __device__ constexpr int column(int half, int j) {
-        constexpr int n = PAIR ? NL / 2 / CH : NL / CH;
-        return PAIR ? (j < n ? half * (BN / 4) + j * CH : BN / 2 + half * (BN / 4) + (j - n) * CH)
-                    : half * NL + j * CH;
-    }
 };
 
 // The six products of three parts, the smallest first.
@@ -148,17 +147,13 @@ __device__ __forceinline__ void take(const T *p, float (&v)[CH], int left, bool 
 __device__ __forceinline__ unsigned char *row_part(unsigned char *tile, int lane, int c) {
     return tile + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16);
 }
-__device__ __forceinline__ void put_row(unsigned char *tile, int lane, const float *v) {
+// N of them from column o on.
+template <int N>
+__device__ __forceinline__ void put_row(unsigned char *tile, int lane, int o, const float *v) {
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-        Vec<bf16, 8>::store(reinterpret_cast<bf16 *>(row_part(tile, lane, c)), v + 8 * c);
+    for (int c = 0; c < N / 8; ++c)
+        Vec<bf16, 8>::store(reinterpret_cast<bf16 *>(row_part(tile, lane, o / 8 + c)), v + 8 * c);
 }
-__device__ __forceinline__ void get_row(unsigned char *tile, int lane, float *v) {
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        Vec<bf16, 8>::load(reinterpret_cast<const bf16 *>(row_part(tile, lane, c)), v + 8 * c);
-}
-
 // P parts of eight numbers, `plane` elements apart.
 template <int P>
 __device__ __forceinline__ void put_parts(bf16 *p, int64_t plane, const float *v) {
@@ -199,10 +194,10 @@ __device__ __forceinline__ float column_sums(const float (&x)[CH], int lane) {
     return v[0];
 }
 
-template <int MODE, int P, int BN>
-__global__ void __launch_bounds__(GCfg<MODE, P, BN>::THREADS, 1)
+template <int MODE, int P, int BN, int CG>
+__global__ void __launch_bounds__(GCfg<MODE, P, BN, CG>::THREADS, 1)
 gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
-    using C = GCfg<MODE, P, BN>;
+    using C = GCfg<MODE, P, BN, CG>;
     using T = std::conditional_t<P == 1, bf16, float>;
     constexpr int STAGES = C::STAGES, CH = C::CH;
     extern __shared__ unsigned char smem_raw[];
@@ -211,24 +206,28 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
     unsigned char *rooms = base + size_t(STAGES) * C::STAGE;
     uint64_t *full = reinterpret_cast<uint64_t *>(rooms + C::EWARPS * C::ROOM);
     uint64_t *empty = full + STAGES, *accfull = empty + STAGES, *accempty = accfull + 2;
-    uint64_t *done = accempty + 2, *dybar = done + 1;  // dybar: [warp][chunk]
-    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dybar + 2 * C::EWARPS);
+    uint64_t *done = accempty + 2, *dybar = done + 1;  // dybar: of each warp
+    uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dybar + C::EWARPS);
     volatile int *stop = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
-    const int tiles = a.mt * a.nt;
-    const int64_t items = int64_t(tiles) * a.nsplit;
+    const int tiles = a.mt * a.nt, items = tiles * a.nsplit;
+    // the blocks of a tile: one, or a cluster of two with 128 rows each
+    const int rank = CG > 1 ? int(cluster_ctarank()) : 0;
+    const int first = int(blockIdx.x) / CG, step = int(gridDim.x) / CG;
     if (threadIdx.x == 0) {
         for (int s = 0; s < STAGES; ++s) mbar_init(&full[s], 1), mbar_init(&empty[s], 1);
-        for (int s = 0; s < 2; ++s) mbar_init(&accfull[s], 1), mbar_init(&accempty[s], C::EWARPS);
+        for (int s = 0; s < 2; ++s)
+            mbar_init(&accfull[s], 1), mbar_init(&accempty[s], CG * C::EWARPS);
         mbar_init(done, 1);
-        for (int s = 0; s < 2 * C::EWARPS; ++s) mbar_init(&dybar[s], 1);
+        for (int s = 0; s < C::EWARPS; ++s) mbar_init(&dybar[s], 1);
         *stop = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 2) tmem_alloc(tmem_slot, C::COLS);
+    if (warp == 2) tmem_alloc<CG>(tmem_slot, C::COLS);
     tc_fence_before();
     __syncthreads();
+    if (CG > 1) cluster_sync_all();  // both blocks' barriers exist
     tc_fence_after();
     const uint32_t tmem = uniform(int(*tmem_slot));
 
@@ -244,12 +243,12 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
     // an item: a tile and a part of its contraction
     struct Item {
         int m, n, k0, k1, split;
-        __device__ __forceinline__ Item(const GemmArgs &a, int64_t i, int tiles) {
-            split = int(i / tiles);
-            const int t = int(i - int64_t(split) * tiles);
-            m = t / a.nt, n = t - m * a.nt;
-            k0 = int(int64_t(a.kb) * split / a.nsplit);
-            k1 = int(int64_t(a.kb) * (split + 1) / a.nsplit);
+        __device__ __forceinline__ Item(const GemmArgs &a, int i, int tiles) {
+            split = unsigned(i) / unsigned(tiles);
+            const unsigned t = i - split * tiles;
+            m = t / unsigned(a.nt), n = t - m * a.nt;
+            k0 = unsigned(a.kb * split) / unsigned(a.nsplit);  // (below 2^30: nsplit <= 2^16)
+            k1 = unsigned(a.kb * (split + 1)) / unsigned(a.nsplit);
         }
     };
 
@@ -259,67 +258,85 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
             int s = 0;
             unsigned phase = 1;  // (of the ring's first round: passes at once)
             int64_t issued = 0;
-            bool ok = !(a.withhold && blockIdx.x == 0);
-            for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            bool ok = !(a.withhold && first == 0);
+            for (int i = first; ok && i < items; i += step) {
                 const Item it(a, i, tiles);
                 const int dw_mt = a.mt / 2;  // DW: tiles of dWg, then of dWu
+                const int m0 = (MODE == G_DW && it.m >= dw_mt ? it.m - dw_mt : it.m) * C::M +
+                               rank * BM;
                 for (int k = it.k0; ok && k < it.k1; ++k)
 #pragma unroll
                     for (int p = P - 1; p >= 0; --p) {
                         if (!(ok = await(&empty[s], phase))) break;
                         unsigned char *A = base + size_t(s) * C::STAGE, *B = A + C::A_BYTES;
+                        // (both blocks' bytes are counted in the first)
                         uint64_t *bar = &full[s];
-                        mbar_arrive_expect_tx(bar, C::STAGE);
+                        if (rank == 0) mbar_arrive_expect_tx(bar, CG * C::STAGE);
+                        const uint32_t pair_bar = CG > 1 ? map_shared_rank(bar, 0) : 0;
+                        auto load = [&](unsigned char *to, const CUtensorMap *map, int c, int r) {
+                            if (CG > 1)
+                                tma_load_3d_pair(to, map, c, r, p, pair_bar);
+                            else
+                                tma_load_3d(to, map, c, r, p, bar);
+                        };
                         if (C::PAIR) {
-                            tma_load_3d(A, &maps.a0, k * BK, it.m * BM, p, bar);
-                            tma_load_3d(B, &maps.b0, k * BK, it.n * (BN / 2), p, bar);
-                            tma_load_3d(B + C::B_BYTES / 2, &maps.b1, k * BK, it.n * (BN / 2), p,
-                                        bar);
-                        } else if (MODE == G_DX) {
-                            const bool up = k >= a.kb0;
-                            const int f = (up ? k - a.kb0 : k) * BK;
-                            tma_load_3d(A, up ? &maps.a1 : &maps.a0, f, it.m * BM, p, bar);
-#pragma unroll
-                            for (int j = 0; j < BN / 64; ++j)
-                                tma_load_3d(B + j * PANEL, up ? &maps.b1 : &maps.b0,
-                                            it.n * BN + 64 * j, f, p, bar);
+                            load(A, &maps.a0, k * BK, m0);
+                            if (CG > 1) {  // the first block Wg, the second Wu
+                                load(B, rank ? &maps.b1 : &maps.b0, k * BK, it.n * (BN / 2));
+                            } else {
+                                load(B, &maps.b0, k * BK, it.n * (BN / 2));
+                                load(B + C::B_BYTES / 2, &maps.b1, k * BK, it.n * (BN / 2));
+                            }
                         } else {
-                            const bool up = it.m >= dw_mt;
-                            const int f = (up ? it.m - dw_mt : it.m) * BM;
+                            const int n0 = it.n * BN + rank * (BN / CG);
+                            if (MODE == G_DX) {
+                                const bool up = k >= a.kb0;
+                                const int f = (up ? k - a.kb0 : k) * BK;
+                                load(A, up ? &maps.a1 : &maps.a0, f, m0);
 #pragma unroll
-                            for (int j = 0; j < BM / 64; ++j)
-                                tma_load_3d(A + j * PANEL, up ? &maps.a1 : &maps.a0, f + 64 * j,
-                                            k * BK, p, bar);
+                                for (int j = 0; j < BN / CG / 64; ++j)
+                                    load(B + j * PANEL, up ? &maps.b1 : &maps.b0, n0 + 64 * j, f);
+                            } else {
 #pragma unroll
-                            for (int j = 0; j < BN / 64; ++j)
-                                tma_load_3d(B + j * PANEL, &maps.b0, it.n * BN + 64 * j, k * BK, p,
-                                            bar);
+                                for (int j = 0; j < BM / 64; ++j)
+                                    load(A + j * PANEL, it.m >= dw_mt ? &maps.a1 : &maps.a0,
+                                         m0 + 64 * j, k * BK);
+#pragma unroll
+                                for (int j = 0; j < BN / CG / 64; ++j)
+                                    load(B + j * PANEL, &maps.b0, n0 + 64 * j, k * BK);
+                            }
                         }
                         ++issued;
                         if (++s == STAGES) s = 0, phase ^= 1;
                     }
             }
-            // nothing is in flight when the block ends
-            for (int64_t k = issued > STAGES ? issued - STAGES : 0; k < issued; ++k)
+            // nothing is in flight when the blocks end
+            for (int64_t k = rank ? issued : issued > STAGES ? issued - STAGES : 0; k < issued; ++k)
                 mbar_wait_bounded(&full[k % STAGES], unsigned((k / STAGES) & 1), a.timeout_ns);
         }
     } else if (warp == 1) {
-        // ---- products ---------------------------------------------------------------
-        if (elect_one()) {
+        // ---- products, of both blocks by the first ------------------------------------
+        if (elect_one() && rank == 0) {
             constexpr bool AR = MODE == G_DW, BR = !C::PAIR;  // contracted along their rows
-            constexpr uint32_t id = mma_idesc(BN, BR, AR);
+            constexpr uint32_t id = mma_idesc(BN, BR, AR, C::M);
             constexpr uint32_t da = AR ? 16 * 128 / 16 : 2, db = BR ? 16 * 128 / 16 : 2;
             const uint32_t a0 = smem_operand(smem_u32(base), AR ? PANEL : 16);
             const uint32_t b0 = smem_operand(smem_u32(base) + C::A_BYTES, BR ? PANEL : 16);
             int s = 0, buf = 0;
             unsigned phase = 0, aphase = 1;
             bool ok = true;
-            for (int64_t i = blockIdx.x; ok && i < items; i += gridDim.x) {
+            auto commit = [](uint64_t *bar) {
+                if (CG > 1)
+                    mma_commit_pair(bar);
+                else
+                    mma_commit(bar);
+            };
+            for (int i = first; ok && i < items; i += step) {
                 const Item it(a, i, tiles);
                 for (int k = it.k0; k < it.k1; ++k) {
                     // (float32: an accumulator for every 64 of the depth)
-                    const bool first = P > 1 || k == it.k0;
-                    if (first && !(ok = await(&accempty[buf], aphase))) break;
+                    const bool fresh = P > 1 || k == it.k0;
+                    if (fresh && !(ok = await(&accempty[buf], aphase))) break;
                     int at[P];  // the stages of the parts, which come in falling order
 #pragma unroll
                     for (int p = P - 1; p >= 0; --p) {
@@ -338,25 +355,29 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                                        bs = b0 + at[pb] * (C::STAGE / 16);
 #pragma unroll
                         for (int j = 0; j < BK / 16; ++j)
-                            mma_ss<SMEM_128B>(d, as + j * da, bs + j * db, id,
-                                              !first || q > 0 || j > 0);
-                        if (P == 1 || q == 5) mma_commit(&empty[at[0]]);
-                        if (P > 1 && q == 4) mma_commit(&empty[at[P > 1 ? 1 : 0]]);
-                        if (P > 1 && q == 1) mma_commit(&empty[at[P > 1 ? 2 : 0]]);
+                            if (CG > 1)
+                                mma_ss_pair<SMEM_128B>(d, as + j * da, bs + j * db, id,
+                                                       !fresh || q > 0 || j > 0);
+                            else
+                                mma_ss<SMEM_128B>(d, as + j * da, bs + j * db, id,
+                                                  !fresh || q > 0 || j > 0);
+                        if (P == 1 || q == 5) commit(&empty[at[0]]);
+                        if (P > 1 && q == 4) commit(&empty[at[P > 1 ? 1 : 0]]);
+                        if (P > 1 && q == 1) commit(&empty[at[P > 1 ? 2 : 0]]);
                     }
                     if (P > 1 || k + 1 == it.k1) {
-                        mma_commit(&accfull[buf]);
+                        commit(&accfull[buf]);
                         buf ^= 1;
                         if (buf == 0) aphase ^= 1;
                     }
                 }
             }
-            mma_commit(done);
+            commit(done);
             mbar_wait_bounded(done, 0, a.timeout_ns);
         }
     } else if (warp >= 4) {
         // ---- accumulators -------------------------------------------------------------
-        const int quad = warp % 4, half = (warp - 4) / 4;
+        const int quad = warp % 4, part = (warp - 4) / 4;  // its rows, its columns
         const uint32_t lanes = uint32_t(quad * 32) << 16;
         int buf = 0;
         unsigned phase = 0;
@@ -365,28 +386,25 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
         auto release = [&]() {
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&accempty[buf]);
+            if (lane == 0) {
+                if (CG > 1)
+                    mbar_arrive_cluster(map_shared_rank(&accempty[buf], 0));
+                else
+                    mbar_arrive(&accempty[buf]);
+            }
             buf ^= 1;
             if (buf == 0) phase ^= 1;
         };
-        // the warp's room, and what goes through it
+        // the warp's room: dy behind da and du where there are three
         unsigned char *room = rooms + (warp - 4) * C::ROOM;
         unsigned char *dyroom = room + (P == 1 && MODE == G_GRAD ? 4096 : 0);
         const bool leader = elect_one();
-        unsigned dyphase = 0;
-        int64_t dyissued[2] = {-1, -1};  // the last item whose chunk is under way or there
-        // a column of a row of unaligned arrays
-        auto place = [](int r, int c) { return P > 1 ? r * 32 + (c ^ r) : r * 34 + c; };
-        constexpr int W = P > 1 ? 1 : 2;
-        auto dy_ahead = [&](int64_t i, int j) {
-            if (i >= items) return;
-            const Item it(a, i, tiles);
-            uint64_t *bar = &dybar[2 * (warp - 4) + j];
-            mbar_arrive_expect_tx(bar, 2048);
-            tma_load_3d(dyroom + j * 2048, &maps.dy, it.n * (BN / 2) + C::column(half, j),
-                        it.m * BM + quad * 32, 0, bar);
-            dyissued[j] = i;
+        // Where column c of row r of an unaligned array is, so that neither the lanes of a
+        // row nor those of a column meet in a bank.
+        auto place = [](int r, int c) {
+            return P > 1 ? r * 32 + (c ^ r) : r * 32 + ((((c >> 1) ^ (r >> 1)) << 1) | (c & 1));
         };
+        constexpr int W = P > 1 ? 1 : 2;
         auto rows_in = [&](T *to, const T *from, int64_t r0, int c0) {
             T v[32];  // (all loads before the first store)
             from += r0 * a.N + c0 + lane;
@@ -406,18 +424,23 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
             for (int r = 0; r < 32; ++r, to += a.N)
                 if (r < rows) *to = v[r];
         };
-        auto own_row = [&](const T *p, float *v) {
-#pragma unroll
-            for (int c = 0; c < 32; c += W) Vec<T, W>::load(p + place(lane, c), v + c);
-        };
-        auto set_row = [&](T *p, const float *v) {
-#pragma unroll
-            for (int c = 0; c < 32; c += W) Vec<T, W>::store(p + place(lane, c), v + c);
-        };
+        // the warp's tile of an item
+        auto tile_row = [&](const Item &it) { return it.m * C::M + rank * BM + quad * 32; };
+        auto tile_column = [&](const Item &it) { return it.n * (BN / 2) + part * CH; };
+        // dy is copied a tile ahead
         constexpr bool AHEAD = MODE == G_GRAD && C::STAGED && P == 1;
-        if (AHEAD && a.dvec && leader)
-            for (int j = 0; j < C::NL / 2 / CH; ++j) dy_ahead(blockIdx.x, j);
-        for (int64_t i = blockIdx.x; i < items; i += gridDim.x) {
+        uint64_t *mydy = &dybar[warp - 4];
+        unsigned dyphase = 0;
+        bool dyahead = false;  // under way
+        auto dy_ahead = [&](int i) {
+            dyahead = i < items;
+            if (!dyahead) return;
+            const Item it(a, i, tiles);
+            mbar_arrive_expect_tx(mydy, 2048);
+            tma_load_3d(dyroom, &maps.dy, tile_column(it), tile_row(it), 0, mydy);
+        };
+        if (AHEAD && a.dvec && leader) dy_ahead(first);
+        for (int i = first; i < items; i += step) {
             const Item it(a, i, tiles);
             float sum[P == 1 ? 1 : C::NL];
             if (P > 1) {
@@ -425,8 +448,7 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                     if (leader) bulk_wait_read_all();
                     __syncwarp();
                     rows_in(reinterpret_cast<T *>(dyroom), static_cast<const T *>(a.dy),
-                            int64_t(it.m) * BM + quad * 32,
-                            it.n * (BN / 2) + C::column(half, 0));
+                            tile_row(it), tile_column(it));
                 }
 #pragma unroll
                 for (int c = 0; c < (P == 1 ? 1 : C::NL); ++c) sum[c] = 0.0f;
@@ -436,7 +458,10 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
 #pragma unroll
                     for (int j = 0; j < C::NL / CH; ++j) {
                         float v[CH];
-                        tmem_load<CH>(tmem + lanes + buf * BN + C::column(half, j), v);
+                        tmem_load<CH>(tmem + lanes + buf * BN +
+                                          (C::PAIR ? j * (BN / 2) + part * CH
+                                                   : part * C::NL + j * CH),
+                                      v);
 #pragma unroll
                         for (int c = 0; c < CH; ++c) sum[(P == 1 ? 0 : j * CH + c)] += v[c];
                     }
@@ -444,59 +469,76 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                 }
                 if (!ok) break;
             }
-            // chunk j of the thread's columns
-            auto get = [&](int j, float (&v)[CH]) {
-                if (P == 1) {
-                    tmem_load<CH>(tmem + lanes + buf * BN + C::column(half, j), v);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < CH; ++c) v[c] = sum[P == 1 ? 0 : j * CH + c];
-                }
-            };
             if constexpr (C::PAIR) {
-                constexpr int n = C::NL / 2 / CH;
-                static_assert(P == 1 || n == 1, "one chunk of dy");
-                const int64_t row0 = int64_t(it.m) * BM + quad * 32, row = row0 + lane;
+                constexpr int SUB = C::EWARPS == 16 ? 16 : CH;  // units at a time
+                const int64_t row0 = tile_row(it), row = row0 + lane;
+                const int c0 = tile_column(it), left = row < a.M ? a.N - c0 : 0;
+                const bool live = row0 < a.M && c0 < a.N;  // the warp has something to write
+                const T *dysrc = static_cast<const T *>(a.dy);
+                uint4 dyraw[AHEAD ? 4 : 1];  // the thread's 32 units of dy
+                if constexpr (AHEAD) {
+                    if (a.dvec) {
+                        if (!(ok = __all_sync(0xffffffffu, await(mydy, dyphase)))) break;
+                        dyphase ^= 1;
+                        dyahead = false;
 #pragma unroll
-                for (int j = 0; j < n; ++j) {
-                    const int c0 = it.n * (BN / 2) + C::column(half, j);
-                    const int left = row < a.M ? a.N - c0 : 0;
-                    const bool live = row0 < a.M && c0 < a.N;  // the warp has something to write
-                    float dy[MODE == G_GRAD ? CH : 1];
+                        for (int c = 0; c < 4; ++c)
+                            dyraw[c] = *reinterpret_cast<const uint4 *>(row_part(dyroom, lane, c));
+                        __syncwarp();
+                        if (leader) dy_ahead(i + step);
+                    } else {
+                        rows_in(reinterpret_cast<T *>(dyroom), dysrc, row0, c0);
+                        __syncwarp();
+#pragma unroll
+                        for (int c = 0; c < 16; ++c)
+                            (&dyraw[c / 4].x)[c % 4] = *reinterpret_cast<const uint32_t *>(
+                                reinterpret_cast<const T *>(dyroom) + place(lane, 2 * c));
+                        __syncwarp();
+                    }
+                }
+                if (P == 1) {
+                    if (!(ok = wait())) break;
+                    tc_fence_after();
+                }
+                if (C::STAGED) {
+                    if (P == 1 && leader) bulk_wait_read_all();  // the room is free
+                    __syncwarp();
+                }
+#pragma unroll
+                for (int h = 0; h < CH / SUB; ++h) {
+                    const int o = h * SUB;  // of the warp's units
+                    float dy[MODE == G_GRAD ? SUB : 1], g[SUB], u[SUB];
                     if constexpr (MODE == G_GRAD) {
-                        const T *src = static_cast<const T *>(a.dy);
-                        if (!C::STAGED) {
-                            take<T, CH>(src + row * a.N + c0, dy, left, a.dvec);
-                        } else if (P == 1 && a.dvec) {
-                            if (!(ok = __all_sync(0xffffffffu,
-                                                  await(&dybar[2 * (warp - 4) + j], dyphase))))
-                                break;
-                            get_row(dyroom + j * 2048, lane, dy);
-                            __syncwarp();
-                            if (leader) dy_ahead(i + gridDim.x, j);
+                        const T *mine = reinterpret_cast<const T *>(dyroom);
+                        if constexpr (!C::STAGED) {
+                            take<T, SUB>(dysrc + row * a.N + c0, dy, left, a.dvec);
+                        } else if constexpr (AHEAD) {
+#pragma unroll
+                            for (int c = 0; c < SUB / 8; ++c)
+                                Vec<bf16, 8>::load(
+                                    reinterpret_cast<const bf16 *>(&dyraw[o / 8 + c]), dy + 8 * c);
                         } else {
-                            if (P == 1) rows_in(reinterpret_cast<T *>(dyroom), src, row0, c0);
-                            __syncwarp();
-                            own_row(reinterpret_cast<const T *>(dyroom), dy);
-                            __syncwarp();
+#pragma unroll
+                            for (int c = 0; c < SUB; ++c) dy[c] = float(mine[place(lane, o + c)]);
                         }
                     }
-                    if (P == 1 && j == 0) {
-                        if (!(ok = wait())) break;
-                        tc_fence_after();
+                    if (P == 1) {
+                        tmem_load<SUB>(tmem + lanes + buf * BN + part * CH + o, g);
+                        tmem_load<SUB>(tmem + lanes + buf * BN + BN / 2 + part * CH + o, u);
+                        if (o + SUB == CH) release();
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < SUB; ++c)
+                            g[c] = sum[P == 1 ? 0 : o + c], u[c] = sum[P == 1 ? 0 : CH + o + c];
                     }
-                    float g[CH], u[CH];
-                    get(j, g);
-                    get(n + j, u);
-                    if (P == 1 && j == n - 1) release();
                     if (a.bg != nullptr) {
-                        float bg = 0.0f, bu = 0.0f;  // of column c0 + lane
-                        if (lane < CH && c0 + lane < a.N) {
-                            Vec<T, 1>::load(static_cast<const T *>(a.bg) + c0 + lane, &bg);
-                            Vec<T, 1>::load(static_cast<const T *>(a.bu) + c0 + lane, &bu);
+                        float bg = 0.0f, bu = 0.0f;  // of unit lane
+                        if (lane < SUB && c0 + o + lane < a.N) {
+                            Vec<T, 1>::load(static_cast<const T *>(a.bg) + c0 + o + lane, &bg);
+                            Vec<T, 1>::load(static_cast<const T *>(a.bu) + c0 + o + lane, &bu);
                         }
 #pragma unroll
-                        for (int c = 0; c < CH; ++c) {
+                        for (int c = 0; c < SUB; ++c) {
                             g[c] += __shfl_sync(0xffffffffu, bg, c);
                             u[c] += __shfl_sync(0xffffffffu, bu, c);
                         }
@@ -504,32 +546,22 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                     if constexpr (MODE == G_FWD) {
                         act_switch(a.act, [&](auto act) {
 #pragma unroll
-                            for (int c = 0; c < CH; ++c)
+                            for (int c = 0; c < SUB; ++c)
                                 g[c] = act_value<act.value, P == 1>(g[c]) * u[c];
                         });
-                        T *out = static_cast<T *>(a.out);
-                        if (!C::STAGED) {
-                            put<T, CH>(out + row * a.N + c0, g, left, a.vec);
-                        } else if (P == 1 && a.vec) {
-                            if (leader) bulk_wait_read_all();  // the room is free
-                            __syncwarp();
-                            put_row(room, lane, g);
-                            fence_proxy_async_smem();
-                            __syncwarp();
-                            if (leader && live) {
-                                tma_store_3d(&maps.o0, room, c0, int(row0), 0);
-                                bulk_commit();
-                            }
-                        } else {
-                            set_row(reinterpret_cast<T *>(room), g);
-                            __syncwarp();
-                            rows_out(out, reinterpret_cast<const T *>(room), row0, c0);
-                            __syncwarp();
-                        }
+                        if (!C::STAGED)
+                            put<T, SUB>(static_cast<T *>(a.out) + row * a.N + c0, g, left, a.vec);
+                        else if (P == 1 && a.vec)
+                            put_row<SUB>(room, lane, o, g);
+                        else
+#pragma unroll
+                            for (int c = 0; c < SUB; c += W)
+                                Vec<T, W>::store(reinterpret_cast<T *>(room) + place(lane, o + c),
+                                                 g + c);
                     } else {
                         act_switch(a.act, [&](auto act) {
 #pragma unroll
-                            for (int c = 0; c < CH; ++c) {
+                            for (int c = 0; c < SUB; ++c) {
                                 float slope;
                                 const float f = act_both<act.value, P == 1>(g[c], slope);
                                 g[c] = dy[c] * u[c] * slope;
@@ -537,50 +569,73 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                             }
                         });
                         if (a.bpart != nullptr) {  // (before they are rounded)
-                            const float sg = column_sums<CH>(g, lane);
-                            const float su = column_sums<CH>(u, lane);
-                            float *o = a.bpart + (int64_t(it.m) * 4 + quad) * 2 * a.N + c0 + lane;
-                            if (lane < CH && c0 + lane < a.N) o[0] = sg, o[a.N] = su;
+                            const float sg = column_sums<SUB>(g, lane);
+                            const float su = column_sums<SUB>(u, lane);
+                            float *to = a.bpart +
+                                        ((int64_t(it.m) * CG + rank) * 4 + quad) * 2 * a.N + c0 +
+                                        o + lane;
+                            if (lane < SUB && c0 + o + lane < a.N) to[0] = sg, to[a.N] = su;
                         }
-                        if constexpr (C::STAGED) {
+                        if constexpr (!C::STAGED) {
+                            const int64_t plane = a.M * a.ld;
+                            bf16 *to = a.d + row * a.ld + c0;
 #pragma unroll
-                            for (int part = 0; part < P; ++part) {
-                                if (leader) bulk_wait_read_all();
-                                __syncwarp();
-                                put_row(room, lane, g);
-                                put_row(room + 2048, lane, u);
+                            for (int c = 0; c < SUB; c += 8)
+                                if (c < left) {  // (the rows' padding takes zeros)
+                                    put_parts<P>(to + c, plane, g + c);
+                                    put_parts<P>(to + P * plane + c, plane, u + c);
+                                }
+                        } else if constexpr (P == 1) {
+                            put_row<SUB>(room, lane, o, g);
+                            put_row<SUB>(room + 2048, lane, o, u);
+                        } else {
+                            // three parts, one after the other through the room
+                            __syncwarp();
+#pragma unroll
+                            for (int k = 0; k < P; ++k) {
+                                if (k > 0) {
+                                    if (leader) bulk_wait_read_all();
+                                    __syncwarp();
+                                }
+                                put_row<SUB>(room, lane, 0, g);
+                                put_row<SUB>(room + 2048, lane, 0, u);
                                 fence_proxy_async_smem();
                                 __syncwarp();
                                 if (leader && live) {
-                                    tma_store_3d(&maps.o0, room, c0, int(row0), part);
-                                    tma_store_3d(&maps.o1, room + 2048, c0, int(row0), part);
+                                    tma_store_3d(&maps.o0, room, c0, int(row0), k);
+                                    tma_store_3d(&maps.o1, room + 2048, c0, int(row0), k);
                                     bulk_commit();
                                 }
-                                if (part + 1 < P)
 #pragma unroll
-                                    for (int c = 0; c < CH; ++c)
-                                        g[c] = rest<bf16>(g[c]), u[c] = rest<bf16>(u[c]);
+                                for (int c = 0; c < SUB; ++c)
+                                    g[c] = rest<bf16>(g[c]), u[c] = rest<bf16>(u[c]);
                             }
-                        } else {
-                            const int64_t plane = a.M * a.ld;
-                            bf16 *at = a.d + row * a.ld + c0;
-#pragma unroll
-                            for (int c = 0; c < CH; c += 8)
-                                if (c < left) {  // (the rows' padding takes zeros)
-                                    put_parts<P>(at + c, plane, g + c);
-                                    put_parts<P>(at + P * plane + c, plane, u + c);
-                                }
                         }
                     }
                 }
-                if (!ok) break;
-                dyphase ^= 1;
+                if constexpr (C::STAGED && (P == 1 || MODE == G_FWD)) {
+                    if (MODE == G_GRAD || (P == 1 && a.vec)) {
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (leader && live) {
+                            tma_store_3d(&maps.o0, room, c0, int(row0), 0);
+                            if (MODE == G_GRAD)
+                                tma_store_3d(&maps.o1, room + 2048, c0, int(row0), 0);
+                            bulk_commit();
+                        }
+                    } else {
+                        __syncwarp();
+                        rows_out(static_cast<T *>(a.out), reinterpret_cast<const T *>(room), row0,
+                                 c0);
+                        __syncwarp();
+                    }
+                }
             } else {
                 constexpr int n = C::NL / CH;
                 const int dw_mt = a.mt / 2;
                 const bool up = MODE == G_DW && it.m >= dw_mt;
                 const int64_t row =
-                    int64_t(up ? it.m - dw_mt : it.m) * BM + quad * 32 + lane;
+                    int64_t(up ? it.m - dw_mt : it.m) * C::M + rank * BM + quad * 32 + lane;
                 if (P == 1) {
                     if (!(ok = wait())) break;
                     tc_fence_after();
@@ -588,9 +643,14 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
 #pragma unroll
                 for (int j = 0; j < n; ++j) {
                     float v[CH];
-                    get(j, v);
-                    if (P == 1 && j == n - 1) release();
-                    const int c0 = it.n * BN + C::column(half, j);
+                    if (P == 1) {
+                        tmem_load<CH>(tmem + lanes + buf * BN + part * C::NL + j * CH, v);
+                        if (j == n - 1) release();
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < CH; ++c) v[c] = sum[P == 1 ? 0 : j * CH + c];
+                    }
+                    const int c0 = it.n * BN + part * C::NL + j * CH;
                     const int left = row < a.M ? a.N - c0 : 0;
                     if (a.nsplit > 1) {
                         const int64_t all = MODE == G_DW ? 2 * a.M : a.M;
@@ -605,19 +665,15 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
         }
         // nothing is in flight when the block ends
         if (leader) bulk_wait_read_all();
-        if (AHEAD && !ok && leader)
-            for (int j = 0; j < 2; ++j)
-                if (dyissued[j] >= 0)
-                    mbar_wait_bounded(&dybar[2 * (warp - 4) + j],
-                                      unsigned((dyissued[j] - blockIdx.x) / gridDim.x) & 1,
-                                      a.timeout_ns);
+        if (AHEAD && dyahead && !ok) mbar_wait_bounded(mydy, dyphase, a.timeout_ns);
     }
     __syncwarp();
     tc_fence_before();
     __syncthreads();
+    if (CG > 1) cluster_sync_all();  // neither block's memory is in use any more
     if (warp == 2) {
         tc_fence_after();
-        tmem_free(tmem, C::COLS);
+        tmem_free<CG>(tmem, C::COLS);
     }
 }
 
@@ -746,52 +802,78 @@ struct Scratch {
 // forward, 600 + 30 for the gradients, 500 + 8 for plain results.  Parts cost their
 // writes and reads and a launch.
 struct GemmPlan {
-    int BN = 0, nsplit = 1;
+    int BN = 0, CG = 1, nsplit = 1;
+    int rows() const { return BM * CG; }
 };
-GemmPlan plan_gemm(int sms, int mode, int P, int64_t M, int64_t N, int64_t mtiles, int64_t kb) {
+GemmPlan plan_gemm(int sms, int mode, int P, int64_t M, int64_t N, int64_t kb) {
     GemmPlan best;
     double least = 1e300;
     const bool pair = mode == G_FWD || mode == G_GRAD;
-    for (int BN = P == 1 ? 256 : 128; BN >= 64; BN /= 2) {
-        const int64_t tiles = mtiles * ceil_div(N, pair ? BN / 2 : BN);
-        const double stage = (P == 1 ? 1.0 : 6.7) * (BN == 256 ? 708 : BN == 128 ? 385 : 277);
+    const char *force = getenv("PCBN");
+    for (int kind = 0; kind < 4; ++kind) {
+        const int CG = kind < 2 ? 2 : 1, BN = kind == 0 ? 256 : kind < 3 ? 128 : 64;
+        if (P > 1 && BN == 256) continue;
+        if (force && (P > 1 && atoi(force) == 0 ? 1 : atoi(force)) != kind) continue;
+        const double stage = (P == 1 ? 1.0 : 6.7) *
+                             (kind == 0 ? 560 : kind == 1 ? 300 : kind == 2 ? 385 : 277);
+        const int64_t tall = BM * CG;
+        const int64_t mtiles = mode == G_DW ? 2 * ceil_div(M / 2, tall) : ceil_div(M, tall);
+        const int64_t tiles = mtiles * ceil_div(N, pair ? BN / 2 : BN), units = sms / CG;
         const double epilogue = mode == G_FWD    ? 1500 + 14.0 * BN
                                 : mode == G_GRAD ? 600 + 30.0 * BN
                                                  : 500 + 8.0 * BN;
         // (a part has a row of a chain's length at most in bfloat16)
-        const int64_t first = !pair && P == 1 ? ceil_div(kb * BK, CHAIN) : 1;
+        const int64_t least_parts = !pair && P == 1 ? ceil_div(kb * BK, CHAIN) : 1;
         const int64_t most = pair ? 1 : kb < 64 ? kb : 64;
-        for (int64_t ns = first; ns <= (most > first ? most : first); ++ns) {
+        for (int64_t ns = least_parts; ns <= (most > least_parts ? most : least_parts); ++ns) {
             const double k = double(ceil_div(kb, ns));
             const double item = k * stage > epilogue ? k * stage : epilogue;
-            double cost = double(ceil_div(tiles * ns, sms)) * item + epilogue + 1500;
+            double cost = double(ceil_div(tiles * ns, units)) * item + epilogue + 1500 * CG;
             if (ns > 1) cost += 6000 + 8.0 * double(ns) * double(M) * double(N) / 3000;
-            if (cost < least) least = cost, best.BN = BN, best.nsplit = int(ns);
+            if (cost < least) least = cost, best.BN = BN, best.CG = CG, best.nsplit = int(ns);
         }
     }
     return best;
 }
 
-template <int MODE, int P, int BN>
+template <int MODE, int P, int BN, int CG>
 cudaError_t run_gemm(const DeviceInfo &dev, const GemmMaps &maps, const GemmArgs &g,
                      cudaStream_t st) {
-    using C = GCfg<MODE, P, BN>;
+    using C = GCfg<MODE, P, BN, CG>;
     static std::atomic<uint64_t> done{0};
-    const cudaError_t e =
-        allow_smem(gated_gemm_kernel<MODE, P, BN>, int(C::SMEM), dev.device, done);
+    cudaError_t e =
+        allow_smem(gated_gemm_kernel<MODE, P, BN, CG>, int(C::SMEM), dev.device, done);
     if (e != cudaSuccess) return e;
-    const int64_t items = int64_t(g.mt) * g.nt * g.nsplit;
-    const unsigned blocks = unsigned(items < dev.sm_count ? items : dev.sm_count);
-    gated_gemm_kernel<MODE, P, BN><<<blocks, C::THREADS, C::SMEM, st>>>(maps, g);
-    return cudaGetLastError();
+    const int64_t items = int64_t(g.mt) * g.nt * g.nsplit, units = dev.sm_count / CG;
+    if (items > (int64_t(1) << 30)) return cudaErrorInvalidConfiguration;
+    const unsigned blocks = unsigned(items < units ? items : units) * CG;
+    if (CG == 1) {
+        gated_gemm_kernel<MODE, P, BN, CG><<<blocks, C::THREADS, C::SMEM, st>>>(maps, g);
+        return cudaGetLastError();
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(C::THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = CG;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, gated_gemm_kernel<MODE, P, BN, CG>, maps, g);
 }
 template <int MODE, int P>
-cudaError_t run_gemm(const DeviceInfo &dev, const GemmMaps &maps, const GemmArgs &g, int BN,
-                     cudaStream_t st) {
-    if constexpr (P == 1)
-        if (BN == 256) return run_gemm<MODE, P, 256>(dev, maps, g, st);
-    return BN == 128 ? run_gemm<MODE, P, 128>(dev, maps, g, st)
-                     : run_gemm<MODE, P, 64>(dev, maps, g, st);
+cudaError_t run_gemm(const DeviceInfo &dev, const GemmMaps &maps, const GemmArgs &g,
+                     const GemmPlan &p, cudaStream_t st) {
+    if (p.CG == 2) {
+        if constexpr (P == 1)
+            if (p.BN == 256) return run_gemm<MODE, P, 256, 2>(dev, maps, g, st);
+        return run_gemm<MODE, P, 128, 2>(dev, maps, g, st);
+    }
+    return p.BN == 128 ? run_gemm<MODE, P, 128, 1>(dev, maps, g, st)
+                       : run_gemm<MODE, P, 64, 1>(dev, maps, g, st);
 }
 
 template <class T>
@@ -862,8 +944,8 @@ GemmArgs gemm_args(const DeviceInfo &dev, const GatedArgs &a) {
 struct BackwardPlan {
     Scratch s;
     Inputs in;
-    int ld = 0, mt = 0, ft = 0, kf = 0, kr = 0;
-    GemmPlan px, pw;
+    int ld = 0, kf = 0, kr = 0;
+    GemmPlan pg, px, pw;
     size_t d_at = 0, part_x = 0, part_w = 0, part_b = 0;
 };
 template <class T, int P>
@@ -872,19 +954,21 @@ BackwardPlan plan_backward(const DeviceInfo &dev, const GatedArgs &a) {
     plan_inputs<T, P>(a, b.in, b.s);
     b.ld = pad8(a.F);
     b.d_at = b.s.take(size_t(2) * P * a.rows * b.ld * sizeof(bf16));
-    b.mt = int(ceil_div(a.rows, BM)), b.ft = int(ceil_div(a.F, BM));
+    b.pg = plan_gemm(dev.sm_count, G_GRAD, P, a.rows, a.F, ceil_div(a.C, BK));
     b.kf = int(ceil_div(a.F, BK)), b.kr = int(ceil_div(a.rows, BK));
     if (a.dx) {
-        b.px = plan_gemm(dev.sm_count, G_DX, P, a.rows, a.C, b.mt, 2 * b.kf);
+        b.px = plan_gemm(dev.sm_count, G_DX, P, a.rows, a.C, 2 * b.kf);
         if (b.px.nsplit > 1)
             b.part_x = b.s.take(size_t(b.px.nsplit) * a.rows * a.C * sizeof(float));
     }
     if (a.dwg) {
-        b.pw = plan_gemm(dev.sm_count, G_DW, P, 2 * a.F, a.C, 2 * b.ft, b.kr);
+        b.pw = plan_gemm(dev.sm_count, G_DW, P, 2 * int64_t(a.F), a.C, b.kr);
         if (b.pw.nsplit > 1)
             b.part_w = b.s.take(size_t(b.pw.nsplit) * 2 * a.F * a.C * sizeof(float));
     }
-    if (a.dbg) b.part_b = b.s.take(size_t(b.mt) * 4 * 2 * a.F * sizeof(float));
+    if (a.dbg)
+        b.part_b = b.s.take(size_t(ceil_div(a.rows, b.pg.rows())) * b.pg.CG * 4 * 2 * a.F *
+                            sizeof(float));
     return b;
 }
 
@@ -921,15 +1005,15 @@ cudaError_t forward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st) 
     if (e == cudaSuccess) {
         GemmArgs g = gemm_args(dev, a);
         g.M = a.rows, g.N = a.F, g.kb = int(ceil_div(a.C, BK)), g.kb0 = g.kb;
-        g.mt = int(ceil_div(a.rows, BM));
-        const GemmPlan p = plan_gemm(dev.sm_count, G_FWD, P, g.M, g.N, g.mt, g.kb);
+        const GemmPlan p = plan_gemm(dev.sm_count, G_FWD, P, g.M, g.N, g.kb);
+        g.mt = int(ceil_div(a.rows, p.rows()));
         g.nt = int(ceil_div(a.F, p.BN / 2));
         g.out = a.y, g.vec = a.F % (16 / sizeof(T)) == 0 && aligned16(a.y);
         GemmMaps m{};
         const bool ok = make_map3(&m.a0, in.x, BM) && make_map3(&m.b0, in.wg, p.BN / 2) &&
                         make_map3(&m.b1, in.wu, p.BN / 2) &&
                         (P > 1 || !g.vec || make_tile_map(&m.o0, a.y, a.rows, a.F, a.F));
-        e = ok ? run_gemm<G_FWD, P>(dev, m, g, p.BN, st) : cudaErrorInvalidValue;
+        e = ok ? run_gemm<G_FWD, P>(dev, m, g, p, st) : cudaErrorInvalidValue;
     }
     return memory.give(e);
 }
@@ -939,8 +1023,8 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
     BackwardPlan b = plan_backward<T, P>(dev, a);
     Scratch &s = b.s;
     Inputs &in = b.in;
-    const int ld = b.ld, mt = b.mt, ft = b.ft, kf = b.kf, kr = b.kr;
-    const GemmPlan px = b.px, pw = b.pw;
+    const int ld = b.ld, kf = b.kf, kr = b.kr;
+    const GemmPlan p = b.pg, px = b.px, pw = b.pw;
     const size_t part_x = b.part_x, part_w = b.part_w, part_b = b.part_b;
     Memory memory{st};
     cudaError_t e = memory.take(dev, s, a);
@@ -954,8 +1038,8 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
     auto partials = [&](size_t at) { return reinterpret_cast<float *>(s.base + at); };
     if (e == cudaSuccess) {
         GemmArgs g = gemm_args(dev, a);
-        g.M = a.rows, g.N = a.F, g.kb = int(ceil_div(a.C, BK)), g.kb0 = g.kb, g.mt = mt;
-        const GemmPlan p = plan_gemm(dev.sm_count, G_GRAD, P, g.M, g.N, g.mt, g.kb);
+        g.M = a.rows, g.N = a.F, g.kb = int(ceil_div(a.C, BK)), g.kb0 = g.kb;
+        g.mt = int(ceil_div(a.rows, p.rows()));
         g.nt = int(ceil_div(a.F, p.BN / 2));
         g.d = const_cast<bf16 *>(d[0].p), g.ld = ld;
         g.dvec = a.F % (16 / sizeof(T)) == 0 && aligned16(a.dy);
@@ -966,11 +1050,12 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
                         make_map3(&m.b1, in.wu, p.BN / 2) &&
                         make_map3(&m.o0, d[0], 32, 32) && make_map3(&m.o1, d[1], 32, 32) &&
                         (P > 1 || !g.dvec || make_tile_map(&m.dy, a.dy, a.rows, a.F, a.F));
-        e = ok ? run_gemm<G_GRAD, P>(dev, m, g, p.BN, st) : cudaErrorInvalidValue;
+        e = ok ? run_gemm<G_GRAD, P>(dev, m, g, p, st) : cudaErrorInvalidValue;
     }
     if (e == cudaSuccess && a.dx) {
         GemmArgs g = gemm_args(dev, a);
-        g.M = a.rows, g.N = a.C, g.kb0 = kf, g.kb = 2 * kf, g.mt = mt;
+        g.M = a.rows, g.N = a.C, g.kb0 = kf, g.kb = 2 * kf;
+        g.mt = int(ceil_div(a.rows, px.rows()));
         g.nt = int(ceil_div(a.C, px.BN)), g.nsplit = px.nsplit;
         g.out = a.dx, g.vec = a.C % (16 / sizeof(T)) == 0 && aligned16(a.dx);
         g.part = partials(part_x);
@@ -978,13 +1063,14 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
         const bool ok = make_map3(&m.a0, d[0], BM) &&
                         make_map3(&m.a1, d[1], BM) &&
                         make_map3(&m.b0, in.wg, 64) && make_map3(&m.b1, in.wu, 64);
-        e = ok ? run_gemm<G_DX, P>(dev, m, g, px.BN, st) : cudaErrorInvalidValue;
+        e = ok ? run_gemm<G_DX, P>(dev, m, g, px, st) : cudaErrorInvalidValue;
         if (e == cudaSuccess && g.nsplit > 1)
             e = join<T>(g.part, g.nsplit, a.rows * a.C, a.rows * a.C, a.dx, nullptr, st);
     }
     if (e == cudaSuccess && a.dwg) {
         GemmArgs g = gemm_args(dev, a);
-        g.M = a.F, g.N = a.C, g.kb = kr, g.kb0 = kr, g.mt = 2 * ft;
+        g.M = a.F, g.N = a.C, g.kb = kr, g.kb0 = kr;
+        g.mt = 2 * int(ceil_div(a.F, pw.rows()));
         g.nt = int(ceil_div(a.C, pw.BN)), g.nsplit = pw.nsplit;
         g.out = a.dwg, g.out2 = a.dwu;
         g.vec = a.C % (16 / sizeof(T)) == 0 && aligned16(a.dwg) && aligned16(a.dwu);
@@ -992,14 +1078,14 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
         GemmMaps m{};
         const bool ok = make_map3(&m.a0, d[0], 64) && make_map3(&m.a1, d[1], 64) &&
                         make_map3(&m.b0, in.x, 64);
-        e = ok ? run_gemm<G_DW, P>(dev, m, g, pw.BN, st) : cudaErrorInvalidValue;
+        e = ok ? run_gemm<G_DW, P>(dev, m, g, pw, st) : cudaErrorInvalidValue;
         const int64_t n = int64_t(a.F) * a.C;
         if (e == cudaSuccess && g.nsplit > 1)
             e = join<T>(g.part, g.nsplit, 2 * n, n, a.dwg, a.dwu, st);
     }
     if (e == cudaSuccess && a.dbg) {
         gated_bias_kernel<T><<<unsigned(ceil_div(2 * a.F, 32)), dim3(32, 32), 0, st>>>(
-            partials(part_b), 4 * mt, a.F, static_cast<T *>(a.dbg), static_cast<T *>(a.dbu));
+            partials(part_b), int(4 * p.CG * ceil_div(a.rows, p.rows())), a.F, static_cast<T *>(a.dbg), static_cast<T *>(a.dbu));
         e = cudaGetLastError();
     }
     return memory.give(e);

@@ -12,17 +12,32 @@ namespace pcn {
 
 // --- tensor memory ------------------------------------------------------------
 
-// Whole warp.  `ncols` a power of two, 32..512; the address lands in *slot.
+// Whole warp.  `ncols` a power of two, 32..512; the address lands in *slot.  CG: the
+// blocks of a product, 1, or 2 that are a cluster (then a warp in each calls this).
+template <int CG = 1>
 __device__ __forceinline__ void tmem_alloc(uint32_t *slot, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                     smem_u32(slot)),
-                 "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    if (CG == 1) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(slot)),
+                     "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                         smem_u32(slot)),
+                     "r"(ncols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    }
 }
+template <int CG = 1>
 __device__ __forceinline__ void tmem_free(uint32_t addr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr),
-                 "r"(ncols));
+    if (CG == 1)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(addr),
+                     "r"(ncols));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(addr),
+                     "r"(ncols));
 }
 
 // 32 columns of this warp's 32 lanes: register c holds column c of the
@@ -108,11 +123,12 @@ __device__ __forceinline__ uint32_t smem_operand(uint32_t addr, uint32_t lead = 
 constexpr uint32_t SMEM_128B = (1024 >> 4) | (1u << 14) | (2u << 29);
 constexpr uint32_t SMEM_64B = (512 >> 4) | (1u << 14) | (4u << 29);
 
-// bfloat16 x bfloat16 -> float32, M = 128.  `b_rows`: B's contraction runs
-// over its rows (MN-major) instead of along them; `a_rows`: A's.
-__host__ __device__ constexpr uint32_t mma_idesc(int N, bool b_rows, bool a_rows = false) {
+// bfloat16 x bfloat16 -> float32, M = 128, or 256 of two blocks.  `b_rows`: B's
+// contraction runs over its rows (MN-major) instead of along them; `a_rows`: A's.
+__host__ __device__ constexpr uint32_t mma_idesc(int N, bool b_rows, bool a_rows = false,
+                                                 int M = 128) {
     return (1u << 4) | (1u << 7) | (1u << 10) | (a_rows ? 1u << 15 : 0u) |
-           (b_rows ? 1u << 16 : 0u) | (uint32_t(N / 8) << 17) | (uint32_t(128 / 16) << 24);
+           (b_rows ? 1u << 16 : 0u) | (uint32_t(N / 8) << 17) | (uint32_t(M / 16) << 24);
 }
 
 // One thread.  D (tensor memory) = A B + (accumulate ? D : 0), 16 deep; A and B
@@ -140,6 +156,29 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint3
         "r"(a), "r"(b), "r"(idesc), "r"(uint32_t(accumulate)), "n"(HI)
         : "memory");
 }
+// The same of two blocks, by a thread of the cluster's first: each has half the rows of
+// A and of D and half of B's, at the same addresses.
+template <uint32_t HI>
+__device__ __forceinline__ void mma_ss_pair(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                            bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 ra, rb;\n\t"
+        "mov.b64 ra, {%1, %5};\n\t"
+        "mov.b64 rb, {%2, %5};\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::2.kind::f16 [%0], ra, rb, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(uint32_t(accumulate)), "n"(HI)
+        : "memory");
+}
+// An arrival at `bar` in both blocks when this thread's products of both so far are done.
+__device__ __forceinline__ void mma_commit_pair(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 "
+        "[%0], %1;" ::"r"(smem_u32(bar)),
+        "h"(uint16_t(3))
+        : "memory");
+}
+
 // `bar` completes (one arrival) when this thread's products so far have.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile(
@@ -166,6 +205,23 @@ __device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, i
         "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
         "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
         : "memory");
+}
+
+// For the products of two blocks: to this block's memory, the bytes counted at `bar`, a
+// shared::cluster address in either block.
+__device__ __forceinline__ void tma_load_3d_pair(void *dst, const CUtensorMap *map, int c0, int c1,
+                                                 int c2, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::"
+        "bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
+// An arrival at a barrier of another block of the cluster.  Of this block's work it
+// orders what the tensor cores' own fences order: a release for the whole cluster waits
+// for the thread's stores to global memory, 1000 cycles and more.
+__device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 // Shared to global memory, in the issuing thread's bulk group.  What lies past the
