@@ -40,7 +40,6 @@
 #include "pc_tiles.cuh"
 #include "pointcloud.h"
 
-#include <cstdlib>
 #include <type_traits>
 
 namespace pcn {
@@ -794,13 +793,22 @@ struct Scratch {
     }
 };
 
-// The columns of a tile and the parts of the contraction: the smallest estimate in SM
-// cycles.  Measured per 64 of the depth: 708 cycles with 256 columns, 385 with 128, 277
-// with 64 (32,768 x 8192 x 1024, all SMs; the products alone would be 512, 256 and 192:
-// operand reads and the copies share the memory's 128 bytes a cycle), float32 six times
-// 430 with 128; a tile's epilogue, under the next tile's products, 1500 + 14 a column
-// forward, 600 + 30 for the gradients, 500 + 8 for plain results.  Parts cost their
-// writes and reads and a launch.
+// The kinds of a tile: its columns, and the blocks that share it.
+struct GemmKind {
+    int BN, CG;
+    // SM cycles, measured: 64 of the depth (32,768 x 8192 x 1024 bf16, all SMs; the products
+    // alone take 512, 256, 256 and 192); a tile's epilogue, which runs under the next tile's
+    // products: forward (silu), gradients, plain results; a launch's start and end.
+    double stage, forward, grad, plain, fixed;
+};
+constexpr GemmKind KINDS[] = {{256, 2, 620, 4400, 7000, 2600, 6300},
+                              {128, 2, 350, 2650, 3500, 1500, 6300},
+                              {128, 1, 385, 3000, 4100, 1500, 4200},
+                              {64, 1, 277, 2400, 4100, 1000, 4200}};
+
+// The kind of tile and the parts of the contraction, by the smallest estimate.  float32:
+// six products for one, epilogues three times as long (and no tiles of 256 columns, whose
+// sums a thread could not hold).  Parts cost their writes and reads and a launch.
 struct GemmPlan {
     int BN = 0, CG = 1, nsplit = 1;
     int rows() const { return BM * CG; }
@@ -809,28 +817,26 @@ GemmPlan plan_gemm(int sms, int mode, int P, int64_t M, int64_t N, int64_t kb) {
     GemmPlan best;
     double least = 1e300;
     const bool pair = mode == G_FWD || mode == G_GRAD;
-    const char *force = getenv("PCBN");
-    for (int kind = 0; kind < 4; ++kind) {
-        const int CG = kind < 2 ? 2 : 1, BN = kind == 0 ? 256 : kind < 3 ? 128 : 64;
-        if (P > 1 && BN == 256) continue;
-        if (force && (P > 1 && atoi(force) == 0 ? 1 : atoi(force)) != kind) continue;
-        const double stage = (P == 1 ? 1.0 : 6.7) *
-                             (kind == 0 ? 560 : kind == 1 ? 300 : kind == 2 ? 385 : 277);
-        const int64_t tall = BM * CG;
+    for (const GemmKind &kind : KINDS) {
+        if (P > 1 && kind.BN == 256) continue;
+        const double stage = kind.stage * (P == 1 ? 1.0 : 6.3);
+        const double epilogue = (mode == G_FWD    ? kind.forward
+                                 : mode == G_GRAD ? kind.grad
+                                                  : kind.plain) *
+                                (P == 1 ? 1.0 : 3.0);
+        const int64_t tall = BM * kind.CG, units = sms / kind.CG;
         const int64_t mtiles = mode == G_DW ? 2 * ceil_div(M / 2, tall) : ceil_div(M, tall);
-        const int64_t tiles = mtiles * ceil_div(N, pair ? BN / 2 : BN), units = sms / CG;
-        const double epilogue = mode == G_FWD    ? 1500 + 14.0 * BN
-                                : mode == G_GRAD ? 600 + 30.0 * BN
-                                                 : 500 + 8.0 * BN;
+        const int64_t tiles = mtiles * ceil_div(N, pair ? kind.BN / 2 : kind.BN);
         // (a part has a row of a chain's length at most in bfloat16)
-        const int64_t least_parts = !pair && P == 1 ? ceil_div(kb * BK, CHAIN) : 1;
+        const int64_t fewest = !pair && P == 1 ? ceil_div(kb * BK, CHAIN) : 1;
         const int64_t most = pair ? 1 : kb < 64 ? kb : 64;
-        for (int64_t ns = least_parts; ns <= (most > least_parts ? most : least_parts); ++ns) {
-            const double k = double(ceil_div(kb, ns));
-            const double item = k * stage > epilogue ? k * stage : epilogue;
-            double cost = double(ceil_div(tiles * ns, units)) * item + epilogue + 1500 * CG;
+        for (int64_t ns = fewest; ns <= (most > fewest ? most : fewest); ++ns) {
+            const double k = double(ceil_div(kb, ns)) * stage;
+            double cost = double(ceil_div(tiles * ns, units)) * (k > epilogue ? k : epilogue) +
+                          epilogue + kind.fixed;
             if (ns > 1) cost += 6000 + 8.0 * double(ns) * double(M) * double(N) / 3000;
-            if (cost < least) least = cost, best.BN = BN, best.CG = CG, best.nsplit = int(ns);
+            if (cost < least)
+                least = cost, best.BN = kind.BN, best.CG = kind.CG, best.nsplit = int(ns);
         }
     }
     return best;
