@@ -21,39 +21,60 @@ _ACTIVATIONS = {"none": PC_ACT_NONE, None: PC_ACT_NONE, "silu": PC_ACT_SILU,
 
 
 def _activation(name) -> int:
-    code = _ACTIVATIONS.get(name) if name is None or isinstance(name, str) else None
-    if code is None:
+    try:
+        return _ACTIVATIONS[name]
+    except (KeyError, TypeError):
         raise ValueError("activation must be one of 'none', 'silu', 'gelu', 'relu', 'sigmoid' "
-                         f"(got {name!r})")
-    return code
+                         f"(got {name!r})") from None
+
+
+def _packed(t, name: str, shape, dtype, index: int):
+    """The address of a packed tensor of a given shape, type and device (the short way for
+    what is right; _same says what is wrong)."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape \
+            and t.get_device() == index and t.is_contiguous():
+        return t.data_ptr()
+    return _same(t, name, shape, dtype, index).data_ptr()
+
+
+def _count(shape) -> int:
+    n = 1
+    for k in shape:
+        n *= k
+    return n
 
 
 # --- group norm -------------------------------------------------------------------
 
+def _group_param(t, name: str, x, C: int, index: int):
+    if not isinstance(t, torch.Tensor) or t.shape != (C,) or t.get_device() != index \
+            or not t.is_contiguous() or t.dtype not in (torch.float32, x.dtype):
+        raise ValueError(f"{name} must be a contiguous float32 or {x.dtype} tensor "
+                         f"[{C}] on {x.device}")
+    return t.data_ptr(), t.dtype
+
+
 def _group_args(x, groups, weight, bias, activation, lengths):
     code = _code(x, "x")
-    if x.dim() != 3 or not x.is_contiguous():
-        raise ValueError(f"x must be contiguous [B, L, C] (got {tuple(x.shape)})")
-    B, L, C = x.shape
-    index, pt = x.get_device(), None
+    shape = x.shape
+    if len(shape) != 3 or not x.is_contiguous():
+        raise ValueError(f"x must be contiguous [B, L, C] (got {tuple(shape)})")
+    B, L, C = shape
+    index = x.get_device()
     groups = int(groups)
     if groups < 1 or C % groups:
         raise ValueError(f"groups={groups} must divide the {C} channels")
-    for t, name in ((weight, "weight"), (bias, "bias")):
-        if t is None:
-            continue
-        if not isinstance(t, torch.Tensor) or not t.is_cuda or t.get_device() != index \
-                or t.shape != (C,) or not t.is_contiguous() \
-                or t.dtype not in (torch.float32, x.dtype):
-            raise ValueError(f"{name} must be a contiguous float32 or {x.dtype} tensor "
-                             f"[{C}] on {x.device}")
-        if pt is not None and t.dtype is not pt:
+    pw = pb = wt = bt = None
+    if weight is not None:
+        pw, wt = _group_param(weight, "weight", x, C, index)
+    if bias is not None:
+        pb, bt = _group_param(bias, "bias", x, C, index)
+        if wt is not None and bt is not wt:
             raise ValueError("weight and bias must have the same dtype")
-        pt = t.dtype
-    if lengths is not None:
-        _check_lengths(lengths, B, x.device, "lengths")
-    return (code, index, B, L, C, groups, PC_F32 if pt is None else _DTYPES[pt],
-            _activation(activation))
+    pt = wt or bt
+    pl = None if lengths is None else _check_lengths(lengths, B, x.device, "lengths").data_ptr()
+    return (code, index, B, L, C, groups, pw, pb, PC_F32 if pt is None else _DTYPES[pt],
+            _activation(activation), pl)
 
 
 def pc_group_norm(x: torch.Tensor, groups: int, weight: torch.Tensor | None = None,
@@ -68,20 +89,21 @@ def pc_group_norm(x: torch.Tensor, groups: int, weight: torch.Tensor | None = No
     Only the first ``lengths[b]`` points count ([B] int64); what lies past them
     is not read into any result, and y is 0 there.
     """
-    code, index, B, L, C, groups, pcode, act = _group_args(x, groups, weight, bias, activation,
-                                                           lengths)
+    code, index, B, L, C, groups, pw, pb, pcode, act, pl = _group_args(
+        x, groups, weight, bias, activation, lengths)
     if out is None:
         out = torch.empty_like(x)
     else:
         _same(out, "out", x.shape, x.dtype, index)
-    mean = rstd = None
-    if return_stats:
-        mean = torch.empty((B, groups), dtype=torch.float32, device=x.device)
-        rstd = torch.empty_like(mean)
-    _run("pc_group_norm", lib().pc_group_norm, index, x.data_ptr(), code, B, L, C, groups,
-         _ptr_or_none(weight), _ptr_or_none(bias), pcode, float(eps), act,
-         _ptr_or_none(lengths), out.data_ptr(), _ptr_or_none(mean), _ptr_or_none(rstd))
-    return (out, mean, rstd) if return_stats else out
+    if not return_stats:
+        _run("pc_group_norm", lib().pc_group_norm, index, x.data_ptr(), code, B, L, C, groups,
+             pw, pb, pcode, float(eps), act, pl, out.data_ptr(), None, None)
+        return out
+    mean = torch.empty((B, groups), dtype=torch.float32, device=x.device)
+    rstd = torch.empty_like(mean)
+    _run("pc_group_norm", lib().pc_group_norm, index, x.data_ptr(), code, B, L, C, groups, pw,
+         pb, pcode, float(eps), act, pl, out.data_ptr(), mean.data_ptr(), rstd.data_ptr())
+    return out, mean, rstd
 
 
 def pc_group_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.Tensor,
@@ -95,18 +117,17 @@ def pc_group_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.
     for what is not needed or for a parameter that is None.  ``mean`` and
     ``rstd`` are the forward call's statistics; ``bias`` enters the
     activation's derivative."""
-    code, index, B, L, C, groups, pcode, act = _group_args(x, groups, weight, bias, activation,
-                                                           lengths)
-    _same(grad_out, "grad_out", x.shape, x.dtype, index)
-    _same(mean, "mean", (B, groups), torch.float32, index)
-    _same(rstd, "rstd", (B, groups), torch.float32, index)
+    code, index, B, L, C, groups, pw, pb, pcode, act, pl = _group_args(
+        x, groups, weight, bias, activation, lengths)
+    pg = _packed(grad_out, "grad_out", x.shape, x.dtype, index)
+    pm = _packed(mean, "mean", (B, groups), torch.float32, index)
+    pr = _packed(rstd, "rstd", (B, groups), torch.float32, index)
     dx = torch.empty_like(x) if need_x else None
     dw = torch.empty_like(weight) if weight is not None and need_weight else None
     db = torch.empty_like(bias) if bias is not None and need_bias else None
-    _run("pc_group_norm_backward", lib().pc_group_norm_backward, index, grad_out.data_ptr(),
-         x.data_ptr(), code, B, L, C, groups, mean.data_ptr(), rstd.data_ptr(),
-         _ptr_or_none(weight), _ptr_or_none(bias), pcode, act, _ptr_or_none(lengths),
-         _ptr_or_none(dx), _ptr_or_none(dw), _ptr_or_none(db))
+    _run("pc_group_norm_backward", lib().pc_group_norm_backward, index, pg, x.data_ptr(), code,
+         B, L, C, groups, pm, pr, pw, pb, pcode, act, pl, _ptr_or_none(dx), _ptr_or_none(dw),
+         _ptr_or_none(db))
     return dx, dw, db
 
 
@@ -114,34 +135,34 @@ def pc_group_norm_backward(grad_out: torch.Tensor, x: torch.Tensor, mean: torch.
 
 def _gated_args(x, w_gate, w_up, b_gate, b_up, activation):
     code = _code(x, "x")
-    if x.dim() < 1 or not x.is_contiguous():
+    shape = x.shape
+    if not shape or not x.is_contiguous():
         raise ValueError("x must be contiguous with at least one axis")
-    C, index, dtype = x.shape[-1], x.get_device(), x.dtype
+    C, index, dtype = shape[-1], x.get_device(), x.dtype
     if not isinstance(w_gate, torch.Tensor) or w_gate.dim() != 2 or w_gate.shape[1] != C:
         raise ValueError(f"w_gate must be a {dtype} CUDA tensor [F, {C}]")
-    F = w_gate.shape[0]
-    _same(w_gate, "w_gate", (F, C), dtype, index)
-    _same(w_up, "w_up", (F, C), dtype, index)
-    if (b_gate is None) != (b_up is None):
+    ws = w_gate.shape
+    F = ws[0]
+    pg, pu = _packed(w_gate, "w_gate", ws, dtype, index), _packed(w_up, "w_up", ws, dtype, index)
+    bg = bu = None
+    if b_gate is not None and b_up is not None:
+        bg = _packed(b_gate, "b_gate", (F,), dtype, index)
+        bu = _packed(b_up, "b_up", (F,), dtype, index)
+    elif not (b_gate is None and b_up is None):
         raise ValueError("b_gate and b_up go together")
-    if b_gate is not None:
-        _same(b_gate, "b_gate", (F,), dtype, index)
-        _same(b_up, "b_up", (F,), dtype, index)
-    rows = 1
-    for n in x.shape[:-1]:
-        rows *= n
-    return index, (x.data_ptr(), code, rows, C, F, w_gate.data_ptr(), w_up.data_ptr(),
-                   _ptr_or_none(b_gate), _ptr_or_none(b_up), _activation(activation)), F
+    rows = shape[0] if len(shape) == 2 else _count(shape[:-1])
+    return index, (x.data_ptr(), code, rows, C, F, pg, pu, bg, bu, _activation(activation)), F
 
 
 PC_GATED_GRAD_X, PC_GATED_GRAD_WEIGHT, PC_GATED_GRAD_BIAS = 1, 2, 4
 
 
+# Calls of as many elements take their scratch from torch's allocator, which keeps it
+# (the library's pool does for smaller ones).
+LARGE = 1 << 24
+
+
 def _workspace(x, rows: int, C: int, F: int, gradients: int, index: int):
-    """Scratch of a large call from torch's allocator, which keeps it (the library's
-    pool does for smaller ones)."""
-    if rows * (C + 2 * F) < 1 << 24:
-        return None, 0
     with torch.cuda.device(index):
         n = lib().pc_gated_linear_workspace_bytes(_DTYPES[x.dtype], rows, C, F, gradients)
     return (torch.empty(n, dtype=torch.uint8, device=x.device), n) if n else (None, 0)
@@ -161,7 +182,9 @@ def pc_gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
         out = torch.empty(shape, dtype=x.dtype, device=x.device)
     else:
         _same(out, "out", shape, x.dtype, index)
-    work, n = _workspace(x, *args[2:5], 0, index)
+    work, n = None, 0
+    if args[2] * (args[3] + 2 * F) >= LARGE:
+        work, n = _workspace(x, *args[2:5], 0, index)
     _run("pc_gated_linear", lib().pc_gated_linear, index, *args, out.data_ptr(),
          _ptr_or_none(work), n)
     return out
@@ -185,7 +208,9 @@ def pc_gated_linear_backward(grad_out: torch.Tensor, x: torch.Tensor, w_gate: to
         dbg, dbu = torch.empty_like(b_gate), torch.empty_like(b_up)
     which = (PC_GATED_GRAD_X if need_x else 0) | (PC_GATED_GRAD_WEIGHT if need_weight else 0) \
         | (PC_GATED_GRAD_BIAS if dbg is not None else 0)
-    work, n = _workspace(x, *args[2:5], which, index) if which else (None, 0)
+    work, n = None, 0
+    if which and args[2] * (args[3] + 2 * F) >= LARGE:
+        work, n = _workspace(x, *args[2:5], which, index)
     _run("pc_gated_linear_backward", lib().pc_gated_linear_backward, index,
          grad_out.data_ptr(), *args, _ptr_or_none(dx), _ptr_or_none(dwg), _ptr_or_none(dwu),
          _ptr_or_none(dbg), _ptr_or_none(dbu), _ptr_or_none(work), n)
@@ -194,20 +219,23 @@ def pc_gated_linear_backward(grad_out: torch.Tensor, x: torch.Tensor, w_gate: to
 
 # --- lookup -----------------------------------------------------------------------
 
-def _lookup(idx, name: str, index: int):
-    if not isinstance(idx, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if idx.dtype is not torch.int64 or not idx.is_cuda or idx.get_device() != index \
-            or not idx.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous int64 tensor on cuda:{index}")
-    return idx
+def _lookup(idx, index: int):
+    """The address of indices."""
+    if isinstance(idx, torch.Tensor) and idx.dtype is torch.int64 \
+            and idx.get_device() == index and idx.is_contiguous():
+        return idx.data_ptr()
+    raise ValueError(f"idx must be a contiguous int64 tensor on cuda:{index}")
 
 
-def _count(shape) -> int:
-    n = 1
-    for k in shape:
-        n *= k
-    return n
+def _lookup_sizes(idx, ts):
+    """Tables, rows, channels, indices into each; the shape of the rows looked up."""
+    s = idx.shape
+    if len(ts) == 2:
+        return 1, ts[0], ts[1], idx.numel(), (*s, ts[1])
+    B = ts[0]
+    if not s or s[0] != B:
+        raise ValueError(f"idx must have shape [{B}, ...] (got {tuple(s)})")
+    return B, ts[1], ts[2], _count(s[1:]), (*s, ts[2])
 
 
 def pc_embedding(table: torch.Tensor, idx: torch.Tensor, scale: float = 1.0, *,
@@ -220,25 +248,18 @@ def pc_embedding(table: torch.Tensor, idx: torch.Tensor, scale: float = 1.0, *,
     PC_ERR_INVALID_ARGUMENT in the device status word.
     """
     code = _code(table, "table")
-    if table.dim() not in (2, 3) or not table.is_contiguous():
-        raise ValueError(f"table must be contiguous [V, C] or [B, V, C] "
-                         f"(got {tuple(table.shape)})")
+    ts = table.shape
+    if len(ts) not in (2, 3) or not table.is_contiguous():
+        raise ValueError(f"table must be contiguous [V, C] or [B, V, C] (got {tuple(ts)})")
     index = table.get_device()
-    _lookup(idx, "idx", index)
-    B, T = 1, _count(idx.shape)
-    if table.dim() == 3:
-        B = table.shape[0]
-        if idx.dim() < 1 or idx.shape[0] != B:
-            raise ValueError(f"idx must have shape [{B}, ...] (got {tuple(idx.shape)})")
-        T = _count(idx.shape[1:])
-    V, C = table.shape[-2:]
-    shape = (*idx.shape, C)
+    pi = _lookup(idx, index)
+    B, V, C, T, shape = _lookup_sizes(idx, ts)
     if out is None:
         out = torch.empty(shape, dtype=table.dtype, device=table.device)
     else:
         _same(out, "out", shape, table.dtype, index)
-    _run("pc_embedding", lib().pc_embedding, index, table.data_ptr(), code, B, V, C,
-         idx.data_ptr(), T, float(scale), out.data_ptr())
+    _run("pc_embedding", lib().pc_embedding, index, table.data_ptr(), code, B, V, C, pi, T,
+         float(scale), out.data_ptr())
     return out
 
 
@@ -253,17 +274,12 @@ def pc_embedding_backward(grad_out: torch.Tensor, idx: torch.Tensor, shape,
     shape = tuple(int(n) for n in shape)
     if len(shape) not in (2, 3):
         raise ValueError(f"shape must be (V, C) or (B, V, C) (got {shape})")
-    _lookup(idx, "idx", index)
-    _same(grad_out, "grad_out", (*idx.shape, shape[-1]), grad_out.dtype, index)
-    B, T = 1, _count(idx.shape)
-    if len(shape) == 3:
-        B = shape[0]
-        if idx.dim() < 1 or idx.shape[0] != B:
-            raise ValueError(f"idx must have shape [{B}, ...] (got {tuple(idx.shape)})")
-        T = _count(idx.shape[1:])
+    pi = _lookup(idx, index)
+    B, V, C, T, rows = _lookup_sizes(idx, shape)
+    pg = _packed(grad_out, "grad_out", rows, grad_out.dtype, index)
     grad = torch.empty(shape, dtype=grad_out.dtype, device=grad_out.device)
-    _run("pc_embedding_backward", lib().pc_embedding_backward, index, grad_out.data_ptr(), code,
-         B, shape[-2], shape[-1], idx.data_ptr(), T, float(scale), grad.data_ptr())
+    _run("pc_embedding_backward", lib().pc_embedding_backward, index, pg, code, B, V, C, pi, T,
+         float(scale), grad.data_ptr())
     return grad
 
 
