@@ -32,7 +32,8 @@ SOURCES = ["pc_api.cu", "pc_fps.cu", "pc_knn.cu", "pc_ball_query.cu",
            "pc_gated.cu", "pc_gated_tc.cu", "pc_embedding.cu"]
 HEADERS = ["pc_device.cuh", "pc_tiles.cuh", "pc_filter.cuh", "pc_stream.cuh",
            "pc_internal.h", "pc_vec.cuh", "pc_attn.cuh", "pc_tcgen05.cuh",
-           "pc_attn_tc.cuh", "pc_act.cuh", "pc_gated.cuh", "pc_group_norm.cuh"]
+           "pc_attn_tc.cuh", "pc_act.cuh", "pc_gated.cuh", "pc_group_norm.cuh",
+           "pc_launch.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = [
     *ARCH, "-O3", "-lineinfo", "-std=c++17", "--fmad=false", "-ftz=false",

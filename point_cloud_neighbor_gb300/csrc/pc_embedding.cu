@@ -19,6 +19,7 @@
 // Bound: memory, the gradient's rows read once in the order of the table's.
 #include "pc_device.cuh"
 #include "pc_internal.h"
+#include "pc_launch.cuh"
 #include "pc_vec.cuh"
 #include "pointcloud.h"
 
@@ -133,6 +134,8 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs &a, uint32_t i, bool
 }
 
 __global__ void __launch_bounds__(EMB_THREADS) sort_count_kernel(SortArgs a) {
+    let_next_start();
+    after_previous();
     __shared__ uint32_t hist[DIGITS];
     hist[threadIdx.x] = hist[threadIdx.x + EMB_THREADS] = 0;
     __syncthreads();
@@ -152,6 +155,8 @@ __global__ void __launch_bounds__(EMB_THREADS) sort_count_kernel(SortArgs a) {
 
 // A warp a digit: the sums over the blocks before, in place, and the total.
 __global__ void __launch_bounds__(EMB_THREADS) sort_scan_kernel(SortArgs a) {
+    let_next_start();
+    after_previous();
     const int d = blockIdx.x * (EMB_THREADS / 32) + threadIdx.x / 32, lane = threadIdx.x % 32;
     if (d >= 1 << a.bits) return;
     uint32_t *row = a.count + size_t(d) * a.blocks, sum = 0;
@@ -170,6 +175,8 @@ __global__ void __launch_bounds__(EMB_THREADS) sort_scan_kernel(SortArgs a) {
 }
 
 __global__ void __launch_bounds__(EMB_THREADS) sort_scatter_kernel(SortArgs a) {
+    let_next_start();
+    after_previous();
     constexpr int WARPS = EMB_THREADS / 32;
     __shared__ uint32_t hist[WARPS][DIGITS], sums[WARPS];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, t = threadIdx.x;
@@ -265,6 +272,8 @@ __device__ __forceinline__ void put_row(const SumArgs &a, uint32_t row, int c, f
 // of one that goes on in the next alone, to its tail.
 template <class T, int V>
 __global__ void __launch_bounds__(EMB_THREADS) emb_chunk_kernel(SumArgs a, int G) {
+    let_next_start();
+    after_previous();
     constexpr int U = 8;
     using R = RawV<T, V>;
     const int per = EMB_THREADS / G, g = threadIdx.x / G, l = threadIdx.x - g * G;
@@ -344,6 +353,8 @@ __device__ __forceinline__ void add_parts(const float *part, uint32_t i0, uint32
 // RUN2 chunks that one row fills and came into.
 template <int V>
 __global__ void __launch_bounds__(EMB_THREADS) emb_second_kernel(SumArgs a, int G) {
+    let_next_start();
+    after_previous();
     const int per = EMB_THREADS / G, g = threadIdx.x / G, l = threadIdx.x - g * G;
     const uint32_t j = blockIdx.x * per + g, span = uint32_t(a.run) * RUN2;
     if (g >= per || (uint64_t(j) + 1) * span > a.n) return;
@@ -363,6 +374,8 @@ __global__ void __launch_bounds__(EMB_THREADS) emb_second_kernel(SumArgs a, int 
 // chunks after it.
 template <class T, int V>
 __global__ void __launch_bounds__(EMB_THREADS) emb_join_kernel(SumArgs a, int G) {
+    let_next_start();
+    after_previous();
     const int per = EMB_THREADS / G, g = threadIdx.x / G, l = threadIdx.x - g * G;
     const uint32_t k = blockIdx.x * per + g;
     if (g >= per || (uint64_t(k) + 1) * a.run >= a.n) return;
@@ -419,16 +432,16 @@ cudaError_t emb_sums(const SumArgs &a, cudaStream_t st) {
     const int G = emb_group(a.C / V), per = EMB_THREADS / G;
     auto blocks = [&](int64_t n) { return unsigned(ceil_div(n, per)); };
     const int64_t chunks = ceil_div(a.n, a.run);
-    emb_chunk_kernel<T, V><<<blocks(chunks), EMB_THREADS, 0, st>>>(a, G);
-    if (chunks > 1) {
-        const int nv = a.C / V, G2 = nv < EMB_THREADS ? nv : EMB_THREADS, per2 = EMB_THREADS / G2;
-        if (chunks > RUN2)
-            emb_second_kernel<V>
-                <<<unsigned(ceil_div(chunks / RUN2, per2)), EMB_THREADS, 0, st>>>(a, G2);
-        emb_join_kernel<T, V>
-            <<<unsigned(ceil_div(chunks - 1, per2)), EMB_THREADS, 0, st>>>(a, G2);
-    }
-    return cudaGetLastError();
+    cudaError_t e =
+        launch(true, emb_chunk_kernel<T, V>, blocks(chunks), EMB_THREADS, 0, st, a, G);
+    const int nv = a.C / V, G2 = nv < EMB_THREADS ? nv : EMB_THREADS, per2 = EMB_THREADS / G2;
+    if (e == cudaSuccess && chunks > RUN2)
+        e = launch(true, emb_second_kernel<V>, unsigned(ceil_div(chunks / RUN2, per2)), EMB_THREADS,
+                   0, st, a, G2);
+    if (e == cudaSuccess && chunks > 1)
+        e = launch(true, emb_join_kernel<T, V>, unsigned(ceil_div(chunks - 1, per2)), EMB_THREADS,
+                   0, st, a, G2);
+    return e;
 }
 
 // The widest vectors that rows of C elements at these addresses can have.
@@ -501,16 +514,16 @@ cudaError_t emb_backward(const DeviceInfo &dev, const void *dy, int dtype, int64
     for (int p = 0; p < passes; ++p) {
         s.shift = p * each;
         s.out = lists[p % 2];
-        sort_count_kernel<<<blocks, EMB_THREADS, 0, st>>>(s);
-        sort_scan_kernel<<<((1 << each) + 7) / 8, EMB_THREADS, 0, st>>>(s);
-        sort_scatter_kernel<<<blocks, EMB_THREADS, 0, st>>>(s);
+        if (e == cudaSuccess) e = launch(p > 0, sort_count_kernel, blocks, EMB_THREADS, 0, st, s);
+        if (e == cudaSuccess)
+            e = launch(true, sort_scan_kernel, ((1 << each) + 7) / 8, EMB_THREADS, 0, st, s);
+        if (e == cudaSuccess) e = launch(true, sort_scatter_kernel, blocks, EMB_THREADS, 0, st, s);
         s.idx = nullptr, s.in = s.out;
     }
     a.sorted = s.out;
     a.head = reinterpret_cast<float *>(mem + 2 * list + count);
     a.tail = a.head + part / sizeof(float);
     a.part2 = a.tail + part / sizeof(float);
-    e = cudaGetLastError();
     if (e == cudaSuccess)
         e = dtype == PC_F32 ? emb_sums_any<float>(a, st) : emb_sums_any<bf16>(a, st);
     const cudaError_t f = scratch_free(mem, st);

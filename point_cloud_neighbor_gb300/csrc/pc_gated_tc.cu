@@ -36,6 +36,7 @@
 // SM's shared memory, so none waits for another's tensor memory.
 #include "pc_act.cuh"
 #include "pc_gated.cuh"
+#include "pc_launch.cuh"
 #include "pc_tcgen05.cuh"
 #include "pc_tiles.cuh"
 #include "pointcloud.h"
@@ -209,6 +210,7 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
     uint32_t *tmem_slot = reinterpret_cast<uint32_t *>(dybar + C::EWARPS);
     volatile int *stop = reinterpret_cast<volatile int *>(tmem_slot + 1);
 
+    let_next_start();
     const int warp = uniform(threadIdx.x / 32), lane = threadIdx.x % 32;
     const int tiles = a.mt * a.nt, items = tiles * a.nsplit;
     // the blocks of a tile: one, or a cluster of two with 128 rows each
@@ -228,6 +230,7 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
     __syncthreads();
     if (CG > 1) cluster_sync_all();  // both blocks' barriers exist
     tc_fence_after();
+    after_previous();
     const uint32_t tmem = uniform(int(*tmem_slot));
 
     // A bounded wait; false: stop.
@@ -693,6 +696,7 @@ constexpr int PACK_ROWS = 16;
 // Rows of T as P bfloat16 parts, padded to eight columns.
 template <class T, int P>
 __global__ void __launch_bounds__(256) gated_pack_kernel(PackJobs jobs) {
+    let_next_start();
     int b = blockIdx.x, k = 0;
     while (k < 2 && b >= jobs.job[k].blocks) b -= jobs.job[k++].blocks;
     const PackJob &j = jobs.job[k];
@@ -715,6 +719,8 @@ __global__ void __launch_bounds__(256) gated_pack_kernel(PackJobs jobs) {
 template <class T, int V>
 __global__ void __launch_bounds__(256)
 gated_join_kernel(const float *part, int nparts, int64_t n, int64_t half, T *out, T *out2) {
+    let_next_start();
+    after_previous();
     const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * V;
     if (i >= n) return;
     float s[V];
@@ -733,6 +739,8 @@ gated_join_kernel(const float *part, int nparts, int64_t n, int64_t half, T *out
 template <class T>
 __global__ void __launch_bounds__(1024)
 gated_bias_kernel(const float *part, int nparts, int F, T *dbg, T *dbu) {
+    let_next_start();
+    after_previous();
     __shared__ float acc[32][33];
     const int c = blockIdx.x * 32 + threadIdx.x;
     float s = 0.0f;
@@ -843,56 +851,40 @@ GemmPlan plan_gemm(int sms, int mode, int P, int64_t M, int64_t N, int64_t kb) {
 }
 
 template <int MODE, int P, int BN, int CG>
-cudaError_t run_gemm(const DeviceInfo &dev, const GemmMaps &maps, const GemmArgs &g,
+cudaError_t run_gemm(const DeviceInfo &dev, const GemmMaps &maps, const GemmArgs &g, bool behind,
                      cudaStream_t st) {
     using C = GCfg<MODE, P, BN, CG>;
     static std::atomic<uint64_t> done{0};
-    cudaError_t e =
+    const cudaError_t e =
         allow_smem(gated_gemm_kernel<MODE, P, BN, CG>, int(C::SMEM), dev.device, done);
     if (e != cudaSuccess) return e;
     const int64_t items = int64_t(g.mt) * g.nt * g.nsplit, units = dev.sm_count / CG;
     if (items > (int64_t(1) << 30)) return cudaErrorInvalidConfiguration;
     const unsigned blocks = unsigned(items < units ? items : units) * CG;
-    if (CG == 1) {
-        gated_gemm_kernel<MODE, P, BN, CG><<<blocks, C::THREADS, C::SMEM, st>>>(maps, g);
-        return cudaGetLastError();
-    }
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(C::THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = st;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = CG;
-    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, gated_gemm_kernel<MODE, P, BN, CG>, maps, g);
+    return launch_clusters(behind, gated_gemm_kernel<MODE, P, BN, CG>, blocks, C::THREADS, C::SMEM,
+                           st, CG, maps, g);
 }
 template <int MODE, int P>
 cudaError_t run_gemm(const DeviceInfo &dev, const GemmMaps &maps, const GemmArgs &g,
-                     const GemmPlan &p, cudaStream_t st) {
+                     const GemmPlan &p, bool behind, cudaStream_t st) {
     if (p.CG == 2) {
         if constexpr (P == 1)
-            if (p.BN == 256) return run_gemm<MODE, P, 256, 2>(dev, maps, g, st);
-        return run_gemm<MODE, P, 128, 2>(dev, maps, g, st);
+            if (p.BN == 256) return run_gemm<MODE, P, 256, 2>(dev, maps, g, behind, st);
+        return run_gemm<MODE, P, 128, 2>(dev, maps, g, behind, st);
     }
-    return p.BN == 128 ? run_gemm<MODE, P, 128, 1>(dev, maps, g, st)
-                       : run_gemm<MODE, P, 64, 1>(dev, maps, g, st);
+    return p.BN == 128 ? run_gemm<MODE, P, 128, 1>(dev, maps, g, behind, st)
+                       : run_gemm<MODE, P, 64, 1>(dev, maps, g, behind, st);
 }
 
 template <class T>
 cudaError_t join(const float *part, int nparts, int64_t n, int64_t half, void *out, void *out2,
                  cudaStream_t st) {
     T *o = static_cast<T *>(out), *o2 = static_cast<T *>(out2);
-    if (n % 4 == 0 && half % 4 == 0 && aligned16(out) && (out2 == nullptr || aligned16(out2)))
-        gated_join_kernel<T, 4><<<unsigned(ceil_div(n, 1024)), 256, 0, st>>>(part, nparts, n, half,
-                                                                            o, o2);
-    else
-        gated_join_kernel<T, 1><<<unsigned(ceil_div(n, 256)), 256, 0, st>>>(part, nparts, n, half,
-                                                                           o, o2);
-    return cudaGetLastError();
+    const bool vec =
+        n % 4 == 0 && half % 4 == 0 && aligned16(out) && (out2 == nullptr || aligned16(out2));
+    return launch(true, vec ? gated_join_kernel<T, 4> : gated_join_kernel<T, 1>,
+                  unsigned(ceil_div(n, vec ? 1024 : 256)), 256, 0, st, part, nparts, n, half, o,
+                  o2);
 }
 
 // x and the weights as operands, split or copied where they have to be.
@@ -900,6 +892,7 @@ struct Inputs {
     Operand x, wg, wu;
     size_t at[3];
     bool packed[3];
+    bool any() const { return packed[0] || packed[1] || packed[2]; }
 };
 template <class T, int P>
 void plan_inputs(const GatedArgs &a, Inputs &in, Scratch &s) {
@@ -1019,7 +1012,7 @@ cudaError_t forward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st) 
         const bool ok = make_map3(&m.a0, in.x, BM) && make_map3(&m.b0, in.wg, p.BN / 2) &&
                         make_map3(&m.b1, in.wu, p.BN / 2) &&
                         (P > 1 || !g.vec || make_tile_map(&m.o0, a.y, a.rows, a.F, a.F));
-        e = ok ? run_gemm<G_FWD, P>(dev, m, g, p, st) : cudaErrorInvalidValue;
+        e = ok ? run_gemm<G_FWD, P>(dev, m, g, p, in.any(), st) : cudaErrorInvalidValue;
     }
     return memory.give(e);
 }
@@ -1056,7 +1049,7 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
                         make_map3(&m.b1, in.wu, p.BN / 2) &&
                         make_map3(&m.o0, d[0], 32, 32) && make_map3(&m.o1, d[1], 32, 32) &&
                         (P > 1 || !g.dvec || make_tile_map(&m.dy, a.dy, a.rows, a.F, a.F));
-        e = ok ? run_gemm<G_GRAD, P>(dev, m, g, p, st) : cudaErrorInvalidValue;
+        e = ok ? run_gemm<G_GRAD, P>(dev, m, g, p, in.any(), st) : cudaErrorInvalidValue;
     }
     if (e == cudaSuccess && a.dx) {
         GemmArgs g = gemm_args(dev, a);
@@ -1069,7 +1062,7 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
         const bool ok = make_map3(&m.a0, d[0], BM) &&
                         make_map3(&m.a1, d[1], BM) &&
                         make_map3(&m.b0, in.wg, 64) && make_map3(&m.b1, in.wu, 64);
-        e = ok ? run_gemm<G_DX, P>(dev, m, g, px, st) : cudaErrorInvalidValue;
+        e = ok ? run_gemm<G_DX, P>(dev, m, g, px, true, st) : cudaErrorInvalidValue;
         if (e == cudaSuccess && g.nsplit > 1)
             e = join<T>(g.part, g.nsplit, a.rows * a.C, a.rows * a.C, a.dx, nullptr, st);
     }
@@ -1084,15 +1077,15 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
         GemmMaps m{};
         const bool ok = make_map3(&m.a0, d[0], 64) && make_map3(&m.a1, d[1], 64) &&
                         make_map3(&m.b0, in.x, 64);
-        e = ok ? run_gemm<G_DW, P>(dev, m, g, pw, st) : cudaErrorInvalidValue;
+        e = ok ? run_gemm<G_DW, P>(dev, m, g, pw, true, st) : cudaErrorInvalidValue;
         const int64_t n = int64_t(a.F) * a.C;
         if (e == cudaSuccess && g.nsplit > 1)
             e = join<T>(g.part, g.nsplit, 2 * n, n, a.dwg, a.dwu, st);
     }
     if (e == cudaSuccess && a.dbg) {
-        gated_bias_kernel<T><<<unsigned(ceil_div(2 * a.F, 32)), dim3(32, 32), 0, st>>>(
-            partials(part_b), int(4 * p.CG * ceil_div(a.rows, p.rows())), a.F, static_cast<T *>(a.dbg), static_cast<T *>(a.dbu));
-        e = cudaGetLastError();
+        e = launch(true, gated_bias_kernel<T>, unsigned(ceil_div(2 * a.F, 32)), dim3(32, 32), 0, st,
+                   partials(part_b), int(4 * p.CG * ceil_div(a.rows, p.rows())), a.F,
+                   static_cast<T *>(a.dbg), static_cast<T *>(a.dbu));
     }
     return memory.give(e);
 }

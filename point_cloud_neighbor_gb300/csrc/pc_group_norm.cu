@@ -25,6 +25,7 @@
 //
 // Bound: memory.
 #include "pc_group_norm.cuh"
+#include "pc_launch.cuh"
 #include "pointcloud.h"
 
 #include <atomic>
@@ -76,6 +77,8 @@ struct GnPlace {
 // Forward 1: the pieces' moments over a block's rows.
 template <class T, int V>
 __global__ void __launch_bounds__(GN_THREADS) gn_stats_kernel(GnArgs a) {
+    let_next_start();
+    after_previous();
     constexpr int U = V >= 4 ? 4 : 8;  // rows in registers
     __shared__ float sm[GN_THREADS * V], ss[GN_THREADS * V], sn[GN_THREADS];
     const GnPlace<V> p(a, a.nblk);
@@ -164,6 +167,8 @@ __global__ void __launch_bounds__(GN_THREADS) gn_stats_kernel(GnArgs a) {
 
 // Forward 2: a group's moments over all blocks; a block per cloud and group.
 __global__ void __launch_bounds__(128) gn_join_kernel(GnArgs a) {
+    let_next_start();
+    after_previous();
     const int64_t bg = blockIdx.x, b = bg / a.G;
     const int g = int(bg % a.G), per = a.per ? a.per : 1, all = a.G * per;
     const int64_t len = gn_len(a, b);
@@ -196,6 +201,8 @@ __global__ void __launch_bounds__(128) gn_join_kernel(GnArgs a) {
 // Forward 3
 template <class T, int V>
 __global__ void __launch_bounds__(GN_THREADS) gn_apply_kernel(GnArgs a, int nblk) {
+    let_next_start();
+    after_previous();
     constexpr int U = V >= 4 ? 4 : 8;
     const GnPlace<V> p(a, nblk);
     if (!p.on) return;
@@ -246,6 +253,8 @@ __global__ void __launch_bounds__(GN_THREADS) gn_apply_kernel(GnArgs a, int nblk
 // Backward 1: the channels' sums of d and d xhat over a block's rows.
 template <class T, int V>
 __global__ void __launch_bounds__(GN_THREADS) gn_sums_kernel(GnArgs a) {
+    let_next_start();
+    after_previous();
     constexpr int U = V >= 4 ? 2 : 4;
     __shared__ float s1[GN_THREADS * V], s2[GN_THREADS * V];
     const GnPlace<V> p(a, a.nblk);
@@ -302,6 +311,8 @@ __global__ void __launch_bounds__(GN_THREADS) gn_sums_kernel(GnArgs a) {
 // Backward 2: the blocks' sums added up, per cloud and channel; 32 columns a
 // block, 32 warps every 32nd of the blocks' sums.
 __global__ void __launch_bounds__(1024) gn_channel_kernel(GnArgs a) {
+    let_next_start();
+    after_previous();
     __shared__ float acc[32][33];
     const int cols = (2 * a.C + 31) / 32;
     const int64_t b = blockIdx.x / cols;
@@ -324,6 +335,8 @@ __global__ void __launch_bounds__(1024) gn_channel_kernel(GnArgs a) {
 // sums over the clouds: dw and db.
 template <class T, int V>
 __global__ void __launch_bounds__(GN_THREADS) gn_dx_kernel(GnArgs a, int nblk, int nparam) {
+    let_next_start();
+    after_previous();
     constexpr int U = V >= 4 ? 2 : 4;
     if (blockIdx.x >= gridDim.x - nparam) {
         const int c = int(blockIdx.x - (gridDim.x - nparam)) * GN_THREADS + threadIdx.x;
@@ -491,23 +504,27 @@ cudaError_t gn_run(GnArgs a, const GnPlan &p) {
             a.mean = reinterpret_cast<float *>(static_cast<char *>(scratch) + parts);
             a.rstd = a.mean + a.B * a.G;
         }
-        gn_stats_kernel<T, V><<<grid, GN_THREADS, 0, st>>>(a);
-        gn_join_kernel<<<unsigned(a.B * a.G), 128, 0, st>>>(a);
-        gn_apply_kernel<T, V><<<grid2, GN_THREADS, 0, st>>>(a, second);
+        e = launch(false, gn_stats_kernel<T, V>, grid, GN_THREADS, 0, st, a);
+        if (e == cudaSuccess)
+            e = launch(true, gn_join_kernel, unsigned(a.B * a.G), 128, 0, st, a);
+        if (e == cudaSuccess)
+            e = launch(true, gn_apply_kernel<T, V>, grid2, GN_THREADS, 0, st, a, second);
     } else {
         const size_t parts = size_t(a.B) * a.nblk * 2 * a.C * sizeof(float);
         const size_t chan = size_t(a.B) * 2 * a.C * sizeof(float);
         if ((e = scratch_alloc(*p.dev, &scratch, parts + chan, st)) != cudaSuccess) return e;
         a.cpart = static_cast<float *>(scratch);
         a.chan = a.cpart + parts / sizeof(float);
-        gn_sums_kernel<T, V><<<grid, GN_THREADS, 0, st>>>(a);
-        gn_channel_kernel<<<unsigned(a.B * ((2 * a.C + 31) / 32)), dim3(32, 32), 0, st>>>(a);
+        e = launch(false, gn_sums_kernel<T, V>, grid, GN_THREADS, 0, st, a);
+        if (e == cudaSuccess)
+            e = launch(true, gn_channel_kernel, unsigned(a.B * ((2 * a.C + 31) / 32)), dim3(32, 32),
+                       0, st, a);
         const int nparam = a.dw || a.db ? int(ceil_div(2 * a.C, GN_THREADS)) : 0;
         const unsigned dxgrid = a.y ? grid2 : 0;
-        if (dxgrid + nparam > 0)
-            gn_dx_kernel<T, V><<<dxgrid + nparam, GN_THREADS, 0, st>>>(a, second, nparam);
+        if (e == cudaSuccess && dxgrid + nparam > 0)
+            e = launch(true, gn_dx_kernel<T, V>, dxgrid + nparam, GN_THREADS, 0, st, a, second,
+                       nparam);
     }
-    e = cudaGetLastError();
     const cudaError_t f = scratch_free(scratch, st);
     return e == cudaSuccess ? f : e;
 }

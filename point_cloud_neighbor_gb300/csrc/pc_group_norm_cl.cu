@@ -15,6 +15,7 @@
 // Bound: latency of the copy, the barrier and the store, then memory.
 #include "pc_device.cuh"
 #include "pc_group_norm.cuh"
+#include "pc_launch.cuh"
 #include "pointcloud.h"
 
 #include <algorithm>
@@ -328,6 +329,7 @@ __global__ void __launch_bounds__(CT, 1) gn_cluster_forward_kernel(ClArgs k) {
 template <class T, int V>
 __global__ void __launch_bounds__(CT, 1) gn_cluster_backward_kernel(ClArgs k) {
     extern __shared__ __align__(16) unsigned char smem[];
+    let_next_start();
     const GnArgs &a = k.a;
     constexpr int U = V >= 4 ? 2 : 4;
     const ClShared sh(smem + 2 * k.room, a.G, cl_exchange(a.C, V));
@@ -492,6 +494,7 @@ __global__ void __launch_bounds__(CT, 1) gn_cluster_backward_kernel(ClArgs k) {
 template <class T>
 __global__ void __launch_bounds__(1024)
 gn_param_kernel(const float *part, int64_t nparts, int C, bool f32, void *db, void *dw) {
+    after_previous();
     __shared__ float acc[32][33];
     const int c = blockIdx.x * 32 + threadIdx.x;
     float s = 0.0f;
@@ -554,9 +557,8 @@ cudaError_t run(const DeviceInfo &dev, GnArgs a, bool backward, const GnCluster 
     void *args[] = {&k};
     e = cudaLaunchKernelExC(&cfg, fn, args);
     if (e == cudaSuccess && params) {
-        gn_param_kernel<T><<<unsigned((2 * a.C + 31) / 32), dim3(32, 32), 0, st>>>(
-            a.cpart, a.B * p.blocks, a.C, a.wf32, a.db, a.dw);
-        e = cudaGetLastError();
+        e = launch(true, gn_param_kernel<T>, unsigned((2 * a.C + 31) / 32), dim3(32, 32), 0, st,
+                   a.cpart, a.B * p.blocks, a.C, a.wf32, a.db, a.dw);
     }
     if (scratch) {
         const cudaError_t f = scratch_free(scratch, st);
