@@ -52,7 +52,7 @@ constexpr int PANEL = 64 * 128;  // bytes of a 64 x 64 panel of an MN-major oper
 
 struct GemmMaps {
     CUtensorMap a0, a1, b0, b1;
-    CUtensorMap dy, o0, o1;  // boxes of 32 x 32: GRAD dy, da, du; FWD y in o0
+    CUtensorMap dy, o0, o1;  // boxes of 32 rows: GRAD dy, da, du; FWD y in o0
 };
 
 struct GemmArgs {
@@ -79,17 +79,20 @@ struct GCfg {
     static constexpr int M = BM * CG;  // rows of a tile
     static constexpr int STAGE = A_BYTES + B_BYTES;  // of one part of both operands
     // Warps that take the accumulators: four for the 128 rows, times parts of the columns.
-    // 16 where a tile's arithmetic outlasts its products otherwise.
-    static constexpr int EWARPS = PAIR && BN == 256 ? 16 : 8, THREADS = 32 * (4 + EWARPS);
+    // 16 where a tile's arithmetic outlasts its products otherwise (4084 x 387 x 1021
+    // float32: with 8 the gradients of gelu took half as long again).
+    static constexpr int EWARPS = PAIR && (BN == 256 || (P > 1 && BN == 128)) ? 16 : 8;
+    static constexpr int THREADS = 32 * (4 + EWARPS);
     static constexpr int COLS = 2 * BN;               // tensor memory
     static constexpr int NL = BN / (EWARPS / 4);      // columns of a thread
     static constexpr int CH = PAIR ? NL / 2 : 32;     // PAIR: hidden units, else of a chunk
     static_assert(!PAIR || CH == 32 || CH == 16, "chunks");
-    // PAIR with 32 units a warp: its 32 x 32 tiles of the arrays that are as large as the
-    // result, on their way from or to global memory, 2 KB each in bfloat16: dy, da and
+    // PAIR: a warp's tiles of 32 rows by CH units of the arrays that are as large as the
+    // result, on their way from or to global memory (bfloat16: TILE bytes each): dy, da and
     // du; y.  As tensor maps have them, or (float32, unaligned rows) as place() does.
-    static constexpr bool STAGED = PAIR && CH == 32;
-    static constexpr int ROOM = !STAGED ? 0 : P > 1 ? 4096 : MODE == G_FWD ? 2048 : 6144;
+    static constexpr bool STAGED = PAIR && BN >= 128;
+    static constexpr int TILE = 64 * CH;
+    static constexpr int ROOM = !STAGED ? 0 : (P > 1 || MODE == G_FWD ? (P > 1 ? 2 : 1) : 3) * TILE;
     static constexpr int FIT = (227 * 1024 - 1024 - 512 - EWARPS * ROOM) / STAGE,
                          STAGES = FIT > 8 ? 8 : FIT;
     static_assert(STAGES >= 2 * P, "shared memory");
@@ -143,17 +146,22 @@ __device__ __forceinline__ void take(const T *p, float (&v)[CH], int left, bool 
     }
 }
 
-// A lane's row of 32 bfloat16 of a tile as a tensor map with the 64-byte swizzle has it.
+// 16 bytes of a lane's row of CH bfloat16 of a tile, as a tensor map has it with a swizzle
+// over rows of 64 or 32 bytes.
+template <int CH>
 __device__ __forceinline__ unsigned char *row_part(unsigned char *tile, int lane, int c) {
-    return tile + lane * 64 + ((c ^ ((lane >> 1) & 3)) * 16);
+    return tile + lane * (2 * CH) +
+           ((CH == 32 ? c ^ ((lane >> 1) & 3) : c ^ ((lane >> 2) & 1)) * 16);
 }
 // N of them from column o on.
-template <int N>
+template <int CH, int N>
 __device__ __forceinline__ void put_row(unsigned char *tile, int lane, int o, const float *v) {
 #pragma unroll
     for (int c = 0; c < N / 8; ++c)
-        Vec<bf16, 8>::store(reinterpret_cast<bf16 *>(row_part(tile, lane, o / 8 + c)), v + 8 * c);
+        Vec<bf16, 8>::store(reinterpret_cast<bf16 *>(row_part<CH>(tile, lane, o / 8 + c)),
+                            v + 8 * c);
 }
+
 // P parts of eight numbers, `plane` elements apart.
 template <int P>
 __device__ __forceinline__ void put_parts(bf16 *p, int64_t plane, const float *v) {
@@ -399,32 +407,38 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
         };
         // the warp's room: dy behind da and du where there are three
         unsigned char *room = rooms + (warp - 4) * C::ROOM;
-        unsigned char *dyroom = room + (P == 1 && MODE == G_GRAD ? 4096 : 0);
+        unsigned char *dyroom = room + (P == 1 && MODE == G_GRAD ? 2 * C::TILE : 0);
         const bool leader = elect_one();
         // Where column c of row r of an unaligned array is, so that neither the lanes of a
         // row nor those of a column meet in a bank.
         auto place = [](int r, int c) {
-            return P > 1 ? r * 32 + (c ^ r) : r * 32 + ((((c >> 1) ^ (r >> 1)) << 1) | (c & 1));
+            if (P == 1) return r * 32 + ((((c >> 1) ^ (r >> 1)) << 1) | (c & 1));
+            return CH == 32 ? r * 32 + (c ^ r) : r * 16 + (c ^ ((r >> 1) & 15));
         };
         constexpr int W = P > 1 ? 1 : 2;
+        static_assert(!C::STAGED || P > 1 || CH == 32, "bfloat16 goes in rows of 32");
+        // the rows that go with one instruction, a lane's row and column among them
+        constexpr int RS = C::STAGED ? 32 / CH : 1;
+        const int lr = lane / CH, lc = lane % CH;
         auto rows_in = [&](T *to, const T *from, int64_t r0, int c0) {
-            T v[32];  // (all loads before the first store)
-            from += r0 * a.N + c0 + lane;
-            const int rows = c0 + lane < a.N ? int(min(a.M - r0, int64_t(32))) : 0;
+            T v[32 / RS];  // (all loads before the first store)
+            from += (r0 + lr) * a.N + c0 + lc;
+            const int rows = c0 + lc < a.N ? int(min(a.M - r0, int64_t(32))) : 0;
 #pragma unroll
-            for (int r = 0; r < 32; ++r, from += a.N) v[r] = r < rows ? *from : T(0.0f);
+            for (int r = 0; r < 32; r += RS, from += RS * a.N)
+                v[r / RS] = r + lr < rows ? *from : T(0.0f);
 #pragma unroll
-            for (int r = 0; r < 32; ++r) to[place(r, lane)] = v[r];
+            for (int r = 0; r < 32; r += RS) to[place(r + lr, lc)] = v[r / RS];
         };
         auto rows_out = [&](T *to, const T *from, int64_t r0, int c0) {
-            T v[32];
+            T v[32 / RS];
 #pragma unroll
-            for (int r = 0; r < 32; ++r) v[r] = from[place(r, lane)];
-            to += r0 * a.N + c0 + lane;
-            const int rows = c0 + lane < a.N ? int(min(a.M - r0, int64_t(32))) : 0;
+            for (int r = 0; r < 32; r += RS) v[r / RS] = from[place(r + lr, lc)];
+            to += (r0 + lr) * a.N + c0 + lc;
+            const int rows = c0 + lc < a.N ? int(min(a.M - r0, int64_t(32))) : 0;
 #pragma unroll
-            for (int r = 0; r < 32; ++r, to += a.N)
-                if (r < rows) *to = v[r];
+            for (int r = 0; r < 32; r += RS, to += RS * a.N)
+                if (r + lr < rows) *to = v[r / RS];
         };
         // the warp's tile of an item
         auto tile_row = [&](const Item &it) { return it.m * C::M + rank * BM + quad * 32; };
@@ -438,7 +452,7 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
             dyahead = i < items;
             if (!dyahead) return;
             const Item it(a, i, tiles);
-            mbar_arrive_expect_tx(mydy, 2048);
+            mbar_arrive_expect_tx(mydy, C::TILE);
             tma_load_3d(dyroom, &maps.dy, tile_column(it), tile_row(it), 0, mydy);
         };
         if (AHEAD && a.dvec && leader) dy_ahead(first);
@@ -485,7 +499,7 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                         dyahead = false;
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
-                            dyraw[c] = *reinterpret_cast<const uint4 *>(row_part(dyroom, lane, c));
+                            dyraw[c] = *reinterpret_cast<const uint4 *>(row_part<CH>(dyroom, lane, c));
                         __syncwarp();
                         if (leader) dy_ahead(i + step);
                     } else {
@@ -554,7 +568,7 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                         if (!C::STAGED)
                             put<T, SUB>(static_cast<T *>(a.out) + row * a.N + c0, g, left, a.vec);
                         else if (P == 1 && a.vec)
-                            put_row<SUB>(room, lane, o, g);
+                            put_row<CH, SUB>(room, lane, o, g);
                         else
 #pragma unroll
                             for (int c = 0; c < SUB; c += W)
@@ -588,8 +602,8 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                                     put_parts<P>(to + P * plane + c, plane, u + c);
                                 }
                         } else if constexpr (P == 1) {
-                            put_row<SUB>(room, lane, o, g);
-                            put_row<SUB>(room + 2048, lane, o, u);
+                            put_row<CH, SUB>(room, lane, o, g);
+                            put_row<CH, SUB>(room + C::TILE, lane, o, u);
                         } else {
                             // three parts, one after the other through the room
                             __syncwarp();
@@ -599,13 +613,13 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                                     if (leader) bulk_wait_read_all();
                                     __syncwarp();
                                 }
-                                put_row<SUB>(room, lane, 0, g);
-                                put_row<SUB>(room + 2048, lane, 0, u);
+                                put_row<CH, SUB>(room, lane, 0, g);
+                                put_row<CH, SUB>(room + C::TILE, lane, 0, u);
                                 fence_proxy_async_smem();
                                 __syncwarp();
                                 if (leader && live) {
                                     tma_store_3d(&maps.o0, room, c0, int(row0), k);
-                                    tma_store_3d(&maps.o1, room + 2048, c0, int(row0), k);
+                                    tma_store_3d(&maps.o1, room + C::TILE, c0, int(row0), k);
                                     bulk_commit();
                                 }
 #pragma unroll
@@ -622,7 +636,7 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                         if (leader && live) {
                             tma_store_3d(&maps.o0, room, c0, int(row0), 0);
                             if (MODE == G_GRAD)
-                                tma_store_3d(&maps.o1, room + 2048, c0, int(row0), 0);
+                                tma_store_3d(&maps.o1, room + C::TILE, c0, int(row0), 0);
                             bulk_commit();
                         }
                     } else {
@@ -770,7 +784,7 @@ struct Operand {
     int cols = 0, ld = 0, parts = 1;
 };
 
-// Boxes of `columns` (64, or 32) columns by `box` rows of one part.
+// Boxes of `columns` (64, 32 or 16) columns by `box` rows of one part.
 bool make_map3(CUtensorMap *map, const Operand &o, int box, int columns = 64) {
     const EncodeFn fn = encode_fn();
     if (fn == nullptr) return false;
@@ -779,7 +793,9 @@ bool make_map3(CUtensorMap *map, const Operand &o, int box, int columns = 64) {
     const cuuint32_t b[3] = {cuuint32_t(columns), cuuint32_t(box), 1}, ones[3] = {1, 1, 1};
     return fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<bf16 *>(o.p), dims, strides, b,
               ones, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              columns == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              columns == 64   ? CU_TENSOR_MAP_SWIZZLE_128B
+              : columns == 32 ? CU_TENSOR_MAP_SWIZZLE_64B
+                              : CU_TENSOR_MAP_SWIZZLE_32B,
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
@@ -1047,7 +1063,8 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
         const bool ok = make_map3(&m.a0, in.x, BM) &&
                         make_map3(&m.b0, in.wg, p.BN / 2) &&
                         make_map3(&m.b1, in.wu, p.BN / 2) &&
-                        make_map3(&m.o0, d[0], 32, 32) && make_map3(&m.o1, d[1], 32, 32) &&
+                        make_map3(&m.o0, d[0], 32, P > 1 ? 16 : 32) &&
+                        make_map3(&m.o1, d[1], 32, P > 1 ? 16 : 32) &&
                         (P > 1 || !g.dvec || make_tile_map(&m.dy, a.dy, a.rows, a.F, a.F));
         e = ok ? run_gemm<G_GRAD, P>(dev, m, g, p, in.any(), st) : cudaErrorInvalidValue;
     }

@@ -611,8 +611,8 @@ GnCluster gn_cluster_plan(const DeviceInfo &dev, const GnArgs &a, int dtype, int
     // Estimates in us.  A wave of clusters takes a block's values and a part that does not
     // depend on them; the kernels for any size spread the values over all SMs, read them
     // twice and are three launches.  Measured, forward / backward with all gradients:
-    // 16 x 1024 x 384 bf16 (6 blocks a cloud in one wave / 8 in two) 16.9 / 24.6 against 21.9 /
-    // 28.2; 4 x 4093 x 195 bf16 (16 blocks, element by element) 25.9 / 40.4 against 22.8 / 30.9;
+    // 16 x 1024 x 384 bf16 ragged (6 blocks a cloud in one wave / 9 in two) 16.9 / 23 against
+    // 21.9 / 28.2 (4 blocks 20.9, 8 18.5 / 24.6, 12 21.9 / 33, 16 28.8 / 37); 4 x 4093 x 195 bf16 (16 blocks, element by element) 25.9 / 40.4 against 22.8 / 30.9;
     // 1 x 64 x 384 forward 8 against 11.
     const int VB = V * (dtype == PC_F32 ? 4 : 2);
     const double each = (VB >= 16 ? 0.13 : VB >= 8 ? 0.2 : VB >= 4 ? 0.3 : 0.45) / 1000 *
@@ -625,9 +625,11 @@ GnCluster gn_cluster_plan(const DeviceInfo &dev, const GnArgs &a, int dtype, int
         if (smem > int64_t(dev.smem_per_block_optin) || a.B * K > 2147483647) continue;
         const int at_once = active_clusters(dev, K);
         if (at_once == 0) continue;
-        const double waves = double((a.B + at_once - 1) / at_once);
-        const double cost = waves * ((K > 1 ? 5.0 : 4.0) + 0.1 * K +
-                                     each * double((a.L + K - 1) / K) * a.C);
+        // (a last wave that is not full costs less: fewer blocks, often of short clouds)
+        const double waves = a.B <= at_once
+                                 ? 1.0
+                                 : double(a.B / at_once) + (a.B % at_once ? 0.6 : 0.0);
+        const double cost = waves * (4.0 + 0.35 * K + each * double((a.L + K - 1) / K) * a.C);
         if (cost < 0.97 * least) {
             least = cost;
             p.blocks = K, p.bytes = int(room(K)), p.smem = size_t(smem);
