@@ -59,7 +59,8 @@ struct GemmArgs {
     int64_t M;           // rows of the output
     int N;               // its columns
     int kb0, kb;         // stages of the first part of the contraction (DX: da), of all
-    int mt, nt, nsplit;  // tiles; parts of the contraction
+    int mt, nt, nsplit;  // tiles; parts of the contraction, none of them empty,
+    int per;             // of as many stages each (the last: at most)
     void *out, *out2;    // y; dx; dWg and dWu
     float *part;         // [nsplit][rows of all outputs][N] where nsplit > 1
     const void *bg, *bu, *dy;
@@ -257,8 +258,8 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
             split = unsigned(i) / unsigned(tiles);
             const unsigned t = i - split * tiles;
             m = t / unsigned(a.nt), n = t - m * a.nt;
-            k0 = unsigned(a.kb * split) / unsigned(a.nsplit);  // (below 2^30: nsplit <= 2^16)
-            k1 = unsigned(a.kb * (split + 1)) / unsigned(a.nsplit);
+            k0 = split * a.per;
+            k1 = min(a.kb, k0 + a.per);
         }
     };
 
@@ -834,7 +835,7 @@ constexpr GemmKind KINDS[] = {{256, 2, 620, 4400, 7000, 2600, 6300},
 // six products for one, epilogues three times as long (and no tiles of 256 columns, whose
 // sums a thread could not hold).  Parts cost their writes and reads and a launch.
 struct GemmPlan {
-    int BN = 0, CG = 1, nsplit = 1;
+    int BN = 0, CG = 1, nsplit = 1, per = 1;
     int rows() const { return BM * CG; }
 };
 GemmPlan plan_gemm(int sms, int mode, int P, int64_t M, int64_t N, int64_t kb) {
@@ -855,6 +856,7 @@ GemmPlan plan_gemm(int sms, int mode, int P, int64_t M, int64_t N, int64_t kb) {
         const int64_t fewest = !pair && P == 1 ? ceil_div(kb * BK, CHAIN) : 1;
         const int64_t most = pair ? 1 : kb < 64 ? kb : 64;
         for (int64_t ns = fewest; ns <= (most > fewest ? most : fewest); ++ns) {
+            if (ns > fewest && tiles * (ns - 1) > 4 * units) break;  // (waves enough)
             const double k = double(ceil_div(kb, ns)) * stage;
             double cost = double(ceil_div(tiles * ns, units)) * (k > epilogue ? k : epilogue) +
                           epilogue + kind.fixed;
@@ -863,6 +865,8 @@ GemmPlan plan_gemm(int sms, int mode, int P, int64_t M, int64_t N, int64_t kb) {
                 least = cost, best.BN = kind.BN, best.CG = kind.CG, best.nsplit = int(ns);
         }
     }
+    best.per = int(ceil_div(kb, best.nsplit));
+    best.nsplit = int(ceil_div(kb, best.per));
     return best;
 }
 
@@ -1021,7 +1025,7 @@ cudaError_t forward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st) 
         GemmArgs g = gemm_args(dev, a);
         g.M = a.rows, g.N = a.F, g.kb = int(ceil_div(a.C, BK)), g.kb0 = g.kb;
         const GemmPlan p = plan_gemm(dev.sm_count, G_FWD, P, g.M, g.N, g.kb);
-        g.mt = int(ceil_div(a.rows, p.rows()));
+        g.mt = int(ceil_div(a.rows, p.rows())), g.per = p.per;
         g.nt = int(ceil_div(a.F, p.BN / 2));
         g.out = a.y, g.vec = a.F % (16 / sizeof(T)) == 0 && aligned16(a.y);
         GemmMaps m{};
@@ -1054,7 +1058,7 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
     if (e == cudaSuccess) {
         GemmArgs g = gemm_args(dev, a);
         g.M = a.rows, g.N = a.F, g.kb = int(ceil_div(a.C, BK)), g.kb0 = g.kb;
-        g.mt = int(ceil_div(a.rows, p.rows()));
+        g.mt = int(ceil_div(a.rows, p.rows())), g.per = p.per;
         g.nt = int(ceil_div(a.F, p.BN / 2));
         g.d = const_cast<bf16 *>(d[0].p), g.ld = ld;
         g.dvec = a.F % (16 / sizeof(T)) == 0 && aligned16(a.dy);
@@ -1072,7 +1076,7 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
         GemmArgs g = gemm_args(dev, a);
         g.M = a.rows, g.N = a.C, g.kb0 = kf, g.kb = 2 * kf;
         g.mt = int(ceil_div(a.rows, px.rows()));
-        g.nt = int(ceil_div(a.C, px.BN)), g.nsplit = px.nsplit;
+        g.nt = int(ceil_div(a.C, px.BN)), g.nsplit = px.nsplit, g.per = px.per;
         g.out = a.dx, g.vec = a.C % (16 / sizeof(T)) == 0 && aligned16(a.dx);
         g.part = partials(part_x);
         GemmMaps m{};
@@ -1087,7 +1091,7 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
         GemmArgs g = gemm_args(dev, a);
         g.M = a.F, g.N = a.C, g.kb = kr, g.kb0 = kr;
         g.mt = 2 * int(ceil_div(a.F, pw.rows()));
-        g.nt = int(ceil_div(a.C, pw.BN)), g.nsplit = pw.nsplit;
+        g.nt = int(ceil_div(a.C, pw.BN)), g.nsplit = pw.nsplit, g.per = pw.per;
         g.out = a.dwg, g.out2 = a.dwu;
         g.vec = a.C % (16 / sizeof(T)) == 0 && aligned16(a.dwg) && aligned16(a.dwu);
         g.part = partials(part_w);

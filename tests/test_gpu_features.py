@@ -133,7 +133,9 @@ def gated_all(x, wg, wu, bg, bu, dy, act):
 SHAPES = [(1, 1, 1), (1, 16, 8), (2, 96, 40), (3, 7, 5), (4, 384, 1024), (5, 33, 65), (8, 64, 256),
           (9, 520, 72), (17, 40, 24), (32, 384, 1024), (33, 100, 36), (64, 2048, 512),
           (65, 64, 64), (127, 48, 200), (128, 64, 64), (129, 72, 130), (200, 384, 1024),
-          (257, 515, 333), (1000, 40, 96), (1021, 129, 63), (2500, 64, 16), (4100, 16, 24)]
+          (257, 515, 333), (1000, 40, 96), (1021, 129, 63), (2500, 64, 16), (4100, 16, 24),
+          # sums over more than 16,384 rows and hidden units; the most channels
+          (40000, 16, 24), (3, 40, 9000), (5, 16384, 8), (300, 33, 65536)]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -476,7 +478,9 @@ def emb_reference(dy, idx, shape, scale):
 EMB = [((1, 1), (1,)), ((7, 3), (5,)), ((40, 384), (512,)), ((100, 33), (1000,)),
        ((1000, 8), (4097,)), ((3, 16), (20000,)), ((1, 72), (9001,)), ((300, 515), (64, 3)),
        ((70000, 4), (3000,)), ((5, 24), (0,)), ((4, 64, 40), (4, 30, 9)), ((3, 1000, 64), (3, 2000)),
-       ((33, 5, 7), (33, 1)), ((2, 1, 130), (2, 4200)), ((65535, 16), (300,)), ((65536, 2), (5000,))]
+       ((33, 5, 7), (33, 1)), ((2, 1, 130), (2, 4200)), ((65535, 16), (300,)), ((65536, 2), (5000,)),
+       ((511, 8), (700,)), ((512, 8), (700,)), ((300000, 4), (5000,)), ((9, 24), (200000,)),
+       ((50, 2050), (900,))]
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
@@ -565,6 +569,67 @@ def test_embedding_long_sum_of_one_row():
     s, m = emb_reference(dy, torch.zeros(T, dtype=torch.int64, device=DEV), (3, 4), 1.0)
     close(d, s, (5 * 70 + 600) * U * m + 1e-30, "grad_table")   # 586 sums of 64 runs of 16
     assert not d[1:].any()
+
+
+# --- beyond 32 bits ------------------------------------------------------------------
+
+def test_embedding_beyond_32_bits():
+    """Rows whose offset in the table is beyond 2^31 elements; keys of 28 bits."""
+    V, C = (1 << 21) + 3, 1024
+    table = torch.zeros(V, C, dtype=torch.bfloat16, device=DEV)
+    idx = torch.tensor([V - 1, 5, V - 2, V - 1, -1], device=DEV)
+    table[V - 1], table[V - 2], table[5] = 3.0, 2.0, 1.0
+    y = pc.pc_embedding(table, idx)
+    assert y[:, 0].tolist() == [3, 1, 2, 3, 0] and torch.equal(y, y[:, :1].expand_as(y))
+    d = pc.pc_embedding_backward(y, idx, (V, C))
+    assert (d[V - 1] == 6).all() and (d[V - 2] == 2).all() and (d[5] == 1).all()
+    d[V - 1], d[V - 2], d[5] = 0, 0, 0
+    assert not d.any()
+    del table, d
+    V = (1 << 27) + 9
+    idx = torch.tensor([V - 1, 0, 1 << 27, V - 1], device=DEV)
+    d = pc.pc_embedding_backward(torch.ones(4, 1, device=DEV), idx, (V, 1))
+    assert d[V - 1] == 2 and d[0] == 1 and d[1 << 27] == 1 and d.sum() == 4
+
+
+def test_group_norm_beyond_32_bits():
+    B, L, C = 3, 700_000, 1024
+    x = torch.empty(B, L, C, dtype=torch.bfloat16, device=DEV)
+    g = gen(1)
+    x[2] = torch.randn(L, C, generator=g, device=DEV, dtype=torch.bfloat16)
+    x[:2] = 1
+    w = randn(g, C)
+    y, m, r = pc.pc_group_norm(x, 32, w, w, activation="silu", return_stats=True)
+    y1, m1, r1 = pc.pc_group_norm(x[2:], 32, w, w, activation="silu", return_stats=True)
+    # (other shares of the rows: statistics off by a few roundings, results by one of bfloat16's)
+    assert (r[2] / r1[0] - 1).abs().max() < 1e-5 and (m[2] - m1[0]).abs().max() < 1e-5
+    for i in (0, L // 2, L - 100):
+        a, b = y[2, i:i + 100].float(), y1[0, i:i + 100].float()
+        assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 1e-4).all()
+    del y, y1
+    dx, dw, _ = pc.pc_group_norm_backward(x, x, m, r, 32, w, w, activation="silu")
+    dx1, dw1, _ = pc.pc_group_norm_backward(x[2:], x[2:], m[2:], r[2:], 32, w, w,
+                                            activation="silu")
+    for i in (0, L // 2, L - 100):
+        a, b = dx[2, i:i + 100].float(), dx1[0, i:i + 100].float()
+        assert ((a - b).abs() <= 2.0 ** -7 * b.abs() + 1e-4).all()
+
+
+def test_gated_linear_beyond_32_bits():
+    rows, C, F = 2_200_000, 8, 1024
+    g = gen(2)
+    x = torch.randn(rows, C, generator=g, device=DEV, dtype=torch.bfloat16)
+    wg, wu = (torch.randn(F, C, generator=g, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    y = pc.pc_gated_linear(x, wg, wu)
+    dx, dwg, dwu, _, _ = pc.pc_gated_linear_backward(y, x, wg, wu)
+    ref = gated_reference(x[-1000:], wg, wu, None, None, y[-1000:], "silu")
+    for name, got in (("y", y), ("dx", dx)):
+        close(got[-1000:], *ref[name], name)
+    a, u = x.double() @ wg.double()[:8].T, x.double() @ wu.double()[:8].T
+    s = torch.sigmoid(a)
+    want = (y[:, :8].double() * u * s * (1 + a * (1 - s))).T @ x.double()
+    # one rounding of da and one of the result, 2^-9 each; the error of 2.2e6 terms of random sign
+    assert float((dwg[:8].double() - want).norm() / want.norm()) < 2.0 ** -8
 
 
 # --- autograd, streams, graphs, all together ------------------------------------------
