@@ -31,33 +31,6 @@ namespace {
 constexpr int EMB_THREADS = 256;
 constexpr int RUN2 = 32;  // chunks of a second sum
 
-// V elements as they are in memory.
-template <int BYTES>
-struct Raw;
-template <>
-struct Raw<16> {
-    using type = uint4;
-};
-template <>
-struct Raw<8> {
-    using type = uint2;
-};
-template <>
-struct Raw<4> {
-    using type = uint32_t;
-};
-template <>
-struct Raw<2> {
-    using type = uint16_t;
-};
-template <class T, int V>
-using RawV = typename Raw<V * int(sizeof(T))>::type;
-
-template <class T, int V>
-__device__ __forceinline__ void widen(const RawV<T, V> &r, float *v) {
-    Vec<T, V>::load(reinterpret_cast<const T *>(&r), v);
-}
-
 // --- forward ------------------------------------------------------------------
 
 // G threads a token, U tokens a thread at a time.
@@ -65,8 +38,8 @@ constexpr int FORWARD_TOKENS = 3;
 template <class T, int V>
 __global__ void __launch_bounds__(EMB_THREADS)
 emb_forward_kernel(const T *__restrict__ table, int64_t rows, int C,
-                   const int64_t *__restrict__ idx, int64_t per_cloud, int64_t tokens, float scale,
-                   T *__restrict__ out, int G, int *status) {
+                   const int64_t *__restrict__ idx, int64_t per_cloud, FastDiv clouds,
+                   int64_t tokens, float scale, T *__restrict__ out, int G, int *status) {
     constexpr int U = FORWARD_TOKENS;
     using R = RawV<T, V>;
     const int per = EMB_THREADS / G, g = threadIdx.x / G, l = threadIdx.x - g * G;
@@ -81,7 +54,7 @@ emb_forward_kernel(const T *__restrict__ table, int64_t rows, int C,
         const int64_t r = idx[t];
         int64_t cloud = 0;
         if (per_cloud < tokens)
-            cloud = tokens <= 0xffffffffll ? uint32_t(t) / uint32_t(per_cloud) : t / per_cloud;
+            cloud = tokens < (int64_t(1) << 31) ? clouds.div(uint32_t(t)) : t / per_cloud;
         if (r >= 0 && r < rows)
             from[u] = table + (cloud * rows + r) * C;
         else if (r != -1)
@@ -96,14 +69,15 @@ emb_forward_kernel(const T *__restrict__ table, int64_t rows, int C,
         for (int u = 0; u < U; ++u) {
             const int64_t t = t0 + u * per;
             if (t >= tokens) break;
-            float v[V];
-            widen<T, V>(raw[u], v);
+            if (scale != 1.0f && from[u]) {  // (a row that is not scaled is copied)
+                float v[V];
+                widen<T, V>(raw[u], v);
 #pragma unroll
-            for (int e = 0; e < V; ++e) v[e] = from[u] ? v[e] * scale : 0.0f;
+                for (int e = 0; e < V; ++e) v[e] *= scale;
+                Vec<T, V>::store(reinterpret_cast<T *>(&raw[u]), v);
+            }
             // (written past the caches: they keep the table)
-            R w;
-            Vec<T, V>::store(reinterpret_cast<T *>(&w), v);
-            __stcs(reinterpret_cast<R *>(out + t * C + c), w);
+            __stcs(reinterpret_cast<R *>(out + t * C + c), raw[u]);
         }
     }
 }
@@ -422,7 +396,8 @@ cudaError_t emb_forward(const DeviceInfo &dev, const void *table, int64_t V_, in
     const int64_t blocks = ceil_div(tokens, per * FORWARD_TOKENS);
     if (blocks > 2147483647) return cudaErrorInvalidConfiguration;
     emb_forward_kernel<T, V><<<unsigned(blocks), EMB_THREADS, 0, st>>>(
-        static_cast<const T *>(table), V_, C, idx, T_, tokens, scale, static_cast<T *>(out), G,
+        static_cast<const T *>(table), V_, C, idx, T_,
+        FastDiv(T_ < (int64_t(1) << 31) ? uint32_t(T_) : 1), tokens, scale, static_cast<T *>(out), G,
         dev.status_word);
     return cudaGetLastError();
 }
@@ -488,10 +463,8 @@ cudaError_t emb_backward(const DeviceInfo &dev, const void *dy, int dtype, int64
     a.dy = dy, a.dtable = dtable, a.n = uint32_t(B * T), a.rows = uint32_t(B * V), a.C = C;
     a.scale = scale;
     // 64 tokens a chunk, or 32 or 16 where that leaves the SMs short of warps
-    const int64_t warps = ceil_div(int64_t(C) * es, 512) * a.n;
-    a.run = warps / 64 >= int64_t(dev.sm_count) * 32 ? 64
-            : warps / 32 >= int64_t(dev.sm_count) * 32 ? 32
-                                                       : 16;
+    const int64_t warps = ceil_div(int64_t(C) * es * a.n, 512), enough = int64_t(dev.sm_count) * 8;
+    a.run = warps / 64 >= enough ? 64 : warps / 32 >= enough ? 32 : 16;
     // keys 0 .. rows, the last for absent tokens
     int bits = 0;
     while ((int64_t(1) << bits) <= int64_t(a.rows)) ++bits;

@@ -856,7 +856,7 @@ GemmPlan plan_gemm(int sms, int mode, int P, int64_t M, int64_t N, int64_t kb) {
         const int64_t fewest = !pair && P == 1 ? ceil_div(kb * BK, CHAIN) : 1;
         const int64_t most = pair ? 1 : kb < 64 ? kb : 64;
         for (int64_t ns = fewest; ns <= (most > fewest ? most : fewest); ++ns) {
-            if (ns > fewest && tiles * (ns - 1) > 4 * units) break;  // (waves enough)
+            if (ns > fewest && tiles * (ns - 1) > 8 * units) break;  // (waves enough)
             const double k = double(ceil_div(kb, ns)) * stage;
             double cost = double(ceil_div(tiles * ns, units)) * (k > epilogue ? k : epilogue) +
                           epilogue + kind.fixed;

@@ -79,7 +79,7 @@ template <class T, int V>
 __global__ void __launch_bounds__(GN_THREADS) gn_stats_kernel(GnArgs a) {
     let_next_start();
     after_previous();
-    constexpr int U = V >= 4 ? 4 : 8;  // rows in registers
+    constexpr int U = 8;  // rows in registers
     __shared__ float sm[GN_THREADS * V], ss[GN_THREADS * V], sn[GN_THREADS];
     const GnPlace<V> p(a, a.nblk);
     const int64_t len = gn_len(a, p.b);
@@ -91,29 +91,44 @@ __global__ void __launch_bounds__(GN_THREADS) gn_stats_kernel(GnArgs a) {
     for (int e = 0; e < V; ++e) m[e] = s[e] = 0.0f;
     if (p.on)
         for (int64_t r = r0 + p.r; r < r1; r += int64_t(U) * p.R) {
-            float v[U][V], k = 0.0f;
+            RawV<T, V> raw[U];
+            float k = 0.0f;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
                 const bool in = r + int64_t(u) * p.R < r1;
-                if (in) Vec<T, V>::load(x + (r + int64_t(u) * p.R) * a.C, v[u]);
+                if (in)
+                    raw[u] = *reinterpret_cast<const RawV<T, V> *>(x + (r + int64_t(u) * p.R) * a.C);
                 k += in ? 1.0f : 0.0f;
             }
             const float inv = 1.0f / k, t = n + k, f = k / t, h = n * f;
+            float sum[V], sq[V];
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum[e] = sq[e] = 0.0f;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (u < int(k)) {
+                    float v[V];
+                    widen<T, V>(raw[u], v);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) sum[e] += v[e];
+                }
+#pragma unroll
+            for (int e = 0; e < V; ++e) sum[e] *= inv;  // the mean
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (u < int(k)) {
+                    float v[V];
+                    widen<T, V>(raw[u], v);
+#pragma unroll
+                    for (int e = 0; e < V; ++e) {
+                        const float d = v[e] - sum[e];
+                        sq[e] = fmaf(d, d, sq[e]);
+                    }
+                }
 #pragma unroll
             for (int e = 0; e < V; ++e) {
-                float sum = 0.0f, sq = 0.0f;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (u < int(k)) sum += v[u][e];
-                const float mean = sum * inv;
-#pragma unroll
-                for (int u = 0; u < U; ++u)
-                    if (u < int(k)) {
-                        const float d = v[u][e] - mean;
-                        sq = fmaf(d, d, sq);
-                    }
-                const float d = mean - m[e];
-                s[e] += fmaf(d * d, h, sq);
+                const float d = sum[e] - m[e];
+                s[e] += fmaf(d * d, h, sq[e]);
                 m[e] = fmaf(d, f, m[e]);
             }
             n = t;
@@ -255,7 +270,7 @@ template <class T, int V>
 __global__ void __launch_bounds__(GN_THREADS) gn_sums_kernel(GnArgs a) {
     let_next_start();
     after_previous();
-    constexpr int U = V >= 4 ? 2 : 4;
+    constexpr int U = 2;  // rows in flight
     __shared__ float s1[GN_THREADS * V], s2[GN_THREADS * V];
     const GnPlace<V> p(a, a.nblk);
     const int64_t len = gn_len(a, p.b);
@@ -269,22 +284,27 @@ __global__ void __launch_bounds__(GN_THREADS) gn_sums_kernel(GnArgs a) {
     if (p.on) {
         const GnChannels<T, V> ch(a, p.b, p.c);
         for (int64_t r = r0 + p.r; r < r1; r += int64_t(U) * p.R) {
-            float v[U][V], g[U][V];
+            RawV<T, V> rx[U], rg[U];
 #pragma unroll
             for (int u = 0; u < U; ++u)
                 if (r + int64_t(u) * p.R < r1) {
-                    Vec<T, V>::load(x + (r + int64_t(u) * p.R) * a.C, v[u]);
-                    Vec<T, V>::load(dy + (r + int64_t(u) * p.R) * a.C, g[u]);
+                    const int64_t i = (r + int64_t(u) * p.R) * a.C;
+                    rx[u] = *reinterpret_cast<const RawV<T, V> *>(x + i);
+                    rg[u] = *reinterpret_cast<const RawV<T, V> *>(dy + i);
                 }
-            ch.form(a.act, v, g);
 #pragma unroll
             for (int u = 0; u < U; ++u)
-                if (r + int64_t(u) * p.R < r1)
+                if (r + int64_t(u) * p.R < r1) {
+                    float v[1][V], g[1][V];
+                    widen<T, V>(rx[u], v[0]);
+                    widen<T, V>(rg[u], g[0]);
+                    ch.template form<1>(a.act, v, g);
 #pragma unroll
                     for (int e = 0; e < V; ++e) {
-                        t1[e] += g[u][e];
-                        t2[e] = fmaf(g[u][e], v[u][e], t2[e]);
+                        t1[e] += g[0][e];
+                        t2[e] = fmaf(g[0][e], v[0][e], t2[e]);
                     }
+                }
         }
     }
     const int o = int(threadIdx.x) * V;
@@ -477,7 +497,7 @@ template <class T, int V>
 cudaError_t gn_run(GnArgs a, const GnPlan &p) {
     const int R = GN_THREADS / (a.width / V);
     const int64_t sets = a.B * a.nchunk;
-    const int batch = R * (p.backward ? (V >= 4 ? 2 : 4) : (V >= 4 ? 4 : 8));
+    const int batch = R * (p.backward ? 2 : V >= 4 ? 4 : 8);
     static std::atomic<int> resident[4][64] = {};
     int second = 1;  // blocks a cloud of the second pass
     cudaError_t e;

@@ -111,6 +111,33 @@ struct Vec<bf16, 8> {
     }
 };
 
+// V elements as they are in memory.
+template <int BYTES>
+struct Raw;
+template <>
+struct Raw<16> {
+    using type = uint4;
+};
+template <>
+struct Raw<8> {
+    using type = uint2;
+};
+template <>
+struct Raw<4> {
+    using type = uint32_t;
+};
+template <>
+struct Raw<2> {
+    using type = uint16_t;
+};
+template <class T, int V>
+using RawV = typename Raw<V * int(sizeof(T))>::type;
+
+template <class T, int V>
+__device__ __forceinline__ void widen(const RawV<T, V> &r, float *v) {
+    Vec<T, V>::load(reinterpret_cast<const T *>(&r), v);
+}
+
 // What rounding v to T leaves: v is T(v) + rest<T>(v).
 template <class T>
 __device__ __forceinline__ float rest(float v);
