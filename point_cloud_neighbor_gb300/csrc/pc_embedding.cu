@@ -18,7 +18,7 @@
 // Everything in float32 and in a fixed order.
 // Bound: memory, the gradient's rows read once in the order of the table's, and in small
 // calls the launches.  Measured, 500,000 tokens of 256 float32, a table of 100,000 rows:
-// forward 118 us (5.2 TB/s), backward 17 us of zeros, 33 of sorting, 110 of sums (4.7 TB/s), 24
+// forward 118 us (5.2 TB/s), backward 33 of sorting (with the zeros), 110 of sums (4.7 TB/s), 24
 // of joins; 16 x 16,384 tokens of 128 bfloat16: forward 17 us, backward 45.
 #include "pc_device.cuh"
 #include "pc_internal.h"
@@ -101,7 +101,25 @@ struct SortArgs {
     uint32_t n, absent;            // tokens; the key of those without a row
     int blocks, shift, bits;
     int *status;
+    // Blocks from `blocks` on write zeros to this kernel's share of the table's gradient,
+    // under the sort, which leaves memory idle: words [zero0, zero1) of 16 bytes, or of 2
+    // where the table is not aligned (`narrow`).
+    void *zero;
+    size_t zero0, zero1;
+    bool narrow;
 };
+
+// True in a block that writes zeros, and has.
+__device__ __forceinline__ bool write_zeros(const SortArgs &a) {
+    if (blockIdx.x < a.blocks) return false;
+    const size_t step = size_t(gridDim.x - a.blocks) * EMB_THREADS;
+    size_t i = a.zero0 + size_t(blockIdx.x - a.blocks) * EMB_THREADS + threadIdx.x;
+    if (a.narrow)
+        for (; i < a.zero1; i += step) static_cast<uint16_t *>(a.zero)[i] = 0;
+    else
+        for (; i < a.zero1; i += step) static_cast<uint4 *>(a.zero)[i] = make_uint4(0, 0, 0, 0);
+    return true;
+}
 
 __device__ __forceinline__ uint32_t sort_key(const SortArgs &a, uint32_t i, bool report) {
     const int64_t r = a.idx[i];
@@ -113,6 +131,7 @@ __device__ __forceinline__ uint32_t sort_key(const SortArgs &a, uint32_t i, bool
 __global__ void __launch_bounds__(EMB_THREADS) sort_count_kernel(SortArgs a) {
     let_next_start();
     after_previous();
+    if (write_zeros(a)) return;
     __shared__ uint32_t hist[DIGITS];
     hist[threadIdx.x] = hist[threadIdx.x + EMB_THREADS] = 0;
     __syncthreads();
@@ -154,6 +173,7 @@ __global__ void __launch_bounds__(EMB_THREADS) sort_scan_kernel(SortArgs a) {
 __global__ void __launch_bounds__(EMB_THREADS) sort_scatter_kernel(SortArgs a) {
     let_next_start();
     after_previous();
+    if (write_zeros(a)) return;
     constexpr int WARPS = EMB_THREADS / 32;
     __shared__ uint32_t hist[WARPS][DIGITS], sums[WARPS];
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, t = threadIdx.x;
@@ -458,10 +478,8 @@ cudaError_t emb_sums_any(const SumArgs &a, cudaStream_t st) {
 cudaError_t emb_backward(const DeviceInfo &dev, const void *dy, int dtype, int64_t B, int64_t V,
                          int C, const int64_t *idx, int64_t T, float scale, void *dtable,
                          cudaStream_t st) {
-    // rows without tokens are 0 (the others are written again)
-    const size_t es = dtype == PC_F32 ? 4 : 2;
-    cudaError_t e = cudaMemsetAsync(dtable, 0, size_t(B) * V * C * es, st);
-    if (e != cudaSuccess || B * T == 0) return e;
+    const size_t es = dtype == PC_F32 ? 4 : 2, bytes = size_t(B) * V * C * es;
+    if (B * T == 0) return cudaMemsetAsync(dtable, 0, bytes, st);
     SumArgs a{};
     a.dy = dy, a.dtable = dtable, a.n = uint32_t(B * T), a.rows = uint32_t(B * V), a.C = C;
     a.scale = scale;
@@ -478,7 +496,7 @@ cudaError_t emb_backward(const DeviceInfo &dev, const void *dy, int dtype, int64
     const size_t count = round((size_t(blocks) + 1) * (size_t(1) << each) * 4);
     const size_t chunks = size_t(ceil_div(a.n, a.run)), part = round(chunks * C * 4);
     char *mem = nullptr;
-    e = scratch_alloc(dev, reinterpret_cast<void **>(&mem),
+    cudaError_t e = scratch_alloc(dev, reinterpret_cast<void **>(&mem),
                       2 * list + count + 2 * part + round(chunks / RUN2 * C * 4), st);
     if (e != cudaSuccess) return e;
     uint2 *lists[2] = {reinterpret_cast<uint2 *>(mem), reinterpret_cast<uint2 *>(mem + list)};
@@ -487,13 +505,25 @@ cudaError_t emb_backward(const DeviceInfo &dev, const void *dy, int dtype, int64
     s.count = reinterpret_cast<uint32_t *>(mem + 2 * list);
     s.total = s.count + (size_t(blocks) << each);
     s.blocks = blocks, s.bits = each, s.status = dev.status_word;
+    // rows without tokens are 0 (the others are written again): a share of the zeros in
+    // each of the counts and scatters
+    s.zero = dtable, s.narrow = reinterpret_cast<uintptr_t>(dtable) % 16 || bytes % 16;
+    const size_t words = bytes / (s.narrow ? 2 : 16), shares = 2 * size_t(passes);
+    auto with_zeros = [&](size_t share) {
+        s.zero0 = words * share / shares, s.zero1 = words * (share + 1) / shares;
+        const int64_t want = ceil_div(int64_t(s.zero1 - s.zero0), EMB_THREADS * 8);
+        const int64_t most = int64_t(dev.sm_count) * 4;
+        return unsigned(blocks + (want < most ? want : most));
+    };
     for (int p = 0; p < passes; ++p) {
         s.shift = p * each;
         s.out = lists[p % 2];
-        if (e == cudaSuccess) e = launch(p > 0, sort_count_kernel, blocks, EMB_THREADS, 0, st, s);
+        unsigned grid = with_zeros(2 * p);
+        if (e == cudaSuccess) e = launch(p > 0, sort_count_kernel, grid, EMB_THREADS, 0, st, s);
         if (e == cudaSuccess)
             e = launch(true, sort_scan_kernel, ((1 << each) + 7) / 8, EMB_THREADS, 0, st, s);
-        if (e == cudaSuccess) e = launch(true, sort_scatter_kernel, blocks, EMB_THREADS, 0, st, s);
+        grid = with_zeros(2 * p + 1);
+        if (e == cudaSuccess) e = launch(true, sort_scatter_kernel, grid, EMB_THREADS, 0, st, s);
         s.idx = nullptr, s.in = s.out;
     }
     a.sorted = s.out;
