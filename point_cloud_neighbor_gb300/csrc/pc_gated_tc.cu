@@ -71,6 +71,9 @@ struct GemmMaps {
     CUtensorMap dy, o0, o1;  // boxes of 32 rows: GRAD dy, da, du; FWD y in o0
 };
 
+// Columns of a row of parts, so that all are 16-byte aligned.
+__host__ __device__ inline int pad4(int n) { return (n + 3) / 4 * 4; }
+
 struct GemmArgs {
     int64_t M;           // rows of the output
     int N;               // its columns
@@ -78,7 +81,7 @@ struct GemmArgs {
     int mt, nt, nsplit;  // tiles; parts of the contraction, none of them empty,
     int per;             // of as many stages each (the last: at most)
     void *out, *out2;    // y; dx; dWg and dWu
-    float *part;         // [nsplit][rows of all outputs][N] where nsplit > 1
+    float *part;         // [nsplit][rows of all outputs][pad4(N)] where nsplit > 1
     const void *bg, *bu, *dy;
     bf16 *d;             // [da, du][parts][M][ld]
     float *bpart;        // GRAD: [4 mt][da, du][N], sums over 32 rows, or NULL
@@ -109,7 +112,10 @@ struct GCfg {
     // du; y.  As tensor maps have them, or (float32, unaligned rows) as place() does.
     static constexpr bool STAGED = PAIR && BN >= 128;
     static constexpr int TILE = 64 * CH;
-    static constexpr int ROOM = !STAGED ? 0 : (P > 1 || MODE == G_FWD ? (P > 1 ? 2 : 1) : 3) * TILE;
+    // (plain results: where rows are not 16-byte aligned)
+    static constexpr int ROOM =
+        !PAIR ? 1024 * (P > 1 ? 4 : 2)
+              : !STAGED ? 0 : (P > 1 || MODE == G_FWD ? (P > 1 ? 2 : 1) : 3) * TILE;
     static constexpr int FIT = (227 * 1024 - 1024 - 512 - EWARPS * ROOM) / STAGE,
                          STAGES = FIT > 8 ? 8 : FIT;
     static_assert(STAGES >= 2 * P, "shared memory");
@@ -685,13 +691,21 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                     }
                     const int c0 = it.n * BN + part * C::NL + j * CH;
                     const int left = row < a.M ? a.N - c0 : 0;
+                    T *out = static_cast<T *>(up ? a.out2 : a.out);
                     if (a.nsplit > 1) {
                         const int64_t all = MODE == G_DW ? 2 * a.M : a.M;
-                        put<float, CH>(a.part + (it.split * all + (up ? a.M : 0) + row) * a.N + c0,
-                                       v, left, a.N % 4 == 0);
+                        put<float, CH>(
+                            a.part + (it.split * all + (up ? a.M : 0) + row) * pad4(a.N) + c0, v,
+                            row < a.M ? pad4(a.N) - c0 : 0, true);
+                    } else if (a.vec) {
+                        put<T, CH>(out + row * a.N + c0, v, left, true);
                     } else {
-                        put<T, CH>(static_cast<T *>(up ? a.out2 : a.out) + row * a.N + c0, v, left,
-                                   a.vec);
+#pragma unroll
+                        for (int c = 0; c < CH; c += W)
+                            Vec<T, W>::store(reinterpret_cast<T *>(room) + place(lane, c), v + c);
+                        __syncwarp();
+                        rows_out(out, reinterpret_cast<const T *>(room), row - lane, c0);
+                        __syncwarp();
                     }
                 }
             }
@@ -745,25 +759,37 @@ __global__ void __launch_bounds__(256) gated_pack_kernel(PackJobs jobs) {
 
 // --- sums of parts -------------------------------------------------------------------
 
-// out[i] = sum over the parts, in their order: the first `half` numbers to out,
-// the others to out2.
-template <class T, int V>
+// The sum over the parts, in their order, of rows of N columns: the first `half` rows to
+// out, the others to out2.  A thread four columns.
+template <class T>
 __global__ void __launch_bounds__(256)
-gated_join_kernel(const float *part, int nparts, int64_t n, int64_t half, T *out, T *out2) {
+gated_join_kernel(const float *part, int nparts, int64_t rows, int64_t half, int N, FastDiv groups,
+                  bool vec, T *out, T *out2) {
     let_next_start();
     after_previous();
-    const int64_t i = (int64_t(blockIdx.x) * 256 + threadIdx.x) * V;
-    if (i >= n) return;
-    float s[V];
-    Vec<float, V>::load(part + i, s);
+    const int ld = pad4(N);
+    const int64_t i = int64_t(blockIdx.x) * 256 + threadIdx.x, all = rows * (ld / 4);
+    if (i >= all) return;
+    const int64_t row = all < (int64_t(1) << 31) ? groups.div(uint32_t(i)) : i / (ld / 4);
+    const int c = int(i - row * (ld / 4)) * 4;
+    const float *p = part + row * ld + c;
+    float s[4];
+    Vec<float, 4>::load(p, s);
 #pragma unroll 4
-    for (int p = 1; p < nparts; ++p) {
-        float v[V];
-        Vec<float, V>::load(part + p * n + i, v);
+    for (int k = 1; k < nparts; ++k) {
+        float v[4];
+        Vec<float, 4>::load(p + k * rows * ld, v);
 #pragma unroll
-        for (int e = 0; e < V; ++e) s[e] += v[e];
+        for (int e = 0; e < 4; ++e) s[e] += v[e];
     }
-    Vec<T, V>::store(i < half ? out + i : out2 + (i - half), s);
+    T *to = (row < half ? out + row * N : out2 + (row - half) * N) + c;
+    if (vec) {
+        Vec<T, 4>::store(to, s);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+            if (c + e < N) Vec<T, 1>::store(to + e, s + e);
+    }
 }
 
 // The biases' gradients: 32 columns a block, 32 warps every 32nd part, in a fixed order.
@@ -913,14 +939,13 @@ cudaError_t run_gemm(const DeviceInfo &dev, const GemmMaps &maps, const GemmArgs
 }
 
 template <class T>
-cudaError_t join(const float *part, int nparts, int64_t n, int64_t half, void *out, void *out2,
-                 cudaStream_t st) {
+cudaError_t join(const float *part, int nparts, int64_t rows, int64_t half, int N, void *out,
+                 void *out2, cudaStream_t st) {
     T *o = static_cast<T *>(out), *o2 = static_cast<T *>(out2);
-    const bool vec =
-        n % 4 == 0 && half % 4 == 0 && aligned16(out) && (out2 == nullptr || aligned16(out2));
-    return launch(true, vec ? gated_join_kernel<T, 4> : gated_join_kernel<T, 1>,
-                  unsigned(ceil_div(n, vec ? 1024 : 256)), 256, 0, st, part, nparts, n, half, o,
-                  o2);
+    const bool vec = N % 4 == 0 && aligned16(out) && (out2 == nullptr || aligned16(out2));
+    const int groups = pad4(N) / 4;
+    return launch(true, gated_join_kernel<T>, unsigned(ceil_div(rows * groups, 256)), 256, 0, st,
+                  part, nparts, rows, half, N, FastDiv(groups), vec, o, o2);
 }
 
 // x and the weights as operands, split or copied where they have to be.
@@ -994,12 +1019,12 @@ BackwardPlan plan_backward(const DeviceInfo &dev, const GatedArgs &a) {
     if (a.dx) {
         b.px = plan_gemm(dev.sm_count, G_DX, P, a.rows, a.C, 2 * b.kf);
         if (b.px.nsplit > 1)
-            b.part_x = b.s.take(size_t(b.px.nsplit) * a.rows * a.C * sizeof(float));
+            b.part_x = b.s.take(size_t(b.px.nsplit) * a.rows * pad4(a.C) * sizeof(float));
     }
     if (a.dwg) {
         b.pw = plan_gemm(dev.sm_count, G_DW, P, 2 * int64_t(a.F), a.C, b.kr);
         if (b.pw.nsplit > 1)
-            b.part_w = b.s.take(size_t(b.pw.nsplit) * 2 * a.F * a.C * sizeof(float));
+            b.part_w = b.s.take(size_t(b.pw.nsplit) * 2 * a.F * pad4(a.C) * sizeof(float));
     }
     if (a.dbg)
         b.part_b = b.s.take(size_t(ceil_div(a.rows, b.pg.rows())) * b.pg.CG * 4 * 2 * a.F *
@@ -1101,7 +1126,7 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
                         make_map3(&m.b0, in.wg, 64) && make_map3(&m.b1, in.wu, 64);
         e = ok ? run_gemm<G_DX, P>(dev, m, g, px, true, st) : cudaErrorInvalidValue;
         if (e == cudaSuccess && g.nsplit > 1)
-            e = join<T>(g.part, g.nsplit, a.rows * a.C, a.rows * a.C, a.dx, nullptr, st);
+            e = join<T>(g.part, g.nsplit, a.rows, a.rows, a.C, a.dx, nullptr, st);
     }
     if (e == cudaSuccess && a.dwg) {
         GemmArgs g = gemm_args(dev, a);
@@ -1115,9 +1140,8 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
         const bool ok = make_map3(&m.a0, d[0], 64) && make_map3(&m.a1, d[1], 64) &&
                         make_map3(&m.b0, in.x, 64);
         e = ok ? run_gemm<G_DW, P>(dev, m, g, pw, true, st) : cudaErrorInvalidValue;
-        const int64_t n = int64_t(a.F) * a.C;
         if (e == cudaSuccess && g.nsplit > 1)
-            e = join<T>(g.part, g.nsplit, 2 * n, n, a.dwg, a.dwu, st);
+            e = join<T>(g.part, g.nsplit, 2 * int64_t(a.F), a.F, a.C, a.dwg, a.dwu, st);
     }
     if (e == cudaSuccess && a.dbg) {
         e = launch(true, gated_bias_kernel<T>, unsigned(ceil_div(2 * a.F, 32)), dim3(32, 32), 0, st,
