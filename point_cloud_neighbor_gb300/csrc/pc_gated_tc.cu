@@ -736,15 +736,23 @@ struct PackJob {
 struct PackJobs {
     PackJob job[3];
 };
-constexpr int PACK_ROWS = 16;
+constexpr int PACK_ROWS = 8;
 
 // Rows of T as P bfloat16 parts, padded to eight columns.
 template <class T, int P>
 __global__ void __launch_bounds__(256) gated_pack_kernel(PackJobs jobs) {
     let_next_start();
-    int b = blockIdx.x, k = 0;
-    while (k < 2 && b >= jobs.job[k].blocks) b -= jobs.job[k++].blocks;
-    const PackJob &j = jobs.job[k];
+    // (copied by constant indices: an index computed here would put them in local memory)
+    int b = blockIdx.x;
+    PackJob j = jobs.job[0];
+    if (b >= j.blocks) {
+        b -= j.blocks;
+        j = jobs.job[1];
+        if (b >= j.blocks) {
+            b -= j.blocks;
+            j = jobs.job[2];
+        }
+    }
     const int64_t r0 = int64_t(b) * PACK_ROWS;
     const int rows = int(min(int64_t(PACK_ROWS), j.rows - r0));
     const int groups = j.ld / 8;
