@@ -46,7 +46,8 @@
 // 1024 x 4096 270, 345, 293 and 301 us (2,030, 1,590, 1,880 and 1,830 TFLOP/s of 4 rows C
 // F each); 16,384 x 384 x 1024 20, 30, 26 and 24 us; 100,000 x 512 x 2048 with gelu
 // and biases 250 us forward; 32 x 384 x 1024 4 us.  float32, 4084 x 387 x 1021 with gelu:
-// 38, 51, 37 and 37 us, and 5.5 to split the operands.
+// and biases 43 us forward and 58 for GRAD; without, 37 and 50, and 44 us for DX and 45 for
+// DW, each alone (in a call they overlap); 5.5 to split the operands.
 //
 // Waits are bounded and end as in pc_attn_tc.cu; the blocks take more than half a
 // SM's shared memory, so none waits for another's tensor memory.
