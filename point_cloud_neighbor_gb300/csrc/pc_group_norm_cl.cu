@@ -612,8 +612,8 @@ GnCluster gn_cluster_plan(const DeviceInfo &dev, const GnArgs &a, int dtype, int
     // depend on them; the kernels for any size spread the values over all SMs, read them
     // twice and are three launches.  Measured, forward / backward with all gradients:
     // 16 x 1024 x 384 bf16 ragged (6 blocks a cloud in one wave / 9 in two) 16.9 / 23 against
-    // 21.9 / 28.2 (4 blocks 20.9, 8 18.5 / 24.6, 12 21.9 / 33, 16 28.8 / 37); 4 x 4093 x 195 bf16 (16 blocks, element by element) 25.9 / 40.4 against 22.8 / 30.9;
-    // 1 x 64 x 384 forward 8 against 11.
+    // 21.9 / 28.2 (4 blocks 20.9, 8 18.5 / 24.6, 12 21.9 / 33, 16 28.8 / 37); 4 x 4093 x 195 bf16 (16 blocks, element by
+    // element) 25.9 / 40.4 against 22.8 / 30.9; 1 x 64 x 384 forward 8 against 11.
     const int VB = V * (dtype == PC_F32 ? 4 : 2);
     const double each = (VB >= 16 ? 0.13 : VB >= 8 ? 0.2 : VB >= 4 ? 0.3 : 0.45) / 1000 *
                         (backward ? 1.3 : 1.0);

@@ -790,6 +790,53 @@ def test_other_streams_and_graphs(dtype):
                 assert torch.equal(a, e)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_forms_captured_with_their_gradients(dtype):
+    """A training step of the differentiable forms in a graph, captured without a run of
+    these sizes before it; replayed on other values it gives what an eager step does."""
+    idx, lengths, leaves, dy = chain_inputs(dtype, 11)
+    leaves = [t.requires_grad_() for t in leaves]
+    f = chain(idx, lengths, dtype)
+
+    def step():
+        y = f(*leaves)
+        return [y.detach(), *torch.autograd.grad(y, leaves, dy)]
+    pc.pc_embedding(leaves[0].detach(), idx)  # (the library knows the device)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = step()
+    for k in (1.0, -0.5, 2.0):
+        with torch.no_grad():
+            for t in (leaves[0], leaves[3], dy):
+                t.mul_(k)
+            idx.copy_(idx.roll(1, 0))
+            lengths.copy_(lengths.roll(1))
+        graph.replay()
+        for a, e in zip(got, step()):
+            assert torch.equal(a, e)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_large_calls_at_once_on_streams(dtype):
+    """Calls whose scratch comes from torch's allocator, in several streams at once."""
+    rows, C, F = 33000, 64, 512
+    assert rows * (C + 2 * F) >= pc.features.LARGE
+    ins = [gated_inputs(gen(20 + i), rows, C, F, dtype) for i in range(2)]
+    want = [gated_all(*x, "silu") for x in ins]
+    streams, got = [torch.cuda.Stream() for _ in ins], []
+    torch.cuda.synchronize()
+    for _ in range(3):
+        got = []
+        for s, x in zip(streams, ins):
+            with torch.cuda.stream(s):
+                got.append(gated_all(*x, "silu"))
+    torch.cuda.synchronize()
+    for a, e in zip(got, want):
+        for k in e:
+            assert torch.equal(a[k], e[k]), k
+
+
 def test_results_do_not_change_from_run_to_run():
     for dtype in DTYPES:
         ins = gated_inputs(gen(1), 3000, 128, 256, dtype)
