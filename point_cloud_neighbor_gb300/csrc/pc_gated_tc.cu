@@ -524,6 +524,9 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
                             dyraw[c] = *reinterpret_cast<const uint4 *>(row_part<CH>(dyroom, lane, c));
+                        // (every lane's loads are done before the next copy is issued: they
+                        // can wait behind stores for longer than the copy takes)
+                        fence_proxy_async_smem();
                         __syncwarp();
                         if (leader) dy_ahead(i + step);
                     } else {

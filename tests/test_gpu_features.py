@@ -920,3 +920,20 @@ def test_refusals():
                                               (16,)), "shape")]:
         with pytest.raises((ValueError, pc.PointCloudError), match=what):
             call()
+
+
+@pytest.mark.parametrize("shape", [(300, 304, 65536), (4096, 304, 4096)])
+def test_gated_linear_takes_each_value_of_grad_out_once(shape):
+    """Many tiles a block, each with its own part of grad_out, which is copied a tile ahead:
+    with rows of an identity the weights' gradients are da and du themselves."""
+    rows, C, F = shape
+    g = gen(31)
+    _, wg, wu, _, _, dy = gated_inputs(g, rows, C, F, torch.bfloat16, bias=False)
+    x = torch.eye(rows, C, device=DEV, dtype=torch.bfloat16)
+    n = min(rows, C)
+    want = gated_reference(x[:n], wg, wu, None, None, dy[:n], "silu")
+    for _ in range(4):
+        dx, dwg, dwu, _, _ = pc.pc_gated_linear_backward(dy, x, wg, wu)
+        close(dwg, *want["dwg"], "dwg")
+        close(dwu, *want["dwu"], "dwu")
+        close(dx[:n], *want["dx"], "dx")
