@@ -32,9 +32,11 @@
 // are added up in registers.  A bfloat16 chain over the rows is at most 16,384
 // long, joined in float32.
 //
-// da and du are operands of two products each and have to be bfloat16: one
-// rounding, which leaves dx and dW off by 1.41 times what rounding the results
-// does (a second part would double the work of both).  In float32 they are three parts.
+// da and du are operands of two products each.  bfloat16 calls take two bfloat16 parts
+// of them, what the first leaves and then the first itself (to 2^-17): one part is a rounding
+// of its own, which left dx and dW off by 1.41 times what rounding the results does.  So
+// the products of DX and DW are twice as many; a stage has both parts, and what they are
+// multiplied with once.  float32 calls take three parts.
 //
 // The biases' gradients are summed from the unrounded da and du: 32 rows by
 // shuffles in GRAD, the parts in a kernel of their own.
@@ -42,12 +44,15 @@
 // DX and DW split their contraction among blocks where there are few tiles; the
 // parts are added in a fixed order by a kernel of its own.
 //
-// Bound: the products, and where C is small the epilogue.  Measured, bfloat16: 32,768 x
-// 1024 x 4096 270, 345, 293 and 301 us (2,030, 1,590, 1,880 and 1,830 TFLOP/s of 4 rows C
-// F each); 16,384 x 384 x 1024 20, 30, 26 and 24 us; 100,000 x 512 x 2048 with gelu
-// and biases 250 us forward; 32 x 384 x 1024 4 us.  float32, 4084 x 387 x 1021 with gelu:
-// and biases 43 us forward and 58 for GRAD; without, 37 and 50, and 44 us for DX and 45 for
-// DW, each alone (in a call they overlap); 5.5 to split the operands.
+// Bound: the products, and where C is small the epilogue; GRAD of wide layers also the
+// 8 bytes a unit that it writes.  Measured, each launch alone, bfloat16: 32,768 x 1024 x 4096
+// 268, 387, 556 and 561 us (2,050, 1,420, 1,980 and 1,960 TFLOP/s of 4 rows C F each, DX
+// and DW 8); 16,384 x 384 x 1024 19, 45, 44 and 37 us; 100,000 x 512 x 2048 with gelu and
+// biases 241 us forward (250 to 298 in a run of such calls, with the clock that the power
+// limit leaves); 32 x 384 x 1024 4 us.  float32, 4084 x 387 x 1021 with gelu and biases: 43,
+// 58, 33 and 34 us, and 5 to split the operands.  da and du in one part took 350, 300 and 301
+// us instead of 387, 556 and 561; their two parts by tensor maps of 16 units instead of 32-byte
+// stores 449 instead of 400 (in a pass).
 //
 // Waits are bounded and end as in pc_attn_tc.cu; the blocks take more than half a
 // SM's shared memory, so none waits for another's tensor memory.
@@ -58,6 +63,7 @@
 #include "pc_tiles.cuh"
 #include "pointcloud.h"
 
+#include <cfloat>
 #include <type_traits>
 
 namespace pcn {
@@ -69,7 +75,7 @@ constexpr int PANEL = 64 * 128;  // bytes of a 64 x 64 panel of an MN-major oper
 
 struct GemmMaps {
     CUtensorMap a0, a1, b0, b1;
-    CUtensorMap dy, o0, o1;  // boxes of 32 rows: GRAD dy, da, du; FWD y in o0
+    CUtensorMap dy, o0, o1;  // boxes of 32 rows: GRAD dy, float32 da, du; FWD y in o0
 };
 
 // Columns of a row of parts, so that all are 16-byte aligned.
@@ -84,7 +90,7 @@ struct GemmArgs {
     void *out, *out2;    // y; dx; dWg and dWu
     float *part;         // [nsplit][rows of all outputs][pad4(N)] where nsplit > 1
     const void *bg, *bu, *dy;
-    bf16 *d;             // [da, du][parts][M][ld]
+    bf16 *d;             // [da, du][parts of each: grad_parts][M][ld]
     float *bpart;        // GRAD: [4 mt][da, du][N], sums over 32 rows, or NULL
     int ld, act;
     bool vec, dvec;      // rows of the output, of dy, in 16-byte vectors
@@ -93,12 +99,17 @@ struct GemmArgs {
     int *status;
 };
 
+// Parts of da and du in calls whose operands have P.
+__host__ __device__ constexpr int grad_parts(int P) { return P == 1 ? 2 : P; }
+
 template <int MODE, int P, int BN, int CG>
 struct GCfg {
     static constexpr bool PAIR = MODE == G_FWD || MODE == G_GRAD;
     static constexpr int A_BYTES = BM * 128, B_BYTES = BN / CG * 128;
     static constexpr int M = BM * CG;  // rows of a tile
-    static constexpr int STAGE = A_BYTES + B_BYTES;  // of one part of both operands
+    // parts of A in a stage, beside one of B: both of da or du in bfloat16
+    static constexpr int AP = !PAIR && P == 1 ? grad_parts(P) : 1;
+    static constexpr int STAGE = AP * A_BYTES + B_BYTES;
     // Warps that take the accumulators: four for the 128 rows, times parts of the columns.
     // 16 where a tile's arithmetic outlasts its products otherwise (4084 x 387 x 1021
     // float32: with 8 the gradients of gelu took half as long again).
@@ -109,14 +120,14 @@ struct GCfg {
     static constexpr int CH = PAIR ? NL / 2 : 32;     // PAIR: hidden units, else of a chunk
     static_assert(!PAIR || CH == 32 || CH == 16, "chunks");
     // PAIR: a warp's tiles of 32 rows by CH units of the arrays that are as large as the
-    // result, on their way from or to global memory (bfloat16: TILE bytes each): dy, da and
-    // du; y.  As tensor maps have them, or (float32, unaligned rows) as place() does.
+    // result, on their way from or to global memory (bfloat16: TILE bytes each): dy; y; in
+    // float32 da and du.  As tensor maps have them, or (float32, unaligned rows) as place()
+    // does.
     static constexpr bool STAGED = PAIR && BN >= 128;
     static constexpr int TILE = 64 * CH;
     // (plain results: where rows are not 16-byte aligned)
     static constexpr int ROOM =
-        !PAIR ? 1024 * (P > 1 ? 4 : 2)
-              : !STAGED ? 0 : (P > 1 || MODE == G_FWD ? (P > 1 ? 2 : 1) : 3) * TILE;
+        !PAIR ? 1024 * (P > 1 ? 4 : 2) : !STAGED ? 0 : (P > 1 ? 2 : 1) * TILE;
     static constexpr int FIT = (227 * 1024 - 1024 - 512 - EWARPS * ROOM) / STAGE,
                          STAGES = FIT > 8 ? 8 : FIT;
     static_assert(STAGES >= 2 * P, "shared memory");
@@ -186,6 +197,12 @@ __device__ __forceinline__ void put_row(unsigned char *tile, int lane, int o, co
                             v + 8 * c);
 }
 
+// What rounding v to bfloat16 leaves for a second part: nothing where that is infinite.
+__device__ __forceinline__ float left_over(float v) {
+    const float f = __bfloat162float(__float2bfloat16_rn(v));
+    return fabsf(f) <= FLT_MAX ? v - f : 0.0f;
+}
+
 // P parts of eight numbers, `plane` elements apart.
 template <int P>
 __device__ __forceinline__ void put_parts(bf16 *p, int64_t plane, const float *v) {
@@ -198,10 +215,34 @@ __device__ __forceinline__ void put_parts(bf16 *p, int64_t plane, const float *v
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             w[i] = pack_bf16(t[2 * i], t[2 * i + 1]);
-            const float2 f = unpack_bf16(w[i]);
-            t[2 * i] -= f.x, t[2 * i + 1] -= f.y;
+            if (P == 2) {
+                t[2 * i] = left_over(t[2 * i]), t[2 * i + 1] = left_over(t[2 * i + 1]);
+            } else {
+                const float2 f = unpack_bf16(w[i]);
+                t[2 * i] -= f.x, t[2 * i + 1] -= f.y;
+            }
         }
         *reinterpret_cast<uint4 *>(p + k * plane) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+}
+
+// Two parts of 16 numbers, `plane` elements apart: 32 bytes each, a whole sector of memory
+// in one store, so that a lane writes its row without a detour through shared memory.
+__device__ __forceinline__ void put_both(bf16 *p, int64_t plane, const float (&v)[16]) {
+    float t[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t[i] = v[i];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        uint32_t w[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) w[i] = pack_bf16(t[2 * i], t[2 * i + 1]);
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p + k * plane),
+                     "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]),
+                     "r"(w[7])
+                     : "memory");
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t[i] = left_over(t[i]);
     }
 }
 
@@ -302,16 +343,26 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
 #pragma unroll
                     for (int p = P - 1; p >= 0; --p) {
                         if (!(ok = await(&empty[s], phase))) break;
-                        unsigned char *A = base + size_t(s) * C::STAGE, *B = A + C::A_BYTES;
+                        unsigned char *A = base + size_t(s) * C::STAGE;
+                        unsigned char *B = A + C::AP * C::A_BYTES;
                         // (both blocks' bytes are counted in the first)
                         uint64_t *bar = &full[s];
                         if (rank == 0) mbar_arrive_expect_tx(bar, CG * C::STAGE);
                         const uint32_t pair_bar = CG > 1 ? map_shared_rank(bar, 0) : 0;
-                        auto load = [&](unsigned char *to, const CUtensorMap *map, int c, int r) {
+                        auto load_part = [&](unsigned char *to, const CUtensorMap *map, int c,
+                                             int r, int part) {
                             if (CG > 1)
-                                tma_load_3d_pair(to, map, c, r, p, pair_bar);
+                                tma_load_3d_pair(to, map, c, r, part, pair_bar);
                             else
-                                tma_load_3d(to, map, c, r, p, bar);
+                                tma_load_3d(to, map, c, r, part, bar);
+                        };
+                        auto load = [&](unsigned char *to, const CUtensorMap *map, int c, int r) {
+                            load_part(to, map, c, r, p);
+                        };
+                        auto load_a = [&](int at, const CUtensorMap *map, int c, int r) {
+#pragma unroll
+                            for (int ap = 0; ap < C::AP; ++ap)
+                                load_part(A + ap * C::A_BYTES + at, map, c, r, p + ap);
                         };
                         if (C::PAIR) {
                             load(A, &maps.a0, k * BK, m0);
@@ -326,15 +377,15 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                             if (MODE == G_DX) {
                                 const bool up = k >= a.kb0;
                                 const int f = (up ? k - a.kb0 : k) * BK;
-                                load(A, up ? &maps.a1 : &maps.a0, f, m0);
+                                load_a(0, up ? &maps.a1 : &maps.a0, f, m0);
 #pragma unroll
                                 for (int j = 0; j < BN / CG / 64; ++j)
                                     load(B + j * PANEL, up ? &maps.b1 : &maps.b0, n0 + 64 * j, f);
                             } else {
 #pragma unroll
                                 for (int j = 0; j < BM / 64; ++j)
-                                    load(A + j * PANEL, it.m >= dw_mt ? &maps.a1 : &maps.a0,
-                                         m0 + 64 * j, k * BK);
+                                    load_a(j * PANEL, it.m >= dw_mt ? &maps.a1 : &maps.a0,
+                                           m0 + 64 * j, k * BK);
 #pragma unroll
                                 for (int j = 0; j < BN / CG / 64; ++j)
                                     load(B + j * PANEL, &maps.b0, n0 + 64 * j, k * BK);
@@ -355,7 +406,7 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
             constexpr uint32_t id = mma_idesc(BN, BR, AR, C::M);
             constexpr uint32_t da = AR ? 16 * 128 / 16 : 2, db = BR ? 16 * 128 / 16 : 2;
             const uint32_t a0 = smem_operand(smem_u32(base), AR ? PANEL : 16);
-            const uint32_t b0 = smem_operand(smem_u32(base) + C::A_BYTES, BR ? PANEL : 16);
+            const uint32_t b0 = smem_operand(smem_u32(base) + C::AP * C::A_BYTES, BR ? PANEL : 16);
             int s = 0, buf = 0;
             unsigned phase = 0, aphase = 1;
             bool ok = true;
@@ -383,9 +434,10 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                     const uint32_t d = tmem + buf * BN;
                     // a stage is free after the last product that takes its part
 #pragma unroll
-                    for (int q = 0; q < (P == 1 ? 1 : 6); ++q) {
+                    for (int q = 0; q < (P == 1 ? C::AP : 6); ++q) {
                         const int pa = P == 1 ? 0 : PART_A[q], pb = P == 1 ? 0 : PART_B[q];
-                        const uint32_t as = a0 + at[pa] * (C::STAGE / 16),
+                        const int ap = P == 1 ? C::AP - 1 - q : 0;
+                        const uint32_t as = a0 + at[pa] * (C::STAGE / 16) + ap * (C::A_BYTES / 16),
                                        bs = b0 + at[pb] * (C::STAGE / 16);
 #pragma unroll
                         for (int j = 0; j < BK / 16; ++j)
@@ -395,7 +447,7 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                             else
                                 mma_ss<SMEM_128B>(d, as + j * da, bs + j * db, id,
                                                   !fresh || q > 0 || j > 0);
-                        if (P == 1 || q == 5) commit(&empty[at[0]]);
+                        if (P == 1 ? q == C::AP - 1 : q == 5) commit(&empty[at[0]]);
                         if (P > 1 && q == 4) commit(&empty[at[P > 1 ? 1 : 0]]);
                         if (P > 1 && q == 1) commit(&empty[at[P > 1 ? 2 : 0]]);
                     }
@@ -429,9 +481,7 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
             buf ^= 1;
             if (buf == 0) phase ^= 1;
         };
-        // the warp's room: dy behind da and du where there are three
-        unsigned char *room = rooms + (warp - 4) * C::ROOM;
-        unsigned char *dyroom = room + (P == 1 && MODE == G_GRAD ? 2 * C::TILE : 0);
+        unsigned char *room = rooms + (warp - 4) * C::ROOM, *dyroom = room;  // the warp's
         const bool leader = elect_one();
         // Where column c of row r of an unaligned array is, so that neither the lanes of a
         // row nor those of a column meet in a bank.
@@ -510,11 +560,13 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                 if (!ok) break;
             }
             if constexpr (C::PAIR) {
-                constexpr int SUB = C::EWARPS == 16 ? 16 : CH;  // units at a time
+                // units at a time
+                constexpr int SUB = C::EWARPS == 16 || (MODE == G_GRAD && C::STAGED) ? 16 : CH;
                 const int64_t row0 = tile_row(it), row = row0 + lane;
                 const int c0 = tile_column(it), left = row < a.M ? a.N - c0 : 0;
                 const bool live = row0 < a.M && c0 < a.N;  // the warp has something to write
                 const T *dysrc = static_cast<const T *>(a.dy);
+                constexpr int DP = grad_parts(P);
                 uint4 dyraw[AHEAD ? 4 : 1];  // the thread's 32 units of dy
                 if constexpr (AHEAD) {
                     if (a.dvec) {
@@ -544,7 +596,7 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                     tc_fence_after();
                 }
                 if (C::STAGED) {
-                    if (P == 1 && leader) bulk_wait_read_all();  // the room is free
+                    if (P == 1 && MODE == G_FWD && leader) bulk_wait_read_all();  // the room is free
                     __syncwarp();
                 }
 #pragma unroll
@@ -625,12 +677,17 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
 #pragma unroll
                             for (int c = 0; c < SUB; c += 8)
                                 if (c < left) {  // (the rows' padding takes zeros)
-                                    put_parts<P>(to + c, plane, g + c);
-                                    put_parts<P>(to + P * plane + c, plane, u + c);
+                                    put_parts<DP>(to + c, plane, g + c);
+                                    put_parts<DP>(to + DP * plane + c, plane, u + c);
                                 }
                         } else if constexpr (P == 1) {
-                            put_row<CH, SUB>(room, lane, o, g);
-                            put_row<CH, SUB>(room + C::TILE, lane, o, u);
+                            if (row < a.M && c0 + o < a.N) {
+                                const int64_t plane = a.M * a.ld;
+                                bf16 *to = a.d + row * a.ld + c0 + o;
+                                put_both(to, plane, g);
+                                put_both(to + DP * plane, plane, u);
+                            }
+                            __syncwarp();  // (the loads from tensor memory take whole warps)
                         } else {
                             // three parts, one after the other through the room
                             __syncwarp();
@@ -656,14 +713,12 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                         }
                     }
                 }
-                if constexpr (C::STAGED && (P == 1 || MODE == G_FWD)) {
-                    if (MODE == G_GRAD || (P == 1 && a.vec)) {
+                if constexpr (C::STAGED && MODE == G_FWD) {
+                    if (P == 1 && a.vec) {
                         fence_proxy_async_smem();
                         __syncwarp();
                         if (leader && live) {
                             tma_store_3d(&maps.o0, room, c0, int(row0), 0);
-                            if (MODE == G_GRAD)
-                                tma_store_3d(&maps.o1, room + C::TILE, c0, int(row0), 0);
                             bulk_commit();
                         }
                     } else {
@@ -898,7 +953,7 @@ GemmPlan plan_gemm(int sms, int mode, int P, int64_t M, int64_t N, int64_t kb) {
     const bool pair = mode == G_FWD || mode == G_GRAD;
     for (const GemmKind &kind : KINDS) {
         if (P > 1 && kind.BN == 256) continue;
-        const double stage = kind.stage * (P == 1 ? 1.0 : 6.3);
+        const double stage = kind.stage * (P > 1 ? 6.3 : pair ? 1.0 : grad_parts(P));
         const double epilogue = (mode == G_FWD    ? kind.forward
                                  : mode == G_GRAD ? kind.grad
                                                   : kind.plain) *
@@ -1024,8 +1079,8 @@ template <class T, int P>
 BackwardPlan plan_backward(const DeviceInfo &dev, const GatedArgs &a) {
     BackwardPlan b;
     plan_inputs<T, P>(a, b.in, b.s);
-    b.ld = pad8(a.F);
-    b.d_at = b.s.take(size_t(2) * P * a.rows * b.ld * sizeof(bf16));
+    b.ld = P == 1 ? (a.F + 15) / 16 * 16 : pad8(a.F);  // (16 units go in one store: put_both)
+    b.d_at = b.s.take(size_t(2) * grad_parts(P) * a.rows * b.ld * sizeof(bf16));
     b.pg = plan_gemm(dev.sm_count, G_GRAD, P, a.rows, a.F, ceil_div(a.C, BK));
     b.kf = int(ceil_div(a.F, BK)), b.kr = int(ceil_div(a.rows, BK));
     if (a.dx) {
@@ -1104,8 +1159,9 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
     e = pack_inputs<T, P>(a, in, s, st);
     Operand d[2];
     for (int i = 0; i < 2; ++i) {
-        d[i].p = reinterpret_cast<const bf16 *>(s.base + b.d_at) + int64_t(i) * P * a.rows * ld;
-        d[i].rows = a.rows, d[i].cols = a.F, d[i].ld = ld, d[i].parts = P;
+        d[i].rows = a.rows, d[i].cols = a.F, d[i].ld = ld, d[i].parts = grad_parts(P);
+        d[i].p = reinterpret_cast<const bf16 *>(s.base + b.d_at) +
+                 int64_t(i) * d[i].parts * a.rows * ld;
     }
     auto partials = [&](size_t at) { return reinterpret_cast<float *>(s.base + at); };
     if (e == cudaSuccess) {
@@ -1120,8 +1176,8 @@ cudaError_t backward(const DeviceInfo &dev, const GatedArgs &a, cudaStream_t st)
         const bool ok = make_map3(&m.a0, in.x, BM) &&
                         make_map3(&m.b0, in.wg, p.BN / 2) &&
                         make_map3(&m.b1, in.wu, p.BN / 2) &&
-                        make_map3(&m.o0, d[0], 32, P > 1 ? 16 : 32) &&
-                        make_map3(&m.o1, d[1], 32, P > 1 ? 16 : 32) &&
+                        (P == 1 || (make_map3(&m.o0, d[0], 32, 16) &&
+                                    make_map3(&m.o1, d[1], 32, 16))) &&
                         (P > 1 || !g.dvec || make_tile_map(&m.dy, a.dy, a.rows, a.F, a.F));
         e = ok ? run_gemm<G_GRAD, P>(dev, m, g, p, in.any(), st) : cudaErrorInvalidValue;
     }

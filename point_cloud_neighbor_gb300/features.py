@@ -197,7 +197,9 @@ def pc_gated_linear_backward(grad_out: torch.Tensor, x: torch.Tensor, w_gate: to
                              need_weight: bool = True, need_bias: bool = True):
     """Gradients of :func:`pc_gated_linear`: (grad_x, grad_w_gate, grad_w_up,
     grad_b_gate, grad_b_up), None for what is not needed or was None.  Nothing
-    of the forward call is needed but its arguments."""
+    of the forward call is needed but its arguments.  Only the results are rounded
+    to the type: in bfloat16 the gradients of the two projections enter their
+    products in two parts."""
     index, args, F = _gated_args(x, w_gate, w_up, b_gate, b_up, activation)
     _same(grad_out, "grad_out", (*x.shape[:-1], F), x.dtype, index)
     dx = torch.empty_like(x) if need_x else None

@@ -937,3 +937,41 @@ def test_gated_linear_takes_each_value_of_grad_out_once(shape):
         close(dwg, *want["dwg"], "dwg")
         close(dwu, *want["dwu"], "dwu")
         close(dx[:n], *want["dx"], "dx")
+
+
+@pytest.mark.parametrize("shape", [(300, 384, 512), (4099, 64, 80), (40, 777, 1000), (6, 500, 900),
+                                   (2100, 136, 3000), (20000, 520, 264), (129, 72, 17)])
+def test_gated_linear_gradients_are_rounded_once(shape):
+    """bfloat16: da and du enter the products of grad_x and the weights' gradients as two
+    bfloat16 parts (off by 2^-18), so that the error in norm is that of rounding the float64
+    gradients once, and 2% for what else there is: the approximate silu and its derivative
+    (2^-21 (|a| + 8), here at most 2^-17), the parts, and sums that are cut off (below 2^-15 of
+    the sum of magnitudes, which is at most 30 times a sum of as many terms of random sign)."""
+    rows, C, F = shape
+    ins = x, wg, wu, bg, bu, dy = gated_inputs(gen(21), rows, C, F, torch.bfloat16)
+    got = gated_all(*ins, "silu")
+    a, u = (x.double() @ w.double().T + b.double() for w, b in ((wg, bg), (wu, bu)))
+    f, df = act64(a, "silu")
+    da, du = dy.double() * u * df, dy.double() * f
+    want = {"dx": da @ wg.double() + du @ wu.double(), "dwg": da.T @ x.double(),
+            "dwu": du.T @ x.double(), "dbg": da.sum(0), "dbu": du.sum(0)}
+    for name, w in want.items():
+        e = float((got[name].double() - w).norm() / w.norm())
+        r = float((w.bfloat16().double() - w).norm() / w.norm())
+        assert e <= 1.02 * r, f"{name}: {e:.4g} against {r:.4g}"
+
+
+def test_gated_linear_infinite_gradients_stay_infinite():
+    """bfloat16: what rounding leaves of an infinity is no second part."""
+    x, wg, wu, bg, bu, dy = gated_inputs(gen(22), 70, 64, 72, torch.bfloat16)
+    dy[3, 5] = math.inf
+    dx, dwg, dwu, _, _ = pc.pc_gated_linear_backward(dy, x, wg, wu, bg, bu)
+    a, u = (x[3].double() @ w[5].double() + b[5].double() for w, b in ((wg, bg), (wu, bu)))
+    f, df = act64(a, "silu")
+    for got, ref in ((dwg[5], math.inf * u * df * x[3].double()),
+                     (dwu[5], math.inf * f * x[3].double())):
+        assert torch.equal(got.double(), ref)
+    both = math.inf * u * df * wg[5].double() + math.inf * f * wu[5].double()  # inf, -inf or NaN
+    assert torch.equal(dx[3].double().nan_to_num(7.0), both.nan_to_num(7.0))
+    keep = torch.arange(70, device=DEV) != 3
+    assert torch.isfinite(dx[keep]).all()
