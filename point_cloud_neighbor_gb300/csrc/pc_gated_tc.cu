@@ -664,6 +664,10 @@ gated_gemm_kernel(const __grid_constant__ GemmMaps maps, const GemmArgs a) {
                             }
                         });
                         if (a.bpart != nullptr) {  // (before they are rounded)
+                            // (rows past the end have the biases' values, times 0)
+                            if (row >= a.M)
+#pragma unroll
+                                for (int c = 0; c < SUB; ++c) g[c] = u[c] = 0.0f;
                             const float sg = column_sums<SUB>(g, lane);
                             const float su = column_sums<SUB>(u, lane);
                             float *to = a.bpart +

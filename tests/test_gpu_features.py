@@ -975,3 +975,18 @@ def test_gated_linear_infinite_gradients_stay_infinite():
     assert torch.equal(dx[3].double().nan_to_num(7.0), both.nan_to_num(7.0))
     keep = torch.arange(70, device=DEV) != 3
     assert torch.isfinite(dx[keep]).all()
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("rows", [1, 70, 300])
+def test_gated_linear_bias_gradients_of_infinite_biases(rows, dtype):
+    """The sums over the rows are those of the rows alone, whatever the biases are."""
+    x, wg, wu, bg, bu, dy = gated_inputs(gen(23), rows, 64, 72, dtype)
+    dy = dy.abs() + 0.5
+    want = pc.pc_gated_linear_backward(dy, x, wg, wu, bg, bu, activation="sigmoid")
+    bu = bu.clone()
+    bu[5] = math.inf
+    _, _, _, dbg, dbu = pc.pc_gated_linear_backward(dy, x, wg, wu, bg, bu, activation="sigmoid")
+    assert dbg[5] == math.inf and torch.equal(dbu, want[4])
+    keep = torch.arange(72, device=DEV) != 5
+    assert torch.equal(dbg[keep], want[3][keep])
