@@ -990,3 +990,41 @@ def test_gated_linear_bias_gradients_of_infinite_biases(rows, dtype):
     assert dbg[5] == math.inf and torch.equal(dbu, want[4])
     keep = torch.arange(72, device=DEV) != 5
     assert torch.equal(dbg[keep], want[3][keep])
+
+
+def test_gelu_s_far_side_in_bfloat16():
+    """gelu(z) and its derivative where the normal distribution's function is small: half a
+    unit of bfloat16 (its numbers from 1 to 2 are 2^-7 apart: at most 2^-8 of the value), and
+    2^-16 for the approximation (9e-6 of the distribution's function, a few units of float32
+    beside) of the terms that enter; below float32's normal numbers, 1e-37 |z|."""
+    def gelu64(v):   # (by erfc: 1 + erf keeps no digits there)
+        c = 0.5 * torch.erfc(-v * math.sqrt(0.5))
+        return v * c, c, v * torch.exp(-v * v / 2) / math.sqrt(2 * math.pi)
+
+    z = torch.arange(-13.25, 4.0, 2.0 ** -6, device=DEV, dtype=torch.float64).bfloat16()
+    z = z.unique()
+    rows = z.numel()
+    x = torch.zeros(rows, 8, device=DEV, dtype=torch.bfloat16)
+    x[:, 0], x[:, 1] = z, 1.0
+    wg, wu = (torch.zeros(8, 8, device=DEV, dtype=torch.bfloat16) for _ in range(2))
+    wg[:, 0], wu[:, 1] = 1.0, 1.0            # a = z, u = 1
+    dy = torch.zeros(rows, 8, device=DEV, dtype=torch.bfloat16)
+    dy[:, 3] = 1.0
+    y = pc.pc_gated_linear(x, wg, wu, activation="gelu")
+    dx, *_ = pc.pc_gated_linear_backward(dy, x, wg, wu, activation="gelu")
+    z = z.double()
+    f, c, g = gelu64(z)
+    low = 1e-37 * (1 + z.abs())
+    close(y, f[:, None].expand(rows, 8), (f.abs() * (HALF[torch.bfloat16] + 2.0 ** -16) + low)[:, None], "y")
+    close(dx[:, 0], c + g, (c + g).abs() * HALF[torch.bfloat16] + (c + g.abs()) * 2.0 ** -16 + low,
+          "dx")
+    # group norm's results take the same function: one row of +-z is its own norm
+    v = torch.cat([z, -z]).view(1, -1, 1)
+    s = (v * v).mean().sqrt()
+    h = pc.pc_group_norm((v / s).bfloat16(), 1, s.float().view(1), eps=0.0, activation="gelu")
+    q = (v / s).bfloat16().double()
+    w = float(s.float()) * (q - q.mean()) / ((q - q.mean()) ** 2).mean().sqrt()
+    want, c, g = gelu64(w)
+    # (w itself is off by a few units of float32 of the largest)
+    close(h, want, want.abs() * (HALF[torch.bfloat16] + 2.0 ** -16)
+          + (c + g).abs() * 64 * U * w.abs().max() + 1e-37 * (1 + w.abs()), "group norm")
