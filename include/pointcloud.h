@@ -682,8 +682,11 @@ typedef enum pc_activation {
  * are read once, in one launch, where that is the shorter way; its waits are bounded
  * as those of the attention kernels.
  *
+ * The parameters' gradients are added over clouds in spans of 1024 (up to 64 clouds one
+ * after the other), so that no chain of additions grows with their number.
+ *
  * Scratch (the library's stream-ordered pool): forward 2 float32 for each group and
- * block and each group and cloud, backward 2 C float32 for each block and cloud; the
+ * block and each group and cloud, backward 2 C float32 for each block, cloud and span; the
  * blocks are at most 8 a SM, or one a cloud (16 in a cluster) where that is more.
  */
 int pc_group_norm(const void *x, int dtype, int64_t B, int64_t L, int64_t C, int64_t groups,

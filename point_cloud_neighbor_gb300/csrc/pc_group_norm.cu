@@ -355,8 +355,13 @@ __global__ void __launch_bounds__(1024) gn_channel_kernel(GnArgs a) {
     }
 }
 
-// Backward 3: dx; the blocks from `nparam` on.  The first ones add the channels'
-// sums over the clouds: dw and db.
+// Up to as many clouds a thread adds dw and db one cloud after the other, in blocks of
+// the last kernel; for more in kernels of their own (gn_param_sums): 8192 clouds of
+// 32 x 128 bfloat16 took 836 us with all of them in one thread's chain, 571 us so.
+constexpr int PARAM_CLOUDS = 64;
+
+// Backward 3: dx.  The last `nparam` blocks add the channels' sums over the clouds,
+// of which there are few (PARAM_CLOUDS) then: dw and db.
 template <class T, int V>
 __global__ void __launch_bounds__(GN_THREADS) gn_dx_kernel(GnArgs a, int nblk, int nparam) {
     let_next_start();
@@ -534,16 +539,21 @@ cudaError_t gn_run(GnArgs a, const GnPlan &p) {
         if (e == cudaSuccess)
             e = launch(true, gn_apply_kernel<T, V>, grid2, GN_THREADS, 0, st, a, second);
     } else {
-        const size_t parts = size_t(a.B) * a.nblk * 2 * a.C * sizeof(float);
-        const size_t chan = size_t(a.B) * 2 * a.C * sizeof(float);
-        if ((e = scratch_alloc(*p.dev, &scratch, parts + chan, st)) != cudaSuccess) return e;
+        const bool params = a.dw || a.db, apart = params && a.B > PARAM_CLOUDS;
+        const size_t parts = size_t(a.B) * a.nblk * 2 * a.C, chan = size_t(a.B) * 2 * a.C;
+        const size_t room = apart ? gn_param_room(a.B, a.C) : 0;
+        if ((e = scratch_alloc(*p.dev, &scratch, (parts + chan + room) * sizeof(float), st)) !=
+            cudaSuccess)
+            return e;
         a.cpart = static_cast<float *>(scratch);
-        a.chan = a.cpart + parts / sizeof(float);
+        a.chan = a.cpart + parts;
         e = launch(false, gn_sums_kernel<T, V>, grid, GN_THREADS, 0, st, a);
         if (e == cudaSuccess)
             e = launch(true, gn_channel_kernel, unsigned(a.B * ((2 * a.C + 31) / 32)), dim3(32, 32),
                        0, st, a);
-        const int nparam = a.dw || a.db ? int(ceil_div(2 * a.C, GN_THREADS)) : 0;
+        if (e == cudaSuccess && apart)
+            e = gn_param_sums(a, sizeof(T) == 2 ? PC_BF16 : PC_F32, a.chan, a.B, a.chan + chan, st);
+        const int nparam = params && !apart ? int(ceil_div(2 * a.C, GN_THREADS)) : 0;
         const unsigned dxgrid = a.y ? grid2 : 0;
         if (e == cudaSuccess && dxgrid + nparam > 0)
             e = launch(true, gn_dx_kernel<T, V>, dxgrid + nparam, GN_THREADS, 0, st, a, second,

@@ -110,6 +110,15 @@ struct GnChannels {
     }
 };
 
+// dw and db (a's) from n rows of the channels' sums of d and d xhat, [n][2][C]: rows in
+// spans of GN_SPAN, whose sums are the next rows, as long as there are several.  So a
+// channel's chain of additions grows by 64 for a factor of GN_SPAN in n.  `room`:
+// gn_param_room(n, C) floats.  Launched behind the kernel that writes the rows.
+constexpr int GN_SPAN = 1024;
+size_t gn_param_room(int64_t n, int C);
+cudaError_t gn_param_sums(const GnArgs &a, int dtype, const float *rows, int64_t n, float *room,
+                          cudaStream_t st);
+
 // Clouds that fit the shared memory of a cluster (pc_group_norm_cl.cu): whether these
 // do, and the launch.
 struct GnCluster {

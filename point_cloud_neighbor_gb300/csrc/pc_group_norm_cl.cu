@@ -490,23 +490,32 @@ __global__ void __launch_bounds__(CT, 1) gn_cluster_backward_kernel(ClArgs k) {
     }
 }
 
-// dw and db: the blocks' sums, 32 columns a block, 32 warps every 32nd part.
+// A span of rows of the channels' sums, 32 columns a block, 32 warps every 32nd row: to a
+// row of `next`, or where it is NULL (one span) to dw and db.
 template <class T>
 __global__ void __launch_bounds__(1024)
-gn_param_kernel(const float *part, int64_t nparts, int C, bool f32, void *db, void *dw) {
+gn_param_kernel(const float *part, int64_t nparts, int C, bool f32, void *db, void *dw,
+                float *next) {
+    let_next_start();
     after_previous();
     __shared__ float acc[32][33];
-    const int c = blockIdx.x * 32 + threadIdx.x;
+    const unsigned columns = (2 * C + 31) / 32, span = blockIdx.x / columns;
+    const int c = int(blockIdx.x - span * columns) * 32 + threadIdx.x;
+    const int64_t p0 = int64_t(span) * GN_SPAN, p1 = min(nparts, p0 + GN_SPAN);
     float s = 0.0f;
     if (c < 2 * C)
 #pragma unroll 4
-        for (int64_t p = threadIdx.y; p < nparts; p += 32) s += part[p * 2 * C + c];
+        for (int64_t p = p0 + threadIdx.y; p < p1; p += 32) s += part[p * 2 * C + c];
     acc[threadIdx.y][threadIdx.x] = s;
     __syncthreads();
     if (threadIdx.y == 0 && c < 2 * C) {
         s = 0.0f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) s += acc[i][threadIdx.x];
+        if (next != nullptr) {
+            next[int64_t(span) * 2 * C + c] = s;
+            return;
+        }
         void *out = c < C ? db : dw;
         const int at = c < C ? c : c - C;
         if (out == nullptr) return;
@@ -535,10 +544,10 @@ cudaError_t run(const DeviceInfo &dev, GnArgs a, bool backward, const GnCluster 
     }
     void *scratch = nullptr;
     const bool params = backward && (a.dw || a.db);
+    const int64_t rows = a.B * p.blocks;
     if (params) {
-        if ((e = scratch_alloc(dev, &scratch, size_t(a.B) * p.blocks * 2 * a.C * sizeof(float),
-                               st)) != cudaSuccess)
-            return e;
+        const size_t floats = size_t(rows) * 2 * a.C + gn_param_room(rows, a.C);
+        if ((e = scratch_alloc(dev, &scratch, floats * sizeof(float), st)) != cudaSuccess) return e;
         a.cpart = static_cast<float *>(scratch);
     }
     ClArgs k{a, p.blocks, p.bytes, (debug_stall() & PC_STALL_GROUP_NORM) != 0, wait_timeout_ns(),
@@ -556,10 +565,9 @@ cudaError_t run(const DeviceInfo &dev, GnArgs a, bool backward, const GnCluster 
     cfg.numAttrs = p.blocks > 1 ? 1 : 0;
     void *args[] = {&k};
     e = cudaLaunchKernelExC(&cfg, fn, args);
-    if (e == cudaSuccess && params) {
-        e = launch(true, gn_param_kernel<T>, unsigned((2 * a.C + 31) / 32), dim3(32, 32), 0, st,
-                   a.cpart, a.B * p.blocks, a.C, a.wf32, a.db, a.dw);
-    }
+    if (e == cudaSuccess && params)
+        e = gn_param_sums(a, sizeof(T) == 2 ? PC_BF16 : PC_F32, a.cpart, rows,
+                          a.cpart + size_t(rows) * 2 * a.C, st);
     if (scratch) {
         const cudaError_t f = scratch_free(scratch, st);
         if (e == cudaSuccess) e = f;
@@ -600,6 +608,31 @@ int active_clusters(const DeviceInfo &dev, int K) {
 }
 
 }  // namespace
+
+size_t gn_param_room(int64_t n, int C) {
+    size_t floats = 0;
+    while (n > GN_SPAN) {
+        n = (n + GN_SPAN - 1) / GN_SPAN;
+        floats += size_t(n) * 2 * C;
+    }
+    return floats;
+}
+
+cudaError_t gn_param_sums(const GnArgs &a, int dtype, const float *rows, int64_t n, float *room,
+                          cudaStream_t st) {
+    const unsigned columns = unsigned((2 * a.C + 31) / 32);
+    auto kernel = dtype == PC_F32 ? gn_param_kernel<float> : gn_param_kernel<bf16>;
+    while (n > GN_SPAN) {
+        const int64_t spans = (n + GN_SPAN - 1) / GN_SPAN;
+        const cudaError_t e = launch(true, kernel, unsigned(spans) * columns, dim3(32, 32), 0, st,
+                                     rows, n, a.C, a.wf32, a.db, a.dw, room);
+        if (e != cudaSuccess) return e;
+        rows = room, n = spans;
+        room += size_t(spans) * 2 * a.C;
+    }
+    return launch(true, kernel, columns, dim3(32, 32), 0, st, rows, n, a.C, a.wf32, a.db, a.dw,
+                  nullptr);
+}
 
 GnCluster gn_cluster_plan(const DeviceInfo &dev, const GnArgs &a, int dtype, int V,
                           bool backward) {

@@ -1028,3 +1028,27 @@ def test_gelu_s_far_side_in_bfloat16():
     # (w itself is off by a few units of float32 of the largest)
     close(h, want, want.abs() * (HALF[torch.bfloat16] + 2.0 ** -16)
           + (c + g).abs() * 64 * U * w.abs().max() + 1e-37 * (1 + w.abs()), "group norm")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("shape", [(65, 40, 24, 3), (1025, 9, 40, 5), (8192, 32, 128, 32),
+                                   (65536, 8, 16, 4)])
+def test_group_norm_of_many_clouds(shape, dtype):
+    """The parameters' gradients are sums over all clouds whose chains of additions do not grow
+    with their number: a cloud's L points (and 8 joins), then 64 for every factor of 1024."""
+    B, L, C, G = shape
+    g = gen(B)
+    x, dy = randn(g, B, L, C, dtype=dtype), randn(g, B, L, C, dtype=dtype)
+    w, b = randn(g, C) + 1, randn(g, C)
+    lengths = torch.randint(0, L + 1, (B,), generator=g, device=DEV)
+    got = gn_all(x, G, w, b, "sigmoid", lengths, dy)
+    for name, (want, tol) in gn_reference(x, G, w, b, 1e-5, "sigmoid", lengths, dy).items():
+        close(got[name], want, tol, name)
+    # a cloud's sum of 1 + 7 / 2^13: a chain over the clouds drops the fraction from 2^14 on
+    if dtype is torch.float32 and L == 8:
+        dy.fill_((1 + 7 * 2.0 ** -13) / 8)
+        one = torch.ones(C, device=DEV)
+        y, m, r = pc.pc_group_norm(x, G, one, one, return_stats=True)
+        _, _, db = pc.pc_group_norm_backward(dy, x, m, r, G, one, one)
+        want = torch.full((C,), B * (1 + 7 * 2.0 ** -13), device=DEV, dtype=torch.float64)
+        close(db, want, (L + 8 + 2 * 64) * U * want, "db")
