@@ -33,26 +33,28 @@ __device__ __forceinline__ float logistic(float z) {
 // The normal distribution's cumulative function and e = exp(-z^2 / 2), the far negative
 // side with its relative accuracy.  Not FAST: by erfc.  FAST, for results that are rounded
 // to bfloat16:
-//   erfc(x) = (a1 t + ... + a6 t^6) exp(-x^2),  t = 1 / (1 + p x),  x = |z| / sqrt(2),
+//   erfc(x) = (a1 t + ... + a7 t^7) exp(-x^2),  t = 1 / (1 + p x),  x = |z| / sqrt(2),
 // the form of Hastings's approximations (formula 7.1.26 of Abramowitz and Stegun's Handbook
 // of Mathematical Functions), with coefficients fitted here by linear programming so that
-// the largest relative error over x <= 9.5 (beyond, e is below float32) is least: 3.7e-6,
-// 9e-6 with the roundings.  The printed formula's is absolute (1.5e-7), which leaves 0.7% at
-// z = -7.  It takes half the instructions of erff and shares the exponential with the
-// derivative.
+// the largest relative error over x <= 9.5 (beyond, e is below float32) is least: 5e-7,
+// with the roundings (of the exponent, mostly) 2e-6 from z = -5 on and 8e-6 at the end.  The
+// printed formula's is absolute (1.5e-7), which leaves 0.7% at z = -7.  (With a term less
+// 3.7e-6, which float32 sums of the derivative over many points show.)  It takes half the
+// instructions of erff and shares the exponential with the derivative.
 template <bool FAST>
 __device__ __forceinline__ float normal_cdf(float z, float &e) {
     if (!FAST) {
         e = expf(-0.5f * z * z);
         return 0.5f * erfcf(-0.70710678118654752f * z);
     }
-    const float t = approx_rcp(fmaf(fabsf(z), 0.43500586f * 0.70710678f, 1.0f));
+    const float t = approx_rcp(fmaf(fabsf(z), 0.37339323f * 0.70710678f, 1.0f));
     e = approx_ex2(-0.5f * LOG2_E * z * z);
-    float p = fmaf(0.5f * -0.15174185f, t, 0.5f * 0.38379788f);
-    p = fmaf(p, t, 0.5f * 0.01013461f);
-    p = fmaf(p, t, 0.5f * 0.27484558f);
-    p = fmaf(p, t, 0.5f * 0.2370009f);
-    p = fmaf(p, t, 0.5f * 0.24595915f);
+    float p = fmaf(0.5f * -0.13863525f, t, 0.5f * 0.4069617f);
+    p = fmaf(p, t, 0.5f * -0.15283303f);
+    p = fmaf(p, t, 0.5f * 0.29764012f);
+    p = fmaf(p, t, 0.5f * 0.16079962f);
+    p = fmaf(p, t, 0.5f * 0.21569888f);
+    p = fmaf(p, t, 0.5f * 0.21036738f);
     const float q = p * t * e;
     return z < 0.0f ? q : 1.0f - q;
 }

@@ -1052,3 +1052,34 @@ def test_group_norm_of_many_clouds(shape, dtype):
         _, _, db = pc.pc_group_norm_backward(dy, x, m, r, G, one, one)
         want = torch.full((C,), B * (1 + 7 * 2.0 ** -13), device=DEV, dtype=torch.float64)
         close(db, want, (L + 8 + 2 * 64) * U * want, "db")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+@pytest.mark.parametrize("act", ["gelu", "silu"])
+def test_group_norm_parameter_gradients_in_norm(act, dtype):
+    """float32 sums of the derivative over 16,000 points, whose own errors have random signs:
+    what the approximate functions of bfloat16 calls leave does not, so the error in norm is
+    at most theirs (2^-21 of the terms, to be compared with the sums of as many terms of random
+    sign: a factor of up to 2) beside twice that of the float32 form."""
+    g = gen(41)
+    B, L, C, G = 4, 4093, 195, 13
+    x, dy = ((1.5 * randn(g, B, L, C)).to(dtype), randn(g, B, L, C, dtype=dtype))
+    w, b = 1 + 0.1 * randn(g, C), 0.1 * randn(g, C)
+    got = gn_all(x, G, w, b, act, None, dy)
+    want = gn_reference(x, G, w, b, 1e-5, act, None, dy)
+    v = x.float().view(B, L, G, -1)
+    c = v - v.mean((1, 3), keepdim=True)
+    xh = (c * torch.rsqrt((c * c).mean((1, 3), keepdim=True) + 1e-5)).view(B, L, C)
+    z = xh * w + b
+    if act == "gelu":
+        slope = (0.5 * torch.erfc(-z * math.sqrt(0.5))
+                 + z * torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi))
+    else:
+        s = torch.sigmoid(z)
+        slope = s * (1 + z * (1 - s))
+    d = dy.float() * slope
+    for name, p in (("dw", (d * xh).sum((0, 1))), ("db", d.sum((0, 1)))):
+        ref = want[name][0]
+        e = float((got[name].double() - ref).norm() / ref.norm())
+        r = float((p.double() - ref).norm() / ref.norm())
+        assert e <= 2 * r + 2 * 2.0 ** -21, f"{name}: {e:.3g} against {r:.3g}"
