@@ -179,10 +179,12 @@ __global__ void __launch_bounds__(CT, 1) gn_cluster_forward_kernel(ClArgs k) {
     __syncthreads();
     bool ok = true;
     const T *xs = reinterpret_cast<const T *>(x.at) + p.c;
-    // the thread's own rows: their mean, then the squares around it
-    float m[V], s[V];
+    // the thread's own rows: their mean, then the squares around it.  Means are sums of
+    // differences from one of the values, here and below: around a large mean the sums of
+    // the values themselves would round by a unit of that at every step.
+    float m[V], s[V], base[V];
 #pragma unroll
-    for (int e = 0; e < V; ++e) m[e] = s[e] = 0.0f;
+    for (int e = 0; e < V; ++e) m[e] = s[e] = base[e] = 0.0f;
     int r = p.r;
     for (int j = 0; j < x.pieces; ++j) {
         ok = ok && mbar_wait_bounded(&sh.bars[j], 0, k.timeout_ns);
@@ -191,15 +193,18 @@ __global__ void __launch_bounds__(CT, 1) gn_cluster_forward_kernel(ClArgs k) {
         for (; r < end; r += p.R) {
             float v[V];
             Vec<T, V>::load(xs + r * a.C, v);
+            if (r == p.r)
 #pragma unroll
-            for (int e = 0; e < V; ++e) m[e] += v[e];
+                for (int e = 0; e < V; ++e) base[e] = v[e];
+#pragma unroll
+            for (int e = 0; e < V; ++e) m[e] += v[e] - base[e];
         }
     }
     float cnt = p.on && n > p.r ? float((n - p.r + p.R - 1) / p.R) : 0.0f;
     if (cnt > 0.0f) {
         const float inv = 1.0f / cnt;
 #pragma unroll
-        for (int e = 0; e < V; ++e) m[e] *= inv;
+        for (int e = 0; e < V; ++e) m[e] = fmaf(m[e], inv, base[e]);
 #pragma unroll 4
         for (int i = p.r; i < n; i += p.R) {
             float v[V];
@@ -246,8 +251,9 @@ __global__ void __launch_bounds__(CT, 1) gn_cluster_forward_kernel(ClArgs k) {
     const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
     for (int g = warp; g < a.G; g += CT / 32) {
         float sum = 0.0f, sq = 0.0f;
-        for (int c = lane; c < a.cg; c += 32) sum += sh.red[g * a.cg + c];
-        const float mean = warp_sum(sum) / float(a.cg);
+        const float first = sh.red[g * a.cg];
+        for (int c = lane; c < a.cg; c += 32) sum += sh.red[g * a.cg + c] - first;
+        const float mean = first + warp_sum(sum) / float(a.cg);
         for (int c = lane; c < a.cg; c += 32) {
             const float d = sh.red[g * a.cg + c] - mean;
             sq += fmaf(d * d, float(n), sh.red[a.C + g * a.cg + c]);
@@ -269,10 +275,12 @@ __global__ void __launch_bounds__(CT, 1) gn_cluster_forward_kernel(ClArgs k) {
             for (int i = 0; i < 16; ++i)
                 if (i < k.K) mi[i] = ld_cluster(sh.g1 + g, i), si[i] = ld_cluster(sh.g2 + g, i);
             const float rows = 1.0f / fmaxf(float(len), 1.0f);
+            // (the first block has rows if any has)
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                if (i < k.K)
-                    mean = fmaf(float(split.rows(i)) * rows, mi[i], mean);
+            for (int i = 1; i < 16; ++i)
+                if (i < k.K && split.rows(i) > 0)
+                    mean = fmaf(float(split.rows(i)) * rows, mi[i] - mi[0], mean);
+            mean += mi[0];
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 if (i < k.K) {

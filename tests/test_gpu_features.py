@@ -1083,3 +1083,32 @@ def test_group_norm_parameter_gradients_in_norm(act, dtype):
         e = float((got[name].double() - ref).norm() / ref.norm())
         r = float((p.double() - ref).norm() / ref.norm())
         assert e <= 2 * r + 2 * 2.0 ** -21, f"{name}: {e:.3g} against {r:.3g}"
+
+
+@pytest.mark.parametrize("shape", [(2, 3000, 32, 4), (1, 14000, 8, 1), (1, 100000, 1, 1),
+                                   (3, 1024, 384, 32), (1, 30000, 512, 32), (1, 5000, 515, 5)])
+@pytest.mark.parametrize("mean", [1e2, 1e4])
+def test_group_norm_of_large_means_in_norm(shape, mean):
+    """Results around a large mean against the two-pass float32 form: the variance does not
+    cancel, and the mean is off by a few units of float32 as any float32 mean is (its own
+    rounding, at most 2^-24 of it, and sums of the same length)."""
+    B, L, C, G = shape
+    g = gen(L)
+    x, dy = randn(g, B, L, C) + mean, randn(g, B, L, C)
+    y, m, r = pc.pc_group_norm(x, G, return_stats=True)
+    v = x.double().view(B, L, G, -1)
+    m64 = v.mean((1, 3), keepdim=True)
+    r64 = (v.var((1, 3), unbiased=False, keepdim=True) + 1e-5) ** -0.5
+    want = (v - m64) * r64
+    f = x.view(B, L, G, -1)
+    c = f - f.mean((1, 3), keepdim=True)
+    plain = c * torch.rsqrt((c * c).mean((1, 3), keepdim=True) + 1e-5)
+
+    def off(a):
+        return float((a.double() - want).norm() / want.norm())
+    assert off(y.view_as(want)) <= 3 * off(plain) + U * mean
+    # means that are off by at most e enter the joined squares as sums of n (d + e)^2 instead of
+    # n d^2: a variance of 1 is off by at most 2 e + e^2, rstd by half of that; e is four of the
+    # mean's half units.  Beside it 64 roundings of the sums.
+    e = 4 * U * mean
+    assert float((r.view_as(r64) / r64 - 1).abs().max()) <= 64 * U + e + e * e / 2
