@@ -714,7 +714,9 @@ int pc_group_norm_backward(const void *grad_out, const void *x, int dtype, int64
  *   grad_table[b, v, :] = scale * sum of grad_out[b, t, :] over idx[b, t] = v.
  * The tokens are sorted by their row and added in float32, those of a row in
  * the order of t, in runs that end at every 64th (in smaller calls 32nd or 16th) of the
- * sorted tokens, and these in their order.
+ * sorted tokens, and these in their order; runs of a row that has many in 32s, and these
+ * in 32s again where there are more than 256, so that a row's chain of additions grows with
+ * the logarithm of its tokens.
  *
  * B V and B T are below 2^31 - 2^20 in the backward call (PC_ERR_UNSUPPORTED
  * above); scratch there: 18 bytes a token, and 8 C bytes for every run.

@@ -14,8 +14,10 @@
 // of threads walk over chunks of 64 sorted tokens (fewer in small calls), write the rows
 // that begin and end there, and leave the sums of rows that reach over a chunk's border,
 // which are joined afterwards: a row's chunks in their order, of a row of more than 32
-// chunks in 32s summed by a kernel of their own.  So a frequent row is many groups' work.
-// Everything in float32 and in a fixed order.
+// chunks in 32s summed by a kernel of their own, and these in 32s again as long as there
+// can be more than 256 of them.  So a frequent row is many groups' work, and its chain of
+// additions grows with the logarithm of its tokens.  Everything in float32 and in a fixed
+// order.
 // Bound: memory, the gradient's rows read once in the order of the table's, and in small
 // calls the launches.  Measured, 500,000 tokens of 256 float32, a table of 100,000 rows:
 // forward 118 us (5.2 TB/s), backward 33 of sorting, 110 of sums (4.7 TB/s), 24 of joins,
@@ -33,7 +35,10 @@ namespace pcn {
 namespace {
 
 constexpr int EMB_THREADS = 256;
-constexpr int RUN2 = 32;  // chunks of a second sum
+constexpr int RUN2 = 32;  // chunks of a second sum, these of a third, and so on
+// The levels of sums, that of the chunks' heads the first: with at most 2^31 / 16 chunks
+// the fifth has at most 128.
+constexpr int LEVELS = 5, TOP = 256;
 
 // --- forward ------------------------------------------------------------------
 
@@ -250,8 +255,9 @@ __global__ void __launch_bounds__(EMB_THREADS) sort_scatter_kernel(SortArgs a) {
 struct SumArgs {
     const void *dy;
     const uint2 *sorted;  // row, token
-    float *head, *tail;   // [chunks][C]: see emb_chunk_kernel
-    float *part2;         // sums of RUN2 heads whose chunks are one row's
+    float *tail;          // [chunks][C], as part[0]: see emb_chunk_kernel
+    float *part[LEVELS];  // heads; sums of RUN2 of these whose chunks are one row's; ...
+    int levels;
     void *dtable;
     uint32_t n, rows;     // tokens, rows of all tables
     int C, run;           // tokens of a chunk
@@ -292,7 +298,7 @@ __global__ void __launch_bounds__(EMB_THREADS) emb_chunk_kernel(SumArgs a, int G
         // the row `cur` ends, or the chunk does
         auto close = [&]() {
             if (open)
-                Vec<float, V>::store(a.head + size_t(k) * a.C + c, sum);
+                Vec<float, V>::store(a.part[0] + size_t(k) * a.C + c, sum);
             else
                 put_row<T, V>(a, cur, c, sum);
             open = false;
@@ -348,13 +354,31 @@ __device__ __forceinline__ void add_parts(const float *part, uint32_t i0, uint32
     }
 }
 
-// RUN2 chunks that one row fills and came into.
+// Adds a level's parts [b, e) in their order.  The row fills those below `last`, so where
+// the next level has sums of such, they stand for them.
+template <int V, int L>
+__device__ __forceinline__ void add_level(const SumArgs &a, uint32_t b, uint32_t e, uint32_t last,
+                                          int c, float (&sum)[V]) {
+    if constexpr (L + 1 < LEVELS) {
+        const uint32_t j0 = (b + RUN2 - 1) / RUN2, j1 = last / RUN2;
+        if (L + 1 < a.levels && j0 < j1) {
+            add_parts<V>(a.part[L], b, j0 * RUN2, c, a.C, sum);
+            add_level<V, L + 1>(a, j0, j1, j1, c, sum);
+            add_parts<V>(a.part[L], j1 * RUN2, e, c, a.C, sum);
+            return;
+        }
+    }
+    add_parts<V>(a.part[L], b, e, c, a.C, sum);
+}
+
+// RUN2 parts of a level, of `span` tokens together, that one row fills and came into.
 template <int V>
-__global__ void __launch_bounds__(EMB_THREADS) emb_second_kernel(SumArgs a, int G) {
+__global__ void __launch_bounds__(EMB_THREADS)
+emb_second_kernel(SumArgs a, int G, const float *part, float *to, uint32_t span) {
     let_next_start();
     after_previous();
     const int per = EMB_THREADS / G, g = threadIdx.x / G, l = threadIdx.x - g * G;
-    const uint32_t j = blockIdx.x * per + g, span = uint32_t(a.run) * RUN2;
+    const uint32_t j = blockIdx.x * per + g;
     if (g >= per || (uint64_t(j) + 1) * span > a.n) return;
     const uint32_t row = a.sorted[j * span].x;
     if (row >= a.rows || a.sorted[j * span + span - 1].x != row) return;
@@ -363,8 +387,8 @@ __global__ void __launch_bounds__(EMB_THREADS) emb_second_kernel(SumArgs a, int 
         float sum[V];
 #pragma unroll
         for (int e = 0; e < V; ++e) sum[e] = 0.0f;
-        add_parts<V>(a.head, j * RUN2, (j + 1) * RUN2, c, a.C, sum);
-        Vec<float, V>::store(a.part2 + size_t(j) * a.C + c, sum);
+        add_parts<V>(part, j * RUN2, (j + 1) * RUN2, c, a.C, sum);
+        Vec<float, V>::store(to + size_t(j) * a.C + c, sum);
     }
 }
 
@@ -390,18 +414,11 @@ __global__ void __launch_bounds__(EMB_THREADS) emb_join_kernel(SumArgs a, int G)
         else
             hi = mid - 1;
     }
-    // heads [k + 1, lo]; second sums [j0, j1) of those that the row fills, all but the last
-    const uint32_t h0 = k + 1, h1 = lo + 1, j0 = (h0 + RUN2 - 1) / RUN2, j1 = lo / RUN2;
+    // heads [k + 1, lo], whose chunks the row fills, but perhaps the last
     for (int c = l * V; c < a.C; c += G * V) {
         float sum[V];
         Vec<float, V>::load(a.tail + size_t(k) * a.C + c, sum);
-        if (j0 < j1) {
-            add_parts<V>(a.head, h0, j0 * RUN2, c, a.C, sum);
-            add_parts<V>(a.part2, j0, j1, c, a.C, sum);
-            add_parts<V>(a.head, j1 * RUN2, h1, c, a.C, sum);
-        } else {
-            add_parts<V>(a.head, h0, h1, c, a.C, sum);
-        }
+        add_level<V, 0>(a, k + 1, lo + 1, lo, c, sum);
         put_row<T, V>(a, row, c, sum);
     }
 }
@@ -434,9 +451,12 @@ cudaError_t emb_sums(const SumArgs &a, cudaStream_t st) {
     cudaError_t e =
         launch(true, emb_chunk_kernel<T, V>, blocks(chunks), EMB_THREADS, 0, st, a, G);
     const int nv = a.C / V, G2 = nv < EMB_THREADS ? nv : EMB_THREADS, per2 = EMB_THREADS / G2;
-    if (e == cudaSuccess && chunks > RUN2)
-        e = launch(true, emb_second_kernel<V>, unsigned(ceil_div(chunks / RUN2, per2)), EMB_THREADS,
-                   0, st, a, G2);
+    int64_t sums = chunks, span = a.run;
+    for (int l = 1; e == cudaSuccess && l < a.levels; ++l) {
+        sums /= RUN2, span *= RUN2;
+        e = launch(true, emb_second_kernel<V>, unsigned(ceil_div(sums, per2)), EMB_THREADS, 0, st, a,
+                   G2, a.part[l - 1], a.part[l], uint32_t(span));
+    }
     if (e == cudaSuccess && chunks > 1)
         e = launch(true, emb_join_kernel<T, V>, unsigned(ceil_div(chunks - 1, per2)), EMB_THREADS,
                    0, st, a, G2);
@@ -495,10 +515,17 @@ cudaError_t emb_backward(const DeviceInfo &dev, const void *dy, int dtype, int64
     auto round = [](size_t v) { return (v + 255) / 256 * 256; };
     const size_t list = round(size_t(a.n) * sizeof(uint2));
     const size_t count = round((size_t(blocks) + 1) * (size_t(1) << each) * 4);
-    const size_t chunks = size_t(ceil_div(a.n, a.run)), part = round(chunks * C * 4);
+    const size_t chunks = size_t(ceil_div(a.n, a.run));
+    size_t sums[LEVELS] = {chunks}, parts = round(chunks * C * 4);  // (heads)
+    for (a.levels = 1; a.levels < LEVELS; ++a.levels) {
+        const size_t below = sums[a.levels - 1];
+        if (below <= (a.levels == 1 ? RUN2 : TOP)) break;
+        sums[a.levels] = below / RUN2;
+        parts += round(sums[a.levels] * C * 4);
+    }
     char *mem = nullptr;
     cudaError_t e = scratch_alloc(dev, reinterpret_cast<void **>(&mem),
-                      2 * list + count + 2 * part + round(chunks / RUN2 * C * 4), st);
+                      2 * list + count + round(chunks * C * 4) + parts, st);
     if (e != cudaSuccess) return e;
     uint2 *lists[2] = {reinterpret_cast<uint2 *>(mem), reinterpret_cast<uint2 *>(mem + list)};
     SortArgs s{};
@@ -528,9 +555,10 @@ cudaError_t emb_backward(const DeviceInfo &dev, const void *dy, int dtype, int64
         s.idx = nullptr, s.in = s.out;
     }
     a.sorted = s.out;
-    a.head = reinterpret_cast<float *>(mem + 2 * list + count);
-    a.tail = a.head + part / sizeof(float);
-    a.part2 = a.tail + part / sizeof(float);
+    a.tail = reinterpret_cast<float *>(mem + 2 * list + count);
+    a.part[0] = a.tail + round(chunks * C * 4) / sizeof(float);
+    for (int l = 1; l < a.levels; ++l)
+        a.part[l] = a.part[l - 1] + round(sums[l - 1] * C * 4) / sizeof(float);
     if (e == cudaSuccess)
         e = dtype == PC_F32 ? emb_sums_any<float>(a, st) : emb_sums_any<bf16>(a, st);
     const cudaError_t f = scratch_free(mem, st);

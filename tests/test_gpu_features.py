@@ -1112,3 +1112,43 @@ def test_group_norm_of_large_means_in_norm(shape, mean):
     # mean's half units.  Beside it 64 roundings of the sums.
     e = 4 * U * mean
     assert float((r.view_as(r64) / r64 - 1).abs().max()) <= 64 * U + e + e * e / 2
+
+
+def longest_chain(T, run):
+    """Additions of a row of T tokens: a run; the ends of each level of sums of 32 before the
+    last, at most 31 on either side and a sum's own 32; what the last level has."""
+    n, chain = -(-T // run), run + 32
+    first = True
+    while n > (32 if first else 256):
+        n, chain, first = n // 32, chain + 31 + 31 + 32, False
+    return chain + n
+
+
+@pytest.mark.parametrize("T,C,run", [(600_000, 4, 16), (3_000_000, 4, 64), (20_000_000, 1, 64)])
+def test_embedding_sum_of_a_row_with_most_of_the_tokens(T, C, run):
+    """All of one sign and alike: a chain that is as long as the row has sums of 32 runs drops
+    what is below a unit of what it has at each of them."""
+    v = 1 + 15 * 2.0 ** -18
+    dy = torch.full((T, C), v, device=DEV)
+    idx = torch.full((T,), 3, device=DEV)
+    idx[:5], idx[T // 2] = 1, 6                     # the row begins inside a run
+    d = pc.pc_embedding_backward(dy, idx, (9, C))
+    n = torch.zeros(9, 1, dtype=torch.float64, device=DEV)
+    n[1], n[6], n[3] = 5, 1, T - 6
+    want = (n * v).expand(9, C)
+    close(d, want, longest_chain(T, run) * U * want + 1e-30, "grad_table")
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_embedding_of_many_tokens_and_few_frequent_rows(dtype):
+    g = gen(51)
+    T, V, C = 2_500_000, 5000, 8
+    u = torch.rand(T, generator=g, device=DEV)
+    idx = (V * u ** 8).long().clamp_max(V - 1)
+    idx[torch.rand(T, generator=g, device=DEV) < 0.3] = 777
+    idx[torch.rand(T, generator=g, device=DEV) < 0.1] = -1
+    dy = randn(g, T, C, dtype=dtype)
+    d = pc.pc_embedding_backward(dy, idx, (V, C), 0.5)
+    s, m = emb_reference(dy, idx, (V, C), 0.5)
+    close(d, s, longest_chain(T, 64) * U * m + HALF[dtype] * s.abs() + 1e-30, "grad_table")
+    assert torch.equal(d, pc.pc_embedding_backward(dy, idx, (V, C), 0.5))
