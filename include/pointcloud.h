@@ -750,7 +750,8 @@ int pc_embedding_backward(const void *grad_out, int dtype, int64_t B, int64_t V,
  * pc_gated_linear_workspace_bytes(dtype, rows, C, F, gradients) bytes, else the
  * library's stream-ordered pool (which returns what is beyond 256 MiB at every
  * synchronization, so that large calls spend long on mapping it again).  gradients: 0
- * for the forward call, or which gradients are asked for.  bfloat16 forward calls with C
+ * for the forward call, or which gradients are asked for; with PC_GATED_UNALIGNED where x,
+ * w_gate or w_up is not 16-byte aligned, as bfloat16 calls then copy them.  bfloat16 forward calls with C
  * a multiple of 8 and 16-byte aligned arrays need none; backward calls keep da and du (8
  * bytes a hidden unit and row, float32 12), float32 calls three bfloat16 parts of x and
  * the weights; parts of split sums come to it.
@@ -763,6 +764,7 @@ int pc_embedding_backward(const void *grad_out, int dtype, int64_t B, int64_t V,
 #define PC_GATED_GRAD_X 1
 #define PC_GATED_GRAD_WEIGHT 2
 #define PC_GATED_GRAD_BIAS 4
+#define PC_GATED_UNALIGNED 8
 size_t pc_gated_linear_workspace_bytes(int dtype, int64_t rows, int64_t C, int64_t F,
                                        int gradients);
 

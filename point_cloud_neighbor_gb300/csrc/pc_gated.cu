@@ -131,9 +131,13 @@ extern "C" size_t pc_gated_linear_workspace_bytes(int dtype, int64_t rows, int64
         return 0;
     GatedArgs a{};
     a.rows = rows, a.C = int(C), a.F = int(F);
+    if (gradients & PC_GATED_UNALIGNED)  // (no multiple of 16, and not looked at)
+        a.x = a.wg = a.wu = reinterpret_cast<const char *>(uintptr_t(2));
     void *some = &a;  // (only which gradients there are counts)
     if (gradients & PC_GATED_GRAD_X) a.dx = some;
     if (gradients & PC_GATED_GRAD_WEIGHT) a.dwg = a.dwu = some;
     if (gradients & PC_GATED_GRAD_BIAS) a.dbg = a.dbu = some;
-    return gated_tc_scratch(*dev, a, dtype, gradients != 0);
+    return gated_tc_scratch(
+        *dev, a, dtype,
+        (gradients & (PC_GATED_GRAD_X | PC_GATED_GRAD_WEIGHT | PC_GATED_GRAD_BIAS)) != 0);
 }

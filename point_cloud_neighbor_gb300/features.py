@@ -155,6 +155,7 @@ def _gated_args(x, w_gate, w_up, b_gate, b_up, activation):
 
 
 PC_GATED_GRAD_X, PC_GATED_GRAD_WEIGHT, PC_GATED_GRAD_BIAS = 1, 2, 4
+PC_GATED_UNALIGNED = 8
 
 
 # Calls of as many elements take their scratch from torch's allocator, which keeps it
@@ -162,9 +163,12 @@ PC_GATED_GRAD_X, PC_GATED_GRAD_WEIGHT, PC_GATED_GRAD_BIAS = 1, 2, 4
 LARGE = 1 << 24
 
 
-def _workspace(x, rows: int, C: int, F: int, gradients: int, index: int):
+def _workspace(x, args, gradients: int, index: int):
+    px, code, rows, C, F, pg, pu = args[:7]
+    if (px | pg | pu) % 16:
+        gradients |= PC_GATED_UNALIGNED
     with torch.cuda.device(index):
-        n = lib().pc_gated_linear_workspace_bytes(_DTYPES[x.dtype], rows, C, F, gradients)
+        n = lib().pc_gated_linear_workspace_bytes(code, rows, C, F, gradients)
     return (torch.empty(n, dtype=torch.uint8, device=x.device), n) if n else (None, 0)
 
 
@@ -184,7 +188,7 @@ def pc_gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
         _same(out, "out", shape, x.dtype, index)
     work, n = None, 0
     if args[2] * (args[3] + 2 * F) >= LARGE:
-        work, n = _workspace(x, *args[2:5], 0, index)
+        work, n = _workspace(x, args, 0, index)
     _run("pc_gated_linear", lib().pc_gated_linear, index, *args, out.data_ptr(),
          _ptr_or_none(work), n)
     return out
@@ -212,7 +216,7 @@ def pc_gated_linear_backward(grad_out: torch.Tensor, x: torch.Tensor, w_gate: to
         | (PC_GATED_GRAD_BIAS if dbg is not None else 0)
     work, n = None, 0
     if which and args[2] * (args[3] + 2 * F) >= LARGE:
-        work, n = _workspace(x, *args[2:5], which, index)
+        work, n = _workspace(x, args, which, index)
     _run("pc_gated_linear_backward", lib().pc_gated_linear_backward, index,
          grad_out.data_ptr(), *args, _ptr_or_none(dx), _ptr_or_none(dwg), _ptr_or_none(dwu),
          _ptr_or_none(dbg), _ptr_or_none(dbu), _ptr_or_none(work), n)

@@ -1152,3 +1152,68 @@ def test_embedding_of_many_tokens_and_few_frequent_rows(dtype):
     s, m = emb_reference(dy, idx, (V, C), 0.5)
     close(d, s, longest_chain(T, 64) * U * m + HALF[dtype] * s.abs() + 1e-30, "grad_table")
     assert torch.equal(d, pc.pc_embedding_backward(dy, idx, (V, C), 0.5))
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_gated_linear_workspace_of_unaligned_arrays(dtype):
+    """What the C ABI asks for with PC_GATED_UNALIGNED is enough for arrays at any address: the
+    call takes it (a call that it is too small for leaves it as it was)."""
+    from point_cloud_neighbor_gb300.binding import lib
+    L, code, shape = lib(), 0 if dtype is torch.float32 else 1, (300, 128, 200)
+
+    def moved(t):
+        return torch.empty(t.numel() + 1, dtype=t.dtype, device=DEV)[1:].copy_(
+            t.reshape(-1)).view(t.shape)
+    ins = gated_inputs(gen(8), *shape, dtype)
+    want = gated_all(*ins, "silu")
+    s = torch.cuda.current_stream().cuda_stream
+    flag = pc.features.PC_GATED_UNALIGNED
+    for which in ((0, 1, 2), (0,), (1,), (2,)):          # of x, w_gate and w_up
+        x, wg, wu, bg, bu, dy = [moved(t) if i in which else t for i, t in enumerate(ins)]
+        args = [x.data_ptr(), code, *shape, wg.data_ptr(), wu.data_ptr(), bg.data_ptr(),
+                bu.data_ptr(), 1]
+        outs = {k: torch.full_like(v, math.nan) for k, v in want.items()}
+        for gradients in (0, 7):
+            n = L.pc_gated_linear_workspace_bytes(code, *shape, gradients | flag)
+            plain = L.pc_gated_linear_workspace_bytes(code, *shape, gradients)
+            assert n > plain if dtype is torch.bfloat16 else n == plain
+            for bytes_, used in ((n, True), (plain, dtype is torch.float32)):
+                work = torch.full((n + 256,), 77, dtype=torch.uint8, device=DEV)
+                if gradients:
+                    assert L.pc_gated_linear_backward(
+                        dy.data_ptr(), *args, *[outs[k].data_ptr() for k in
+                                                ("dx", "dwg", "dwu", "dbg", "dbu")],
+                        work.data_ptr(), bytes_, s) == 0
+                else:
+                    assert L.pc_gated_linear(*args, outs["y"].data_ptr(), work.data_ptr(), bytes_,
+                                             s) == 0
+                assert bool((work[:n] != 77).any()) == used
+                assert (work[n:] == 77).all()
+        for k in want:
+            assert torch.equal(outs[k], want[k]), k
+
+
+def test_large_calls_on_unaligned_views_take_one_workspace():
+    """A call whose scratch comes from torch's allocator takes nothing from the library's pool:
+    its size is that of the call's own arrays."""
+    rows, C, F = 33000, 64, 512
+    x, wg, wu, bg, bu, dy = gated_inputs(gen(9), rows, C, F, torch.bfloat16)
+    want = gated_all(x, wg, wu, bg, bu, dy, "silu")
+    flat = torch.empty(x.numel() + 1, dtype=x.dtype, device=DEV)[1:].copy_(x.reshape(-1))
+    xo = flat.view(x.shape)
+    sizes, real = [], pc.features.torch.empty
+
+    def empty(*a, **k):
+        if k.get("dtype") is torch.uint8:
+            sizes.append(a[0])
+        return real(*a, **k)
+    pc.features.torch.empty = empty
+    try:
+        got = gated_all(xo, wg, wu, bg, bu, dy, "silu")
+    finally:
+        pc.features.torch.empty = real
+    for k in want:
+        assert torch.equal(got[k], want[k]), k
+    lib = pc.binding.lib()
+    assert sizes == [lib.pc_gated_linear_workspace_bytes(1, rows, C, F, g) for g in (8, 15)]
+    assert sizes[0] >= 2 * x.numel()
