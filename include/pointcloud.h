@@ -760,6 +760,12 @@ int pc_embedding_backward(const void *grad_out, int dtype, int64_t B, int64_t V,
  * 16,384 products leaves; bfloat16 calls take da and du as two bfloat16 parts each (to
  * 2^-17), float32 calls three parts of each operand (products to 2^-24, sums rounded to
  * nearest every 64).  Device-side waits are bounded as those of the attention kernels.
+ *
+ * Values that are not finite stay visible in the rows and sums that they enter.  In float32
+ * calls an infinity, or a value beyond 3.389e38 (which rounds to one in bfloat16), of x, the
+ * weights, da or du becomes a NaN there, also where the definition gives an infinity or a
+ * number (its parts would be infinities of both signs); in bfloat16 calls that holds for
+ * infinite weights and x where da and du meet them.
  */
 #define PC_GATED_GRAD_X 1
 #define PC_GATED_GRAD_WEIGHT 2

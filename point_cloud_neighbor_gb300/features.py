@@ -179,7 +179,8 @@ def pc_gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_up: torch.Tensor,
     """act(x w_gate^T + b_gate) * (x w_up^T + b_up): the first half of a gated
     feed-forward block.  x [..., C]; w_gate and w_up [F, C], as in a linear
     layer; b_gate and b_up [F], both or neither; all of one dtype.  Returns
-    [..., F]."""
+    [..., F].  In float32 an infinity in x or the weights (or a value beyond
+    3.389e38) makes what it enters NaN, whatever the definition gives there."""
     index, args, F = _gated_args(x, w_gate, w_up, b_gate, b_up, activation)
     shape = (*x.shape[:-1], F)
     if out is None:

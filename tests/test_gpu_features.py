@@ -1217,3 +1217,23 @@ def test_large_calls_on_unaligned_views_take_one_workspace():
     lib = pc.binding.lib()
     assert sizes == [lib.pc_gated_linear_workspace_bytes(1, rows, C, F, g) for g in (8, 15)]
     assert sizes[0] >= 2 * x.numel()
+
+
+def test_gated_linear_of_infinities():
+    """float32: NaN in what they enter, as documented, and nothing elsewhere; bfloat16: what the
+    definition gives forward."""
+    for dtype in DTYPES:
+        x, wg, wu, bg, bu, dy = gated_inputs(gen(24), 40, 64, 72, dtype)
+        want = pc.pc_gated_linear(x, wg, wu, bg, bu, activation="relu")
+        for big in (math.inf, 3.4e38):
+            w = wg.clone()
+            w[7, 3] = big          # (3.4e38 is infinite in bfloat16)
+            y = pc.pc_gated_linear(x, w, wu, bg, bu, activation="relu")
+            keep = torch.arange(72, device=DEV) != 7
+            assert torch.equal(y[:, keep], want[:, keep])
+            if dtype is torch.float32:
+                assert y[:, 7].isnan().all()
+                continue
+            u = x.double() @ wu[7].double() + bu[7].double()
+            up = x[:, 3].double() > 0
+            assert torch.equal(y[:, 7].double(), torch.where(up, math.inf * u, 0.0))
