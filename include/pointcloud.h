@@ -751,15 +751,16 @@ int pc_embedding_backward(const void *grad_out, int dtype, int64_t B, int64_t V,
  * library's stream-ordered pool (which returns what is beyond 256 MiB at every
  * synchronization, so that large calls spend long on mapping it again).  gradients: 0
  * for the forward call, or which gradients are asked for; with PC_GATED_UNALIGNED where x,
- * w_gate or w_up is not 16-byte aligned, as bfloat16 calls then copy them.  bfloat16 forward calls with C
- * a multiple of 8 and 16-byte aligned arrays need none; backward calls keep da and du (8
- * bytes a hidden unit and row, float32 12), float32 calls three bfloat16 parts of x and
- * the weights; parts of split sums come to it.
+ * w_gate or w_up is not 16-byte aligned, as bfloat16 calls then copy them.  bfloat16
+ * forward calls with C a multiple of 8 and 16-byte aligned arrays need none; backward calls
+ * keep da and du (8 bytes a hidden unit and row, float32 12), float32 calls three bfloat16
+ * parts of x and the weights; parts of split sums come to it.
  *
  * Runs on the tensor cores, which add in float32 and cut off what a chain of at most
- * 16,384 products leaves; bfloat16 calls take da and du as two bfloat16 parts each (to
- * 2^-17), float32 calls three parts of each operand (products to 2^-24, sums rounded to
- * nearest every 64).  Device-side waits are bounded as those of the attention kernels.
+ * 16,384 products leaves (twice as many with da and du, which bfloat16 calls take as two
+ * bfloat16 parts each, to 2^-17).  float32 calls take three parts of each operand (products
+ * to 2^-24, sums rounded to nearest every 64).  Device-side waits are bounded as those of
+ * the attention kernels.
  *
  * Values that are not finite stay visible in the rows and sums that they enter.  In float32
  * calls an infinity, or a value beyond 3.389e38 (which rounds to one in bfloat16), of x, the

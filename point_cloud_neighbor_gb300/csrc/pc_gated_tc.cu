@@ -29,8 +29,8 @@
 // high (to 2^-24).  A stage is one part of both operands, free as soon as the last
 // product that takes it is issued.  The tensor cores cut their sums off instead of
 // rounding them, so a chain is 64 long, the small products first, and the chains
-// are added up in registers.  A bfloat16 chain over the rows is at most 16,384
-// long, joined in float32.
+// are added up in registers.  A bfloat16 chain over rows or hidden units takes at most
+// 16,384 of them, joined in float32.
 //
 // da and du are operands of two products each.  bfloat16 calls take two bfloat16 parts
 // of them, what the first leaves and then the first itself (to 2^-17): one part is a rounding
@@ -944,9 +944,12 @@ constexpr GemmKind KINDS[] = {{256, 2, 620, 4400, 7000, 2600, 6300},
                               {128, 1, 385, 3000, 4100, 1500, 4200},
                               {64, 1, 277, 2400, 4100, 1000, 4200}};
 
-// The kind of tile and the parts of the contraction, by the smallest estimate.  float32:
-// six products for one, epilogues three times as long (and no tiles of 256 columns, whose
-// sums a thread could not hold).  Parts cost their writes and reads and a launch.
+// The kind of tile and the parts of the contraction, by the smallest estimate.  bfloat16 DX
+// and DW: two products for one.  float32: six, epilogues three times as long (and no tiles
+// of 256 columns, whose sums a thread could not hold).  Parts cost their writes and reads and
+// a launch.  (With da and du in two parts the choices for the three passes of 2048 x 1024 x
+// 1024, 8192 x 256 x 4096, 32,768 x 1024 x 4096 and 65,536 x 128 x 256 are within 10% of the
+// best kind, which is what two runs of one kind differ by.)
 struct GemmPlan {
     int BN = 0, CG = 1, nsplit = 1, per = 1;
     int rows() const { return BM * CG; }

@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(CT, 1) gn_cluster_backward_kernel(ClArgs k) {
              mbar_wait_bounded(&sh.bars[PIECES + j], 0, k.timeout_ns);
         const int end = p.on ? min(x.rows(j), dy.rows(j)) : 0;
         for (; r < end; r += U * p.R) {
-            // (the rows of a batch past the piece's end are its first ones again, times 0)
+            // (the rows of a batch past the piece's end are its first ones again, and not added)
             float v[U][V], g[U][V];
             const int q = min(U, (end - r + p.R - 1) / p.R);
 #pragma unroll
