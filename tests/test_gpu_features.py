@@ -1237,3 +1237,18 @@ def test_gated_linear_of_infinities():
             u = x.double() @ wu[7].double() + bu[7].double()
             up = x[:, 3].double() > 0
             assert torch.equal(y[:, 7].double(), torch.where(up, math.inf * u, 0.0))
+
+
+def test_group_norm_gradients_of_some_with_many_clouds():
+    g = gen(61)
+    x, dy = randn(g, 1100, 5, 24), randn(g, 1100, 5, 24)
+    w, b = randn(g, 24), randn(g, 24)
+    _, m, r = pc.pc_group_norm(x, 4, w, b, activation="silu", return_stats=True)
+    full = pc.pc_group_norm_backward(dy, x, m, r, 4, w, b, activation="silu")
+    for need in ({"need_x": False}, {"need_weight": False}, {"need_bias": False},
+                 {"need_weight": False, "need_bias": False},
+                 {"need_x": False, "need_weight": False}):
+        some = pc.pc_group_norm_backward(dy, x, m, r, 4, w, b, activation="silu", **need)
+        for f, s, k in zip(full, some, ("need_x", "need_weight", "need_bias")):
+            assert (s is not None) == need.get(k, True)
+            assert s is None or torch.equal(f, s)
